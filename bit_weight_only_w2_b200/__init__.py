@@ -5,6 +5,9 @@ kernels. PyTorch provides device memory and streams. The binding raises if the l
 is missing; there is no fallback.
 
     Y = gemm(x, packed, scales, zeros, bits, group_size)   # Y[M][N] = X[M][K] W^T
+    Y = adapter_gemm(x, packed, scales, zeros, bits, group_size, a, b, scaling, index)
+    dX = gemm_dx(dy, packed_t, scales, zeros, bits, group_size)
+    dX, dA, dB = adapter_backward(dy, x, p, packed_t, scales, zeros, bits, group_size, a, b, scaling, index)
 
 Layouts (see include/lowbit.h): x bf16 [M][K]; packed int32 view of uint32 words
 [N][K*bits/32]; scales / zeros fp16 [K/group_size][N]; y bf16 [M][N].
@@ -13,7 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence, Union
 
 import torch
 
@@ -39,6 +42,11 @@ class GemmDesc(ctypes.Structure):
                 ("bits", ctypes.c_int), ("group_size", ctypes.c_int),
                 ("X", ctypes.c_void_p), ("Wp", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("zeros", ctypes.c_void_p), ("Y", ctypes.c_void_p)]
+
+
+class Adapters(ctypes.Structure):
+    _fields_ = [("num", ctypes.c_int), ("rank", ctypes.c_int), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
+                ("scaling", ctypes.c_void_p), ("index", ctypes.c_void_p)]
 
 
 _lib = None
@@ -102,6 +110,23 @@ def open_library(path: str) -> ctypes.CDLL:
     lib.lowbit_selftest_index_check.restype = i32
     lib.lowbit_gemm_noalloc.argtypes = [i64, i64, i64, i32, i32, p, p, p, p, p, p]
     lib.lowbit_gemm_noalloc.restype = i32
+    ad = ctypes.POINTER(Adapters)
+    lib.lowbit_transposed_words.argtypes = [i64, i64, i32]
+    lib.lowbit_transposed_words.restype = sz
+    lib.lowbit_transpose.argtypes = [p, i64, i64, i32, p, p]
+    lib.lowbit_transpose.restype = i32
+    lib.lowbit_adapter_workspace_size.argtypes = [i64, i64, i64, i32, i32]
+    lib.lowbit_adapter_workspace_size.restype = sz
+    lib.lowbit_adapter_gemm.argtypes = [i64, i64, i64, i32, i32, p, p, p, p, ad, p, p, p, p, p, sz, p]
+    lib.lowbit_adapter_gemm.restype = i32
+    lib.lowbit_gemm_dx.argtypes = [i64, i64, i64, i32, i32, p, p, p, p, p, p, sz, p]
+    lib.lowbit_gemm_dx.restype = i32
+    lib.lowbit_adapter_backward.argtypes = [i64, i64, i64, i32, i32, p, p, p, p, ad, p, p, p, p, p, p, p, p, sz, p]
+    lib.lowbit_adapter_backward.restype = i32
+    lib.lowbit_checkpoint_store.argtypes = [p, i64, i64, p, p, p]
+    lib.lowbit_checkpoint_store.restype = i32
+    lib.lowbit_checkpoint_load.argtypes = [p, p, i64, i64, p, p]
+    lib.lowbit_checkpoint_load.restype = i32
     return lib
 
 
@@ -275,6 +300,222 @@ def gemm_batch(descs: Sequence[GemmDesc], device: Optional[torch.device] = None,
             need = max((workspace_size(d.M, d.K) for d in descs), default=0)
             ws = workspace(dev, need)
         _check(load().lowbit_gemm_batch(arr, len(descs), _ptr(ws), ws.numel(), _stream()), "lowbit_gemm_batch")
+
+
+# ---- adapters, gradients and 8-bit activation copies -----------------------------------------
+class Checkpoint(NamedTuple):
+    """8-bit copy of an activation [M][K]: `codes` float8_e4m3fn [M][K] and `exps` uint8 [M][K/32], a
+    power-of-two exponent + 127 for each 32 values of a row (see lowbit_checkpoint_store)."""
+    codes: torch.Tensor
+    exps: torch.Tensor
+
+
+def checkpoint_empty(M: int, K: int, device) -> Checkpoint:
+    """Buffers for the 8-bit copy of an [M][K] activation (K a multiple of 32)."""
+    if K % 32:
+        raise ValueError(f"K: expected a multiple of 32, got {K}")
+    return Checkpoint(torch.empty((M, K), dtype=torch.float8_e4m3fn, device=device),
+                      torch.empty((M, K // 32), dtype=torch.uint8, device=device))
+
+
+def _check_checkpoint(ck: Checkpoint, M: int, K: int, device, name: str = "checkpoint"):
+    _need(ck.codes, torch.float8_e4m3fn, f"{name}.codes")
+    _need(ck.exps, torch.uint8, f"{name}.exps")
+    if tuple(ck.codes.shape) != (M, K) or tuple(ck.exps.shape) != (M, K // 32) or K % 32:
+        raise ValueError(f"{name}: expected codes {(M, K)} and exps {(M, K // 32)} with K a multiple of 32, got "
+                         f"{tuple(ck.codes.shape)} and {tuple(ck.exps.shape)}")
+    for part, t in (("codes", ck.codes), ("exps", ck.exps)):
+        if t.device != device:
+            raise ValueError(f"{name}.{part}: on {t.device}, expected {device}")
+
+
+def checkpoint_store(x: torch.Tensor, out: Optional[Checkpoint] = None) -> Checkpoint:
+    """The 8-bit copy of x (bf16 [M][K], K a multiple of 32)."""
+    _need(x, torch.bfloat16, "x")
+    _need_cuda(("x", x))
+    M, K = x.shape
+    if out is None:
+        out = checkpoint_empty(M, K, x.device)
+    _check_checkpoint(out, M, K, x.device, "out")
+    with torch.cuda.device(x.device):
+        _check(load().lowbit_checkpoint_store(_ptr(x), M, K, _ptr(out.codes), _ptr(out.exps), _stream()),
+               "lowbit_checkpoint_store")
+    return out
+
+
+def checkpoint_load(ck: Checkpoint, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The bf16 values an 8-bit copy stands for."""
+    _need(ck.codes, torch.float8_e4m3fn, "checkpoint.codes")
+    _need_cuda(("checkpoint.codes", ck.codes))
+    M, K = ck.codes.shape
+    _check_checkpoint(ck, M, K, ck.codes.device)
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.bfloat16, device=ck.codes.device)
+    _check_like(out, "out", (M, K), torch.bfloat16, ck.codes.device)
+    with torch.cuda.device(out.device):
+        _check(load().lowbit_checkpoint_load(_ptr(ck.codes), _ptr(ck.exps), M, K, _ptr(out), _stream()),
+               "lowbit_checkpoint_load")
+    return out
+
+
+def _check_like(t: torch.Tensor, name: str, shape, dtype, device):
+    _need(t, dtype, name, ndim=len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def transposed_words(N: int, K: int, bits: int) -> int:
+    return int(load().lowbit_transposed_words(N, K, bits))
+
+
+def transpose_packed(packed: torch.Tensor, K: int, bits: int) -> torch.Tensor:
+    """W's packed words [N][K*bits/32] -> W^T's [K][ceil(N/128)*128*bits/32], which gemm_dx and
+    adapter_backward read. Done once per weight."""
+    _need(packed, torch.int32, "packed")
+    _need_cuda(("packed", packed))
+    N = packed.shape[0]
+    if bits not in (1, 2, 4) or K * bits % 32 or packed.shape[1] != K * bits // 32:
+        raise ValueError(f"packed: expected [N][{K * bits // 32 if bits in (1, 2, 4) else 'K*bits/32'}] words for K={K}, "
+                         f"bits={bits}, got {tuple(packed.shape)}")
+    out = torch.empty((K, (N + 127) // 128 * 128 * bits // 32), dtype=torch.int32, device=packed.device)
+    with torch.cuda.device(packed.device):
+        _check(load().lowbit_transpose(_ptr(packed), N, K, bits, _ptr(out), _stream()), "lowbit_transpose")
+    return out
+
+
+def adapter_workspace_size(M: int, N: int, K: int, num: int, rank: int) -> int:
+    return int(load().lowbit_adapter_workspace_size(M, N, K, num, rank))
+
+
+def _own_workspace(ws: Optional[torch.Tensor], device, M, N, K, num, rank) -> torch.Tensor:
+    # allocated per call by default: the caching allocator ties it to the current stream (and to the
+    # pool of a graph under capture), so calls on several streams or in several graphs never share it
+    need = adapter_workspace_size(M, N, K, num, rank)
+    if ws is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    _need(ws, torch.uint8, "ws", ndim=1)
+    if ws.device != device:
+        raise ValueError(f"ws: on {ws.device}, expected {device}")
+    return ws
+
+
+def _check_adapters(a, b, scaling, index, M, N, K, device) -> Adapters:
+    _need(a, torch.bfloat16, "a", ndim=3)
+    _need(b, torch.bfloat16, "b", ndim=3)
+    L, R = a.shape[0], a.shape[1]
+    if tuple(a.shape) != (L, R, K) or tuple(b.shape) != (L, N, R):
+        raise ValueError(f"a, b: expected shapes (L, R, {K}) and (L, {N}, R), got {tuple(a.shape)} and {tuple(b.shape)}")
+    _check_like(scaling, "scaling", (L,), torch.float32, device)
+    if index is not None:
+        _check_like(index, "index", (M,), torch.int32, device)
+    for name, t in (("a", a), ("b", b)):
+        if t.device != device:
+            raise ValueError(f"{name}: on {t.device}, expected {device}")
+    return Adapters(L, R, _ptr(a), _ptr(b), _ptr(scaling), _ptr(index))
+
+
+def adapter_gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor],
+                 bits: int, group_size: int, a: torch.Tensor, b: torch.Tensor, scaling: torch.Tensor,
+                 index: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                 p: Optional[torch.Tensor] = None, checkpoint: Optional[Checkpoint] = None,
+                 ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = X W^T + p B^T, p = scaling * X A^T with each token's own adapter (see lowbit_adapter_gemm).
+
+    a bf16 [L][R][K], b bf16 [L][N][R], scaling fp32 [L], index int32 [M] (values outside 0..L-1: no
+    adapter; None: adapter 0 for every token). For training, pass buffers that the backward reads:
+    `p` bf16 [M][R] and, to keep X in 8 bits, `checkpoint` (checkpoint_empty(M, K, device))."""
+    M, N, K = _check_gemm_args(x, packed, scales, zeros, out, bits, group_size)
+    ad = _check_adapters(a, b, scaling, index, M, N, K, x.device)
+    if p is not None:
+        _check_like(p, "p", (M, ad.rank), torch.bfloat16, x.device)
+    if checkpoint is not None:
+        _check_checkpoint(checkpoint, M, K, x.device)
+    with torch.cuda.device(x.device):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        ws = _own_workspace(ws, x.device, M, N, K, ad.num, ad.rank)
+        codes, exps = checkpoint if checkpoint is not None else (None, None)
+        _check(load().lowbit_adapter_gemm(M, N, K, bits, group_size, _ptr(x), _ptr(packed), _ptr(scales), _ptr(zeros),
+                                          ctypes.byref(ad), _ptr(out), _ptr(p), _ptr(codes), _ptr(exps), _ptr(ws),
+                                          ws.numel(), _stream()), "lowbit_adapter_gemm")
+    return out
+
+
+def _check_grad_args(dy, packed_t, scales, zeros, bits: int, group_size: int):
+    _need(dy, torch.bfloat16, "dy")
+    _need(packed_t, torch.int32, "packed_t")
+    _need(scales, torch.float16, "scales")
+    M, N = dy.shape
+    K = packed_t.shape[0]
+    if bits in (1, 2, 4) and packed_t.shape[1] != (N + 127) // 128 * 128 * bits // 32:
+        raise ValueError(f"packed_t: expected {(K, (N + 127) // 128 * 128 * bits // 32)} for N={N}, bits={bits}, "
+                         f"got {tuple(packed_t.shape)}")
+    if group_size > 0 and K % group_size == 0 and tuple(scales.shape) != (K // group_size, N):
+        raise ValueError(f"scales: expected shape {(K // group_size, N)}, got {tuple(scales.shape)}")
+    if zeros is not None:
+        _need(zeros, torch.float16, "zeros")
+        if tuple(zeros.shape) != tuple(scales.shape):
+            raise ValueError(f"zeros: expected the scales' shape {tuple(scales.shape)}, got {tuple(zeros.shape)}")
+    for name, t in (("packed_t", packed_t), ("scales", scales), ("zeros", zeros)):
+        if t is not None and t.device != dy.device:
+            raise ValueError(f"{name}: on {t.device}, but dy is on {dy.device}")
+    _need_cuda(("dy", dy))
+    return M, N, K
+
+
+def gemm_dx(dy: torch.Tensor, packed_t: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor], bits: int,
+            group_size: int, out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dX = dY W, the input gradient of gemm (dy bf16 [M][N], packed_t from transpose_packed)."""
+    M, N, K = _check_grad_args(dy, packed_t, scales, zeros, bits, group_size)
+    if out is not None:
+        _check_like(out, "out", (M, K), torch.bfloat16, dy.device)
+    with torch.cuda.device(dy.device):
+        if out is None:
+            out = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
+        ws = _own_workspace(ws, dy.device, M, N, K, 0, 0)
+        _check(load().lowbit_gemm_dx(M, N, K, bits, group_size, _ptr(dy), _ptr(packed_t), _ptr(scales), _ptr(zeros),
+                                     _ptr(out), _ptr(ws), ws.numel(), _stream()), "lowbit_gemm_dx")
+    return out
+
+
+def adapter_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint], p: torch.Tensor, packed_t: torch.Tensor,
+                     scales: torch.Tensor, zeros: Optional[torch.Tensor], bits: int, group_size: int,
+                     a: torch.Tensor, b: torch.Tensor, scaling: torch.Tensor, index: Optional[torch.Tensor] = None,
+                     dx: Optional[torch.Tensor] = None, da: Optional[torch.Tensor] = None,
+                     db: Optional[torch.Tensor] = None, need_dx: bool = True, ws: Optional[torch.Tensor] = None):
+    """Gradients of adapter_gemm: (dx [M][K], da [L][R][K], db [L][N][R]), all bf16.
+
+    x is the forward's input, or the Checkpoint it filled; p what it wrote. need_dx=False skips
+    dx (a first layer) and returns None in its place."""
+    M, N, K = _check_grad_args(dy, packed_t, scales, zeros, bits, group_size)
+    dev = dy.device
+    ad = _check_adapters(a, b, scaling, index, M, N, K, dev)
+    _check_like(p, "p", (M, ad.rank), torch.bfloat16, dev)
+    if isinstance(x, Checkpoint):
+        _check_checkpoint(x, M, K, dev, "x")
+        xs = (None, _ptr(x.codes), _ptr(x.exps))
+    else:
+        _check_like(x, "x", (M, K), torch.bfloat16, dev)
+        xs = (_ptr(x), None, None)
+    for name, t, shape in (("dx", dx, (M, K)), ("da", da, a.shape), ("db", db, b.shape)):
+        if t is not None:
+            _check_like(t, name, shape, torch.bfloat16, dev)
+    if dx is not None and not need_dx:
+        raise ValueError("dx: a buffer was passed, but need_dx is False")
+    with torch.cuda.device(dev):
+        if need_dx and dx is None:
+            dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        if da is None:
+            da = torch.empty_like(a)
+        if db is None:
+            db = torch.empty_like(b)
+        ws = _own_workspace(ws, dev, M, N, K, ad.num, ad.rank)
+        _check(load().lowbit_adapter_backward(M, N, K, bits, group_size, _ptr(dy), _ptr(packed_t), _ptr(scales),
+                                              _ptr(zeros), ctypes.byref(ad), *xs, _ptr(p), _ptr(dx), _ptr(da),
+                                              _ptr(db), _ptr(ws), ws.numel(), _stream()), "lowbit_adapter_backward")
+    return dx, da, db
 
 
 def device_status(clear: bool = True) -> int:

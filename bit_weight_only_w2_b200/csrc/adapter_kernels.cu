@@ -1,0 +1,781 @@
+// The stages around the fused adapter product: tokens sorted by adapter, the low-rank product
+// ("shrink"), the fp16 copy of the input with the slots' P, and the adapters' gradients.
+//
+// For one product of M tokens, each with an adapter a(m) of rank R (or none):
+//   p[m]  = scaling[a] * in[m] A_a^T            shrink, then summed and scaled by the copy pass
+//   out   = in W^T + p B_a^T                    gemm_kernel.cuh (kExtAdapter / kExtGrad)
+//   dA_a  = sum_{m in a} dp[m]^T x[m],  dB_a = sum_{m in a} dy[m]^T p[m]      wgrad
+// Everything is summed in fp32 in a fixed order (no atomics on results), so results do not depend
+// on timing.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "adapter_internal.h"
+#include "checkpoint.cuh"
+#include "sm100_ptx.cuh"
+
+namespace lowbit {
+namespace {
+
+constexpr int kSmsAssumed = 148;   // the workspace's size may not depend on the device
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ---------------------------------------------------------------------------------------------
+// Plan: the tokens of each adapter, and the slots of each token tile
+// ---------------------------------------------------------------------------------------------
+// One CTA per adapter counts the tokens of lower adapters (its start in the sorted order) and its
+// own, and writes its tokens in ascending order: every warp takes a contiguous range of the
+// tokens, counts its matches, and after one exchange of the counts compacts them by ballots.
+// Scanning all M indices once per adapter costs L * M * 4 bytes of L2 reads, little next to the
+// products for the L and M of a batch, and needs neither atomics nor a second launch.
+// One more CTA per token tile lists the distinct adapters of the tile in ascending order (its
+// "slots") from a bitmap, and each token's slot.
+//
+// Shrink blocks: adapter a's tokens [seg[a], seg[a + 1]) get the block numbers seg[a] / 64 + a + i,
+// i < ceil(count / 64), which never collide: the next adapter starts at
+// floor(seg[a + 1] / 64) + a + 1, and ceil(count / 64) <= floor(seg[a + 1] / 64) -
+// floor(seg[a] / 64) + 1. Numbers in between stay empty (count 0).
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+__device__ __forceinline__ int adapter_of(const int* __restrict__ index, int m, int num) {
+    const int a = index ? index[m] : 0;
+    return a >= 0 && a < num ? a : -1;   // anything else: no adapter
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+    plan_kernel(const int* __restrict__ index, int M, int num, int tile_tokens, int slot_pitch, int num_blocks,
+                int* __restrict__ perm, int* __restrict__ seg, int4* __restrict__ blocks,
+                int* __restrict__ tile_slots, int* __restrict__ slot_adapter, int* __restrict__ token_slot) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x < static_cast<unsigned>(num)) {
+        const int a = blockIdx.x;
+        __shared__ int warp_eq[kPlanWarps], warp_lt[kPlanWarps];
+        const int per = ((M + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
+        const int m0 = min(M, warp * per), m1 = min(M, m0 + per);
+        int eq = 0, lt = 0;
+#pragma unroll 4
+        for (int m = m0 + lane; m < m1; m += 32) {
+            const int v = adapter_of(index, m, num);
+            eq += v == a;
+            lt += v >= 0 && v < a;
+        }
+        eq = __reduce_add_sync(0xffffffffu, eq);
+        lt = __reduce_add_sync(0xffffffffu, lt);
+        if (lane == 0) {
+            warp_eq[warp] = eq;
+            warp_lt[warp] = lt;
+        }
+        __syncthreads();
+        int start = 0, count = 0, before = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanWarps; ++w) {
+            start += warp_lt[w];
+            before += w < warp ? warp_eq[w] : 0;
+            count += warp_eq[w];
+        }
+        int at = start + before;
+        for (int mb = m0; mb < m1; mb += 32) {
+            const int m = mb + lane;
+            const bool mine = m < m1 && adapter_of(index, m, num) == a;
+            const unsigned votes = __ballot_sync(0xffffffffu, mine);
+            if (mine) perm[at + __popc(votes & ((1u << lane) - 1u))] = m;
+            at += __popc(votes);
+        }
+        const int first = start / kShrinkTokens + a;
+        const int last = a + 1 == num ? num_blocks : (start + count) / kShrinkTokens + a + 1;
+        for (int i = threadIdx.x; first + i < last; i += kPlanThreads)
+            blocks[first + i] = make_int4(a, start + i * kShrinkTokens, min(kShrinkTokens, count - i * kShrinkTokens), 0);
+        if (threadIdx.x == 0) {
+            seg[a] = start;
+            if (a + 1 == num) seg[num] = start + count;
+        }
+        return;
+    }
+    // ---- slots of one tile
+    const int tile = blockIdx.x - num;
+    __shared__ unsigned bits[kMaxAdapters / 32];
+    __shared__ int base[kMaxAdapters / 32 + 1];
+    const int words = (num + 31) / 32;
+    for (int i = threadIdx.x; i < words; i += kPlanThreads) bits[i] = 0;
+    __syncthreads();
+    const int m0 = tile * tile_tokens, m1 = min(M, m0 + tile_tokens);
+    for (int m = m0 + static_cast<int>(threadIdx.x); m < m1; m += kPlanThreads) {
+        const int v = adapter_of(index, m, num);
+        if (v >= 0) atomicOr(&bits[v >> 5], 1u << (v & 31));
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i <= words; i += kPlanThreads) {
+        int n = 0;
+        for (int j = 0; j < i; ++j) n += __popc(bits[j]);
+        base[i] = n;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) tile_slots[tile] = base[words];
+    for (int i = threadIdx.x; i < words; i += kPlanThreads) {
+        unsigned b = bits[i];
+        int at = base[i];
+        while (b) {
+            slot_adapter[static_cast<size_t>(tile) * slot_pitch + at++] = i * 32 + __ffs(b) - 1;
+            b &= b - 1;
+        }
+    }
+    for (int m = m0 + static_cast<int>(threadIdx.x); m < m1; m += kPlanThreads) {
+        const int v = adapter_of(index, m, num);
+        token_slot[m] = v < 0 ? -1 : base[v >> 5] + __popc(bits[v >> 5] & ((1u << (v & 31)) - 1u));
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Shrink: partial[s][m][0..Rp) = in[m][slice s] * side_a[slice s]^T for the tokens of each block
+// ---------------------------------------------------------------------------------------------
+// R is at most 128, so the product reads each input row once and is bound by that stream (and,
+// for few tokens per adapter, by the adapters' rows): warp-level MMAs on tiles that cp.async
+// gathers into shared memory keep up with it, and tcgen05's 128-row tiles would be mostly padding.
+// A block is up to 64 tokens of one adapter; the reduction is cut into slices over gridDim.y so
+// that a few blocks fill the GPU, and the slices' fp32 partials are added in order by the copy
+// pass that follows. KMAJOR: the adapter's side is [R][red] (A); otherwise [red][R] (B).
+constexpr int kShrinkThreads = 128;
+constexpr int kShrinkStages = 4;
+__host__ __device__ constexpr int shrink_smem(int rp) { return kShrinkStages * (kShrinkTokens * 128 + rp * 128); }
+
+template <int RP, bool KMAJOR>
+__global__ void __launch_bounds__(kShrinkThreads)
+    shrink_kernel(const __nv_bfloat16* __restrict__ in, const __nv_bfloat16* __restrict__ side, int M, int red, int R,
+                  int kslice, const int* __restrict__ perm, const int4* __restrict__ blocks,
+                  float* __restrict__ partial) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ int tok[kShrinkTokens];
+    constexpr int kXBytes = kShrinkTokens * 128, kStage = kXBytes + RP * 128;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int4 blk = blocks[blockIdx.x];
+    const int count = blk.z;
+    if (count <= 0) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid < kShrinkTokens) tok[tid] = perm[blk.y + min(tid, count - 1)];
+    __syncthreads();
+    const int k_begin = blockIdx.y * kslice, k_end = min(red, k_begin + kslice);
+    const int steps = k_end > k_begin ? (k_end - k_begin + 63) / 64 : 0;
+    const __nv_bfloat16* wside = side + static_cast<size_t>(blk.x) * R * red;
+    const uint32_t s0 = smem_u32(smem);
+    auto load = [&](int step) {
+        const uint32_t st = s0 + (step % kShrinkStages) * kStage;
+        const int k0 = k_begin + step * 64;
+#pragma unroll
+        for (int i = 0; i < kShrinkTokens * 8 / kShrinkThreads; ++i) {
+            const int id = tid + i * kShrinkThreads, row = id >> 3, ch = id & 7;
+            const int k = k0 + ch * 8;
+            const bool ok = row < count && k < k_end;
+            cp_async16(st + row * 128 + ((ch ^ (row & 7)) << 4),
+                       in + (ok ? static_cast<size_t>(tok[row]) * red + k : 0), ok);
+        }
+        const uint32_t ws = st + kXBytes;
+#pragma unroll
+        for (int i = 0; i < RP * 8 / kShrinkThreads; ++i) {
+            const int id = tid + i * kShrinkThreads;
+            if (KMAJOR) {
+                const int row = id >> 3, ch = id & 7;
+                const int k = k0 + ch * 8;
+                const bool ok = row < R && k < k_end;
+                cp_async16(ws + row * 128 + ((ch ^ (row & 7)) << 4), wside + (ok ? static_cast<size_t>(row) * red + k : 0),
+                           ok);
+            } else {
+                constexpr int kCh = RP / 8;
+                const int kr = id / kCh, ch = id % kCh;
+                const bool ok = ch * 8 < R && k0 + kr < k_end;
+                cp_async16(ws + kr * RP * 2 + ((ch ^ (kr & (kCh < 8 ? kCh - 1 : 7))) << 4),
+                           wside + (ok ? static_cast<size_t>(k0 + kr) * R + ch * 8 : 0), ok);
+            }
+        }
+    };
+    float acc[RP / 8][4];
+#pragma unroll
+    for (int i = 0; i < RP / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    const bool active = warp * 16 < count;
+#pragma unroll
+    for (int i = 0; i < kShrinkStages - 1; ++i) {
+        if (i < steps) load(i);
+        cp_async_commit();
+    }
+    for (int step = 0; step < steps; ++step) {
+        cp_async_wait<kShrinkStages - 2>();
+        __syncthreads();
+        if (step + kShrinkStages - 1 < steps) load(step + kShrinkStages - 1);
+        cp_async_commit();
+        if (!active) continue;
+        const uint32_t xs = s0 + (step % kShrinkStages) * kStage, ws = xs + kXBytes;
+#pragma unroll
+        for (int k16 = 0; k16 < 4; ++k16) {
+            uint32_t a[4];
+            const int xr = warp * 16 + (lane & 15), xc = k16 * 2 + (lane >> 4);
+            ldsm_x4(xs + xr * 128 + ((xc ^ (xr & 7)) << 4), a);
+#pragma unroll
+            for (int rt = 0; rt < RP / 16; ++rt) {
+                uint32_t b[4];
+                if (KMAJOR) {
+                    const int r = rt * 16 + (lane & 7) + ((lane >> 4) << 3), ch = k16 * 2 + ((lane >> 3) & 1);
+                    ldsm_x4(ws + r * 128 + ((ch ^ (r & 7)) << 4), b);
+                } else {
+                    constexpr int kCh = RP / 8;
+                    const int kr = k16 * 16 + (lane & 15), ch = rt * 2 + (lane >> 4);
+                    ldsm_x4_trans(ws + kr * RP * 2 + ((ch ^ (kr & (kCh < 8 ? kCh - 1 : 7))) << 4), b);
+                }
+                mma_16816(acc[2 * rt], a, b[0], b[1]);
+                mma_16816(acc[2 * rt + 1], a, b[2], b[3]);
+            }
+        }
+    }
+    if (!active) return;
+    float* out = partial + static_cast<size_t>(blockIdx.y) * M * RP;
+    const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int row = warp * 16 + g + 8 * half;
+        if (row < count) {
+            float* dst = out + static_cast<size_t>(tok[row]) * RP + 2 * q;
+#pragma unroll
+            for (int i = 0; i < RP / 8; ++i)
+                *reinterpret_cast<float2*>(dst + i * 8) = make_float2(acc[i][2 * half], acc[i][2 * half + 1]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Copy pass: fp16 copy of the input, the slots' P, the kept p and the 8-bit copy
+// ---------------------------------------------------------------------------------------------
+// One CTA per token row, as the plain GEMM's conversion (the row's power of two 2^e comes from its
+// largest |value|). P is multiplied by 2^-e as well, since the epilogue multiplies the whole sum
+// by 2^e; that is exact in bf16. p itself is rounded to bf16 once, as the MMA's operand and as
+// what the backward pass reads: 2^-9 of the low-rank term at most, like the output's own rounding.
+struct SideArgs {
+    const float* partial;      // nullptr: no adapters
+    int ksplit;
+    int rp_log2, rank, num;
+    const float* scaling;
+    const int* index;
+    const int* token_slot;
+    const int* tile_slots;
+    int tile_log2;
+    __nv_bfloat16* pslots;
+    long long p_cols;
+    __nv_bfloat16* p_out;      // nullptr: not kept
+    uint8_t* codes;            // nullptr: no 8-bit copy
+    uint8_t* exps;
+};
+
+constexpr int kConvThreads = 256;
+
+template <int PER>
+__global__ void __launch_bounds__(kConvThreads)
+    convert_side_kernel(const uint4* __restrict__ in, int M, int K8, int K8p, uint4* __restrict__ xh,
+                        float* __restrict__ rowmul, const SideArgs s) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int row = blockIdx.x;
+    const uint4* src = in + static_cast<size_t>(row) * K8;
+    uint4* dst = xh + static_cast<size_t>(row) * K8p;
+    uint4 v[PER > 0 ? PER : 1];
+    uint32_t mx = 0;
+    auto amax = [](const uint4& a, uint32_t m) {
+        m = max(m, max(a.x & 0x7FFFu, (a.x >> 16) & 0x7FFFu));
+        m = max(m, max(a.y & 0x7FFFu, (a.y >> 16) & 0x7FFFu));
+        m = max(m, max(a.z & 0x7FFFu, (a.z >> 16) & 0x7FFFu));
+        return max(m, max(a.w & 0x7FFFu, (a.w >> 16) & 0x7FFFu));
+    };
+    if (PER > 0) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = threadIdx.x + j * kConvThreads;
+            v[j] = i < K8 ? src[i] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) mx = amax(v[j], mx);
+    } else {
+        for (int i = threadIdx.x; i < K8; i += kConvThreads) mx = amax(src[i], mx);
+    }
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    __shared__ uint32_t warp_max[kConvThreads / 32];
+    __shared__ float prow[kMaxRank];
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = mx;
+    // this token's low-rank product: the slices' partials in order, times its adapter's scaling
+    int slot = -1;
+    if (s.partial) {
+        slot = s.token_slot[row];
+        const int r = threadIdx.x;
+        if (r < (1 << s.rp_log2)) {
+            float p = 0.f;
+            if (slot >= 0) {
+                const float* part = s.partial + (static_cast<size_t>(row) << s.rp_log2) + r;
+                for (int k = 0; k < s.ksplit; ++k) p += part[(static_cast<size_t>(k) * M) << s.rp_log2];
+                p *= s.scaling[s.index ? s.index[row] : 0];
+            }
+            prow[r] = p;
+            if (s.p_out && r < s.rank) s.p_out[static_cast<size_t>(row) * s.rank + r] = __float2bfloat16_rn(p);
+        }
+    }
+    __syncthreads();
+    mx = 0;
+#pragma unroll
+    for (int w = 0; w < kConvThreads / 32; ++w) mx = max(mx, warp_max[w]);
+    const int E = static_cast<int>(mx >> 7);              // biased exponent of the largest |value|
+    int e = (mx == 0 || E >= 255) ? 0 : E - 142;          // largest * 2^-e in [2^15, 2^16)
+    e = max(-100, min(112, e));
+    const float scale = __int_as_float((127 - e) << 23);  // 2^-e
+    auto cvt = [&](uint32_t w) {
+        const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xFFFF0000u) * scale);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    };
+    auto emit = [&](int i, const uint4& a, bool valid) {
+        if (i < K8p) dst[i] = make_uint4(cvt(a.x), cvt(a.y), cvt(a.z), cvt(a.w));
+        if (s.codes) {   // four neighbouring lanes hold a block of 32 values (K8 is a multiple of 4)
+            uint8_t ex;
+            const uint2 c = checkpoint_encode8(a, ex);
+            if (valid) {
+                const size_t at = static_cast<size_t>(row) * K8 + i;
+                reinterpret_cast<uint2*>(s.codes)[at] = c;
+                if ((i & 3) == 0) s.exps[at >> 2] = ex;
+            }
+        }
+    };
+    if (PER > 0) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = threadIdx.x + j * kConvThreads;
+            emit(i, v[j], i < K8);
+        }
+    } else {
+        // (whole warps take part in every round: the 8-bit copy exchanges between lanes)
+        const int rounds = (K8p + kConvThreads - 1) / kConvThreads;
+        for (int j = 0; j < rounds; ++j) {
+            const int i = threadIdx.x + j * kConvThreads;
+            emit(i, i < K8 ? src[i] : make_uint4(0, 0, 0, 0), i < K8);
+        }
+    }
+    if (threadIdx.x == 0) rowmul[row] = __int_as_float((127 + e) << 23);   // 2^e
+    if (s.partial) {
+        const int cols = s.tile_slots[row >> s.tile_log2] << s.rp_log2;    // the columns the MMA reads
+        uint4* pd = reinterpret_cast<uint4*>(s.pslots + static_cast<size_t>(row) * s.p_cols);
+        for (int c = threadIdx.x; c < cols / 8; c += kConvThreads) {
+            uint4 o = make_uint4(0, 0, 0, 0);
+            if ((c * 8) >> s.rp_log2 == slot) {
+                const float* pr = prow + ((c * 8) & ((1 << s.rp_log2) - 1));
+                uint32_t u[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    // round p first (what p_out holds), then the exact power of two
+                    const float lo = __bfloat162float(__float2bfloat16_rn(pr[2 * q])) * scale;
+                    const float hi = __bfloat162float(__float2bfloat16_rn(pr[2 * q + 1])) * scale;
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+                    u[q] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                o = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+            pd[c] = o;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Adapter gradients: dA_a[r][k] = sum dp[m][r] x[m][k], dB_a[n][r] = sum dy[m][n] p[m][r]
+// ---------------------------------------------------------------------------------------------
+// Both are the same product G^T P over an adapter's tokens, G = x or dy. It reads G once, so it is
+// bound by that stream at small ranks; warp-level MMAs take both operands transposed out of
+// shared memory (ldmatrix.trans), which lets the token rows be gathered as they lie. A CTA owns 128
+// columns of G and all R columns of P; the tokens are cut over the CTAs of a cluster, whose
+// fp32 tiles are added in rank order through distributed shared memory. x may be the 8-bit copy:
+// its codes are widened to bf16 (exactly) on the way into the MMA's tile.
+struct WgradPart {
+    const void* G;             // bf16 [M][C], or the 8-bit codes
+    const uint8_t* exps;       // the 8-bit copy's exponents, nullptr for bf16
+    const __nv_bfloat16* P;    // [M][R]
+    __nv_bfloat16* out;        // [a][R][C] (transposed) or [a][C][R]
+    int C;
+    int tiles;                 // ceil(C / 128)
+};
+struct WgradArgs {
+    WgradPart part[2];         // dA (out transposed), dB
+    int R;
+    const int* perm;
+    const int* seg;
+};
+constexpr int kWgradThreads = 256;
+constexpr int kWgradStages = 3;
+constexpr int kWgradG = 64 * 256;                 // 64 tokens x 128 columns, bf16
+__host__ __device__ constexpr int wgrad_stage(int rp) { return kWgradG + 64 * rp * 2; }
+__host__ __device__ constexpr int wgrad_smem(int rp) { return kWgradStages * wgrad_stage(rp) + kWgradG; }
+
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int RP>
+__global__ void __launch_bounds__(kWgradThreads) wgrad_kernel(const WgradArgs w) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr int kStage = wgrad_stage(RP);
+    constexpr int kCh = RP / 8;
+    constexpr int kAccPitch = RP + 4;
+    static_assert(128 * kAccPitch * 4 <= kWgradStages * kStage, "fp32 tile");
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const bool first = blockIdx.y < static_cast<unsigned>(w.part[0].tiles);
+    const WgradPart part = first ? w.part[0] : w.part[1];
+    const int c0 = (first ? blockIdx.y : blockIdx.y - w.part[0].tiles) * 128;
+    const int a = blockIdx.z, rank = blockIdx.x, ranks = gridDim.x;
+    const int seg0 = w.seg[a], count = w.seg[a + 1] - seg0;
+    const int per = ((count + 63) / 64 + ranks - 1) / ranks * 64;
+    const int t_begin = min(count, rank * per), t_end = min(count, t_begin + per);
+    const int steps = (t_end - t_begin + 63) / 64;
+    const int* perm = w.perm + seg0;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool q8 = part.exps != nullptr;
+    const uint32_t s0 = smem_u32(smem);
+    const uint32_t wide = s0 + kWgradStages * kStage;     // the widened tile of an 8-bit stage
+    auto load = [&](int step) {
+        const uint32_t st = s0 + (step % kWgradStages) * kStage;
+        const int t0 = t_begin + step * 64;
+        if (!q8) {
+            const __nv_bfloat16* G = static_cast<const __nv_bfloat16*>(part.G);
+#pragma unroll
+            for (int i = 0; i < 64 * 16 / kWgradThreads; ++i) {
+                const int id = tid + i * kWgradThreads, row = id >> 4, ch = id & 15;
+                const bool ok = t0 + row < t_end && c0 + ch * 8 < part.C;
+                const size_t src = ok ? static_cast<size_t>(perm[t0 + row]) * part.C + c0 + ch * 8 : 0;
+                cp_async16(st + row * 256 + ((ch ^ (row & 7)) << 4), G + src, ok);
+            }
+        } else {
+            const uint8_t* G = static_cast<const uint8_t*>(part.G);
+#pragma unroll
+            for (int i = 0; i < 64 * 8 / kWgradThreads; ++i) {
+                const int id = tid + i * kWgradThreads, row = id >> 3, ch = id & 7;
+                const bool ok = t0 + row < t_end && c0 + ch * 16 < part.C;
+                const size_t src = ok ? static_cast<size_t>(perm[t0 + row]) * part.C + c0 + ch * 16 : 0;
+                cp_async16(st + row * 128 + ch * 16, G + src, ok);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < (64 * kCh + kWgradThreads - 1) / kWgradThreads; ++i) {
+            const int id = tid + i * kWgradThreads, row = id / kCh, ch = id % kCh;
+            if (row < 64) {
+                const bool ok = t0 + row < t_end && ch * 8 < w.R;
+                const size_t src = ok ? static_cast<size_t>(perm[t0 + row]) * w.R + ch * 8 : 0;
+                cp_async16(st + kWgradG + row * RP * 2 + ((ch ^ (row & (kCh < 8 ? kCh - 1 : 7))) << 4), part.P + src, ok);
+            }
+        }
+    };
+    // widen one 8-bit stage: thread -> 32 columns (one exponent) of a token row
+    auto widen = [&](int step) {
+        const uint8_t* st = smem + (step % kWgradStages) * kStage;
+        const int t0 = t_begin + step * 64;
+        const int row = tid >> 2, blk = tid & 3;
+        uint32_t ex = 0;
+        if (t0 + row < t_end && c0 + blk * 32 < part.C)
+            ex = part.exps[(static_cast<size_t>(perm[t0 + row]) * part.C + c0 + blk * 32) >> 5];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 c = *reinterpret_cast<const uint4*>(st + row * 128 + blk * 32 + i * 16);
+            const uint4 lo = checkpoint_decode8(make_uint2(c.x, c.y), ex), hi = checkpoint_decode8(make_uint2(c.z, c.w), ex);
+            uint8_t* dst = smem + kWgradStages * kStage + row * 256;
+            const int ch = blk * 4 + i * 2;
+            *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) << 4)) = lo;
+            *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (row & 7)) << 4)) = hi;
+        }
+    };
+    float acc[RP / 8][4];
+#pragma unroll
+    for (int i = 0; i < RP / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWgradStages - 1; ++i) {
+        if (i < steps) load(i);
+        cp_async_commit();
+    }
+    for (int step = 0; step < steps; ++step) {
+        cp_async_wait<kWgradStages - 2>();
+        __syncthreads();
+        if (step + kWgradStages - 1 < steps) load(step + kWgradStages - 1);
+        cp_async_commit();
+        const uint32_t st = s0 + (step % kWgradStages) * kStage;
+        uint32_t gs = st;
+        if (q8) {
+            widen(step);
+            __syncthreads();
+            gs = wide;
+        }
+#pragma unroll
+        for (int k16 = 0; k16 < 4; ++k16) {
+            uint32_t g[4];
+            const int tr = k16 * 16 + (lane & 7) + ((lane >> 4) << 3), gc = warp * 2 + ((lane >> 3) & 1);
+            ldsm_x4_trans(gs + tr * 256 + ((gc ^ (tr & 7)) << 4), g);
+            const int pr = k16 * 16 + (lane & 15);
+#pragma unroll
+            for (int rt = 0; rt < RP / 16; ++rt) {
+                uint32_t b[4];
+                const int ch = rt * 2 + (lane >> 4);
+                ldsm_x4_trans(st + kWgradG + pr * RP * 2 + ((ch ^ (pr & (kCh < 8 ? kCh - 1 : 7))) << 4), b);
+                mma_16816(acc[2 * rt], g, b[0], b[1]);
+                mma_16816(acc[2 * rt + 1], g, b[2], b[3]);
+            }
+        }
+        if (q8) __syncthreads();   // the widened tile is rewritten by the next step
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    float* tile = reinterpret_cast<float*>(smem);
+    const int gr = lane >> 2, q = lane & 3;
+#pragma unroll
+    for (int i = 0; i < RP / 8; ++i)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+            *reinterpret_cast<float2*>(tile + (warp * 16 + gr + 8 * half) * kAccPitch + i * 8 + 2 * q) =
+                make_float2(acc[i][2 * half], acc[i][2 * half + 1]);
+    if (ranks > 1) cluster_sync_all();
+    else __syncthreads();
+    // rank r finishes 128 / ranks of the tile's columns
+    const int mine = 128 / ranks, cb = rank * mine;
+    auto total = [&](int c, int r) {
+        if (ranks == 1) return tile[c * kAccPitch + r];
+        const uint32_t at = s0 + (c * kAccPitch + r) * 4;
+        float v = 0.f;
+        for (int k = 0; k < ranks; ++k) v += ld_shared_cluster_f32(map_shared_rank(at, k));
+        return v;
+    };
+    const int R = w.R;
+    if (first) {   // dA [a][R][C]: neighbouring threads take neighbouring columns
+        const int half = mine / 2;
+        for (int i = tid; i < half * R; i += kWgradThreads) {
+            const int c = cb + i % half * 2, r = i / half;
+            if (c0 + c < part.C)
+                *reinterpret_cast<__nv_bfloat162*>(part.out + (static_cast<size_t>(a) * R + r) * part.C + c0 + c) =
+                    __floats2bfloat162_rn(total(c, r), total(c + 1, r));
+        }
+    } else {       // dB [a][C][R]
+        const int half = R / 2;
+        for (int i = tid; i < mine * half; i += kWgradThreads) {
+            const int c = cb + i / half, r = i % half * 2;
+            if (c0 + c < part.C)
+                *reinterpret_cast<__nv_bfloat162*>(part.out + (static_cast<size_t>(a) * part.C + c0 + c) * R + r) =
+                    __floats2bfloat162_rn(total(c, r), total(c, r + 1));
+        }
+    }
+    if (ranks > 1) cluster_sync_all();   // the other ranks may still read this CTA's tile
+}
+
+// ---------------------------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------------------------
+template <class... Args, class... Given>
+lowbit_status launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, int smem, int cluster_x, cudaStream_t stream,
+                         Given... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster_x;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster_x > 1 ? 2 : 1;
+    if (take_injected_failure(kInjectLaunch)) return LOWBIT_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(args)...) == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
+}
+
+// Allows `fn` its dynamic shared memory, once per device (`devices`: one bit per device that has it).
+template <class F>
+bool allow_smem(F fn, int bytes, std::atomic<uint64_t>& devices) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+    if (bit && (devices.load(std::memory_order_acquire) & bit)) return true;
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        cudaSuccess)
+        return false;
+    devices.fetch_or(bit, std::memory_order_acq_rel);
+    return true;
+}
+
+template <int RP, bool KMAJOR>
+lowbit_status shrink_launch(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
+    const ExtWorkspace& w = b.w;
+    auto fn = shrink_kernel<RP, KMAJOR>;
+    static std::atomic<uint64_t> devices{0};
+    if (!allow_smem(fn, shrink_smem(RP), devices)) return LOWBIT_ERR_CUDA;
+    return launch_pdl(fn, dim3(static_cast<unsigned>(w.num_blocks), static_cast<unsigned>(w.ksplit), 1), kShrinkThreads,
+                      shrink_smem(RP), 1, stream, static_cast<const __nv_bfloat16*>(e.in),
+                      static_cast<const __nv_bfloat16*>(e.grad ? e.ad.B : e.ad.A), static_cast<int>(e.M),
+                      static_cast<int>(e.red), e.ad.rank, static_cast<int>(w.kslice), b.at<int>(w.perm),
+                      b.at<int4>(w.blocks), b.at<float>(w.partial));
+}
+
+template <int RP>
+lowbit_status wgrad_launch(const WgradArgs& args, int ranks, int num, cudaStream_t stream) {
+    auto fn = wgrad_kernel<RP>;
+    static std::atomic<uint64_t> devices{0};
+    if (!allow_smem(fn, wgrad_smem(RP), devices)) return LOWBIT_ERR_CUDA;
+    return launch_pdl(fn, dim3(ranks, args.part[0].tiles + args.part[1].tiles, num), kWgradThreads, wgrad_smem(RP), ranks,
+                      stream, args);
+}
+
+}  // namespace
+
+ExtWorkspace ext_workspace(int64_t M, int64_t red, int num, int rank) {
+    ExtWorkspace w = {};
+    w.red64 = (red + 63) / 64 * 64;
+    w.tile_tokens = ext_tile_tokens(M);
+    w.m_tiles = (M + w.tile_tokens - 1) / w.tile_tokens;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    w.xh = take(static_cast<size_t>(M) * w.red64 * 2);
+    w.rowmul = take(static_cast<size_t>(M) * 4);
+    if (num > 0) {
+        const int rp = 1 << slot_log2(rank);
+        w.num_blocks = M / kShrinkTokens + num + 1;
+        // K slices: about two CTAs per SM over the blocks that hold tokens, at least 256 of K each
+        const int64_t busy = M / kShrinkTokens + (num < M ? num : M);
+        int64_t ks = (2 * kSmsAssumed + busy - 1) / (busy > 0 ? busy : 1);
+        if (ks > w.red64 / 256) ks = w.red64 / 256;
+        if (ks > 16) ks = 16;
+        if (ks < 1) ks = 1;
+        w.kslice = ((w.red64 + ks - 1) / ks + 63) / 64 * 64;
+        w.ksplit = static_cast<int>((w.red64 + w.kslice - 1) / w.kslice);
+        w.slot_pitch = num < w.tile_tokens ? num : w.tile_tokens;
+        w.p_cols = (w.slot_pitch * rp + 63) / 64 * 64;
+        w.perm = take(static_cast<size_t>(M) * 4);
+        w.seg = take((static_cast<size_t>(num) + 1) * 4);
+        w.blocks = take(static_cast<size_t>(w.num_blocks) * 16);
+        w.tile_slots = take(static_cast<size_t>(w.m_tiles) * 4);
+        w.slot_adapter = take(static_cast<size_t>(w.m_tiles) * w.slot_pitch * 4);
+        w.token_slot = take(static_cast<size_t>(M) * 4);
+        w.partial = take(static_cast<size_t>(w.ksplit) * M * rp * 4);
+        w.pslots = take(static_cast<size_t>(M) * w.p_cols * 2);
+        w.p = take(static_cast<size_t>(M) * rank * 2);
+    }
+    w.total = at;
+    return w;
+}
+
+lowbit_status launch_plan(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
+    const ExtWorkspace& w = b.w;
+    return launch_pdl(plan_kernel, dim3(static_cast<unsigned>(e.ad.num + w.m_tiles), 1, 1), kPlanThreads, 0, 1, stream,
+                      e.ad.index, static_cast<int>(e.M), e.ad.num, w.tile_tokens, static_cast<int>(w.slot_pitch),
+                      static_cast<int>(w.num_blocks), b.at<int>(w.perm), b.at<int>(w.seg), b.at<int4>(w.blocks),
+                      b.at<int>(w.tile_slots), b.at<int>(w.slot_adapter), b.at<int>(w.token_slot));
+}
+
+lowbit_status launch_shrink(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
+    switch (slot_log2(e.ad.rank)) {
+        case 4: return e.grad ? shrink_launch<16, false>(e, b, stream) : shrink_launch<16, true>(e, b, stream);
+        case 5: return e.grad ? shrink_launch<32, false>(e, b, stream) : shrink_launch<32, true>(e, b, stream);
+        case 6: return e.grad ? shrink_launch<64, false>(e, b, stream) : shrink_launch<64, true>(e, b, stream);
+        default: return e.grad ? shrink_launch<128, false>(e, b, stream) : shrink_launch<128, true>(e, b, stream);
+    }
+}
+
+lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
+    const ExtWorkspace& w = b.w;
+    SideArgs s = {};
+    if (e.ad.num > 0) {
+        s.partial = b.at<float>(w.partial);
+        s.ksplit = w.ksplit;
+        s.rp_log2 = slot_log2(e.ad.rank);
+        s.rank = e.ad.rank;
+        s.num = e.ad.num;
+        s.scaling = e.ad.scaling;
+        s.index = e.ad.index;
+        s.token_slot = b.at<int>(w.token_slot);
+        s.tile_slots = b.at<int>(w.tile_slots);
+        while ((1 << s.tile_log2) < w.tile_tokens) ++s.tile_log2;
+        s.pslots = b.at<__nv_bfloat16>(w.pslots);
+        s.p_cols = w.p_cols;
+        s.p_out = static_cast<__nv_bfloat16*>(e.p_out);
+    }
+    s.codes = e.ck_codes;
+    s.exps = e.ck_exps;
+    const int K8 = static_cast<int>(e.red / 8), K8p = static_cast<int>(w.red64 / 8);
+    const dim3 grid(static_cast<unsigned>(e.M), 1, 1);
+    const uint4* in = static_cast<const uint4*>(e.in);
+    uint4* xh = b.at<uint4>(w.xh);
+    float* rm = b.at<float>(w.rowmul);
+    auto go = [&](auto fn) {
+        return launch_pdl(fn, grid, kConvThreads, 0, 1, stream, in, static_cast<int>(e.M), K8, K8p, xh, rm, s);
+    };
+    if (K8p <= kConvThreads) return go(convert_side_kernel<1>);
+    if (K8p <= 2 * kConvThreads) return go(convert_side_kernel<2>);
+    if (K8p <= 4 * kConvThreads) return go(convert_side_kernel<4>);
+    if (K8p <= 8 * kConvThreads) return go(convert_side_kernel<8>);
+    return go(convert_side_kernel<0>);
+}
+
+lowbit_status launch_wgrad(const WgradProblem& g, const ExtBuffers& b, cudaStream_t stream) {
+    WgradArgs a = {};
+    a.part[0].G = g.x ? g.x : static_cast<const void*>(g.ck_codes);
+    a.part[0].exps = g.x ? nullptr : g.ck_exps;
+    a.part[0].P = static_cast<const __nv_bfloat16*>(g.dp);
+    a.part[0].out = static_cast<__nv_bfloat16*>(g.dA);
+    a.part[0].C = static_cast<int>(g.K);
+    a.part[0].tiles = static_cast<int>((g.K + 127) / 128);
+    a.part[1].G = g.dy;
+    a.part[1].P = static_cast<const __nv_bfloat16*>(g.p);
+    a.part[1].out = static_cast<__nv_bfloat16*>(g.dB);
+    a.part[1].C = static_cast<int>(g.N);
+    a.part[1].tiles = static_cast<int>((g.N + 127) / 128);
+    a.R = g.rank;
+    a.perm = b.at<int>(b.w.perm);
+    a.seg = b.at<int>(b.w.seg);
+    // token slices per tile: enough CTAs for two per SM, slices of at least two 64-token steps
+    const int64_t ctas = static_cast<int64_t>(a.part[0].tiles + a.part[1].tiles) * g.num;
+    int ranks = 1;
+    while (ranks < 8 && ctas * ranks < 2 * num_sms() && g.M / g.num >= 256 * ranks) ranks *= 2;
+    switch (slot_log2(g.rank)) {
+        case 4: return wgrad_launch<16>(a, ranks, g.num, stream);
+        case 5: return wgrad_launch<32>(a, ranks, g.num, stream);
+        case 6: return wgrad_launch<64>(a, ranks, g.num, stream);
+        default: return wgrad_launch<128>(a, ranks, g.num, stream);
+    }
+}
+
+}  // namespace lowbit

@@ -1,0 +1,177 @@
+// Launch of the tensor-memory kernel's adapter and gradient variants (kExtAdapter, kExtGrad): tile
+// choice, tensor maps and launch. Included by one translation unit per code width and direction,
+// so that the instantiations build in parallel.
+#pragma once
+
+#include <atomic>
+
+#include "adapter_internal.h"
+#include "gemm_kernel.cuh"
+
+namespace lowbit {
+namespace {
+
+template <int BITS, int GS, int BT, bool PAIR, int EXT>
+lowbit_status ext_launch(const ExtProblem& e, const ExtBuffers& b, int rows, int ksplit, cudaStream_t stream) {
+    using C = Cfg<BITS, GS, BT, PAIR>;
+    auto kernel = lowbit_gemm_kernel<BITS, GS, BT, PAIR, EXT>;
+    const void* fn = reinterpret_cast<const void*>(kernel);
+    // the shared-memory opt-in is per device: one bit per device that has it
+    static std::atomic<uint64_t> attr_devices{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
+    const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+    if (!bit || !(attr_devices.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+            return LOWBIT_ERR_CUDA;
+        attr_devices.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    const ExtWorkspace& w = b.w;
+    const uint64_t M = e.M, R = e.rows;
+    const uint64_t red_words = EXT == kExtGrad ? uint64_t(e.red + 127) / 128 * 128 * BITS / 32 : uint64_t(e.red) * BITS / 32;
+    const CUtensorMapSwizzle wswz = C::kWRowBytes == 16   ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                    : C::kWRowBytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                          : CU_TENSOR_MAP_SWIZZLE_64B;
+    CUtensorMap mx, mw, ms, mz, my;
+    ExtParams p = {};
+    const uint32_t xbox[3] = {64, static_cast<uint32_t>(C::kXRows), 2};
+    const uint64_t xdims[3] = {64, M, static_cast<uint64_t>(w.red64) / 64};
+    const uint64_t xstr[2] = {static_cast<uint64_t>(w.red64) * 2, 128};
+    bool ok = make_map_3d(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, b.at<void>(w.xh), xdims, xstr, xbox,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
+    ok = ok && make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, e.words, red_words, R, red_words * 4,
+                           C::kWordsPerRow, rows, wswz);
+    ok = ok && make_map_2d(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, e.scales, e.N, e.K / GS, uint64_t(e.N) * 2,
+                           kBlockN, C::kGroupsPerStage, CU_TENSOR_MAP_SWIZZLE_NONE);
+    mz = ms;
+    if (BITS == 4)
+        ok = ok && make_map_2d(&mz, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, e.zeros, e.N, e.K / GS, uint64_t(e.N) * 2,
+                               kBlockN, C::kGroupsPerStage, CU_TENSOR_MAP_SWIZZLE_NONE);
+    ok = ok && make_map_2d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, e.out, R, M, R * 2, rows, BT,
+                           CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e.ad.num > 0) {
+        const uint64_t pdims[3] = {64, M, static_cast<uint64_t>(w.p_cols) / 64};
+        const uint64_t pstr[2] = {static_cast<uint64_t>(w.p_cols) * 2, 128};
+        ok = ok && make_map_3d(&p.map_p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b.at<void>(w.pslots), pdims, pstr, xbox,
+                               CU_TENSOR_MAP_SWIZZLE_128B);
+        p.tile_slots = b.at<int>(w.tile_slots);
+        p.slot_adapter = b.at<int>(w.slot_adapter);
+        p.slot_pitch = static_cast<int>(w.slot_pitch);
+        p.rank = e.ad.rank;
+        p.rank_log2 = slot_log2(e.ad.rank);
+        p.out_rows = static_cast<int>(e.rows);
+        p.side = static_cast<const uint16_t*>(EXT == kExtGrad ? e.ad.A : e.ad.B);
+    }
+    p.status = device_status_address();
+    if (!ok || !p.status) return LOWBIT_ERR_CUDA;
+    p.M = static_cast<int>(e.M);
+    p.N = static_cast<int>(e.rows);
+    p.K = static_cast<int>(e.red);
+    p.num_kb = static_cast<int>((e.red + kBlockK - 1) / kBlockK);
+    p.rows = rows;
+    p.wtx_bytes = static_cast<uint32_t>(C::kWTxFixed + rows * C::kWRowBytes);
+    p.m_tiles = static_cast<int>(w.m_tiles);
+    p.n_tiles = static_cast<int>(PAIR ? e.rows / (2 * rows) : (e.rows + rows - 1) / rows);
+    p.num_tiles = p.m_tiles * p.n_tiles;
+    p.Y = static_cast<__nv_bfloat16*>(e.out);
+    p.rowmul = b.at<float>(w.rowmul);
+    if (ksplit < 0) {
+        // the largest split that leaves every rank at least 24 k-blocks and keeps all clusters
+        // resident at once (as for the plain GEMM)
+        ksplit = 1;
+        const int slots = num_sms() * C::kCtasPerSm;
+        for (int ks = 8; ks >= 2; --ks) {
+            if (p.num_kb / ks < 24 || p.num_tiles * ks > slots) continue;
+            if (p.num_tiles <= cluster_capacity(fn, ks, C::kThreads, C::kSmemBytes)) {
+                ksplit = ks;
+                break;
+            }
+        }
+    }
+    // An unsplit grid of 256-token tiles over a multiple of 256 weight rows runs on CTA pairs.
+    if constexpr (BT == 256 && !PAIR) {
+        if (rows == kBlockN && ksplit == 1 && e.rows % (2 * kBlockN) == 0)
+            return ext_launch<BITS, GS, BT, true, EXT>(e, b, rows, 1, stream);
+    }
+    if (ksplit > p.num_kb) ksplit = p.num_kb;
+    const int kbps = (p.num_kb + ksplit - 1) / ksplit;
+    ksplit = (p.num_kb + kbps - 1) / kbps;     // every rank gets at least one k-block
+    p.kb_per_split = ksplit > 1 ? kbps : p.num_kb;
+    p.ksplit = ksplit;
+
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attrs[2];
+    int na = 0;
+    attrs[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+    if (PAIR) {
+        int pairs = cluster_capacity(fn, 2, C::kThreads, C::kSmemBytes, true);
+        if (pairs > num_sms() / 2) pairs = num_sms() / 2;
+        if (pairs < 1) pairs = 1;
+        cfg.gridDim = dim3(2 * (p.num_tiles < pairs ? p.num_tiles : pairs), 1, 1);
+    } else if (ksplit > 1) {
+        cfg.gridDim = dim3(p.num_tiles, 1, ksplit);
+    } else {
+        const int slots = num_sms() * C::kCtasPerSm;
+        cfg.gridDim = dim3(p.num_tiles < slots ? p.num_tiles : slots, 1, 1);
+    }
+    if (PAIR || ksplit > 1) {
+        attrs[na].id = cudaLaunchAttributeClusterDimension;
+        attrs[na].val.clusterDim.x = PAIR ? 2 : 1;
+        attrs[na].val.clusterDim.y = 1;
+        attrs[na].val.clusterDim.z = PAIR ? 1 : ksplit;
+        ++na;
+    }
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = attrs;
+    cfg.numAttrs = na;
+    if (take_injected_failure(kInjectLaunch)) return LOWBIT_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, mx, mw, ms, mz, my, p) == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
+}
+
+// Weight rows per tile and K slices, by the plain GEMM's rule: one small token tile runs either
+// flat tiles of ceil(rows / #SMs) weight rows with the whole K each, or 128-row tiles with K split
+// over a cluster; W^T's tiles are always 128 rows (a tile's group scales are rows of their own).
+template <int BITS, int GS, int EXT>
+lowbit_status ext_dispatch(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
+    const int bt = b.w.tile_tokens;
+    const int sms = num_sms();
+    const int64_t num_kb = (e.red + kBlockK - 1) / kBlockK;
+    int rows = kBlockN, ksplit = -1;
+    if (bt <= 64) {
+        ksplit = 1;
+        const int64_t tiles128 = b.w.m_tiles * ((e.rows + kBlockN - 1) / kBlockN);
+        const int64_t flat_rows = ((e.rows + sms - 1) / sms + 7) / 8 * 8;
+        const double x_per_w = (2.0 * bt) / (static_cast<double>(flat_rows) * BITS / 8.0);
+        if (EXT == kExtAdapter && flat_rows < kBlockN && x_per_w <= 1.25) {
+            rows = static_cast<int>(flat_rows);
+        } else if (tiles128 * 2 <= 2 * sms && num_kb >= 4) {
+            int64_t s = sms / tiles128;   // one CTA per SM
+            if (s > 8) s = 8;
+            if (s > num_kb / 2) s = num_kb / 2;
+            ksplit = static_cast<int>(s < 1 ? 1 : s);
+        }
+    }
+    switch (bt) {
+        case 32: return ext_launch<BITS, GS, 32, false, EXT>(e, b, rows, ksplit, stream);
+        case 64: return ext_launch<BITS, GS, 64, false, EXT>(e, b, rows, ksplit, stream);
+        case 128: return ext_launch<BITS, GS, 128, false, EXT>(e, b, rows, ksplit, stream);
+        case 256: return ext_launch<BITS, GS, 256, false, EXT>(e, b, rows, ksplit, stream);
+        default: return LOWBIT_ERR_UNSUPPORTED;
+    }
+}
+
+}  // namespace
+}  // namespace lowbit
+
+// Defines ext_gemm_b<BITS> (EXT = kExtAdapter) or ext_grad_b<BITS> (kExtGrad).
+#define LOWBIT_EXT_ENTRY(NAME, BITS, EXT)                                                       \
+    namespace lowbit {                                                                          \
+    lowbit_status NAME(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {         \
+        return e.group_size == 64 ? ext_dispatch<BITS, 64, EXT>(e, b, stream)                   \
+                                  : ext_dispatch<BITS, 128, EXT>(e, b, stream);                 \
+    }                                                                                           \
+    }

@@ -20,6 +20,7 @@
 
 #include <cstdint>
 
+#include "adapter_internal.h"
 #include "lowbit_internal.h"
 
 namespace lowbit {
@@ -158,7 +159,49 @@ lowbit_status reset_counter(cudaStream_t stream) {
     return LOWBIT_OK;
 }
 
+// W^T words from W's: row k of the result holds the codes of column k, packed along n in the same
+// layout; rows are filled up to a multiple of 128 columns with zero fields (whose scales the
+// gradient kernel reads as zero). A thread builds one word from its CPW source fields; lanes run
+// along k, so their source words are neighbours.
+template <int BITS>
+__global__ void transpose_kernel(const uint32_t* __restrict__ packed, int64_t N, int64_t K, int64_t wpr_out,
+                                 uint32_t* __restrict__ out) {
+    constexpr int CPW = 32 / BITS;
+    const int64_t wpr = K / CPW, total = K * wpr_out;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < total; t += stride) {
+        const int64_t k = t % K, j = t / K;
+        // column k's word within a row of W, and its bit position there
+        int64_t word = k / CPW;
+        int pos = static_cast<int>(k % 2) * 16 + static_cast<int>(k % CPW / 2) * BITS;
+        if (BITS != 1 && word < wpr / 4 * 4) {
+            const int in = static_cast<int>(k % (4 * CPW));
+            word = k / (4 * CPW) * 4 + in % 8 / 2;
+            pos = in % 2 * 16 + in / 8 * BITS;
+        }
+        bool block;
+        const int64_t col = word_codes<BITS>(j, wpr_out, block);   // row 0: the word's first column
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < CPW; ++i) {
+            const int64_t n = col + (block ? i / 2 * 8 + i % 2 : i);
+            if (n < N) w |= ((packed[n * wpr + word] >> pos) & ((1u << BITS) - 1u)) << ((i % 2) * 16 + (i / 2) * BITS);
+        }
+        out[k * wpr_out + j] = w;
+    }
+}
+
 }  // namespace
+
+lowbit_status transpose_launch(const uint32_t* packed, int64_t N, int64_t K, int bits, uint32_t* out, cudaStream_t s) {
+    const int64_t wpr_out = (N + 127) / 128 * 128 * bits / 32;
+    const int grid = grid_for(K * wpr_out);
+    if (take_injected_failure(kInjectLaunch)) return LOWBIT_ERR_CUDA;
+    if (bits == 1) transpose_kernel<1><<<grid, 256, 0, s>>>(packed, N, K, wpr_out, out);
+    else if (bits == 2) transpose_kernel<2><<<grid, 256, 0, s>>>(packed, N, K, wpr_out, out);
+    else transpose_kernel<4><<<grid, 256, 0, s>>>(packed, N, K, wpr_out, out);
+    return cudaGetLastError() == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
+}
 
 lowbit_status pack_launch(const int8_t* codes, int64_t N, int64_t K, int bits, uint32_t* packed,
                           cudaStream_t stream, unsigned long long* bad) {

@@ -243,6 +243,98 @@ int lowbit_debug_checks_enabled(void);
  * Asynchronous. */
 lowbit_status lowbit_selftest_index_check(void* stream);
 
+/* ---- Low-rank adapters beside the packed linear, and gradients --------------------------------
+ *
+ * A frozen packed W serves many requests, each with a low-rank adapter of its own:
+ *
+ *   p[m] = scaling[a] * X[m] * A_a^T          a = index[m], A_a [R][K], p [M][R]
+ *   Y[m] = X[m] * W^T + p[m] * B_a^T          B_a [N][R]
+ *
+ * and is trained through: dX = dY * W + dp * A_a with dp[m] = scaling[a] * dY[m] * B_a, dA_a = the
+ * sum of dp[m]^T * X[m] and dB_a = the sum of dY[m]^T * p[m] over the tokens of adapter a.
+ * The pages have no counterpart: they run a fixed transformer. */
+
+#define LOWBIT_MAX_ADAPTERS 4096
+#define LOWBIT_MAX_RANK 128
+
+/* Adapters of one linear (device pointers). */
+typedef struct lowbit_adapters {
+    int num;              /* L, 1 .. LOWBIT_MAX_ADAPTERS                                          */
+    int rank;             /* R, a multiple of 8 up to LOWBIT_MAX_RANK (fill smaller ones with 0)  */
+    const void* A;        /* bf16 [L][R][K], 16-byte aligned                                      */
+    const void* B;        /* bf16 [L][N][R], 16-byte aligned                                      */
+    const float* scaling; /* fp32 [L]                                                             */
+    const int32_t* index; /* [M]: adapter of each token; values outside 0 .. L-1 mean none.       */
+                          /* NULL: every token takes adapter 0                                    */
+} lowbit_adapters;
+
+/* Words of W^T as the gradient entry points read it: row k holds column k's codes, packed along N
+ * in the layout above, filled up to a multiple of 128 columns with zero fields.
+ * K * ceil(N / 128) * 128 * bits / 32; 0 for invalid arguments. */
+size_t lowbit_transposed_words(int64_t N, int64_t K, int bits);
+
+/* packed [N][K*bits/32] -> W^T's words (lowbit_transposed_words(N, K, bits) of them). Done once per
+ * weight; fields are moved as they are. Asynchronous on `stream`. Both 16-byte aligned. */
+lowbit_status lowbit_transpose(const uint32_t* packed, int64_t N, int64_t K, int bits, uint32_t* packed_t,
+                               void* stream);
+
+/* Bytes of workspace for the three entry points below (num = rank = 0 for lowbit_gemm_dx): one
+ * size for the forward and backward of a linear. It holds the fp16 copy of the wider of X and dY and,
+ * with adapters, the tokens' order, the low-rank products and up to
+ * M * min(num, 256) * (rank rounded up to a power of two >= 16) bf16 values. 0 for invalid arguments. */
+size_t lowbit_adapter_workspace_size(int64_t M, int64_t N, int64_t K, int num, int rank);
+
+/* Y = X W^T + p B^T in one pass over Y (asynchronous; never synchronises). Arguments as for
+ * lowbit_gemm, and
+ *   P         bf16 [M][R], 16-byte aligned, or NULL: p, which the backward pass needs (0 for tokens
+ *             without an adapter)
+ *   ck_codes  [M][K] bytes, 16-byte aligned, and ck_exps [M][K/32] bytes, or both NULL: the 8-bit copy
+ *             of X (see lowbit_checkpoint_store), written in the same pass over X
+ *   workspace 256-byte aligned, >= lowbit_adapter_workspace_size(M, N, K, num, rank)
+ * p is summed in fp32 and rounded to bf16 once; p B^T is added to X W^T in fp32, so Y is rounded
+ * once. Tokens of one 256-token tile share tensor-core products in which other adapters' entries of
+ * p are zero: an infinity or NaN in one adapter's A, B or scaling can therefore also reach tokens of
+ * other adapters (as NaN). Nothing that the call reads may be written by concurrent work. Results do
+ * not depend on timing. */
+lowbit_status lowbit_adapter_gemm(int64_t M, int64_t N, int64_t K, int bits, int group_size, const void* X,
+                                  const uint32_t* Wp, const void* scales, const void* zeros,
+                                  const lowbit_adapters* adapters, void* Y, void* P, uint8_t* ck_codes,
+                                  uint8_t* ck_exps, void* workspace, size_t workspace_bytes, void* stream);
+
+/* dX = dY W, the input gradient of lowbit_gemm: dY bf16 [M][N], Wt from lowbit_transpose, dX bf16
+ * [M][K], all 16-byte aligned; scales and zeros as for the forward. A uint4 weight is (q - z) * s
+ * with the difference and the product rounded to fp16 (2^-11 relative each). */
+lowbit_status lowbit_gemm_dx(int64_t M, int64_t N, int64_t K, int bits, int group_size, const void* dY,
+                             const uint32_t* Wt, const void* scales, const void* zeros, void* dX, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* The gradients of lowbit_adapter_gemm.
+ *   dY   bf16 [M][N];  P  bf16 [M][R], as the forward wrote it
+ *   X    bf16 [M][K], or NULL with its 8-bit copy in ck_codes / ck_exps
+ *   dX   bf16 [M][K], or NULL if it is not needed
+ *   dA   bf16 [L][R][K], dB bf16 [L][N][R]: written in full (zero for an adapter without tokens)
+ * all 16-byte aligned. Sums are fp32, in a fixed order; dp is rounded to bf16 once and dA, dB and dX
+ * once each. (An infinity or NaN in one adapter reaches dX of others as in the forward; dA and dB
+ * are formed from the adapter's own tokens alone.) */
+lowbit_status lowbit_adapter_backward(int64_t M, int64_t N, int64_t K, int bits, int group_size, const void* dY,
+                                      const uint32_t* Wt, const void* scales, const void* zeros,
+                                      const lowbit_adapters* adapters, const void* X, const uint8_t* ck_codes,
+                                      const uint8_t* ck_exps, const void* P, void* dX, void* dA, void* dB,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* 8-bit copy of an activation X bf16 [M][K], K a multiple of 32: per 32 neighbouring values of a row,
+ * e = the smallest exponent with max |x| <= 448 * 2^e over the block's finite values, codes = x * 2^-e
+ * rounded to e4m3 (nearest even, never saturating), exps = e + 127 clamped at 0 (0 for a block without
+ * nonzero finite values). Infinities and NaN become NaN. codes [M][K] 16-byte aligned, exps
+ * [M][K/32]. Asynchronous. */
+lowbit_status lowbit_checkpoint_store(const void* X, int64_t M, int64_t K, uint8_t* codes, uint8_t* exps,
+                                      void* stream);
+
+/* The values a copy stands for: X = code * 2^(exps - 127) in bf16 (exact wherever that is not below
+ * bf16's subnormal range). Asynchronous. */
+lowbit_status lowbit_checkpoint_load(const uint8_t* codes, const uint8_t* exps, int64_t M, int64_t K, void* X,
+                                     void* stream);
+
 #ifdef __cplusplus
 }
 #endif
