@@ -16,8 +16,8 @@ bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 
 constexpr int64_t kMaxSize = int64_t(1) << 31;
 
-// The linear's own arguments, by lowbit_gemm's rules (the workspace is checked separately).
-lowbit_status check_linear(int64_t M, int64_t N, int64_t K, int bits, int gs, const void* in, const uint32_t* W,
+// The linear by lowbit_gemm's description (the workspace is checked separately).
+GemmProblem linear_problem(int64_t M, int64_t N, int64_t K, int bits, int gs, const void* in, const uint32_t* W,
                            const void* scales, const void* zeros, const void* out) {
     GemmProblem g;
     g.M = M;
@@ -32,7 +32,12 @@ lowbit_status check_linear(int64_t M, int64_t N, int64_t K, int bits, int gs, co
     g.Y = const_cast<void*>(out);
     g.workspace = reinterpret_cast<void*>(uintptr_t(256));
     g.workspace_bytes = SIZE_MAX;
-    return validate_gemm(g);
+    return g;
+}
+
+lowbit_status check_linear(int64_t M, int64_t N, int64_t K, int bits, int gs, const void* in, const uint32_t* W,
+                           const void* scales, const void* zeros, const void* out) {
+    return validate_gemm(linear_problem(M, N, K, bits, gs, in, W, scales, zeros, out));
 }
 
 lowbit_status check_adapters(const lowbit_adapters* a, int64_t N, int64_t K) {
@@ -105,7 +110,7 @@ LOWBIT_API lowbit_status lowbit_transpose(const uint32_t* packed, int64_t N, int
 LOWBIT_API size_t lowbit_adapter_workspace_size(int64_t M, int64_t N, int64_t K, int num, int rank) {
     if (M < 0 || N < 0 || K < 0 || num < 0 || num > kMaxAdapters || rank < 0 || rank > kMaxRank) return 0;
     if (num > 0 && rank == 0) return 0;
-    const size_t f = ext_workspace(M, K, num, rank).total, b = ext_workspace(M, N, num, rank).total;
+    const size_t f = ext_workspace(M, N, K, num, rank).total, b = ext_workspace(M, K, N, num, rank).total;
     return f > b ? f : b;
 }
 
@@ -133,10 +138,19 @@ LOWBIT_API lowbit_status lowbit_adapter_gemm(int64_t M, int64_t N, int64_t K, in
     e.p_out = P;
     e.ck_codes = ck_codes;
     e.ck_exps = ck_exps;
-    ExtBuffers b{ext_workspace(M, K, e.ad.num, e.ad.rank), static_cast<uint8_t*>(workspace)};
+    ExtBuffers b{ext_workspace(M, N, K, e.ad.num, e.ad.rank), static_cast<uint8_t*>(workspace)};
     if ((st = check_workspace(workspace, workspace_bytes, b.w.total)) != LOWBIT_OK) return st;
     if ((st = check_device()) != LOWBIT_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const GemmProblem g = linear_problem(M, N, K, bits, group_size, X, Wp, scales, zeros, Y);
+    if (smallm_supported(g)) {
+        // up to 16 tokens: the small-M kernel, which reads X directly and adds the low-rank terms itself
+        if (ck_codes && (st = checkpoint_store_launch(X, M * K, ck_codes, ck_exps, s)) != LOWBIT_OK) return st;
+        float* p = b.at<float>(b.w.partial);
+        if ((st = launch_shrink_small(e, p, s)) != LOWBIT_OK) return st;
+        const LowRank lr = {p, e.ad.B, e.ad.index, e.ad.num, e.ad.rank};
+        return smallm_launch(g, 0, 0, M <= 8, s, &lr);
+    }
     if ((st = prepare(e, b, s)) != LOWBIT_OK) return st;
     return product(e, b, s);
 }
@@ -164,7 +178,7 @@ LOWBIT_API lowbit_status lowbit_gemm_dx(int64_t M, int64_t N, int64_t K, int bit
         if ((st = check_device()) != LOWBIT_OK) return st;
         return cudaMemsetAsync(dX, 0, static_cast<size_t>(M) * K * 2, s) == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
     }
-    ExtBuffers b{ext_workspace(M, N, 0, 0), static_cast<uint8_t*>(workspace)};
+    ExtBuffers b{ext_workspace(M, K, N, 0, 0), static_cast<uint8_t*>(workspace)};
     if ((st = check_workspace(workspace, workspace_bytes, b.w.total)) != LOWBIT_OK) return st;
     if ((st = check_device()) != LOWBIT_OK) return st;
     if ((st = prepare(e, b, s)) != LOWBIT_OK) return st;
@@ -205,7 +219,7 @@ LOWBIT_API lowbit_status lowbit_adapter_backward(int64_t M, int64_t N, int64_t K
     e.zeros = zeros;
     e.out = dX;
     e.ad = adapter_set(adapters);
-    ExtBuffers b{ext_workspace(M, N, e.ad.num, e.ad.rank), static_cast<uint8_t*>(workspace)};
+    ExtBuffers b{ext_workspace(M, K, N, e.ad.num, e.ad.rank), static_cast<uint8_t*>(workspace)};
     if ((st = check_workspace(workspace, workspace_bytes, b.w.total)) != LOWBIT_OK) return st;
     e.p_out = b.at<void>(b.w.p);
     if ((st = check_device()) != LOWBIT_OK) return st;

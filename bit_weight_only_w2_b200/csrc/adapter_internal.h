@@ -12,13 +12,10 @@ namespace lowbit {
 
 constexpr int kMaxAdapters = 4096;
 constexpr int kMaxRank = 128;
-constexpr int kShrinkTokens = 64;   // tokens of one adapter per block of the shrink kernel
+constexpr int kShrinkTokens = 128;  // tokens of one adapter per block of the shrink kernel
 
 // Slot width: the rank rounded up to a power of two >= 16 (one MMA K step).
 inline int slot_log2(int rank) { return rank <= 16 ? 4 : rank <= 32 ? 5 : rank <= 64 ? 6 : 7; }
-
-// Tokens per tile of the tensor-memory kernel for M tokens.
-inline int ext_tile_tokens(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
 
 struct AdapterSet {
     int num = 0, rank = 0;        // L adapters of rank R; num == 0: none
@@ -55,7 +52,8 @@ struct ExtProblem {
 //   p        bf16 [M][R] (backward: dp)
 struct ExtWorkspace {
     int64_t red64;
-    int tile_tokens;
+    int tile_tokens;         // tokens per tile and K slices of the product, chosen from the sizes
+    int product_split;
     int64_t m_tiles;
     int64_t num_blocks;      // shrink blocks, at most
     int ksplit;              // K slices of the shrink kernel
@@ -64,7 +62,7 @@ struct ExtWorkspace {
     int64_t p_cols;          // columns of pslots
     size_t xh, rowmul, perm, seg, blocks, tile_slots, slot_adapter, token_slot, partial, pslots, p, total;
 };
-ExtWorkspace ext_workspace(int64_t M, int64_t red, int num, int rank);
+ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int rank);
 
 struct ExtBuffers {
     ExtWorkspace w;
@@ -81,6 +79,8 @@ struct ExtBuffers {
 lowbit_status launch_plan(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream);
 lowbit_status launch_shrink(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream);
 lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream);
+// Up to 16 tokens: p fp32 [M][R], scaled, for the small-M kernel's low-rank term.
+lowbit_status launch_shrink_small(const ExtProblem& e, float* p, cudaStream_t stream);
 
 struct WgradProblem {
     const void* dy;            // bf16 [M][N]

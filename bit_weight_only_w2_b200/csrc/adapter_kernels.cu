@@ -13,7 +13,9 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "adapter_internal.h"
 #include "checkpoint.cuh"
@@ -26,6 +28,13 @@ constexpr int kSmsAssumed = 148;   // the workspace's size may not depend on the
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 ldg_nc_v4(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -63,10 +72,10 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 // One more CTA per token tile lists the distinct adapters of the tile in ascending order (its
 // "slots") from a bitmap, and each token's slot.
 //
-// Shrink blocks: adapter a's tokens [seg[a], seg[a + 1]) get the block numbers seg[a] / 64 + a + i,
-// i < ceil(count / 64), which never collide: the next adapter starts at
-// floor(seg[a + 1] / 64) + a + 1, and ceil(count / 64) <= floor(seg[a + 1] / 64) -
-// floor(seg[a] / 64) + 1. Numbers in between stay empty (count 0).
+// Shrink blocks of T = kShrinkTokens: adapter a's tokens [seg[a], seg[a + 1]) get the block numbers
+// seg[a] / T + a + i, i < ceil(count / T), which never collide: the next adapter starts at
+// floor(seg[a + 1] / T) + a + 1, and ceil(count / T) <= floor(seg[a + 1] / T) -
+// floor(seg[a] / T) + 1. Numbers in between stay empty (count 0).
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
@@ -166,10 +175,10 @@ __global__ void __launch_bounds__(kPlanThreads)
 // R is at most 128, so the product reads each input row once and is bound by that stream (and,
 // for few tokens per adapter, by the adapters' rows): warp-level MMAs on tiles that cp.async
 // gathers into shared memory keep up with it, and tcgen05's 128-row tiles would be mostly padding.
-// A block is up to 64 tokens of one adapter; the reduction is cut into slices over gridDim.y so
+// A block is up to 128 tokens of one adapter; the reduction is cut into slices over gridDim.y so
 // that a few blocks fill the GPU, and the slices' fp32 partials are added in order by the copy
 // pass that follows. KMAJOR: the adapter's side is [R][red] (A); otherwise [red][R] (B).
-constexpr int kShrinkThreads = 128;
+constexpr int kShrinkThreads = 256;
 constexpr int kShrinkStages = 4;
 __host__ __device__ constexpr int shrink_smem(int rp) { return kShrinkStages * (kShrinkTokens * 128 + rp * 128); }
 
@@ -206,8 +215,9 @@ __global__ void __launch_bounds__(kShrinkThreads)
         }
         const uint32_t ws = st + kXBytes;
 #pragma unroll
-        for (int i = 0; i < RP * 8 / kShrinkThreads; ++i) {
+        for (int i = 0; i < (RP * 8 + kShrinkThreads - 1) / kShrinkThreads; ++i) {
             const int id = tid + i * kShrinkThreads;
+            if (RP * 8 < kShrinkThreads && id >= RP * 8) break;
             if (KMAJOR) {
                 const int row = id >> 3, ch = id & 7;
                 const int k = k0 + ch * 8;
@@ -275,6 +285,57 @@ __global__ void __launch_bounds__(kShrinkThreads)
     }
 }
 
+// Shrink for up to 16 tokens, which may all have adapters of their own: p[m][r] for two ranks of one
+// token per CTA, each of the four warps a quarter of the reduction, lanes on 16-byte pieces. It is
+// bound by the latency of its loads (A's rows come from memory once; 1 MB or so), so it has no
+// stages: every load of a warp's quarter is in flight at once for the usual widths. The result is
+// final (scaled fp32): the small-M kernel reads it directly.
+constexpr int kShrinkSmallWarps = 4;
+
+__global__ void __launch_bounds__(32 * kShrinkSmallWarps)
+    shrink_small_kernel(const uint4* __restrict__ in, const uint4* __restrict__ A, int K8, int R, int num,
+                        const float* __restrict__ scaling, const int* __restrict__ index, float* __restrict__ p,
+                        __nv_bfloat16* __restrict__ p_out) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int m = blockIdx.y, r = 2 * blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int a = adapter_of(index, m, num);
+    float s0 = 0.f, s1 = 0.f;
+    if (a >= 0) {
+        const uint4* x = in + static_cast<size_t>(m) * K8;
+        const uint4* a0 = A + (static_cast<size_t>(a) * R + r) * K8;
+        const uint4* a1 = a0 + K8;
+        auto dot = [](uint32_t u, uint32_t v, float s) {
+            s = fmaf(__uint_as_float(u << 16), __uint_as_float(v << 16), s);
+            return fmaf(__uint_as_float(u & 0xFFFF0000u), __uint_as_float(v & 0xFFFF0000u), s);
+        };
+#pragma unroll 4
+        for (int i = warp * 32 + lane; i < K8; i += 32 * kShrinkSmallWarps) {
+            const uint4 u = __ldg(x + i), v = __ldg(a0 + i), w = __ldg(a1 + i);
+            s0 = dot(u.x, v.x, dot(u.y, v.y, dot(u.z, v.z, dot(u.w, v.w, s0))));
+            s1 = dot(u.x, w.x, dot(u.y, w.y, dot(u.z, w.z, dot(u.w, w.w, s1))));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+        s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+    }
+    __shared__ float2 part[kShrinkSmallWarps];
+    if (lane == 0) part[warp] = make_float2(s0, s1);
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kShrinkSmallWarps; ++w) s += threadIdx.x ? part[w].y : part[w].x;
+        if (a >= 0) s *= scaling[a];
+        const size_t at = static_cast<size_t>(m) * R + r + threadIdx.x;
+        p[at] = s;
+        if (p_out) p_out[at] = __float2bfloat16_rn(s);
+    }
+}
+
 // ---------------------------------------------------------------------------------------------
 // Copy pass: fp16 copy of the input, the slots' P, the kept p and the 8-bit copy
 // ---------------------------------------------------------------------------------------------
@@ -283,7 +344,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
 // by 2^e; that is exact in bf16. p itself is rounded to bf16 once, as the MMA's operand and as
 // what the backward pass reads: 2^-9 of the low-rank term at most, like the output's own rounding.
 struct SideArgs {
-    const float* partial;      // nullptr: no adapters
+    const float* partial;      // [ksplit][M][Rp]
     int ksplit;
     int rp_log2, rank, num;
     const float* scaling;
@@ -294,22 +355,50 @@ struct SideArgs {
     __nv_bfloat16* pslots;
     long long p_cols;
     __nv_bfloat16* p_out;      // nullptr: not kept
-    uint8_t* codes;            // nullptr: no 8-bit copy
+    uint8_t* codes;            // 8-bit copy
     uint8_t* exps;
 };
 
 constexpr int kConvThreads = 256;
 
-template <int PER>
-__global__ void __launch_bounds__(kConvThreads)
+// LR: with adapters; CK: with the 8-bit copy. (A kernel each, so that the plain copy keeps the
+// registers, and so the resident rows, that its bandwidth needs.)
+template <int PER, bool LR, bool CK>
+__global__ void __launch_bounds__(kConvThreads, 4)
     convert_side_kernel(const uint4* __restrict__ in, int M, int K8, int K8p, uint4* __restrict__ xh,
                         float* __restrict__ rowmul, const SideArgs s) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int row = blockIdx.x;
+    const int row = blockIdx.x, tid = threadIdx.x;
     const uint4* src = in + static_cast<size_t>(row) * K8;
     uint4* dst = xh + static_cast<size_t>(row) * K8p;
     uint4 v[PER > 0 ? PER : 1];
+    if (PER > 0) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = tid + j * kConvThreads;
+            v[j] = i < K8 ? ldg_nc_v4(src + i) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    // This token's low-rank product: the slices' partials in order, times its adapter's scaling. Its
+    // loads are asked for together with the row's, none waiting for another.
+    __shared__ float prow[kMaxRank];
+    int slot = -1, cols = 0;
+    if (LR) {
+        slot = s.token_slot[row];
+        cols = s.tile_slots[row >> s.tile_log2] << s.rp_log2;   // the columns the MMA reads
+        if (tid < (1 << s.rp_log2)) {
+            const int a = adapter_of(s.index, row, s.num);
+            const float* part = s.partial + (static_cast<size_t>(row) << s.rp_log2) + tid;
+            const size_t step = static_cast<size_t>(M) << s.rp_log2;
+            float p = 0.f;
+#pragma unroll 8
+            for (int k = 0; k < s.ksplit; ++k) p += part[k * step];
+            p = a < 0 ? 0.f : p * s.scaling[a];                  // (no adapter: its partials are not written)
+            prow[tid] = p;
+            if (s.p_out && tid < s.rank) s.p_out[static_cast<size_t>(row) * s.rank + tid] = __float2bfloat16_rn(p);
+        }
+    }
     uint32_t mx = 0;
     auto amax = [](const uint4& a, uint32_t m) {
         m = max(m, max(a.x & 0x7FFFu, (a.x >> 16) & 0x7FFFu));
@@ -319,35 +408,30 @@ __global__ void __launch_bounds__(kConvThreads)
     };
     if (PER > 0) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int i = threadIdx.x + j * kConvThreads;
-            v[j] = i < K8 ? src[i] : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
         for (int j = 0; j < PER; ++j) mx = amax(v[j], mx);
     } else {
-        for (int i = threadIdx.x; i < K8; i += kConvThreads) mx = amax(src[i], mx);
+        for (int i = tid; i < K8; i += kConvThreads) mx = amax(src[i], mx);
+    }
+    auto copy8 = [&](int i, const uint4& a, bool valid) {
+        // four neighbouring lanes hold a block of 32 values (K8 is a multiple of 4)
+        uint8_t ex;
+        const uint2 c = checkpoint_encode8(a, ex);
+        if (valid) {
+            const size_t at = static_cast<size_t>(row) * K8 + i;
+            reinterpret_cast<uint2*>(s.codes)[at] = c;
+            if ((i & 3) == 0) s.exps[at >> 2] = ex;
+        }
+    };
+    if (CK && PER > 0) {   // (before the row's maximum is known: it does not need it)
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = tid + j * kConvThreads;
+            if (j * kConvThreads < K8) copy8(i, v[j], i < K8);
+        }
     }
     mx = __reduce_max_sync(0xffffffffu, mx);
     __shared__ uint32_t warp_max[kConvThreads / 32];
-    __shared__ float prow[kMaxRank];
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = mx;
-    // this token's low-rank product: the slices' partials in order, times its adapter's scaling
-    int slot = -1;
-    if (s.partial) {
-        slot = s.token_slot[row];
-        const int r = threadIdx.x;
-        if (r < (1 << s.rp_log2)) {
-            float p = 0.f;
-            if (slot >= 0) {
-                const float* part = s.partial + (static_cast<size_t>(row) << s.rp_log2) + r;
-                for (int k = 0; k < s.ksplit; ++k) p += part[(static_cast<size_t>(k) * M) << s.rp_log2];
-                p *= s.scaling[s.index ? s.index[row] : 0];
-            }
-            prow[r] = p;
-            if (s.p_out && r < s.rank) s.p_out[static_cast<size_t>(row) * s.rank + r] = __float2bfloat16_rn(p);
-        }
-    }
+    if ((tid & 31) == 0) warp_max[tid >> 5] = mx;
     __syncthreads();
     mx = 0;
 #pragma unroll
@@ -360,37 +444,26 @@ __global__ void __launch_bounds__(kConvThreads)
         const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xFFFF0000u) * scale);
         return *reinterpret_cast<const uint32_t*>(&h);
     };
-    auto emit = [&](int i, const uint4& a, bool valid) {
-        if (i < K8p) dst[i] = make_uint4(cvt(a.x), cvt(a.y), cvt(a.z), cvt(a.w));
-        if (s.codes) {   // four neighbouring lanes hold a block of 32 values (K8 is a multiple of 4)
-            uint8_t ex;
-            const uint2 c = checkpoint_encode8(a, ex);
-            if (valid) {
-                const size_t at = static_cast<size_t>(row) * K8 + i;
-                reinterpret_cast<uint2*>(s.codes)[at] = c;
-                if ((i & 3) == 0) s.exps[at >> 2] = ex;
-            }
-        }
-    };
     if (PER > 0) {
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int i = threadIdx.x + j * kConvThreads;
-            emit(i, v[j], i < K8);
+            const int i = tid + j * kConvThreads;
+            if (i < K8p) dst[i] = make_uint4(cvt(v[j].x), cvt(v[j].y), cvt(v[j].z), cvt(v[j].w));
         }
     } else {
         // (whole warps take part in every round: the 8-bit copy exchanges between lanes)
         const int rounds = (K8p + kConvThreads - 1) / kConvThreads;
         for (int j = 0; j < rounds; ++j) {
-            const int i = threadIdx.x + j * kConvThreads;
-            emit(i, i < K8 ? src[i] : make_uint4(0, 0, 0, 0), i < K8);
+            const int i = tid + j * kConvThreads;
+            const uint4 a = i < K8 ? src[i] : make_uint4(0, 0, 0, 0);
+            if (i < K8p) dst[i] = make_uint4(cvt(a.x), cvt(a.y), cvt(a.z), cvt(a.w));
+            if (CK) copy8(i, a, i < K8);
         }
     }
-    if (threadIdx.x == 0) rowmul[row] = __int_as_float((127 + e) << 23);   // 2^e
-    if (s.partial) {
-        const int cols = s.tile_slots[row >> s.tile_log2] << s.rp_log2;    // the columns the MMA reads
+    if (tid == 0) rowmul[row] = __int_as_float((127 + e) << 23);   // 2^e
+    if (LR) {
         uint4* pd = reinterpret_cast<uint4*>(s.pslots + static_cast<size_t>(row) * s.p_cols);
-        for (int c = threadIdx.x; c < cols / 8; c += kConvThreads) {
+        for (int c = tid; c < cols / 8; c += kConvThreads) {
             uint4 o = make_uint4(0, 0, 0, 0);
             if ((c * 8) >> s.rp_log2 == slot) {
                 const float* pr = prow + ((c * 8) & ((1 << s.rp_log2) - 1));
@@ -439,6 +512,10 @@ constexpr int kWgradG = 64 * 256;                 // 64 tokens x 128 columns, bf
 __host__ __device__ constexpr int wgrad_stage(int rp) { return kWgradG + 64 * rp * 2; }
 __host__ __device__ constexpr int wgrad_smem(int rp) { return kWgradStages * wgrad_stage(rp) + kWgradG; }
 
+// Token ids of a step, ring of kTokRing steps: read from memory a step before the copies that need
+// them, so that no copy waits for its row's address.
+constexpr int kTokRing = 4;
+
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -464,19 +541,25 @@ __global__ void __launch_bounds__(kWgradThreads) wgrad_kernel(const WgradArgs w)
     const int steps = (t_end - t_begin + 63) / 64;
     const int* perm = w.perm + seg0;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __shared__ int tok[kTokRing][64];
+    auto token_of = [&](int step, int i) {   // rows past the end: token 0 of the range, not read
+        const int t = t_begin + step * 64 + i;
+        return t < t_end ? perm[t] : 0;
+    };
     const bool q8 = part.exps != nullptr;
     const uint32_t s0 = smem_u32(smem);
     const uint32_t wide = s0 + kWgradStages * kStage;     // the widened tile of an 8-bit stage
     auto load = [&](int step) {
         const uint32_t st = s0 + (step % kWgradStages) * kStage;
         const int t0 = t_begin + step * 64;
+        const int* ids = tok[step % kTokRing];
         if (!q8) {
             const __nv_bfloat16* G = static_cast<const __nv_bfloat16*>(part.G);
 #pragma unroll
             for (int i = 0; i < 64 * 16 / kWgradThreads; ++i) {
                 const int id = tid + i * kWgradThreads, row = id >> 4, ch = id & 15;
                 const bool ok = t0 + row < t_end && c0 + ch * 8 < part.C;
-                const size_t src = ok ? static_cast<size_t>(perm[t0 + row]) * part.C + c0 + ch * 8 : 0;
+                const size_t src = ok ? static_cast<size_t>(ids[row]) * part.C + c0 + ch * 8 : 0;
                 cp_async16(st + row * 256 + ((ch ^ (row & 7)) << 4), G + src, ok);
             }
         } else {
@@ -485,8 +568,8 @@ __global__ void __launch_bounds__(kWgradThreads) wgrad_kernel(const WgradArgs w)
             for (int i = 0; i < 64 * 8 / kWgradThreads; ++i) {
                 const int id = tid + i * kWgradThreads, row = id >> 3, ch = id & 7;
                 const bool ok = t0 + row < t_end && c0 + ch * 16 < part.C;
-                const size_t src = ok ? static_cast<size_t>(perm[t0 + row]) * part.C + c0 + ch * 16 : 0;
-                cp_async16(st + row * 128 + ch * 16, G + src, ok);
+                const size_t src = ok ? static_cast<size_t>(ids[row]) * part.C + c0 + ch * 16 : 0;
+                cp_async16(st + row * 128 + ((ch ^ (row & 7)) << 4), G + src, ok);
             }
         }
 #pragma unroll
@@ -494,47 +577,61 @@ __global__ void __launch_bounds__(kWgradThreads) wgrad_kernel(const WgradArgs w)
             const int id = tid + i * kWgradThreads, row = id / kCh, ch = id % kCh;
             if (row < 64) {
                 const bool ok = t0 + row < t_end && ch * 8 < w.R;
-                const size_t src = ok ? static_cast<size_t>(perm[t0 + row]) * w.R + ch * 8 : 0;
+                const size_t src = ok ? static_cast<size_t>(ids[row]) * w.R + ch * 8 : 0;
                 cp_async16(st + kWgradG + row * RP * 2 + ((ch ^ (row & (kCh < 8 ? kCh - 1 : 7))) << 4), part.P + src, ok);
             }
         }
     };
-    // widen one 8-bit stage: thread -> 32 columns (one exponent) of a token row
-    auto widen = [&](int step) {
+    // 8-bit x: each warp widens its own 16 columns of a stage, lane -> token rows lane and lane + 32.
+    // The exponents of the rows' block come from memory a step ahead.
+    const int blk = c0 / 32 + warp / 2;
+    auto exponent_of = [&](int step, int i) -> uint32_t {
+        const int row = lane + 32 * i;
+        if (t_begin + step * 64 + row >= t_end || c0 + warp * 16 >= part.C) return 0;
+        return part.exps[static_cast<size_t>(tok[step % kTokRing][row]) * (part.C / 32) + blk];
+    };
+    auto widen = [&](int step, const uint32_t (&ex)[2]) {
         const uint8_t* st = smem + (step % kWgradStages) * kStage;
-        const int t0 = t_begin + step * 64;
-        const int row = tid >> 2, blk = tid & 3;
-        uint32_t ex = 0;
-        if (t0 + row < t_end && c0 + blk * 32 < part.C)
-            ex = part.exps[(static_cast<size_t>(perm[t0 + row]) * part.C + c0 + blk * 32) >> 5];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint4 c = *reinterpret_cast<const uint4*>(st + row * 128 + blk * 32 + i * 16);
-            const uint4 lo = checkpoint_decode8(make_uint2(c.x, c.y), ex), hi = checkpoint_decode8(make_uint2(c.z, c.w), ex);
+            const int row = lane + 32 * i;
+            const uint4 c = *reinterpret_cast<const uint4*>(st + row * 128 + ((warp ^ (row & 7)) << 4));
             uint8_t* dst = smem + kWgradStages * kStage + row * 256;
-            const int ch = blk * 4 + i * 2;
-            *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) << 4)) = lo;
-            *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (row & 7)) << 4)) = hi;
+            *reinterpret_cast<uint4*>(dst + (((2 * warp) ^ (row & 7)) << 4)) = checkpoint_decode8(make_uint2(c.x, c.y), ex[i]);
+            *reinterpret_cast<uint4*>(dst + (((2 * warp + 1) ^ (row & 7)) << 4)) =
+                checkpoint_decode8(make_uint2(c.z, c.w), ex[i]);
         }
     };
     float acc[RP / 8][4];
 #pragma unroll
     for (int i = 0; i < RP / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    if (tid < 64 * kWgradStages) tok[tid >> 6][tid & 63] = token_of(tid >> 6, tid & 63);
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < kWgradStages - 1; ++i) {
         if (i < steps) load(i);
         cp_async_commit();
+    }
+    uint32_t ex[2] = {0, 0};
+    if (q8) {
+        ex[0] = exponent_of(0, 0);
+        ex[1] = exponent_of(0, 1);
     }
     for (int step = 0; step < steps; ++step) {
         cp_async_wait<kWgradStages - 2>();
         __syncthreads();
         if (step + kWgradStages - 1 < steps) load(step + kWgradStages - 1);
         cp_async_commit();
+        const int ahead = tid < 64 ? token_of(step + kWgradStages, tid) : 0;
         const uint32_t st = s0 + (step % kWgradStages) * kStage;
         uint32_t gs = st;
         if (q8) {
-            widen(step);
-            __syncthreads();
+            const uint32_t now[2] = {ex[0], ex[1]};
+            ex[0] = exponent_of(step + 1, 0);
+            ex[1] = exponent_of(step + 1, 1);
+            __syncwarp();                // the previous step's fragments of this warp's columns are read
+            widen(step, now);
+            __syncwarp();
             gs = wide;
         }
 #pragma unroll
@@ -552,7 +649,8 @@ __global__ void __launch_bounds__(kWgradThreads) wgrad_kernel(const WgradArgs w)
                 mma_16816(acc[2 * rt + 1], g, b[2], b[3]);
             }
         }
-        if (q8) __syncthreads();   // the widened tile is rewritten by the next step
+        // (slot (step + 3) % 4 held step - 1's tokens, which every thread is done with)
+        if (tid < 64) tok[(step + kWgradStages) % kTokRing][tid] = ahead;
     }
     cp_async_wait<0>();
     __syncthreads();
@@ -658,10 +756,60 @@ lowbit_status wgrad_launch(const WgradArgs& args, int ranks, int num, cudaStream
 
 }  // namespace
 
-ExtWorkspace ext_workspace(int64_t M, int64_t red, int num, int rank) {
+namespace {
+
+// Tokens per tile and K slices of the product. The time of a launch is modelled as
+//   waves * blocks per slice * t(tile) + the slices' reduction s(tile),
+// a block being 128 of the reduction (slot columns included: as many adapters as a tile's tokens
+// would hold drawn at random), with t and s fitted to B200 sweeps of the plain product over tiles,
+// slices, M = 24 .. 1537 and the text encoder's and square widths (in us: a tile of 32 / 64 / 128 /
+// 256 tokens takes 0.42 / 0.5 / 0.68 / 0.8 per block and 1.5 / 2 / 3 / 7 for a reduction). The
+// model's choice was within 10 % of the best of each sweep; fixed rules on M alone left 30-40 % at
+// M = 100 .. 200 (for example 4096 x 4096 at 203 tokens: 29.8 us unsplit, 21.7 as 128 x 2 slices).
+void choose_tile(int64_t M, int64_t rows, int64_t red, int num, int rank, int* tile, int* split) {
+    static constexpr int kTile[4] = {32, 64, 128, 256};
+    static constexpr double kBlockUs[4] = {0.42, 0.5, 0.68, 0.8}, kSplitUs[4] = {1.5, 2.0, 3.0, 7.0};
+    // clusters of ks CTAs, one per SM, that the GPU's processing clusters hold at once
+    static constexpr int kClusters[9] = {0, kSmsAssumed, 74, 48, 32, 24, 24, 16, 16};
+    double best = 0;
+    *tile = 0;
+    for (int i = 0; i < 4; ++i) {
+        const int bt = kTile[i];
+        if (bt < 256 && M > 16 * bt) continue;   // (small tiles of many tokens re-read W too often)
+        const int64_t tiles = (M + bt - 1) / bt * ((rows + 127) / 128);
+        double slots = 0;
+        if (num > 0) {
+            const double tokens = M < bt ? M : bt;
+            slots = num * -std::expm1(-tokens / num);
+        }
+        const double blocks = static_cast<double>((red + 127) / 128) + slots * (1 << slot_log2(rank)) / 128;
+        for (int ks = 1; ks <= 8; ++ks) {
+            if (ks > 1 && blocks < 3 * ks) break;
+            const int cap = kClusters[ks];
+            double t = kBlockUs[i], waves;
+            if (bt <= 64 && tiles > cap) {   // two CTAs per SM, which share its issue slots
+                waves = static_cast<double>((tiles + 2 * cap - 1) / (2 * cap));
+                t *= 1.5;
+            } else {
+                waves = static_cast<double>((tiles + cap - 1) / cap);
+            }
+            if (ks > 1 && waves > 1) continue;   // (a split grid is not persistent)
+            const double us = waves * std::ceil(blocks / ks) * t + (ks > 1 ? kSplitUs[i] : 0.0);
+            if (!*tile || us < best) {
+                best = us;
+                *tile = bt;
+                *split = ks;
+            }
+        }
+    }
+}
+
+}  // namespace
+
+ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int rank) {
     ExtWorkspace w = {};
     w.red64 = (red + 63) / 64 * 64;
-    w.tile_tokens = ext_tile_tokens(M);
+    choose_tile(M, rows, red, num, rank, &w.tile_tokens, &w.product_split);
     w.m_tiles = (M + w.tile_tokens - 1) / w.tile_tokens;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -715,6 +863,13 @@ lowbit_status launch_shrink(const ExtProblem& e, const ExtBuffers& b, cudaStream
     }
 }
 
+lowbit_status launch_shrink_small(const ExtProblem& e, float* p, cudaStream_t stream) {
+    return launch_pdl(shrink_small_kernel, dim3(e.ad.rank / 2, static_cast<unsigned>(e.M), 1), 32 * kShrinkSmallWarps, 0, 1,
+                      stream, static_cast<const uint4*>(e.in), static_cast<const uint4*>(e.ad.A),
+                      static_cast<int>(e.red / 8), e.ad.rank, e.ad.num, e.ad.scaling, e.ad.index, p,
+                      static_cast<__nv_bfloat16*>(e.p_out));
+}
+
 lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
     const ExtWorkspace& w = b.w;
     SideArgs s = {};
@@ -743,11 +898,16 @@ lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStrea
     auto go = [&](auto fn) {
         return launch_pdl(fn, grid, kConvThreads, 0, 1, stream, in, static_cast<int>(e.M), K8, K8p, xh, rm, s);
     };
-    if (K8p <= kConvThreads) return go(convert_side_kernel<1>);
-    if (K8p <= 2 * kConvThreads) return go(convert_side_kernel<2>);
-    if (K8p <= 4 * kConvThreads) return go(convert_side_kernel<4>);
-    if (K8p <= 8 * kConvThreads) return go(convert_side_kernel<8>);
-    return go(convert_side_kernel<0>);
+    auto pick = [&](auto lr, auto ck) {
+        constexpr bool LR = decltype(lr)::value, CK = decltype(ck)::value;
+        if (K8p <= kConvThreads) return go(convert_side_kernel<1, LR, CK>);
+        if (K8p <= 2 * kConvThreads) return go(convert_side_kernel<2, LR, CK>);
+        if (K8p <= 4 * kConvThreads) return go(convert_side_kernel<4, LR, CK>);
+        if (K8p <= 8 * kConvThreads) return go(convert_side_kernel<8, LR, CK>);
+        return go(convert_side_kernel<0, LR, CK>);
+    };
+    if (e.ad.num == 0) return pick(std::false_type{}, std::false_type{});   // (the copy comes with adapters only)
+    return s.codes ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});
 }
 
 lowbit_status launch_wgrad(const WgradProblem& g, const ExtBuffers& b, cudaStream_t stream) {
@@ -766,10 +926,20 @@ lowbit_status launch_wgrad(const WgradProblem& g, const ExtBuffers& b, cudaStrea
     a.R = g.rank;
     a.perm = b.at<int>(b.w.perm);
     a.seg = b.at<int>(b.w.seg);
-    // token slices per tile: enough CTAs for two per SM, slices of at least two 64-token steps
+    // Token slices per tile (a cluster's CTAs): whichever of 1, 2, 4, 8 gives the smallest waves x
+    // (steps per slice + a slice's fixed cost, about four steps, and two more for the reduction), two
+    // CTAs per SM and the tokens taken as evenly shared by the adapters.
     const int64_t ctas = static_cast<int64_t>(a.part[0].tiles + a.part[1].tiles) * g.num;
+    const int64_t steps = (g.M / g.num + 63) / 64;
     int ranks = 1;
-    while (ranks < 8 && ctas * ranks < 2 * num_sms() && g.M / g.num >= 256 * ranks) ranks *= 2;
+    int64_t best = 0;
+    for (int r = 1; r <= 8; r *= 2) {
+        const int64_t cost = (ctas * r + 2 * kSmsAssumed - 1) / (2 * kSmsAssumed) * ((steps + r - 1) / r + (r > 1 ? 6 : 4));
+        if (r == 1 || cost < best) {
+            best = cost;
+            ranks = r;
+        }
+    }
     switch (slot_log2(g.rank)) {
         case 4: return wgrad_launch<16>(a, ranks, g.num, stream);
         case 5: return wgrad_launch<32>(a, ranks, g.num, stream);

@@ -1,5 +1,5 @@
-// Launch of the tensor-memory kernel's adapter and gradient variants (kExtAdapter, kExtGrad): tile
-// choice, tensor maps and launch. Included by one translation unit per code width and direction,
+// Launch of the tensor-memory kernel's adapter and gradient variants (kExtAdapter, kExtGrad): tensor
+// maps and launch. Included by one translation unit per code width and direction,
 // so that the instantiations build in parallel.
 #pragma once
 
@@ -13,7 +13,7 @@ namespace {
 
 template <int BITS, int GS, int BT, bool PAIR, int EXT>
 lowbit_status ext_launch(const ExtProblem& e, const ExtBuffers& b, int rows, int ksplit, cudaStream_t stream) {
-    using C = Cfg<BITS, GS, BT, PAIR>;
+    using C = Cfg<BITS, GS, BT, PAIR, EXT>;
     auto kernel = lowbit_gemm_kernel<BITS, GS, BT, PAIR, EXT>;
     const void* fn = reinterpret_cast<const void*>(kernel);
     // the shared-memory opt-in is per device: one bit per device that has it
@@ -52,15 +52,27 @@ lowbit_status ext_launch(const ExtProblem& e, const ExtBuffers& b, int rows, int
     if (e.ad.num > 0) {
         const uint64_t pdims[3] = {64, M, static_cast<uint64_t>(w.p_cols) / 64};
         const uint64_t pstr[2] = {static_cast<uint64_t>(w.p_cols) * 2, 128};
-        ok = ok && make_map_3d(&p.map_p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b.at<void>(w.pslots), pdims, pstr, xbox,
+        const uint32_t pbox[3] = {64, static_cast<uint32_t>(C::kXRows), C::kPHalves};
+        ok = ok && make_map_3d(&p.map_p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b.at<void>(w.pslots), pdims, pstr, pbox,
                                CU_TENSOR_MAP_SWIZZLE_128B);
         p.tile_slots = b.at<int>(w.tile_slots);
         p.slot_adapter = b.at<int>(w.slot_adapter);
         p.slot_pitch = static_cast<int>(w.slot_pitch);
-        p.rank = e.ad.rank;
         p.rank_log2 = slot_log2(e.ad.rank);
-        p.out_rows = static_cast<int>(e.rows);
-        p.side = static_cast<const uint16_t*>(EXT == kExtGrad ? e.ad.A : e.ad.B);
+        // the weight side, (R, N, L) or (K, R, L): ranks past R read as zero
+        const uint64_t rk = e.ad.rank, in = EXT == kExtGrad ? R : rk, mid = EXT == kExtGrad ? rk : R;
+        const uint64_t sdims[3] = {in, mid, static_cast<uint64_t>(e.ad.num)};
+        const uint64_t sstr[2] = {in * 2, in * mid * 2};
+        p.chunk_log2 = side_chunk_log2(EXT == kExtGrad, p.rank_log2, C::kSlotCols);
+        const uint32_t chunk = 1u << p.chunk_log2;
+        const uint32_t fbox[3] = {chunk, kBlockN, 1}, gbox[3] = {64, chunk, 1};
+        const CUtensorMapSwizzle fswz = chunk == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                        : chunk == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                      : CU_TENSOR_MAP_SWIZZLE_128B;
+        ok = ok && (EXT == kExtGrad
+                        ? make_map_3d(&p.map_side, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, e.ad.A, sdims, sstr, gbox,
+                                      CU_TENSOR_MAP_SWIZZLE_128B)
+                        : make_map_3d(&p.map_side, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, e.ad.B, sdims, sstr, fbox, fswz));
     }
     p.status = device_status_address();
     if (!ok || !p.status) return LOWBIT_ERR_CUDA;
@@ -75,19 +87,6 @@ lowbit_status ext_launch(const ExtProblem& e, const ExtBuffers& b, int rows, int
     p.num_tiles = p.m_tiles * p.n_tiles;
     p.Y = static_cast<__nv_bfloat16*>(e.out);
     p.rowmul = b.at<float>(w.rowmul);
-    if (ksplit < 0) {
-        // the largest split that leaves every rank at least 24 k-blocks and keeps all clusters
-        // resident at once (as for the plain GEMM)
-        ksplit = 1;
-        const int slots = num_sms() * C::kCtasPerSm;
-        for (int ks = 8; ks >= 2; --ks) {
-            if (p.num_kb / ks < 24 || p.num_tiles * ks > slots) continue;
-            if (p.num_tiles <= cluster_capacity(fn, ks, C::kThreads, C::kSmemBytes)) {
-                ksplit = ks;
-                break;
-            }
-        }
-    }
     // An unsplit grid of 256-token tiles over a multiple of 256 weight rows runs on CTA pairs.
     if constexpr (BT == 256 && !PAIR) {
         if (rows == kBlockN && ksplit == 1 && e.rows % (2 * kBlockN) == 0)
@@ -132,30 +131,10 @@ lowbit_status ext_launch(const ExtProblem& e, const ExtBuffers& b, int rows, int
     return cudaLaunchKernelEx(&cfg, kernel, mx, mw, ms, mz, my, p) == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
 
-// Weight rows per tile and K slices, by the plain GEMM's rule: one small token tile runs either
-// flat tiles of ceil(rows / #SMs) weight rows with the whole K each, or 128-row tiles with K split
-// over a cluster; W^T's tiles are always 128 rows (a tile's group scales are rows of their own).
 template <int BITS, int GS, int EXT>
 lowbit_status ext_dispatch(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
-    const int bt = b.w.tile_tokens;
-    const int sms = num_sms();
-    const int64_t num_kb = (e.red + kBlockK - 1) / kBlockK;
-    int rows = kBlockN, ksplit = -1;
-    if (bt <= 64) {
-        ksplit = 1;
-        const int64_t tiles128 = b.w.m_tiles * ((e.rows + kBlockN - 1) / kBlockN);
-        const int64_t flat_rows = ((e.rows + sms - 1) / sms + 7) / 8 * 8;
-        const double x_per_w = (2.0 * bt) / (static_cast<double>(flat_rows) * BITS / 8.0);
-        if (EXT == kExtAdapter && flat_rows < kBlockN && x_per_w <= 1.25) {
-            rows = static_cast<int>(flat_rows);
-        } else if (tiles128 * 2 <= 2 * sms && num_kb >= 4) {
-            int64_t s = sms / tiles128;   // one CTA per SM
-            if (s > 8) s = 8;
-            if (s > num_kb / 2) s = num_kb / 2;
-            ksplit = static_cast<int>(s < 1 ? 1 : s);
-        }
-    }
-    switch (bt) {
+    const int rows = kBlockN, ksplit = b.w.product_split;
+    switch (b.w.tile_tokens) {
         case 32: return ext_launch<BITS, GS, 32, false, EXT>(e, b, rows, ksplit, stream);
         case 64: return ext_launch<BITS, GS, 64, false, EXT>(e, b, rows, ksplit, stream);
         case 128: return ext_launch<BITS, GS, 128, false, EXT>(e, b, rows, ksplit, stream);

@@ -64,7 +64,25 @@ constexpr int kSmemLimit = 232448;  // 227 KB opt-in dynamic shared memory per b
 // CTA decodes its 128 weight rows into its own tensor memory and loads half of the X tile (BT/2
 // tokens); the even CTA issues the MMAs, which read both halves of X, so every X element read
 // into shared memory serves 256 weight rows instead of 128.
-template <int BITS, int GS, int BT, bool PAIR = false>
+//
+// Variants of the kernel that adapters and gradients run on (EXT).
+//   kExtAdapter   Y = X W^T + P B: behind the K of the packed weights the reduction goes on over
+//                 `slot` columns, Rp (a power of two >= 16) for each adapter that the token tile
+//                 holds. The X side of a slot is P (bf16, zero in the rows of other adapters'
+//                 tokens), the weight side the adapter's rows B[a][n][0..R). Both come through the X
+//                 ring (a stage of each per block of columns) and are multiplied bf16 x bf16 out of
+//                 shared memory onto the same fp32 accumulators, so Y is rounded once and the
+//                 dequant warps have no part in it. (Rows of B moved through the tensor-memory ring
+//                 by the dequant warps, from global memory or from 4 KB weight stages, cost 4-5 us
+//                 per block of 128 columns against 0.8 for a block of packed weights.)
+//   kExtGrad      dX = dY W (+ dP A): the packed words of W^T (rows k, codes along n). A group
+//                 scale now belongs to a column pair of the reduction instead of to the row, so the
+//                 stage's scales [group of the tile's rows][128 n] multiply fp16x2 pairs. The
+//                 adapters' weight side is A[a][0..R)[k], which lies with its rows k contiguous: an
+//                 MN-major operand.
+constexpr int kExtNone = 0, kExtAdapter = 1, kExtGrad = 2;
+
+template <int BITS, int GS, int BT, bool PAIR = false, int EXT = kExtNone>
 struct Cfg {
     static_assert(BITS == 1 || BITS == 2 || BITS == 4, "bits");
     static_assert(GS == 64 || GS == 128, "group size");
@@ -137,7 +155,13 @@ struct Cfg {
     }
     static_assert(PAIR || max_recv_bytes() <= kXStages * kXStageBytes, "split-K receive buffer");
     static constexpr uint32_t kIdesc = idesc_f16_f32(PAIR ? 2 * kBlockN : kBlockN, BT);
-    static constexpr uint32_t kIdescBf16 = idesc_bf16_f32(PAIR ? 2 * kBlockN : kBlockN, BT);
+    // Slot columns: a block of them is what fits one X stage as 128 rows of the weight side; P's box
+    // of a block is one or two 64-wide halves.
+    static constexpr int kSlotCols = kXStageBytes >= 256 * 128 ? 128 : kXStageBytes / 256;
+    static constexpr int kPHalves = (kSlotCols + 63) / 64;
+    static_assert(EXT == kExtNone || (kSlotCols >= 32 && kPHalves * kXHalfBytes <= kXStageBytes), "slot block");
+    static constexpr uint32_t kIdescSlot =
+        idesc_bf16_f32(PAIR ? 2 * kBlockN : kBlockN, BT) | (EXT == kExtGrad ? kIdescTransposeA : 0u);
     // the last tile's bf16 Y box [BT][128 rows] is staged at the start of the (idle) X ring
     static constexpr int kYStageBytes = BT * kBlockN * 2;
     static_assert(kYStageBytes <= kXStages * kXStageBytes, "Y staging");
@@ -155,29 +179,24 @@ struct KernelParams {
     const float* rowmul; // per-row power-of-two factor written by the X conversion pass
 };
 
-// Variants of the kernel that adapters and gradients run on.
-//   kExtAdapter   Y = X W^T + P B: behind the K of the packed weights the reduction goes on over
-//                 `slot` columns, Rp (a power of two >= 16) for each adapter that the token tile
-//                 holds. The X side of a slot is P (bf16, zero in the rows of other adapters'
-//                 tokens), the weight side the adapter's rows B[a][n][0..R), read by the dequant
-//                 warps straight from global memory into the tensor-memory ring. Those blocks
-//                 run as bf16 x bf16 MMAs on the same fp32 accumulators, so Y is rounded once.
-//   kExtGrad      dX = dY W (+ dP A): the packed words of W^T (rows k, codes along n). A group
-//                 scale now belongs to a column pair of the reduction instead of to the row, so the
-//                 stage's scales [group of the tile's rows][128 n] multiply fp16x2 pairs. The
-//                 adapters' weight side is A[a][0..R)[k].
-constexpr int kExtNone = 0, kExtAdapter = 1, kExtGrad = 2;
-
 struct ExtParams : KernelParams {
-    CUtensorMap map_p;       // P as (64, M, columns / 64) bf16, boxes like X's
+    CUtensorMap map_p;       // P as (64, M, columns / 64) bf16, boxes of kPHalves halves
+    CUtensorMap map_side;    // B as (R, N, L), boxes of `chunk` ranks x 128 rows, or A as (K, R, L),
+                             // boxes of 64 rows x `chunk` ranks
     const int* tile_slots;   // slots of each token tile (nullptr: no adapters)
     const int* slot_adapter; // [token tile][slot_pitch]
     int slot_pitch;
-    int rank, rank_log2;     // R, and log2 of the slot width Rp
-    int out_rows;            // rows of one adapter's weight side: N (kExtAdapter) or K (kExtGrad)
-    const uint16_t* side;    // B [a][out_rows][R], or A [a][R][out_rows] (kExtGrad)
+    int rank_log2;           // log2 of the slot width Rp
+    int chunk_log2;          // log2 of the slot columns per box of the weight side
     unsigned* status;        // the device status word
 };
+// Slot columns per box: up to 64 for B (the widest swizzled row), whole slots for A, and no more
+// than a block.
+inline int side_chunk_log2(bool grad, int rank_log2, int slot_cols) {
+    int c = rank_log2;
+    while ((1 << c) > slot_cols || (!grad && c > 6)) --c;
+    return c;
+}
 template <int EXT>
 using ParamsOf = std::conditional_t<EXT == kExtNone, KernelParams, ExtParams>;
 
@@ -247,35 +266,43 @@ __device__ __forceinline__ void decode_word_b4(uint32_t v, uint16_t s, float cz,
 }
 
 // One 64-wide half of a reduction stage of W^T: the row's codes as above, but each pair of
-// columns has scales (and zeros) of its own, `sp` / `zp` holding them as 32 fp16x2 words. Binary
-// and ternary weights are again exactly +-s or 0. uint4: q is exact, q - z and the product with s
-// are each rounded to fp16 once (2^-11 relative each, no cancellation behind a rounding), which
-// halves the instructions of an fp32 product per weight; the sum of both is below the 2^-9 of
-// one bf16 rounding.
+// columns has scales (and zeros) of its own, read from shared memory (`s4`, `z4`) four pairs at a
+// time. Binary and ternary weights are again exactly +-s or 0. uint4: q is exact, q - z and the
+// product with s are each rounded to fp16 once (2^-11 relative each, no cancellation behind a
+// rounding), which halves the instructions of an fp32 product per weight; both together stay below
+// the 2^-9 of one bf16 rounding.
 template <int BITS>
-__device__ __forceinline__ void decode_half_grad(const uint32_t* words, const uint32_t* sp, const uint32_t* zp,
+__device__ __forceinline__ void decode_half_grad(const uint32_t* words, const uint4* s4, const uint4* z4,
                                                  uint32_t (&out)[32]) {
-    constexpr uint32_t kMagic = 0x64006400u;                     // 1024.0, as in the decoders above
-    if (BITS == 1) {
+    constexpr uint32_t kMagic = 0x64006400u;   // 1024.0, and the constants of the decoders above
+    constexpr uint32_t kMul[5] = {0x3C003C00u, 0x34003400u, 0x2C002C00u, 0x24002400u, 0x1C001C00u};
+    constexpr uint32_t kAdd2[5] = {0xE401E401u, 0xDC04DC04u, 0xD410D410u, 0xCC40CC40u, 0xC500C500u};
+    constexpr uint32_t kAdd4[2] = {0xE400E400u, 0xD400D400u};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) out[i] = xor_andnot(sp[i], words[i >> 4] << (15 - (i & 15)), 0x80008000u);
-    } else if (BITS == 2) {
+    for (int g = 0; g < 8; ++g) {              // pairs 4g .. 4g + 3 of the half
+        const uint4 sv = s4[g];
+        const uint32_t sp[4] = {sv.x, sv.y, sv.z, sv.w};
+        uint32_t zp[4] = {0, 0, 0, 0};
+        if (BITS == 4) {
+            const uint4 zv = z4[g];
+            zp[0] = zv.x; zp[1] = zv.y; zp[2] = zv.z; zp[3] = zv.w;
+        }
 #pragma unroll
-        for (int w = 0; w < 4; ++w) decode_word_b2(words[w], 0x3C003C00u, out, w);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) out[i] = f16x2_mul(out[i], sp[i]);
-    } else {
-        constexpr uint32_t kMul[2] = {0x3C003C00u, 0x2C002C00u};   // 1, 1/16
-        constexpr uint32_t kAdd[2] = {0xE400E400u, 0xD400D400u};   // -1024, -64
-#pragma unroll
-        for (int w = 0; w < 8; ++w)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int i = 16 * (w >> 2) + 4 * c + (w & 3);
-                const uint32_t e = and_or(words[w] >> ((c < 2) ? 0 : 8), 0x000F000Fu << (4 * (c & 1)), kMagic);
-                const uint32_t q = f16x2_fma(e, kMul[c & 1], kAdd[c & 1]);
-                out[i] = f16x2_mul(f16x2_sub(q, zp[i]), sp[i]);
+        for (int q = 0; q < 4; ++q) {
+            if (BITS == 1) {
+                const int i = 4 * g + q;
+                out[i] = xor_andnot(sp[q], words[i >> 4] << (15 - (i & 15)), 0x80008000u);
+            } else if (BITS == 2) {            // pair g of word q
+                const int j = g < 5 ? g : g - 5;
+                const uint32_t e = and_or(words[q] >> (g < 5 ? 0 : 10), 0x00030003u << (2 * j), kMagic);
+                out[4 * g + q] = f16x2_mul(f16x2_fma(e, kMul[j], kAdd2[j]), sp[q]);
+            } else {                           // pair c of word q of block g / 4
+                const int c = g & 3;
+                const uint32_t e = and_or(words[4 * (g >> 2) + q] >> (c < 2 ? 0 : 8), 0x000F000Fu << (4 * (c & 1)), kMagic);
+                const uint32_t v = f16x2_fma(e, kMul[2 * (c & 1)], kAdd4[c & 1]);
+                out[4 * g + q] = f16x2_mul(f16x2_sub(v, zp[q]), sp[q]);
             }
+        }
     }
 }
 
@@ -283,11 +310,11 @@ __device__ __forceinline__ void decode_half_grad(const uint32_t* words, const ui
 // The kernel
 // ---------------------------------------------------------------------------------------------
 template <int BITS, int GS, int BT, bool PAIR, int EXT = kExtNone>
-__global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR>::kThreads, Cfg<BITS, GS, BT, PAIR>::kCtasPerSm)
+__global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BITS, GS, BT, PAIR, EXT>::kCtasPerSm)
     lowbit_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_z,
                        const __grid_constant__ CUtensorMap map_y, const __grid_constant__ ParamsOf<EXT> p) {
-    using C = Cfg<BITS, GS, BT, PAIR>;
+    using C = Cfg<BITS, GS, BT, PAIR, EXT>;
     constexpr int SX = C::kXStages;
     constexpr int SW = C::kWStages;
     constexpr int NA = C::kNumA;
@@ -373,15 +400,23 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR>::kThreads, Cfg<BITS, G
     // starting at pair_rank * p.rows
     const int n_stride = PAIR ? 2 * p.rows : p.rows;
     const int n_off = PAIR ? static_cast<int>(pair_rank) * p.rows : 0;
-    // Reduction columns that the adapters of tile `tile`'s tokens add behind this CTA's K slice
-    // (a multiple of 16, in blocks of 128; the last K slice takes them). Read after
-    // grid_dependency_wait().
-    auto extra_cols = [&](int tile) -> int {
+    // The slot columns that the adapters of tile t's tokens add behind this CTA's K slice: columns
+    // [x0, x1) of the tile's, multiples of 16, in blocks of kSlotCols shared out over the K slices.
+    // Read after grid_dependency_wait().
+    struct Extra {
+        int x0, x1;
+        __device__ int blocks() const { return (x1 - x0 + C::kSlotCols - 1) / C::kSlotCols; }
+    };
+    auto extra_of = [&](int t) -> Extra {
         if constexpr (EXT == kExtNone) {
-            return 0;
+            return Extra{0, 0};
         } else {
-            if (!p.tile_slots || (split && kb_end != p.num_kb)) return 0;
-            return p.tile_slots[tile / p.n_tiles] << p.rank_log2;
+            if (!p.tile_slots || t >= my_tiles) return Extra{0, 0};
+            const int cols = __ldg(p.tile_slots + (tile0 + t * tile_step) / p.n_tiles) << p.rank_log2;
+            if (!split) return Extra{0, cols};
+            const int per = ((cols + C::kSlotCols - 1) / C::kSlotCols + p.ksplit - 1) / p.ksplit * C::kSlotCols;
+            const int x0 = min(cols, static_cast<int>(blockIdx.z) * per);
+            return Extra{x0, min(cols, x0 + per)};
         }
     };
     unsigned* status;
@@ -393,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR>::kThreads, Cfg<BITS, G
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
         if (lane == 0) {
-            const uint32_t total = static_cast<uint32_t>(my_tiles * nkb);
+            const uint32_t total = static_cast<uint32_t>(my_tiles * nkb);   // (slot columns not counted)
             auto coords = [&](uint32_t it, int& m0, int& n0, int& kb) {
                 const int tile = tile0 + static_cast<int>(it / nkb) * tile_step;
                 kb = kb_begin + static_cast<int>(it % nkb);
@@ -413,23 +448,59 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR>::kThreads, Cfg<BITS, G
                 tma_load_2d(&map_s, &wfull[s], st + C::kSOff, sx, sy);
                 if (BITS == 4) tma_load_2d(&map_z, &wfull[s], st + C::kZOff, sx, sy);
             };
-            // the next X block to request: block xj of the CTA's tile xt, which has xn of them
-            int xt = 0, xj = 0, xn = 0;
-            auto x_blocks = [&](int t) {
-                return t < my_tiles ? nkb + (extra_cols(tile0 + t * tile_step) + kBlockK - 1) / kBlockK : 0;
+            // With slot columns a tile has more X stages than nkb: behind the K blocks, P and the weight
+            // side of each block of columns. xj: the next stage of tile xt (of nkb + 2 * blocks).
+            int xt = 0, xj = 0;
+            Extra xe{0, 0};
+            auto issue_slots = [&](uint32_t s) {
+                if constexpr (EXT != kExtNone) {
+                    const int tile = tile0 + xt * tile_step;
+                    const int m0 = tile / p.n_tiles * BT, n0 = tile % p.n_tiles * n_stride + n_off;
+                    const int c0 = xe.x0 + (xj - nkb) / 2 * C::kSlotCols;
+                    const int c1 = min(xe.x1, c0 + C::kSlotCols);
+                    uint8_t* st = smem + s * C::kXStageBytes;
+                    auto load = [&](const CUtensorMap* map, uint8_t* dst, int x, int y, int z) {
+                        if (PAIR)
+                            tma_load_3d_pair(map, on_issuer(&xfull[s]), dst, x, y, z);
+                        else
+                            tma_load_3d(map, &xfull[s], dst, x, y, z);
+                    };
+                    if (((xj - nkb) & 1) == 0) {
+                        if (issuer) mbar_arrive_expect_tx(&xfull[s], kPairCtas * C::kPHalves * C::kXHalfBytes);
+                        load(&p.map_p, st, 0, m0 + static_cast<int>(pair_rank) * C::kXRows, c0 / 64);
+                    } else {
+                        const int chunk = 1 << p.chunk_log2, chunks = (c1 - c0) >> p.chunk_log2;
+                        const int* slots = p.slot_adapter + static_cast<size_t>(tile / p.n_tiles) * p.slot_pitch;
+                        if (issuer) mbar_arrive_expect_tx(&xfull[s], kPairCtas * (chunks << (p.chunk_log2 + 8)));
+                        for (int i = 0; i < chunks; ++i) {
+                            const int c = c0 + i * chunk, r = c & ((1 << p.rank_log2) - 1);
+                            const int a = __ldg(slots + (c >> p.rank_log2));
+                            uint8_t* dst = st + i * chunk * 256;
+                            if (EXT == kExtAdapter) {
+                                load(&p.map_side, dst, r, n0, a);
+                            } else {
+                                load(&p.map_side, dst, n0, r, a);
+                                load(&p.map_side, dst + chunk * 128, n0 + 64, r, a);
+                            }
+                        }
+                    }
+                    if (++xj == nkb + 2 * xe.blocks()) {
+                        xj = 0;
+                        xe = extra_of(++xt);
+                    }
+                }
             };
             auto issue_x = [&](uint32_t it) {
                 int m0, n0, kb;
-                const CUtensorMap* map = &map_x;
                 if constexpr (EXT == kExtNone) {
                     coords(it, m0, n0, kb);
                 } else {
+                    if (xj >= nkb) return issue_slots(it % SX);
                     m0 = ((tile0 + xt * tile_step) / p.n_tiles) * BT;
-                    kb = xj < nkb ? kb_begin + xj : xj - nkb;
-                    if (xj >= nkb) map = &p.map_p;
-                    if (++xj == xn) {
+                    kb = kb_begin + xj;
+                    if (++xj == nkb + 2 * xe.blocks()) {
                         xj = 0;
-                        xn = x_blocks(++xt);
+                        xe = extra_of(++xt);
                     }
                 }
                 const uint32_t s = it % SX;
@@ -437,11 +508,11 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR>::kThreads, Cfg<BITS, G
                 // box (64 k, kXRows tokens, 2 halves) = both 128-byte-swizzled K halves in one request
                 if (!PAIR) {
                     mbar_arrive_expect_tx(&xfull[s], C::kXBytes);
-                    tma_load_3d(map, &xfull[s], st, 0, m0, kb * 2);
+                    tma_load_3d(&map_x, &xfull[s], st, 0, m0, kb * 2);
                 } else {
                     // both halves complete on the issuer's barrier, which expects both
                     if (issuer) mbar_arrive_expect_tx(&xfull[s], 2 * C::kXBytes);
-                    tma_load_3d_pair(map, on_issuer(&xfull[s]), st, 0, m0 + static_cast<int>(pair_rank) * C::kXRows,
+                    tma_load_3d_pair(&map_x, on_issuer(&xfull[s]), st, 0, m0 + static_cast<int>(pair_rank) * C::kXRows,
                                      kb * 2);
                 }
             };
@@ -452,7 +523,7 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR>::kThreads, Cfg<BITS, G
             const uint32_t wpre = total < static_cast<uint32_t>(SW) ? total : static_cast<uint32_t>(SW);
             for (; itw < wpre; ++itw) issue_w(itw);
             grid_dependency_wait();
-            if (EXT != kExtNone) xn = x_blocks(0);
+            if constexpr (EXT != kExtNone) xe = extra_of(0);
             auto x_left = [&] { return EXT == kExtNone ? itx < total : xt < my_tiles; };
             // Fill both rings as their slots free up, without blocking on either.
             bool ok = true;
@@ -509,7 +580,11 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR>::kThreads, Cfg<BITS, G
             uint32_t it = 0, ait = 0, tcount = 0;
             bool ok = true;
             bool issued = false;
-            if (EXT != kExtNone) grid_dependency_wait();   // before the tiles' slot counts
+            Extra xe{0, 0};
+            if constexpr (EXT != kExtNone) {
+                grid_dependency_wait();   // before the tiles' slot counts
+                xe = extra_of(0);
+            }
             for (int t = 0; t < my_tiles && ok; ++t, ++tcount) {
                 const uint32_t b = tcount % NACC, acc_ph = (tcount / NACC) & 1u;
                 if (!mbar_wait(&accempty[b], acc_ph ^ 1u, abort_flag, status)) {
@@ -518,29 +593,23 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR>::kThreads, Cfg<BITS, G
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + b * BT;
-                const int xcols = extra_cols(tile0 + t * tile_step);
-                const int kb_last = kb_end + (xcols + kBlockK - 1) / kBlockK;
-                for (int kb = kb_begin; kb < kb_last; ++kb, ++it, ++ait) {
+                const Extra xnext = extra_of(t + 1);   // (its latency hides behind this tile's MMAs)
+                for (int kb = kb_begin; kb < kb_end; ++kb, ++it, ++ait) {
                     const uint32_t s = it % SX, ph = (it / SX) & 1u;
                     const uint32_t a = ait % NA, aph = (ait / NA) & 1u;
                     if (!mbar_wait(&xfull[s], ph, abort_flag, status)) { ok = false; break; }
                     if (!mbar_wait(&afull[a], aph, abort_flag, status)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t xs = smem_u32(smem + s * C::kXStageBytes);
-                    // a block behind K: bf16 operands, and only the columns that slots fill
-                    const bool extra = EXT != kExtNone && kb >= kb_end;
-                    const uint32_t idesc = extra ? C::kIdescBf16 : C::kIdesc;
-                    const int kks = extra ? min(kBlockK, xcols - (kb - kb_end) * kBlockK) / 16 : kBlockK / 16;
 #pragma unroll
                     for (int kk = 0; kk < kBlockK / 16; ++kk) {
-                        if (EXT != kExtNone && kk >= kks) break;
                         const uint32_t a_tmem = tmem_base + C::kACol0 + a * 64 + kk * 8;
                         const uint64_t bdesc =
                             smem_desc_k_sw128(xs + (kk >> 2) * C::kXHalfBytes + (kk & 3) * 32);
                         if (PAIR)
-                            mma_f16_ts_pair(d_tmem, a_tmem, bdesc, idesc, (kb > kb_begin || kk > 0) ? 1u : 0u);
+                            mma_f16_ts_pair(d_tmem, a_tmem, bdesc, C::kIdesc, (kb > kb_begin || kk > 0) ? 1u : 0u);
                         else
-                            mma_f16_ts(d_tmem, a_tmem, bdesc, idesc, (kb > kb_begin || kk > 0) ? 1u : 0u);
+                            mma_f16_ts(d_tmem, a_tmem, bdesc, C::kIdesc, (kb > kb_begin || kk > 0) ? 1u : 0u);
                     }
                     issued = true;
                     if (PAIR) {
@@ -550,6 +619,45 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR>::kThreads, Cfg<BITS, G
                         mma_commit(&xempty[s]);
                         mma_commit(&aempty[a]);
                     }
+                }
+                if constexpr (EXT != kExtNone) {
+                    // slot columns: P in one stage (the MMA's B operand), the weight side in the next (A)
+                    for (int c0 = xe.x0; ok && c0 < xe.x1; c0 += C::kSlotCols, it += 2) {
+                        const uint32_t sp = it % SX, ss = (it + 1) % SX;
+                        if (!mbar_wait(&xfull[sp], (it / SX) & 1u, abort_flag, status) ||
+                            !mbar_wait(&xfull[ss], ((it + 1) / SX) & 1u, abort_flag, status)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t ps = smem_u32(smem + sp * C::kXStageBytes);
+                        const uint32_t as = smem_u32(smem + ss * C::kXStageBytes);
+                        const int cols = min(C::kSlotCols, xe.x1 - c0);
+#pragma unroll 1
+                        for (int c = 0; c < cols; c += 16) {
+                            // P's box starts at a multiple of 64 columns
+                            const int pc = (c0 & 63) + c;
+                            const uint64_t bdesc =
+                                smem_desc_k_sw128(ps + (pc >> 6) * C::kXHalfBytes + (pc & 63) * 2);
+                            const uint32_t box = as + ((c >> p.chunk_log2) << (p.chunk_log2 + 8));
+                            const int in = c & ((1 << p.chunk_log2) - 1);
+                            const uint64_t adesc = EXT == kExtAdapter
+                                                       ? smem_desc_k(box + in * 2, 2 << p.chunk_log2)
+                                                       : smem_desc_mn_sw128(box + in * 128, 128 << p.chunk_log2);
+                            if (PAIR)
+                                mma_f16_ss_pair(d_tmem, adesc, bdesc, C::kIdescSlot, 1u);
+                            else
+                                mma_f16_ss(d_tmem, adesc, bdesc, C::kIdescSlot, 1u);
+                        }
+                        if (PAIR) {
+                            mma_commit_pair_mc(&xempty[sp], 0x3);
+                            mma_commit_pair_mc(&xempty[ss], 0x3);
+                        } else {
+                            mma_commit(&xempty[sp]);
+                            mma_commit(&xempty[ss]);
+                        }
+                    }
+                    xe = xnext;
                 }
                 if (!ok) break;
                 if (PAIR)
@@ -644,20 +752,10 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR>::kThreads, Cfg<BITS, G
                     if constexpr (EXT == kExtGrad) {
                         // scales (zeros) of the half's 64 columns for this row's group: the same
                         // words for the whole warp (a group holds at least 64 rows)
-                        uint32_t sp[32], zp[32];
                         const int gr = (GS == 64) ? (row >> 6) : 0;
-                        const uint4* s4 = reinterpret_cast<const uint4*>(st + C::kSOff + gr * kBlockN * 2 + h * 128);
-                        const uint4* z4 = reinterpret_cast<const uint4*>(st + C::kZOff + gr * kBlockN * 2 + h * 128);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint4 v = s4[i];
-                            sp[4 * i] = v.x; sp[4 * i + 1] = v.y; sp[4 * i + 2] = v.z; sp[4 * i + 3] = v.w;
-                            if (BITS == 4) {
-                                const uint4 u = z4[i];
-                                zp[4 * i] = u.x; zp[4 * i + 1] = u.y; zp[4 * i + 2] = u.z; zp[4 * i + 3] = u.w;
-                            }
-                        }
-                        decode_half_grad<BITS>(words[hh], sp, zp, out);
+                        const uint8_t* sz = st + gr * kBlockN * 2 + h * 128;
+                        decode_half_grad<BITS>(words[hh], reinterpret_cast<const uint4*>(sz + C::kSOff),
+                                               reinterpret_cast<const uint4*>(sz + C::kZOff), out);
                     } else if (BITS == 1) {
                         decode_half_b1(words[hh][0], words[hh][1], s2[hh], out);
                     } else if (BITS == 2) {
@@ -680,65 +778,6 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR>::kThreads, Cfg<BITS, G
                         mbar_arrive_remote(on_issuer(&afull[a]));
                     else
                         mbar_arrive(&afull[a]);
-                }
-            }
-            if constexpr (EXT != kExtNone) {
-                // --- the adapters' blocks: bf16 rows of their weight side, from global memory
-                if (!ok) break;
-                if (t == 0) grid_dependency_wait();
-                const int tile = tile0 + t * tile_step;
-                const int xcols = extra_cols(tile);
-                const int n = (tile % p.n_tiles) * n_stride + n_off + row;
-                const bool n_ok = row_ok && n < p.out_rows;
-                const int* slots = p.slot_adapter + static_cast<size_t>(tile / p.n_tiles) * p.slot_pitch;
-                for (int c0 = 0; c0 < xcols; c0 += kBlockK, ++ait) {
-                    const uint32_t a = ait % NA, aph = (ait / NA) & 1u;
-                    bool waited = false;
-#pragma unroll
-                    for (int hh = 0; hh < kHalvesPerPart; ++hh) {
-                        const int h = part * kHalvesPerPart + hh;
-                        uint32_t out[32];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {          // eight columns of one slot at a time
-                            const int c = c0 + h * 64 + j * 8;
-                            const int r = c & ((1 << p.rank_log2) - 1);
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            if (n_ok && c < xcols && r < p.rank) {
-                                const size_t ad = static_cast<size_t>(slots[c >> p.rank_log2]);
-                                if constexpr (EXT == kExtAdapter) {
-                                    v = __ldg(reinterpret_cast<const uint4*>(p.side + (ad * p.out_rows + n) * p.rank + r));
-                                } else {
-                                    const uint16_t* src = p.side + (ad * p.rank + r) * p.out_rows + n;
-                                    uint32_t u[8];
-#pragma unroll
-                                    for (int q = 0; q < 8; ++q) u[q] = __ldg(src + static_cast<size_t>(q) * p.out_rows);
-                                    v = make_uint4(u[0] | (u[1] << 16), u[2] | (u[3] << 16), u[4] | (u[5] << 16),
-                                                   u[6] | (u[7] << 16));
-                                }
-                            }
-                            out[4 * j] = v.x; out[4 * j + 1] = v.y; out[4 * j + 2] = v.z; out[4 * j + 3] = v.w;
-                        }
-                        if (!waited) {
-                            if (!__all_sync(0xffffffffu, mbar_wait(&aempty[a], aph ^ 1u, abort_flag, status))) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            waited = true;
-                        }
-                        if (dcheck(C::kACol0 + a * 64 + h * 32 + 32 <= C::kTmemCols, status))
-                            tmem_st32(lane_base + C::kACol0 + a * 64 + h * 32, out);
-                    }
-                    if (!ok) break;
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (PAIR && !issuer)
-                            mbar_arrive_remote(on_issuer(&afull[a]));
-                        else
-                            mbar_arrive(&afull[a]);
-                    }
                 }
             }
         }

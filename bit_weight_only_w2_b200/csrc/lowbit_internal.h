@@ -57,7 +57,14 @@ lowbit_status launch_convert_x(const GemmProblem& g, cudaStream_t stream);
 // to 8 tokens as its n8 operand (M <= 8; rows a multiple of 16). smallm_supported: whether the
 // shape fits the kernel at all.
 bool smallm_supported(const GemmProblem& g);
-lowbit_status smallm_launch(const GemmProblem& g, int rows, int ksplit, bool swap, cudaStream_t stream);
+struct LowRank {            // a low-rank term added before Y is rounded: Y[m] += p[m] * b[index[m]]^T
+    const float* p;         // [M][rank]
+    const void* b;          // bf16 [num][N][rank]
+    const int32_t* index;   // [M], out-of-range values: none; nullptr: 0 for every token
+    int num, rank;
+};
+lowbit_status smallm_launch(const GemmProblem& g, int rows, int ksplit, bool swap, cudaStream_t stream,
+                            const LowRank* lr = nullptr);
 
 // Device address of the current device's status word (nullptr on failure).
 unsigned* device_status_address();

@@ -3,4 +3,4 @@
 
 #include "smallm_kernel.cuh"
 
-LOWBIT_SMALLM_TABLE(1)
+LOWBIT_SMALLM_TABLE(kernel_b1, 1, false)

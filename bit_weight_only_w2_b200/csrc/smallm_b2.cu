@@ -3,4 +3,4 @@
 
 #include "smallm_kernel.cuh"
 
-LOWBIT_SMALLM_TABLE(2)
+LOWBIT_SMALLM_TABLE(kernel_b2, 2, false)

@@ -3,4 +3,4 @@
 
 #include "smallm_kernel.cuh"
 
-LOWBIT_SMALLM_TABLE(4)
+LOWBIT_SMALLM_TABLE(kernel_b4, 4, false)

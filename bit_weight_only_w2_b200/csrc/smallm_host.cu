@@ -12,7 +12,8 @@ namespace lowbit {
 namespace smallm {
 namespace {
 
-const void* kernel_for(int bits, int gs, int noct, bool swap) {
+const void* kernel_for(int bits, int gs, int noct, bool swap, bool lr) {
+    if (lr) return bits == 1 ? kernel_lr_b1(gs, noct, swap) : bits == 2 ? kernel_lr_b2(gs, noct, swap) : kernel_lr_b4(gs, noct, swap);
     switch (bits) {
         case 1: return kernel_b1(gs, noct, swap);
         case 2: return kernel_b2(gs, noct, swap);
@@ -30,7 +31,7 @@ bool prepare(const void* fn) {
         const void* fn;
         int dev;
     };
-    static Done done[8 * 3 * 2 * (kMaxOct + kMaxOct / 2)];
+    static Done done[2 * 8 * 3 * 2 * (kMaxOct + kMaxOct / 2)];
     static int used = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
@@ -124,15 +125,16 @@ Choice choose(const void* probe, int bits, int gs, int N, int K, int force_rows,
 }
 
 template <int BITS, int GS>
-lowbit_status launch(const GemmProblem& g, int force_rows, int force_split, bool swap, cudaStream_t stream) {
+lowbit_status launch(const GemmProblem& g, int force_rows, int force_split, bool swap, const LowRank* lr,
+                     cudaStream_t stream) {
     using F = Fmt<BITS, GS>;
     const int M = static_cast<int>(g.M), N = static_cast<int>(g.N), K = static_cast<int>(g.K);
-    const void* probe = kernel_for(BITS, GS, 8, swap);
+    const void* probe = kernel_for(BITS, GS, 8, swap, lr != nullptr);
     if (!probe || !prepare(probe)) return LOWBIT_ERR_CUDA;
     const Choice ch = choose(probe, BITS, GS, N, K, force_rows, force_split, swap);
-    const void* fn = kernel_for(BITS, GS, ch.rows / 8, swap);
+    const void* fn = kernel_for(BITS, GS, ch.rows / 8, swap, lr != nullptr);
     if (!fn || !prepare(fn)) return LOWBIT_ERR_CUDA;
-    Params p;
+    LrParams p = {};
     int smem = 0;
     if (!layout<BITS, GS>(ch.rows, ch.ksplit, swap, &p, &smem)) return LOWBIT_ERR_UNSUPPORTED;
     p.M = M;
@@ -144,6 +146,13 @@ lowbit_status launch(const GemmProblem& g, int force_rows, int force_split, bool
     p.Y = static_cast<__nv_bfloat16*>(g.Y);
     p.status = device_status_address();
     if (!p.status) return LOWBIT_ERR_CUDA;
+    if (lr) {
+        p.lr_p = lr->p;
+        p.lr_b = static_cast<const __nv_bfloat16*>(lr->b);
+        p.lr_index = lr->index;
+        p.lr_num = lr->num;
+        p.lr_rank = lr->rank;
+    }
 
     CUtensorMap mx, mw, ms, mz;
     const uint64_t xdims[3] = {64, static_cast<uint64_t>(M), static_cast<uint64_t>(K) / 64};
@@ -181,7 +190,7 @@ lowbit_status launch(const GemmProblem& g, int force_rows, int force_split, bool
     cfg.stream = stream;
     cfg.attrs = attrs;
     cfg.numAttrs = na;
-    void* args[] = {&mx, &mw, &ms, &mz, &p};
+    void* args[] = {&mx, &mw, &ms, &mz, &p};   // (the plain kernel takes the Params part of p)
     if (take_injected_failure(kInjectLaunch)) return LOWBIT_ERR_CUDA;
     return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
@@ -191,17 +200,18 @@ lowbit_status launch(const GemmProblem& g, int force_rows, int force_split, bool
 
 bool smallm_supported(const GemmProblem& g) { return g.M >= 1 && g.M <= smallm::kTokens; }
 
-lowbit_status smallm_launch(const GemmProblem& g, int rows, int ksplit, bool swap, cudaStream_t stream) {
+lowbit_status smallm_launch(const GemmProblem& g, int rows, int ksplit, bool swap, cudaStream_t stream,
+                            const LowRank* lr) {
     if (!smallm_supported(g) || (swap && g.M > smallm::kSwapTokens)) return LOWBIT_ERR_UNSUPPORTED;
     if (rows < 0 || rows > smallm::kMaxRows || rows % (swap ? 16 : 8) != 0 || ksplit < 0 || ksplit > 8)
         return LOWBIT_ERR_UNSUPPORTED;
     switch (g.bits * 1000 + g.group_size) {
-        case 1064: return smallm::launch<1, 64>(g, rows, ksplit, swap, stream);
-        case 1128: return smallm::launch<1, 128>(g, rows, ksplit, swap, stream);
-        case 2064: return smallm::launch<2, 64>(g, rows, ksplit, swap, stream);
-        case 2128: return smallm::launch<2, 128>(g, rows, ksplit, swap, stream);
-        case 4064: return smallm::launch<4, 64>(g, rows, ksplit, swap, stream);
-        case 4128: return smallm::launch<4, 128>(g, rows, ksplit, swap, stream);
+        case 1064: return smallm::launch<1, 64>(g, rows, ksplit, swap, lr, stream);
+        case 1128: return smallm::launch<1, 128>(g, rows, ksplit, swap, lr, stream);
+        case 2064: return smallm::launch<2, 64>(g, rows, ksplit, swap, lr, stream);
+        case 2128: return smallm::launch<2, 128>(g, rows, ksplit, swap, lr, stream);
+        case 4064: return smallm::launch<4, 64>(g, rows, ksplit, swap, lr, stream);
+        case 4128: return smallm::launch<4, 128>(g, rows, ksplit, swap, lr, stream);
         default: return LOWBIT_ERR_UNSUPPORTED;
     }
 }

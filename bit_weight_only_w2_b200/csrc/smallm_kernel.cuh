@@ -47,6 +47,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "lowbit_internal.h"
 #include "sm100_ptx.cuh"
@@ -92,6 +93,20 @@ struct Params {
     __nv_bfloat16* Y;
     unsigned* status;     // the device status word (bounded waits record timeouts here)
 };
+
+// The LR variant of the kernel adds the low-rank term of each token's adapter to the fp32 sums before
+// Y is rounded: Y[m][n] += lr_p[m][0..R) . lr_b[a][n][0..R), a = lr_index[m]. At 16 tokens those are
+// 16 * R products per weight row, far fewer than the row's 16 * K, so the threads that finish an
+// output form them with fp32 FMAs on rows of B read once from memory (asked into L2 when the CTA
+// starts). A variant of its own, so that the plain kernel's registers stay what they are.
+struct LrParams : Params {
+    const float* lr_p;           // [M][R], scaled
+    const __nv_bfloat16* lr_b;   // [lr_num][N][R]
+    const int* lr_index;         // nullptr: adapter 0 for every token
+    int lr_num, lr_rank;
+};
+template <bool LR>
+using ParamsFor = std::conditional_t<LR, LrParams, Params>;
 
 // Shared-memory layout for `rows` weight rows per tile (a multiple of 16 when `swap`). Every TMA
 // destination starts on a 128-byte boundary (1024 for the swizzled X and code boxes). Returns
@@ -185,11 +200,44 @@ __device__ __forceinline__ uint32_t dec_b1(uint32_t v, int c) {       // +-1 by 
     return xor_andnot(0x3F803F80u, v << (15 - c), 0x80008000u);
 }
 
-template <int BITS, int GS, int NOCT, bool SWAP>
+// Adapter of token m (-1: none, also for rows past M).
+__device__ __forceinline__ int lr_adapter(const LrParams& p, int m) {
+    if (m >= p.M) return -1;
+    const int a = p.lr_index ? p.lr_index[m] : 0;
+    return a >= 0 && a < p.lr_num ? a : -1;
+}
+__device__ __forceinline__ float lr_dot8(const uint4& w, const float4& u, const float4& v, float s) {
+    s = fmaf(u.x, __uint_as_float(w.x << 16), s);
+    s = fmaf(u.y, __uint_as_float(w.x & 0xFFFF0000u), s);
+    s = fmaf(u.z, __uint_as_float(w.y << 16), s);
+    s = fmaf(u.w, __uint_as_float(w.y & 0xFFFF0000u), s);
+    s = fmaf(v.x, __uint_as_float(w.z << 16), s);
+    s = fmaf(v.y, __uint_as_float(w.z & 0xFFFF0000u), s);
+    s = fmaf(v.z, __uint_as_float(w.w << 16), s);
+    return fmaf(v.w, __uint_as_float(w.w & 0xFFFF0000u), s);
+}
+// The low-rank terms of token m (of adapter a >= 0) in rows n0 and n1.
+__device__ __forceinline__ float2 lr_term(const LrParams& p, int a, int m, int n0, int n1) {
+    const __nv_bfloat16* b = p.lr_b + static_cast<size_t>(a) * p.N * p.lr_rank;
+    const uint4* b0 = reinterpret_cast<const uint4*>(b + static_cast<size_t>(n0) * p.lr_rank);
+    const uint4* b1 = reinterpret_cast<const uint4*>(b + static_cast<size_t>(n1) * p.lr_rank);
+    const float4* q = reinterpret_cast<const float4*>(p.lr_p + static_cast<size_t>(m) * p.lr_rank);
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < p.lr_rank / 8; ++i) {
+        const uint4 w0 = __ldg(b0 + i), w1 = __ldg(b1 + i);
+        const float4 u = q[2 * i], v = q[2 * i + 1];
+        s.x = lr_dot8(w0, u, v, s.x);
+        s.y = lr_dot8(w1, u, v, s.y);
+    }
+    return s;
+}
+
+template <int BITS, int GS, int NOCT, bool SWAP, bool LR>
 __global__ void __launch_bounds__(kThreads, 1)
     lowbit_smallm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_z,
-                         const Params p) {
+                         const ParamsFor<LR> p) {
     using F = Fmt<BITS, GS>;
     static_assert(!SWAP || NOCT % 2 == 0, "weights as the 16-row operand take rows in pairs of octets");
     constexpr int R = 8 * NOCT;                       // weight rows per tile
@@ -241,6 +289,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (ks > 1) cluster_sync_all();   // every CTA of the cluster has started (remote stores target it)
     grid_launch_dependents();
+    // (lr_index and B, like the packed weights, are not written by the kernel just before)
+    if constexpr (LR) {
+        const int n0 = static_cast<int>(blockIdx.x) * R;
+        const int lines = (min(R, p.N - n0) * p.lr_rank * 2 + 127) / 128 + 1;
+        for (int i = static_cast<int>(threadIdx.x) + rank * kThreads; i < p.M * lines; i += kThreads * ks) {
+            const int a = lr_adapter(p, i / lines);
+            const size_t end = (static_cast<size_t>(a) * p.N + min(n0 + R, p.N)) * p.lr_rank;
+            const size_t at = (static_cast<size_t>(a) * p.N + n0) * p.lr_rank + i % lines * 64;
+            if (a >= 0 && at < end) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.lr_b + at));
+        }
+    }
 
     // Ring step `gs` of this CTA: tile blockIdx.x + (gs / nst) * gridDim.x, K step gs % nst.
     // Every CTA of a slice reads the same X (only its weight rows differ). Walking the slice's K
@@ -582,6 +641,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // rows n and n + 8 of unit o, tokens 2q and 2q + 1
                 const int n = n0 + 16 * o + g;
                 const int t0 = 2 * q;
+                if constexpr (LR) {
+                    // (row n + 8 past N: its term is not stored, row n's stands in)
+                    const int n8 = n + 8 < p.N ? n + 8 : n;
+                    const int a0 = n < p.N ? lr_adapter(p, t0) : -1, a1 = n < p.N ? lr_adapter(p, t0 + 1) : -1;
+                    if (a0 >= 0) {
+                        const float2 u = lr_term(p, a0, t0, n, n8);
+                        v.x += u.x;
+                        v.z += u.y;
+                    }
+                    if (a1 >= 0) {
+                        const float2 u = lr_term(p, a1, t0 + 1, n, n8);
+                        v.y += u.x;
+                        v.w += u.y;
+                    }
+                }
                 if (dcheck(o < NUT && n >= 0, p.status)) {
                     const float vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -593,6 +667,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 const int n = n0 + 8 * o + 2 * q;
                 if (n < p.N && dcheck(n >= 0 && n + 1 < p.N && o < NUT, p.status)) {
+                    if constexpr (LR) {
+                        const int a0 = lr_adapter(p, g), a1 = lr_adapter(p, g + 8);
+                        if (a0 >= 0) {
+                            const float2 u = lr_term(p, a0, g, n, n + 1);
+                            v.x += u.x;
+                            v.y += u.y;
+                        }
+                        if (a1 >= 0) {
+                            const float2 u = lr_term(p, a1, g + 8, n, n + 1);
+                            v.z += u.x;
+                            v.w += u.y;
+                        }
+                    }
                     if (g < p.M)
                         *reinterpret_cast<__nv_bfloat162*>(p.Y + static_cast<size_t>(g) * p.N + n) =
                             __floats2bfloat162_rn(v.x, v.y);
@@ -656,41 +743,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Kernel entry for (BITS, GS), `noct` octets per tile (1..16) and the orientation (`swap`:
-// weights as the 16-row operand, even `noct` only), or nullptr. One definition per code width
-// lives in its own translation unit so the instantiations build in parallel.
+// weights as the 16-row operand, even `noct` only), or nullptr; kernel_lr_*: with the low-rank term.
+// One definition per code width and variant lives in its own translation unit so the
+// instantiations build in parallel.
 const void* kernel_b1(int group_size, int noct, bool swap);
 const void* kernel_b2(int group_size, int noct, bool swap);
 const void* kernel_b4(int group_size, int noct, bool swap);
+const void* kernel_lr_b1(int group_size, int noct, bool swap);
+const void* kernel_lr_b2(int group_size, int noct, bool swap);
+const void* kernel_lr_b4(int group_size, int noct, bool swap);
 
 }  // namespace smallm
 }  // namespace lowbit
 
-// Defines kernel_b<BITS>: tables of the sixteen octet counts (and the eight even ones with weights
-// as the 16-row operand) for both group sizes.
-#define LOWBIT_SMALLM_TABLE(BITS)                                                                     \
+// Defines NAME: tables of the sixteen octet counts (and the eight even ones with weights as the
+// 16-row operand) for both group sizes.
+#define LOWBIT_SMALLM_TABLE(NAME, BITS, LR)                                                           \
     namespace lowbit {                                                                                \
     namespace smallm {                                                                                \
     template <int GS, int... Ns>                                                                      \
-    static const void* pick_##BITS(int noct, std::integer_sequence<int, Ns...>) {                     \
+    static const void* pick(int noct, std::integer_sequence<int, Ns...>) {                            \
         static const void* const table[] = {                                                          \
-            reinterpret_cast<const void*>(&lowbit_smallm_kernel<BITS, GS, Ns + 1, false>)...};        \
+            reinterpret_cast<const void*>(&lowbit_smallm_kernel<BITS, GS, Ns + 1, false, LR>)...};    \
         return (noct >= 1 && noct <= static_cast<int>(sizeof...(Ns))) ? table[noct - 1] : nullptr;    \
     }                                                                                                 \
     template <int GS, int... Ns>                                                                      \
-    static const void* pick_swap_##BITS(int noct, std::integer_sequence<int, Ns...>) {                \
+    static const void* pick_swap(int noct, std::integer_sequence<int, Ns...>) {                       \
         static const void* const table[] = {                                                          \
-            reinterpret_cast<const void*>(&lowbit_smallm_kernel<BITS, GS, 2 * (Ns + 1), true>)...};   \
+            reinterpret_cast<const void*>(&lowbit_smallm_kernel<BITS, GS, 2 * (Ns + 1), true, LR>)...}; \
         return (noct >= 2 && noct % 2 == 0 && noct / 2 <= static_cast<int>(sizeof...(Ns)))           \
                    ? table[noct / 2 - 1] : nullptr;                                                   \
     }                                                                                                 \
-    const void* kernel_b##BITS(int group_size, int noct, bool swap) {                                 \
+    const void* NAME(int group_size, int noct, bool swap) {                                           \
         if (swap) {                                                                                   \
-            if (group_size == 64) return pick_swap_##BITS<64>(noct, std::make_integer_sequence<int, kMaxOct / 2>{}); \
-            if (group_size == 128) return pick_swap_##BITS<128>(noct, std::make_integer_sequence<int, kMaxOct / 2>{}); \
+            if (group_size == 64) return pick_swap<64>(noct, std::make_integer_sequence<int, kMaxOct / 2>{}); \
+            if (group_size == 128) return pick_swap<128>(noct, std::make_integer_sequence<int, kMaxOct / 2>{}); \
             return nullptr;                                                                           \
         }                                                                                             \
-        if (group_size == 64) return pick_##BITS<64>(noct, std::make_integer_sequence<int, kMaxOct>{}); \
-        if (group_size == 128) return pick_##BITS<128>(noct, std::make_integer_sequence<int, kMaxOct>{}); \
+        if (group_size == 64) return pick<64>(noct, std::make_integer_sequence<int, kMaxOct>{});      \
+        if (group_size == 128) return pick<128>(noct, std::make_integer_sequence<int, kMaxOct>{});    \
         return nullptr;                                                                               \
     }                                                                                                 \
     }                                                                                                 \

@@ -183,6 +183,26 @@ __device__ __forceinline__ void mma_commit_pair_mc(uint64_t* bar, uint16_t cta_m
         : "memory");
 }
 
+// The same with A in shared memory (in both CTAs' for the pair form, 128 rows each).
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Shared-memory matrix descriptor (tcgen05 format): K-major operand, 128-byte swizzle,
 // 8-row x 128-byte core groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t smem_addr) {
@@ -193,6 +213,21 @@ __device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t smem_addr) {
     d |= static_cast<uint64_t>(1u) << 46;                        // descriptor version   [46,48)
     d |= static_cast<uint64_t>(2u) << 61;                        // layout: SWIZZLE_128B [61,64)
     return d;
+}
+
+// K-major operand whose rows are `row_bytes` = 32, 64 or 128 bytes, swizzled over that width:
+// 8-row core groups 8 * row_bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_k(uint32_t smem_addr, uint32_t row_bytes) {
+    const uint64_t layout = row_bytes == 128 ? 2u : row_bytes == 64 ? 4u : 6u;   // SWIZZLE_128B / 64B / 32B
+    return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1u) << 16 |
+           static_cast<uint64_t>((8 * row_bytes) >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | layout << 61;
+}
+// MN-major operand, 128-byte swizzle: rows of 64 consecutive M (or N) elements, one row per K;
+// 8-row groups along K 1024 bytes apart (stride byte offset), the next 64 elements of M
+// `m_bytes` further on (leading byte offset).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t smem_addr, uint32_t m_bytes) {
+    return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | static_cast<uint64_t>((m_bytes >> 4) & 0x3FFFu) << 16 |
+           static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
 }
 
 // Instruction descriptor for kind::f16 with fp16 A/B, fp32 D, both K-major, shape M x N.
@@ -208,6 +243,7 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
     return idesc_f16_f32(M, N) | (1u << 7) | (1u << 10);   // A and B format: BF16
 }
+constexpr uint32_t kIdescTransposeA = 1u << 15;            // A is MN-major
 
 // ---- cluster rank ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_ctarank() {
