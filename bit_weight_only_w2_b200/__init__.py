@@ -14,7 +14,9 @@ Layouts (see include/lowbit.h): x bf16 [M][K]; packed int32 view of uint32 words
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional, Sequence, Union
 
@@ -329,33 +331,24 @@ def _check_checkpoint(ck: Checkpoint, M: int, K: int, device, name: str = "check
             raise ValueError(f"{name}.{part}: on {t.device}, expected {device}")
 
 
-def checkpoint_store(x: torch.Tensor, out: Optional[Checkpoint] = None) -> Checkpoint:
-    """The 8-bit copy of x (bf16 [M][K], K a multiple of 32)."""
-    _need(x, torch.bfloat16, "x")
-    _need_cuda(("x", x))
-    M, K = x.shape
-    if out is None:
-        out = checkpoint_empty(M, K, x.device)
-    _check_checkpoint(out, M, K, x.device, "out")
-    with torch.cuda.device(x.device):
-        _check(load().lowbit_checkpoint_store(_ptr(x), M, K, _ptr(out.codes), _ptr(out.exps), _stream()),
-               "lowbit_checkpoint_store")
-    return out
+# The entry points below run in a few microseconds on the GPU, so their checks come in two forms:
+# one boolean expression over everything that a correct call satisfies (about 2 us), and, only when it
+# does not hold, the checks that name what is wrong. Both accept the same calls.
+_BF16, _F16, _F32, _I32, _U8 = torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8
+_F8 = torch.float8_e4m3fn
 
 
-def checkpoint_load(ck: Checkpoint, out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """The bf16 values an 8-bit copy stands for."""
-    _need(ck.codes, torch.float8_e4m3fn, "checkpoint.codes")
-    _need_cuda(("checkpoint.codes", ck.codes))
-    M, K = ck.codes.shape
-    _check_checkpoint(ck, M, K, ck.codes.device)
-    if out is None:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=ck.codes.device)
-    _check_like(out, "out", (M, K), torch.bfloat16, ck.codes.device)
-    with torch.cuda.device(out.device):
-        _check(load().lowbit_checkpoint_load(_ptr(ck.codes), _ptr(ck.exps), M, K, _ptr(out), _stream()),
-               "lowbit_checkpoint_load")
-    return out
+def _fits(t, dtype, shape, dev: int) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _raw_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _on_device(dev: int):
+    """The context to launch on device `dev`: nothing to do on the current one."""
+    return contextlib.nullcontext() if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _check_like(t: torch.Tensor, name: str, shape, dtype, device):
@@ -364,6 +357,46 @@ def _check_like(t: torch.Tensor, name: str, shape, dtype, device):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _copy_fits(ck, M: int, K: int, dev: int) -> bool:
+    return K % 32 == 0 and _fits(ck.codes, _F8, (M, K), dev) and _fits(ck.exps, _U8, (M, K // 32), dev)
+
+
+def checkpoint_store(x: torch.Tensor, out: Optional[Checkpoint] = None) -> Checkpoint:
+    """The 8-bit copy of x (bf16 [M][K], K a multiple of 32)."""
+    if not (x.dim() == 2 and x.dtype is _BF16 and x.is_contiguous() and x.is_cuda):
+        _need(x, _BF16, "x")
+        _need_cuda(("x", x))
+    M, K = x.shape
+    dev = x.get_device()
+    if out is None:
+        out = checkpoint_empty(M, K, x.device)
+    elif not _copy_fits(out, M, K, dev):
+        _check_checkpoint(out, M, K, x.device, "out")
+    with _on_device(dev):
+        _check(load().lowbit_checkpoint_store(x.data_ptr(), M, K, out.codes.data_ptr(), out.exps.data_ptr(),
+                                              _raw_stream(dev)), "lowbit_checkpoint_store")
+    return out
+
+
+def checkpoint_load(ck: Checkpoint, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The bf16 values an 8-bit copy stands for."""
+    codes = ck.codes
+    if not (codes.dim() == 2 and codes.is_cuda and _copy_fits(ck, *codes.shape, codes.get_device())):
+        _need(codes, _F8, "checkpoint.codes")
+        _need_cuda(("checkpoint.codes", codes))
+        _check_checkpoint(ck, *codes.shape, codes.device)
+    M, K = codes.shape
+    dev = codes.get_device()
+    if out is None:
+        out = torch.empty((M, K), dtype=_BF16, device=codes.device)
+    elif not _fits(out, _BF16, (M, K), dev):
+        _check_like(out, "out", (M, K), _BF16, codes.device)
+    with _on_device(dev):
+        _check(load().lowbit_checkpoint_load(codes.data_ptr(), ck.exps.data_ptr(), M, K, out.data_ptr(),
+                                             _raw_stream(dev)), "lowbit_checkpoint_load")
+    return out
 
 
 def transposed_words(N: int, K: int, bits: int) -> int:
@@ -385,23 +418,33 @@ def transpose_packed(packed: torch.Tensor, K: int, bits: int) -> torch.Tensor:
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def adapter_workspace_size(M: int, N: int, K: int, num: int, rank: int) -> int:
+    """Bytes of workspace of adapter_gemm, adapter_backward and (num = rank = 0) gemm_dx."""
     return int(load().lowbit_adapter_workspace_size(M, N, K, num, rank))
 
 
-def _own_workspace(ws: Optional[torch.Tensor], device, M, N, K, num, rank) -> torch.Tensor:
+def _own_workspace(ws: Optional[torch.Tensor], like: torch.Tensor, M, N, K, num, rank):
     # allocated per call by default: the caching allocator ties it to the current stream (and to the
     # pool of a graph under capture), so calls on several streams or in several graphs never share it
-    need = adapter_workspace_size(M, N, K, num, rank)
     if ws is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    _need(ws, torch.uint8, "ws", ndim=1)
-    if ws.device != device:
-        raise ValueError(f"ws: on {ws.device}, expected {device}")
-    return ws
+        need = adapter_workspace_size(M, N, K, num, rank)
+        return like.new_empty(need // 2 + 1), need
+    _need(ws, _U8, "ws", ndim=1)
+    if ws.device != like.device:
+        raise ValueError(f"ws: on {ws.device}, expected {like.device}")
+    return ws, ws.numel()
 
 
-def _check_adapters(a, b, scaling, index, M, N, K, device) -> Adapters:
+def _adapters_fit(a, b, scaling, index, M: int, N: int, K: int, dev: int) -> bool:
+    if a.dim() != 3:
+        return False
+    L, R, _ = a.shape
+    return (_fits(a, _BF16, (L, R, K), dev) and _fits(b, _BF16, (L, N, R), dev) and _fits(scaling, _F32, (L,), dev) and
+            (index is None or _fits(index, _I32, (M,), dev)))
+
+
+def _check_adapters(a, b, scaling, index, M, N, K, device) -> None:
     _need(a, torch.bfloat16, "a", ndim=3)
     _need(b, torch.bfloat16, "b", ndim=3)
     L, R = a.shape[0], a.shape[1]
@@ -413,7 +456,21 @@ def _check_adapters(a, b, scaling, index, M, N, K, device) -> Adapters:
     for name, t in (("a", a), ("b", b)):
         if t.device != device:
             raise ValueError(f"{name}: on {t.device}, expected {device}")
-    return Adapters(L, R, _ptr(a), _ptr(b), _ptr(scaling), _ptr(index))
+
+
+def _linear_fits(x, words, scales, zeros, bits: int, group_size: int, transposed: bool) -> bool:
+    """x [M][K] with W's words, or dy [M][N] with W^T's."""
+    if not (x.dim() == 2 and scales.dim() == 2 and words.dim() == 2 and x.is_cuda and bits in (1, 2, 4) and group_size > 0):
+        return False
+    dev = x.get_device()
+    M, red = x.shape
+    N = scales.shape[1]
+    K = words.shape[0] if transposed else red
+    wide = (K, (N + 127) // 128 * 128 * bits // 32) if transposed else (N, K * bits // 32)
+    groups = (K // group_size, N)
+    return (K % group_size == 0 and x.dtype is _BF16 and x.is_contiguous() and _fits(words, _I32, wide, dev) and
+            _fits(scales, _F16, groups, dev) and (zeros is None or _fits(zeros, _F16, groups, dev)) and
+            (not transposed or red == N))
 
 
 def adapter_gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor],
@@ -426,20 +483,29 @@ def adapter_gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, ze
     a bf16 [L][R][K], b bf16 [L][N][R], scaling fp32 [L], index int32 [M] (values outside 0..L-1: no
     adapter; None: adapter 0 for every token). For training, pass buffers that the backward reads:
     `p` bf16 [M][R] and, to keep X in 8 bits, `checkpoint` (checkpoint_empty(M, K, device))."""
-    M, N, K = _check_gemm_args(x, packed, scales, zeros, out, bits, group_size)
-    ad = _check_adapters(a, b, scaling, index, M, N, K, x.device)
-    if p is not None:
-        _check_like(p, "p", (M, ad.rank), torch.bfloat16, x.device)
-    if checkpoint is not None:
+    if not _linear_fits(x, packed, scales, zeros, bits, group_size, False):
+        _check_gemm_args(x, packed, scales, zeros, out, bits, group_size)
+    M, K = x.shape
+    N = scales.shape[1]
+    dev = x.get_device()
+    if not _adapters_fit(a, b, scaling, index, M, N, K, dev):
+        _check_adapters(a, b, scaling, index, M, N, K, x.device)
+    L, R, _ = a.shape
+    if out is None:
+        out = x.new_empty((M, N))
+    elif not _fits(out, _BF16, (M, N), dev):
+        _check_like(out, "out", (M, N), _BF16, x.device)
+    if p is not None and not _fits(p, _BF16, (M, R), dev):
+        _check_like(p, "p", (M, R), _BF16, x.device)
+    if checkpoint is not None and not _copy_fits(checkpoint, M, K, dev):
         _check_checkpoint(checkpoint, M, K, x.device)
-    with torch.cuda.device(x.device):
-        if out is None:
-            out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-        ws = _own_workspace(ws, x.device, M, N, K, ad.num, ad.rank)
-        codes, exps = checkpoint if checkpoint is not None else (None, None)
-        _check(load().lowbit_adapter_gemm(M, N, K, bits, group_size, _ptr(x), _ptr(packed), _ptr(scales), _ptr(zeros),
-                                          ctypes.byref(ad), _ptr(out), _ptr(p), _ptr(codes), _ptr(exps), _ptr(ws),
-                                          ws.numel(), _stream()), "lowbit_adapter_gemm")
+    ad = Adapters(L, R, a.data_ptr(), b.data_ptr(), scaling.data_ptr(), _ptr(index))
+    codes, exps = checkpoint if checkpoint is not None else (None, None)
+    with _on_device(dev):
+        ws, ws_bytes = _own_workspace(ws, x, M, N, K, L, R)
+        _check(load().lowbit_adapter_gemm(M, N, K, bits, group_size, x.data_ptr(), packed.data_ptr(), scales.data_ptr(),
+                                          _ptr(zeros), ctypes.byref(ad), out.data_ptr(), _ptr(p), _ptr(codes), _ptr(exps),
+                                          ws.data_ptr(), ws_bytes, _raw_stream(dev)), "lowbit_adapter_gemm")
     return out
 
 
@@ -468,15 +534,20 @@ def _check_grad_args(dy, packed_t, scales, zeros, bits: int, group_size: int):
 def gemm_dx(dy: torch.Tensor, packed_t: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor], bits: int,
             group_size: int, out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dX = dY W, the input gradient of gemm (dy bf16 [M][N], packed_t from transpose_packed)."""
-    M, N, K = _check_grad_args(dy, packed_t, scales, zeros, bits, group_size)
-    if out is not None:
-        _check_like(out, "out", (M, K), torch.bfloat16, dy.device)
-    with torch.cuda.device(dy.device):
-        if out is None:
-            out = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
-        ws = _own_workspace(ws, dy.device, M, N, K, 0, 0)
-        _check(load().lowbit_gemm_dx(M, N, K, bits, group_size, _ptr(dy), _ptr(packed_t), _ptr(scales), _ptr(zeros),
-                                     _ptr(out), _ptr(ws), ws.numel(), _stream()), "lowbit_gemm_dx")
+    if not _linear_fits(dy, packed_t, scales, zeros, bits, group_size, True):
+        _check_grad_args(dy, packed_t, scales, zeros, bits, group_size)
+    M, N = dy.shape
+    K = packed_t.shape[0]
+    dev = dy.get_device()
+    if out is None:
+        out = dy.new_empty((M, K))
+    elif not _fits(out, _BF16, (M, K), dev):
+        _check_like(out, "out", (M, K), _BF16, dy.device)
+    with _on_device(dev):
+        ws, ws_bytes = _own_workspace(ws, dy, M, N, K, 0, 0)
+        _check(load().lowbit_gemm_dx(M, N, K, bits, group_size, dy.data_ptr(), packed_t.data_ptr(), scales.data_ptr(),
+                                     _ptr(zeros), out.data_ptr(), ws.data_ptr(), ws_bytes, _raw_stream(dev)),
+               "lowbit_gemm_dx")
     return out
 
 
@@ -489,32 +560,42 @@ def adapter_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint], p: to
 
     x is the forward's input, or the Checkpoint it filled; p what it wrote. need_dx=False skips
     dx (a first layer) and returns None in its place."""
-    M, N, K = _check_grad_args(dy, packed_t, scales, zeros, bits, group_size)
-    dev = dy.device
-    ad = _check_adapters(a, b, scaling, index, M, N, K, dev)
-    _check_like(p, "p", (M, ad.rank), torch.bfloat16, dev)
+    if not _linear_fits(dy, packed_t, scales, zeros, bits, group_size, True):
+        _check_grad_args(dy, packed_t, scales, zeros, bits, group_size)
+    M, N = dy.shape
+    K = packed_t.shape[0]
+    dev = dy.get_device()
+    if not _adapters_fit(a, b, scaling, index, M, N, K, dev):
+        _check_adapters(a, b, scaling, index, M, N, K, dy.device)
+    L, R, _ = a.shape
+    if not _fits(p, _BF16, (M, R), dev):
+        _check_like(p, "p", (M, R), _BF16, dy.device)
     if isinstance(x, Checkpoint):
-        _check_checkpoint(x, M, K, dev, "x")
-        xs = (None, _ptr(x.codes), _ptr(x.exps))
+        if not _copy_fits(x, M, K, dev):
+            _check_checkpoint(x, M, K, dy.device, "x")
+        xs = (None, x.codes.data_ptr(), x.exps.data_ptr())
     else:
-        _check_like(x, "x", (M, K), torch.bfloat16, dev)
-        xs = (_ptr(x), None, None)
-    for name, t, shape in (("dx", dx, (M, K)), ("da", da, a.shape), ("db", db, b.shape)):
-        if t is not None:
-            _check_like(t, name, shape, torch.bfloat16, dev)
+        if not _fits(x, _BF16, (M, K), dev):
+            _check_like(x, "x", (M, K), _BF16, dy.device)
+        xs = (x.data_ptr(), None, None)
+    for name, t, shape in (("dx", dx, (M, K)), ("da", da, (L, R, K)), ("db", db, (L, N, R))):
+        if t is not None and not _fits(t, _BF16, shape, dev):
+            _check_like(t, name, shape, _BF16, dy.device)
     if dx is not None and not need_dx:
         raise ValueError("dx: a buffer was passed, but need_dx is False")
-    with torch.cuda.device(dev):
-        if need_dx and dx is None:
-            dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-        if da is None:
-            da = torch.empty_like(a)
-        if db is None:
-            db = torch.empty_like(b)
-        ws = _own_workspace(ws, dev, M, N, K, ad.num, ad.rank)
-        _check(load().lowbit_adapter_backward(M, N, K, bits, group_size, _ptr(dy), _ptr(packed_t), _ptr(scales),
-                                              _ptr(zeros), ctypes.byref(ad), *xs, _ptr(p), _ptr(dx), _ptr(da),
-                                              _ptr(db), _ptr(ws), ws.numel(), _stream()), "lowbit_adapter_backward")
+    if need_dx and dx is None:
+        dx = dy.new_empty((M, K))
+    if da is None:
+        da = dy.new_empty((L, R, K))
+    if db is None:
+        db = dy.new_empty((L, N, R))
+    ad = Adapters(L, R, a.data_ptr(), b.data_ptr(), scaling.data_ptr(), _ptr(index))
+    with _on_device(dev):
+        ws, ws_bytes = _own_workspace(ws, dy, M, N, K, L, R)
+        _check(load().lowbit_adapter_backward(M, N, K, bits, group_size, dy.data_ptr(), packed_t.data_ptr(),
+                                              scales.data_ptr(), _ptr(zeros), ctypes.byref(ad), *xs, p.data_ptr(),
+                                              _ptr(dx), da.data_ptr(), db.data_ptr(), ws.data_ptr(), ws_bytes,
+                                              _raw_stream(dev)), "lowbit_adapter_backward")
     return dx, da, db
 
 

@@ -20,6 +20,7 @@
 #include "adapter_internal.h"
 #include "checkpoint.cuh"
 #include "sm100_ptx.cuh"
+#include "tcgen05_ptx.cuh"
 
 namespace lowbit {
 namespace {
@@ -29,38 +30,11 @@ constexpr int kSmsAssumed = 148;   // the workspace's size may not depend on the
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ uint4 ldg_nc_v4(const uint4* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // ---------------------------------------------------------------------------------------------
 // Plan: the tokens of each adapter, and the slots of each token tile
 // ---------------------------------------------------------------------------------------------
@@ -170,118 +144,218 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // ---------------------------------------------------------------------------------------------
+// Gathered products on tcgen05: the common part of shrink and wgrad
+// ---------------------------------------------------------------------------------------------
+// Both multiply 128 rows by Rp <= 128 columns over a long reduction whose rows are gathered (the
+// tokens of one adapter), and read their wide operand once, so they are bound by that stream. Eight
+// producer warps copy a stage of 64 reduction elements with 16-byte cp.async into the swizzled
+// layouts the MMA reads; a thread makes its own finished copies visible to the tensor cores
+// (proxy fence) before its warp arrives on the stage's barrier. One thread issues the MMAs
+// (bf16 x bf16, fp32 in tensor memory) and frees stages by commits. Warp-level MMAs with ldmatrix
+// were bound by shared-memory reads instead: every warp reads all of the narrow operand again (90 us
+// for the two gradients of 4173 tokens x 9216 at rank 64, floor 18).
+constexpr int kGatherWarps = 8;                              // producers; one more warp issues MMAs
+constexpr int kGatherThreads = 32 * (kGatherWarps + 1);
+constexpr int kWideBytes = 128 * 128;                        // 128 x 64 bf16
+__host__ __device__ constexpr int gather_stage(int rp) { return kWideBytes + rp * 128; }
+
+struct GatherPipe {
+    uint64_t* full;
+    uint64_t* empty;
+    uint64_t* done;
+    volatile int* abort_flag;
+    unsigned* status;
+};
+
+// Producer side of stage `step` being copied: wait for its slot; false if the wait gave up.
+template <int S>
+__device__ __forceinline__ bool gather_wait_slot(const GatherPipe& g, int step) {
+    return __all_sync(0xffffffffu, mbar_wait(&g.empty[step % S], ((step / S) & 1u) ^ 1u, g.abort_flag, g.status));
+}
+// Stage `step`'s copies of this thread are complete (or its stores made): hand it to the MMAs.
+template <int S>
+__device__ __forceinline__ void gather_publish(const GatherPipe& g, int step) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&g.full[step % S]);
+}
+// MMA side: `steps` stages of four K = 16 products each; `issue(stage address, k16, accumulate)`.
+// Returns once they have completed (or a wait gave up).
+template <int S, class Issue>
+__device__ __forceinline__ void gather_mma(const GatherPipe& g, uint32_t s0, int stage_bytes, int steps, Issue issue) {
+    bool issued = false;
+    for (int step = 0; step < steps; ++step) {
+        if (!mbar_wait(&g.full[step % S], (step / S) & 1u, g.abort_flag, g.status)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k16 = 0; k16 < 4; ++k16) issue(s0 + (step % S) * stage_bytes, k16, step > 0 || k16 > 0 ? 1u : 0u);
+        mma_commit(&g.empty[step % S]);
+        issued = true;
+    }
+    if (issued) {   // (also after a wait that gave up: tensor memory may not be freed under an MMA)
+        mma_commit(g.done);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(g.done, 0)) {
+            if (clock64() - t0 > kWaitLimitCycles) {
+                atomicOr(g.status, kDevErrTimeout);
+                *g.abort_flag = 1;
+                break;
+            }
+        }
+    }
+}
+
+// 16-byte chunk `ch` of row `row` in a tile whose rows are `rb` bytes, swizzled over that width.
+__device__ __forceinline__ uint32_t swizzled(int row, int ch, int rb) {
+    const int x = rb == 128 ? row & 7 : rb == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
+    return static_cast<uint32_t>(row * rb + ((ch ^ x) << 4));
+}
+// The narrow operand as MN-major [64 reduction rows][Rp]: rows of up to 128 bytes; Rp = 128 is two
+// such tiles of 64 columns, 8 KB apart. Chunk `ch` of the Rp / 8 of a row.
+template <int RP>
+__device__ __forceinline__ uint32_t narrow_mn_offset(int row, int ch) {
+    constexpr int rb = RP < 64 ? RP * 2 : 128;
+    return static_cast<uint32_t>((ch >> 3) * 8192) + swizzled(row, ch & 7, rb);
+}
+template <int RP>
+__device__ __forceinline__ uint64_t narrow_mn_desc(uint32_t tile, int k16) {
+    constexpr int rb = RP < 64 ? RP * 2 : 128;
+    return smem_desc_mn(tile + k16 * 16 * rb, rb, 8192);
+}
+
+// ---------------------------------------------------------------------------------------------
 // Shrink: partial[s][m][0..Rp) = in[m][slice s] * side_a[slice s]^T for the tokens of each block
 // ---------------------------------------------------------------------------------------------
-// R is at most 128, so the product reads each input row once and is bound by that stream (and,
-// for few tokens per adapter, by the adapters' rows): warp-level MMAs on tiles that cp.async
-// gathers into shared memory keep up with it, and tcgen05's 128-row tiles would be mostly padding.
-// A block is up to 128 tokens of one adapter; the reduction is cut into slices over gridDim.y so
-// that a few blocks fill the GPU, and the slices' fp32 partials are added in order by the copy
-// pass that follows. KMAJOR: the adapter's side is [R][red] (A); otherwise [red][R] (B).
-constexpr int kShrinkThreads = 256;
-constexpr int kShrinkStages = 4;
-__host__ __device__ constexpr int shrink_smem(int rp) { return kShrinkStages * (kShrinkTokens * 128 + rp * 128); }
+// A block is up to 128 tokens of one adapter (the MMA's 128 rows); the reduction is cut into
+// slices over gridDim.y so that a few blocks fill the GPU, and the slices' fp32 partials are added
+// in order by the copy pass that follows. KMAJOR: the adapter's side is [R][red] (A); otherwise
+// [red][R] (B).
+template <int RP>
+constexpr int kShrinkStages = RP == 128 ? 3 : 4;
+template <int RP>
+constexpr int kShrinkSmem = 1024 + kShrinkStages<RP> * gather_stage(RP) + 1024;
 
 template <int RP, bool KMAJOR>
-__global__ void __launch_bounds__(kShrinkThreads)
+__global__ void __launch_bounds__(kGatherThreads, 2)
     shrink_kernel(const __nv_bfloat16* __restrict__ in, const __nv_bfloat16* __restrict__ side, int M, int red, int R,
                   int kslice, const int* __restrict__ perm, const int4* __restrict__ blocks,
-                  float* __restrict__ partial) {
-    extern __shared__ __align__(1024) uint8_t smem[];
+                  float* __restrict__ partial, unsigned* __restrict__ status) {
+    constexpr int S = kShrinkStages<RP>, kStage = gather_stage(RP);
+    constexpr uint32_t kCols = RP < 32 ? 32 : RP;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t bars[2 * S + 1];
+    __shared__ uint32_t tmem_holder;
+    __shared__ int abort_word;
     __shared__ int tok[kShrinkTokens];
-    constexpr int kXBytes = kShrinkTokens * 128, kStage = kXBytes + RP * 128;
+    const GatherPipe g = {bars, bars + S, bars + 2 * S, &abort_word, status};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dependency_wait();
     grid_launch_dependents();
     const int4 blk = blocks[blockIdx.x];
     const int count = blk.z;
     if (count <= 0) return;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid < kShrinkTokens) tok[tid] = perm[blk.y + min(tid, count - 1)];
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&bars[i], kGatherWarps);
+            mbar_init(&bars[S + i], 1);
+        }
+        mbar_init(g.done, 1);
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    if (warp == kGatherWarps) {
+        tmem_alloc(&tmem_holder, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_holder, s0 = smem_u32(smem);
     const int k_begin = blockIdx.y * kslice, k_end = min(red, k_begin + kslice);
-    const int steps = k_end > k_begin ? (k_end - k_begin + 63) / 64 : 0;
+    const int steps = (k_end - k_begin + 63) / 64;
     const __nv_bfloat16* wside = side + static_cast<size_t>(blk.x) * R * red;
-    const uint32_t s0 = smem_u32(smem);
-    auto load = [&](int step) {
-        const uint32_t st = s0 + (step % kShrinkStages) * kStage;
-        const int k0 = k_begin + step * 64;
+    if (warp < kGatherWarps) {
+        // this thread's copies of a stage: chunk tid % 8 of token rows tid / 8 + 32 i, and its share of
+        // the adapter's side
+        const int ch = tid & 7, row0 = tid >> 3;
+        const __nv_bfloat16* xrow[4];
 #pragma unroll
-        for (int i = 0; i < kShrinkTokens * 8 / kShrinkThreads; ++i) {
-            const int id = tid + i * kShrinkThreads, row = id >> 3, ch = id & 7;
-            const int k = k0 + ch * 8;
-            const bool ok = row < count && k < k_end;
-            cp_async16(st + row * 128 + ((ch ^ (row & 7)) << 4),
-                       in + (ok ? static_cast<size_t>(tok[row]) * red + k : 0), ok);
-        }
-        const uint32_t ws = st + kXBytes;
+        for (int i = 0; i < 4; ++i) xrow[i] = in + static_cast<size_t>(tok[row0 + 32 * i]) * red + ch * 8;
+        auto load = [&](int step) {
+            const uint32_t st = s0 + (step % S) * kStage;
+            const int k0 = k_begin + step * 64;
+            const bool k_ok = k0 + ch * 8 < k_end;
 #pragma unroll
-        for (int i = 0; i < (RP * 8 + kShrinkThreads - 1) / kShrinkThreads; ++i) {
-            const int id = tid + i * kShrinkThreads;
-            if (RP * 8 < kShrinkThreads && id >= RP * 8) break;
-            if (KMAJOR) {
-                const int row = id >> 3, ch = id & 7;
-                const int k = k0 + ch * 8;
-                const bool ok = row < R && k < k_end;
-                cp_async16(ws + row * 128 + ((ch ^ (row & 7)) << 4), wside + (ok ? static_cast<size_t>(row) * red + k : 0),
-                           ok);
-            } else {
-                constexpr int kCh = RP / 8;
-                const int kr = id / kCh, ch = id % kCh;
-                const bool ok = ch * 8 < R && k0 + kr < k_end;
-                cp_async16(ws + kr * RP * 2 + ((ch ^ (kr & (kCh < 8 ? kCh - 1 : 7))) << 4),
-                           wside + (ok ? static_cast<size_t>(k0 + kr) * R + ch * 8 : 0), ok);
+            for (int i = 0; i < 4; ++i) {
+                const int row = row0 + 32 * i;
+                const bool ok = row < count && k_ok;
+                cp_async16(st + swizzled(row, ch, 128), ok ? xrow[i] + k0 : in, ok);
             }
-        }
-    };
-    float acc[RP / 8][4];
+            const uint32_t ws = st + kWideBytes;
 #pragma unroll
-    for (int i = 0; i < RP / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    const bool active = warp * 16 < count;
-#pragma unroll
-    for (int i = 0; i < kShrinkStages - 1; ++i) {
-        if (i < steps) load(i);
-        cp_async_commit();
-    }
-    for (int step = 0; step < steps; ++step) {
-        cp_async_wait<kShrinkStages - 2>();
-        __syncthreads();
-        if (step + kShrinkStages - 1 < steps) load(step + kShrinkStages - 1);
-        cp_async_commit();
-        if (!active) continue;
-        const uint32_t xs = s0 + (step % kShrinkStages) * kStage, ws = xs + kXBytes;
-#pragma unroll
-        for (int k16 = 0; k16 < 4; ++k16) {
-            uint32_t a[4];
-            const int xr = warp * 16 + (lane & 15), xc = k16 * 2 + (lane >> 4);
-            ldsm_x4(xs + xr * 128 + ((xc ^ (xr & 7)) << 4), a);
-#pragma unroll
-            for (int rt = 0; rt < RP / 16; ++rt) {
-                uint32_t b[4];
+            for (int i = 0; i < (RP * 8 + 255) / 256; ++i) {
+                const int id = tid + i * 256;
+                if (RP * 8 < 256 && id >= RP * 8) break;
                 if (KMAJOR) {
-                    const int r = rt * 16 + (lane & 7) + ((lane >> 4) << 3), ch = k16 * 2 + ((lane >> 3) & 1);
-                    ldsm_x4(ws + r * 128 + ((ch ^ (r & 7)) << 4), b);
+                    const int row = id >> 3, k = k0 + (id & 7) * 8;
+                    const bool ok = row < R && k < k_end;
+                    cp_async16(ws + swizzled(row, id & 7, 128), wside + (ok ? static_cast<size_t>(row) * red + k : 0), ok);
                 } else {
-                    constexpr int kCh = RP / 8;
-                    const int kr = k16 * 16 + (lane & 15), ch = rt * 2 + (lane >> 4);
-                    ldsm_x4_trans(ws + kr * RP * 2 + ((ch ^ (kr & (kCh < 8 ? kCh - 1 : 7))) << 4), b);
+                    const int row = id / (RP / 8), c = id % (RP / 8);
+                    const bool ok = c * 8 < R && k0 + row < k_end;
+                    cp_async16(ws + narrow_mn_offset<RP>(row, c),
+                               wside + (ok ? static_cast<size_t>(k0 + row) * R + c * 8 : 0), ok);
                 }
-                mma_16816(acc[2 * rt], a, b[0], b[1]);
-                mma_16816(acc[2 * rt + 1], a, b[2], b[3]);
+            }
+        };
+        bool ok = true;
+        int published = 0;
+        for (int step = 0; step < steps; ++step) {
+            if (!(ok = gather_wait_slot<S>(g, step))) break;
+            load(step);
+            cp_async_commit();
+            if (step >= S - 2) {
+                cp_async_wait<S - 2>();
+                gather_publish<S>(g, published++);
+            }
+        }
+        cp_async_wait<0>();
+        if (ok)
+            while (published < steps) gather_publish<S>(g, published++);
+    } else if (lane == 0) {
+        constexpr uint32_t idesc = idesc_bf16_f32(128, RP) | (KMAJOR ? 0u : kIdescTransposeB);
+        gather_mma<S>(g, s0, kStage, steps, [&](uint32_t st, int k16, uint32_t acc) {
+            const uint32_t ws = st + kWideBytes;
+            mma_f16_ss(tmem, smem_desc_k_sw128(st + k16 * 32),
+                       KMAJOR ? smem_desc_k_sw128(ws + k16 * 32) : narrow_mn_desc<RP>(ws, k16), idesc, acc);
+        });
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp < 4 && !*g.abort_flag) {   // warp w reads tensor-memory lanes 32 w .. 32 w + 31: its tokens
+        const int row = warp * 32 + lane;
+        float* dst = partial + (static_cast<size_t>(blockIdx.y) * M + tok[row]) * RP;
+#pragma unroll
+        for (int c = 0; c < RP; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+            tmem_wait_ld();
+            if (row < count) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
         }
     }
-    if (!active) return;
-    float* out = partial + static_cast<size_t>(blockIdx.y) * M * RP;
-    const int g = lane >> 2, q = lane & 3;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int row = warp * 16 + g + 8 * half;
-        if (row < count) {
-            float* dst = out + static_cast<size_t>(tok[row]) * RP + 2 * q;
-#pragma unroll
-            for (int i = 0; i < RP / 8; ++i)
-                *reinterpret_cast<float2*>(dst + i * 8) = make_float2(acc[i][2 * half], acc[i][2 * half + 1]);
-        }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kGatherWarps) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
     }
 }
 
@@ -486,12 +560,10 @@ __global__ void __launch_bounds__(kConvThreads, 4)
 // ---------------------------------------------------------------------------------------------
 // Adapter gradients: dA_a[r][k] = sum dp[m][r] x[m][k], dB_a[n][r] = sum dy[m][n] p[m][r]
 // ---------------------------------------------------------------------------------------------
-// Both are the same product G^T P over an adapter's tokens, G = x or dy. It reads G once, so it is
-// bound by that stream at small ranks; warp-level MMAs take both operands transposed out of
-// shared memory (ldmatrix.trans), which lets the token rows be gathered as they lie. A CTA owns 128
-// columns of G and all R columns of P; the tokens are cut over the CTAs of a cluster, whose
-// fp32 tiles are added in rank order through distributed shared memory. x may be the 8-bit copy:
-// its codes are widened to bf16 (exactly) on the way into the MMA's tile.
+// Both are the same product G^T P over an adapter's tokens, G = x or dy: A = G^T (128 columns of G,
+// MN-major), B = P (MN-major), reduction over the tokens in stages of 64. The tokens are cut over the
+// CTAs of a cluster, whose fp32 tiles are added in rank order through distributed shared memory. x
+// may be the 8-bit copy: a thread widens the codes that it copied itself into the MMA's tile (exactly).
 struct WgradPart {
     const void* G;             // bf16 [M][C], or the 8-bit codes
     const uint8_t* exps;       // the 8-bit copy's exponents, nullptr for bf16
@@ -505,30 +577,52 @@ struct WgradArgs {
     int R;
     const int* perm;
     const int* seg;
+    unsigned* status;
 };
-constexpr int kWgradThreads = 256;
 constexpr int kWgradStages = 3;
-constexpr int kWgradG = 64 * 256;                 // 64 tokens x 128 columns, bf16
-__host__ __device__ constexpr int wgrad_stage(int rp) { return kWgradG + 64 * rp * 2; }
-__host__ __device__ constexpr int wgrad_smem(int rp) { return kWgradStages * wgrad_stage(rp) + kWgradG; }
+constexpr int kRawBytes = 64 * 128;               // 64 tokens x 128 codes
+template <int RP>
+constexpr int kWgradSmem = 1024 + kWgradStages * (gather_stage(RP) + kRawBytes);
 
-// Token ids of a step, ring of kTokRing steps: read from memory a step before the copies that need
-// them, so that no copy waits for its row's address.
-constexpr int kTokRing = 4;
-
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
 template <int RP>
-__global__ void __launch_bounds__(kWgradThreads) wgrad_kernel(const WgradArgs w) {
-    extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr int kStage = wgrad_stage(RP);
-    constexpr int kCh = RP / 8;
+__global__ void __launch_bounds__(kGatherThreads, RP == 128 ? 1 : 2) wgrad_kernel(const WgradArgs w) {
+    constexpr int S = kWgradStages, kStage = gather_stage(RP);
+    constexpr uint32_t kCols = RP < 32 ? 32 : RP;
     constexpr int kAccPitch = RP + 4;
-    static_assert(128 * kAccPitch * 4 <= kWgradStages * kStage, "fp32 tile");
+    static_assert(128 * kAccPitch * 4 <= S * (kStage + kRawBytes), "fp32 tile");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t bars[2 * S + 1];
+    __shared__ uint32_t tmem_holder;
+    __shared__ int abort_word;
+    const GatherPipe g = {bars, bars + S, bars + 2 * S, &abort_word, w.status};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&bars[i], kGatherWarps);
+            mbar_init(&bars[S + i], 1);
+        }
+        mbar_init(g.done, 1);
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    if (warp == kGatherWarps) {
+        tmem_alloc(&tmem_holder, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_holder, s0 = smem_u32(smem);
     grid_dependency_wait();
     grid_launch_dependents();
     const bool first = blockIdx.y < static_cast<unsigned>(w.part[0].tiles);
@@ -540,155 +634,177 @@ __global__ void __launch_bounds__(kWgradThreads) wgrad_kernel(const WgradArgs w)
     const int t_begin = min(count, rank * per), t_end = min(count, t_begin + per);
     const int steps = (t_end - t_begin + 63) / 64;
     const int* perm = w.perm + seg0;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    __shared__ int tok[kTokRing][64];
-    auto token_of = [&](int step, int i) {   // rows past the end: token 0 of the range, not read
-        const int t = t_begin + step * 64 + i;
-        return t < t_end ? perm[t] : 0;
-    };
-    const bool q8 = part.exps != nullptr;
-    const uint32_t s0 = smem_u32(smem);
-    const uint32_t wide = s0 + kWgradStages * kStage;     // the widened tile of an 8-bit stage
-    auto load = [&](int step) {
-        const uint32_t st = s0 + (step % kWgradStages) * kStage;
-        const int t0 = t_begin + step * 64;
-        const int* ids = tok[step % kTokRing];
-        if (!q8) {
-            const __nv_bfloat16* G = static_cast<const __nv_bfloat16*>(part.G);
-#pragma unroll
-            for (int i = 0; i < 64 * 16 / kWgradThreads; ++i) {
-                const int id = tid + i * kWgradThreads, row = id >> 4, ch = id & 15;
-                const bool ok = t0 + row < t_end && c0 + ch * 8 < part.C;
-                const size_t src = ok ? static_cast<size_t>(ids[row]) * part.C + c0 + ch * 8 : 0;
-                cp_async16(st + row * 256 + ((ch ^ (row & 7)) << 4), G + src, ok);
-            }
-        } else {
-            const uint8_t* G = static_cast<const uint8_t*>(part.G);
-#pragma unroll
-            for (int i = 0; i < 64 * 8 / kWgradThreads; ++i) {
-                const int id = tid + i * kWgradThreads, row = id >> 3, ch = id & 7;
-                const bool ok = t0 + row < t_end && c0 + ch * 16 < part.C;
-                const size_t src = ok ? static_cast<size_t>(ids[row]) * part.C + c0 + ch * 16 : 0;
-                cp_async16(st + row * 128 + ((ch ^ (row & 7)) << 4), G + src, ok);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < (64 * kCh + kWgradThreads - 1) / kWgradThreads; ++i) {
-            const int id = tid + i * kWgradThreads, row = id / kCh, ch = id % kCh;
-            if (row < 64) {
-                const bool ok = t0 + row < t_end && ch * 8 < w.R;
-                const size_t src = ok ? static_cast<size_t>(ids[row]) * w.R + ch * 8 : 0;
-                cp_async16(st + kWgradG + row * RP * 2 + ((ch ^ (row & (kCh < 8 ? kCh - 1 : 7))) << 4), part.P + src, ok);
-            }
-        }
-    };
-    // 8-bit x: each warp widens its own 16 columns of a stage, lane -> token rows lane and lane + 32.
-    // The exponents of the rows' block come from memory a step ahead.
-    const int blk = c0 / 32 + warp / 2;
-    auto exponent_of = [&](int step, int i) -> uint32_t {
-        const int row = lane + 32 * i;
-        if (t_begin + step * 64 + row >= t_end || c0 + warp * 16 >= part.C) return 0;
-        return part.exps[static_cast<size_t>(tok[step % kTokRing][row]) * (part.C / 32) + blk];
-    };
-    auto widen = [&](int step, const uint32_t (&ex)[2]) {
-        const uint8_t* st = smem + (step % kWgradStages) * kStage;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = lane + 32 * i;
-            const uint4 c = *reinterpret_cast<const uint4*>(st + row * 128 + ((warp ^ (row & 7)) << 4));
-            uint8_t* dst = smem + kWgradStages * kStage + row * 256;
-            *reinterpret_cast<uint4*>(dst + (((2 * warp) ^ (row & 7)) << 4)) = checkpoint_decode8(make_uint2(c.x, c.y), ex[i]);
-            *reinterpret_cast<uint4*>(dst + (((2 * warp + 1) ^ (row & 7)) << 4)) =
-                checkpoint_decode8(make_uint2(c.z, c.w), ex[i]);
-        }
-    };
-    float acc[RP / 8][4];
-#pragma unroll
-    for (int i = 0; i < RP / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    if (tid < 64 * kWgradStages) tok[tid >> 6][tid & 63] = token_of(tid >> 6, tid & 63);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kWgradStages - 1; ++i) {
-        if (i < steps) load(i);
-        cp_async_commit();
-    }
-    uint32_t ex[2] = {0, 0};
-    if (q8) {
-        ex[0] = exponent_of(0, 0);
-        ex[1] = exponent_of(0, 1);
-    }
-    for (int step = 0; step < steps; ++step) {
-        cp_async_wait<kWgradStages - 2>();
-        __syncthreads();
-        if (step + kWgradStages - 1 < steps) load(step + kWgradStages - 1);
-        cp_async_commit();
-        const int ahead = tid < 64 ? token_of(step + kWgradStages, tid) : 0;
-        const uint32_t st = s0 + (step % kWgradStages) * kStage;
-        uint32_t gs = st;
-        if (q8) {
-            const uint32_t now[2] = {ex[0], ex[1]};
-            ex[0] = exponent_of(step + 1, 0);
-            ex[1] = exponent_of(step + 1, 1);
-            __syncwarp();                // the previous step's fragments of this warp's columns are read
-            widen(step, now);
-            __syncwarp();
-            gs = wide;
-        }
-#pragma unroll
-        for (int k16 = 0; k16 < 4; ++k16) {
-            uint32_t g[4];
-            const int tr = k16 * 16 + (lane & 7) + ((lane >> 4) << 3), gc = warp * 2 + ((lane >> 3) & 1);
-            ldsm_x4_trans(gs + tr * 256 + ((gc ^ (tr & 7)) << 4), g);
-            const int pr = k16 * 16 + (lane & 15);
-#pragma unroll
-            for (int rt = 0; rt < RP / 16; ++rt) {
-                uint32_t b[4];
-                const int ch = rt * 2 + (lane >> 4);
-                ldsm_x4_trans(st + kWgradG + pr * RP * 2 + ((ch ^ (pr & (kCh < 8 ? kCh - 1 : 7))) << 4), b);
-                mma_16816(acc[2 * rt], g, b[0], b[1]);
-                mma_16816(acc[2 * rt + 1], g, b[2], b[3]);
-            }
-        }
-        // (slot (step + 3) % 4 held step - 1's tokens, which every thread is done with)
-        if (tid < 64) tok[(step + kWgradStages) % kTokRing][tid] = ahead;
-    }
-    cp_async_wait<0>();
-    __syncthreads();
-    float* tile = reinterpret_cast<float*>(smem);
-    const int gr = lane >> 2, q = lane & 3;
-#pragma unroll
-    for (int i = 0; i < RP / 8; ++i)
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-            *reinterpret_cast<float2*>(tile + (warp * 16 + gr + 8 * half) * kAccPitch + i * 8 + 2 * q) =
-                make_float2(acc[i][2 * half], acc[i][2 * half + 1]);
-    if (ranks > 1) cluster_sync_all();
-    else __syncthreads();
-    // rank r finishes 128 / ranks of the tile's columns
-    const int mine = 128 / ranks, cb = rank * mine;
-    auto total = [&](int c, int r) {
-        if (ranks == 1) return tile[c * kAccPitch + r];
-        const uint32_t at = s0 + (c * kAccPitch + r) * 4;
-        float v = 0.f;
-        for (int k = 0; k < ranks; ++k) v += ld_shared_cluster_f32(map_shared_rank(at, k));
-        return v;
-    };
     const int R = w.R;
+    if (warp < kGatherWarps) {
+        const bool q8 = part.exps != nullptr;
+        uint8_t* raw = smem + S * kStage;
+        // Token ids of this thread's rows a step ahead, so that no copy waits for its row's address:
+        // rows tid / 16 + 16 i of a bf16 G, rows tid / 8 + 32 i (i < 2) of an 8-bit one, and rows
+        // tid / 4 + ... of P (by 4, 8, 16 or 32 lanes a row; at most one row for Rp <= 32)
+        constexpr int kPLanes = RP / 8, kPRows = kPLanes <= 4 ? 1 : kPLanes * 64 / 256;
+        int ids[4], pid[kPRows];
+        auto fetch = [&](int step) {
+            const int t0 = t_begin + step * 64;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = t0 + (q8 ? (tid >> 3) + 32 * i : (tid >> 4) + 16 * i);
+                ids[i] = (!q8 || i < 2) && t < t_end ? perm[t] : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < kPRows; ++i) {
+                const int t = t0 + tid / kPLanes + i * (256 / kPLanes);
+                pid[i] = tid / kPLanes + i * (256 / kPLanes) < 64 && t < t_end ? perm[t] : -1;
+            }
+        };
+        uint32_t ex[S][2] = {};                       // exponents of the thread's two code chunks, per raw slot
+        auto load = [&](int step, uint32_t (&e)[2]) {
+            const uint32_t st = s0 + (step % S) * kStage;
+            if (!q8) {
+                const __nv_bfloat16* G = static_cast<const __nv_bfloat16*>(part.G);
+                const int ch = tid & 15;
+                const bool c_ok = c0 + ch * 8 < part.C;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool ok = ids[i] >= 0 && c_ok;
+                    const size_t src = ok ? static_cast<size_t>(ids[i]) * part.C + c0 + ch * 8 : 0;
+                    cp_async16(st + (ch >> 3) * 8192 + swizzled((tid >> 4) + 16 * i, ch & 7, 128), G + src, ok);
+                }
+            } else {
+                const uint8_t* G = static_cast<const uint8_t*>(part.G);
+                const int ch = tid & 7;
+                const bool c_ok = c0 + ch * 16 < part.C;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool ok = ids[i] >= 0 && c_ok;
+                    const size_t src = ok ? static_cast<size_t>(ids[i]) * part.C + c0 + ch * 16 : 0;
+                    cp_async16(smem_u32(raw) + (step % S) * kRawBytes + (tid + 256 * i) * 16, G + src, ok);
+                    e[i] = ok ? part.exps[src >> 5] : 0;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPRows; ++i) {
+                const int row = tid / kPLanes + i * (256 / kPLanes), ch = tid % kPLanes;
+                if (row < 64) {
+                    const bool ok = pid[i] >= 0 && ch * 8 < R;
+                    const size_t src = ok ? static_cast<size_t>(pid[i]) * R + ch * 8 : 0;
+                    cp_async16(st + kWideBytes + narrow_mn_offset<RP>(row, ch), part.P + src, ok);
+                }
+            }
+        };
+        auto widen = [&](int step, const uint32_t (&e)[2]) {
+            uint8_t* st = smem + (step % S) * kStage;
+            const int ch = tid & 7;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 c = *reinterpret_cast<const uint4*>(raw + (step % S) * kRawBytes + (tid + 256 * i) * 16);
+                const int row = (tid >> 3) + 32 * i;
+                uint8_t* half = st + (ch >> 2) * 8192;
+                *reinterpret_cast<uint4*>(half + swizzled(row, (2 * ch) & 7, 128)) =
+                    checkpoint_decode8(make_uint2(c.x, c.y), e[i]);
+                *reinterpret_cast<uint4*>(half + swizzled(row, (2 * ch + 1) & 7, 128)) =
+                    checkpoint_decode8(make_uint2(c.z, c.w), e[i]);
+            }
+        };
+        bool ok = true;
+        fetch(0);
+        // (unrolled by the ring's length, so that the exponents stay in registers)
+        for (int base = 0; ok && base < steps + S - 2; base += S) {
+#pragma unroll
+            for (int u = 0; u < S; ++u) {
+                const int step = base + u;
+                if (!ok || step >= steps + S - 2) break;
+                if (step < steps) {
+                    if (!(ok = gather_wait_slot<S>(g, step))) break;
+                    load(step, ex[u]);
+                    fetch(step + 1);
+                }
+                cp_async_commit();
+                if (step >= S - 2) {
+                    cp_async_wait<S - 2>();
+                    if (q8) widen(step - (S - 2), ex[(u + 2) % S]);
+                    gather_publish<S>(g, step - (S - 2));
+                }
+            }
+        }
+        cp_async_wait<0>();
+    } else if (lane == 0) {
+        constexpr uint32_t idesc = idesc_bf16_f32(128, RP) | kIdescTransposeA | kIdescTransposeB;
+        gather_mma<S>(g, s0, kStage, steps, [&](uint32_t st, int k16, uint32_t acc) {
+            mma_f16_ss(tmem, smem_desc_mn(st + k16 * 2048, 128, 8192), narrow_mn_desc<RP>(st + kWideBytes, k16), idesc, acc);
+        });
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // the fp32 tile [128 columns of G][Rp], over the drained ring
+    float* tile = reinterpret_cast<float*>(smem);
+    if (warp < 4) {
+        float* dst = tile + (warp * 32 + lane) * kAccPitch;
+#pragma unroll
+        for (int c = 0; c < RP; c += 16) {
+            uint32_t v[16] = {};
+            if (steps > 0) {
+                tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+                tmem_wait_ld();
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kGatherWarps) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
+    }
+    if (ranks > 1) cluster_sync_all();
+    // rank r finishes 128 / ranks of the tile's columns: it adds the ranks' parts into its own tile
+    // (which no other rank reads there), four values a load, then all store from shared memory
+    const int mine = 128 / ranks, cb = rank * mine;
+    if (ranks > 1) {
+        constexpr int kQuads = RP / 4;
+        for (int i = tid; i < mine * kQuads; i += kGatherThreads) {
+            const uint32_t off = static_cast<uint32_t>(((cb + i / kQuads) * kAccPitch + i % kQuads * 4) * 4);
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < ranks) v[k] = ld_shared_cluster_v4(map_shared_rank(s0 + off, k));
+#pragma unroll
+            for (int k = 1; k < 8; ++k)
+                if (k < ranks) {
+                    v[0].x += v[k].x;
+                    v[0].y += v[k].y;
+                    v[0].z += v[k].z;
+                    v[0].w += v[k].w;
+                }
+            *reinterpret_cast<float4*>(smem + off) = v[0];
+        }
+        __syncthreads();
+    }
     if (first) {   // dA [a][R][C]: neighbouring threads take neighbouring columns
-        const int half = mine / 2;
-        for (int i = tid; i < half * R; i += kWgradThreads) {
-            const int c = cb + i % half * 2, r = i / half;
+        const int half_log2 = 31 - __clz(mine / 2);   // 128 / ranks is a power of two
+        for (int i = tid; i < R << half_log2; i += kGatherThreads) {
+            const int c = cb + (i & ((1 << half_log2) - 1)) * 2, r = i >> half_log2;
             if (c0 + c < part.C)
                 *reinterpret_cast<__nv_bfloat162*>(part.out + (static_cast<size_t>(a) * R + r) * part.C + c0 + c) =
-                    __floats2bfloat162_rn(total(c, r), total(c + 1, r));
+                    __floats2bfloat162_rn(tile[c * kAccPitch + r], tile[(c + 1) * kAccPitch + r]);
         }
     } else {       // dB [a][C][R]
-        const int half = R / 2;
-        for (int i = tid; i < mine * half; i += kWgradThreads) {
-            const int c = cb + i / half, r = i % half * 2;
-            if (c0 + c < part.C)
-                *reinterpret_cast<__nv_bfloat162*>(part.out + (static_cast<size_t>(a) * part.C + c0 + c) * R + r) =
-                    __floats2bfloat162_rn(total(c, r), total(c, r + 1));
+        for (int i = tid; i < mine * (RP / 8); i += kGatherThreads) {
+            const int c = cb + i / (RP / 8), r = i % (RP / 8) * 8;
+            if (c0 + c < part.C && r < R) {
+                const float* f = tile + c * kAccPitch + r;
+                uint32_t u[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * q], f[2 * q + 1]);
+                    u[q] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                *reinterpret_cast<uint4*>(part.out + (static_cast<size_t>(a) * part.C + c0 + c) * R + r) =
+                    make_uint4(u[0], u[1], u[2], u[3]);
+            }
         }
     }
     if (ranks > 1) cluster_sync_all();   // the other ranks may still read this CTA's tile
@@ -737,20 +853,21 @@ lowbit_status shrink_launch(const ExtProblem& e, const ExtBuffers& b, cudaStream
     const ExtWorkspace& w = b.w;
     auto fn = shrink_kernel<RP, KMAJOR>;
     static std::atomic<uint64_t> devices{0};
-    if (!allow_smem(fn, shrink_smem(RP), devices)) return LOWBIT_ERR_CUDA;
-    return launch_pdl(fn, dim3(static_cast<unsigned>(w.num_blocks), static_cast<unsigned>(w.ksplit), 1), kShrinkThreads,
-                      shrink_smem(RP), 1, stream, static_cast<const __nv_bfloat16*>(e.in),
+    unsigned* status = device_status_address();
+    if (!status || !allow_smem(fn, kShrinkSmem<RP>, devices)) return LOWBIT_ERR_CUDA;
+    return launch_pdl(fn, dim3(static_cast<unsigned>(w.num_blocks), static_cast<unsigned>(w.ksplit), 1), kGatherThreads,
+                      kShrinkSmem<RP>, 1, stream, static_cast<const __nv_bfloat16*>(e.in),
                       static_cast<const __nv_bfloat16*>(e.grad ? e.ad.B : e.ad.A), static_cast<int>(e.M),
                       static_cast<int>(e.red), e.ad.rank, static_cast<int>(w.kslice), b.at<int>(w.perm),
-                      b.at<int4>(w.blocks), b.at<float>(w.partial));
+                      b.at<int4>(w.blocks), b.at<float>(w.partial), status);
 }
 
 template <int RP>
 lowbit_status wgrad_launch(const WgradArgs& args, int ranks, int num, cudaStream_t stream) {
     auto fn = wgrad_kernel<RP>;
     static std::atomic<uint64_t> devices{0};
-    if (!allow_smem(fn, wgrad_smem(RP), devices)) return LOWBIT_ERR_CUDA;
-    return launch_pdl(fn, dim3(ranks, args.part[0].tiles + args.part[1].tiles, num), kWgradThreads, wgrad_smem(RP), ranks,
+    if (!allow_smem(fn, kWgradSmem<RP>, devices)) return LOWBIT_ERR_CUDA;
+    return launch_pdl(fn, dim3(ranks, args.part[0].tiles + args.part[1].tiles, num), kGatherThreads, kWgradSmem<RP>, ranks,
                       stream, args);
 }
 
@@ -926,6 +1043,8 @@ lowbit_status launch_wgrad(const WgradProblem& g, const ExtBuffers& b, cudaStrea
     a.R = g.rank;
     a.perm = b.at<int>(b.w.perm);
     a.seg = b.at<int>(b.w.seg);
+    a.status = device_status_address();
+    if (!a.status) return LOWBIT_ERR_CUDA;
     // Token slices per tile (a cluster's CTAs): whichever of 1, 2, 4, 8 gives the smallest waves x
     // (steps per slice + a slice's fixed cost, about four steps, and two more for the reduction), two
     // CTAs per SM and the tokens taken as evenly shared by the adapters.

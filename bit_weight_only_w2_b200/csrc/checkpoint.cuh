@@ -29,28 +29,41 @@ __device__ __forceinline__ uint32_t checkpoint_exponent(uint32_t amax) {
 }
 
 // Eight bf16 values of one thread -> eight codes; the block's four neighbouring lanes (aligned to 4)
-// call together. `exponent` is the block's byte.
+// call together. `exponent` is the block's byte. The product with 2^-e is formed in bf16 (exact, or
+// below e4m3's range); a block with an infinity or NaN takes the longer way.
 __device__ __forceinline__ uint2 checkpoint_encode8(const uint4& v, uint8_t& exponent) {
-    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0;
+    uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    auto lanes_max = [](uint32_t m) {
+        m = max(m & 0xFFFFu, m >> 16);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    };
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    uint32_t m = lanes_max(__vmaxs2(__vmaxs2(in[0] & kAbs, in[1] & kAbs), __vmaxs2(in[2] & kAbs, in[3] & kAbs)));
+    if (__any_sync(0xffffffffu, m >= 0x7F80u)) {
+        uint32_t f = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max(finite_abs_bf16(in[i]), finite_abs_bf16(in[i] >> 16)));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        for (int i = 0; i < 4; ++i) {
+            f = max(f, max(finite_abs_bf16(in[i]), finite_abs_bf16(in[i] >> 16)));
+            if ((in[i] & 0x7F80u) == 0x7F80u) in[i] |= 0x7FFFu;               // an infinity becomes NaN too
+            if ((in[i] & 0x7F800000u) == 0x7F800000u) in[i] |= 0x7FFF0000u;
+        }
+        m = lanes_max(f);
+    }
     const uint32_t kept = checkpoint_exponent(m);
     exponent = static_cast<uint8_t>(kept);
-    // 2^(127 - kept): kept <= 247, so the scale is a normal fp32 number
-    const float scale = __uint_as_float((254u - kept) << 23);
+    // 2^(127 - kept): kept <= 247, so the scale is a normal number
+    const uint32_t s1 = (254u - kept) << 7, s2 = s1 | (s1 << 16);
     uint32_t pair[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = make_float2(__uint_as_float(in[i] << 16) * scale, __uint_as_float(in[i] & 0xFFFF0000u) * scale);
-        uint32_t c = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-        if ((in[i] & 0x7F80u) == 0x7F80u) c = (c & 0xFF00u) | 0x7Fu;
-        if ((in[i] & 0x7F800000u) == 0x7F800000u) c = (c & 0xFFu) | 0x7F00u;
-        pair[i] = c & 0xFFFFu;
+        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&in[i]),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&s2));
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&y);
+        pair[i] = __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)),
+                                           __NV_SATFINITE, __NV_E4M3);
     }
-    return make_uint2(pair[0] | (pair[1] << 16), pair[2] | (pair[3] << 16));
+    return make_uint2(__byte_perm(pair[0], pair[1], 0x5410), __byte_perm(pair[2], pair[3], 0x5410));
 }
 
 // Eight codes -> eight bf16 values (two per word). Exact: four significant bits times a power of

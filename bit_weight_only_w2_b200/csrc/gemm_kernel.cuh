@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                             const int in = c & ((1 << p.chunk_log2) - 1);
                             const uint64_t adesc = EXT == kExtAdapter
                                                        ? smem_desc_k(box + in * 2, 2 << p.chunk_log2)
-                                                       : smem_desc_mn_sw128(box + in * 128, 128 << p.chunk_log2);
+                                                       : smem_desc_mn(box + in * 128, 128, 128 << p.chunk_log2);
                             if (PAIR)
                                 mma_f16_ss_pair(d_tmem, adesc, bdesc, C::kIdescSlot, 1u);
                             else

@@ -222,12 +222,13 @@ __device__ __forceinline__ uint64_t smem_desc_k(uint32_t smem_addr, uint32_t row
     return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1u) << 16 |
            static_cast<uint64_t>((8 * row_bytes) >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | layout << 61;
 }
-// MN-major operand, 128-byte swizzle: rows of 64 consecutive M (or N) elements, one row per K;
-// 8-row groups along K 1024 bytes apart (stride byte offset), the next 64 elements of M
-// `m_bytes` further on (leading byte offset).
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t smem_addr, uint32_t m_bytes) {
+// MN-major operand: one row per K of `row_bytes` = 32, 64 or 128 bytes of consecutive M (or N)
+// elements, swizzled over that width; 8-row groups along K 8 * row_bytes apart (stride byte
+// offset), the next row_bytes / 2 elements of M `m_bytes` further on (leading byte offset).
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t smem_addr, uint32_t row_bytes, uint32_t m_bytes) {
+    const uint64_t layout = row_bytes == 128 ? 2u : row_bytes == 64 ? 4u : 6u;
     return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | static_cast<uint64_t>((m_bytes >> 4) & 0x3FFFu) << 16 |
-           static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
+           static_cast<uint64_t>((8 * row_bytes) >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | layout << 61;
 }
 
 // Instruction descriptor for kind::f16 with fp16 A/B, fp32 D, both K-major, shape M x N.
@@ -244,6 +245,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
     return idesc_f16_f32(M, N) | (1u << 7) | (1u << 10);   // A and B format: BF16
 }
 constexpr uint32_t kIdescTransposeA = 1u << 15;            // A is MN-major
+constexpr uint32_t kIdescTransposeB = 1u << 16;            // B is MN-major
 
 // ---- cluster rank ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_ctarank() {
