@@ -407,12 +407,17 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
         int x0, x1;
         __device__ int blocks() const { return (x1 - x0 + C::kSlotCols - 1) / C::kSlotCols; }
     };
-    auto extra_of = [&](int t) -> Extra {
+    // Split in a load and the arithmetic on it, so that a tile's count can be asked for a tile ahead
+    // without the asking thread waiting for it.
+    auto slots_of = [&](int t) -> int {
+        if constexpr (EXT == kExtNone) return 0;
+        else return p.tile_slots && t < my_tiles ? __ldg(p.tile_slots + (tile0 + t * tile_step) / p.n_tiles) : 0;
+    };
+    auto extra_of = [&](int slots) -> Extra {
         if constexpr (EXT == kExtNone) {
             return Extra{0, 0};
         } else {
-            if (!p.tile_slots || t >= my_tiles) return Extra{0, 0};
-            const int cols = __ldg(p.tile_slots + (tile0 + t * tile_step) / p.n_tiles) << p.rank_log2;
+            const int cols = slots << p.rank_log2;
             if (!split) return Extra{0, cols};
             const int per = ((cols + C::kSlotCols - 1) / C::kSlotCols + p.ksplit - 1) / p.ksplit * C::kSlotCols;
             const int x0 = min(cols, static_cast<int>(blockIdx.z) * per);
@@ -435,9 +440,18 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                 m0 = (tile / p.n_tiles) * BT;
                 n0 = (tile % p.n_tiles) * n_stride + n_off;
             };
+            // The variants keep the next stages' coordinates at hand instead of deriving them from `it`:
+            // the X ring's refill latency bounds the kernel (divisions between a slot's release and its
+            // next request cost 4.5 % on 4173 x 9216 x 9216).
+            int wt = 0, wk = kb_begin, wn0 = (tile0 % p.n_tiles) * n_stride + n_off;
             auto issue_w = [&](uint32_t it) {
                 int m0, n0, kb;
-                coords(it, m0, n0, kb);
+                if constexpr (EXT == kExtNone) {
+                    coords(it, m0, n0, kb);
+                } else {
+                    n0 = wn0;
+                    kb = wk;
+                }
                 const uint32_t s = it % SW;
                 uint8_t* st = wring + s * C::kWStageBytes;
                 mbar_arrive_expect_tx(&wfull[s], p.wtx_bytes);
@@ -447,15 +461,32 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                 const int sy = EXT == kExtGrad ? n0 / GS : kb * C::kGroupsPerStage;
                 tma_load_2d(&map_s, &wfull[s], st + C::kSOff, sx, sy);
                 if (BITS == 4) tma_load_2d(&map_z, &wfull[s], st + C::kZOff, sx, sy);
+                if (EXT != kExtNone && ++wk == kb_end) {
+                    wk = kb_begin;
+                    wn0 = ((tile0 + ++wt * tile_step) % p.n_tiles) * n_stride + n_off;
+                }
             };
             // With slot columns a tile has more X stages than nkb: behind the K blocks, P and the weight
             // side of each block of columns. xj: the next stage of tile xt (of nkb + 2 * blocks).
-            int xt = 0, xj = 0;
+            int xt = 0, xj = 0, xn = nkb, xm0 = (tile0 / p.n_tiles) * BT + static_cast<int>(pair_rank) * C::kXRows;
+            int next_slots = 0;
             Extra xe{0, 0};
+            auto start_tile = [&](int slots) {
+                xe = extra_of(slots);
+                xn = nkb + 2 * xe.blocks();
+                next_slots = slots_of(xt + 1);
+            };
+            auto next_x = [&] {
+                if (++xj == xn) {
+                    xj = 0;
+                    xm0 = ((tile0 + ++xt * tile_step) / p.n_tiles) * BT + static_cast<int>(pair_rank) * C::kXRows;
+                    start_tile(next_slots);
+                }
+            };
             auto issue_slots = [&](uint32_t s) {
                 if constexpr (EXT != kExtNone) {
                     const int tile = tile0 + xt * tile_step;
-                    const int m0 = tile / p.n_tiles * BT, n0 = tile % p.n_tiles * n_stride + n_off;
+                    const int n0 = tile % p.n_tiles * n_stride + n_off;
                     const int c0 = xe.x0 + (xj - nkb) / 2 * C::kSlotCols;
                     const int c1 = min(xe.x1, c0 + C::kSlotCols);
                     uint8_t* st = smem + s * C::kXStageBytes;
@@ -467,7 +498,7 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                     };
                     if (((xj - nkb) & 1) == 0) {
                         if (issuer) mbar_arrive_expect_tx(&xfull[s], kPairCtas * C::kPHalves * C::kXHalfBytes);
-                        load(&p.map_p, st, 0, m0 + static_cast<int>(pair_rank) * C::kXRows, c0 / 64);
+                        load(&p.map_p, st, 0, xm0, c0 / 64);
                     } else {
                         const int chunk = 1 << p.chunk_log2, chunks = (c1 - c0) >> p.chunk_log2;
                         const int* slots = p.slot_adapter + static_cast<size_t>(tile / p.n_tiles) * p.slot_pitch;
@@ -484,37 +515,32 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                             }
                         }
                     }
-                    if (++xj == nkb + 2 * xe.blocks()) {
-                        xj = 0;
-                        xe = extra_of(++xt);
-                    }
+                    next_x();
                 }
             };
             auto issue_x = [&](uint32_t it) {
-                int m0, n0, kb;
-                if constexpr (EXT == kExtNone) {
-                    coords(it, m0, n0, kb);
-                } else {
-                    if (xj >= nkb) return issue_slots(it % SX);
-                    m0 = ((tile0 + xt * tile_step) / p.n_tiles) * BT;
-                    kb = kb_begin + xj;
-                    if (++xj == nkb + 2 * xe.blocks()) {
-                        xj = 0;
-                        xe = extra_of(++xt);
-                    }
-                }
                 const uint32_t s = it % SX;
+                int m, kb;   // first token row of this CTA's box, k-block
+                if constexpr (EXT == kExtNone) {
+                    int m0, n0;
+                    coords(it, m0, n0, kb);
+                    m = m0 + static_cast<int>(pair_rank) * C::kXRows;
+                } else {
+                    if (xj >= nkb) return issue_slots(s);
+                    m = xm0;
+                    kb = kb_begin + xj;
+                }
                 uint8_t* st = smem + s * C::kXStageBytes;
                 // box (64 k, kXRows tokens, 2 halves) = both 128-byte-swizzled K halves in one request
                 if (!PAIR) {
                     mbar_arrive_expect_tx(&xfull[s], C::kXBytes);
-                    tma_load_3d(&map_x, &xfull[s], st, 0, m0, kb * 2);
+                    tma_load_3d(&map_x, &xfull[s], st, 0, m, kb * 2);
                 } else {
                     // both halves complete on the issuer's barrier, which expects both
                     if (issuer) mbar_arrive_expect_tx(&xfull[s], 2 * C::kXBytes);
-                    tma_load_3d_pair(&map_x, on_issuer(&xfull[s]), st, 0, m0 + static_cast<int>(pair_rank) * C::kXRows,
-                                     kb * 2);
+                    tma_load_3d_pair(&map_x, on_issuer(&xfull[s]), st, 0, m, kb * 2);
                 }
+                if (EXT != kExtNone) next_x();
             };
             // The packed weights and scales are not written by the kernel just before this one
             // (the X conversion, which itself starts only once everything earlier in the stream
@@ -523,7 +549,9 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
             const uint32_t wpre = total < static_cast<uint32_t>(SW) ? total : static_cast<uint32_t>(SW);
             for (; itw < wpre; ++itw) issue_w(itw);
             grid_dependency_wait();
-            if constexpr (EXT != kExtNone) xe = extra_of(0);
+            if constexpr (EXT != kExtNone) {
+                start_tile(slots_of(0));
+            }
             auto x_left = [&] { return EXT == kExtNone ? itx < total : xt < my_tiles; };
             // Fill both rings as their slots free up, without blocking on either.
             bool ok = true;
@@ -583,7 +611,7 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
             Extra xe{0, 0};
             if constexpr (EXT != kExtNone) {
                 grid_dependency_wait();   // before the tiles' slot counts
-                xe = extra_of(0);
+                xe = extra_of(slots_of(0));
             }
             for (int t = 0; t < my_tiles && ok; ++t, ++tcount) {
                 const uint32_t b = tcount % NACC, acc_ph = (tcount / NACC) & 1u;
@@ -593,7 +621,7 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + b * BT;
-                const Extra xnext = extra_of(t + 1);   // (its latency hides behind this tile's MMAs)
+                const int next_slots = slots_of(t + 1);
                 for (int kb = kb_begin; kb < kb_end; ++kb, ++it, ++ait) {
                     const uint32_t s = it % SX, ph = (it / SX) & 1u;
                     const uint32_t a = ait % NA, aph = (ait / NA) & 1u;
@@ -657,7 +685,7 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                             mma_commit(&xempty[ss]);
                         }
                     }
-                    xe = xnext;
+                    xe = extra_of(next_slots);
                 }
                 if (!ok) break;
                 if (PAIR)
