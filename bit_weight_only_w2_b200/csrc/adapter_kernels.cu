@@ -289,9 +289,10 @@ __global__ void __launch_bounds__(kGatherThreads, 2)
             const bool k_ok = k0 + ch * 8 < k_end;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                // (rows past the block's tokens are not filled: whatever they hold stays in their own
+                // rows of the product, which are not stored)
                 const int row = row0 + 32 * i;
-                const bool ok = row < count && k_ok;
-                cp_async16(st + swizzled(row, ch, 128), ok ? xrow[i] + k0 : in, ok);
+                if (row < count) cp_async16(st + swizzled(row, ch, 128), k_ok ? xrow[i] + k0 : in, k_ok);
             }
             const uint32_t ws = st + kWideBytes;
 #pragma unroll
@@ -939,9 +940,9 @@ ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int ra
     if (num > 0) {
         const int rp = 1 << slot_log2(rank);
         w.num_blocks = M / kShrinkTokens + num + 1;
-        // K slices: about two CTAs per SM over the blocks that hold tokens, at least 256 of K each
+        // K slices: one wave of two CTAs per SM over the blocks that hold tokens, at least 256 of K each
         const int64_t busy = M / kShrinkTokens + (num < M ? num : M);
-        int64_t ks = (2 * kSmsAssumed + busy - 1) / (busy > 0 ? busy : 1);
+        int64_t ks = 2 * kSmsAssumed / (busy > 0 ? busy : 1);
         if (ks > w.red64 / 256) ks = w.red64 / 256;
         if (ks > 16) ks = 16;
         if (ks < 1) ks = 1;
