@@ -79,7 +79,7 @@ lowbit_status product(const ExtProblem& e, const ExtBuffers& b, cudaStream_t str
 lowbit_status prepare(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
     lowbit_status st = LOWBIT_OK;
     if (e.ad.num > 0) {
-        if ((st = launch_plan(e, b, stream)) != LOWBIT_OK) return st;
+        if (e.ad.index && (st = launch_plan(e, b, stream)) != LOWBIT_OK) return st;
         if ((st = launch_shrink(e, b, stream)) != LOWBIT_OK) return st;
     }
     return launch_convert(e, b, stream);
@@ -224,7 +224,8 @@ LOWBIT_API lowbit_status lowbit_adapter_backward(int64_t M, int64_t N, int64_t K
     e.p_out = b.at<void>(b.w.p);
     if ((st = check_device()) != LOWBIT_OK) return st;
     if ((st = prepare(e, b, s)) != LOWBIT_OK) return st;
-    WgradProblem g = {dY, X, ck_codes, ck_exps, P, e.p_out, dA, dB, M, N, K, e.ad.num, e.ad.rank};
+    WgradProblem g = {dY, X, ck_codes, ck_exps, P, e.p_out, dA, dB, M, N, K, e.ad.num, e.ad.rank,
+                      e.ad.index != nullptr};
     if ((st = launch_wgrad(g, b, s)) != LOWBIT_OK) return st;
     return dX ? product(e, b, s) : LOWBIT_OK;
 }

@@ -93,6 +93,7 @@ struct WgradProblem {
     void* dB;                  // bf16 [L][N][R]
     int64_t M, N, K;
     int num, rank;
+    bool planned;              // false: no index, every token has adapter 0
 };
 lowbit_status launch_wgrad(const WgradProblem& g, const ExtBuffers& b, cudaStream_t stream);
 

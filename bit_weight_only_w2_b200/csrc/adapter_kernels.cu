@@ -50,6 +50,8 @@ __device__ __forceinline__ void cp_async_wait() {
 // seg[a] / T + a + i, i < ceil(count / T), which never collide: the next adapter starts at
 // floor(seg[a + 1] / T) + a + 1, and ceil(count / T) <= floor(seg[a + 1] / T) -
 // floor(seg[a] / T) + 1. Numbers in between stay empty (count 0).
+// Without an index every token has adapter 0 and lies where it belongs: no plan is made, and the
+// kernels below are given null pointers for its parts (perm, blocks, seg, token_slot).
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
@@ -252,10 +254,14 @@ __global__ void __launch_bounds__(kGatherThreads, 2)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int4 blk = blocks[blockIdx.x];
+    const int at = static_cast<int>(blockIdx.x) * kShrinkTokens;
+    const int4 blk = blocks ? blocks[blockIdx.x] : make_int4(0, at, min(kShrinkTokens, M - at), 0);
     const int count = blk.z;
     if (count <= 0) return;
-    if (tid < kShrinkTokens) tok[tid] = perm[blk.y + min(tid, count - 1)];
+    if (tid < kShrinkTokens) {
+        const int t = blk.y + min(tid, count - 1);
+        tok[tid] = perm ? perm[t] : t;
+    }
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&bars[i], kGatherWarps);
@@ -372,12 +378,13 @@ __global__ void __launch_bounds__(32 * kShrinkSmallWarps)
                         const float* __restrict__ scaling, const int* __restrict__ index, float* __restrict__ p,
                         __nv_bfloat16* __restrict__ p_out) {
     grid_dependency_wait();
-    grid_launch_dependents();
+    grid_launch_dependents();   // (only now: the small-M kernel that follows reads X without waiting)
     const int m = blockIdx.y, r = 2 * blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int a = adapter_of(index, m, num);
-    float s0 = 0.f, s1 = 0.f;
+    float s0 = 0.f, s1 = 0.f, sc = 0.f;
     if (a >= 0) {
+        sc = scaling[a];
         const uint4* x = in + static_cast<size_t>(m) * K8;
         const uint4* a0 = A + (static_cast<size_t>(a) * R + r) * K8;
         const uint4* a1 = a0 + K8;
@@ -404,7 +411,7 @@ __global__ void __launch_bounds__(32 * kShrinkSmallWarps)
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < kShrinkSmallWarps; ++w) s += threadIdx.x ? part[w].y : part[w].x;
-        if (a >= 0) s *= scaling[a];
+        s *= sc;
         const size_t at = static_cast<size_t>(m) * R + r + threadIdx.x;
         p[at] = s;
         if (p_out) p_out[at] = __float2bfloat16_rn(s);
@@ -460,8 +467,8 @@ __global__ void __launch_bounds__(kConvThreads, 4)
     __shared__ float prow[kMaxRank];
     int slot = -1, cols = 0;
     if (LR) {
-        slot = s.token_slot[row];
-        cols = s.tile_slots[row >> s.tile_log2] << s.rp_log2;   // the columns the MMA reads
+        slot = s.token_slot ? s.token_slot[row] : 0;
+        cols = (s.tile_slots ? s.tile_slots[row >> s.tile_log2] : 1) << s.rp_log2;   // the columns the MMA reads
         if (tid < (1 << s.rp_log2)) {
             const int a = adapter_of(s.index, row, s.num);
             const float* part = s.partial + (static_cast<size_t>(row) << s.rp_log2) + tid;
@@ -575,7 +582,7 @@ struct WgradPart {
 };
 struct WgradArgs {
     WgradPart part[2];         // dA (out transposed), dB
-    int R;
+    int R, M;
     const int* perm;
     const int* seg;
     unsigned* status;
@@ -630,11 +637,11 @@ __global__ void __launch_bounds__(kGatherThreads, RP == 128 ? 1 : 2) wgrad_kerne
     const WgradPart part = first ? w.part[0] : w.part[1];
     const int c0 = (first ? blockIdx.y : blockIdx.y - w.part[0].tiles) * 128;
     const int a = blockIdx.z, rank = blockIdx.x, ranks = gridDim.x;
-    const int seg0 = w.seg[a], count = w.seg[a + 1] - seg0;
+    const int seg0 = w.seg ? w.seg[a] : 0, count = w.seg ? w.seg[a + 1] - seg0 : a == 0 ? w.M : 0;
     const int per = ((count + 63) / 64 + ranks - 1) / ranks * 64;
     const int t_begin = min(count, rank * per), t_end = min(count, t_begin + per);
     const int steps = (t_end - t_begin + 63) / 64;
-    const int* perm = w.perm + seg0;
+    auto token = [&](int t) { return w.perm ? w.perm[seg0 + t] : t; };
     const int R = w.R;
     if (warp < kGatherWarps) {
         const bool q8 = part.exps != nullptr;
@@ -649,12 +656,12 @@ __global__ void __launch_bounds__(kGatherThreads, RP == 128 ? 1 : 2) wgrad_kerne
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int t = t0 + (q8 ? (tid >> 3) + 32 * i : (tid >> 4) + 16 * i);
-                ids[i] = (!q8 || i < 2) && t < t_end ? perm[t] : -1;
+                ids[i] = (!q8 || i < 2) && t < t_end ? token(t) : -1;
             }
 #pragma unroll
             for (int i = 0; i < kPRows; ++i) {
                 const int t = t0 + tid / kPLanes + i * (256 / kPLanes);
-                pid[i] = tid / kPLanes + i * (256 / kPLanes) < 64 && t < t_end ? perm[t] : -1;
+                pid[i] = tid / kPLanes + i * (256 / kPLanes) < 64 && t < t_end ? token(t) : -1;
             }
         };
         uint32_t ex[S][2] = {};                       // exponents of the thread's two code chunks, per raw slot
@@ -856,11 +863,13 @@ lowbit_status shrink_launch(const ExtProblem& e, const ExtBuffers& b, cudaStream
     static std::atomic<uint64_t> devices{0};
     unsigned* status = device_status_address();
     if (!status || !allow_smem(fn, kShrinkSmem<RP>, devices)) return LOWBIT_ERR_CUDA;
-    return launch_pdl(fn, dim3(static_cast<unsigned>(w.num_blocks), static_cast<unsigned>(w.ksplit), 1), kGatherThreads,
+    const int64_t num_blocks = e.ad.index ? w.num_blocks : (e.M + kShrinkTokens - 1) / kShrinkTokens;
+    return launch_pdl(fn, dim3(static_cast<unsigned>(num_blocks), static_cast<unsigned>(w.ksplit), 1), kGatherThreads,
                       kShrinkSmem<RP>, 1, stream, static_cast<const __nv_bfloat16*>(e.in),
                       static_cast<const __nv_bfloat16*>(e.grad ? e.ad.B : e.ad.A), static_cast<int>(e.M),
-                      static_cast<int>(e.red), e.ad.rank, static_cast<int>(w.kslice), b.at<int>(w.perm),
-                      b.at<int4>(w.blocks), b.at<float>(w.partial), status);
+                      static_cast<int>(e.red), e.ad.rank, static_cast<int>(w.kslice),
+                      e.ad.index ? b.at<int>(w.perm) : nullptr, e.ad.index ? b.at<int4>(w.blocks) : nullptr,
+                      b.at<float>(w.partial), status);
 }
 
 template <int RP>
@@ -999,8 +1008,8 @@ lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStrea
         s.num = e.ad.num;
         s.scaling = e.ad.scaling;
         s.index = e.ad.index;
-        s.token_slot = b.at<int>(w.token_slot);
-        s.tile_slots = b.at<int>(w.tile_slots);
+        s.token_slot = e.ad.index ? b.at<int>(w.token_slot) : nullptr;
+        s.tile_slots = e.ad.index ? b.at<int>(w.tile_slots) : nullptr;
         while ((1 << s.tile_log2) < w.tile_tokens) ++s.tile_log2;
         s.pslots = b.at<__nv_bfloat16>(w.pslots);
         s.p_cols = w.p_cols;
@@ -1042,8 +1051,9 @@ lowbit_status launch_wgrad(const WgradProblem& g, const ExtBuffers& b, cudaStrea
     a.part[1].C = static_cast<int>(g.N);
     a.part[1].tiles = static_cast<int>((g.N + 127) / 128);
     a.R = g.rank;
-    a.perm = b.at<int>(b.w.perm);
-    a.seg = b.at<int>(b.w.seg);
+    a.M = static_cast<int>(g.M);
+    a.perm = g.planned ? b.at<int>(b.w.perm) : nullptr;
+    a.seg = g.planned ? b.at<int>(b.w.seg) : nullptr;
     a.status = device_status_address();
     if (!a.status) return LOWBIT_ERR_CUDA;
     // Token slices per tile (a cluster's CTAs): whichever of 1, 2, 4, 8 gives the smallest waves x

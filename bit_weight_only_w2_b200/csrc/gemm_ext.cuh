@@ -55,7 +55,8 @@ lowbit_status ext_launch(const ExtProblem& e, const ExtBuffers& b, int rows, int
         const uint32_t pbox[3] = {64, static_cast<uint32_t>(C::kXRows), C::kPHalves};
         ok = ok && make_map_3d(&p.map_p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b.at<void>(w.pslots), pdims, pstr, pbox,
                                CU_TENSOR_MAP_SWIZZLE_128B);
-        p.tile_slots = b.at<int>(w.tile_slots);
+        p.adapters = true;
+        p.tile_slots = e.ad.index ? b.at<int>(w.tile_slots) : nullptr;
         p.slot_adapter = b.at<int>(w.slot_adapter);
         p.slot_pitch = static_cast<int>(w.slot_pitch);
         p.rank_log2 = slot_log2(e.ad.rank);

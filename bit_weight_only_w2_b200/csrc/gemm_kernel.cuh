@@ -183,7 +183,8 @@ struct ExtParams : KernelParams {
     CUtensorMap map_p;       // P as (64, M, columns / 64) bf16, boxes of kPHalves halves
     CUtensorMap map_side;    // B as (R, N, L), boxes of `chunk` ranks x 128 rows, or A as (K, R, L),
                              // boxes of 64 rows x `chunk` ranks
-    const int* tile_slots;   // slots of each token tile (nullptr: no adapters)
+    bool adapters;           // any at all
+    const int* tile_slots;   // slots of each token tile (nullptr: one, adapter 0)
     const int* slot_adapter; // [token tile][slot_pitch]
     int slot_pitch;
     int rank_log2;           // log2 of the slot width Rp
@@ -411,7 +412,8 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
     // without the asking thread waiting for it.
     auto slots_of = [&](int t) -> int {
         if constexpr (EXT == kExtNone) return 0;
-        else return p.tile_slots && t < my_tiles ? __ldg(p.tile_slots + (tile0 + t * tile_step) / p.n_tiles) : 0;
+        else if (!p.adapters || t >= my_tiles) return 0;
+        else return p.tile_slots ? __ldg(p.tile_slots + (tile0 + t * tile_step) / p.n_tiles) : 1;
     };
     auto extra_of = [&](int slots) -> Extra {
         if constexpr (EXT == kExtNone) {
@@ -505,7 +507,7 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                         if (issuer) mbar_arrive_expect_tx(&xfull[s], kPairCtas * (chunks << (p.chunk_log2 + 8)));
                         for (int i = 0; i < chunks; ++i) {
                             const int c = c0 + i * chunk, r = c & ((1 << p.rank_log2) - 1);
-                            const int a = __ldg(slots + (c >> p.rank_log2));
+                            const int a = p.tile_slots ? __ldg(slots + (c >> p.rank_log2)) : 0;
                             uint8_t* dst = st + i * chunk * 256;
                             if (EXT == kExtAdapter) {
                                 load(&p.map_side, dst, r, n0, a);

@@ -289,18 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (ks > 1) cluster_sync_all();   // every CTA of the cluster has started (remote stores target it)
     grid_launch_dependents();
-    // (lr_index and B, like the packed weights, are not written by the kernel just before)
-    if constexpr (LR) {
-        const int n0 = static_cast<int>(blockIdx.x) * R;
-        const int lines = (min(R, p.N - n0) * p.lr_rank * 2 + 127) / 128 + 1;
-        for (int i = static_cast<int>(threadIdx.x) + rank * kThreads; i < p.M * lines; i += kThreads * ks) {
-            const int a = lr_adapter(p, i / lines);
-            const size_t end = (static_cast<size_t>(a) * p.N + min(n0 + R, p.N)) * p.lr_rank;
-            const size_t at = (static_cast<size_t>(a) * p.N + n0) * p.lr_rank + i % lines * 64;
-            if (a >= 0 && at < end) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.lr_b + at));
-        }
-    }
-
     // Ring step `gs` of this CTA: tile blockIdx.x + (gs / nst) * gridDim.x, K step gs % nst.
     // Every CTA of a slice reads the same X (only its weight rows differ). Walking the slice's K
     // steps from a different first step per CTA spreads those reads over the whole slice, instead
@@ -334,11 +322,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pre = min(look, total);
     if (threadIdx.x == 0) {
         if (pre > 0) issue(0, true, false);
-        grid_dependency_wait();
+        // (LR: the kernel just before, which forms lr_p, let this one start only after everything
+        // before itself had completed, X with it; so only lr_p is waited for, at the tile's end, and the
+        // whole product overlaps that kernel)
+        if (!LR) grid_dependency_wait();
         for (int gs = 0; gs < pre; ++gs) {
             if (gs > 0) issue(gs, true, false);
             issue(gs, false, true);
             iss[gs] = 1;
+        }
+    }
+
+    // The rows of B that this CTA's first tile will need, asked into L2 by the warps that do not start
+    // the ring. (lr_index and B, like the packed weights, are not written by the kernel just before.)
+    if constexpr (LR) {
+        if (warp > 0) {
+            const int n0 = static_cast<int>(blockIdx.x) * R;
+            const int lines = (min(R, p.N - n0) * p.lr_rank * 2 + 127) / 128 + 1;
+            for (int i = static_cast<int>(threadIdx.x) - 32 + rank * (kThreads - 32); i < p.M * lines;
+                     i += (kThreads - 32) * ks) {
+                const int a = lr_adapter(p, i / lines);
+                const size_t end = (static_cast<size_t>(a) * p.N + min(n0 + R, p.N)) * p.lr_rank;
+                const size_t at = (static_cast<size_t>(a) * p.N + n0) * p.lr_rank + i % lines * 64;
+                if (a >= 0 && at < end) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.lr_b + at));
+            }
         }
     }
 
@@ -376,6 +383,47 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int o = 0; o < NH; ++o) acc[o][0] = acc[o][1] = acc[o][2] = acc[o][3] = 0.f;
 
+    // Low-rank term of this lane's four outputs of unit o of the tile at row n0 (see `store` below for
+    // which they are).
+    [[maybe_unused]] int ad0 = -1, ad1 = -1;   // the adapters of the lane's two tokens
+    if constexpr (LR) {
+        ad0 = lr_adapter(p, SWAP ? 2 * q : g);
+        ad1 = lr_adapter(p, SWAP ? 2 * q + 1 : g + 8);
+    }
+    [[maybe_unused]] auto lowrank = [&](int n0, int o) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if constexpr (LR) {
+            if constexpr (SWAP) {
+                const int n = n0 + 16 * o + g, t0 = 2 * q;
+                const int n8 = n + 8 < p.N ? n + 8 : n;   // (a row past N: not stored, row n stands in)
+                const int a0 = n < p.N ? ad0 : -1, a1 = n < p.N ? ad1 : -1;
+                if (a0 >= 0) {
+                    const float2 u = lr_term(p, a0, t0, n, n8);
+                    v.x = u.x;
+                    v.z = u.y;
+                }
+                if (a1 >= 0) {
+                    const float2 u = lr_term(p, a1, t0 + 1, n, n8);
+                    v.y = u.x;
+                    v.w = u.y;
+                }
+            } else {
+                const int n = n0 + 8 * o + 2 * q;
+                const int a0 = n < p.N ? ad0 : -1, a1 = n < p.N ? ad1 : -1;
+                if (a0 >= 0) {
+                    const float2 u = lr_term(p, a0, g, n, n + 1);
+                    v.x = u.x;
+                    v.y = u.y;
+                }
+                if (a1 >= 0) {
+                    const float2 u = lr_term(p, a1, g + 8, n, n + 1);
+                    v.z = u.x;
+                    v.w = u.y;
+                }
+            }
+        }
+        return v;
+    };
     // ---- the phases of one ring step, shared by both loop drivers below ----
     // P1: this warp's group: fp32 (s, -s * c) of every row of its units, into `tab` (negated so
     // that the scale epilogue is two packed FMAs per pair of accumulators)
@@ -637,25 +685,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         const int n0 = t * R;
         auto store = [&](int o, float4 v) {
+            if constexpr (LR) {
+                const float4 u = lowrank(n0, o);
+                v.x += u.x;
+                v.y += u.y;
+                v.z += u.z;
+                v.w += u.w;
+            }
             if constexpr (SWAP) {
                 // rows n and n + 8 of unit o, tokens 2q and 2q + 1
                 const int n = n0 + 16 * o + g;
                 const int t0 = 2 * q;
-                if constexpr (LR) {
-                    // (row n + 8 past N: its term is not stored, row n's stands in)
-                    const int n8 = n + 8 < p.N ? n + 8 : n;
-                    const int a0 = n < p.N ? lr_adapter(p, t0) : -1, a1 = n < p.N ? lr_adapter(p, t0 + 1) : -1;
-                    if (a0 >= 0) {
-                        const float2 u = lr_term(p, a0, t0, n, n8);
-                        v.x += u.x;
-                        v.z += u.y;
-                    }
-                    if (a1 >= 0) {
-                        const float2 u = lr_term(p, a1, t0 + 1, n, n8);
-                        v.y += u.x;
-                        v.w += u.y;
-                    }
-                }
                 if (dcheck(o < NUT && n >= 0, p.status)) {
                     const float vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -667,19 +707,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 const int n = n0 + 8 * o + 2 * q;
                 if (n < p.N && dcheck(n >= 0 && n + 1 < p.N && o < NUT, p.status)) {
-                    if constexpr (LR) {
-                        const int a0 = lr_adapter(p, g), a1 = lr_adapter(p, g + 8);
-                        if (a0 >= 0) {
-                            const float2 u = lr_term(p, a0, g, n, n + 1);
-                            v.x += u.x;
-                            v.y += u.y;
-                        }
-                        if (a1 >= 0) {
-                            const float2 u = lr_term(p, a1, g + 8, n, n + 1);
-                            v.z += u.x;
-                            v.w += u.y;
-                        }
-                    }
                     if (g < p.M)
                         *reinterpret_cast<__nv_bfloat162*>(p.Y + static_cast<size_t>(g) * p.N + n) =
                             __floats2bfloat162_rn(v.x, v.y);
