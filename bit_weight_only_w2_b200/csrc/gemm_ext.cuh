@@ -11,21 +11,58 @@
 namespace lowbit {
 namespace {
 
+// Shared-memory opt-in of a kernel, once per device (one bit per device that has it).
+template <int BITS, int GS, int BT, bool PAIR, int EXT>
+bool ext_allow_smem() {
+    using C = Cfg<BITS, GS, BT, PAIR, EXT>;
+    static std::atomic<uint64_t> devices{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+    if (bit && (devices.load(std::memory_order_acquire) & bit)) return true;
+    if (cudaFuncSetAttribute(lowbit_gemm_kernel<BITS, GS, BT, PAIR, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kSmemBytes) != cudaSuccess)
+        return false;
+    devices.fetch_or(bit, std::memory_order_acq_rel);
+    return true;
+}
+
+// Clusters of `ks` CTA pairs that the current device holds at once (asked once per device and ks).
+template <int BITS, int GS, int EXT>
+int pair_clusters(int ks) {
+    using C = Cfg<BITS, GS, 256, true, EXT>;
+    constexpr int kDevices = 16;
+    static std::atomic<int> cached[kDevices][5];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || !ext_allow_smem<BITS, GS, 256, true, EXT>()) return 0;
+    const bool keep = dev < kDevices;
+    if (keep && cached[dev][ks].load(std::memory_order_relaxed) > 0) return cached[dev][ks].load(std::memory_order_relaxed);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = ks;
+    cfg.gridDim = dim3(2, 1, ks);
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, lowbit_gemm_kernel<BITS, GS, 256, true, EXT>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    if (keep && n > 0) cached[dev][ks].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 template <int BITS, int GS, int BT, bool PAIR, int EXT>
 lowbit_status ext_launch(const ExtProblem& e, const ExtBuffers& b, int rows, int ksplit, cudaStream_t stream) {
     using C = Cfg<BITS, GS, BT, PAIR, EXT>;
     auto kernel = lowbit_gemm_kernel<BITS, GS, BT, PAIR, EXT>;
     const void* fn = reinterpret_cast<const void*>(kernel);
-    // the shared-memory opt-in is per device: one bit per device that has it
-    static std::atomic<uint64_t> attr_devices{0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
-    const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
-    if (!bit || !(attr_devices.load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
-            return LOWBIT_ERR_CUDA;
-        attr_devices.fetch_or(bit, std::memory_order_acq_rel);
-    }
+    if (!ext_allow_smem<BITS, GS, BT, PAIR, EXT>()) return LOWBIT_ERR_CUDA;
     const ExtWorkspace& w = b.w;
     const uint64_t M = e.M, R = e.rows;
     const uint64_t red_words = EXT == kExtGrad ? uint64_t(e.red + 127) / 128 * 128 * BITS / 32 : uint64_t(e.red) * BITS / 32;
@@ -88,14 +125,16 @@ lowbit_status ext_launch(const ExtProblem& e, const ExtBuffers& b, int rows, int
     p.num_tiles = p.m_tiles * p.n_tiles;
     p.Y = static_cast<__nv_bfloat16*>(e.out);
     p.rowmul = b.at<float>(w.rowmul);
-    // An unsplit grid of 256-token tiles over a multiple of 256 weight rows runs on CTA pairs.
-    if constexpr (BT == 256 && !PAIR) {
-        if (rows == kBlockN && ksplit == 1 && e.rows % (2 * kBlockN) == 0)
-            return ext_launch<BITS, GS, BT, true, EXT>(e, b, rows, 1, stream);
-    }
     if (ksplit > p.num_kb) ksplit = p.num_kb;
     const int kbps = (p.num_kb + ksplit - 1) / ksplit;
     ksplit = (p.num_kb + kbps - 1) / kbps;     // every rank gets at least one k-block
+    // 256-token tiles over a multiple of 256 weight rows run on CTA pairs, split ones if the GPU holds
+    // all of their clusters at once (a split grid is not persistent)
+    if constexpr (BT == 256 && !PAIR) {
+        const int pair_tiles = static_cast<int>(w.m_tiles * (e.rows / (2 * kBlockN)));
+        if (e.rows % (2 * kBlockN) == 0 && (ksplit == 1 || (ksplit <= 4 && pair_tiles <= pair_clusters<BITS, GS, EXT>(ksplit))))
+            return ext_launch<BITS, GS, BT, true, EXT>(e, b, rows, ksplit, stream);
+    }
     p.kb_per_split = ksplit > 1 ? kbps : p.num_kb;
     p.ksplit = ksplit;
 
@@ -105,7 +144,9 @@ lowbit_status ext_launch(const ExtProblem& e, const ExtBuffers& b, int rows, int
     attrs[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attrs[na].val.programmaticStreamSerializationAllowed = 1;
     ++na;
-    if (PAIR) {
+    if (PAIR && ksplit > 1) {
+        cfg.gridDim = dim3(2 * p.num_tiles, 1, ksplit);
+    } else if (PAIR) {
         int pairs = cluster_capacity(fn, 2, C::kThreads, C::kSmemBytes, true);
         if (pairs > num_sms() / 2) pairs = num_sms() / 2;
         if (pairs < 1) pairs = 1;
@@ -120,7 +161,7 @@ lowbit_status ext_launch(const ExtProblem& e, const ExtBuffers& b, int rows, int
         attrs[na].id = cudaLaunchAttributeClusterDimension;
         attrs[na].val.clusterDim.x = PAIR ? 2 : 1;
         attrs[na].val.clusterDim.y = 1;
-        attrs[na].val.clusterDim.z = PAIR ? 1 : ksplit;
+        attrs[na].val.clusterDim.z = ksplit;
         ++na;
     }
     cfg.blockDim = dim3(C::kThreads, 1, 1);

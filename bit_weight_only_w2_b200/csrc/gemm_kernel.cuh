@@ -153,7 +153,7 @@ struct Cfg {
         for (int ks = 2; ks <= 8; ++ks) m = recv_bytes(ks) > m ? recv_bytes(ks) : m;
         return m;
     }
-    static_assert(PAIR || max_recv_bytes() <= kXStages * kXStageBytes, "split-K receive buffer");
+    static_assert((PAIR && EXT == kExtNone) || max_recv_bytes() <= kXStages * kXStageBytes, "split-K receive buffer");
     static constexpr uint32_t kIdesc = idesc_f16_f32(PAIR ? 2 * kBlockN : kBlockN, BT);
     // Slot columns: a block of them is what fits one X stage as 128 rows of the weight side; P's box
     // of a block is one or two 64-wide halves.
@@ -342,10 +342,15 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
     // the issuer's X barrier, its dequant and epilogue warps arrive on the issuer's A-ready and
     // accumulator-free barriers, and the issuer's commits arrive on the empty / ready barriers of
     // both CTAs (same offsets).
-    const uint32_t pair_rank = PAIR ? cluster_ctarank() : 0u;
+    // (The variants also split K over clusters of CTA pairs: ranks 2z and 2z + 1 are slice z's pair.)
+    constexpr bool kPairSplit = PAIR && EXT != kExtNone;
+    const uint32_t ctarank = PAIR ? cluster_ctarank() : 0u;
+    const uint32_t pair_rank = kPairSplit ? ctarank & 1u : ctarank;
+    const uint32_t lead = kPairSplit ? ctarank & ~1u : 0u;   // cluster rank of the pair's issuer
+    const uint16_t pair_mask = static_cast<uint16_t>(kPairSplit ? 0x3u << lead : 0x3u);
     const bool issuer = pair_rank == 0;
     constexpr int kPairCtas = PAIR ? 2 : 1;
-    auto on_issuer = [&](uint64_t* bar) { return map_shared_rank(smem_u32(bar), 0u); };
+    auto on_issuer = [&](uint64_t* bar) { return map_shared_rank(smem_u32(bar), lead); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < SX; ++i) {
@@ -643,8 +648,8 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                     }
                     issued = true;
                     if (PAIR) {
-                        mma_commit_pair_mc(&xempty[s], 0x3);
-                        mma_commit_pair_mc(&aempty[a], 0x3);
+                        mma_commit_pair_mc(&xempty[s], pair_mask);
+                        mma_commit_pair_mc(&aempty[a], pair_mask);
                     } else {
                         mma_commit(&xempty[s]);
                         mma_commit(&aempty[a]);
@@ -680,8 +685,8 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                                 mma_f16_ss(d_tmem, adesc, bdesc, C::kIdescSlot, 1u);
                         }
                         if (PAIR) {
-                            mma_commit_pair_mc(&xempty[sp], 0x3);
-                            mma_commit_pair_mc(&xempty[ss], 0x3);
+                            mma_commit_pair_mc(&xempty[sp], pair_mask);
+                            mma_commit_pair_mc(&xempty[ss], pair_mask);
                         } else {
                             mma_commit(&xempty[sp]);
                             mma_commit(&xempty[ss]);
@@ -691,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                 }
                 if (!ok) break;
                 if (PAIR)
-                    mma_commit_pair_mc(&accfull[b], 0x3);
+                    mma_commit_pair_mc(&accfull[b], pair_mask);
                 else
                     mma_commit(&accfull[b]);
             }
@@ -961,7 +966,7 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
         // Receive buffer of an owner: [source rank][128 rows][P 16-byte chunks], P = its column
         // count / 4 made odd, so that 32 rows' chunks at one column fall in distinct banks.
         const int ks = p.ksplit;
-        const int rank = static_cast<int>(cluster_ctarank());
+        const int rank = static_cast<int>(kPairSplit ? ctarank >> 1 : cluster_ctarank());
         const int per_rank = ((BT + ks - 1) / ks + 3) / 4 * 4;
         const int chunks = per_rank / 4;
         const int P = chunks | 1;
@@ -992,7 +997,7 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                     const int cl = (col - owner * per_rank) >> 2;
                     const uint32_t off = static_cast<uint32_t>(((rank * kBlockN + row) * P + cl) * 16);
                     if (dcheck(owner < ks && off + 16 <= static_cast<uint32_t>(C::kXStages * C::kXStageBytes), status))
-                        st_shared_cluster_v4(map_shared_rank(recv0 + off, static_cast<uint32_t>(owner)),
+                        st_shared_cluster_v4(map_shared_rank(recv0 + off, static_cast<uint32_t>(kPairSplit ? 2 * owner + pair_rank : owner)),
                                              make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
                                                          __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])));
                 }
@@ -1004,9 +1009,9 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
             const int quarter = warp & 3;
             const int epart = e >> 2;
             const int row = quarter * 32 + lane;
-            const int tile = blockIdx.x;
+            const int tile = tile0;
             const int m0 = (tile / p.n_tiles) * BT;
-            const int n = (tile % p.n_tiles) * p.rows + row;
+            const int n = (tile % p.n_tiles) * n_stride + n_off + row;
             const int cb = rank * per_rank;
             const int cend = min(min(BT, cb + per_rank), p.M - m0);
             const float* fac = reinterpret_cast<const float*>(wring);

@@ -102,3 +102,20 @@ def test_transpose(N, K, bits):
     got = lb.transpose_packed(lb.pack(codes, bits), K, bits)
     assert got.numel() == lb.transposed_words(N, K, bits)
     assert torch.equal(got, lb.pack(wide, bits))
+
+
+@pytest.mark.parametrize("bits,gs", FORMATS)
+@pytest.mark.parametrize("M,L,R,index", [(500, 3, 32, "sorted"), (511, 40, 64, "holes"), (400, 1, 8, None)])
+def test_split_pairs(M, L, R, index, bits, gs):
+    """Sizes that run K slices over clusters of CTA pairs, in both directions."""
+    pr = Problem(M, 3200, 2560, bits, gs, L, R, index)
+    y, p, _ = run_forward(pr)
+    ry, ey, rp, ep = forward_ref(pr)
+    check(p, rp, ep, "p")
+    check(y, ry, ey, "y")
+    pr = Problem(M, 2560, 3200, bits, gs, L, R, index)
+    got = lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args())
+    assert lb.device_status() == 0
+    for (r, e), g in zip(backward_ref(pr, pr.x), got):
+        check(g, r, e, "gradient")
+    assert torch.equal(lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args())[0], got[0])
