@@ -232,88 +232,71 @@ __device__ __forceinline__ uint64_t narrow_mn_desc(uint32_t tile, int k16) {
 // slices over gridDim.y so that a few blocks fill the GPU, and the slices' fp32 partials are added
 // in order by the copy pass that follows. KMAJOR: the adapter's side is [R][red] (A); otherwise
 // [red][R] (B).
+// A block of at most 32 tokens (a decode batch of many adapters) brings so few bytes a stage that its
+// ring is cut into stages of 32 rows and made deeper instead; the MMA's other 96 rows then read
+// whatever follows, which stays in rows of the product that nobody stores. (203 tokens, 64 rank-32
+// adapters of 4096: 12.6 us with four stages of 128 rows.)
+constexpr int kFewTokens = 32;
 template <int RP>
 constexpr int kShrinkStages = RP == 128 ? 3 : 4;
 template <int RP>
-constexpr int kShrinkSmem = 1024 + kShrinkStages<RP> * gather_stage(RP) + 1024;
+constexpr int kShrinkFewStages = RP == 128 ? 4 : RP == 64 ? 6 : 8;
+template <int RP>
+constexpr int kShrinkRing = kShrinkStages<RP> * gather_stage(RP);
+template <int RP>
+constexpr int kShrinkSmem = 1024 + kShrinkRing<RP>;
 
-template <int RP, bool KMAJOR>
-__global__ void __launch_bounds__(kGatherThreads, 2)
-    shrink_kernel(const __nv_bfloat16* __restrict__ in, const __nv_bfloat16* __restrict__ side, int M, int red, int R,
-                  int kslice, const int* __restrict__ perm, const int4* __restrict__ blocks,
-                  float* __restrict__ partial, unsigned* __restrict__ status) {
-    constexpr int S = kShrinkStages<RP>, kStage = gather_stage(RP);
-    constexpr uint32_t kCols = RP < 32 ? 32 : RP;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t bars[2 * S + 1];
-    __shared__ uint32_t tmem_holder;
-    __shared__ int abort_word;
-    __shared__ int tok[kShrinkTokens];
-    const GatherPipe g = {bars, bars + S, bars + 2 * S, &abort_word, status};
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int at = static_cast<int>(blockIdx.x) * kShrinkTokens;
-    const int4 blk = blocks ? blocks[blockIdx.x] : make_int4(0, at, min(kShrinkTokens, M - at), 0);
-    const int count = blk.z;
-    if (count <= 0) return;
-    if (tid < kShrinkTokens) {
-        const int t = blk.y + min(tid, count - 1);
-        tok[tid] = perm ? perm[t] : t;
-    }
-    if (tid == 0) {
-        for (int i = 0; i < S; ++i) {
-            mbar_init(&bars[i], kGatherWarps);
-            mbar_init(&bars[S + i], 1);
-        }
-        mbar_init(g.done, 1);
-        abort_word = 0;
-        fence_mbar_init();
-    }
-    if (warp == kGatherWarps) {
-        tmem_alloc(&tmem_holder, kCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_holder, s0 = smem_u32(smem);
-    const int k_begin = blockIdx.y * kslice, k_end = min(red, k_begin + kslice);
+struct ShrinkArgs {
+    const __nv_bfloat16* in;
+    const __nv_bfloat16* side;
+    int M, red, R, kslice;
+    const int* perm;
+    const int4* blocks;
+    float* partial;
+    unsigned* status;
+};
+
+// The stages of one block: ROWS token rows each, S stages.
+template <int RP, bool KMAJOR, int ROWS, int S>
+__device__ __forceinline__ void shrink_stages(const ShrinkArgs& p, const GatherPipe& g, const int* tok, int count,
+                                              const __nv_bfloat16* wside, uint32_t s0, uint32_t tmem) {
+    constexpr int kXBytes = ROWS * 128, kStage = kXBytes + RP * 128;
+    static_assert((S - 1) * kStage + kWideBytes <= kShrinkRing<RP> && S * kStage <= kShrinkRing<RP>, "ring");
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int k_begin = blockIdx.y * p.kslice, k_end = min(p.red, k_begin + p.kslice);
     const int steps = (k_end - k_begin + 63) / 64;
-    const __nv_bfloat16* wside = side + static_cast<size_t>(blk.x) * R * red;
     if (warp < kGatherWarps) {
         // this thread's copies of a stage: chunk tid % 8 of token rows tid / 8 + 32 i, and its share of
         // the adapter's side
         const int ch = tid & 7, row0 = tid >> 3;
-        const __nv_bfloat16* xrow[4];
+        const __nv_bfloat16* xrow[ROWS / 32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) xrow[i] = in + static_cast<size_t>(tok[row0 + 32 * i]) * red + ch * 8;
+        for (int i = 0; i < ROWS / 32; ++i) xrow[i] = p.in + static_cast<size_t>(tok[row0 + 32 * i]) * p.red + ch * 8;
         auto load = [&](int step) {
             const uint32_t st = s0 + (step % S) * kStage;
             const int k0 = k_begin + step * 64;
             const bool k_ok = k0 + ch * 8 < k_end;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < ROWS / 32; ++i) {
                 // (rows past the block's tokens are not filled: whatever they hold stays in their own
                 // rows of the product, which are not stored)
                 const int row = row0 + 32 * i;
-                if (row < count) cp_async16(st + swizzled(row, ch, 128), k_ok ? xrow[i] + k0 : in, k_ok);
+                if (row < count) cp_async16(st + swizzled(row, ch, 128), k_ok ? xrow[i] + k0 : p.in, k_ok);
             }
-            const uint32_t ws = st + kWideBytes;
+            const uint32_t ws = st + kXBytes;
 #pragma unroll
             for (int i = 0; i < (RP * 8 + 255) / 256; ++i) {
                 const int id = tid + i * 256;
                 if (RP * 8 < 256 && id >= RP * 8) break;
                 if (KMAJOR) {
                     const int row = id >> 3, k = k0 + (id & 7) * 8;
-                    const bool ok = row < R && k < k_end;
-                    cp_async16(ws + swizzled(row, id & 7, 128), wside + (ok ? static_cast<size_t>(row) * red + k : 0), ok);
+                    const bool ok = row < p.R && k < k_end;
+                    cp_async16(ws + swizzled(row, id & 7, 128), wside + (ok ? static_cast<size_t>(row) * p.red + k : 0), ok);
                 } else {
                     const int row = id / (RP / 8), c = id % (RP / 8);
-                    const bool ok = c * 8 < R && k0 + row < k_end;
+                    const bool ok = c * 8 < p.R && k0 + row < k_end;
                     cp_async16(ws + narrow_mn_offset<RP>(row, c),
-                               wside + (ok ? static_cast<size_t>(k0 + row) * R + c * 8 : 0), ok);
+                               wside + (ok ? static_cast<size_t>(k0 + row) * p.R + c * 8 : 0), ok);
                 }
             }
         };
@@ -331,21 +314,67 @@ __global__ void __launch_bounds__(kGatherThreads, 2)
         cp_async_wait<0>();
         if (ok)
             while (published < steps) gather_publish<S>(g, published++);
-    } else if (lane == 0) {
+    } else if ((tid & 31) == 0) {
         constexpr uint32_t idesc = idesc_bf16_f32(128, RP) | (KMAJOR ? 0u : kIdescTransposeB);
         gather_mma<S>(g, s0, kStage, steps, [&](uint32_t st, int k16, uint32_t acc) {
-            const uint32_t ws = st + kWideBytes;
+            const uint32_t ws = st + kXBytes;
             mma_f16_ss(tmem, smem_desc_k_sw128(st + k16 * 32),
                        KMAJOR ? smem_desc_k_sw128(ws + k16 * 32) : narrow_mn_desc<RP>(ws, k16), idesc, acc);
         });
     }
+}
+
+template <int RP, bool KMAJOR>
+__global__ void __launch_bounds__(kGatherThreads, 2) shrink_kernel(const ShrinkArgs p) {
+    constexpr int S = kShrinkStages<RP>, F = kShrinkFewStages<RP>, kBars = S > F ? S : F;
+    constexpr uint32_t kCols = RP < 32 ? 32 : RP;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t bars[2 * kBars + 1];
+    __shared__ uint32_t tmem_holder;
+    __shared__ int abort_word;
+    __shared__ int tok[kShrinkTokens];
+    const GatherPipe g = {bars, bars + kBars, bars + 2 * kBars, &abort_word, p.status};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int at = static_cast<int>(blockIdx.x) * kShrinkTokens;
+    const int4 blk = p.blocks ? p.blocks[blockIdx.x] : make_int4(0, at, min(kShrinkTokens, p.M - at), 0);
+    const int count = blk.z;
+    if (count <= 0) return;
+    if (tid < kShrinkTokens) {
+        const int t = blk.y + min(tid, count - 1);
+        tok[tid] = p.perm ? p.perm[t] : t;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kBars; ++i) {
+            mbar_init(&g.full[i], kGatherWarps);
+            mbar_init(&g.empty[i], 1);
+        }
+        mbar_init(g.done, 1);
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    if (warp == kGatherWarps) {
+        tmem_alloc(&tmem_holder, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_holder, s0 = smem_u32(smem);
+    const __nv_bfloat16* wside = p.side + static_cast<size_t>(blk.x) * p.R * p.red;
+    if (count <= kFewTokens)
+        shrink_stages<RP, KMAJOR, kFewTokens, F>(p, g, tok, count, wside, s0, tmem);
+    else
+        shrink_stages<RP, KMAJOR, kShrinkTokens, S>(p, g, tok, count, wside, s0, tmem);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp < 4 && !*g.abort_flag) {   // warp w reads tensor-memory lanes 32 w .. 32 w + 31: its tokens
+    if (warp < 4 && warp * 32 < count && !*g.abort_flag) {   // warp w reads tensor-memory lanes 32 w ..: its tokens
         const int row = warp * 32 + lane;
-        float* dst = partial + (static_cast<size_t>(blockIdx.y) * M + tok[row]) * RP;
+        float* dst = p.partial + (static_cast<size_t>(blockIdx.y) * p.M + tok[row]) * RP;
 #pragma unroll
         for (int c = 0; c < RP; c += 16) {
             uint32_t v[16];
@@ -863,13 +892,20 @@ lowbit_status shrink_launch(const ExtProblem& e, const ExtBuffers& b, cudaStream
     static std::atomic<uint64_t> devices{0};
     unsigned* status = device_status_address();
     if (!status || !allow_smem(fn, kShrinkSmem<RP>, devices)) return LOWBIT_ERR_CUDA;
+    ShrinkArgs p;
+    p.in = static_cast<const __nv_bfloat16*>(e.in);
+    p.side = static_cast<const __nv_bfloat16*>(e.grad ? e.ad.B : e.ad.A);
+    p.M = static_cast<int>(e.M);
+    p.red = static_cast<int>(e.red);
+    p.R = e.ad.rank;
+    p.kslice = static_cast<int>(w.kslice);
+    p.perm = e.ad.index ? b.at<int>(w.perm) : nullptr;
+    p.blocks = e.ad.index ? b.at<int4>(w.blocks) : nullptr;
+    p.partial = b.at<float>(w.partial);
+    p.status = status;
     const int64_t num_blocks = e.ad.index ? w.num_blocks : (e.M + kShrinkTokens - 1) / kShrinkTokens;
     return launch_pdl(fn, dim3(static_cast<unsigned>(num_blocks), static_cast<unsigned>(w.ksplit), 1), kGatherThreads,
-                      kShrinkSmem<RP>, 1, stream, static_cast<const __nv_bfloat16*>(e.in),
-                      static_cast<const __nv_bfloat16*>(e.grad ? e.ad.B : e.ad.A), static_cast<int>(e.M),
-                      static_cast<int>(e.red), e.ad.rank, static_cast<int>(w.kslice),
-                      e.ad.index ? b.at<int>(w.perm) : nullptr, e.ad.index ? b.at<int4>(w.blocks) : nullptr,
-                      b.at<float>(w.partial), status);
+                      kShrinkSmem<RP>, 1, stream, p);
 }
 
 template <int RP>
