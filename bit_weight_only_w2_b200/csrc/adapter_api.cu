@@ -110,8 +110,12 @@ LOWBIT_API lowbit_status lowbit_transpose(const uint32_t* packed, int64_t N, int
 LOWBIT_API size_t lowbit_adapter_workspace_size(int64_t M, int64_t N, int64_t K, int num, int rank) {
     if (M < 0 || N < 0 || K < 0 || num < 0 || num > kMaxAdapters || rank < 0 || rank > kMaxRank) return 0;
     if (num > 0 && rank == 0) return 0;
-    const size_t f = ext_workspace(M, N, K, num, rank).total, b = ext_workspace(M, K, N, num, rank).total;
-    return f > b ? f : b;
+    // (without an index the product is laid out for one adapter; whichever needs more)
+    size_t most = 0;
+    for (int n : {num, num > 1 ? 1 : num})
+        for (size_t t : {ext_workspace(M, N, K, n, rank).total, ext_workspace(M, K, N, n, rank).total})
+            if (t > most) most = t;
+    return most;
 }
 
 LOWBIT_API lowbit_status lowbit_adapter_gemm(int64_t M, int64_t N, int64_t K, int bits, int group_size, const void* X,
@@ -138,7 +142,7 @@ LOWBIT_API lowbit_status lowbit_adapter_gemm(int64_t M, int64_t N, int64_t K, in
     e.p_out = P;
     e.ck_codes = ck_codes;
     e.ck_exps = ck_exps;
-    ExtBuffers b{ext_workspace(M, N, K, e.ad.num, e.ad.rank), static_cast<uint8_t*>(workspace)};
+    ExtBuffers b{ext_workspace(M, N, K, e.ad.index ? e.ad.num : 1, e.ad.rank), static_cast<uint8_t*>(workspace)};
     if ((st = check_workspace(workspace, workspace_bytes, b.w.total)) != LOWBIT_OK) return st;
     if ((st = check_device()) != LOWBIT_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -219,7 +223,7 @@ LOWBIT_API lowbit_status lowbit_adapter_backward(int64_t M, int64_t N, int64_t K
     e.zeros = zeros;
     e.out = dX;
     e.ad = adapter_set(adapters);
-    ExtBuffers b{ext_workspace(M, K, N, e.ad.num, e.ad.rank), static_cast<uint8_t*>(workspace)};
+    ExtBuffers b{ext_workspace(M, K, N, e.ad.index ? e.ad.num : 1, e.ad.rank), static_cast<uint8_t*>(workspace)};
     if ((st = check_workspace(workspace, workspace_bytes, b.w.total)) != LOWBIT_OK) return st;
     e.p_out = b.at<void>(b.w.p);
     if ((st = check_device()) != LOWBIT_OK) return st;

@@ -46,6 +46,12 @@ __device__ __forceinline__ void cp_async_wait() {
 // One more CTA per token tile lists the distinct adapters of the tile in ascending order (its
 // "slots") from a bitmap, and each token's slot.
 //
+// A tile's slots share products in which other adapters' entries of P are zero, and zero times an
+// infinity or NaN in the weight side would spread to their tokens. So the adapters in use have their
+// weight side looked over here, cut over gridDim.y (it is read by the product soon after, from L2
+// then): a `bad` one is multiplied as zeros with P = NaN, which gives its own tokens NaN and others
+// nothing.
+//
 // Shrink blocks of T = kShrinkTokens: adapter a's tokens [seg[a], seg[a + 1]) get the block numbers
 // seg[a] / T + a + i, i < ceil(count / T), which never collide: the next adapter starts at
 // floor(seg[a + 1] / T) + a + 1, and ceil(count / T) <= floor(seg[a + 1] / T) -
@@ -60,16 +66,28 @@ __device__ __forceinline__ int adapter_of(const int* __restrict__ index, int m, 
     return a >= 0 && a < num ? a : -1;   // anything else: no adapter
 }
 
+__device__ __forceinline__ bool adapter_bad(const int* __restrict__ bad, int a, int num) {
+    int b = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanSlices; ++i) b |= __ldg(bad + static_cast<size_t>(i) * num + a);
+    return b != 0;
+}
+
 __global__ void __launch_bounds__(kPlanThreads)
     plan_kernel(const int* __restrict__ index, int M, int num, int tile_tokens, int slot_pitch, int num_blocks,
-                int* __restrict__ perm, int* __restrict__ seg, int4* __restrict__ blocks,
-                int* __restrict__ tile_slots, int* __restrict__ slot_adapter, int* __restrict__ token_slot) {
+                const uint4* __restrict__ side, int64_t side8, int* __restrict__ perm, int* __restrict__ seg,
+                int4* __restrict__ blocks, int* __restrict__ tile_slots, int* __restrict__ slot_adapter,
+                int* __restrict__ token_slot, int* __restrict__ bad) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (blockIdx.x < static_cast<unsigned>(num)) {
         const int a = blockIdx.x;
         __shared__ int warp_eq[kPlanWarps], warp_lt[kPlanWarps];
+        // this CTA's share of the weight side
+        const uint4* mine8 = side + static_cast<size_t>(a) * side8;
+        const int64_t stride = static_cast<int64_t>(gridDim.y) * kPlanThreads;
+        const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kPlanThreads + threadIdx.x;
         const int per = ((M + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
         const int m0 = min(M, warp * per), m1 = min(M, m0 + per);
         int eq = 0, lt = 0;
@@ -93,6 +111,18 @@ __global__ void __launch_bounds__(kPlanThreads)
             before += w < warp ? warp_eq[w] : 0;
             count += warp_eq[w];
         }
+        bool odd = false;
+        if (count > 0) {
+            auto look = [&](uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; };
+#pragma unroll 8
+            for (int64_t i = i0; i < side8; i += stride) {
+                const uint4 v = ldg_nc_v4(mine8 + i);
+                odd |= look(v.x) | look(v.y) | look(v.z) | look(v.w);
+            }
+        }
+        const int any_odd = __syncthreads_or(odd);
+        if (threadIdx.x == 0) bad[static_cast<size_t>(blockIdx.y) * num + a] = any_odd;
+        if (blockIdx.y > 0) return;
         int at = start + before;
         for (int mb = m0; mb < m1; mb += 32) {
             const int m = mb + lane;
@@ -111,6 +141,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
         return;
     }
+    if (blockIdx.y > 0) return;
     // ---- slots of one tile
     const int tile = blockIdx.x - num;
     __shared__ unsigned bits[kMaxAdapters / 32];
@@ -462,6 +493,7 @@ struct SideArgs {
     const int* index;
     const int* token_slot;
     const int* tile_slots;
+    const int* bad;            // [kPlanSlices][num], nullptr: not looked over
     int tile_log2;
     __nv_bfloat16* pslots;
     long long p_cols;
@@ -506,8 +538,9 @@ __global__ void __launch_bounds__(kConvThreads, 4)
 #pragma unroll 8
             for (int k = 0; k < s.ksplit; ++k) p += part[k * step];
             p = a < 0 ? 0.f : p * s.scaling[a];                  // (no adapter: its partials are not written)
-            prow[tid] = p;
             if (s.p_out && tid < s.rank) s.p_out[static_cast<size_t>(row) * s.rank + tid] = __float2bfloat16_rn(p);
+            if (s.bad && a >= 0 && adapter_bad(s.bad, a, s.num)) p = __int_as_float(0x7FC00000);   // NaN
+            prow[tid] = p;
         }
     }
     uint32_t mx = 0;
@@ -924,14 +957,16 @@ namespace {
 // Tokens per tile and K slices of the product. The time of a launch is modelled as
 //   waves * blocks per slice * t(tile) + the slices' reduction s(tile),
 // a block being 128 of the reduction (slot columns included: as many adapters as a tile's tokens
-// would hold drawn at random), with t and s fitted to B200 sweeps of the plain product over tiles,
-// slices, M = 24 .. 1537 and the text encoder's and square widths (in us: a tile of 32 / 64 / 128 /
-// 256 tokens takes 0.42 / 0.5 / 0.68 / 0.8 per block and 1.5 / 2 / 3 / 7 for a reduction). The
-// model's choice was within 10 % of the best of each sweep; fixed rules on M alone left 30-40 % at
-// M = 100 .. 200 (for example 4096 x 4096 at 203 tokens: 29.8 us unsplit, 21.7 as 128 x 2 slices).
+// would hold drawn at random), with t and s fitted to B200 sweeps over tiles, slices, M = 24 .. 1537
+// and the text encoder's and square widths (in us: a tile of 32 / 64 / 128 / 256 tokens takes 0.42 /
+// 0.5 / 0.68 / 0.82 per block and 1.5 / 2 / 3 / 9 for a reduction, 3 more where two split 64-token
+// tiles share an SM). The model's choice is mostly within 10 % of the best of each sweep; a rule on
+// M alone left 30-40 % at M = 100 .. 200 (4096 x 4096 at 203 tokens: 29.8 us unsplit, 21.1 as 128
+// tokens x 2 slices).
 void choose_tile(int64_t M, int64_t rows, int64_t red, int num, int rank, int* tile, int* split) {
     static constexpr int kTile[4] = {32, 64, 128, 256};
-    static constexpr double kBlockUs[4] = {0.42, 0.5, 0.68, 0.8}, kSplitUs[4] = {1.5, 2.0, 3.0, 7.0};
+    static constexpr double kBlockUs[4] = {0.42, 0.5, 0.68, 0.82}, kSplitUs[4] = {1.5, 2.0, 3.0, 9.0};
+    static constexpr double kSharedUs[4] = {0.0, 3.0, 0.0, 0.0};
     // clusters of ks CTAs, one per SM, that the GPU's processing clusters hold at once
     static constexpr int kClusters[9] = {0, kSmsAssumed, 74, 48, 32, 24, 24, 16, 16};
     double best = 0;
@@ -957,7 +992,8 @@ void choose_tile(int64_t M, int64_t rows, int64_t red, int num, int rank, int* t
                 waves = static_cast<double>((tiles + cap - 1) / cap);
             }
             if (ks > 1 && waves > 1) continue;   // (a split grid is not persistent)
-            const double us = waves * std::ceil(blocks / ks) * t + (ks > 1 ? kSplitUs[i] : 0.0);
+            const double us = waves * std::ceil(blocks / ks) * t + (ks > 1 ? kSplitUs[i] : 0.0) +
+                              (ks > 1 && tiles > cap ? kSharedUs[i] : 0.0);
             if (!*tile || us < best) {
                 best = us;
                 *tile = bt;
@@ -1001,6 +1037,7 @@ ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int ra
         w.tile_slots = take(static_cast<size_t>(w.m_tiles) * 4);
         w.slot_adapter = take(static_cast<size_t>(w.m_tiles) * w.slot_pitch * 4);
         w.token_slot = take(static_cast<size_t>(M) * 4);
+        w.bad = take(static_cast<size_t>(kPlanSlices) * num * 4);
         w.partial = take(static_cast<size_t>(w.ksplit) * M * rp * 4);
         w.pslots = take(static_cast<size_t>(M) * w.p_cols * 2);
         w.p = take(static_cast<size_t>(M) * rank * 2);
@@ -1011,10 +1048,11 @@ ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int ra
 
 lowbit_status launch_plan(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
     const ExtWorkspace& w = b.w;
-    return launch_pdl(plan_kernel, dim3(static_cast<unsigned>(e.ad.num + w.m_tiles), 1, 1), kPlanThreads, 0, 1, stream,
-                      e.ad.index, static_cast<int>(e.M), e.ad.num, w.tile_tokens, static_cast<int>(w.slot_pitch),
-                      static_cast<int>(w.num_blocks), b.at<int>(w.perm), b.at<int>(w.seg), b.at<int4>(w.blocks),
-                      b.at<int>(w.tile_slots), b.at<int>(w.slot_adapter), b.at<int>(w.token_slot));
+    return launch_pdl(plan_kernel, dim3(static_cast<unsigned>(e.ad.num + w.m_tiles), kPlanSlices, 1), kPlanThreads, 0, 1,
+                      stream, e.ad.index, static_cast<int>(e.M), e.ad.num, w.tile_tokens, static_cast<int>(w.slot_pitch),
+                      static_cast<int>(w.num_blocks), static_cast<const uint4*>(e.grad ? e.ad.A : e.ad.B),
+                      e.rows * e.ad.rank / 8, b.at<int>(w.perm), b.at<int>(w.seg), b.at<int4>(w.blocks),
+                      b.at<int>(w.tile_slots), b.at<int>(w.slot_adapter), b.at<int>(w.token_slot), b.at<int>(w.bad));
 }
 
 lowbit_status launch_shrink(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
@@ -1046,6 +1084,7 @@ lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStrea
         s.index = e.ad.index;
         s.token_slot = e.ad.index ? b.at<int>(w.token_slot) : nullptr;
         s.tile_slots = e.ad.index ? b.at<int>(w.tile_slots) : nullptr;
+        s.bad = e.ad.index ? b.at<int>(w.bad) : nullptr;
         while ((1 << s.tile_log2) < w.tile_tokens) ++s.tile_log2;
         s.pslots = b.at<__nv_bfloat16>(w.pslots);
         s.p_cols = w.p_cols;

@@ -292,10 +292,10 @@ size_t lowbit_adapter_workspace_size(int64_t M, int64_t N, int64_t K, int num, i
  *             of X (see lowbit_checkpoint_store), written in the same pass over X
  *   workspace 256-byte aligned, >= lowbit_adapter_workspace_size(M, N, K, num, rank)
  * p is summed in fp32 and rounded to bf16 once; p B^T is added to X W^T in fp32, so Y is rounded
- * once. Tokens of one 256-token tile share tensor-core products in which other adapters' entries of
- * p are zero: an infinity or NaN in one adapter's A, B or scaling can therefore also reach tokens of
- * other adapters (as NaN). Nothing that the call reads may be written by concurrent work. Results do
- * not depend on timing. */
+ * once. An infinity or NaN in one adapter reaches its own tokens only. (More than 16 tokens with an
+ * index: an adapter whose B is not finite throughout gives its tokens NaN in every column.) Nothing
+ * that the call reads may be written by concurrent work, and Wp, scales and zeros not by the kernel
+ * enqueued immediately before the call, as for lowbit_gemm. Results do not depend on timing. */
 lowbit_status lowbit_adapter_gemm(int64_t M, int64_t N, int64_t K, int bits, int group_size, const void* X,
                                   const uint32_t* Wp, const void* scales, const void* zeros,
                                   const lowbit_adapters* adapters, void* Y, void* P, uint8_t* ck_codes,
@@ -314,8 +314,8 @@ lowbit_status lowbit_gemm_dx(int64_t M, int64_t N, int64_t K, int bits, int grou
  *   dX   bf16 [M][K], or NULL if it is not needed
  *   dA   bf16 [L][R][K], dB bf16 [L][N][R]: written in full (zero for an adapter without tokens)
  * all 16-byte aligned. Sums are fp32, in a fixed order; dp is rounded to bf16 once and dA, dB and dX
- * once each. (An infinity or NaN in one adapter reaches dX of others as in the forward; dA and dB
- * are formed from the adapter's own tokens alone.) */
+ * once each. An infinity or NaN in one adapter reaches its own tokens' dX (NaN in every column if its A
+ * is not finite throughout and there is an index) and its own dA and dB only. */
 lowbit_status lowbit_adapter_backward(int64_t M, int64_t N, int64_t K, int bits, int group_size, const void* dY,
                                       const uint32_t* Wt, const void* scales, const void* zeros,
                                       const lowbit_adapters* adapters, const void* X, const uint8_t* ck_codes,

@@ -119,3 +119,214 @@ def test_split_pairs(M, L, R, index, bits, gs):
     for (r, e), g in zip(backward_ref(pr, pr.x), got):
         check(g, r, e, "gradient")
     assert torch.equal(lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args())[0], got[0])
+
+
+@pytest.mark.parametrize("M", [9, 16, 40, 100, 300])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_not_finite_adapters_stay_apart(M, value):
+    """An adapter with an infinity or NaN gives its own tokens non-finite results and changes no other bit."""
+    pr = Problem(M, 512, 264, 2, 64, 4, 16, "random")
+    own = pr.rows() == 1
+    y0, p0, _ = run_forward(pr)
+    g0 = lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args())
+    for name, at in (("b", (1, 100, 3)), ("a", (1, 5, 300)), ("scaling", (1,))):
+        t = getattr(pr, name)
+        kept = t.clone()
+        t[at] = value
+        y, p, _ = run_forward(pr)
+        assert torch.equal(y[~own], y0[~own]) and torch.equal(p[~own], p0[~own])
+        assert (~torch.isfinite(y[own])).any(1).all()
+        dx, da, db = lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args())
+        assert torch.equal(dx[~own], g0[0][~own]) and (~torch.isfinite(dx[own])).any(1).all()
+        for got, want in ((da, g0[1]), (db, g0[2])):
+            assert torch.equal(got[[0, 2, 3]], want[[0, 2, 3]])
+        assert torch.equal(db, g0[2])                    # (dB does not read the adapter at all)
+        setattr(pr, name, kept)
+
+
+@pytest.mark.parametrize("M", [7, 16, 60, 300])
+def test_not_finite_tokens_stay_apart(M):
+    """A token whose input is not finite affects its own row and, in the backward, its adapter's gradients."""
+    pr = Problem(M, 256, 264, 4, 64, 3, 24, "random")
+    y0, p0, _ = run_forward(pr)
+    g0 = lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args())
+    bad = M // 2
+    others = torch.arange(M, device="cuda") != bad
+    a_bad = int(pr.rows()[bad])
+    rest = [l for l in range(3) if l != a_bad]
+    for value in (float("nan"), float("inf")):
+        pr.x[bad, 17] = value
+        y, p, _ = run_forward(pr)
+        assert torch.equal(y[others], y0[others]) and torch.equal(p[others], p0[others])
+        assert not torch.isfinite(y[bad]).all()
+        pr.dy[bad, 3] = value
+        dx, da, db = lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args())
+        assert torch.equal(dx[others], g0[0][others]) and not torch.isfinite(dx[bad]).all()
+        assert torch.equal(da[rest], g0[1][rest]) and torch.equal(db[rest], g0[2][rest])
+
+
+def test_no_adapter_is_the_plain_product():
+    """Tokens without an adapter get what the linear alone gives, to the last bit of a shared tile choice."""
+    for M in (12, 80, 300):
+        pr = Problem(M, 512, 512, 2, 128, 2, 16, "none")
+        y, p, _ = run_forward(pr)
+        assert not p.any()
+        ry, ey, _, _ = forward_ref(pr)
+        check(y, ry, ey, "y")
+        dx, da, db = lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args())
+        assert not da.any() and not db.any()
+        assert torch.equal(dx, lb.gemm_dx(pr.dy, pr.packed_t, *pr.args()))
+
+
+def test_gradients_against_differences():
+    """Directional derivatives of sum(y * dy) by central differences in 64 bits of the reference forward,
+    against the gradients of the kernels along the same directions."""
+    pr = Problem(60, 256, 136, 2, 64, 3, 16, "holes")
+    p = run_forward(pr)[1]
+    pr.p = p
+    dx, da, db = lb.adapter_backward(pr.dy, pr.x, p, pr.packed_t, *pr.args(), *pr.adapter_args())
+    w, rows, dy = pr.weights(), pr.rows(), pr.dy.double()
+
+    def loss(x, a, b):
+        y = x @ w.T
+        for l in range(pr.L):
+            m = (rows == l).nonzero().flatten()
+            y[m] += float(pr.scaling[l]) * (x[m] @ a[l].T) @ b[l].T
+        return (y * dy).sum()
+
+    x, a, b = pr.x.double(), pr.a.double(), pr.b.double()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    for i, (t, grad) in enumerate(((x, dx), (a, da), (b, db))):
+        v = torch.randn(t.shape, generator=g, device="cuda", dtype=torch.float64)
+        args = [x, a, b]
+        h = 2.0 ** -10
+        args[i] = t + h * v
+        up = loss(*args)
+        args[i] = t - h * v
+        slope = (up - loss(*args)) / (2 * h)       # exact: the loss is at most quadratic in each
+        want = (grad.double() * v).sum()
+        # each gradient entry is off by at most its own rounding 2^-8 and the 2^-8 of dp or p behind it
+        assert abs(want - slope) <= 2 * 2.0 ** -8 * (grad.double().abs() * v.abs()).sum() + 1e-9 * slope.abs()
+
+
+def test_streams_devices_and_graphs():
+    """The calls on a side stream, and captured twice into graphs that replay in turn on new inputs."""
+    prs = [Problem(M, 512, 264, 2, 64, 3, 16, "random", seed=i) for i, M in enumerate((10, 90, 300))]
+    want = []
+    for pr in prs:
+        y, p, ck = run_forward(pr)
+        want.append((y, p, *lb.adapter_backward(pr.dy, ck, p, pr.packed_t, *pr.args(), *pr.adapter_args())))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for pr, w in zip(prs, want):
+            y, p, ck = run_forward(pr)
+            got = (y, p, *lb.adapter_backward(pr.dy, ck, p, pr.packed_t, *pr.args(), *pr.adapter_args()))
+            assert all(torch.equal(a, b) for a, b in zip(got, w))
+    torch.cuda.current_stream().wait_stream(side)
+
+    graphs = []
+    for pr in prs:
+        g = torch.cuda.CUDAGraph()
+        out = {}
+        with torch.cuda.graph(g):
+            p = torch.empty(pr.M, pr.R, dtype=torch.bfloat16, device="cuda")
+            ck = lb.checkpoint_empty(pr.M, pr.K, "cuda")
+            y = lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args(), p=p, checkpoint=ck)
+            out["got"] = (y, p, *lb.adapter_backward(pr.dy, ck, p, pr.packed_t, *pr.args(), *pr.adapter_args()))
+        graphs.append((g, out))
+    for turn in range(2):
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for (_, out), w in zip(graphs, want):
+            assert all(torch.equal(a, b) for a, b in zip(out["got"], w))
+        # the same graphs on other values in the same buffers
+        for pr in prs:
+            pr.x.copy_(torch.randn_like(pr.x) if turn == 0 else pr.x)
+            if turn == 0:
+                pr.index.copy_(torch.randint(-1, 3, (pr.M,), device="cuda", dtype=torch.int32))
+        if turn == 0:
+            want = []
+            for pr in prs:
+                y, p, ck = run_forward(pr)
+                want.append((y, p, *lb.adapter_backward(pr.dy, ck, p, pr.packed_t, *pr.args(), *pr.adapter_args())))
+    assert lb.device_status() == 0
+
+
+def test_results_repeat():
+    for M, L, index in ((16, 5, "random"), (203, 64, "random"), (700, 3, "sorted")):
+        pr = Problem(M, 1024, 520, 4, 64, L, 32, index)
+        first = None
+        for _ in range(4):
+            y, p, ck = run_forward(pr)
+            got = (y, p, ck.codes.view(torch.uint8), *lb.adapter_backward(pr.dy, ck, p, pr.packed_t, *pr.args(), *pr.adapter_args()))
+            assert first is None or all(torch.equal(a, b) for a, b in zip(got, first))
+            first = got
+
+
+def test_buffers_given_and_rows_behind():
+    """Outputs in given buffers; memory behind each is left as it was; a workspace of exactly the stated size."""
+    for M in (3, 50, 270):
+        pr = Problem(M, 256, 264, 2, 64, 3, 24, "random")
+        rows = lambda n, k: torch.full((n + 8, k), 7.0, dtype=torch.bfloat16, device="cuda")
+        y, p, dx, db = rows(M, 264), rows(M, 24), rows(M, 256), rows(3 * 264, 24)
+        da = rows(3 * 24, 256)
+        n = lb.adapter_workspace_size(M, 264, 256, 3, 24)
+        ws = torch.full((n + 256,), 9, dtype=torch.uint8, device="cuda")
+        lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args(), out=y[:M], p=p[:M], ws=ws[:n])
+        lb.adapter_backward(pr.dy, pr.x, p[:M], pr.packed_t, *pr.args(), *pr.adapter_args(), dx=dx[:M],
+                            da=da[:72].view(3, 24, 256), db=db[:3 * 264].view(3, 264, 24), ws=ws[:n])
+        assert torch.equal(y[:M], run_forward(pr)[0])
+        for t, m in ((y, M), (p, M), (dx, M), (da, 72), (db, 3 * 264)):
+            assert (t[m:] == 7).all()
+        assert (ws[n:] == 9).all()
+        with pytest.raises(lb.LowbitError):
+            lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args(), ws=ws[:M * 256 * 2])
+
+
+def test_empty_batches():
+    pr = Problem(5, 256, 264, 2, 64, 3, 24, "random")
+    none = lambda k: torch.empty(0, k, dtype=torch.bfloat16, device="cuda")
+    idx = torch.empty(0, dtype=torch.int32, device="cuda")
+    y = lb.adapter_gemm(none(256), pr.packed, *pr.args(), pr.a, pr.b, pr.scaling, idx)
+    assert y.shape == (0, 264)
+    dx, da, db = lb.adapter_backward(none(264), none(256), none(24), pr.packed_t, *pr.args(), pr.a, pr.b, pr.scaling, idx)
+    assert dx.shape == (0, 256) and not da.any() and not db.any()
+    assert lb.gemm_dx(none(264), pr.packed_t, *pr.args()).shape == (0, 256)
+    assert lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args(), need_dx=False)[0] is None
+
+
+def test_injected_failures_reach_the_caller():
+    lib = lb.load()
+    for M in (8, 100):
+        pr = Problem(M, 256, 264, 2, 64, 3, 24, "random")
+        want = run_forward(pr)[0]
+        for what in (1, 2):
+            assert lib.lowbit_test_fail_next(what) == 0
+            with pytest.raises(lb.LowbitError, match="CUDA"):
+                lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args())
+            assert lib.lowbit_test_fail_next(what) == 0
+            with pytest.raises(lb.LowbitError, match="CUDA"):
+                lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args())
+        assert lib.lowbit_test_fail_next(2) == 0
+        with pytest.raises(lb.LowbitError, match="CUDA"):
+            lb.checkpoint_store(pr.x)
+        assert torch.equal(run_forward(pr)[0], want)
+
+
+def test_debug_build():
+    """The same calls on the build with device-side index checks: no check fires, and the same results."""
+    pr = Problem(150, 512, 264, 2, 64, 5, 24, "holes")
+    y, p, ck = run_forward(pr)
+    g = lb.adapter_backward(pr.dy, ck, p, pr.packed_t, *pr.args(), *pr.adapter_args())
+    release = lb._lib
+    try:
+        lb._lib = lb.load_debug()
+        y2, p2, ck2 = run_forward(pr)
+        g2 = lb.adapter_backward(pr.dy, ck2, p2, pr.packed_t, *pr.args(), *pr.adapter_args())
+        assert lb.device_status() == 0
+    finally:
+        lb._lib = release
+    assert torch.equal(y, y2) and torch.equal(p, p2) and all(torch.equal(a, b) for a, b in zip(g, g2))
