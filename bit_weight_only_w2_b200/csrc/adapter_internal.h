@@ -12,7 +12,6 @@ namespace lowbit {
 
 constexpr int kMaxAdapters = 4096;
 constexpr int kMaxRank = 128;
-constexpr int kPlanSlices = 4;      // CTAs per adapter of the plan kernel
 constexpr int kShrinkTokens = 128;  // tokens of one adapter per block of the shrink kernel
 
 // Slot width: the rank rounded up to a power of two >= 16 (one MMA K step).
@@ -48,8 +47,8 @@ struct ExtProblem {
 //   xh       fp16 copy of the input, rows of red64 (red rounded up to 64) elements
 //   rowmul   fp32 per token
 //   and with adapters: perm (tokens sorted by adapter), seg (start of each adapter's tokens, L + 1
-//   entries), blocks (int4 per shrink block), tile_slots, slot_adapter, token_slot, bad (adapters whose
-//   weight side is not finite), partial (fp32 [ksplit][M][Rp]), pslots (bf16 [M][slot columns])
+//   entries), blocks (int4 per shrink block), tile_slots, slot_adapter, slot_side, token_slot, odd_parts and bad (which
+//   adapters' weight sides are not finite), partial (fp32 [ksplit][M][Rp]), pslots (bf16 [M][slot columns])
 //   p        bf16 [M][R] (backward: dp)
 struct ExtWorkspace {
     int64_t red64;
@@ -59,9 +58,10 @@ struct ExtWorkspace {
     int64_t num_blocks;      // shrink blocks, at most
     int ksplit;              // K slices of the shrink kernel
     int64_t kslice;
+    int plan_slices;         // CTAs per adapter of the plan kernel
     int64_t slot_pitch;      // slots of a tile, at most
     int64_t p_cols;          // columns of pslots
-    size_t xh, rowmul, perm, seg, blocks, tile_slots, slot_adapter, token_slot, bad, partial, pslots, p, total;
+    size_t xh, rowmul, perm, seg, blocks, tile_slots, slot_adapter, slot_side, token_slot, odd_parts, bad, partial, pslots, p, total;
 };
 ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int rank);
 

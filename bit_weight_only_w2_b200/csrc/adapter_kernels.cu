@@ -49,8 +49,8 @@ __device__ __forceinline__ void cp_async_wait() {
 // A tile's slots share products in which other adapters' entries of P are zero, and zero times an
 // infinity or NaN in the weight side would spread to their tokens. So the adapters in use have their
 // weight side looked over here, cut over gridDim.y (it is read by the product soon after, from L2
-// then): a `bad` one is multiplied as zeros with P = NaN, which gives its own tokens NaN and others
-// nothing.
+// then); the shrink kernel joins the parts. A `bad` one is multiplied as zeros with P = NaN, which
+// gives its own tokens NaN and others nothing.
 //
 // Shrink blocks of T = kShrinkTokens: adapter a's tokens [seg[a], seg[a + 1]) get the block numbers
 // seg[a] / T + a + i, i < ceil(count / T), which never collide: the next adapter starts at
@@ -66,28 +66,38 @@ __device__ __forceinline__ int adapter_of(const int* __restrict__ index, int m, 
     return a >= 0 && a < num ? a : -1;   // anything else: no adapter
 }
 
-__device__ __forceinline__ bool adapter_bad(const int* __restrict__ bad, int a, int num) {
-    int b = 0;
-#pragma unroll
-    for (int i = 0; i < kPlanSlices; ++i) b |= __ldg(bad + static_cast<size_t>(i) * num + a);
-    return b != 0;
-}
-
 __global__ void __launch_bounds__(kPlanThreads)
     plan_kernel(const int* __restrict__ index, int M, int num, int tile_tokens, int slot_pitch, int num_blocks,
                 const uint4* __restrict__ side, int64_t side8, int* __restrict__ perm, int* __restrict__ seg,
                 int4* __restrict__ blocks, int* __restrict__ tile_slots, int* __restrict__ slot_adapter,
-                int* __restrict__ token_slot, int* __restrict__ bad) {
+                int* __restrict__ token_slot, int* __restrict__ odd_parts) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (blockIdx.x < static_cast<unsigned>(num)) {
         const int a = blockIdx.x;
         __shared__ int warp_eq[kPlanWarps], warp_lt[kPlanWarps];
-        // this CTA's share of the weight side
-        const uint4* mine8 = side + static_cast<size_t>(a) * side8;
-        const int64_t stride = static_cast<int64_t>(gridDim.y) * kPlanThreads;
-        const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kPlanThreads + threadIdx.x;
+        if (blockIdx.y > 0) {
+            // look over this CTA's share of the weight side, if the adapter has tokens at all
+            bool used = false;
+            for (int m = threadIdx.x; m < M; m += kPlanThreads) used |= adapter_of(index, m, num) == a;
+            if (!__syncthreads_or(used)) return;
+            const uint4* mine = side + static_cast<size_t>(a) * side8;
+            const int64_t stride = static_cast<int64_t>(gridDim.y - 1) * kPlanThreads;
+            bool odd = false;
+            auto look = [&](uint32_t w) { odd |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; };
+#pragma unroll 4
+            for (int64_t i = static_cast<int64_t>(blockIdx.y - 1) * kPlanThreads + threadIdx.x; i < side8; i += stride) {
+                const uint4 v = __ldg(mine + i);
+                look(v.x);
+                look(v.y);
+                look(v.z);
+                look(v.w);
+            }
+            const int any = __syncthreads_or(odd);
+            if (threadIdx.x == 0) odd_parts[static_cast<size_t>(blockIdx.y - 1) * num + a] = any;
+            return;
+        }
         const int per = ((M + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
         const int m0 = min(M, warp * per), m1 = min(M, m0 + per);
         int eq = 0, lt = 0;
@@ -111,18 +121,6 @@ __global__ void __launch_bounds__(kPlanThreads)
             before += w < warp ? warp_eq[w] : 0;
             count += warp_eq[w];
         }
-        bool odd = false;
-        if (count > 0) {
-            auto look = [&](uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; };
-#pragma unroll 8
-            for (int64_t i = i0; i < side8; i += stride) {
-                const uint4 v = ldg_nc_v4(mine8 + i);
-                odd |= look(v.x) | look(v.y) | look(v.z) | look(v.w);
-            }
-        }
-        const int any_odd = __syncthreads_or(odd);
-        if (threadIdx.x == 0) bad[static_cast<size_t>(blockIdx.y) * num + a] = any_odd;
-        if (blockIdx.y > 0) return;
         int at = start + before;
         for (int mb = m0; mb < m1; mb += 32) {
             const int m = mb + lane;
@@ -134,7 +132,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         const int first = start / kShrinkTokens + a;
         const int last = a + 1 == num ? num_blocks : (start + count) / kShrinkTokens + a + 1;
         for (int i = threadIdx.x; first + i < last; i += kPlanThreads)
-            blocks[first + i] = make_int4(a, start + i * kShrinkTokens, min(kShrinkTokens, count - i * kShrinkTokens), 0);
+            blocks[first + i] = make_int4(a, start + i * kShrinkTokens, min(kShrinkTokens, count - i * kShrinkTokens), i == 0);
         if (threadIdx.x == 0) {
             seg[a] = start;
             if (a + 1 == num) seg[num] = start + count;
@@ -283,6 +281,9 @@ struct ShrinkArgs {
     int M, red, R, kslice;
     const int* perm;
     const int4* blocks;
+    const int* odd_parts;      // [slices][num] of the plan kernel
+    int slices, num;
+    int* bad;                  // [num]
     float* partial;
     unsigned* status;
 };
@@ -376,6 +377,12 @@ __global__ void __launch_bounds__(kGatherThreads, 2) shrink_kernel(const ShrinkA
     if (tid < kShrinkTokens) {
         const int t = blk.y + min(tid, count - 1);
         tok[tid] = p.perm ? p.perm[t] : t;
+    }
+    if (blk.w && blockIdx.y == 0) {   // the adapter's first block: join the parts of its weight side's look-over
+        int odd = 0;
+        for (int i = tid; i < p.slices; i += kGatherThreads) odd |= p.odd_parts[static_cast<size_t>(i) * p.num + blk.x];
+        odd = __syncthreads_or(odd);
+        if (tid == 0) p.bad[blk.x] = odd;
     }
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
@@ -493,7 +500,10 @@ struct SideArgs {
     const int* index;
     const int* token_slot;
     const int* tile_slots;
-    const int* bad;            // [kPlanSlices][num], nullptr: not looked over
+    const int* bad;            // [num], nullptr: no index, nothing was looked over
+    const int* slot_adapter;   // [token tile][slot_pitch]
+    int* slot_side;            // the same with `num` for a bad adapter, for the product
+    int slot_pitch;
     int tile_log2;
     __nv_bfloat16* pslots;
     long long p_cols;
@@ -539,7 +549,7 @@ __global__ void __launch_bounds__(kConvThreads, 4)
             for (int k = 0; k < s.ksplit; ++k) p += part[k * step];
             p = a < 0 ? 0.f : p * s.scaling[a];                  // (no adapter: its partials are not written)
             if (s.p_out && tid < s.rank) s.p_out[static_cast<size_t>(row) * s.rank + tid] = __float2bfloat16_rn(p);
-            if (s.bad && a >= 0 && adapter_bad(s.bad, a, s.num)) p = __int_as_float(0x7FC00000);   // NaN
+            if (s.bad && a >= 0 && s.bad[a]) p = __int_as_float(0x7FC00000);   // NaN
             prow[tid] = p;
         }
     }
@@ -606,6 +616,13 @@ __global__ void __launch_bounds__(kConvThreads, 4)
     }
     if (tid == 0) rowmul[row] = __int_as_float((127 + e) << 23);   // 2^e
     if (LR) {
+        if (s.bad && (row & ((1 << s.tile_log2) - 1)) == 0) {      // a tile's first row: its slots' weight sides
+            const size_t at = static_cast<size_t>(row >> s.tile_log2) * s.slot_pitch;
+            for (int i = tid; i < cols >> s.rp_log2; i += kConvThreads) {
+                const int a = s.slot_adapter[at + i];
+                s.slot_side[at + i] = s.bad[a] ? s.num : a;
+            }
+        }
         uint4* pd = reinterpret_cast<uint4*>(s.pslots + static_cast<size_t>(row) * s.p_cols);
         for (int c = tid; c < cols / 8; c += kConvThreads) {
             uint4 o = make_uint4(0, 0, 0, 0);
@@ -934,6 +951,10 @@ lowbit_status shrink_launch(const ExtProblem& e, const ExtBuffers& b, cudaStream
     p.kslice = static_cast<int>(w.kslice);
     p.perm = e.ad.index ? b.at<int>(w.perm) : nullptr;
     p.blocks = e.ad.index ? b.at<int4>(w.blocks) : nullptr;
+    p.odd_parts = b.at<int>(w.odd_parts);
+    p.slices = w.plan_slices;
+    p.num = e.ad.num;
+    p.bad = b.at<int>(w.bad);
     p.partial = b.at<float>(w.partial);
     p.status = status;
     const int64_t num_blocks = e.ad.index ? w.num_blocks : (e.M + kShrinkTokens - 1) / kShrinkTokens;
@@ -1036,8 +1057,15 @@ ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int ra
         w.blocks = take(static_cast<size_t>(w.num_blocks) * 16);
         w.tile_slots = take(static_cast<size_t>(w.m_tiles) * 4);
         w.slot_adapter = take(static_cast<size_t>(w.m_tiles) * w.slot_pitch * 4);
+        w.slot_side = take(static_cast<size_t>(w.m_tiles) * w.slot_pitch * 4);
         w.token_slot = take(static_cast<size_t>(M) * 4);
-        w.bad = take(static_cast<size_t>(kPlanSlices) * num * 4);
+        // CTAs per adapter of the plan kernel: about four per SM in all, 32 KB of the weight side each
+        const int64_t parts = (rows * rank / 8 + 2047) / 2048;
+        w.plan_slices = static_cast<int>(4 * kSmsAssumed / num < parts ? 4 * kSmsAssumed / num : parts);
+        if (w.plan_slices > 64) w.plan_slices = 64;
+        if (w.plan_slices < 1) w.plan_slices = 1;
+        w.odd_parts = take(static_cast<size_t>(w.plan_slices) * num * 4);
+        w.bad = take(static_cast<size_t>(num) * 4);
         w.partial = take(static_cast<size_t>(w.ksplit) * M * rp * 4);
         w.pslots = take(static_cast<size_t>(M) * w.p_cols * 2);
         w.p = take(static_cast<size_t>(M) * rank * 2);
@@ -1048,11 +1076,11 @@ ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int ra
 
 lowbit_status launch_plan(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
     const ExtWorkspace& w = b.w;
-    return launch_pdl(plan_kernel, dim3(static_cast<unsigned>(e.ad.num + w.m_tiles), kPlanSlices, 1), kPlanThreads, 0, 1,
+    return launch_pdl(plan_kernel, dim3(static_cast<unsigned>(e.ad.num + w.m_tiles), 1 + w.plan_slices, 1), kPlanThreads, 0, 1,
                       stream, e.ad.index, static_cast<int>(e.M), e.ad.num, w.tile_tokens, static_cast<int>(w.slot_pitch),
                       static_cast<int>(w.num_blocks), static_cast<const uint4*>(e.grad ? e.ad.A : e.ad.B),
                       e.rows * e.ad.rank / 8, b.at<int>(w.perm), b.at<int>(w.seg), b.at<int4>(w.blocks),
-                      b.at<int>(w.tile_slots), b.at<int>(w.slot_adapter), b.at<int>(w.token_slot), b.at<int>(w.bad));
+                      b.at<int>(w.tile_slots), b.at<int>(w.slot_adapter), b.at<int>(w.token_slot), b.at<int>(w.odd_parts));
 }
 
 lowbit_status launch_shrink(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
@@ -1085,6 +1113,9 @@ lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStrea
         s.token_slot = e.ad.index ? b.at<int>(w.token_slot) : nullptr;
         s.tile_slots = e.ad.index ? b.at<int>(w.tile_slots) : nullptr;
         s.bad = e.ad.index ? b.at<int>(w.bad) : nullptr;
+        s.slot_adapter = b.at<int>(w.slot_adapter);
+        s.slot_side = b.at<int>(w.slot_side);
+        s.slot_pitch = static_cast<int>(w.slot_pitch);
         while ((1 << s.tile_log2) < w.tile_tokens) ++s.tile_log2;
         s.pslots = b.at<__nv_bfloat16>(w.pslots);
         s.p_cols = w.p_cols;

@@ -94,10 +94,7 @@ lowbit_status ext_launch(const ExtProblem& e, const ExtBuffers& b, int rows, int
                                CU_TENSOR_MAP_SWIZZLE_128B);
         p.adapters = true;
         p.tile_slots = e.ad.index ? b.at<int>(w.tile_slots) : nullptr;
-        p.slot_adapter = b.at<int>(w.slot_adapter);
-        p.bad = b.at<int>(w.bad);
-        p.bad_slices = kPlanSlices;
-        p.num = e.ad.num;
+        p.slot_side = b.at<int>(w.slot_side);
         p.slot_pitch = static_cast<int>(w.slot_pitch);
         p.rank_log2 = slot_log2(e.ad.rank);
         // the weight side, (R, N, L) or (K, R, L): ranks past R read as zero

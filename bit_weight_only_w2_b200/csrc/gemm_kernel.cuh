@@ -185,9 +185,7 @@ struct ExtParams : KernelParams {
                              // boxes of 64 rows x `chunk` ranks
     bool adapters;           // any at all
     const int* tile_slots;   // slots of each token tile (nullptr: one, adapter 0)
-    const int* slot_adapter; // [token tile][slot_pitch]
-    const int* bad;          // [bad_slices][num]: an adapter with any set is multiplied as zeros
-    int bad_slices, num;
+    const int* slot_side;    // [token tile][slot_pitch]: adapter, or L (read as zeros) if it is not finite
     int slot_pitch;
     int rank_log2;           // log2 of the slot width Rp
     int chunk_log2;          // log2 of the slot columns per box of the weight side
@@ -510,17 +508,11 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
                         load(&p.map_p, st, 0, xm0, c0 / 64);
                     } else {
                         const int chunk = 1 << p.chunk_log2, chunks = (c1 - c0) >> p.chunk_log2;
-                        const int* slots = p.slot_adapter + static_cast<size_t>(tile / p.n_tiles) * p.slot_pitch;
+                        const int* slots = p.slot_side + static_cast<size_t>(tile / p.n_tiles) * p.slot_pitch;
                         if (issuer) mbar_arrive_expect_tx(&xfull[s], kPairCtas * (chunks << (p.chunk_log2 + 8)));
                         for (int i = 0; i < chunks; ++i) {
                             const int c = c0 + i * chunk, r = c & ((1 << p.rank_log2) - 1);
-                            int a = 0;
-                            if (p.tile_slots) {
-                                a = __ldg(slots + (c >> p.rank_log2));
-                                int b = 0;
-                                for (int j = 0; j < p.bad_slices; ++j) b |= __ldg(p.bad + j * p.num + a);
-                                if (b) a = p.num;   // past the last adapter: the copy fills zeros
-                            }
+                            const int a = p.tile_slots ? __ldg(slots + (c >> p.rank_log2)) : 0;
                             uint8_t* dst = st + i * chunk * 256;
                             if (EXT == kExtAdapter) {
                                 load(&p.map_side, dst, r, n0, a);
