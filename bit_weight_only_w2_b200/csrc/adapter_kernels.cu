@@ -27,14 +27,6 @@ namespace {
 
 constexpr int kSmsAssumed = 148;   // the workspace's size may not depend on the device
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 // ---------------------------------------------------------------------------------------------
 // Plan: the tokens of each adapter, and the slots of each token tile
 // ---------------------------------------------------------------------------------------------
@@ -178,81 +170,92 @@ __global__ void __launch_bounds__(kPlanThreads)
 // Gathered products on tcgen05: the common part of shrink and wgrad
 // ---------------------------------------------------------------------------------------------
 // Both multiply 128 rows by Rp <= 128 columns over a long reduction whose rows are gathered (the
-// tokens of one adapter), and read their wide operand once, so they are bound by that stream. Eight
-// producer warps copy a stage of 64 reduction elements with 16-byte cp.async into the swizzled
-// layouts the MMA reads; a thread makes its own finished copies visible to the tensor cores
-// (proxy fence) before its warp arrives on the stage's barrier. One thread issues the MMAs
-// (bf16 x bf16, fp32 in tensor memory) and frees stages by commits. Warp-level MMAs with ldmatrix
-// were bound by shared-memory reads instead: every warp reads all of the narrow operand again (90 us
-// for the two gradients of 4173 tokens x 9216 at rank 64, floor 18).
-constexpr int kGatherWarps = 8;                              // producers; one more warp issues MMAs
-constexpr int kGatherThreads = 32 * (kGatherWarps + 1);
+// tokens of one adapter), and read their wide operand once, so they are bound by that stream. One
+// warp gathers: each four lanes hold sixteen rows of a stage and ask for them as one box where they
+// follow one another (the tokens of one request do), else four rows a lane by tile::gather4; both
+// arrive swizzled as the MMA reads them. One thread issues the MMAs (bf16 x bf16, fp32 in tensor
+// memory) and frees stages by commits. Slower forms that came before: warp-level MMAs with ldmatrix,
+// bound by shared-memory reads (90 us for the two gradients of 4173 tokens x 9216 at rank 64, floor
+// 18), 16-byte cp.async by eight warps, bound by the instructions that form their addresses (55 us),
+// and gather4 alone, which takes about 80 clocks per 512 bytes (130 us).
 constexpr int kWideBytes = 128 * 128;                        // 128 x 64 bf16
 __host__ __device__ constexpr int gather_stage(int rp) { return kWideBytes + rp * 128; }
 
+__device__ __forceinline__ void* shared_ptr(uint32_t a) {
+    return reinterpret_cast<void*>(__cvta_shared_to_generic(a));
+}
+// Four rows of a 2-D tensor map whose box is one row high, to consecutive rows of shared memory.
+// Rows outside the tensor arrive as zeros.
+__device__ __forceinline__ void tma_gather4(const CUtensorMap* map, uint64_t* bar, uint32_t dst, int x, const int (&r)[4]) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+        : "memory");
+}
+
+// This lane's four rows `r` of a stage: sixteen rows held by four neighbouring lanes come as one box
+// (of `box`, 16 rows high) if they follow one another, else each lane gathers its own (`one`, one row
+// high). `rows` says which, from gather_plan; dst: where this lane's rows go, row_bytes apart.
+__device__ __forceinline__ bool gather_plan(const int (&r)[4], bool valid) {
+    const int lane = threadIdx.x & 31;
+    const int first = __shfl_sync(0xffffffffu, r[0], lane & ~3) + 4 * (lane & 3);
+    const bool run = valid && r[0] == first && r[1] == first + 1 && r[2] == first + 2 && r[3] == first + 3;
+    return ((__ballot_sync(0xffffffffu, run) >> (lane & ~3)) & 0xFu) == 0xFu;
+}
+__device__ __forceinline__ void gather_rows(const CUtensorMap* box, const CUtensorMap* one, uint64_t* bar, uint32_t dst,
+                                            int x, const int (&r)[4], bool as_box) {
+    if (!as_box) tma_gather4(one, bar, dst, x, r);
+    else if ((threadIdx.x & 3) == 0) tma_load_2d(box, bar, shared_ptr(dst), x, r[0]);
+}
+
 struct GatherPipe {
-    uint64_t* full;
-    uint64_t* empty;
+    uint64_t* full;            // a stage's copies have landed (one expecting arrival)
+    uint64_t* empty;           // its products have read it
     uint64_t* done;
     volatile int* abort_flag;
     unsigned* status;
 };
-
-// Producer side of stage `step` being copied: wait for its slot; false if the wait gave up.
-template <int S>
-__device__ __forceinline__ bool gather_wait_slot(const GatherPipe& g, int step) {
-    return __all_sync(0xffffffffu, mbar_wait(&g.empty[step % S], ((step / S) & 1u) ^ 1u, g.abort_flag, g.status));
-}
-// Stage `step`'s copies of this thread are complete (or its stores made): hand it to the MMAs.
-template <int S>
-__device__ __forceinline__ void gather_publish(const GatherPipe& g, int step) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&g.full[step % S]);
-}
-// MMA side: `steps` stages of four K = 16 products each; `issue(stage address, k16, accumulate)`.
-// Returns once they have completed (or a wait gave up).
-template <int S, class Issue>
-__device__ __forceinline__ void gather_mma(const GatherPipe& g, uint32_t s0, int stage_bytes, int steps, Issue issue) {
-    bool issued = false;
-    for (int step = 0; step < steps; ++step) {
-        if (!mbar_wait(&g.full[step % S], (step / S) & 1u, g.abort_flag, g.status)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int k16 = 0; k16 < 4; ++k16) issue(s0 + (step % S) * stage_bytes, k16, step > 0 || k16 > 0 ? 1u : 0u);
-        mma_commit(&g.empty[step % S]);
-        issued = true;
+__device__ __forceinline__ void gather_init(const GatherPipe& g, int stages, int readers) {
+    for (int i = 0; i < stages; ++i) {
+        mbar_init(&g.full[i], 1);
+        mbar_init(&g.empty[i], readers);
     }
-    if (issued) {   // (also after a wait that gave up: tensor memory may not be freed under an MMA)
-        mma_commit(g.done);
+    mbar_init(g.done, 1);
+    *g.abort_flag = 0;
+}
+// Ends the issuing thread's products: no MMA may be in flight when tensor memory is freed, whatever
+// ended its loop.
+__device__ __forceinline__ void gather_drain_mma(const GatherPipe& g) {
+    mma_commit(g.done);
+    const long long t0 = clock64();
+    while (!mbar_try_wait(g.done, 0)) {
+        if (clock64() - t0 > kWaitLimitCycles) {
+            atomicOr(g.status, kDevErrTimeout);
+            *g.abort_flag = 1;
+            break;
+        }
+    }
+}
+// Waits (bounded) for the copies of the stages [from, to) still in flight before the CTA may exit.
+template <int S>
+__device__ __forceinline__ void gather_drain_copies(const GatherPipe& g, int from, int to) {
+    for (int i = from; i < to; ++i) {
         const long long t0 = clock64();
-        while (!mbar_try_wait(g.done, 0)) {
-            if (clock64() - t0 > kWaitLimitCycles) {
-                atomicOr(g.status, kDevErrTimeout);
-                *g.abort_flag = 1;
-                break;
-            }
+        while (!mbar_try_wait(&g.full[i % S], (i / S) & 1u) && clock64() - t0 < kWaitLimitCycles) {
         }
     }
 }
 
-// 16-byte chunk `ch` of row `row` in a tile whose rows are `rb` bytes, swizzled over that width.
-__device__ __forceinline__ uint32_t swizzled(int row, int ch, int rb) {
-    const int x = rb == 128 ? row & 7 : rb == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
-    return static_cast<uint32_t>(row * rb + ((ch ^ x) << 4));
-}
 // The narrow operand as MN-major [64 reduction rows][Rp]: rows of up to 128 bytes; Rp = 128 is two
-// such tiles of 64 columns, 8 KB apart. Chunk `ch` of the Rp / 8 of a row.
-template <int RP>
-__device__ __forceinline__ uint32_t narrow_mn_offset(int row, int ch) {
-    constexpr int rb = RP < 64 ? RP * 2 : 128;
-    return static_cast<uint32_t>((ch >> 3) * 8192) + swizzled(row, ch & 7, rb);
-}
+// such tiles of 64 columns, 8 KB apart.
 template <int RP>
 __device__ __forceinline__ uint64_t narrow_mn_desc(uint32_t tile, int k16) {
     constexpr int rb = RP < 64 ? RP * 2 : 128;
     return smem_desc_mn(tile + k16 * 16 * rb, rb, 8192);
 }
+template <int RP>
+constexpr int kNarrowCols = RP < 64 ? RP : 64;
 
 // ---------------------------------------------------------------------------------------------
 // Shrink: partial[s][m][0..Rp) = in[m][slice s] * side_a[slice s]^T for the tokens of each block
@@ -263,9 +266,9 @@ __device__ __forceinline__ uint64_t narrow_mn_desc(uint32_t tile, int k16) {
 // [red][R] (B).
 // A block of at most 32 tokens (a decode batch of many adapters) brings so few bytes a stage that its
 // ring is cut into stages of 32 rows and made deeper instead; the MMA's other 96 rows then read
-// whatever follows, which stays in rows of the product that nobody stores. (203 tokens, 64 rank-32
-// adapters of 4096: 12.6 us with four stages of 128 rows.)
+// whatever follows, which stays in rows of the product that nobody stores.
 constexpr int kFewTokens = 32;
+constexpr int kShrinkThreads = 160;   // four warps that store, one of them gathering; one issuing MMAs
 template <int RP>
 constexpr int kShrinkStages = RP == 128 ? 3 : 4;
 template <int RP>
@@ -276,9 +279,10 @@ template <int RP>
 constexpr int kShrinkSmem = 1024 + kShrinkRing<RP>;
 
 struct ShrinkArgs {
-    const __nv_bfloat16* in;
-    const __nv_bfloat16* side;
-    int M, red, R, kslice;
+    CUtensorMap map_in;        // the input as (red, M), boxes of 64 x 16
+    CUtensorMap map_in1;       // the same, boxes of 64 x 1
+    CUtensorMap map_side;      // A as (red, R, L), boxes of 64 x Rp, or B as (R, red, L), boxes of up to 64 x 64
+    int M, red, kslice;
     const int* perm;
     const int4* blocks;
     const int* odd_parts;      // [slices][num] of the plan kernel
@@ -288,76 +292,70 @@ struct ShrinkArgs {
     unsigned* status;
 };
 
-// The stages of one block: ROWS token rows each, S stages.
+// The stages of one block: ROWS token rows each, S stages. The gathering warp is warp 0, the issuing
+// thread the first of warp 4.
 template <int RP, bool KMAJOR, int ROWS, int S>
 __device__ __forceinline__ void shrink_stages(const ShrinkArgs& p, const GatherPipe& g, const int* tok, int count,
-                                              const __nv_bfloat16* wside, uint32_t s0, uint32_t tmem) {
+                                              int adapter, uint32_t s0, uint32_t tmem) {
     constexpr int kXBytes = ROWS * 128, kStage = kXBytes + RP * 128;
     static_assert((S - 1) * kStage + kWideBytes <= kShrinkRing<RP> && S * kStage <= kShrinkRing<RP>, "ring");
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int k_begin = blockIdx.y * p.kslice, k_end = min(p.red, k_begin + p.kslice);
     const int steps = (k_end - k_begin + 63) / 64;
-    if (warp < kGatherWarps) {
-        // this thread's copies of a stage: chunk tid % 8 of token rows tid / 8 + 32 i, and its share of
-        // the adapter's side
-        const int ch = tid & 7, row0 = tid >> 3;
-        const __nv_bfloat16* xrow[ROWS / 32];
+    if (warp == 0) {
+        // this lane's four token rows (past the block's tokens the last one again, or nothing: whatever
+        // those rows hold stays in their own rows of the product, which are not stored)
+        const int groups = (count + 3) / 4;
+        int rows[4] = {tok[4 * lane], tok[4 * lane + 1], tok[4 * lane + 2], tok[4 * lane + 3]};
+        // (rows past the block's tokens may be any: the next ones, to make up a box)
+        const int lead = tok[4 * (lane & ~3)] + 4 * (lane & 3);
 #pragma unroll
-        for (int i = 0; i < ROWS / 32; ++i) xrow[i] = p.in + static_cast<size_t>(tok[row0 + 32 * i]) * p.red + ch * 8;
-        auto load = [&](int step) {
-            const uint32_t st = s0 + (step % S) * kStage;
+        for (int i = 0; i < 4; ++i)
+            if (4 * lane + i >= count) rows[i] = lead + i;
+        const bool as_box = gather_plan(rows, true);
+        const bool asks = ROWS == 128 || lane < ROWS / 4 ? lane < groups || (as_box && (lane & ~3) < groups) : false;
+        const int bytes = __popc(__ballot_sync(0xffffffffu, asks)) * 512 + RP * 128;
+        int step = 0;
+        for (; step < steps; ++step) {
+            const int s = step % S;
+            if (!__all_sync(0xffffffffu, mbar_wait(&g.empty[s], ((step / S) & 1u) ^ 1u, g.abort_flag, g.status))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&g.full[s], bytes);
+            __syncwarp();
+            const uint32_t st = s0 + s * kStage;
             const int k0 = k_begin + step * 64;
-            const bool k_ok = k0 + ch * 8 < k_end;
-#pragma unroll
-            for (int i = 0; i < ROWS / 32; ++i) {
-                // (rows past the block's tokens are not filled: whatever they hold stays in their own
-                // rows of the product, which are not stored)
-                const int row = row0 + 32 * i;
-                if (row < count) cp_async16(st + swizzled(row, ch, 128), k_ok ? xrow[i] + k0 : p.in, k_ok);
-            }
-            const uint32_t ws = st + kXBytes;
-#pragma unroll
-            for (int i = 0; i < (RP * 8 + 255) / 256; ++i) {
-                const int id = tid + i * 256;
-                if (RP * 8 < 256 && id >= RP * 8) break;
+            if (asks) gather_rows(&p.map_in, &p.map_in1, &g.full[s], st + lane * 512, k0, rows, as_box);
+            if (lane == 0) {
+                uint8_t* ws = static_cast<uint8_t*>(shared_ptr(st + kXBytes));
                 if (KMAJOR) {
-                    const int row = id >> 3, k = k0 + (id & 7) * 8;
-                    const bool ok = row < p.R && k < k_end;
-                    cp_async16(ws + swizzled(row, id & 7, 128), wside + (ok ? static_cast<size_t>(row) * p.red + k : 0), ok);
+                    tma_load_3d(&p.map_side, &g.full[s], ws, k0, 0, adapter);
                 } else {
-                    const int row = id / (RP / 8), c = id % (RP / 8);
-                    const bool ok = c * 8 < p.R && k0 + row < k_end;
-                    cp_async16(ws + narrow_mn_offset<RP>(row, c),
-                               wside + (ok ? static_cast<size_t>(k0 + row) * p.R + c * 8 : 0), ok);
+                    tma_load_3d(&p.map_side, &g.full[s], ws, 0, k0, adapter);
+                    if (RP == 128) tma_load_3d(&p.map_side, &g.full[s], ws + 8192, 64, k0, adapter);
                 }
             }
-        };
-        bool ok = true;
-        int published = 0;
-        for (int step = 0; step < steps; ++step) {
-            if (!(ok = gather_wait_slot<S>(g, step))) break;
-            load(step);
-            cp_async_commit();
-            if (step >= S - 2) {
-                cp_async_wait<S - 2>();
-                gather_publish<S>(g, published++);
-            }
         }
-        cp_async_wait<0>();
-        if (ok)
-            while (published < steps) gather_publish<S>(g, published++);
-    } else if ((tid & 31) == 0) {
+        if (step < steps) gather_drain_copies<S>(g, max(0, step - S), step);
+    } else if (threadIdx.x == 128) {
         constexpr uint32_t idesc = idesc_bf16_f32(128, RP) | (KMAJOR ? 0u : kIdescTransposeB);
-        gather_mma<S>(g, s0, kStage, steps, [&](uint32_t st, int k16, uint32_t acc) {
-            const uint32_t ws = st + kXBytes;
-            mma_f16_ss(tmem, smem_desc_k_sw128(st + k16 * 32),
-                       KMAJOR ? smem_desc_k_sw128(ws + k16 * 32) : narrow_mn_desc<RP>(ws, k16), idesc, acc);
-        });
+        int step = 0;
+        for (; step < steps; ++step) {
+            const int s = step % S;
+            if (!mbar_wait(&g.full[s], (step / S) & 1u, g.abort_flag, g.status)) break;
+            tc_fence_after();
+            const uint32_t st = s0 + s * kStage, ws = st + kXBytes;
+#pragma unroll
+            for (int k16 = 0; k16 < 4; ++k16)
+                mma_f16_ss(tmem, smem_desc_k_sw128(st + k16 * 32),
+                           KMAJOR ? smem_desc_k_sw128(ws + k16 * 32) : narrow_mn_desc<RP>(ws, k16), idesc,
+                           step > 0 || k16 > 0 ? 1u : 0u);
+            mma_commit(&g.empty[s]);
+        }
+        if (step > 0) gather_drain_mma(g);
     }
 }
 
 template <int RP, bool KMAJOR>
-__global__ void __launch_bounds__(kGatherThreads, 2) shrink_kernel(const ShrinkArgs p) {
+__global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_constant__ ShrinkArgs p) {
     constexpr int S = kShrinkStages<RP>, F = kShrinkFewStages<RP>, kBars = S > F ? S : F;
     constexpr uint32_t kCols = RP < 32 ? 32 : RP;
     extern __shared__ uint8_t smem_raw[];
@@ -368,6 +366,11 @@ __global__ void __launch_bounds__(kGatherThreads, 2) shrink_kernel(const ShrinkA
     __shared__ int tok[kShrinkTokens];
     const GatherPipe g = {bars, bars + kBars, bars + 2 * kBars, &abort_word, p.status};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 128) {
+        tma_prefetch_desc(&p.map_in);
+        tma_prefetch_desc(&p.map_in1);
+        tma_prefetch_desc(&p.map_side);
+    }
     grid_dependency_wait();
     grid_launch_dependents();
     const int at = static_cast<int>(blockIdx.x) * kShrinkTokens;
@@ -380,20 +383,15 @@ __global__ void __launch_bounds__(kGatherThreads, 2) shrink_kernel(const ShrinkA
     }
     if (blk.w && blockIdx.y == 0) {   // the adapter's first block: join the parts of its weight side's look-over
         int odd = 0;
-        for (int i = tid; i < p.slices; i += kGatherThreads) odd |= p.odd_parts[static_cast<size_t>(i) * p.num + blk.x];
+        for (int i = tid; i < p.slices; i += kShrinkThreads) odd |= p.odd_parts[static_cast<size_t>(i) * p.num + blk.x];
         odd = __syncthreads_or(odd);
         if (tid == 0) p.bad[blk.x] = odd;
     }
     if (tid == 0) {
-        for (int i = 0; i < kBars; ++i) {
-            mbar_init(&g.full[i], kGatherWarps);
-            mbar_init(&g.empty[i], 1);
-        }
-        mbar_init(g.done, 1);
-        abort_word = 0;
+        gather_init(g, kBars, 1);
         fence_mbar_init();
     }
-    if (warp == kGatherWarps) {
+    if (warp == 4) {
         tmem_alloc(&tmem_holder, kCols);
         tmem_relinquish();
     }
@@ -401,11 +399,10 @@ __global__ void __launch_bounds__(kGatherThreads, 2) shrink_kernel(const ShrinkA
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_holder, s0 = smem_u32(smem);
-    const __nv_bfloat16* wside = p.side + static_cast<size_t>(blk.x) * p.R * p.red;
     if (count <= kFewTokens)
-        shrink_stages<RP, KMAJOR, kFewTokens, F>(p, g, tok, count, wside, s0, tmem);
+        shrink_stages<RP, KMAJOR, kFewTokens, F>(p, g, tok, count, blk.x, s0, tmem);
     else
-        shrink_stages<RP, KMAJOR, kShrinkTokens, S>(p, g, tok, count, wside, s0, tmem);
+        shrink_stages<RP, KMAJOR, kShrinkTokens, S>(p, g, tok, count, blk.x, s0, tmem);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -427,7 +424,7 @@ __global__ void __launch_bounds__(kGatherThreads, 2) shrink_kernel(const ShrinkA
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kGatherWarps) {
+    if (warp == 4) {
         tc_fence_after();
         tmem_dealloc(tmem, kCols);
     }
@@ -648,61 +645,60 @@ __global__ void __launch_bounds__(kConvThreads, 4)
 // Adapter gradients: dA_a[r][k] = sum dp[m][r] x[m][k], dB_a[n][r] = sum dy[m][n] p[m][r]
 // ---------------------------------------------------------------------------------------------
 // Both are the same product G^T P over an adapter's tokens, G = x or dy: A = G^T (128 columns of G,
-// MN-major), B = P (MN-major), reduction over the tokens in stages of 64. The tokens are cut over the
-// CTAs of a cluster, whose fp32 tiles are added in rank order through distributed shared memory. x
-// may be the 8-bit copy: a thread widens the codes that it copied itself into the MMA's tile (exactly).
+// MN-major), B = P (MN-major), reduction over the tokens in stages of 64. Persistent CTAs, one per SM,
+// walk tiles of both gradients and all adapters through one deep ring, with two accumulators, so that a
+// tile's start and its stores lie under its neighbours' products.
+// x may be the 8-bit copy: four warps widen a stage's codes into the MMA's tile (exactly).
 struct WgradPart {
-    const void* G;             // bf16 [M][C], or the 8-bit codes
-    const uint8_t* exps;       // the 8-bit copy's exponents, nullptr for bf16
-    const __nv_bfloat16* P;    // [M][R]
-    __nv_bfloat16* out;        // [a][R][C] (transposed) or [a][C][R]
+    const uint8_t* exps;       // the 8-bit copy's exponents, nullptr for a bf16 G
+    __nv_bfloat16* out;        // [a][R][C] (dA) or [a][C][R] (dB)
     int C;
     int tiles;                 // ceil(C / 128)
 };
 struct WgradArgs {
-    WgradPart part[2];         // dA (out transposed), dB
-    int R, M;
+    CUtensorMap map_g[2], map_g1[2];   // G as (C, M): boxes of 64 bf16 or 128 codes x 16 rows, x 1 row
+    CUtensorMap map_p[2], map_p1[2];   // P as (R, M): boxes of up to 64 x 16 rows, x 1 row
+    WgradPart part[2];         // dA, dB
+    int R, M, num;
     const int* perm;
     const int* seg;
     unsigned* status;
 };
-constexpr int kWgradStages = 3;
+constexpr int kWgradThreads = 32 * 10;            // 0 gathers, 1 issues MMAs, 2..5 widen, 6..9 store
+constexpr int kWgradWideners = 4;
+template <int RP>
+constexpr int kWgradStages = RP == 128 ? 5 : RP == 64 ? 6 : 7;
 constexpr int kRawBytes = 64 * 128;               // 64 tokens x 128 codes
 template <int RP>
-constexpr int kWgradSmem = 1024 + kWgradStages * (gather_stage(RP) + kRawBytes);
-
-__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
+constexpr int kWgradSmem = 1024 + kWgradStages<RP> * (gather_stage(RP) + kRawBytes);
 
 template <int RP>
-__global__ void __launch_bounds__(kGatherThreads, RP == 128 ? 1 : 2) wgrad_kernel(const WgradArgs w) {
-    constexpr int S = kWgradStages, kStage = gather_stage(RP);
-    constexpr uint32_t kCols = RP < 32 ? 32 : RP;
-    constexpr int kAccPitch = RP + 4;
-    static_assert(128 * kAccPitch * 4 <= S * (kStage + kRawBytes), "fp32 tile");
+__global__ void __launch_bounds__(kWgradThreads, 1) wgrad_kernel(const __grid_constant__ WgradArgs w) {
+    constexpr int S = kWgradStages<RP>, kStage = gather_stage(RP);
+    constexpr uint32_t kAcc = RP, kCols = 2 * kAcc < 32 ? 32 : 2 * kAcc;
+    static_assert(kWgradSmem<RP> <= 227 * 1024, "shared memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t bars[2 * S + 1];
+    uint8_t* raw = smem + S * kStage;
+    __shared__ uint64_t bars[2 * S + 1], wide[S], accfull[2], accempty[2];
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_word;
     const GatherPipe g = {bars, bars + S, bars + 2 * S, &abort_word, w.status};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < S; ++i) {
-            mbar_init(&bars[i], kGatherWarps);
-            mbar_init(&bars[S + i], 1);
+        gather_init(g, S, 1 + kWgradWideners);
+        for (int i = 0; i < S; ++i) mbar_init(&wide[i], kWgradWideners);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accfull[i], 1);
+            mbar_init(&accempty[i], 4);
+            tma_prefetch_desc(&w.map_g[i]);
+            tma_prefetch_desc(&w.map_g1[i]);
+            tma_prefetch_desc(&w.map_p[i]);
+            tma_prefetch_desc(&w.map_p1[i]);
         }
-        mbar_init(g.done, 1);
-        abort_word = 0;
         fence_mbar_init();
     }
-    if (warp == kGatherWarps) {
+    if (warp == 1) {
         tmem_alloc(&tmem_holder, kCols);
         tmem_relinquish();
     }
@@ -712,189 +708,237 @@ __global__ void __launch_bounds__(kGatherThreads, RP == 128 ? 1 : 2) wgrad_kerne
     const uint32_t tmem = tmem_holder, s0 = smem_u32(smem);
     grid_dependency_wait();
     grid_launch_dependents();
-    const bool first = blockIdx.y < static_cast<unsigned>(w.part[0].tiles);
-    const WgradPart part = first ? w.part[0] : w.part[1];
-    const int c0 = (first ? blockIdx.y : blockIdx.y - w.part[0].tiles) * 128;
-    const int a = blockIdx.z, rank = blockIdx.x, ranks = gridDim.x;
-    const int seg0 = w.seg ? w.seg[a] : 0, count = w.seg ? w.seg[a + 1] - seg0 : a == 0 ? w.M : 0;
-    const int per = ((count + 63) / 64 + ranks - 1) / ranks * 64;
-    const int t_begin = min(count, rank * per), t_end = min(count, t_begin + per);
-    const int steps = (t_end - t_begin + 63) / 64;
-    auto token = [&](int t) { return w.perm ? w.perm[seg0 + t] : t; };
-    const int R = w.R;
-    if (warp < kGatherWarps) {
-        const bool q8 = part.exps != nullptr;
-        uint8_t* raw = smem + S * kStage;
-        // Token ids of this thread's rows a step ahead, so that no copy waits for its row's address:
-        // rows tid / 16 + 16 i of a bf16 G, rows tid / 8 + 32 i (i < 2) of an 8-bit one, and rows
-        // tid / 4 + ... of P (by 4, 8, 16 or 32 lanes a row; at most one row for Rp <= 32)
-        constexpr int kPLanes = RP / 8, kPRows = kPLanes <= 4 ? 1 : kPLanes * 64 / 256;
-        int ids[4], pid[kPRows];
-        auto fetch = [&](int step) {
-            const int t0 = t_begin + step * 64;
+    const int tiles = w.part[0].tiles + w.part[1].tiles;
+    const int64_t items = static_cast<int64_t>(tiles) * w.num, stride = gridDim.x;
+    // Item -> 128 columns of one part for one adapter. Its segment's bounds are the only loads; they are
+    // asked for an item ahead.
+    struct Item {
+        int a, part, c0, seg0, count;
+        __device__ int steps() const { return (count + 63) / 64; }
+    };
+    auto item_of = [&](int64_t i) {
+        Item it = {0, 0, 0, 0, 0};
+        if (i < items) {
+            const int y = static_cast<int>(i % tiles);
+            it.a = static_cast<int>(i / tiles);
+            it.part = y < w.part[0].tiles ? 0 : 1;
+            it.c0 = (it.part ? y - w.part[0].tiles : y) * 128;
+            it.seg0 = w.seg ? w.seg[it.a] : 0;
+            it.count = (w.seg ? w.seg[it.a + 1] : it.a == 0 ? w.M : 0) - it.seg0;
+        }
+        return it;
+    };
+    if (warp == 0) {
+        // ---------------------------------------------------------------- gather
+        // lane -> token rows 4 (lane % 16) .. + 3 of a stage, columns 64 (lane / 16) .. of G
+        const int row = 4 * (lane & 15), half = lane >> 4;
+        auto rows_of = [&](const Item& it, int step, int (&r)[4]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = t0 + (q8 ? (tid >> 3) + 32 * i : (tid >> 4) + 16 * i);
-                ids[i] = (!q8 || i < 2) && t < t_end ? token(t) : -1;
-            }
-#pragma unroll
-            for (int i = 0; i < kPRows; ++i) {
-                const int t = t0 + tid / kPLanes + i * (256 / kPLanes);
-                pid[i] = tid / kPLanes + i * (256 / kPLanes) < 64 && t < t_end ? token(t) : -1;
+                const int t = step * 64 + row + i;
+                r[i] = t >= it.count ? w.M : w.perm ? w.perm[it.seg0 + t] : t;   // (row M: zeros)
             }
         };
-        uint32_t ex[S][2] = {};                       // exponents of the thread's two code chunks, per raw slot
-        auto load = [&](int step, uint32_t (&e)[2]) {
-            const uint32_t st = s0 + (step % S) * kStage;
-            if (!q8) {
-                const __nv_bfloat16* G = static_cast<const __nv_bfloat16*>(part.G);
-                const int ch = tid & 15;
-                const bool c_ok = c0 + ch * 8 < part.C;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool ok = ids[i] >= 0 && c_ok;
-                    const size_t src = ok ? static_cast<size_t>(ids[i]) * part.C + c0 + ch * 8 : 0;
-                    cp_async16(st + (ch >> 3) * 8192 + swizzled((tid >> 4) + 16 * i, ch & 7, 128), G + src, ok);
-                }
-            } else {
-                const uint8_t* G = static_cast<const uint8_t*>(part.G);
-                const int ch = tid & 7;
-                const bool c_ok = c0 + ch * 16 < part.C;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool ok = ids[i] >= 0 && c_ok;
-                    const size_t src = ok ? static_cast<size_t>(ids[i]) * part.C + c0 + ch * 16 : 0;
-                    cp_async16(smem_u32(raw) + (step % S) * kRawBytes + (tid + 256 * i) * 16, G + src, ok);
-                    e[i] = ok ? part.exps[src >> 5] : 0;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kPRows; ++i) {
-                const int row = tid / kPLanes + i * (256 / kPLanes), ch = tid % kPLanes;
-                if (row < 64) {
-                    const bool ok = pid[i] >= 0 && ch * 8 < R;
-                    const size_t src = ok ? static_cast<size_t>(pid[i]) * R + ch * 8 : 0;
-                    cp_async16(st + kWideBytes + narrow_mn_offset<RP>(row, ch), part.P + src, ok);
-                }
-            }
-        };
-        auto widen = [&](int step, const uint32_t (&e)[2]) {
-            uint8_t* st = smem + (step % S) * kStage;
-            const int ch = tid & 7;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint4 c = *reinterpret_cast<const uint4*>(raw + (step % S) * kRawBytes + (tid + 256 * i) * 16);
-                const int row = (tid >> 3) + 32 * i;
-                uint8_t* half = st + (ch >> 2) * 8192;
-                *reinterpret_cast<uint4*>(half + swizzled(row, (2 * ch) & 7, 128)) =
-                    checkpoint_decode8(make_uint2(c.x, c.y), e[i]);
-                *reinterpret_cast<uint4*>(half + swizzled(row, (2 * ch + 1) & 7, 128)) =
-                    checkpoint_decode8(make_uint2(c.z, c.w), e[i]);
-            }
-        };
+        int it = 0, rows[4];
         bool ok = true;
-        fetch(0);
-        // (unrolled by the ring's length, so that the exponents stay in registers)
-        for (int base = 0; ok && base < steps + S - 2; base += S) {
+        Item next = item_of(blockIdx.x);
+        rows_of(next, 0, rows);
+        for (int64_t i = blockIdx.x; ok && i < items; i += stride) {
+            const Item cur = next;
+            next = item_of(i + stride);
+            const int steps = cur.steps();
+            const bool q8 = w.part[cur.part].exps != nullptr;
+            const CUtensorMap *mg = &w.map_g[cur.part], *mg1 = &w.map_g1[cur.part];
+            const CUtensorMap *mp = &w.map_p[cur.part], *mp1 = &w.map_p1[cur.part];
+            for (int step = 0; step < steps; ++step, ++it) {
+                int after[4];
+                if (step + 1 < steps) rows_of(cur, step + 1, after);   // (a stage ahead of its use)
+                else rows_of(next, 0, after);
+                const int s = it % S;
+                const bool as_box = gather_plan(rows, step * 64 + row + 4 <= cur.count);
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&g.empty[s], ((it / S) & 1u) ^ 1u, g.abort_flag, g.status)))) break;
+                if (lane == 0) mbar_arrive_expect_tx(&g.full[s], (q8 ? kRawBytes : kWideBytes) + RP * 128);
+                __syncwarp();
+                const uint32_t st = s0 + s * kStage;
+                if (!q8) gather_rows(mg, mg1, &g.full[s], st + half * 8192 + row * 128, cur.c0 + half * 64, rows, as_box);
+                else if (half == 0) gather_rows(mg, mg1, &g.full[s], smem_u32(raw) + s * kRawBytes + row * 128, cur.c0, rows, as_box);
+                // P: rows of kNarrowCols columns, a second tile of 64 for Rp = 128
+                if (half == 0 || RP == 128)
+                    gather_rows(mp, mp1, &g.full[s], st + kWideBytes + half * 8192 + row * kNarrowCols<RP> * 2, half * 64, rows,
+                                as_box);
 #pragma unroll
-            for (int u = 0; u < S; ++u) {
-                const int step = base + u;
-                if (!ok || step >= steps + S - 2) break;
-                if (step < steps) {
-                    if (!(ok = gather_wait_slot<S>(g, step))) break;
-                    load(step, ex[u]);
-                    fetch(step + 1);
+                for (int j = 0; j < 4; ++j) rows[j] = after[j];
+            }
+            if (steps == 0) rows_of(next, 0, rows);
+        }
+        if (!ok) gather_drain_copies<S>(g, max(0, it - S), it);
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_bf16_f32(128, RP) | kIdescTransposeA | kIdescTransposeB;
+            int it = 0, n = 0;
+            uint32_t wide_phase = 0;                 // bit s: the phase that slot s's widening completes next
+            bool ok = true;
+            Item next = item_of(blockIdx.x);
+            for (int64_t i = blockIdx.x; ok && i < items; i += stride) {
+                const int steps = next.steps();
+                const bool q8 = w.part[next.part].exps != nullptr;
+                next = item_of(i + stride);
+                if (steps == 0) continue;
+                const int b = n & 1;
+                if (!(ok = mbar_wait(&accempty[b], ((n >> 1) & 1u) ^ 1u, g.abort_flag, g.status))) break;
+                tc_fence_after();
+                for (int step = 0; step < steps; ++step, ++it) {
+                    const int s = it % S;
+                    if (!(ok = mbar_wait(&g.full[s], (it / S) & 1u, g.abort_flag, g.status))) break;
+                    if (q8) {
+                        if (!(ok = mbar_wait(&wide[s], (wide_phase >> s) & 1u, g.abort_flag, g.status))) break;
+                        wide_phase ^= 1u << s;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = s0 + s * kStage;
+#pragma unroll
+                    for (int k16 = 0; k16 < 4; ++k16)
+                        mma_f16_ss(tmem + b * kAcc, smem_desc_mn(st + k16 * 2048, 128, 8192),
+                                   narrow_mn_desc<RP>(st + kWideBytes, k16), idesc, step > 0 || k16 > 0 ? 1u : 0u);
+                    mma_commit(&g.empty[s]);
                 }
-                cp_async_commit();
-                if (step >= S - 2) {
-                    cp_async_wait<S - 2>();
-                    if (q8) widen(step - (S - 2), ex[(u + 2) % S]);
-                    gather_publish<S>(g, step - (S - 2));
+                if (!ok) break;
+                mma_commit(&accfull[b]);
+                ++n;
+            }
+            if (it > 0) gather_drain_mma(g);
+        }
+    } else if (warp < 2 + kWgradWideners) {
+        // ---------------------------------------------------------------- widen 8-bit stages
+        // thread -> 16 columns (chunk tid % 8) of token rows tid / 8 + 16 i; row ids come two stages and
+        // exponents one stage ahead
+        const int wt = tid - 64, ch = wt & 7, row0 = wt >> 3;
+        int it = 0;
+        Item next = item_of(blockIdx.x);
+        bool ok = true;
+        for (int64_t i = blockIdx.x; ok && i < items; i += stride) {
+            const Item cur = next;
+            next = item_of(i + stride);
+            const int steps = cur.steps();
+            const WgradPart& part = w.part[cur.part];
+            if (part.exps == nullptr) {
+                // nothing to do but to keep in step with the ring: a warp that fell behind or ran ahead by
+                // two of a slot's fills would take one for the other
+                for (int step = 0; step < steps; ++step, ++it) {
+                    const int s = it % S;
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&g.full[s], (it / S) & 1u, g.abort_flag, g.status)))) break;
+                    if (lane == 0) mbar_arrive(&g.empty[s]);
                 }
+                continue;
+            }
+            const bool c_ok = cur.c0 + ch * 16 < part.C;
+            auto ids_of = [&](int step, int (&id)[4]) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = step * 64 + row0 + 16 * j;
+                    id[j] = t < cur.count && c_ok ? (w.perm ? w.perm[cur.seg0 + t] : t) : -1;
+                }
+            };
+            auto exps_of = [&](const int (&id)[4], uint32_t (&e)[4]) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    e[j] = id[j] >= 0 ? part.exps[static_cast<size_t>(id[j]) * (part.C / 32) + (cur.c0 + ch * 16) / 32] : 0;
+            };
+            int id[4];
+            uint32_t e[4];
+            ids_of(0, id);
+            exps_of(id, e);
+            ids_of(1, id);
+            for (int step = 0; step < steps; ++step, ++it) {
+                const int s = it % S;
+                uint32_t e_next[4];
+                exps_of(id, e_next);
+                ids_of(step + 2, id);
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&g.full[s], (it / S) & 1u, g.abort_flag, g.status)))) break;
+                uint8_t* half = smem + s * kStage + (ch >> 2) * 8192;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = row0 + 16 * j;
+                    const uint4 c = *reinterpret_cast<const uint4*>(raw + s * kRawBytes + row * 128 + ch * 16);
+                    uint8_t* dst = half + row * 128;
+                    *reinterpret_cast<uint4*>(dst + ((((2 * ch) & 7) ^ (row & 7)) << 4)) =
+                        checkpoint_decode8(make_uint2(c.x, c.y), e[j]);
+                    *reinterpret_cast<uint4*>(dst + ((((2 * ch + 1) & 7) ^ (row & 7)) << 4)) =
+                        checkpoint_decode8(make_uint2(c.z, c.w), e[j]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&wide[s]);
+                    mbar_arrive(&g.empty[s]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e[j] = e_next[j];
             }
         }
-        cp_async_wait<0>();
-    } else if (lane == 0) {
-        constexpr uint32_t idesc = idesc_bf16_f32(128, RP) | kIdescTransposeA | kIdescTransposeB;
-        gather_mma<S>(g, s0, kStage, steps, [&](uint32_t st, int k16, uint32_t acc) {
-            mma_f16_ss(tmem, smem_desc_mn(st + k16 * 2048, 128, 8192), narrow_mn_desc<RP>(st + kWideBytes, k16), idesc, acc);
-        });
+    } else {
+        // ---------------------------------------------------------------- stores: lane = column of G
+        const int quarter = warp & 3, R = w.R;
+        int n = 0;
+        Item next = item_of(blockIdx.x);
+        for (int64_t i = blockIdx.x; i < items; i += stride) {
+            const Item it = next;
+            next = item_of(i + stride);
+            const bool some = it.count > 0, first = it.part == 0;
+            __nv_bfloat16* out = w.part[it.part].out;
+            const int C = w.part[it.part].C, c = it.c0 + quarter * 32 + lane, b = n & 1;
+            if (some) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&accfull[b], (n >> 1) & 1u, g.abort_flag, g.status))) break;
+                tc_fence_after();
+            }
+#pragma unroll
+            for (int r0 = 0; r0 < RP; r0 += 16) {
+                if (r0 >= R) break;
+                uint32_t v[16] = {};
+                if (some) {
+                    tmem_ld16(tmem + b * kAcc + (static_cast<uint32_t>(quarter * 32) << 16) + r0, v);
+                    tmem_wait_ld();
+                }
+                uint32_t u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                    u[j] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                if (first) {
+                    // dA [a][R][C]: neighbouring lanes swap halves, so that each stores two columns of one rank
+                    const bool even = (lane & 1) == 0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t other = __shfl_xor_sync(0xffffffffu, u[j], 1);
+                        const uint32_t word = even ? __byte_perm(u[j], other, 0x5410) : __byte_perm(other, u[j], 0x7632);
+                        const int r = r0 + 2 * j + (even ? 0 : 1), ce = c & ~1;
+                        if (r < R && ce < C)
+                            *reinterpret_cast<uint32_t*>(out + (static_cast<size_t>(it.a) * R + r) * C + ce) = word;
+                    }
+                } else if (c < C) {
+                    // dB [a][C][R]: eight ranks a store
+                    uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<size_t>(it.a) * C + c) * R + r0);
+                    dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
+                    if (r0 + 8 < R) dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
+                }
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&accempty[b]);
+                ++n;
+            }
+        }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    // the fp32 tile [128 columns of G][Rp], over the drained ring
-    float* tile = reinterpret_cast<float*>(smem);
-    if (warp < 4) {
-        float* dst = tile + (warp * 32 + lane) * kAccPitch;
-#pragma unroll
-        for (int c = 0; c < RP; c += 16) {
-            uint32_t v[16] = {};
-            if (steps > 0) {
-                tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
-                tmem_wait_ld();
-            }
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == kGatherWarps) {
+    if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kCols);
     }
-    if (ranks > 1) cluster_sync_all();
-    // rank r finishes 128 / ranks of the tile's columns: it adds the ranks' parts into its own tile
-    // (which no other rank reads there), four values a load, then all store from shared memory
-    const int mine = 128 / ranks, cb = rank * mine;
-    if (ranks > 1) {
-        constexpr int kQuads = RP / 4;
-        for (int i = tid; i < mine * kQuads; i += kGatherThreads) {
-            const uint32_t off = static_cast<uint32_t>(((cb + i / kQuads) * kAccPitch + i % kQuads * 4) * 4);
-            float4 v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < ranks) v[k] = ld_shared_cluster_v4(map_shared_rank(s0 + off, k));
-#pragma unroll
-            for (int k = 1; k < 8; ++k)
-                if (k < ranks) {
-                    v[0].x += v[k].x;
-                    v[0].y += v[k].y;
-                    v[0].z += v[k].z;
-                    v[0].w += v[k].w;
-                }
-            *reinterpret_cast<float4*>(smem + off) = v[0];
-        }
-        __syncthreads();
-    }
-    if (first) {   // dA [a][R][C]: neighbouring threads take neighbouring columns
-        const int half_log2 = 31 - __clz(mine / 2);   // 128 / ranks is a power of two
-        for (int i = tid; i < R << half_log2; i += kGatherThreads) {
-            const int c = cb + (i & ((1 << half_log2) - 1)) * 2, r = i >> half_log2;
-            if (c0 + c < part.C)
-                *reinterpret_cast<__nv_bfloat162*>(part.out + (static_cast<size_t>(a) * R + r) * part.C + c0 + c) =
-                    __floats2bfloat162_rn(tile[c * kAccPitch + r], tile[(c + 1) * kAccPitch + r]);
-        }
-    } else {       // dB [a][C][R]
-        for (int i = tid; i < mine * (RP / 8); i += kGatherThreads) {
-            const int c = cb + i / (RP / 8), r = i % (RP / 8) * 8;
-            if (c0 + c < part.C && r < R) {
-                const float* f = tile + c * kAccPitch + r;
-                uint32_t u[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * q], f[2 * q + 1]);
-                    u[q] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-                *reinterpret_cast<uint4*>(part.out + (static_cast<size_t>(a) * part.C + c0 + c) * R + r) =
-                    make_uint4(u[0], u[1], u[2], u[3]);
-            }
-        }
-    }
-    if (ranks > 1) cluster_sync_all();   // the other ranks may still read this CTA's tile
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -935,19 +979,36 @@ bool allow_smem(F fn, int bytes, std::atomic<uint64_t>& devices) {
     return true;
 }
 
+// Map of a [rows][cols] row-major tensor, boxes of `box` columns x `high` rows.
+bool make_map_rows(CUtensorMap* map, CUtensorMapDataType type, int elem, const void* base, int64_t cols, int64_t rows, int box,
+                   int high, CUtensorMapSwizzle swz) {
+    return make_map_2d(map, type, elem, base, cols, rows, static_cast<uint64_t>(cols) * elem, box, high, swz);
+}
+CUtensorMapSwizzle swizzle_of(int bytes) {
+    return bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+}
+
 template <int RP, bool KMAJOR>
 lowbit_status shrink_launch(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
     const ExtWorkspace& w = b.w;
     auto fn = shrink_kernel<RP, KMAJOR>;
     static std::atomic<uint64_t> devices{0};
-    unsigned* status = device_status_address();
-    if (!status || !allow_smem(fn, kShrinkSmem<RP>, devices)) return LOWBIT_ERR_CUDA;
     ShrinkArgs p;
-    p.in = static_cast<const __nv_bfloat16*>(e.in);
-    p.side = static_cast<const __nv_bfloat16*>(e.grad ? e.ad.B : e.ad.A);
+    p.status = device_status_address();
+    if (!p.status || !allow_smem(fn, kShrinkSmem<RP>, devices)) return LOWBIT_ERR_CUDA;
+    const uint64_t in = KMAJOR ? e.red : e.ad.rank, mid = KMAJOR ? e.ad.rank : e.red;
+    const uint64_t dims[3] = {in, mid, static_cast<uint64_t>(e.ad.num)};
+    const uint64_t strides[2] = {in * 2, in * mid * 2};
+    constexpr uint32_t cols = KMAJOR ? 64 : kNarrowCols<RP>;
+    const uint32_t box[3] = {cols, KMAJOR ? RP : 64, 1};
+    const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (!make_map_rows(&p.map_in, bf16, 2, e.in, e.red, e.M, 64, 16, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_rows(&p.map_in1, bf16, 2, e.in, e.red, e.M, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_3d(&p.map_side, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, e.grad ? e.ad.B : e.ad.A, dims, strides, box,
+                     swizzle_of(cols * 2)))
+        return LOWBIT_ERR_CUDA;
     p.M = static_cast<int>(e.M);
     p.red = static_cast<int>(e.red);
-    p.R = e.ad.rank;
     p.kslice = static_cast<int>(w.kslice);
     p.perm = e.ad.index ? b.at<int>(w.perm) : nullptr;
     p.blocks = e.ad.index ? b.at<int4>(w.blocks) : nullptr;
@@ -956,19 +1017,32 @@ lowbit_status shrink_launch(const ExtProblem& e, const ExtBuffers& b, cudaStream
     p.num = e.ad.num;
     p.bad = b.at<int>(w.bad);
     p.partial = b.at<float>(w.partial);
-    p.status = status;
     const int64_t num_blocks = e.ad.index ? w.num_blocks : (e.M + kShrinkTokens - 1) / kShrinkTokens;
-    return launch_pdl(fn, dim3(static_cast<unsigned>(num_blocks), static_cast<unsigned>(w.ksplit), 1), kGatherThreads,
+    return launch_pdl(fn, dim3(static_cast<unsigned>(num_blocks), static_cast<unsigned>(w.ksplit), 1), kShrinkThreads,
                       kShrinkSmem<RP>, 1, stream, p);
 }
 
 template <int RP>
-lowbit_status wgrad_launch(const WgradArgs& args, int ranks, int num, cudaStream_t stream) {
+lowbit_status wgrad_launch(const WgradProblem& g, WgradArgs& a, cudaStream_t stream) {
     auto fn = wgrad_kernel<RP>;
     static std::atomic<uint64_t> devices{0};
     if (!allow_smem(fn, kWgradSmem<RP>, devices)) return LOWBIT_ERR_CUDA;
-    return launch_pdl(fn, dim3(ranks, args.part[0].tiles + args.part[1].tiles, num), kGatherThreads, kWgradSmem<RP>, ranks,
-                      stream, args);
+    constexpr int cols = kNarrowCols<RP>;
+    const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    bool ok = true;
+    for (int high : {16, 1}) {
+        CUtensorMap *mg = high == 1 ? a.map_g1 : a.map_g, *mp = high == 1 ? a.map_p1 : a.map_p;
+        ok = ok &&
+             (g.x ? make_map_rows(&mg[0], bf16, 2, g.x, g.K, g.M, 64, high, CU_TENSOR_MAP_SWIZZLE_128B)
+                  : make_map_rows(&mg[0], u8, 1, g.ck_codes, g.K, g.M, 128, high, CU_TENSOR_MAP_SWIZZLE_NONE)) &&
+             make_map_rows(&mg[1], bf16, 2, g.dy, g.N, g.M, 64, high, CU_TENSOR_MAP_SWIZZLE_128B) &&
+             make_map_rows(&mp[0], bf16, 2, g.dp, g.rank, g.M, cols, high, swizzle_of(cols * 2)) &&
+             make_map_rows(&mp[1], bf16, 2, g.p, g.rank, g.M, cols, high, swizzle_of(cols * 2));
+    }
+    if (!ok) return LOWBIT_ERR_CUDA;
+    const int64_t items = static_cast<int64_t>(a.part[0].tiles + a.part[1].tiles) * g.num;
+    return launch_pdl(fn, dim3(static_cast<unsigned>(items < num_sms() ? items : num_sms()), 1, 1), kWgradThreads,
+                      kWgradSmem<RP>, 1, stream, a);
 }
 
 }  // namespace
@@ -1145,42 +1219,25 @@ lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStrea
 
 lowbit_status launch_wgrad(const WgradProblem& g, const ExtBuffers& b, cudaStream_t stream) {
     WgradArgs a = {};
-    a.part[0].G = g.x ? g.x : static_cast<const void*>(g.ck_codes);
     a.part[0].exps = g.x ? nullptr : g.ck_exps;
-    a.part[0].P = static_cast<const __nv_bfloat16*>(g.dp);
     a.part[0].out = static_cast<__nv_bfloat16*>(g.dA);
     a.part[0].C = static_cast<int>(g.K);
     a.part[0].tiles = static_cast<int>((g.K + 127) / 128);
-    a.part[1].G = g.dy;
-    a.part[1].P = static_cast<const __nv_bfloat16*>(g.p);
     a.part[1].out = static_cast<__nv_bfloat16*>(g.dB);
     a.part[1].C = static_cast<int>(g.N);
     a.part[1].tiles = static_cast<int>((g.N + 127) / 128);
     a.R = g.rank;
     a.M = static_cast<int>(g.M);
+    a.num = g.num;
     a.perm = g.planned ? b.at<int>(b.w.perm) : nullptr;
     a.seg = g.planned ? b.at<int>(b.w.seg) : nullptr;
     a.status = device_status_address();
     if (!a.status) return LOWBIT_ERR_CUDA;
-    // Token slices per tile (a cluster's CTAs): whichever of 1, 2, 4, 8 gives the smallest waves x
-    // (steps per slice + a slice's fixed cost, about four steps, and two more for the reduction), two
-    // CTAs per SM and the tokens taken as evenly shared by the adapters.
-    const int64_t ctas = static_cast<int64_t>(a.part[0].tiles + a.part[1].tiles) * g.num;
-    const int64_t steps = (g.M / g.num + 63) / 64;
-    int ranks = 1;
-    int64_t best = 0;
-    for (int r = 1; r <= 8; r *= 2) {
-        const int64_t cost = (ctas * r + 2 * kSmsAssumed - 1) / (2 * kSmsAssumed) * ((steps + r - 1) / r + (r > 1 ? 6 : 4));
-        if (r == 1 || cost < best) {
-            best = cost;
-            ranks = r;
-        }
-    }
     switch (slot_log2(g.rank)) {
-        case 4: return wgrad_launch<16>(a, ranks, g.num, stream);
-        case 5: return wgrad_launch<32>(a, ranks, g.num, stream);
-        case 6: return wgrad_launch<64>(a, ranks, g.num, stream);
-        default: return wgrad_launch<128>(a, ranks, g.num, stream);
+        case 4: return wgrad_launch<16>(g, a, stream);
+        case 5: return wgrad_launch<32>(g, a, stream);
+        case 6: return wgrad_launch<64>(g, a, stream);
+        default: return wgrad_launch<128>(g, a, stream);
     }
 }
 

@@ -330,3 +330,21 @@ def test_debug_build():
     finally:
         lb._lib = release
     assert torch.equal(y, y2) and torch.equal(p, p2) and all(torch.equal(a, b) for a, b in zip(g, g2))
+
+
+@pytest.mark.parametrize("R", [8, 32, 64, 128])
+@pytest.mark.parametrize("index", ["sorted", "random"])
+def test_gradients_over_many_tiles(R, index):
+    """More tiles than SMs, so that a CTA goes through several, of the 8-bit and the bf16 operand, with long
+    and empty segments; tokens that follow one another and tokens that do not."""
+    pr = Problem(2500, 4096, 5120, 2, 128, 4, R, index)
+    idx = pr.index.clone()
+    idx[idx == 2] = 3                     # an adapter without tokens
+    pr.index = idx
+    for x in (pr.x, lb.checkpoint_store(pr.x)):
+        value = lb.checkpoint_load(x) if isinstance(x, lb.Checkpoint) else x
+        got = lb.adapter_backward(pr.dy, x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args(), need_dx=False)
+        assert lb.device_status() == 0
+        _, (ra, ea), (rb, eb) = backward_ref(pr, value)
+        check(got[1], ra, ea, "da")
+        check(got[2], rb, eb, "db")
