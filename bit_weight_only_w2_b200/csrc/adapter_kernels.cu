@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kConvThreads, 4)
 // Adapter gradients: dA_a[r][k] = sum dp[m][r] x[m][k], dB_a[n][r] = sum dy[m][n] p[m][r]
 // ---------------------------------------------------------------------------------------------
 // Both are the same product G^T P over an adapter's tokens, G = x or dy: A = G^T (128 columns of G,
-// MN-major), B = P (MN-major), reduction over the tokens in stages of 64. Persistent CTAs, one per SM,
+// MN-major), B = P (MN-major), reduction over the tokens in stages of 64. Persistent CTAs
 // walk tiles of both gradients and all adapters through one deep ring, with two accumulators, so that a
 // tile's start and its stores lie under its neighbours' products.
 // x may be the 8-bit copy: four warps widen a stage's codes into the MMA's tile (exactly).
@@ -656,27 +656,30 @@ struct WgradPart {
     int tiles;                 // ceil(C / 128)
 };
 struct WgradArgs {
-    CUtensorMap map_g[2], map_g1[2];   // G as (C, M): boxes of 64 bf16 or 128 codes x 16 rows, x 1 row
-    CUtensorMap map_p[2], map_p1[2];   // P as (R, M): boxes of up to 64 x 16 rows, x 1 row
+    // of dA and dB: G as (C, M), boxes of 64 bf16 or 128 codes, and P as (R, M), boxes of up to 64, by
+    // 64 rows (a whole stage), 16 rows and 1 row
+    CUtensorMap map_g[3][2], map_p[3][2];
     WgradPart part[2];         // dA, dB
     int R, M, num;
     const int* perm;
     const int* seg;
     unsigned* status;
 };
-constexpr int kWgradThreads = 32 * 10;            // 0 gathers, 1 issues MMAs, 2..5 widen, 6..9 store
-constexpr int kWgradWideners = 4;
+constexpr int kWgradWideners = 8;
+constexpr int kWgradThreads = 32 * (6 + kWgradWideners);   // warp 0 gathers, 1 issues MMAs, then widen, 4 store
 template <int RP>
-constexpr int kWgradStages = RP == 128 ? 5 : RP == 64 ? 6 : 7;
+constexpr int kWgradCtas = RP == 128 ? 1 : 2;              // per SM
+template <int RP>
+constexpr int kWgradStages = RP == 128 ? 5 : RP == 16 ? 4 : 3;
 constexpr int kRawBytes = 64 * 128;               // 64 tokens x 128 codes
 template <int RP>
 constexpr int kWgradSmem = 1024 + kWgradStages<RP> * (gather_stage(RP) + kRawBytes);
 
 template <int RP>
-__global__ void __launch_bounds__(kWgradThreads, 1) wgrad_kernel(const __grid_constant__ WgradArgs w) {
+__global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(const __grid_constant__ WgradArgs w) {
     constexpr int S = kWgradStages<RP>, kStage = gather_stage(RP);
     constexpr uint32_t kAcc = RP, kCols = 2 * kAcc < 32 ? 32 : 2 * kAcc;
-    static_assert(kWgradSmem<RP> <= 227 * 1024, "shared memory");
+    static_assert(kWgradCtas<RP> * (kWgradSmem<RP> + 2048) <= 228 * 1024, "shared memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* raw = smem + S * kStage;
@@ -691,10 +694,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1) wgrad_kernel(const __grid_co
         for (int i = 0; i < 2; ++i) {
             mbar_init(&accfull[i], 1);
             mbar_init(&accempty[i], 4);
-            tma_prefetch_desc(&w.map_g[i]);
-            tma_prefetch_desc(&w.map_g1[i]);
-            tma_prefetch_desc(&w.map_p[i]);
-            tma_prefetch_desc(&w.map_p1[i]);
+            tma_prefetch_desc(&w.map_g[0][i]);
+            tma_prefetch_desc(&w.map_p[0][i]);
         }
         fence_mbar_init();
     }
@@ -739,37 +740,66 @@ __global__ void __launch_bounds__(kWgradThreads, 1) wgrad_kernel(const __grid_co
                 r[i] = t >= it.count ? w.M : w.perm ? w.perm[it.seg0 + t] : t;   // (row M: zeros)
             }
         };
-        int it = 0, rows[4];
+        // the stage whose rows are asked for next, two ahead of the one that is copied
+        int64_t ai = blockIdx.x;
+        int astep = -1;
+        Item aitem = item_of(ai), anext = item_of(ai + stride);
+        auto rows_ahead = [&](int (&r)[4]) {
+            if (++astep >= aitem.steps()) {
+                astep = 0;
+                do {
+                    ai += stride;
+                    aitem = anext;
+                    anext = item_of(ai + stride);
+                } while (ai < items && aitem.steps() == 0);
+            }
+            rows_of(aitem, astep, r);
+        };
+        int it = 0, rows[4], rows1[4];
         bool ok = true;
+        if (aitem.steps() == 0) astep = 0;   // (moves on to the first item with tokens)
+        rows_ahead(rows);
+        rows_ahead(rows1);
         Item next = item_of(blockIdx.x);
-        rows_of(next, 0, rows);
         for (int64_t i = blockIdx.x; ok && i < items; i += stride) {
             const Item cur = next;
             next = item_of(i + stride);
             const int steps = cur.steps();
             const bool q8 = w.part[cur.part].exps != nullptr;
-            const CUtensorMap *mg = &w.map_g[cur.part], *mg1 = &w.map_g1[cur.part];
-            const CUtensorMap *mp = &w.map_p[cur.part], *mp1 = &w.map_p1[cur.part];
             for (int step = 0; step < steps; ++step, ++it) {
-                int after[4];
-                if (step + 1 < steps) rows_of(cur, step + 1, after);   // (a stage ahead of its use)
-                else rows_of(next, 0, after);
+                int rows2[4];
+                rows_ahead(rows2);
                 const int s = it % S;
                 const bool as_box = gather_plan(rows, step * 64 + row + 4 <= cur.count);
+                // whether all 64 rows follow one another: one request for each 64 columns then
+                const int first = __shfl_sync(0xffffffffu, rows[0], 0);
+                const bool as_stage = __all_sync(0xffffffffu, as_box && rows[0] == first + row);
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&g.empty[s], ((it / S) & 1u) ^ 1u, g.abort_flag, g.status)))) break;
                 if (lane == 0) mbar_arrive_expect_tx(&g.full[s], (q8 ? kRawBytes : kWideBytes) + RP * 128);
                 __syncwarp();
-                const uint32_t st = s0 + s * kStage;
-                if (!q8) gather_rows(mg, mg1, &g.full[s], st + half * 8192 + row * 128, cur.c0 + half * 64, rows, as_box);
-                else if (half == 0) gather_rows(mg, mg1, &g.full[s], smem_u32(raw) + s * kRawBytes + row * 128, cur.c0, rows, as_box);
-                // P: rows of kNarrowCols columns, a second tile of 64 for Rp = 128
-                if (half == 0 || RP == 128)
-                    gather_rows(mp, mp1, &g.full[s], st + kWideBytes + half * 8192 + row * kNarrowCols<RP> * 2, half * 64, rows,
-                                as_box);
+                const uint32_t st = s0 + s * kStage, rw = smem_u32(raw) + s * kRawBytes, ps = st + kWideBytes;
+                if (as_stage) {
+                    if ((lane & 15) == 0) {
+                        if (!q8) tma_load_2d(&w.map_g[0][cur.part], &g.full[s], shared_ptr(st + half * 8192), cur.c0 + half * 64, first);
+                        else if (half == 0) tma_load_2d(&w.map_g[0][cur.part], &g.full[s], shared_ptr(rw), cur.c0, first);
+                        if (half == 0 || RP == 128)
+                            tma_load_2d(&w.map_p[0][cur.part], &g.full[s], shared_ptr(ps + half * 8192), half * 64, first);
+                    }
+                } else {
+                    const CUtensorMap *mg = &w.map_g[1][cur.part], *mg1 = &w.map_g[2][cur.part];
+                    if (!q8) gather_rows(mg, mg1, &g.full[s], st + half * 8192 + row * 128, cur.c0 + half * 64, rows, as_box);
+                    else if (half == 0) gather_rows(mg, mg1, &g.full[s], rw + row * 128, cur.c0, rows, as_box);
+                    // P: rows of kNarrowCols columns, a second tile of 64 for Rp = 128
+                    if (half == 0 || RP == 128)
+                        gather_rows(&w.map_p[1][cur.part], &w.map_p[2][cur.part], &g.full[s],
+                                    ps + half * 8192 + row * kNarrowCols<RP> * 2, half * 64, rows, as_box);
+                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) rows[j] = after[j];
+                for (int j = 0; j < 4; ++j) {
+                    rows[j] = rows1[j];
+                    rows1[j] = rows2[j];
+                }
             }
-            if (steps == 0) rows_of(next, 0, rows);
         }
         if (!ok) gather_drain_copies<S>(g, max(0, it - S), it);
     } else if (warp == 1) {
@@ -811,8 +841,9 @@ __global__ void __launch_bounds__(kWgradThreads, 1) wgrad_kernel(const __grid_co
         }
     } else if (warp < 2 + kWgradWideners) {
         // ---------------------------------------------------------------- widen 8-bit stages
-        // thread -> 16 columns (chunk tid % 8) of token rows tid / 8 + 16 i; row ids come two stages and
+        // thread -> 16 columns (chunk tid % 8) of token rows tid / 8 + 32 i; row ids come two stages and
         // exponents one stage ahead
+        constexpr int kRowsOf = 64 * 8 / (32 * kWgradWideners), kStep = 64 / kRowsOf;
         const int wt = tid - 64, ch = wt & 7, row0 = wt >> 3;
         int it = 0;
         Item next = item_of(blockIdx.x);
@@ -833,33 +864,33 @@ __global__ void __launch_bounds__(kWgradThreads, 1) wgrad_kernel(const __grid_co
                 continue;
             }
             const bool c_ok = cur.c0 + ch * 16 < part.C;
-            auto ids_of = [&](int step, int (&id)[4]) {
+            auto ids_of = [&](int step, int (&id)[kRowsOf]) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = step * 64 + row0 + 16 * j;
+                for (int j = 0; j < kRowsOf; ++j) {
+                    const int t = step * 64 + row0 + kStep * j;
                     id[j] = t < cur.count && c_ok ? (w.perm ? w.perm[cur.seg0 + t] : t) : -1;
                 }
             };
-            auto exps_of = [&](const int (&id)[4], uint32_t (&e)[4]) {
+            auto exps_of = [&](const int (&id)[kRowsOf], uint32_t (&e)[kRowsOf]) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < kRowsOf; ++j)
                     e[j] = id[j] >= 0 ? part.exps[static_cast<size_t>(id[j]) * (part.C / 32) + (cur.c0 + ch * 16) / 32] : 0;
             };
-            int id[4];
-            uint32_t e[4];
+            int id[kRowsOf];
+            uint32_t e[kRowsOf];
             ids_of(0, id);
             exps_of(id, e);
             ids_of(1, id);
             for (int step = 0; step < steps; ++step, ++it) {
                 const int s = it % S;
-                uint32_t e_next[4];
+                uint32_t e_next[kRowsOf];
                 exps_of(id, e_next);
                 ids_of(step + 2, id);
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&g.full[s], (it / S) & 1u, g.abort_flag, g.status)))) break;
                 uint8_t* half = smem + s * kStage + (ch >> 2) * 8192;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int row = row0 + 16 * j;
+                for (int j = 0; j < kRowsOf; ++j) {
+                    const int row = row0 + kStep * j;
                     const uint4 c = *reinterpret_cast<const uint4*>(raw + s * kRawBytes + row * 128 + ch * 16);
                     uint8_t* dst = half + row * 128;
                     *reinterpret_cast<uint4*>(dst + ((((2 * ch) & 7) ^ (row & 7)) << 4)) =
@@ -874,7 +905,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) wgrad_kernel(const __grid_co
                     mbar_arrive(&g.empty[s]);
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) e[j] = e_next[j];
+                for (int j = 0; j < kRowsOf; ++j) e[j] = e_next[j];
             }
         }
     } else {
@@ -1030,8 +1061,9 @@ lowbit_status wgrad_launch(const WgradProblem& g, WgradArgs& a, cudaStream_t str
     constexpr int cols = kNarrowCols<RP>;
     const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     bool ok = true;
-    for (int high : {16, 1}) {
-        CUtensorMap *mg = high == 1 ? a.map_g1 : a.map_g, *mp = high == 1 ? a.map_p1 : a.map_p;
+    for (int k = 0; k < 3; ++k) {
+        const int high = k == 0 ? 64 : k == 1 ? 16 : 1;
+        CUtensorMap *mg = a.map_g[k], *mp = a.map_p[k];
         ok = ok &&
              (g.x ? make_map_rows(&mg[0], bf16, 2, g.x, g.K, g.M, 64, high, CU_TENSOR_MAP_SWIZZLE_128B)
                   : make_map_rows(&mg[0], u8, 1, g.ck_codes, g.K, g.M, 128, high, CU_TENSOR_MAP_SWIZZLE_NONE)) &&
@@ -1040,8 +1072,8 @@ lowbit_status wgrad_launch(const WgradProblem& g, WgradArgs& a, cudaStream_t str
              make_map_rows(&mp[1], bf16, 2, g.p, g.rank, g.M, cols, high, swizzle_of(cols * 2));
     }
     if (!ok) return LOWBIT_ERR_CUDA;
-    const int64_t items = static_cast<int64_t>(a.part[0].tiles + a.part[1].tiles) * g.num;
-    return launch_pdl(fn, dim3(static_cast<unsigned>(items < num_sms() ? items : num_sms()), 1, 1), kWgradThreads,
+    const int64_t items = static_cast<int64_t>(a.part[0].tiles + a.part[1].tiles) * g.num, slots = kWgradCtas<RP> * num_sms();
+    return launch_pdl(fn, dim3(static_cast<unsigned>(items < slots ? items : slots), 1, 1), kWgradThreads,
                       kWgradSmem<RP>, 1, stream, a);
 }
 
