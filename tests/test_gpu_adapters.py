@@ -1,5 +1,9 @@
 """Adapters beside the packed linear, their gradients and the 8-bit activation copy on the GPU,
 against 64-bit references with bounds counted from the roundings (tests/_adapters.py)."""
+import subprocess
+import sys
+import threading
+
 import pytest
 import torch
 
@@ -348,3 +352,56 @@ def test_gradients_over_many_tiles(R, index):
         _, (ra, ea), (rb, eb) = backward_ref(pr, value)
         check(got[1], ra, ea, "da")
         check(got[2], rb, eb, "db")
+
+
+def test_two_threads_on_two_streams():
+    """Calls of two host threads on streams of their own at once, each against its own results alone."""
+    prs = [Problem(M, 1024, 776, 2, 64, 5, 32, "random", seed=M) for M in (14, 410)]
+    want, bad = [], []
+    for pr in prs:
+        y, p, ck = run_forward(pr)
+        want.append((y, *lb.adapter_backward(pr.dy, ck, p, pr.packed_t, *pr.args(), *pr.adapter_args())))
+    torch.cuda.synchronize()
+
+    def work(pr, w):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                p = torch.empty(pr.M, pr.R, dtype=torch.bfloat16, device="cuda")
+                ck = lb.checkpoint_empty(pr.M, pr.K, "cuda")
+                y = lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args(), p=p, checkpoint=ck)
+                got = (y, *lb.adapter_backward(pr.dy, ck, p, pr.packed_t, *pr.args(), *pr.adapter_args()))
+                if not all(torch.equal(a, b) for a, b in zip(got, w)):
+                    bad.append(pr.M)
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(prs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and lb.device_status() == 0
+
+
+@pytest.mark.parametrize("M", [12, 300])
+def test_first_call_under_capture(M):
+    """A process whose first calls of these entry points are captured."""
+    code = f"""
+import torch, bit_weight_only_w2_b200 as lb
+from tests._adapters import Problem, forward_ref, check
+pr = Problem({M}, 512, 264, 2, 64, 3, 16, "random")
+p = torch.empty(pr.M, pr.R, dtype=torch.bfloat16, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args(), p=p)
+    dx, da, db = lb.adapter_backward(pr.dy, pr.x, p, pr.packed_t, *pr.args(), *pr.adapter_args())
+g.replay()
+torch.cuda.synchronize()
+ry, ey, rp, ep = forward_ref(pr)
+check(y, ry, ey, "y")
+check(p, rp, ep, "p")
+eager = lb.adapter_backward(pr.dy, pr.x, p, pr.packed_t, *pr.args(), *pr.adapter_args())
+assert all(torch.equal(a, b) for a, b in zip(eager, (dx, da, db)))
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
