@@ -354,6 +354,21 @@ def test_gradients_over_many_tiles(R, index):
         check(got[2], rb, eb, "db")
 
 
+@pytest.mark.parametrize("M,L,index", [(600, 1, None), (2100, 1, "holes"), (2100, 2, "last"), (2100, 3, None),
+                                       (1100, 2, "random")])
+@pytest.mark.parametrize("R", [16, 40, 64, 128])
+def test_gradients_of_many_tokens(M, L, index, R):
+    """Few tiles and many tokens; the same bits every time."""
+    pr = Problem(M, 320, 264, 4, 64, L, R, index)
+    for x in (pr.x, lb.checkpoint_store(pr.x)):
+        value = lb.checkpoint_load(x) if isinstance(x, lb.Checkpoint) else x
+        calls = [lb.adapter_backward(pr.dy, x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args()) for _ in range(3)]
+        assert lb.device_status() == 0
+        for (r, e), got in zip(backward_ref(pr, value), calls[0]):
+            check(got, r, e, "gradient")
+        assert all(torch.equal(a, b) for c in calls[1:] for a, b in zip(c, calls[0]))
+
+
 def test_two_threads_on_two_streams():
     """Calls of two host threads on streams of their own at once, each against its own results alone."""
     prs = [Problem(M, 1024, 776, 2, 64, 5, 32, "random", seed=M) for M in (14, 410)]
