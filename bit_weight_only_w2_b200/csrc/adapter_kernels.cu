@@ -48,6 +48,7 @@ constexpr int kSmsAssumed = 148;   // the workspace's size may not depend on the
 // seg[a] / T + a + i, i < ceil(count / T), which never collide: the next adapter starts at
 // floor(seg[a + 1] / T) + a + 1, and ceil(count / T) <= floor(seg[a + 1] / T) -
 // floor(seg[a] / T) + 1. Numbers in between stay empty (count 0).
+//
 // Without an index every token has adapter 0 and lies where it belongs: no plan is made, and the
 // kernels below are given null pointers for its parts (perm, blocks, seg, token_slot).
 constexpr int kPlanThreads = 512;
@@ -194,9 +195,9 @@ __device__ __forceinline__ void tma_gather4(const CUtensorMap* map, uint64_t* ba
         : "memory");
 }
 
-// This lane's four rows `r` of a stage: sixteen rows held by four neighbouring lanes come as one box
-// (of `box`, 16 rows high) if they follow one another, else each lane gathers its own (`one`, one row
-// high). `rows` says which, from gather_plan; dst: where this lane's rows go, row_bytes apart.
+// This lane's four rows `r` of a stage, to `dst`: sixteen rows held by four neighbouring lanes come as
+// one box (of `box`, 16 rows high) if they follow one another, which gather_plan finds out (`valid`:
+// whether all four rows are in the stage), else each lane gathers its own (`one`, one row high).
 __device__ __forceinline__ bool gather_plan(const int (&r)[4], bool valid) {
     const int lane = threadIdx.x & 31;
     const int first = __shfl_sync(0xffffffffu, r[0], lane & ~3) + 4 * (lane & 3);
@@ -263,7 +264,8 @@ constexpr int kNarrowCols = RP < 64 ? RP : 64;
 // A block is up to 128 tokens of one adapter (the MMA's 128 rows); the reduction is cut into
 // slices over gridDim.y so that a few blocks fill the GPU, and the slices' fp32 partials are added
 // in order by the copy pass that follows. KMAJOR: the adapter's side is [R][red] (A); otherwise
-// [red][R] (B).
+// [red][R] (B). Bound by the stream of the input and, beside it from L2, of the adapter's side, once a
+// block: 22 us cold for 4173 tokens x 9216 at rank 64 (3.7 TB/s of DRAM, 5.4 TB/s with L2).
 // A block of at most 32 tokens (a decode batch of many adapters) brings so few bytes a stage that its
 // ring is cut into stages of 32 rows and made deeper instead; the MMA's other 96 rows then read
 // whatever follows, which stays in rows of the product that nobody stores.
@@ -487,8 +489,10 @@ __global__ void __launch_bounds__(32 * kShrinkSmallWarps)
 // ---------------------------------------------------------------------------------------------
 // One CTA per token row, as the plain GEMM's conversion (the row's power of two 2^e comes from its
 // largest |value|). P is multiplied by 2^-e as well, since the epilogue multiplies the whole sum
-// by 2^e; that is exact in bf16. p itself is rounded to bf16 once, as the MMA's operand and as
-// what the backward pass reads: 2^-9 of the low-rank term at most, like the output's own rounding.
+// by 2^e; that is exact in bf16. p (in the backward dp) itself is rounded to bf16 once, as the MMA's
+// operand and as what the gradients read: 2^-8 of each entry at most, like the output's own rounding.
+// Against 64 bits the gradients of A are then 2.4e-3 off in the norm where one rounding of the result
+// alone gives 1.7e-3; a second bf16 term for the remainder would double the slot columns.
 struct SideArgs {
     const float* partial;      // [ksplit][M][Rp]
     int ksplit;
@@ -645,10 +649,13 @@ __global__ void __launch_bounds__(kConvThreads, 4)
 // Adapter gradients: dA_a[r][k] = sum dp[m][r] x[m][k], dB_a[n][r] = sum dy[m][n] p[m][r]
 // ---------------------------------------------------------------------------------------------
 // Both are the same product G^T P over an adapter's tokens, G = x or dy: A = G^T (128 columns of G,
-// MN-major), B = P (MN-major), reduction over the tokens in stages of 64. Persistent CTAs
-// walk tiles of both gradients and all adapters through one deep ring, with two accumulators, so that a
-// tile's start and its stores lie under its neighbours' products.
-// x may be the 8-bit copy: four warps widen a stage's codes into the MMA's tile (exactly).
+// MN-major), B = P (MN-major), reduction over the tokens in stages of 64. Persistent CTAs walk tiles of
+// both gradients and all adapters through one ring, with two accumulators, so that a tile's start and
+// its stores lie under its neighbours' products. x may be the 8-bit copy: eight warps widen a stage's
+// codes into the MMA's tile (exactly). Bound by the stream of x and dy: beyond a start of some 15 us,
+// 30 us per 151 MB of bf16 (5.0 TB/s, 0.77 of the copy rate; P comes from L2 on top), 50 us cold for
+// three adapters of 1391 tokens x (9216 + 9216) at rank 64 with x in 8 bits. Cutting the tokens of few
+// tiles into slices that meet in a workspace cost 12 us a slice and gained nothing.
 struct WgradPart {
     const uint8_t* exps;       // the 8-bit copy's exponents, nullptr for a bf16 G
     __nv_bfloat16* out;        // [a][R][C] (dA) or [a][C][R] (dB)

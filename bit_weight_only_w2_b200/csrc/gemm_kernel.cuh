@@ -271,7 +271,7 @@ __device__ __forceinline__ void decode_word_b4(uint32_t v, uint16_t s, float cz,
 // time. Binary and ternary weights are again exactly +-s or 0. uint4: q is exact, q - z and the
 // product with s are each rounded to fp16 once (2^-11 relative each, no cancellation behind a
 // rounding), which halves the instructions of an fp32 product per weight; both together stay below
-// the 2^-9 of one bf16 rounding.
+// the 2^-8 of one bf16 rounding.
 template <int BITS>
 __device__ __forceinline__ void decode_half_grad(const uint32_t* words, const uint4* s4, const uint4* z4,
                                                  uint32_t (&out)[32]) {
