@@ -331,15 +331,52 @@ def _check_checkpoint(ck: Checkpoint, M: int, K: int, device, name: str = "check
             raise ValueError(f"{name}.{part}: on {t.device}, expected {device}")
 
 
-# The entry points below run in a few microseconds on the GPU, so their checks come in two forms:
-# one boolean expression over everything that a correct call satisfies (about 2 us), and, only when it
-# does not hold, the checks that name what is wrong. Both accept the same calls.
+# The entry points below run in a few microseconds on the GPU, so their arguments are checked in three
+# forms that accept the same calls: compiled (_marshal.so: checks, allocations and the library call),
+# one boolean expression over everything that a correct call satisfies (where _marshal.so was built
+# for another PyTorch, or is not there), and, only when that does not hold, the checks that name what
+# is wrong.
 _BF16, _F16, _F32, _I32, _U8 = torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8
 _F8 = torch.float8_e4m3fn
 
 
 def _fits(t, dtype, shape, dev: int) -> bool:
     return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+class _Marshalled:
+    """The compiled calls of the loaded library. Each returns None where it leaves the call to Python."""
+
+    def __init__(self, lib):
+        self.lib = lib
+        try:
+            from . import _marshal
+        except ImportError:
+            _marshal = None
+        if _marshal is not None and _marshal.torch_version != torch.__version__.split("+")[0]:
+            _marshal = None
+        size = self._address("adapter_workspace_size")
+        for name in ("adapter_gemm", "gemm_dx", "adapter_backward"):
+            self._set(_marshal, name, size)
+        for name in ("checkpoint_store", "checkpoint_load"):
+            self._set(_marshal, name)
+
+    def _address(self, name: str) -> int:
+        return ctypes.cast(getattr(self.lib, "lowbit_" + name), ctypes.c_void_p).value
+
+    def _set(self, module, name: str, *more) -> None:
+        call = getattr(module, name, None)
+        setattr(self, name, (lambda *args: None) if call is None else functools.partial(call, self._address(name), *more))
+
+
+_marshalled: Optional[_Marshalled] = None
+
+
+def _calls() -> _Marshalled:
+    global _marshalled
+    if _marshalled is None or _marshalled.lib is not _lib:
+        _marshalled = _Marshalled(load())
+    return _marshalled
 
 
 def _raw_stream(dev: int) -> int:
@@ -365,6 +402,11 @@ def _copy_fits(ck, M: int, K: int, dev: int) -> bool:
 
 def checkpoint_store(x: torch.Tensor, out: Optional[Checkpoint] = None) -> Checkpoint:
     """The 8-bit copy of x (bf16 [M][K], K a multiple of 32)."""
+    r = _calls().checkpoint_store(x) if out is None else None
+    if r is not None:
+        if type(r) is int:
+            raise LowbitError(r, "lowbit_checkpoint_store")
+        return Checkpoint(*r)
     if not (x.dim() == 2 and x.dtype is _BF16 and x.is_contiguous() and x.is_cuda):
         _need(x, _BF16, "x")
         _need_cuda(("x", x))
@@ -383,6 +425,11 @@ def checkpoint_store(x: torch.Tensor, out: Optional[Checkpoint] = None) -> Check
 def checkpoint_load(ck: Checkpoint, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The bf16 values an 8-bit copy stands for."""
     codes = ck.codes
+    r = _calls().checkpoint_load(codes, ck.exps, out)
+    if r is not None:
+        if type(r) is int:
+            raise LowbitError(r, "lowbit_checkpoint_load")
+        return r
     if not (codes.dim() == 2 and codes.is_cuda and _copy_fits(ck, *codes.shape, codes.get_device())):
         _need(codes, _F8, "checkpoint.codes")
         _need_cuda(("checkpoint.codes", codes))
@@ -483,6 +530,12 @@ def adapter_gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, ze
     a bf16 [L][R][K], b bf16 [L][N][R], scaling fp32 [L], index int32 [M] (values outside 0..L-1: no
     adapter; None: adapter 0 for every token). For training, pass buffers that the backward reads:
     `p` bf16 [M][R] and, to keep X in 8 bits, `checkpoint` (checkpoint_empty(M, K, device))."""
+    codes, exps = checkpoint if checkpoint is not None else (None, None)
+    r = _calls().adapter_gemm(x, packed, scales, zeros, bits, group_size, a, b, scaling, index, out, p, codes, exps, ws)
+    if r is not None:
+        if type(r) is int:
+            raise LowbitError(r, "lowbit_adapter_gemm")
+        return r
     if not _linear_fits(x, packed, scales, zeros, bits, group_size, False):
         _check_gemm_args(x, packed, scales, zeros, out, bits, group_size)
     M, K = x.shape
@@ -500,7 +553,6 @@ def adapter_gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, ze
     if checkpoint is not None and not _copy_fits(checkpoint, M, K, dev):
         _check_checkpoint(checkpoint, M, K, x.device)
     ad = Adapters(L, R, a.data_ptr(), b.data_ptr(), scaling.data_ptr(), _ptr(index))
-    codes, exps = checkpoint if checkpoint is not None else (None, None)
     with _on_device(dev):
         ws, ws_bytes = _own_workspace(ws, x, M, N, K, L, R)
         _check(load().lowbit_adapter_gemm(M, N, K, bits, group_size, x.data_ptr(), packed.data_ptr(), scales.data_ptr(),
@@ -534,6 +586,11 @@ def _check_grad_args(dy, packed_t, scales, zeros, bits: int, group_size: int):
 def gemm_dx(dy: torch.Tensor, packed_t: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor], bits: int,
             group_size: int, out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dX = dY W, the input gradient of gemm (dy bf16 [M][N], packed_t from transpose_packed)."""
+    r = _calls().gemm_dx(dy, packed_t, scales, zeros, bits, group_size, out, ws)
+    if r is not None:
+        if type(r) is int:
+            raise LowbitError(r, "lowbit_gemm_dx")
+        return r
     if not _linear_fits(dy, packed_t, scales, zeros, bits, group_size, True):
         _check_grad_args(dy, packed_t, scales, zeros, bits, group_size)
     M, N = dy.shape
@@ -560,6 +617,13 @@ def adapter_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint], p: to
 
     x is the forward's input, or the Checkpoint it filled; p what it wrote. need_dx=False skips
     dx (a first layer) and returns None in its place."""
+    xs = (None, x.codes, x.exps) if isinstance(x, Checkpoint) else (x, None, None)
+    r = _calls().adapter_backward(dy, packed_t, scales, zeros, bits, group_size, a, b, scaling, index, *xs, p, dx, da, db,
+                                  need_dx, ws)
+    if r is not None:
+        if type(r) is int:
+            raise LowbitError(r, "lowbit_adapter_backward")
+        return r
     if not _linear_fits(dy, packed_t, scales, zeros, bits, group_size, True):
         _check_grad_args(dy, packed_t, scales, zeros, bits, group_size)
     M, N = dy.shape

@@ -3,7 +3,8 @@
     python -m bit_weight_only_w2_b200.build [--force] [--debug]
 
 Objects go to ``_build/`` at the repository root; the shared library is written next to this
-file so the Python binding (and a copy of the tree on another machine) finds it. ``--debug``
+file so the Python binding (and a copy of the tree on another machine) finds it, and beside it
+_marshal.so, which marshals the arguments of the binding's short calls (g++). ``--debug``
 builds liblowbit_debug.so instead: the same sources with device-side index checks
 (LOWBIT_DEBUG_CHECKS), objects in ``_build/debug/``.
 """
@@ -21,6 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liblowbit.so")
 DEBUG_LIB = os.path.join(PKG, "liblowbit_debug.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL_LIB = os.path.join(PKG, "_marshal.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -78,7 +81,33 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fvisibility=hidden"]
         subprocess.check_call(cmd)
         os.replace(tmp, lib)
+    if not debug:
+        build_marshal(force)
     return lib
+
+
+def build_marshal(force: bool = False) -> str:
+    """Build _marshal.so against the installed PyTorch; the binding uses it with that version only."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    if not force and not _stale(MARSHAL_LIB, [MARSHAL_SRC, os.path.join(INCLUDE, "lowbit.h"), torch.version.__file__]):
+        return MARSHAL_LIB
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    headers = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = MARSHAL_LIB + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+           *(f"-isystem{h}" for h in headers), MARSHAL_SRC,
+           "-o", tmp, f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL_LIB)
+    return MARSHAL_LIB
 
 
 if __name__ == "__main__":
