@@ -420,3 +420,38 @@ print("ok")
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values in x, dx and the 8-bit copy, and 2^32 bytes in each: rows at both ends and
+    across the borders, and the gradients of an adapter whose tokens are those rows."""
+    M, K, N = 234057, 9216, 136
+    pr = Problem(48, K, N, 2, 64, 2, 16)
+    border = (1 << 31) // K
+    rows = torch.cat([torch.arange(0, 8), torch.arange(border // 2 - 4, border // 2 + 4),
+                      torch.arange(border - 8, border + 16), torch.arange(M - 8, M)]).cuda()
+    assert len(rows) == pr.M and M * K > 1 << 31
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").fill_(0.5)
+    dy = torch.full((M, N), 0.01, dtype=torch.bfloat16, device="cuda")
+    index = torch.zeros(M, dtype=torch.int32, device="cuda")
+    x[rows], dy[rows], index[rows] = pr.x, pr.dy, 1
+    p, ck = torch.empty(M, 16, dtype=torch.bfloat16, device="cuda"), lb.checkpoint_empty(M, K, "cuda")
+    y = lb.adapter_gemm(x, pr.packed, *pr.args(), pr.a, pr.b, pr.scaling, index, p=p, checkpoint=ck)
+    pr.index = torch.ones(pr.M, dtype=torch.int32, device="cuda")
+    ry, ey, rp, ep = forward_ref(pr)
+    check(p[rows], rp, ep, "p")
+    check(y[rows], ry, ey, "y")
+    codes, exps, _ = checkpoint_ref(pr.x)
+    assert torch.equal(ck.exps[rows].cpu(), exps) and torch.equal(ck.codes[rows].double().cpu(), codes)
+    again = lb.checkpoint_store(x)
+    assert torch.equal(again.codes.view(torch.uint8), ck.codes.view(torch.uint8)) and torch.equal(again.exps, ck.exps)
+    del again
+    pr.p, kept = p[rows], lb.checkpoint_load(lb.Checkpoint(ck.codes[rows].contiguous(), ck.exps[rows].contiguous()))
+    assert torch.equal(lb.checkpoint_load(ck)[rows], kept)
+    for inp, seen in ((x, pr.x), (ck, kept)):
+        dx, da, db = lb.adapter_backward(dy, inp, p, pr.packed_t, *pr.args(), pr.a, pr.b, pr.scaling, index)
+        (rdx, edx), (rda, eda), (rdb, edb) = backward_ref(pr, seen)
+        check(dx[rows], rdx, edx, "dx")
+        check(da[1], rda[1], eda[1], "da")
+        check(db[1], rdb[1], edb[1], "db")
+    assert lb.device_status() == 0
