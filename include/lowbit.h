@@ -252,7 +252,9 @@ lowbit_status lowbit_selftest_index_check(void* stream);
  *
  * and is trained through: dX = dY * W + dp * A_a with dp[m] = scaling[a] * dY[m] * B_a, dA_a = the
  * sum of dp[m]^T * X[m] and dB_a = the sum of dY[m]^T * p[m] over the tokens of adapter a.
- * The pages have no counterpart: they run a fixed transformer. */
+ * The pages have no counterpart: they run a fixed transformer. No output and no workspace of these
+ * entry points may overlap an input or another output; a workspace belongs to one call until its work
+ * on the GPU is done. */
 
 #define LOWBIT_MAX_ADAPTERS 4096
 #define LOWBIT_MAX_RANK 128
