@@ -1103,8 +1103,10 @@ void choose_tile(int64_t M, int64_t rows, int64_t red, int num, int rank, int* t
     static constexpr int kTile[4] = {32, 64, 128, 256};
     static constexpr double kBlockUs[4] = {0.42, 0.5, 0.68, 0.82}, kSplitUs[4] = {1.5, 2.0, 3.0, 9.0};
     static constexpr double kSharedUs[4] = {0.0, 3.0, 0.0, 0.0};
-    // clusters of ks CTAs, one per SM, that the GPU's processing clusters hold at once
-    static constexpr int kClusters[9] = {0, kSmsAssumed, 74, 48, 32, 24, 24, 16, 16};
+    // clusters of ks CTAs, one per SM, that the GPU's processing clusters hold at once (a B200 said 45, 33,
+    // 26, 22, 15 and 15 from three CTAs on, others have their SMs spread differently; one too many here
+    // costs a second wave: 53 instead of 40 us for 945 tokens x 7680 -> 384)
+    static constexpr int kClusters[9] = {0, kSmsAssumed, 74, 44, 32, 24, 21, 15, 15};
     double best = 0;
     *tile = 0;
     for (int i = 0; i < 4; ++i) {
