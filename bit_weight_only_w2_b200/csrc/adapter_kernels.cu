@@ -515,6 +515,9 @@ struct SideArgs {
 
 constexpr int kConvThreads = 256;
 
+// With adapters the row itself is copied before the wait for the shrink kernel, which runs meanwhile:
+// that kernel let this one start only after everything earlier in the stream was complete.
+//
 // PER: 16-byte pieces of the row that a thread holds (0: any width, the row is read twice). 512 threads
 // of four pieces instead of 256 of eight took 50 us instead of 41 for 4173 x 9216 with the 8-bit copy.
 // LR: with adapters; CK: with the 8-bit copy. (A kernel each, so that the plain copy keeps the
@@ -523,8 +526,10 @@ template <int PER, bool LR, bool CK>
 __global__ void __launch_bounds__(kConvThreads, 4)
     convert_side_kernel(const uint4* __restrict__ in, int M, int K8, int K8p, uint4* __restrict__ xh,
                         float* __restrict__ rowmul, const SideArgs s) {
-    grid_dependency_wait();
-    grid_launch_dependents();
+    if (!LR) {
+        grid_dependency_wait();
+        grid_launch_dependents();
+    }
     const int row = blockIdx.x, tid = threadIdx.x;
     const uint4* src = in + static_cast<size_t>(row) * K8;
     uint4* dst = xh + static_cast<size_t>(row) * K8p;
@@ -534,26 +539,6 @@ __global__ void __launch_bounds__(kConvThreads, 4)
         for (int j = 0; j < PER; ++j) {
             const int i = tid + j * kConvThreads;
             v[j] = i < K8 ? ldg_nc_v4(src + i) : make_uint4(0, 0, 0, 0);
-        }
-    }
-    // This token's low-rank product: the slices' partials in order, times its adapter's scaling. Its
-    // loads are asked for together with the row's, none waiting for another.
-    __shared__ float prow[kMaxRank];
-    int slot = -1, cols = 0;
-    if (LR) {
-        slot = s.token_slot ? s.token_slot[row] : 0;
-        cols = (s.tile_slots ? s.tile_slots[row >> s.tile_log2] : 1) << s.rp_log2;   // the columns the MMA reads
-        if (tid < (1 << s.rp_log2)) {
-            const int a = adapter_of(s.index, row, s.num);
-            const float* part = s.partial + (static_cast<size_t>(row) << s.rp_log2) + tid;
-            const size_t step = static_cast<size_t>(M) << s.rp_log2;
-            float p = 0.f;
-#pragma unroll 8
-            for (int k = 0; k < s.ksplit; ++k) p += part[k * step];
-            p = a < 0 ? 0.f : p * s.scaling[a];                  // (no adapter: its partials are not written)
-            if (s.p_out && tid < s.rank) s.p_out[static_cast<size_t>(row) * s.rank + tid] = __float2bfloat16_rn(p);
-            if (s.bad && a >= 0 && s.bad[a]) p = __int_as_float(0x7FC00000);   // NaN
-            prow[tid] = p;
         }
     }
     uint32_t mx = 0;   // two running maxima of |value| bits, one per half word
@@ -619,6 +604,25 @@ __global__ void __launch_bounds__(kConvThreads, 4)
     }
     if (tid == 0) rowmul[row] = __int_as_float((127 + e) << 23);   // 2^e
     if (LR) {
+        // this token's low-rank product: the slices' partials in order, times its adapter's scaling
+        __shared__ float prow[kMaxRank];
+        grid_dependency_wait();
+        grid_launch_dependents();   // (not earlier: what follows takes tensor memory, which that kernel needs first)
+        const int slot = s.token_slot ? s.token_slot[row] : 0;
+        const int cols = (s.tile_slots ? s.tile_slots[row >> s.tile_log2] : 1) << s.rp_log2;   // the columns the MMA reads
+        if (tid < (1 << s.rp_log2)) {
+            const int a = adapter_of(s.index, row, s.num);
+            const float* part = s.partial + (static_cast<size_t>(row) << s.rp_log2) + tid;
+            const size_t step = static_cast<size_t>(M) << s.rp_log2;
+            float p = 0.f;
+#pragma unroll 8
+            for (int k = 0; k < s.ksplit; ++k) p += part[k * step];
+            p = a < 0 ? 0.f : p * s.scaling[a];                  // (no adapter: its partials are not written)
+            if (s.p_out && tid < s.rank) s.p_out[static_cast<size_t>(row) * s.rank + tid] = __float2bfloat16_rn(p);
+            if (s.bad && a >= 0 && s.bad[a]) p = __int_as_float(0x7FC00000);   // NaN
+            prow[tid] = p;
+        }
+        __syncthreads();
         if (s.bad && (row & ((1 << s.tile_log2) - 1)) == 0) {      // a tile's first row: its slots' weight sides
             const size_t at = static_cast<size_t>(row >> s.tile_log2) * s.slot_pitch;
             for (int i = tid; i < cols >> s.rp_log2; i += kConvThreads) {
