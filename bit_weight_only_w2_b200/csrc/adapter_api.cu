@@ -228,10 +228,10 @@ LOWBIT_API lowbit_status lowbit_adapter_backward(int64_t M, int64_t N, int64_t K
     e.p_out = b.at<void>(b.w.p);
     if ((st = check_device()) != LOWBIT_OK) return st;
     if ((st = prepare(e, b, s)) != LOWBIT_OK) return st;
-    WgradProblem g = {dY, X, ck_codes, ck_exps, P, e.p_out, dA, dB, M, N, K, e.ad.num, e.ad.rank,
-                      e.ad.index != nullptr};
-    if ((st = launch_wgrad(g, b, s)) != LOWBIT_OK) return st;
-    return dX ? product(e, b, s) : LOWBIT_OK;
+    if (dX && (st = product(e, b, s)) != LOWBIT_OK) return st;
+    const WgradProblem g = {dY, X, ck_codes, ck_exps, P, e.p_out, dA, dB, M, N, K, e.ad.num, e.ad.rank,
+                            e.ad.index != nullptr, dX != nullptr};
+    return launch_wgrad(g, b, s);
 }
 
 static lowbit_status check_checkpoint(const void* x, int64_t M, int64_t K, const uint8_t* codes, const uint8_t* exps) {

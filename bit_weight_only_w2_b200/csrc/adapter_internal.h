@@ -95,6 +95,7 @@ struct WgradProblem {
     int64_t M, N, K;
     int num, rank;
     bool planned;              // false: no index, every token has adapter 0
+    bool beside_product;       // launched right after the product, beside which it runs
 };
 lowbit_status launch_wgrad(const WgradProblem& g, const ExtBuffers& b, cudaStream_t stream);
 

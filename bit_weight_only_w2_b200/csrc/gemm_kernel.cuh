@@ -391,8 +391,10 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
     const uint32_t tmem_base = *tmem_holder;
 
     // Programmatic dependent launch: the next kernel in the stream may start its prologue now.
-    // Threads that touch global memory wait for the previous kernel (the X conversion) first.
-    grid_launch_dependents();
+    // Threads that touch global memory wait for the previous kernel (the X conversion) first. (kExtGrad:
+    // not before that has completed, since the kernel that may follow, the adapters' gradients, reads
+    // what it wrote without waiting for this one.)
+    if constexpr (EXT != kExtGrad) grid_launch_dependents();
 
     const bool split = p.ksplit > 1;
     const int kb_begin = split ? static_cast<int>(blockIdx.z) * p.kb_per_split : 0;
@@ -556,6 +558,7 @@ __global__ void __launch_bounds__(Cfg<BITS, GS, BT, PAIR, EXT>::kThreads, Cfg<BI
             const uint32_t wpre = total < static_cast<uint32_t>(SW) ? total : static_cast<uint32_t>(SW);
             for (; itw < wpre; ++itw) issue_w(itw);
             grid_dependency_wait();
+            if constexpr (EXT == kExtGrad) grid_launch_dependents();
             if constexpr (EXT != kExtNone) {
                 start_tile(slots_of(0));
             }

@@ -455,3 +455,41 @@ def test_offsets_past_32_bits():
         check(da[1], rda[1], eda[1], "da")
         check(db[1], rdb[1], edb[1], "db")
     assert lb.device_status() == 0
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_in_a_row_on_one_workspace(graph):
+    """Kernels of neighbouring calls overlap at their ends: a row of calls of different lengths on one
+    workspace gives what the same calls give one by one."""
+    prs = [Problem(1200, 2048, 2048, 2, 64, 1, 8, None), Problem(90, 512, 264, 4, 64, 3, 64), Problem(40, 256, 1032, 1, 128, 2, 16),
+           Problem(700, 384, 4096, 2, 128, 4, 128, "holes")]
+    size = max(lb.adapter_workspace_size(pr.M, pr.N, pr.K, pr.L, pr.R) for pr in prs)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def row(between):
+        out = []
+        for pr in prs + prs[::-1]:
+            for call in (lambda: [lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args(), ws=ws)],
+                         lambda: list(lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args(), ws=ws)),
+                         lambda: [lb.gemm_dx(pr.dy, pr.packed_t, *pr.args(), ws=ws)],
+                         lambda: list(lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args(), ws=ws)),
+                         lambda: list(lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args(),
+                                                          need_dx=False, ws=ws))[1:]):
+                out += call()
+                between()
+        return out
+
+    want = row(torch.cuda.synchronize)
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = row(lambda: None)
+    for _ in range(10):
+        if graph:
+            for t in got:
+                t.zero_()
+            g.replay()
+        else:
+            got = row(lambda: None)
+        assert lb.device_status() == 0
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
