@@ -511,7 +511,54 @@ struct SideArgs {
     __nv_bfloat16* p_out;      // nullptr: not kept
     uint8_t* codes;            // 8-bit copy
     uint8_t* exps;
+    bool beside;               // a copy without the slots' P that runs beside the shrink kernel
 };
+
+// P of one token: the slices' partials in order, times its adapter's scaling, in its slot's columns and
+// zeros in the tile's others. By T threads (`tid`), which `sync` joins; `scale`: the row's 2^-e.
+template <int T, class Sync>
+__device__ __forceinline__ void side_row(const SideArgs& s, int row, int M, float scale, int tid, float* prow, Sync sync) {
+    const int slot = s.token_slot ? s.token_slot[row] : 0;
+    const int cols = (s.tile_slots ? s.tile_slots[row >> s.tile_log2] : 1) << s.rp_log2;   // the columns the MMA reads
+    const int a = adapter_of(s.index, row, s.num);
+    const bool odd = s.bad && a >= 0 && s.bad[a];
+    for (int r = tid; r < (1 << s.rp_log2); r += T) {
+        const float* part = s.partial + (static_cast<size_t>(row) << s.rp_log2) + r;
+        const size_t step = static_cast<size_t>(M) << s.rp_log2;
+        float p = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < s.ksplit; ++k) p += part[k * step];
+        p = a < 0 ? 0.f : p * s.scaling[a];                      // (no adapter: its partials are not written)
+        if (s.p_out && r < s.rank) s.p_out[static_cast<size_t>(row) * s.rank + r] = __float2bfloat16_rn(p);
+        prow[r] = odd ? __int_as_float(0x7FC00000) : p;          // NaN
+    }
+    sync();
+    if (s.bad && (row & ((1 << s.tile_log2) - 1)) == 0) {        // a tile's first row: its slots' weight sides
+        const size_t at = static_cast<size_t>(row >> s.tile_log2) * s.slot_pitch;
+        for (int i = tid; i < cols >> s.rp_log2; i += T) {
+            const int b = s.slot_adapter[at + i];
+            s.slot_side[at + i] = s.bad[b] ? s.num : b;
+        }
+    }
+    uint4* pd = reinterpret_cast<uint4*>(s.pslots + static_cast<size_t>(row) * s.p_cols);
+    for (int c = tid; c < cols / 8; c += T) {
+        uint4 o = make_uint4(0, 0, 0, 0);
+        if ((c * 8) >> s.rp_log2 == slot) {
+            const float* pr = prow + ((c * 8) & ((1 << s.rp_log2) - 1));
+            uint32_t u[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                // round p first (what p_out holds), then the exact power of two
+                const float lo = __bfloat162float(__float2bfloat16_rn(pr[2 * q])) * scale;
+                const float hi = __bfloat162float(__float2bfloat16_rn(pr[2 * q + 1])) * scale;
+                const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+                u[q] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            o = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        pd[c] = o;
+    }
+}
 
 constexpr int kConvThreads = 256;
 
@@ -520,14 +567,14 @@ constexpr int kConvThreads = 256;
 //
 // PER: 16-byte pieces of the row that a thread holds (0: any width, the row is read twice). 512 threads
 // of four pieces instead of 256 of eight took 50 us instead of 41 for 4173 x 9216 with the 8-bit copy.
-// LR: with adapters; CK: with the 8-bit copy. (A kernel each, so that the plain copy keeps the
+// LR: with the slots' P; CK: with the 8-bit copy. (A kernel each, so that the plain copy keeps the
 // registers, and so the resident rows, that its bandwidth needs.)
 template <int PER, bool LR, bool CK>
 __global__ void __launch_bounds__(kConvThreads, 4)
     convert_side_kernel(const uint4* __restrict__ in, int M, int K8, int K8p, uint4* __restrict__ xh,
                         float* __restrict__ rowmul, const SideArgs s) {
     if (!LR) {
-        grid_dependency_wait();
+        if (!s.beside) grid_dependency_wait();
         grid_launch_dependents();
     }
     const int row = blockIdx.x, tid = threadIdx.x;
@@ -604,51 +651,28 @@ __global__ void __launch_bounds__(kConvThreads, 4)
     }
     if (tid == 0) rowmul[row] = __int_as_float((127 + e) << 23);   // 2^e
     if (LR) {
-        // this token's low-rank product: the slices' partials in order, times its adapter's scaling
         __shared__ float prow[kMaxRank];
         grid_dependency_wait();
         grid_launch_dependents();   // (not earlier: what follows takes tensor memory, which that kernel needs first)
-        const int slot = s.token_slot ? s.token_slot[row] : 0;
-        const int cols = (s.tile_slots ? s.tile_slots[row >> s.tile_log2] : 1) << s.rp_log2;   // the columns the MMA reads
-        if (tid < (1 << s.rp_log2)) {
-            const int a = adapter_of(s.index, row, s.num);
-            const float* part = s.partial + (static_cast<size_t>(row) << s.rp_log2) + tid;
-            const size_t step = static_cast<size_t>(M) << s.rp_log2;
-            float p = 0.f;
-#pragma unroll 8
-            for (int k = 0; k < s.ksplit; ++k) p += part[k * step];
-            p = a < 0 ? 0.f : p * s.scaling[a];                  // (no adapter: its partials are not written)
-            if (s.p_out && tid < s.rank) s.p_out[static_cast<size_t>(row) * s.rank + tid] = __float2bfloat16_rn(p);
-            if (s.bad && a >= 0 && s.bad[a]) p = __int_as_float(0x7FC00000);   // NaN
-            prow[tid] = p;
-        }
-        __syncthreads();
-        if (s.bad && (row & ((1 << s.tile_log2) - 1)) == 0) {      // a tile's first row: its slots' weight sides
-            const size_t at = static_cast<size_t>(row >> s.tile_log2) * s.slot_pitch;
-            for (int i = tid; i < cols >> s.rp_log2; i += kConvThreads) {
-                const int a = s.slot_adapter[at + i];
-                s.slot_side[at + i] = s.bad[a] ? s.num : a;
-            }
-        }
-        uint4* pd = reinterpret_cast<uint4*>(s.pslots + static_cast<size_t>(row) * s.p_cols);
-        for (int c = tid; c < cols / 8; c += kConvThreads) {
-            uint4 o = make_uint4(0, 0, 0, 0);
-            if ((c * 8) >> s.rp_log2 == slot) {
-                const float* pr = prow + ((c * 8) & ((1 << s.rp_log2) - 1));
-                uint32_t u[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    // round p first (what p_out holds), then the exact power of two
-                    const float lo = __bfloat162float(__float2bfloat16_rn(pr[2 * q])) * scale;
-                    const float hi = __bfloat162float(__float2bfloat16_rn(pr[2 * q + 1])) * scale;
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-                    u[q] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-                o = make_uint4(u[0], u[1], u[2], u[3]);
-            }
-            pd[c] = o;
-        }
+        side_row<kConvThreads>(s, row, M, scale, tid, prow, [] { __syncthreads(); });
+    } else if (s.beside && row == 0) {
+        grid_dependency_wait();     // what waits for this kernel waits for the shrink kernel as well
     }
+}
+
+// The slots' P by itself, a warp per token, after the copy of more rows than the GPU holds at once.
+constexpr int kSideWarps = 8;
+constexpr int kSideRows = 1024;
+
+__global__ void __launch_bounds__(32 * kSideWarps)
+    side_kernel(int M, const float* __restrict__ rowmul, const SideArgs s) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    __shared__ float prow[kSideWarps][kMaxRank];
+    const int warp = threadIdx.x >> 5, row = blockIdx.x * kSideWarps + warp;
+    if (row >= M) return;
+    const float scale = __int_as_float((254 << 23) - __float_as_int(rowmul[row]));   // of 2^e the inverse
+    side_row<32>(s, row, M, scale, threadIdx.x & 31, prow[warp], [] { __syncwarp(); });
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -1267,8 +1291,13 @@ lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStrea
         if (K8p <= 8 * kConvThreads) return go(convert_side_kernel<8, LR, CK>);
         return go(convert_side_kernel<0, LR, CK>);
     };
-    if (e.ad.num == 0) return pick(std::false_type{}, std::false_type{});   // (the copy comes with adapters only)
-    return s.codes ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});
+    if (e.ad.num == 0) return pick(std::false_type{}, std::false_type{});   // (the 8-bit copy comes with adapters only)
+    if (e.M <= kSideRows) return s.codes ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});
+    s.beside = true;
+    const lowbit_status st = s.codes ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{});
+    if (st != LOWBIT_OK) return st;
+    return launch_pdl(side_kernel, dim3(static_cast<unsigned>((e.M + kSideWarps - 1) / kSideWarps), 1, 1), 32 * kSideWarps, 0, 1,
+                      stream, static_cast<int>(e.M), rm, s);
 }
 
 lowbit_status launch_wgrad(const WgradProblem& g, const ExtBuffers& b, cudaStream_t stream) {
