@@ -522,15 +522,39 @@ __device__ __forceinline__ void side_row(const SideArgs& s, int row, int M, floa
     const int cols = (s.tile_slots ? s.tile_slots[row >> s.tile_log2] : 1) << s.rp_log2;   // the columns the MMA reads
     const int a = adapter_of(s.index, row, s.num);
     const bool odd = s.bad && a >= 0 && s.bad[a];
-    for (int r = tid; r < (1 << s.rp_log2); r += T) {
-        const float* part = s.partial + (static_cast<size_t>(row) << s.rp_log2) + r;
-        const size_t step = static_cast<size_t>(M) << s.rp_log2;
-        float p = 0.f;
-#pragma unroll 8
-        for (int k = 0; k < s.ksplit; ++k) p += part[k * step];
+    const float* part = s.partial + (static_cast<size_t>(row) << s.rp_log2);
+    const size_t step = static_cast<size_t>(M) << s.rp_log2;
+    auto keep = [&](int r, float p) {
         p = a < 0 ? 0.f : p * s.scaling[a];                      // (no adapter: its partials are not written)
         if (s.p_out && r < s.rank) s.p_out[static_cast<size_t>(row) * s.rank + r] = __float2bfloat16_rn(p);
         prow[r] = odd ? __int_as_float(0x7FC00000) : p;          // NaN
+    };
+    if (T == 32) {
+        // four ranks a lane, and as many slices at once as the warp's lanes then hold
+        const int log2 = s.rp_log2 - 2, r = (tid & ((1 << log2) - 1)) * 4;
+        float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = tid >> log2; k < s.ksplit; k += 32 >> log2) {
+            const float4 v = *reinterpret_cast<const float4*>(part + k * step + r);
+            p = make_float4(p.x + v.x, p.y + v.y, p.z + v.z, p.w + v.w);
+        }
+        for (int o = 1 << log2; o < 32; o <<= 1) {
+            p.x += __shfl_xor_sync(0xffffffffu, p.x, o);
+            p.y += __shfl_xor_sync(0xffffffffu, p.y, o);
+            p.z += __shfl_xor_sync(0xffffffffu, p.z, o);
+            p.w += __shfl_xor_sync(0xffffffffu, p.w, o);
+        }
+        if (tid < 1 << log2) {
+            keep(r, p.x);
+            keep(r + 1, p.y);
+            keep(r + 2, p.z);
+            keep(r + 3, p.w);
+        }
+    } else if (tid < (1 << s.rp_log2)) {
+        float p = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < s.ksplit; ++k) p += part[k * step + tid];
+        keep(tid, p);
     }
     sync();
     if (s.bad && (row & ((1 << s.tile_log2) - 1)) == 0) {        // a tile's first row: its slots' weight sides
@@ -660,9 +684,12 @@ __global__ void __launch_bounds__(kConvThreads, 4)
     }
 }
 
-// The slots' P by itself, a warp per token, after the copy of more rows than the GPU holds at once.
+// The slots' P by itself, a warp per token, after the copy of more rows than the GPU holds at once (about
+// five an SM, whose copies would all wait for the shrink kernel before the next ones start). From 770 to
+// 1000 tokens both ways take the same within 4 %, the kernel of its own 1 % less on average; below 700 it
+// costs up to 7 % (one launch more), and 4173 tokens x 9216 gain 9 us of 536.
 constexpr int kSideWarps = 8;
-constexpr int kSideRows = 1024;
+constexpr int kSideRows = 5 * kSmsAssumed;
 
 __global__ void __launch_bounds__(32 * kSideWarps)
     side_kernel(int M, const float* __restrict__ rowmul, const SideArgs s) {
