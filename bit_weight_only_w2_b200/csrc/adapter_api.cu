@@ -229,7 +229,7 @@ LOWBIT_API lowbit_status lowbit_adapter_backward(int64_t M, int64_t N, int64_t K
     if ((st = check_device()) != LOWBIT_OK) return st;
     if ((st = prepare(e, b, s)) != LOWBIT_OK) return st;
     if (dX && (st = product(e, b, s)) != LOWBIT_OK) return st;
-    const WgradProblem g = {dY, X, ck_codes, ck_exps, P, e.p_out, dA, dB, M, N, K, e.ad.num, e.ad.rank,
+    const WgradProblem g = {dY, X, ck_codes, ck_exps, P, e.p_out, b.at<void>(b.w.p_rest), dA, dB, M, N, K, e.ad.num, e.ad.rank,
                             e.ad.index != nullptr, dX != nullptr};
     return launch_wgrad(g, b, s);
 }

@@ -49,7 +49,7 @@ struct ExtProblem {
 //   and with adapters: perm (tokens sorted by adapter), seg (start of each adapter's tokens, L + 1
 //   entries), blocks (int4 per shrink block), tile_slots, slot_adapter, slot_side, token_slot, odd_parts and bad (which
 //   adapters' weight sides are not finite), partial (fp32 [ksplit][M][Rp]), pslots (bf16 [M][slot columns])
-//   p        bf16 [M][R] (backward: dp)
+//   p        bf16 [M][R] (backward: dp), and p_rest, what its rounding left
 struct ExtWorkspace {
     int64_t red64;
     int tile_tokens;         // tokens per tile and K slices of the product, chosen from the sizes
@@ -61,7 +61,7 @@ struct ExtWorkspace {
     int plan_slices;         // CTAs per adapter of the plan kernel
     int64_t slot_pitch;      // slots of a tile, at most
     int64_t p_cols;          // columns of pslots
-    size_t xh, rowmul, perm, seg, blocks, tile_slots, slot_adapter, slot_side, token_slot, odd_parts, bad, partial, pslots, p, total;
+    size_t xh, rowmul, perm, seg, blocks, tile_slots, slot_adapter, slot_side, token_slot, odd_parts, bad, partial, pslots, p, p_rest, total;
 };
 ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int rank);
 
@@ -89,7 +89,8 @@ struct WgradProblem {
     const uint8_t* ck_codes;   // the 8-bit copy
     const uint8_t* ck_exps;
     const void* p;             // bf16 [M][R]
-    const void* dp;            // bf16 [M][R]
+    const void* dp;            // bf16 [M][R], and
+    const void* dp_rest;       // what its rounding left
     void* dA;                  // bf16 [L][R][K]
     void* dB;                  // bf16 [L][N][R]
     int64_t M, N, K;

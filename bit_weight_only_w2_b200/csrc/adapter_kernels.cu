@@ -489,10 +489,11 @@ __global__ void __launch_bounds__(32 * kShrinkSmallWarps)
 // ---------------------------------------------------------------------------------------------
 // One CTA per token row, as the plain GEMM's conversion (the row's power of two 2^e comes from its
 // largest |value|). P is multiplied by 2^-e as well, since the epilogue multiplies the whole sum
-// by 2^e; that is exact in bf16. p (in the backward dp) itself is rounded to bf16 once, as the MMA's
-// operand and as what the gradients read: 2^-8 of each entry at most, like the output's own rounding.
-// Against 64 bits the gradients of A are then 2.4e-3 off in the norm where one rounding of the result
-// alone gives 1.7e-3; a second bf16 term for the remainder would double the slot columns.
+// by 2^e; that is exact in bf16. p (in the backward dp) itself is rounded to bf16 once as the MMA's
+// operand: 2^-8 of each entry at most, like the output's own rounding, and there beside the larger
+// product with W. dA has nothing beside it, so it gets dp in two bf16 terms, the second for what the first
+// leaves (2^-16): with the first alone it was 2.4e-3 off in the norm against 64 bits, and more where a few
+// large channels of x rule it, with both 1.7e-3, which is the rounding of the result.
 struct SideArgs {
     const float* partial;      // [ksplit][M][Rp]
     int ksplit;
@@ -509,6 +510,7 @@ struct SideArgs {
     __nv_bfloat16* pslots;
     long long p_cols;
     __nv_bfloat16* p_out;      // nullptr: not kept
+    __nv_bfloat16* p_rest;     // what p_out's rounding leaves, or nullptr
     uint8_t* codes;            // 8-bit copy
     uint8_t* exps;
     bool beside;               // a copy without the slots' P that runs beside the shrink kernel
@@ -526,7 +528,15 @@ __device__ __forceinline__ void side_row(const SideArgs& s, int row, int M, floa
     const size_t step = static_cast<size_t>(M) << s.rp_log2;
     auto keep = [&](int r, float p) {
         p = a < 0 ? 0.f : p * s.scaling[a];                      // (no adapter: its partials are not written)
-        if (s.p_out && r < s.rank) s.p_out[static_cast<size_t>(row) * s.rank + r] = __float2bfloat16_rn(p);
+        if (s.p_out && r < s.rank) {
+            const __nv_bfloat16 h = __float2bfloat16_rn(p);
+            const size_t at = static_cast<size_t>(row) * s.rank + r;
+            s.p_out[at] = h;
+            if (s.p_rest) {
+                const float rest = p - __bfloat162float(h);
+                s.p_rest[at] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);   // (an infinity is all in the first)
+            }
+        }
         prow[r] = odd ? __int_as_float(0x7FC00000) : p;          // NaN
     };
     if (T == 32) {
@@ -708,8 +718,8 @@ __global__ void __launch_bounds__(32 * kSideWarps)
 // Both are the same product G^T P over an adapter's tokens, G = x or dy: A = G^T (128 columns of G,
 // MN-major), B = P (MN-major), reduction over the tokens in stages of 64. Persistent CTAs walk tiles of
 // both gradients and all adapters through one ring, with two accumulators, so that a tile's start and
-// its stores lie under its neighbours' products. x may be the 8-bit copy: eight warps widen a stage's
-// codes into the MMA's tile (exactly). Bound by the stream of x and dy: beyond a start of some 15 us,
+// its stores lie under its neighbours' products. dA multiplies dp's two terms into one accumulator. x may
+// be the 8-bit copy: eight warps widen a stage's codes into the MMA's tile (exactly). Bound by the stream of x and dy: beyond a start of some 15 us,
 // 30 us per 151 MB of bf16 (5.0 TB/s, 0.77 of the copy rate; P comes from L2 on top), 50 us cold for
 // three adapters of 1391 tokens x (9216 + 9216) at rank 64 with x in 8 bits. Cutting the tokens of few
 // tiles into slices that meet in a workspace cost 12 us a slice and gained nothing.
@@ -725,7 +735,7 @@ struct WgradPart {
 struct WgradArgs {
     // of dA and dB: G as (C, M), boxes of 64 bf16 or 128 codes, and P as (R, M), boxes of up to 64, by
     // 64 rows (a whole stage), 16 rows and 1 row
-    CUtensorMap map_g[3][2], map_p[3][2];
+    CUtensorMap map_g[3][2], map_p[3][2], map_rest[3];   // (map_rest: dp's second term)
     WgradPart part[2];         // dA, dB
     int R, M, num;
     bool beside;               // the kernel before is the product, which this one runs beside
@@ -738,27 +748,30 @@ constexpr int kWgradThreads = 32 * (6 + kWgradWideners);   // warp 0 gathers, 1 
 template <int RP>
 constexpr int kWgradCtas = RP == 128 ? 1 : 2;              // per SM
 template <int RP>
-constexpr int kWgradStages = RP == 128 ? 5 : RP == 16 ? 4 : 3;
-constexpr int kRawBytes = 64 * 128;               // 64 tokens x 128 codes
+constexpr int kWgradStages = RP == 16 ? 5 : RP == 64 ? 3 : 4;
+constexpr int kRawBytes = 64 * 128;               // 64 tokens x 128 codes, in the second half of G's tile
+__host__ __device__ constexpr int wgrad_stage(int rp) { return gather_stage(rp) + rp * 128; }
 template <int RP>
-constexpr int kWgradSmem = 1024 + kWgradStages<RP> * (gather_stage(RP) + kRawBytes);
+constexpr int kWgradSmem = 1024 + kWgradStages<RP> * wgrad_stage(RP);
 
 template <int RP>
 __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(const __grid_constant__ WgradArgs w) {
-    constexpr int S = kWgradStages<RP>, kStage = gather_stage(RP);
+    constexpr int S = kWgradStages<RP>, kStage = wgrad_stage(RP);
     constexpr uint32_t kAcc = RP, kCols = 2 * kAcc < 32 ? 32 : 2 * kAcc;
     static_assert(kWgradCtas<RP> * (kWgradSmem<RP> + 2048) <= 228 * 1024, "shared memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* raw = smem + S * kStage;
-    __shared__ uint64_t bars[2 * S + 1], wide[S], accfull[2], accempty[2];
+    __shared__ uint64_t bars[2 * S + 1], taken[S], wide[S], accfull[2], accempty[2];
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_word;
     const GatherPipe g = {bars, bars + S, bars + 2 * S, &abort_word, w.status};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         gather_init(g, S, 1 + kWgradWideners);
-        for (int i = 0; i < S; ++i) mbar_init(&wide[i], kWgradWideners);
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&taken[i], kWgradWideners);
+            mbar_init(&wide[i], kWgradWideners);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&accfull[i], 1);
             mbar_init(&accempty[i], 4);
@@ -833,7 +846,7 @@ __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(co
             const Item cur = next;
             next = item_of(i + stride);
             const int steps = cur.steps();
-            const bool q8 = w.part[cur.part].exps != nullptr;
+            const bool q8 = w.part[cur.part].exps != nullptr, dA = cur.part == 0;
             for (int step = 0; step < steps; ++step, ++it) {
                 int rows2[4];
                 rows_ahead(rows2);
@@ -843,24 +856,28 @@ __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(co
                 const int first = __shfl_sync(0xffffffffu, rows[0], 0);
                 const bool as_stage = __all_sync(0xffffffffu, as_box && rows[0] == first + row);
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&g.empty[s], ((it / S) & 1u) ^ 1u, g.abort_flag, g.status)))) break;
-                if (lane == 0) mbar_arrive_expect_tx(&g.full[s], (q8 ? kRawBytes : kWideBytes) + RP * 128);
+                if (lane == 0) mbar_arrive_expect_tx(&g.full[s], (q8 ? kRawBytes : kWideBytes) + (dA ? 2 : 1) * RP * 128);
                 __syncwarp();
-                const uint32_t st = s0 + s * kStage, rw = smem_u32(raw) + s * kRawBytes, ps = st + kWideBytes;
+                const uint32_t st = s0 + s * kStage, rw = st + kWideBytes - kRawBytes, ps = st + kWideBytes;
                 if (as_stage) {
                     if ((lane & 15) == 0) {
                         if (!q8) tma_load_2d(&w.map_g[0][cur.part], &g.full[s], shared_ptr(st + half * 8192), cur.c0 + half * 64, first);
                         else if (half == 0) tma_load_2d(&w.map_g[0][cur.part], &g.full[s], shared_ptr(rw), cur.c0, first);
-                        if (half == 0 || RP == 128)
+                        if (half == 0 || RP == 128) {
                             tma_load_2d(&w.map_p[0][cur.part], &g.full[s], shared_ptr(ps + half * 8192), half * 64, first);
+                            if (dA) tma_load_2d(&w.map_rest[0], &g.full[s], shared_ptr(ps + RP * 128 + half * 8192), half * 64, first);
+                        }
                     }
                 } else {
                     const CUtensorMap *mg = &w.map_g[1][cur.part], *mg1 = &w.map_g[2][cur.part];
                     if (!q8) gather_rows(mg, mg1, &g.full[s], st + half * 8192 + row * 128, cur.c0 + half * 64, rows, as_box);
                     else if (half == 0) gather_rows(mg, mg1, &g.full[s], rw + row * 128, cur.c0, rows, as_box);
                     // P: rows of kNarrowCols columns, a second tile of 64 for Rp = 128
-                    if (half == 0 || RP == 128)
-                        gather_rows(&w.map_p[1][cur.part], &w.map_p[2][cur.part], &g.full[s],
-                                    ps + half * 8192 + row * kNarrowCols<RP> * 2, half * 64, rows, as_box);
+                    if (half == 0 || RP == 128) {
+                        const uint32_t to = ps + half * 8192 + row * kNarrowCols<RP> * 2;
+                        gather_rows(&w.map_p[1][cur.part], &w.map_p[2][cur.part], &g.full[s], to, half * 64, rows, as_box);
+                        if (dA) gather_rows(&w.map_rest[1], &w.map_rest[2], &g.full[s], to + RP * 128, half * 64, rows, as_box);
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -880,7 +897,7 @@ __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(co
             Item next = item_of(blockIdx.x);
             for (int64_t i = blockIdx.x; ok && i < items; i += stride) {
                 const int steps = next.steps();
-                const bool q8 = w.part[next.part].exps != nullptr;
+                const bool q8 = w.part[next.part].exps != nullptr, dA = next.part == 0;
                 next = item_of(i + stride);
                 if (steps == 0) continue;
                 const int b = n & 1;
@@ -899,6 +916,12 @@ __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(co
                     for (int k16 = 0; k16 < 4; ++k16)
                         mma_f16_ss(tmem + b * kAcc, smem_desc_mn(st + k16 * 2048, 128, 8192),
                                    narrow_mn_desc<RP>(st + kWideBytes, k16), idesc, step > 0 || k16 > 0 ? 1u : 0u);
+                    if (dA) {
+#pragma unroll
+                        for (int k16 = 0; k16 < 4; ++k16)
+                            mma_f16_ss(tmem + b * kAcc, smem_desc_mn(st + k16 * 2048, 128, 8192),
+                                       narrow_mn_desc<RP>(st + kWideBytes + RP * 128, k16), idesc, 1u);
+                    }
                     mma_commit(&g.empty[s]);
                 }
                 if (!ok) break;
@@ -914,6 +937,7 @@ __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(co
         constexpr int kRowsOf = 64 * 8 / (32 * kWgradWideners), kStep = 64 / kRowsOf;
         const int wt = tid - 64, ch = wt & 7, row0 = wt >> 3;
         int it = 0;
+        uint32_t taken_phase = 0;                    // bit s: the phase that slot s's taking completes next
         Item next = item_of(blockIdx.x);
         bool ok = true;
         for (int64_t i = blockIdx.x; ok && i < items; i += stride) {
@@ -955,16 +979,24 @@ __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(co
                 exps_of(id, e_next);
                 ids_of(step + 2, id);
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&g.full[s], (it / S) & 1u, g.abort_flag, g.status)))) break;
-                uint8_t* half = smem + s * kStage + (ch >> 2) * 8192;
+                uint8_t *tile = smem + s * kStage, *half = tile + (ch >> 2) * 8192;
+                uint4 c[kRowsOf];
+#pragma unroll
+                for (int j = 0; j < kRowsOf; ++j)
+                    c[j] = *reinterpret_cast<const uint4*>(tile + kWideBytes - kRawBytes + (row0 + kStep * j) * 128 + ch * 16);
+                // the codes lie where their values go: every warp has to have taken its own
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&taken[s]);
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&taken[s], (taken_phase >> s) & 1u, g.abort_flag, g.status)))) break;
+                taken_phase ^= 1u << s;
 #pragma unroll
                 for (int j = 0; j < kRowsOf; ++j) {
                     const int row = row0 + kStep * j;
-                    const uint4 c = *reinterpret_cast<const uint4*>(raw + s * kRawBytes + row * 128 + ch * 16);
                     uint8_t* dst = half + row * 128;
                     *reinterpret_cast<uint4*>(dst + ((((2 * ch) & 7) ^ (row & 7)) << 4)) =
-                        checkpoint_decode8(make_uint2(c.x, c.y), e[j]);
+                        checkpoint_decode8(make_uint2(c[j].x, c[j].y), e[j]);
                     *reinterpret_cast<uint4*>(dst + ((((2 * ch + 1) & 7) ^ (row & 7)) << 4)) =
-                        checkpoint_decode8(make_uint2(c.z, c.w), e[j]);
+                        checkpoint_decode8(make_uint2(c[j].z, c[j].w), e[j]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1138,6 +1170,7 @@ lowbit_status wgrad_launch(const WgradProblem& g, WgradArgs& a, cudaStream_t str
                   : make_map_rows(&mg[0], u8, 1, g.ck_codes, g.K, g.M, 128, high, CU_TENSOR_MAP_SWIZZLE_NONE)) &&
              make_map_rows(&mg[1], bf16, 2, g.dy, g.N, g.M, 64, high, CU_TENSOR_MAP_SWIZZLE_128B) &&
              make_map_rows(&mp[0], bf16, 2, g.dp, g.rank, g.M, cols, high, swizzle_of(cols * 2)) &&
+             make_map_rows(&a.map_rest[k], bf16, 2, g.dp_rest, g.rank, g.M, cols, high, swizzle_of(cols * 2)) &&
              make_map_rows(&mp[1], bf16, 2, g.p, g.rank, g.M, cols, high, swizzle_of(cols * 2));
     }
     if (!ok) return LOWBIT_ERR_CUDA;
@@ -1248,6 +1281,7 @@ ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int ra
         w.partial = take(static_cast<size_t>(w.ksplit) * M * rp * 4);
         w.pslots = take(static_cast<size_t>(M) * w.p_cols * 2);
         w.p = take(static_cast<size_t>(M) * rank * 2);
+        w.p_rest = take(static_cast<size_t>(M) * rank * 2);
     }
     w.total = at;
     return w;
@@ -1299,6 +1333,7 @@ lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStrea
         s.pslots = b.at<__nv_bfloat16>(w.pslots);
         s.p_cols = w.p_cols;
         s.p_out = static_cast<__nv_bfloat16*>(e.p_out);
+        s.p_rest = e.grad ? b.at<__nv_bfloat16>(w.p_rest) : nullptr;
     }
     s.codes = e.ck_codes;
     s.exps = e.ck_exps;

@@ -315,9 +315,10 @@ lowbit_status lowbit_gemm_dx(int64_t M, int64_t N, int64_t K, int bits, int grou
  *   X    bf16 [M][K], or NULL with its 8-bit copy in ck_codes / ck_exps
  *   dX   bf16 [M][K], or NULL if it is not needed
  *   dA   bf16 [L][R][K], dB bf16 [L][N][R]: written in full (zero for an adapter without tokens)
- * all 16-byte aligned. Sums are fp32, in a fixed order; dp is rounded to bf16 once and dA, dB and dX
- * once each. An infinity or NaN in one adapter reaches its own tokens' dX (NaN in every column if its A
- * is not finite throughout and there is an index) and its own dA and dB only. */
+ * all 16-byte aligned. Sums are fp32, in a fixed order; dp is rounded to bf16 once for dX and kept in two
+ * bf16 terms (2^-16) for dA; dA, dB and dX are rounded once each. An infinity or NaN in one adapter reaches
+ * its own tokens' dX (NaN in every column if its A is not finite throughout and there is an index) and its
+ * own dA and dB only; an infinity in X may reach dA as NaN. */
 lowbit_status lowbit_adapter_backward(int64_t M, int64_t N, int64_t K, int bits, int group_size, const void* dY,
                                       const uint32_t* Wt, const void* scales, const void* zeros,
                                       const lowbit_adapters* adapters, const void* X, const uint8_t* ck_codes,

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import bit_weight_only_w2_b200 as lb
-from tests._adapters import Problem, backward_ref, check, checkpoint_ref, forward_ref
+from tests._adapters import H32, HB16, Problem, backward_ref, check, checkpoint_ref, forward_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -493,3 +493,27 @@ def test_calls_in_a_row_on_one_workspace(graph):
             got = row(lambda: None)
         assert lb.device_status() == 0
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("M,L,index", [(3, 1, None), (65, 2, "sorted"), (40, 7, "random")])
+@pytest.mark.parametrize("R", [8, 24, 64, 128])
+@pytest.mark.parametrize("eight", [False, True])
+def test_da_is_rounded_once(M, L, index, R, eight):
+    """dA within half a step of bf16, where a few large channels and few tokens leave nothing to average
+    dp's rounding: dp comes in two terms (2^-16)."""
+    pr = Problem(M, 256, 264, 2, 64, L, R, index)
+    pr.x[:, 5::100] *= 16
+    x = lb.checkpoint_store(pr.x) if eight else pr.x
+    seen = (lb.checkpoint_load(x) if eight else x).double()
+    da = lb.adapter_backward(pr.dy, x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args())[1]
+    assert lb.device_status() == 0
+    rows, h = pr.rows(), HB16
+    for l in range(L):
+        m = (rows == l).nonzero().flatten()
+        dy, b, sc, n = pr.dy[m].double(), pr.b[l].double(), float(pr.scaling[l]), len(m)
+        dp = sc * (dy @ b)
+        f = (pr.N + 2) * H32 * sc * (dy.abs() @ b.abs())
+        pe = f + h * h * (dp.abs() + f)
+        ref = dp.T @ seen[m]
+        e = pe.T @ seen[m].abs() + 2 * n * H32 * (1 + h) * (dp.abs().T @ seen[m].abs())
+        check(da[l], ref, e + h * (ref.abs() + e), "da")
