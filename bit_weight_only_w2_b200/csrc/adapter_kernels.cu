@@ -719,10 +719,11 @@ __global__ void __launch_bounds__(32 * kSideWarps)
 // MN-major), B = P (MN-major), reduction over the tokens in stages of 64. Persistent CTAs walk tiles of
 // both gradients and all adapters through one ring, with two accumulators, so that a tile's start and
 // its stores lie under its neighbours' products. dA multiplies dp's two terms into one accumulator. x may
-// be the 8-bit copy: eight warps widen a stage's codes into the MMA's tile (exactly). Bound by the stream of x and dy: beyond a start of some 15 us,
-// 30 us per 151 MB of bf16 (5.0 TB/s, 0.77 of the copy rate; P comes from L2 on top), 50 us cold for
-// three adapters of 1391 tokens x (9216 + 9216) at rank 64 with x in 8 bits. Cutting the tokens of few
-// tiles into slices that meet in a workspace cost 12 us a slice and gained nothing.
+// be the 8-bit copy: eight warps widen a stage's codes into the MMA's tile (exactly). Bound by the stream
+// of x and dy: beyond a start of some 15 us, 30 us per 151 MB of bf16 (5.0 TB/s, 0.77 of the copy rate; P
+// comes from L2 on top), 56 us cold for three adapters of 1391 tokens x (9216 + 9216) at rank 64 with x in
+// 8 bits, dp's second term 6 of them. Cutting the tokens of few tiles into slices that meet in a workspace
+// cost 12 us a slice and gained nothing, nor did more stages.
 // With dX it comes after the product and runs beside it: the product lets it start once the copy pass
 // (all that it depends on) is complete, and it ends only when the product has. (After one another, wgrad
 // first: 28.1 instead of 20.3 us for 77 tokens x 2560 x 2560, 565 instead of 533 for the 4173 tokens.)
