@@ -1262,6 +1262,7 @@ ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int ra
         if (ks > 16) ks = 16;
         if (ks < 1) ks = 1;
         w.kslice = ((w.red64 + ks - 1) / ks + 63) / 64 * 64;
+        if (w.kslice < 64) w.kslice = 64;   // (an empty reduction)
         w.ksplit = static_cast<int>((w.red64 + w.kslice - 1) / w.kslice);
         w.slot_pitch = num < w.tile_tokens ? num : w.tile_tokens;
         w.p_cols = (w.slot_pitch * rp + 63) / 64 * 64;

@@ -1,0 +1,20 @@
+"""Host side of the adapter entry points, without a GPU: sizes of the workspace, and calls at the edges
+of what they take."""
+import subprocess
+import sys
+
+import pytest
+
+import bit_weight_only_w2_b200 as lb
+
+
+@pytest.mark.parametrize("N,K", [(0, 64), (64, 0), (0, 0)])
+def test_workspace_size_of_an_empty_linear(N, K):
+    """A linear without rows or columns has a size like any other (a division by its empty K slices ended
+    the process, so each is asked for in one of its own)."""
+    code = (f"import ctypes; f = ctypes.CDLL({lb.LIB_PATH!r}).lowbit_adapter_workspace_size; f.restype = ctypes.c_size_t; "
+            f"f.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int] * 2; print(*[f(m, {N}, {K}, l, r) for m in (0, 1, 17, 5000) "
+            f"for l, r in ((0, 0), (1, 8), (300, 128))])")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
+    assert all(int(n) % 256 == 0 for n in r.stdout.split())
