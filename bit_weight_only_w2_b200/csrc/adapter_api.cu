@@ -113,7 +113,7 @@ LOWBIT_API size_t lowbit_adapter_workspace_size(int64_t M, int64_t N, int64_t K,
     // (without an index the product is laid out for one adapter; whichever needs more)
     size_t most = 0;
     for (int n : {num, num > 1 ? 1 : num})
-        for (size_t t : {ext_workspace(M, N, K, n, rank).total, ext_workspace(M, K, N, n, rank).total})
+        for (size_t t : {ext_workspace_bound(M, N, K, n, rank), ext_workspace_bound(M, K, N, n, rank)})
             if (t > most) most = t;
     return most;
 }

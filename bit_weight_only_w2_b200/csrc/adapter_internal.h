@@ -64,6 +64,8 @@ struct ExtWorkspace {
     size_t xh, rowmul, perm, seg, blocks, tile_slots, slot_adapter, slot_side, token_slot, odd_parts, bad, partial, pslots, p, p_rest, total;
 };
 ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int rank);
+// Bytes that hold the workspace of M tokens or fewer: grows with M, which `total` does not everywhere.
+size_t ext_workspace_bound(int64_t M, int64_t rows, int64_t red, int num, int rank);
 
 struct ExtBuffers {
     ExtWorkspace w;

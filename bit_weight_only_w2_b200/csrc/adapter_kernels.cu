@@ -1193,8 +1193,8 @@ namespace {
 // tiles share an SM). The model's choice is mostly within 10 % of the best of each sweep; a rule on
 // M alone left 30-40 % at M = 100 .. 200 (4096 x 4096 at 203 tokens: 29.8 us unsplit, 21.1 as 128
 // tokens x 2 slices).
+constexpr int kTileTokens[4] = {32, 64, 128, 256};
 void choose_tile(int64_t M, int64_t rows, int64_t red, int num, int rank, int* tile, int* split) {
-    static constexpr int kTile[4] = {32, 64, 128, 256};
     static constexpr double kBlockUs[4] = {0.42, 0.5, 0.68, 0.82}, kSplitUs[4] = {1.5, 2.0, 3.0, 9.0};
     static constexpr double kSharedUs[4] = {0.0, 3.0, 0.0, 0.0};
     // clusters of ks CTAs, one per SM, that the GPU's processing clusters hold at once (a B200 said 45, 33,
@@ -1204,7 +1204,7 @@ void choose_tile(int64_t M, int64_t rows, int64_t red, int num, int rank, int* t
     double best = 0;
     *tile = 0;
     for (int i = 0; i < 4; ++i) {
-        const int bt = kTile[i];
+        const int bt = kTileTokens[i];
         if (bt < 256 && M > 16 * bt) continue;   // (small tiles of many tokens re-read W too often)
         const int64_t tiles = (M + bt - 1) / bt * ((rows + 127) / 128);
         double slots = 0;
@@ -1235,13 +1235,21 @@ void choose_tile(int64_t M, int64_t rows, int64_t red, int num, int rank, int* t
     }
 }
 
-}  // namespace
+// K slices of the shrink kernel: one wave of two CTAs per SM over the blocks that hold tokens. (Slices down to
+// 64 of K: at least 256 each took 28.9 us against 24.8 for 306 tokens of K = 512 that do not follow one
+// another, 39.4 against 36.2 for the backward of 879 tokens, and nothing more anywhere but 1 us in 45.)
+constexpr int kMaxSlices = 16;
+int64_t shrink_slices(int64_t M, int64_t red64, int num) {
+    const int64_t busy = M / kShrinkTokens + (num < M ? num : M);
+    int64_t ks = 2 * kSmsAssumed / (busy > 0 ? busy : 1);
+    if (ks > red64 / 64) ks = red64 / 64;
+    if (ks > kMaxSlices) ks = kMaxSlices;
+    return ks < 1 ? 1 : ks;
+}
 
-ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int rank) {
-    ExtWorkspace w = {};
-    w.red64 = (red + 63) / 64 * 64;
-    choose_tile(M, rows, red, num, rank, &w.tile_tokens, &w.product_split);
-    w.m_tiles = (M + w.tile_tokens - 1) / w.tile_tokens;
+// The parts of the workspace one after another, of `slots` slots in all tiles and `partial_rows` rows of
+// partials in all K slices.
+void lay_out(ExtWorkspace& w, int64_t M, int64_t rows, int num, int rank, int64_t slots, int64_t partial_rows) {
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t o = at;
@@ -1253,25 +1261,13 @@ ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int ra
     if (num > 0) {
         const int rp = 1 << slot_log2(rank);
         w.num_blocks = M / kShrinkTokens + num + 1;
-        // K slices: one wave of two CTAs per SM over the blocks that hold tokens. (Slices down to 64 of K: at
-        // least 256 each took 28.9 us against 24.8 for 306 tokens of K = 512 that do not follow one another,
-        // 39.4 against 36.2 for the backward of 879 tokens, and nothing more anywhere but 1 us in 45.)
-        const int64_t busy = M / kShrinkTokens + (num < M ? num : M);
-        int64_t ks = 2 * kSmsAssumed / (busy > 0 ? busy : 1);
-        if (ks > w.red64 / 64) ks = w.red64 / 64;
-        if (ks > 16) ks = 16;
-        if (ks < 1) ks = 1;
-        w.kslice = ((w.red64 + ks - 1) / ks + 63) / 64 * 64;
-        if (w.kslice < 64) w.kslice = 64;   // (an empty reduction)
-        w.ksplit = static_cast<int>((w.red64 + w.kslice - 1) / w.kslice);
-        w.slot_pitch = num < w.tile_tokens ? num : w.tile_tokens;
         w.p_cols = (w.slot_pitch * rp + 63) / 64 * 64;
         w.perm = take(static_cast<size_t>(M) * 4);
         w.seg = take((static_cast<size_t>(num) + 1) * 4);
         w.blocks = take(static_cast<size_t>(w.num_blocks) * 16);
         w.tile_slots = take(static_cast<size_t>(w.m_tiles) * 4);
-        w.slot_adapter = take(static_cast<size_t>(w.m_tiles) * w.slot_pitch * 4);
-        w.slot_side = take(static_cast<size_t>(w.m_tiles) * w.slot_pitch * 4);
+        w.slot_adapter = take(static_cast<size_t>(slots) * 4);
+        w.slot_side = take(static_cast<size_t>(slots) * 4);
         w.token_slot = take(static_cast<size_t>(M) * 4);
         // CTAs per adapter of the plan kernel: about four per SM in all, 32 KB of the weight side each
         const int64_t parts = (rows * rank / 8 + 2047) / 2048;
@@ -1280,13 +1276,54 @@ ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int ra
         if (w.plan_slices < 1) w.plan_slices = 1;
         w.odd_parts = take(static_cast<size_t>(w.plan_slices) * num * 4);
         w.bad = take(static_cast<size_t>(num) * 4);
-        w.partial = take(static_cast<size_t>(w.ksplit) * M * rp * 4);
+        w.partial = take(static_cast<size_t>(partial_rows) * rp * 4);
         w.pslots = take(static_cast<size_t>(M) * w.p_cols * 2);
         w.p = take(static_cast<size_t>(M) * rank * 2);
         w.p_rest = take(static_cast<size_t>(M) * rank * 2);
     }
     w.total = at;
+}
+
+}  // namespace
+
+ExtWorkspace ext_workspace(int64_t M, int64_t rows, int64_t red, int num, int rank) {
+    ExtWorkspace w = {};
+    w.red64 = (red + 63) / 64 * 64;
+    choose_tile(M, rows, red, num, rank, &w.tile_tokens, &w.product_split);
+    w.m_tiles = (M + w.tile_tokens - 1) / w.tile_tokens;
+    if (num > 0) {
+        w.slot_pitch = num < w.tile_tokens ? num : w.tile_tokens;
+        const int64_t ks = shrink_slices(M, w.red64, num);
+        w.kslice = ((w.red64 + ks - 1) / ks + 63) / 64 * 64;
+        if (w.kslice < 64) w.kslice = 64;   // (an empty reduction)
+        w.ksplit = static_cast<int>((w.red64 + w.kslice - 1) / w.kslice);
+    }
+    lay_out(w, M, rows, num, rank, w.m_tiles * w.slot_pitch, w.ksplit * M);
     return w;
+}
+
+// The largest workspace of up to M tokens. A longer batch may get narrower tiles (fewer slots of P each) or
+// fewer K slices of the shrink kernel, so the size for M itself falls here and there as M grows; the bound
+// takes each part that depends on them at its most, and the others grow with M.
+size_t ext_workspace_bound(int64_t M, int64_t rows, int64_t red, int num, int rank) {
+    ExtWorkspace w = {};
+    w.red64 = (red + 63) / 64 * 64;
+    w.m_tiles = (M + kTileTokens[0] - 1) / kTileTokens[0];
+    int64_t slots = 0, partial_rows = M;
+    for (int bt : kTileTokens) {
+        w.slot_pitch = num < bt ? num : bt;   // (the last one, of the widest tile, stays)
+        const int64_t n = (M + bt - 1) / bt * w.slot_pitch;
+        if (n > slots) slots = n;
+    }
+    // k slices are taken up to the M where `busy` (see shrink_slices) passes 2 * kSmsAssumed / k
+    for (int64_t k = 2; k <= kMaxSlices && k <= w.red64 / 64; ++k) {
+        const int64_t busy = 2 * kSmsAssumed / k, past = (busy - num) * kShrinkTokens + kShrinkTokens - 1;
+        int64_t m = past > busy ? past : busy;
+        if (m > M) m = M;
+        if (k * m > partial_rows) partial_rows = k * m;
+    }
+    lay_out(w, M, rows, num, rank, slots, partial_rows);
+    return w.total;
 }
 
 lowbit_status launch_plan(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {

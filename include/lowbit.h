@@ -281,7 +281,7 @@ lowbit_status lowbit_transpose(const uint32_t* packed, int64_t N, int64_t K, int
                                void* stream);
 
 /* Bytes of workspace for the three entry points below (num = rank = 0 for lowbit_gemm_dx): one
- * size for the forward and backward of a linear. It holds the fp16 copy of the wider of X and dY and,
+ * size for the forward and backward of a linear, with M tokens or any fewer. It holds the fp16 copy of the wider of X and dY and,
  * with adapters, the tokens' order, the low-rank products and up to
  * M * min(num, 256) * (rank rounded up to a power of two >= 16) bf16 values. 0 for invalid arguments. */
 size_t lowbit_adapter_workspace_size(int64_t M, int64_t N, int64_t K, int num, int rank);

@@ -18,3 +18,13 @@ def test_workspace_size_of_an_empty_linear(N, K):
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr
     assert all(int(n) % 256 == 0 for n in r.stdout.split())
+
+
+@pytest.mark.parametrize("N,K", [(4096, 4096), (9728, 2560), (384, 7680), (136, 256), (9216, 9216)])
+@pytest.mark.parametrize("R", [8, 32, 128])
+@pytest.mark.parametrize("L", [0, 1, 3, 64, 256, 300, 4096])
+def test_workspace_of_a_larger_batch_serves_a_smaller_one(N, K, R, L):
+    """The size never falls as the batch grows, through every choice of tile and of K slices."""
+    size = lb.load().lowbit_adapter_workspace_size
+    sizes = [size(M, N, K, L, R if L else 0) for M in [*range(0, 2400), *range(2400, 41000, 61)]]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))

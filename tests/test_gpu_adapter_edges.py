@@ -1,0 +1,26 @@
+"""Adapters, gradients and 8-bit copies on the GPU at the edges of what the entry points take, against the
+64-bit references of tests/_adapters.py."""
+import pytest
+import torch
+
+import bit_weight_only_w2_b200 as lb
+from tests._adapters import Problem, backward_ref, check, forward_ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("N,K,L,R,M,largest", [(4096, 4096, 256, 128, 147, 148), (1024, 512, 64, 32, 256, 257),
+                                               (1032, 640, 300, 64, 88, 768), (264, 256, 4096, 128, 19, 64)])
+def test_workspace_of_a_larger_batch(N, K, L, R, M, largest):
+    """A batch on the workspace of a larger one gets what it gets on its own, and leaves what lies behind."""
+    pr = Problem(M, K, N, 2, 64, L, R, "random")
+    size = lb.adapter_workspace_size(largest, N, K, L, R)
+    ws = torch.full((size + 256,), 9, dtype=torch.uint8, device="cuda")
+    y = lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args(), ws=ws[:size])
+    got = lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args(), ws=ws[:size])
+    assert lb.device_status() == 0 and (ws[size:] == 9).all()
+    assert torch.equal(y, lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args()))
+    ry, ey, _, _ = forward_ref(pr)
+    check(y, ry, ey, "y")
+    for (r, e), g in zip(backward_ref(pr, pr.x), got):
+        check(g, r, e, "gradient")
