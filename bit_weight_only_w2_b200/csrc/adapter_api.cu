@@ -42,7 +42,7 @@ lowbit_status check_linear(int64_t M, int64_t N, int64_t K, int bits, int gs, co
 
 lowbit_status check_adapters(const lowbit_adapters* a, int64_t N, int64_t K) {
     if (!a || a->num < 1 || a->rank < 1) return LOWBIT_ERR_INVALID_ARG;
-    if (!a->A || !a->B || !a->scaling) return LOWBIT_ERR_INVALID_ARG;
+    if (!a->A || (N > 0 && !a->B) || !a->scaling) return LOWBIT_ERR_INVALID_ARG;
     if (!aligned(a->A, 16) || !aligned(a->B, 16) || !aligned(a->scaling, 4) || !aligned(a->index, 4))
         return LOWBIT_ERR_ALIGNMENT;
     if (a->num > kMaxAdapters || a->rank > kMaxRank || a->rank % 8 != 0) return LOWBIT_ERR_UNSUPPORTED;
@@ -126,7 +126,8 @@ LOWBIT_API lowbit_status lowbit_adapter_gemm(int64_t M, int64_t N, int64_t K, in
     if (st != LOWBIT_OK) return st;
     if ((st = check_adapters(adapters, N, K)) != LOWBIT_OK || (st = check_copy(ck_codes, ck_exps)) != LOWBIT_OK) return st;
     if (!aligned(P, 16)) return LOWBIT_ERR_ALIGNMENT;
-    if (M == 0 || N == 0) return LOWBIT_OK;
+    if (M == 0) return LOWBIT_OK;
+    if (N == 0) return P || ck_codes ? LOWBIT_ERR_UNSUPPORTED : LOWBIT_OK;   // (neither P nor the copy is empty)
     ExtProblem e;
     e.M = M;
     e.rows = e.N = N;

@@ -297,7 +297,8 @@ size_t lowbit_adapter_workspace_size(int64_t M, int64_t N, int64_t K, int num, i
  * once. An infinity or NaN in one adapter reaches its own tokens only. (More than 16 tokens with an
  * index: an adapter whose B is not finite throughout gives its tokens NaN in every column.) Nothing
  * that the call reads may be written by concurrent work, and Wp, scales and zeros not by the kernel
- * enqueued immediately before the call, as for lowbit_gemm. Results do not depend on timing. */
+ * enqueued immediately before the call, as for lowbit_gemm. Results do not depend on timing. N == 0 is a
+ * no-op only where neither P nor the copy is asked for, else LOWBIT_ERR_UNSUPPORTED. */
 lowbit_status lowbit_adapter_gemm(int64_t M, int64_t N, int64_t K, int bits, int group_size, const void* X,
                                   const uint32_t* Wp, const void* scales, const void* zeros,
                                   const lowbit_adapters* adapters, void* Y, void* P, uint8_t* ck_codes,
@@ -315,7 +316,7 @@ lowbit_status lowbit_gemm_dx(int64_t M, int64_t N, int64_t K, int bits, int grou
  *   X    bf16 [M][K], or NULL with its 8-bit copy in ck_codes / ck_exps
  *   dX   bf16 [M][K], or NULL if it is not needed
  *   dA   bf16 [L][R][K], dB bf16 [L][N][R]: written in full (zero for an adapter without tokens)
- * all 16-byte aligned. Sums are fp32, in a fixed order; dp is rounded to bf16 once for dX and kept in two
+ * N > 0 (else LOWBIT_ERR_UNSUPPORTED); all 16-byte aligned. Sums are fp32, in a fixed order; dp is rounded to bf16 once for dX and kept in two
  * bf16 terms (2^-16) for dA; dA, dB and dX are rounded once each. An infinity or NaN in one adapter reaches
  * its own tokens' dX (NaN in every column if its A is not finite throughout and there is an index) and its
  * own dA and dB only; an infinity in X may reach dA as NaN. */

@@ -6,6 +6,7 @@ import sys
 import pytest
 
 import bit_weight_only_w2_b200 as lb
+from tests.test_adapter_abi import A, adapters, backward, forward
 
 
 @pytest.mark.parametrize("N,K", [(0, 64), (64, 0), (0, 0)])
@@ -28,3 +29,15 @@ def test_workspace_of_a_larger_batch_serves_a_smaller_one(N, K, R, L):
     size = lb.load().lowbit_adapter_workspace_size
     sizes = [size(M, N, K, L, R if L else 0) for M in [*range(0, 2400), *range(2400, 41000, 61)]]
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+def test_a_linear_without_rows_leaves_nothing_unwritten():
+    """N = 0: nothing to do for Y, but P and the 8-bit copy are not empty, so a call that asks for them is
+    refused instead of returning OK with both as they were. B is empty then, and may be null."""
+    lib = lb.load()
+    assert forward(lib, adapters(), N=0, P=A) == 3
+    assert forward(lib, adapters(), N=0, codes=A, exps=A) == 3
+    assert forward(lib, adapters(B=None), N=0) == 0
+    assert forward(lib, adapters(), N=0, M=0, P=A, codes=A, exps=A) == 0
+    assert forward(lib, adapters(B=None)) == 1
+    assert backward(lib, adapters(B=None), N=0, dB=None) == 3

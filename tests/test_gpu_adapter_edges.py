@@ -24,3 +24,18 @@ def test_workspace_of_a_larger_batch(N, K, L, R, M, largest):
     check(y, ry, ey, "y")
     for (r, e), g in zip(backward_ref(pr, pr.x), got):
         check(g, r, e, "gradient")
+
+
+def test_a_linear_without_rows():
+    pr = Problem(20, 256, 8, 2, 64, 2, 16)
+    none = dict(packed=pr.packed[:0], scales=pr.scales[:, :0].contiguous(), zeros=None, bits=2, group_size=64, a=pr.a,
+                b=pr.b[:, :0].contiguous(), scaling=pr.scaling, index=pr.index)
+    assert lb.adapter_gemm(pr.x, **none).shape == (20, 0)
+    with pytest.raises(lb.LowbitError, match="UNSUPPORTED"):
+        lb.adapter_gemm(pr.x, **none, p=pr.p)
+    with pytest.raises(lb.LowbitError, match="UNSUPPORTED"):
+        lb.adapter_gemm(pr.x, **none, checkpoint=lb.checkpoint_empty(20, 256, "cuda"))
+    dy, wt = pr.dy[:, :0].contiguous(), pr.packed_t[:, :0].contiguous()
+    assert not lb.gemm_dx(dy, wt, none["scales"], None, 2, 64).any()      # a sum over nothing
+    with pytest.raises(lb.LowbitError, match="UNSUPPORTED"):
+        lb.adapter_backward(dy, pr.x, pr.p, wt, none["scales"], None, 2, 64, pr.a, none["b"], pr.scaling, pr.index)
