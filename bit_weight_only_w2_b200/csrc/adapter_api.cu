@@ -40,13 +40,12 @@ lowbit_status check_linear(int64_t M, int64_t N, int64_t K, int bits, int gs, co
     return validate_gemm(linear_problem(M, N, K, bits, gs, in, W, scales, zeros, out));
 }
 
-lowbit_status check_adapters(const lowbit_adapters* a, int64_t N, int64_t K) {
+lowbit_status check_adapters(const lowbit_adapters* a, int64_t N) {
     if (!a || a->num < 1 || a->rank < 1) return LOWBIT_ERR_INVALID_ARG;
     if (!a->A || (N > 0 && !a->B) || !a->scaling) return LOWBIT_ERR_INVALID_ARG;
     if (!aligned(a->A, 16) || !aligned(a->B, 16) || !aligned(a->scaling, 4) || !aligned(a->index, 4))
         return LOWBIT_ERR_ALIGNMENT;
     if (a->num > kMaxAdapters || a->rank > kMaxRank || a->rank % 8 != 0) return LOWBIT_ERR_UNSUPPORTED;
-    if ((N + 127) / 128 + (K + 127) / 128 > 65535) return LOWBIT_ERR_UNSUPPORTED;   // a grid dimension
     return LOWBIT_OK;
 }
 
@@ -124,7 +123,7 @@ LOWBIT_API lowbit_status lowbit_adapter_gemm(int64_t M, int64_t N, int64_t K, in
                                              uint8_t* ck_exps, void* workspace, size_t workspace_bytes, void* stream) {
     lowbit_status st = check_linear(M, N, K, bits, group_size, X, Wp, scales, zeros, Y);
     if (st != LOWBIT_OK) return st;
-    if ((st = check_adapters(adapters, N, K)) != LOWBIT_OK || (st = check_copy(ck_codes, ck_exps)) != LOWBIT_OK) return st;
+    if ((st = check_adapters(adapters, N)) != LOWBIT_OK || (st = check_copy(ck_codes, ck_exps)) != LOWBIT_OK) return st;
     if (!aligned(P, 16)) return LOWBIT_ERR_ALIGNMENT;
     if (M == 0) return LOWBIT_OK;
     if (N == 0) return P || ck_codes ? LOWBIT_ERR_UNSUPPORTED : LOWBIT_OK;   // (neither P nor the copy is empty)
@@ -199,7 +198,7 @@ LOWBIT_API lowbit_status lowbit_adapter_backward(int64_t M, int64_t N, int64_t K
     // (dX may be absent; the linear's checks want an output, so dA stands in)
     lowbit_status st = check_linear(M, N, K, bits, group_size, dY, Wt, scales, zeros, dX ? dX : dA);
     if (st != LOWBIT_OK) return st;
-    if ((st = check_adapters(adapters, N, K)) != LOWBIT_OK || (st = check_copy(ck_codes, ck_exps)) != LOWBIT_OK) return st;
+    if ((st = check_adapters(adapters, N)) != LOWBIT_OK || (st = check_copy(ck_codes, ck_exps)) != LOWBIT_OK) return st;
     if (!dA || (N > 0 && !dB)) return LOWBIT_ERR_INVALID_ARG;
     if (M > 0 && (!P || (X == nullptr) == (ck_codes == nullptr))) return LOWBIT_ERR_INVALID_ARG;
     if (N == 0) return LOWBIT_ERR_UNSUPPORTED;

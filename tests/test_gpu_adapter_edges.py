@@ -39,3 +39,16 @@ def test_a_linear_without_rows():
     assert not lb.gemm_dx(dy, wt, none["scales"], None, 2, 64).any()      # a sum over nothing
     with pytest.raises(lb.LowbitError, match="UNSUPPORTED"):
         lb.adapter_backward(dy, pr.x, pr.p, wt, none["scales"], None, 2, 64, pr.a, none["b"], pr.scaling, pr.index)
+
+
+def test_a_linear_of_many_rows():
+    """More than 65535 row tiles of 128, in both directions."""
+    pr = Problem(20, 64, (1 << 23) + 136, 2, 64, 2, 8, "random")
+    y = lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args())
+    ry, ey, _, _ = forward_ref(pr)
+    check(y, ry, ey, "y")
+    del y, ry, ey
+    got = lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args())
+    assert lb.device_status() == 0
+    for (r, e), g in zip(backward_ref(pr, pr.x), got):
+        check(g, r, e, "gradient")
