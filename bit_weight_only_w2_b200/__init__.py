@@ -550,8 +550,8 @@ def adapter_gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, ze
         _check_like(out, "out", (M, N), _BF16, x.device)
     if p is not None and not _fits(p, _BF16, (M, R), dev):
         _check_like(p, "p", (M, R), _BF16, x.device)
-    if checkpoint is not None and not _copy_fits(checkpoint, M, K, dev):
-        _check_checkpoint(checkpoint, M, K, x.device)
+    if checkpoint is not None and not _copy_fits(Checkpoint(codes, exps), M, K, dev):   # (any pair will do)
+        _check_checkpoint(Checkpoint(codes, exps), M, K, x.device)
     ad = Adapters(L, R, a.data_ptr(), b.data_ptr(), scaling.data_ptr(), _ptr(index))
     with _on_device(dev):
         ws, ws_bytes = _own_workspace(ws, x, M, N, K, L, R)

@@ -52,3 +52,21 @@ def test_a_linear_of_many_rows():
     assert lb.device_status() == 0
     for (r, e), g in zip(backward_ref(pr, pr.x), got):
         check(g, r, e, "gradient")
+
+
+@pytest.mark.parametrize("compiled", [True, False])
+def test_a_pair_as_checkpoint(compiled, monkeypatch):
+    """A plain (codes, exps) pair is taken with the compiled marshalling and without it, and checked."""
+    if not compiled:
+        calls = object.__new__(lb._Marshalled)
+        calls.lib = lb.load()
+        calls.adapter_gemm = lambda *args: None
+        monkeypatch.setattr(lb, "_marshalled", calls)
+    pr = Problem(20, 256, 136, 2, 64, 2, 16)
+    want = lb.checkpoint_empty(20, 256, "cuda")
+    y = lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args(), checkpoint=want)
+    codes, exps = torch.zeros_like(want.codes), torch.zeros_like(want.exps)
+    assert torch.equal(lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args(), checkpoint=(codes, exps)), y)
+    assert torch.equal(codes.view(torch.uint8), want.codes.view(torch.uint8)) and torch.equal(exps, want.exps)
+    with pytest.raises(ValueError, match="checkpoint"):
+        lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args(), checkpoint=(codes[1:], exps))
