@@ -4,7 +4,8 @@
 
 Objects go to ``_build/`` at the repository root; the shared library is written next to this
 file so the Python binding (and a copy of the tree on another machine) finds it, and beside it
-_marshal.so, which marshals the arguments of the binding's short calls (g++). ``--debug``
+_marshal.so, which marshals the arguments of the binding's short calls (g++ and PyTorch's headers;
+where they are missing the library is built all the same). ``--debug``
 builds liblowbit_debug.so instead: the same sources with device-side index checks
 (LOWBIT_DEBUG_CHECKS), objects in ``_build/debug/``.
 """
@@ -14,6 +15,7 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -86,8 +88,20 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     return lib
 
 
-def build_marshal(force: bool = False) -> str:
-    """Build _marshal.so against the installed PyTorch; the binding uses it with that version only."""
+def build_marshal(force: bool = False) -> Optional[str]:
+    """Build _marshal.so against the installed PyTorch; the binding uses it with that version only, and does
+    without it where it is missing. So where it cannot be built (no PyTorch, no C++ compiler, no headers) this
+    says so on stderr and returns None."""
+    try:
+        return _build_marshal(force)
+    except (ImportError, OSError, RuntimeError) as e:
+        if os.path.exists(MARSHAL_LIB):   # (of other sources or another PyTorch)
+            os.remove(MARSHAL_LIB)
+        print(f"_marshal.so was not built, the binding marshals in Python: {e}", file=sys.stderr)
+        return None
+
+
+def _build_marshal(force: bool) -> str:
     import sysconfig
 
     import torch
@@ -100,12 +114,13 @@ def build_marshal(force: bool = False) -> str:
     headers = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     tmp = MARSHAL_LIB + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DLOWBIT_TORCH_VERSION="{torch.__version__.split("+")[0]}"', f"-I{INCLUDE}",
            *(f"-isystem{h}" for h in headers), MARSHAL_SRC,
            "-o", tmp, f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, MARSHAL_LIB)
     return MARSHAL_LIB
 

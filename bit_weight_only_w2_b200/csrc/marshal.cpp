@@ -13,7 +13,6 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/headeronly/version.h>
 
 #include <cstdint>
 #include <exception>
@@ -314,7 +313,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, n
 PyMODINIT_FUNC PyInit__marshal(void) {
     PyObject* m = PyModule_Create(&module);
     // the PyTorch whose headers this was compiled with: the binding uses it with no other
-    if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) != 0) {
+    if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", LOWBIT_TORCH_VERSION) != 0) {
         Py_DECREF(m);
         return nullptr;
     }

@@ -1,0 +1,32 @@
+"""The build without what only the compiled marshalling needs: the library comes out all the same."""
+import os
+import sys
+
+import pytest
+
+from bit_weight_only_w2_b200 import build as b
+
+
+def compiler_missing(monkeypatch):
+    monkeypatch.setenv("CXX", "no-such-compiler")
+
+
+def compiler_failing(monkeypatch):
+    monkeypatch.setenv("CXX", "false")
+
+
+def torch_missing(monkeypatch):
+    monkeypatch.setitem(sys.modules, "torch", None)
+
+
+@pytest.mark.parametrize("without", [compiler_missing, compiler_failing, torch_missing])
+def test_build_without_the_marshalling(without, monkeypatch, tmp_path, capsys):
+    lib = tmp_path / "_marshal.so"
+    lib.write_bytes(b"of other sources")
+    os.utime(lib, (0, 0))
+    monkeypatch.setattr(b, "MARSHAL_LIB", str(lib))
+    monkeypatch.setattr(b, "sources", list)          # (the library as it is)
+    without(monkeypatch)
+    assert b.build() == b.LIB
+    assert list(tmp_path.iterdir()) == []
+    assert "_marshal.so was not built" in capsys.readouterr().err
