@@ -263,7 +263,7 @@ constexpr int kNarrowCols = RP < 64 ? RP : 64;
 // ---------------------------------------------------------------------------------------------
 // A block is up to 128 tokens of one adapter (the MMA's 128 rows); the reduction is cut into
 // slices over gridDim.y so that a few blocks fill the GPU, and the slices' fp32 partials are added
-// in order by the copy pass that follows. KMAJOR: the adapter's side is [R][red] (A); otherwise
+// by the pass that writes the slots' P (side_row). KMAJOR: the adapter's side is [R][red] (A); otherwise
 // [red][R] (B). Bound by the stream of the input and, beside it from L2, of the adapter's side, once a
 // block: 22 us cold for 4173 tokens x 9216 at rank 64 (3.7 TB/s of DRAM, 5.4 TB/s with L2).
 // A block of at most 32 tokens (a decode batch of many adapters) brings so few bytes a stage that its
@@ -516,8 +516,10 @@ struct SideArgs {
     bool beside;               // a copy without the slots' P that runs beside the shrink kernel
 };
 
-// P of one token: the slices' partials in order, times its adapter's scaling, in its slot's columns and
-// zeros in the tile's others. By T threads (`tid`), which `sync` joins; `scale`: the row's 2^-e.
+// P of one token: the sum of the slices' partials, times its adapter's scaling, in its slot's columns and
+// zeros in the tile's others. By T threads (`tid`), which `sync` joins; `scale`: the row's 2^-e. The sum's
+// order is fixed by T and the rank: slice after slice, or (T == 32) strided over groups of lanes and then
+// across them, so p's last bits may differ between batches that the copy pass and side_kernel handle.
 template <int T, class Sync>
 __device__ __forceinline__ void side_row(const SideArgs& s, int row, int M, float scale, int tid, float* prow, Sync sync) {
     const int slot = s.token_slot ? s.token_slot[row] : 0;
@@ -1078,22 +1080,17 @@ __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(co
 // Host side
 // ---------------------------------------------------------------------------------------------
 template <class... Args, class... Given>
-lowbit_status launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, int smem, int cluster_x, cudaStream_t stream,
-                         Given... args) {
+lowbit_status launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, Given... args) {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attrs[2];
+    cudaLaunchAttribute attrs[1];
     attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attrs[0].val.programmaticStreamSerializationAllowed = 1;
-    attrs[1].id = cudaLaunchAttributeClusterDimension;
-    attrs[1].val.clusterDim.x = cluster_x;
-    attrs[1].val.clusterDim.y = 1;
-    attrs[1].val.clusterDim.z = 1;
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attrs;
-    cfg.numAttrs = cluster_x > 1 ? 2 : 1;
+    cfg.numAttrs = 1;
     if (take_injected_failure(kInjectLaunch)) return LOWBIT_ERR_CUDA;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(args)...) == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
@@ -1152,7 +1149,7 @@ lowbit_status shrink_launch(const ExtProblem& e, const ExtBuffers& b, cudaStream
     p.partial = b.at<float>(w.partial);
     const int64_t num_blocks = e.ad.index ? w.num_blocks : (e.M + kShrinkTokens - 1) / kShrinkTokens;
     return launch_pdl(fn, dim3(static_cast<unsigned>(num_blocks), static_cast<unsigned>(w.ksplit), 1), kShrinkThreads,
-                      kShrinkSmem<RP>, 1, stream, p);
+                      kShrinkSmem<RP>, stream, p);
 }
 
 template <int RP>
@@ -1177,7 +1174,7 @@ lowbit_status wgrad_launch(const WgradProblem& g, WgradArgs& a, cudaStream_t str
     if (!ok) return LOWBIT_ERR_CUDA;
     const int64_t items = static_cast<int64_t>(a.part[0].tiles + a.part[1].tiles) * g.num, slots = kWgradCtas<RP> * num_sms();
     return launch_pdl(fn, dim3(static_cast<unsigned>(items < slots ? items : slots), 1, 1), kWgradThreads,
-                      kWgradSmem<RP>, 1, stream, a);
+                      kWgradSmem<RP>, stream, a);
 }
 
 }  // namespace
@@ -1328,7 +1325,7 @@ size_t ext_workspace_bound(int64_t M, int64_t rows, int64_t red, int num, int ra
 
 lowbit_status launch_plan(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
     const ExtWorkspace& w = b.w;
-    return launch_pdl(plan_kernel, dim3(static_cast<unsigned>(e.ad.num + w.m_tiles), 1 + w.plan_slices, 1), kPlanThreads, 0, 1,
+    return launch_pdl(plan_kernel, dim3(static_cast<unsigned>(e.ad.num + w.m_tiles), 1 + w.plan_slices, 1), kPlanThreads, 0,
                       stream, e.ad.index, static_cast<int>(e.M), e.ad.num, w.tile_tokens, static_cast<int>(w.slot_pitch),
                       static_cast<int>(w.num_blocks), static_cast<const uint4*>(e.grad ? e.ad.A : e.ad.B),
                       e.rows * e.ad.rank / 8, b.at<int>(w.perm), b.at<int>(w.seg), b.at<int4>(w.blocks),
@@ -1345,7 +1342,7 @@ lowbit_status launch_shrink(const ExtProblem& e, const ExtBuffers& b, cudaStream
 }
 
 lowbit_status launch_shrink_small(const ExtProblem& e, float* p, cudaStream_t stream) {
-    return launch_pdl(shrink_small_kernel, dim3(e.ad.rank / 2, static_cast<unsigned>(e.M), 1), 32 * kShrinkSmallWarps, 0, 1,
+    return launch_pdl(shrink_small_kernel, dim3(e.ad.rank / 2, static_cast<unsigned>(e.M), 1), 32 * kShrinkSmallWarps, 0,
                       stream, static_cast<const uint4*>(e.in), static_cast<const uint4*>(e.ad.A),
                       static_cast<int>(e.red / 8), e.ad.rank, e.ad.num, e.ad.scaling, e.ad.index, p,
                       static_cast<__nv_bfloat16*>(e.p_out));
@@ -1382,7 +1379,7 @@ lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStrea
     uint4* xh = b.at<uint4>(w.xh);
     float* rm = b.at<float>(w.rowmul);
     auto go = [&](auto fn) {
-        return launch_pdl(fn, grid, kConvThreads, 0, 1, stream, in, static_cast<int>(e.M), K8, K8p, xh, rm, s);
+        return launch_pdl(fn, grid, kConvThreads, 0, stream, in, static_cast<int>(e.M), K8, K8p, xh, rm, s);
     };
     auto pick = [&](auto lr, auto ck) {
         constexpr bool LR = decltype(lr)::value, CK = decltype(ck)::value;
@@ -1397,7 +1394,7 @@ lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStrea
     s.beside = true;
     const lowbit_status st = s.codes ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{});
     if (st != LOWBIT_OK) return st;
-    return launch_pdl(side_kernel, dim3(static_cast<unsigned>((e.M + kSideWarps - 1) / kSideWarps), 1, 1), 32 * kSideWarps, 0, 1,
+    return launch_pdl(side_kernel, dim3(static_cast<unsigned>((e.M + kSideWarps - 1) / kSideWarps), 1, 1), 32 * kSideWarps, 0,
                       stream, static_cast<int>(e.M), rm, s);
 }
 
