@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     plan_kernel(const int* __restrict__ index, int M, int num, int tile_tokens, int slot_pitch, int num_blocks,
                 const uint4* __restrict__ side, int64_t side8, int* __restrict__ perm, int* __restrict__ seg,
                 int4* __restrict__ blocks, int* __restrict__ tile_slots, int* __restrict__ slot_adapter,
-                int* __restrict__ token_slot, int* __restrict__ odd_parts) {
+                int* __restrict__ token_slot, int* __restrict__ odd_parts, unsigned* status) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -119,13 +119,15 @@ __global__ void __launch_bounds__(kPlanThreads)
             const int m = mb + lane;
             const bool mine = m < m1 && adapter_of(index, m, num) == a;
             const unsigned votes = __ballot_sync(0xffffffffu, mine);
-            if (mine) perm[at + __popc(votes & ((1u << lane) - 1u))] = m;
+            const int to = at + __popc(votes & ((1u << lane) - 1u));
+            if (mine && dcheck(to >= 0 && to < M, status)) perm[to] = m;
             at += __popc(votes);
         }
         const int first = start / kShrinkTokens + a;
         const int last = a + 1 == num ? num_blocks : (start + count) / kShrinkTokens + a + 1;
         for (int i = threadIdx.x; first + i < last; i += kPlanThreads)
-            blocks[first + i] = make_int4(a, start + i * kShrinkTokens, min(kShrinkTokens, count - i * kShrinkTokens), i == 0);
+            if (dcheck(first + i < num_blocks, status))
+                blocks[first + i] = make_int4(a, start + i * kShrinkTokens, min(kShrinkTokens, count - i * kShrinkTokens), i == 0);
         if (threadIdx.x == 0) {
             seg[a] = start;
             if (a + 1 == num) seg[num] = start + count;
@@ -156,10 +158,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (int i = threadIdx.x; i < words; i += kPlanThreads) {
         unsigned b = bits[i];
         int at = base[i];
-        while (b) {
-            slot_adapter[static_cast<size_t>(tile) * slot_pitch + at++] = i * 32 + __ffs(b) - 1;
-            b &= b - 1;
-        }
+        for (; b; b &= b - 1, ++at)
+            if (dcheck(at < slot_pitch, status)) slot_adapter[static_cast<size_t>(tile) * slot_pitch + at] = i * 32 + __ffs(b) - 1;
     }
     for (int m = m0 + static_cast<int>(threadIdx.x); m < m1; m += kPlanThreads) {
         const int v = adapter_of(index, m, num);
@@ -381,13 +381,14 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(const __grid_
     if (count <= 0) return;
     if (tid < kShrinkTokens) {
         const int t = blk.y + min(tid, count - 1);
-        tok[tid] = p.perm ? p.perm[t] : t;
+        const int m = !dcheck(t >= 0 && t < p.M, p.status) ? 0 : p.perm ? p.perm[t] : t;
+        tok[tid] = dcheck(m >= 0 && m < p.M, p.status) ? m : 0;
     }
     if (blk.w && blockIdx.y == 0) {   // the adapter's first block: join the parts of its weight side's look-over
         int odd = 0;
         for (int i = tid; i < p.slices; i += kShrinkThreads) odd |= p.odd_parts[static_cast<size_t>(i) * p.num + blk.x];
         odd = __syncthreads_or(odd);
-        if (tid == 0) p.bad[blk.x] = odd;
+        if (tid == 0 && dcheck(blk.x >= 0 && blk.x < p.num, p.status)) p.bad[blk.x] = odd;
     }
     if (tid == 0) {
         gather_init(g, kBars, 1);
@@ -514,6 +515,7 @@ struct SideArgs {
     uint8_t* codes;            // 8-bit copy
     uint8_t* exps;
     bool beside;               // a copy without the slots' P that runs beside the shrink kernel
+    unsigned* status;          // the device status word
 };
 
 // P of one token: the sum of the slices' partials, times its adapter's scaling, in its slot's columns and
@@ -572,8 +574,9 @@ __device__ __forceinline__ void side_row(const SideArgs& s, int row, int M, floa
     if (s.bad && (row & ((1 << s.tile_log2) - 1)) == 0) {        // a tile's first row: its slots' weight sides
         const size_t at = static_cast<size_t>(row >> s.tile_log2) * s.slot_pitch;
         for (int i = tid; i < cols >> s.rp_log2; i += T) {
+            if (!dcheck(i < s.slot_pitch, s.status)) break;
             const int b = s.slot_adapter[at + i];
-            s.slot_side[at + i] = s.bad[b] ? s.num : b;
+            if (dcheck(b >= 0 && b < s.num, s.status)) s.slot_side[at + i] = s.bad[b] ? s.num : b;
         }
     }
     uint4* pd = reinterpret_cast<uint4*>(s.pslots + static_cast<size_t>(row) * s.p_cols);
@@ -592,7 +595,7 @@ __device__ __forceinline__ void side_row(const SideArgs& s, int row, int M, floa
             }
             o = make_uint4(u[0], u[1], u[2], u[3]);
         }
-        pd[c] = o;
+        if (dcheck(c * 8 + 8 <= s.p_cols && slot < s.slot_pitch, s.status)) pd[c] = o;
     }
 }
 
@@ -813,6 +816,11 @@ __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(co
         }
         return it;
     };
+    auto token_of = [&](const Item& it, int t) {
+        if (!dcheck(it.seg0 >= 0 && it.seg0 + t < w.M, w.status)) return 0;
+        const int m = w.perm ? w.perm[it.seg0 + t] : t;
+        return dcheck(m >= 0 && m < w.M, w.status) ? m : 0;
+    };
     if (warp == 0) {
         // ---------------------------------------------------------------- gather
         // lane -> token rows 4 (lane % 16) .. + 3 of a stage, columns 64 (lane / 16) .. of G
@@ -821,7 +829,7 @@ __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(co
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int t = step * 64 + row + i;
-                r[i] = t >= it.count ? w.M : w.perm ? w.perm[it.seg0 + t] : t;   // (row M: zeros)
+                r[i] = t >= it.count ? w.M : token_of(it, t);   // (row M: zeros)
             }
         };
         // the stage whose rows are asked for next, two ahead of the one that is copied
@@ -963,7 +971,7 @@ __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(co
 #pragma unroll
                 for (int j = 0; j < kRowsOf; ++j) {
                     const int t = step * 64 + row0 + kStep * j;
-                    id[j] = t < cur.count && c_ok ? (w.perm ? w.perm[cur.seg0 + t] : t) : -1;
+                    id[j] = t < cur.count && c_ok ? token_of(cur, t) : -1;
                 }
             };
             auto exps_of = [&](const int (&id)[kRowsOf], uint32_t (&e)[kRowsOf]) {
@@ -1048,10 +1056,10 @@ __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(co
                         const uint32_t other = __shfl_xor_sync(0xffffffffu, u[j], 1);
                         const uint32_t word = even ? __byte_perm(u[j], other, 0x5410) : __byte_perm(other, u[j], 0x7632);
                         const int r = r0 + 2 * j + (even ? 0 : 1), ce = c & ~1;
-                        if (r < R && ce < C)
+                        if (r < R && ce < C && dcheck(it.a < w.num && ce >= 0 && ce + 1 < C, w.status))
                             *reinterpret_cast<uint32_t*>(out + (static_cast<size_t>(it.a) * R + r) * C + ce) = word;
                     }
-                } else if (c < C) {
+                } else if (c < C && dcheck(it.a < w.num && c >= 0 && r0 + 8 <= R, w.status)) {
                     // dB [a][C][R]: eight ranks a store
                     uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<size_t>(it.a) * C + c) * R + r0);
                     dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
@@ -1325,11 +1333,14 @@ size_t ext_workspace_bound(int64_t M, int64_t rows, int64_t red, int num, int ra
 
 lowbit_status launch_plan(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
     const ExtWorkspace& w = b.w;
+    unsigned* status = device_status_address();
+    if (!status) return LOWBIT_ERR_CUDA;
     return launch_pdl(plan_kernel, dim3(static_cast<unsigned>(e.ad.num + w.m_tiles), 1 + w.plan_slices, 1), kPlanThreads, 0,
                       stream, e.ad.index, static_cast<int>(e.M), e.ad.num, w.tile_tokens, static_cast<int>(w.slot_pitch),
                       static_cast<int>(w.num_blocks), static_cast<const uint4*>(e.grad ? e.ad.A : e.ad.B),
                       e.rows * e.ad.rank / 8, b.at<int>(w.perm), b.at<int>(w.seg), b.at<int4>(w.blocks),
-                      b.at<int>(w.tile_slots), b.at<int>(w.slot_adapter), b.at<int>(w.token_slot), b.at<int>(w.odd_parts));
+                      b.at<int>(w.tile_slots), b.at<int>(w.slot_adapter), b.at<int>(w.token_slot), b.at<int>(w.odd_parts),
+                      status);
 }
 
 lowbit_status launch_shrink(const ExtProblem& e, const ExtBuffers& b, cudaStream_t stream) {
@@ -1352,6 +1363,8 @@ lowbit_status launch_convert(const ExtProblem& e, const ExtBuffers& b, cudaStrea
     const ExtWorkspace& w = b.w;
     SideArgs s = {};
     if (e.ad.num > 0) {
+        s.status = device_status_address();
+        if (!s.status) return LOWBIT_ERR_CUDA;
         s.partial = b.at<float>(w.partial);
         s.ksplit = w.ksplit;
         s.rp_log2 = slot_log2(e.ad.rank);

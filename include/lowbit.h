@@ -231,8 +231,9 @@ lowbit_status lowbit_test_fail_next(int what);
 
 /* 1 if this library was built with device-side index checks (LOWBIT_DEBUG_CHECKS, shipped as
  * liblowbit_debug.so), else 0. In such a build every global store of Y, every load of a row
- * factor and every tensor-memory store of decoded weights first checks its index against the
- * problem's bounds; a failed check records LOWBIT_ERR_DEVICE_CHECK in the device status word
+ * factor and every tensor-memory store of decoded weights, and with adapters every list entry that
+ * another kernel wrote (tokens sorted by adapter, blocks, slots) and every store of dA and dB, first
+ * checks its index against the problem's bounds; a failed check records LOWBIT_ERR_DEVICE_CHECK in the device status word
  * and skips the access instead of trapping, so the context stays usable. */
 int lowbit_debug_checks_enabled(void);
 

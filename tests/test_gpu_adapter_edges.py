@@ -70,3 +70,33 @@ def test_a_pair_as_checkpoint(compiled, monkeypatch):
     assert torch.equal(codes.view(torch.uint8), want.codes.view(torch.uint8)) and torch.equal(exps, want.exps)
     with pytest.raises(ValueError, match="checkpoint"):
         lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args(), checkpoint=(codes[1:], exps))
+
+
+@pytest.mark.parametrize("M,K,N,L,R,index", [(9, 256, 136, 3, 24, "holes"), (17, 256, 136, 4096, 16, "random"),
+                                             (150, 384, 264, 5, 128, "sorted"), (900, 256, 520, 40, 32, "holes"),
+                                             (900, 512, 264, 1, 64, None), (2100, 192, 264, 300, 8, "random")])
+@pytest.mark.parametrize("eight", [False, True])
+def test_index_checks(M, K, N, L, R, index, eight):
+    """The build with device-side index checks: none fires, through every kernel of the entry points (up to
+    16 tokens, P by the copy pass and by a kernel of its own, x in bf16 and in 8 bits, far more adapters than
+    the batch uses), and the results are the release build's."""
+    pr = Problem(M, K, N, 2, 64, L, R, index)
+
+    def run():
+        p, ck = torch.empty(M, R, dtype=torch.bfloat16, device="cuda"), lb.checkpoint_empty(M, K, "cuda")
+        y = lb.adapter_gemm(pr.x, pr.packed, *pr.args(), *pr.adapter_args(), p=p, checkpoint=ck)
+        g = lb.adapter_backward(pr.dy, ck if eight else pr.x, p, pr.packed_t, *pr.args(), *pr.adapter_args())
+        assert lb.device_status() == 0
+        return y, p, ck.codes.view(torch.uint8), ck.exps, *g, lb.gemm_dx(pr.dy, pr.packed_t, *pr.args())
+
+    want = run()
+    release = lb._lib
+    try:
+        lb._lib = lb.load_debug()
+        assert lb._lib.lowbit_debug_checks_enabled() == 1
+        got = run()
+    finally:
+        lb._lib = release
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    ry, ey, _, _ = forward_ref(pr)
+    check(want[0], ry, ey, "y")
