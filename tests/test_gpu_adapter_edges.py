@@ -100,3 +100,25 @@ def test_index_checks(M, K, N, L, R, index, eight):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     ry, ey, _, _ = forward_ref(pr)
     check(want[0], ry, ey, "y")
+
+
+@pytest.mark.parametrize("M", [9, 40, 300])
+@pytest.mark.parametrize("K,N", [(9216, 136), (256, 9216)])
+def test_adapters_past_32_bits(M, K, N):
+    """More than 2^31 values in A and dA, or in B and dB: the first and the last adapter in use, the others
+    without tokens."""
+    L, R = 1830, 128
+    pr = Problem(M, K, N, 2, 64, 2, R, "random")
+    assert L * R * max(K, N) > 1 << 31
+    a, b = (torch.zeros(L, *t.shape[1:], dtype=torch.bfloat16, device="cuda") for t in (pr.a, pr.b))
+    scaling, ends = torch.ones(L, device="cuda"), [0, L - 1]
+    a[ends], b[ends], scaling[ends] = pr.a, pr.b, pr.scaling
+    index = pr.index * (L - 1)
+    y = lb.adapter_gemm(pr.x, pr.packed, *pr.args(), a, b, scaling, index)
+    ry, ey, _, _ = forward_ref(pr)
+    check(y, ry, ey, "y")
+    dx, da, db = lb.adapter_backward(pr.dy, pr.x, pr.p, pr.packed_t, *pr.args(), a, b, scaling, index)
+    assert lb.device_status() == 0
+    for (r, e), g, name in zip(backward_ref(pr, pr.x), (dx, da[ends], db[ends]), ("dx", "da", "db")):
+        check(g, r, e, name)
+    assert not da[1:-1].any() and not db[1:-1].any()
