@@ -529,7 +529,10 @@ def adapter_gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, ze
 
     a bf16 [L][R][K], b bf16 [L][N][R], scaling fp32 [L], index int32 [M] (values outside 0..L-1: no
     adapter; None: adapter 0 for every token). For training, pass buffers that the backward reads:
-    `p` bf16 [M][R] and, to keep X in 8 bits, `checkpoint` (checkpoint_empty(M, K, device))."""
+    `p` bf16 [M][R] and, to keep X in 8 bits, `checkpoint` (checkpoint_empty(M, K, device)). No autograd
+    graph is recorded, whatever requires_grad says of the inputs: the caller calls adapter_backward (from a
+    torch.autograd.Function, say). With an index and more than 16 tokens, an adapter whose b is not finite
+    throughout gives its own tokens NaN in every column; else only the columns concerned change."""
     codes, exps = checkpoint if checkpoint is not None else (None, None)
     r = _calls().adapter_gemm(x, packed, scales, zeros, bits, group_size, a, b, scaling, index, out, p, codes, exps, ws)
     if r is not None:
@@ -585,7 +588,8 @@ def _check_grad_args(dy, packed_t, scales, zeros, bits: int, group_size: int):
 
 def gemm_dx(dy: torch.Tensor, packed_t: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor], bits: int,
             group_size: int, out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """dX = dY W, the input gradient of gemm (dy bf16 [M][N], packed_t from transpose_packed)."""
+    """dX = dY W, the input gradient of gemm (dy bf16 [M][N], packed_t from transpose_packed). Like gemm
+    it records no autograd graph."""
     r = _calls().gemm_dx(dy, packed_t, scales, zeros, bits, group_size, out, ws)
     if r is not None:
         if type(r) is int:
@@ -616,7 +620,8 @@ def adapter_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint], p: to
     """Gradients of adapter_gemm: (dx [M][K], da [L][R][K], db [L][N][R]), all bf16.
 
     x is the forward's input, or the Checkpoint it filled; p what it wrote. need_dx=False skips
-    dx (a first layer) and returns None in its place."""
+    dx (a first layer) and returns None in its place. Called by the user: adapter_gemm records no
+    autograd graph, and this call has no gradients of its own."""
     xs = (None, x.codes, x.exps) if isinstance(x, Checkpoint) else (x, None, None)
     r = _calls().adapter_backward(dy, packed_t, scales, zeros, bits, group_size, a, b, scaling, index, *xs, p, dx, da, db,
                                   need_dx, ws)

@@ -492,7 +492,8 @@ __global__ void __launch_bounds__(32 * kShrinkSmallWarps)
 // largest |value|). P is multiplied by 2^-e as well, since the epilogue multiplies the whole sum
 // by 2^e; that is exact in bf16. p (in the backward dp) itself is rounded to bf16 once as the MMA's
 // operand: 2^-8 of each entry at most, like the output's own rounding, and there beside the larger
-// product with W. dA has nothing beside it, so it gets dp in two bf16 terms, the second for what the first
+// product with W (2.0e-3 off in the norm against 64 bits where adapters weigh most, 1.7e-3 with p in fp32 as
+// up to 16 tokens have it; a second term would double the slots' columns). dA has nothing beside it, so it gets dp in two bf16 terms, the second for what the first
 // leaves (2^-16): with the first alone it was 2.4e-3 off in the norm against 64 bits, and more where a few
 // large channels of x rule it, with both 1.7e-3, which is the rounding of the result.
 struct SideArgs {

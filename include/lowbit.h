@@ -294,8 +294,8 @@ size_t lowbit_adapter_workspace_size(int64_t M, int64_t N, int64_t K, int num, i
  *   ck_codes  [M][K] bytes, 16-byte aligned, and ck_exps [M][K/32] bytes, or both NULL: the 8-bit copy
  *             of X (see lowbit_checkpoint_store), written in the same pass over X
  *   workspace 256-byte aligned, >= lowbit_adapter_workspace_size(M, N, K, num, rank)
- * p is summed in fp32 and rounded to bf16 once; p B^T is added to X W^T in fp32, so Y is rounded
- * once. An infinity or NaN in one adapter reaches its own tokens only. (More than 16 tokens with an
+ * P is summed in fp32 and rounded to bf16 once; p B^T, of p in bf16 (up to 16 tokens in fp32), is added
+ * to X W^T in fp32, so Y is rounded once. An infinity or NaN in one adapter reaches its own tokens only. (More than 16 tokens with an
  * index: an adapter whose B is not finite throughout gives its tokens NaN in every column.) Nothing
  * that the call reads may be written by concurrent work, and Wp, scales and zeros not by the kernel
  * enqueued immediately before the call, as for lowbit_gemm. Results do not depend on timing. N == 0 is a
@@ -307,7 +307,8 @@ lowbit_status lowbit_adapter_gemm(int64_t M, int64_t N, int64_t K, int bits, int
 
 /* dX = dY W, the input gradient of lowbit_gemm: dY bf16 [M][N], Wt from lowbit_transpose, dX bf16
  * [M][K], all 16-byte aligned; scales and zeros as for the forward. A uint4 weight is (q - z) * s
- * with the difference and the product rounded to fp16 (2^-11 relative each). */
+ * with the difference and the product rounded to fp16 (2^-11 relative each; 2^-25 absolute for products
+ * below fp16's normal range). */
 lowbit_status lowbit_gemm_dx(int64_t M, int64_t N, int64_t K, int bits, int group_size, const void* dY,
                              const uint32_t* Wt, const void* scales, const void* zeros, void* dX, void* workspace,
                              size_t workspace_bytes, void* stream);
