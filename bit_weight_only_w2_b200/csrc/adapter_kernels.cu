@@ -185,6 +185,17 @@ __host__ __device__ constexpr int gather_stage(int rp) { return kWideBytes + rp 
 __device__ __forceinline__ void* shared_ptr(uint32_t a) {
     return reinterpret_cast<void*>(__cvta_shared_to_generic(a));
 }
+// Sixteen bytes of shared memory, read where this stands: an ordinary load whose value is used only later may
+// take effect later, behind an arrival that hands the bytes back (in the tensor-memory product such loads
+// read a stage that had been refilled).
+__device__ __forceinline__ uint4 shared_now(const void* from) {
+    uint4 v;
+    asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(smem_u32(from))
+                 : "memory");
+    return v;
+}
 // Four rows of a 2-D tensor map whose box is one row high, to consecutive rows of shared memory.
 // Rows outside the tensor arrive as zeros.
 __device__ __forceinline__ void tma_gather4(const CUtensorMap* map, uint64_t* bar, uint32_t dst, int x, const int (&r)[4]) {
@@ -995,7 +1006,7 @@ __global__ void __launch_bounds__(kWgradThreads, kWgradCtas<RP>) wgrad_kernel(co
                 uint4 c[kRowsOf];
 #pragma unroll
                 for (int j = 0; j < kRowsOf; ++j)
-                    c[j] = *reinterpret_cast<const uint4*>(tile + kWideBytes - kRawBytes + (row0 + kStep * j) * 128 + ch * 16);
+                    c[j] = shared_now(tile + kWideBytes - kRawBytes + (row0 + kStep * j) * 128 + ch * 16);
                 // the codes lie where their values go: every warp has to have taken its own
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&taken[s]);
