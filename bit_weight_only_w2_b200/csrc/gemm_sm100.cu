@@ -224,8 +224,16 @@ bool encode_cached(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const 
         b[i] = box[i];
     }
     for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
-    const CUresult r = fn(map, dtype, rank, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    auto encode = [&] {
+        return fn(map, dtype, rank, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    int dev = 0;
+    // A host thread that has done no CUDA work yet has no context, and this driver call binds none (the
+    // runtime's launches do): selecting its device does, also under a stream capture.
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+        r = encode();
     if (r != CUDA_SUCCESS) return false;
     std::lock_guard<std::mutex> lock(mu);
     sl.used = true;

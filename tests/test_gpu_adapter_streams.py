@@ -64,3 +64,36 @@ def test_mixed_calls():
              (33, 2688, 744, 4, 64, 3, 48, None), (1541, 1408, 744, 4, 128, 1, 128, "sorted"),
              (512, 2560, 2560, 2, 128, 2, 16, "sorted"), (64, 512, 9728, 4, 64, 5, 16, "random")]
     run([Problem(*c) for c in cases], 4800)
+
+
+@pytest.mark.parametrize("call", ["forward", "forward of few tokens", "gradients", "gemm_dx", "gemm", "gemm of few tokens"])
+def test_first_cuda_work_of_a_thread(call):
+    """A host thread that has no CUDA context yet, with buffers whose tensor maps are new: everything given,
+    so that no allocation binds one first."""
+    pr = Problem(9 if "few" in call else 90, 256, 264, 2, 64, 3, 16, "random")
+    size = max(lb.adapter_workspace_size(pr.M, pr.N, pr.K, pr.L, pr.R), lb.workspace_size(pr.M, pr.K))
+    kept = []
+    for _ in range(3):
+        x, dy = pr.x.clone(), pr.dy.clone()
+        y, dx, da, db = (torch.empty_like(t) for t in (dy, x, pr.a, pr.b))
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        calls = {"forward": lambda: lb.adapter_gemm(x, pr.packed, *pr.args(), *pr.adapter_args(), out=y, ws=ws),
+                 "gradients": lambda: lb.adapter_backward(dy, x, pr.p, pr.packed_t, *pr.args(), *pr.adapter_args(), dx=dx,
+                                                          da=da, db=db, ws=ws),
+                 "gemm_dx": lambda: lb.gemm_dx(dy, pr.packed_t, *pr.args(), out=dx, ws=ws),
+                 "gemm": lambda: lb.gemm(x, pr.packed, *pr.args(), out=y, ws=ws)}
+        failed = []
+
+        def work():
+            try:
+                calls[call.split(" of ")[0]]()
+            except Exception as e:
+                failed.append(e)
+
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+        assert not failed, failed
+        kept.append((x, dy, y, dx, da, db, ws))   # (the next round's buffers lie elsewhere)
+    assert lb.device_status() == 0
