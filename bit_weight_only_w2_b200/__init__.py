@@ -8,6 +8,8 @@ is missing; there is no fallback.
     Y = adapter_gemm(x, packed, scales, zeros, bits, group_size, a, b, scaling, index)
     dX = gemm_dx(dy, packed_t, scales, zeros, bits, group_size)
     dX, dA, dB = adapter_backward(dy, x, p, packed_t, scales, zeros, bits, group_size, a, b, scaling, index)
+    Y = embedding(tokens, weight, scales, zeros, bits, group_size)          # a table of vocabulary rows
+    loss, lse = cross_entropy(x, labels, weight, scales, zeros, bits, group_size)
 
 Layouts (see include/lowbit.h): x bf16 [M][K]; packed int32 view of uint32 words
 [N][K*bits/32]; scales / zeros fp16 [K/group_size][N]; y bf16 [M][N].
@@ -129,6 +131,19 @@ def open_library(path: str) -> ctypes.CDLL:
     lib.lowbit_checkpoint_store.restype = i32
     lib.lowbit_checkpoint_load.argtypes = [p, p, i64, i64, p, p]
     lib.lowbit_checkpoint_load.restype = i32
+    f32 = ctypes.c_float
+    lib.lowbit_cross_entropy_workspace_size.argtypes = [i64, i64, i64, i32, i32]
+    lib.lowbit_cross_entropy_workspace_size.restype = sz
+    lib.lowbit_cross_entropy.argtypes = [i64, i64, i64, i64, i32, i32, p, p, p, p, p, p, p, p, sz, p]
+    lib.lowbit_cross_entropy.restype = i32
+    lib.lowbit_cross_entropy_backward.argtypes = [i64, i64, i64, i64, i32, i32, p, p, p, p, p, p, p, p, p, p, sz, p]
+    lib.lowbit_cross_entropy_backward.restype = i32
+    lib.lowbit_embedding.argtypes = [i64, i64, i64, i32, i32, p, p, p, p, f32, p, p]
+    lib.lowbit_embedding.restype = i32
+    lib.lowbit_embedding_workspace_size.argtypes = [i64, i64, i64]
+    lib.lowbit_embedding_workspace_size.restype = sz
+    lib.lowbit_embedding_backward.argtypes = [i64, i64, i64, i64, p, p, f32, p, p, sz, p]
+    lib.lowbit_embedding_backward.restype = i32
     return lib
 
 
@@ -666,6 +681,172 @@ def adapter_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint], p: to
                                               _ptr(dx), da.data_ptr(), db.data_ptr(), ws.data_ptr(), ws_bytes,
                                               _raw_stream(dev)), "lowbit_adapter_backward")
     return dx, da, db
+
+
+# ---- a vocabulary: token embeddings and the softmax cross entropy -------------------------------
+# A table of rows is bits=16: weight bf16 [N][K], scales and zeros None; or packed: weight int32 words
+# [N][K*bits/32] (pack), scales (and zeros) fp16 [K/group_size][N], as a linear's.
+def _table_shape(weight, scales, zeros, bits: int, group_size: int):
+    """(N, K) of a table whose tensors fit one another."""
+    if bits == 16:
+        _need(weight, _BF16, "weight")
+        if scales is not None or zeros is not None:
+            raise ValueError("scales, zeros: a bf16 table (bits=16) has none")
+        return weight.shape
+    if bits not in (1, 2, 4):
+        raise ValueError(f"bits: expected 1, 2, 4 or 16, got {bits}")
+    _need(weight, _I32, "weight")
+    if scales is None:
+        raise ValueError("scales: a packed table needs them")
+    _need(scales, _F16, "scales")
+    N, K = weight.shape[0], weight.shape[1] * 32 // bits
+    if group_size <= 0 or K % group_size:
+        raise ValueError(f"group_size: expected a divisor of K = {K}, got {group_size}")
+    for name, t in (("scales", scales), ("zeros", zeros)):
+        if t is not None:
+            _check_like(t, name, (K // group_size, N), _F16, weight.device)
+    return N, K
+
+
+@functools.lru_cache(maxsize=4096)
+def cross_entropy_workspace_size(M: int, vocab: int, K: int, bits: int, backward: int = 0) -> int:
+    """Bytes of workspace of cross_entropy (backward=0) and cross_entropy_backward (1, or 2 with dW)."""
+    return int(load().lowbit_cross_entropy_workspace_size(M, vocab, K, bits, backward))
+
+
+@functools.lru_cache(maxsize=4096)
+def embedding_workspace_size(T: int, rows: int, K: int) -> int:
+    """Bytes of workspace of embedding_backward."""
+    return int(load().lowbit_embedding_workspace_size(T, rows, K))
+
+
+def _bytes_or(ws: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
+    # (allocated per call by default, as the adapters' workspace is)
+    if ws is None:
+        return torch.empty(max(need, 1), dtype=_U8, device=device)
+    _need(ws, _U8, "ws", ndim=1)
+    if ws.device != device:
+        raise ValueError(f"ws: on {ws.device}, expected {device}")
+    return ws
+
+
+def _loss_args(x, labels, weight, scales, zeros, bits, group_size, vocab):
+    _need(x, _BF16, "x")
+    N, K = _table_shape(weight, scales, zeros, bits, group_size)
+    M = x.shape[0]
+    if x.shape[1] != K:
+        raise ValueError(f"x: expected [M][{K}] for the table, got {tuple(x.shape)}")
+    _check_like(labels, "labels", (M,), _I32, x.device)
+    if weight.device != x.device:
+        raise ValueError(f"weight: on {weight.device}, but x is on {x.device}")
+    _need_cuda(("x", x))
+    if vocab is None:
+        vocab = N
+    if not 1 <= vocab <= N:
+        raise ValueError(f"vocab: expected 1 .. {N} (the table's rows), got {vocab}")
+    return M, N, K, vocab
+
+
+def cross_entropy(x: torch.Tensor, labels: torch.Tensor, weight: torch.Tensor, scales: Optional[torch.Tensor] = None,
+                  zeros: Optional[torch.Tensor] = None, bits: int = 16, group_size: int = 0,
+                  vocab: Optional[int] = None, loss: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                  ws: Optional[torch.Tensor] = None):
+    """(loss, lse), fp32 [M]: each token's softmax cross entropy over logits = x W^T, which are not stored.
+
+    x bf16 [M][K]; labels int32 [M], a label outside 0 .. vocab-1 (-100, say) having no loss; the table W is
+    bf16 (bits=16) or packed; vocab: the rows that take part (default: all; rows behind them fill a packed
+    table up). Records no autograd graph: call cross_entropy_backward with the lse."""
+    M, N, K, vocab = _loss_args(x, labels, weight, scales, zeros, bits, group_size, vocab)
+    dev = x.get_device()
+    if loss is None:
+        loss = x.new_empty(M, dtype=_F32)
+    else:
+        _check_like(loss, "loss", (M,), _F32, x.device)
+    if lse is None:
+        lse = x.new_empty(M, dtype=_F32)
+    else:
+        _check_like(lse, "lse", (M,), _F32, x.device)
+    with _on_device(dev):
+        ws = _bytes_or(ws, cross_entropy_workspace_size(M, vocab, K, bits, 0), x.device)
+        _check(load().lowbit_cross_entropy(M, vocab, N, K, bits, group_size, x.data_ptr(), weight.data_ptr(), _ptr(scales),
+                                           _ptr(zeros), labels.data_ptr(), loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                           ws.numel(), _raw_stream(dev)), "lowbit_cross_entropy")
+    return loss, lse
+
+
+def cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, labels: torch.Tensor, lse: torch.Tensor,
+                           weight: torch.Tensor, scales: Optional[torch.Tensor] = None,
+                           zeros: Optional[torch.Tensor] = None, bits: int = 16, group_size: int = 0,
+                           vocab: Optional[int] = None, need_dw: bool = False, dx: Optional[torch.Tensor] = None,
+                           dw: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """(dx bf16 [M][K], dw bf16 [N][K] or None), the gradients of cross_entropy for grad fp32 [M], the gradient of
+    each token's loss (1 / number of tokens for their mean). dw: a bf16 table's, with need_dw; a packed one is frozen."""
+    M, N, K, vocab = _loss_args(x, labels, weight, scales, zeros, bits, group_size, vocab)
+    _check_like(grad, "grad", (M,), _F32, x.device)
+    _check_like(lse, "lse", (M,), _F32, x.device)
+    if need_dw and bits != 16:
+        raise ValueError("need_dw: a packed table is frozen, it has no gradient")
+    if dw is not None and not need_dw:
+        raise ValueError("dw: a buffer was passed, but need_dw is False")
+    dev = x.get_device()
+    if dx is None:
+        dx = x.new_empty((M, K))
+    else:
+        _check_like(dx, "dx", (M, K), _BF16, x.device)
+    if need_dw and dw is None:
+        dw = x.new_empty((N, K))
+    elif dw is not None:
+        _check_like(dw, "dw", (N, K), _BF16, x.device)
+    with _on_device(dev):
+        ws = _bytes_or(ws, cross_entropy_workspace_size(M, vocab, K, bits, 2 if need_dw else 1), x.device)
+        _check(load().lowbit_cross_entropy_backward(M, vocab, N, K, bits, group_size, x.data_ptr(), weight.data_ptr(),
+                                                    _ptr(scales), _ptr(zeros), labels.data_ptr(), lse.data_ptr(),
+                                                    grad.data_ptr(), dx.data_ptr(), _ptr(dw), ws.data_ptr(), ws.numel(),
+                                                    _raw_stream(dev)), "lowbit_cross_entropy_backward")
+    return dx, dw
+
+
+def embedding(tokens: torch.Tensor, weight: torch.Tensor, scales: Optional[torch.Tensor] = None,
+              zeros: Optional[torch.Tensor] = None, bits: int = 16, group_size: int = 0, multiplier: float = 1.0,
+              out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """multiplier * the table's rows of tokens int32 [T]: bf16 [T][K], zeros for a token outside the table."""
+    N, K = _table_shape(weight, scales, zeros, bits, group_size)
+    _need(tokens, _I32, "tokens", ndim=1)
+    T = tokens.shape[0]
+    if tokens.device != weight.device:
+        raise ValueError(f"tokens: on {tokens.device}, but the table is on {weight.device}")
+    _need_cuda(("weight", weight))
+    dev = weight.get_device()
+    if out is None:
+        out = torch.empty((T, K), dtype=_BF16, device=weight.device)
+    else:
+        _check_like(out, "out", (T, K), _BF16, weight.device)
+    with _on_device(dev):
+        _check(load().lowbit_embedding(T, N, K, bits, group_size, tokens.data_ptr(), weight.data_ptr(), _ptr(scales), _ptr(zeros),
+                                       multiplier, out.data_ptr(), _raw_stream(dev)), "lowbit_embedding")
+    return out
+
+
+def embedding_backward(tokens: torch.Tensor, dy: torch.Tensor, rows: int, first: int = 0, multiplier: float = 1.0,
+                       out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of rows first .. first + rows - 1 of a table, bf16 [rows][K], for dy bf16 [T][K] of the
+    embeddings of tokens int32 [T]. Rows without tokens are zeros; a row's sum is fp32, in the tokens' order."""
+    _need(dy, _BF16, "dy")
+    T, K = dy.shape
+    _check_like(tokens, "tokens", (T,), _I32, dy.device)
+    _need_cuda(("dy", dy))
+    if rows < 0 or first < 0:
+        raise ValueError(f"rows, first: expected none below 0, got {rows} and {first}")
+    dev = dy.get_device()
+    if out is None:
+        out = dy.new_empty((rows, K))
+    else:
+        _check_like(out, "out", (rows, K), _BF16, dy.device)
+    with _on_device(dev):
+        ws = _bytes_or(ws, embedding_workspace_size(T, rows, K), dy.device)
+        _check(load().lowbit_embedding_backward(T, K, first, rows, tokens.data_ptr(), dy.data_ptr(), multiplier, out.data_ptr(),
+                                                ws.data_ptr(), ws.numel(), _raw_stream(dev)), "lowbit_embedding_backward")
+    return out
 
 
 def device_status(clear: bool = True) -> int:

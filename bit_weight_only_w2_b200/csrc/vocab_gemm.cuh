@@ -1,0 +1,741 @@
+// The products of the softmax cross entropy over a vocabulary, one kernel for sm_100a:
+//
+//   kVocabStats  l = X W^T, kept in tensor memory only: each tile leaves, per token, the maximum r of its
+//                columns and s = sum exp(l - r), and the logit of the token's label
+//   kVocabGrad   l again, and G = f (exp(l - lse) - [column = label]) in 16 bits, a piece of the columns at a time
+//   kVocabDx     dX += G W over a piece (fp32 sums in the workspace)
+//   kVocabDw     dW = G^T X, the rows of a piece
+//
+// W is bf16, or decoded from packed binary, ternary or uint4 words inside the kernel. Precision: bf16 tables
+// multiply bf16 x bf16; packed ones fp16 x fp16 on an exact fp16 copy of X (a power of two per row taken out),
+// binary and ternary weights being exact in fp16. A uint4 weight (q - z) s is not: one rounding to fp16 (2^-11)
+// moves a logit by some 2^-12 of |x||w|, which an fp32 loss shows, so the logits take it as the sum of two fp16
+// values (2^-22, twice the MMAs); dX, rounded to bf16, takes the first of them. Sums are fp32 throughout.
+//
+// Design. A CTA's tile is 128 rows (tokens; vocabulary rows for dW) on the lanes of tensor memory, so that a
+// softmax over columns stays inside a thread, by 128 columns, or 256 for a CTA pair (cta_group::2), each of whose
+// CTAs holds half of the columns' operand. Both operands come through one shared-memory ring of 64-wide stages:
+//   * warp 8 (one lane): TMA of the rows' operand, and of a bf16 table's rows;
+//   * warp 10 (packed tables): TMA of the words and scales of 128 rows x 128 columns; warps 11-18 decode them, a row
+//     of 64 codes per lane, into the swizzled layout the MMA reads;
+//   * warp 9 (one lane): tcgen05.mma, two accumulators in tensor memory;
+//   * warps 0-7: the epilogue of one tile, beside the MMAs of the next.
+// Persistent grids; tiles go through the tokens first, so that a table's rows are read from memory once.
+// Operands are K-major for the logits; for the gradients the table [v][k] (dX: reduced over v), G [m][v] and X [m][k]
+// (dW: reduced over m) are read as they lie, as MN-major operands, so nothing is transposed.
+#pragma once
+
+#include <atomic>
+
+#include "gemm_kernel.cuh"
+#include "vocab_internal.h"
+
+namespace lowbit {
+namespace vocab {
+
+constexpr int kStageBytes = 32768;      // 128 x 64 of the rows' operand, 128 x 64 of the columns'
+constexpr int kOperandBytes = 16384;
+constexpr int kEpiWarps = 8;
+
+template <int MODE, int BITS, bool PAIR>
+struct Cfg {
+    static constexpr bool kPacked = BITS != kDense && MODE != kVocabDw;
+    static_assert(MODE != kVocabDw || (BITS == kDense && PAIR), "dW: bf16 tables, CTA pairs");
+    static constexpr bool kLogits = MODE == kVocabStats || MODE == kVocabGrad;
+    static constexpr int kTerms = kLogits && BITS == 4 ? 2 : 1;   // fp16 values per weight
+    static constexpr int kDqWarps = kPacked ? 8 : 0;
+    static constexpr int kThreads = 32 * (kEpiWarps + (kPacked ? 3 : 2) + kDqWarps);
+    static constexpr int kCols = PAIR ? 256 : 128;                // of a tile
+    static constexpr int kRows = PAIR ? 256 : 128;
+    static constexpr int kTmemCols = 2 * kCols;
+    // Stages of words: kLogits 128 rows, kVocabDx 64 (one stage of the reduction), 128 codes of each
+    static constexpr int kWRows = kLogits ? 128 : 64;
+    static constexpr int kWRowBytes = kPacked ? 128 * BITS / 8 : 0;
+    static constexpr int kWBytes = kWRows * kWRowBytes;
+    static constexpr int kSBytes = kPacked ? 2 * kWRows * 2 : 0;  // room for two groups
+    static constexpr int kZBytes = BITS == 4 ? kSBytes : 0;
+    static constexpr int kWStageBytes = (kWBytes + kSBytes + kZBytes + 1023) / 1024 * 1024;
+    static constexpr int kWStages = kPacked ? 4 : 0;
+    static constexpr int kStagingBytes = (MODE == kVocabGrad || MODE == kVocabDw) ? kEpiWarps * 4096 : 0;
+    static constexpr int kFit = (kSmemLimit - 2048 - kStagingBytes - kWStages * kWStageBytes) / kStageBytes;
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static_assert(kStages >= 3, "shared memory");
+    static constexpr int kWOff = kStages * kStageBytes;
+    static constexpr int kStagingOff = kWOff + kWStages * kWStageBytes;
+    static constexpr int kBarOff = kStagingOff + kStagingBytes;
+    static constexpr int kSmemBytes = 1024 + kBarOff + 1024;
+    static_assert(kSmemBytes <= kSmemLimit && kSmemBytes > kSmemLimit / 2, "one CTA per SM (tensor memory)");
+    static constexpr bool kAMn = MODE == kVocabDw, kBMn = !kLogits;   // MN-major operands
+    static constexpr uint32_t kIdesc = (BITS == kDense ? idesc_bf16_f32(kRows, kCols) : idesc_f16_f32(kRows, kCols)) |
+                                       (kAMn ? kIdescTransposeA : 0u) | (kBMn ? kIdescTransposeB : 0u);
+    // arrivals of decoding warps per stage: 128 rows (or 64 rows x two halves), 32 a warp
+    static constexpr int kDqArrivals = 4 * (PAIR ? 2 : 1);
+    static constexpr int kWReaders = kLogits ? 8 : 4;             // decoding warps that read a stage of words
+};
+
+struct Params {
+    int M;                  // tokens
+    int vocab;
+    int stages;             // of a tile's whole reduction
+    int per_slice;          // of a slice of it (kVocabDx), else `stages`
+    int m_tiles, n_tiles, num_tiles;
+    int v0;                 // first column (vocabulary row) of the piece
+    int groups;             // scale groups per 128 codes: 1 or 2
+    uint32_t wtx;           // bytes of a stage of words
+    const float* rowmul;    // packed: the power of two taken out of each token's row
+    const int32_t* labels;
+    const float* lse;
+    const float* grad;
+    float2* part;           // kVocabStats: [2 * n_tiles][M]
+    float* target;          // [M]
+    float4* acc;            // kVocabDx: [tile][CTA of the pair][warp][column / 4][lane]
+    int accumulate;         // add to what acc holds
+    float gscale;           // packed: the power of two in G
+    int out_rows, out_cols; // kVocabGrad, kVocabDw: of what map_out covers
+    unsigned* status;
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {   // 2^x, within 2 ulp; 0 below fp32's normal range
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t cluster_bar, void* dst, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// What rounding (q - z) s to fp16 left of the four pairs of a uint4 word, itself rounded to fp16 (decode_word_b4
+// gave the first terms).
+__device__ __forceinline__ void decode_rest_b4(uint32_t v, uint16_t s, float cz, uint32_t* out, int w) {
+    uint32_t first[32];
+    decode_word_b4(v, s, cz, first, w);
+    constexpr uint32_t kMagic = 0x64006400u;
+    constexpr uint32_t kMul[2] = {0x3C003C00u, 0x2C002C00u};
+    constexpr uint32_t kAdd[2] = {0xE400E400u, 0xD400D400u};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int i = 16 * (w >> 2) + 4 * c + (w & 3);
+        const uint32_t e = and_or(v >> (c < 2 ? 0 : 8), 0x000F000Fu << (4 * (c & 1)), kMagic);
+        float lo, hi;
+        fma_f16x2_f32(f16x2_fma(e, kMul[c & 1], kAdd[c & 1]), s, cz, lo, hi);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&first[i]));
+        out[i] = pack_f16x2(lo - f.x, hi - f.y);
+    }
+}
+
+template <int MODE, int BITS, bool PAIR>
+__global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
+    vocab_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                 const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_z,
+                 const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Params p) {
+    using C = Cfg<MODE, BITS, PAIR>;
+    constexpr int S = C::kStages, SW = C::kWStages > 0 ? C::kWStages : 1, T = C::kTerms;
+    constexpr int kCtas = PAIR ? 2 : 1;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+    uint64_t* bfull = full + S;       // packed: the decoded half of a stage
+    uint64_t* empty = bfull + S;
+    uint64_t* wfull = empty + S;
+    uint64_t* wempty = wfull + SW;
+    uint64_t* accfull = wempty + SW;
+    uint64_t* accempty = accfull + 2;
+    uint64_t* drain = accempty + 2;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const bool issuer = rank == 0;
+    auto on_issuer = [&](uint64_t* bar) { return map_shared_rank(smem_u32(bar), 0); };
+    auto arrive_on_issuer = [&](uint64_t* bar) {
+        if (PAIR && !issuer)
+            mbar_arrive_remote(on_issuer(bar));
+        else
+            mbar_arrive(bar);
+    };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&bfull[i], C::kDqArrivals);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < SW; ++i) {
+            mbar_init(&wfull[i], 1);
+            mbar_init(&wempty[i], C::kWReaders);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accfull[i], 1);
+            mbar_init(&accempty[i], kCtas * kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_desc(&map_a);
+        tma_prefetch_desc(&map_b);
+        if (C::kPacked) tma_prefetch_desc(&map_s);
+    }
+    if (warp == 9) {
+        tmem_alloc<PAIR>(tmem_holder, C::kTmemCols);
+        tmem_relinquish<PAIR>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR) cluster_sync_all();   // both CTAs' barriers are initialised before either uses the other's
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    grid_launch_dependents();
+    grid_dependency_wait();
+
+    const int tile0 = static_cast<int>(PAIR ? blockIdx.x >> 1 : blockIdx.x);
+    const int tile_step = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x);
+    const int per_mn = p.m_tiles * p.n_tiles;
+    // Tile t of the grid: rows [m0, ..) and columns [n0, ..) of this CTA's, stages [j0, j1) of the reduction.
+    struct Tile {
+        int m0, n0, j0, j1;
+    };
+    auto tile_of = [&](int t) {
+        const int slice = t / per_mn, mn = t - slice * per_mn, n = mn / p.m_tiles, m = mn - n * p.m_tiles;
+        Tile r;
+        r.m0 = m * C::kRows + static_cast<int>(rank) * 128;
+        r.n0 = n * C::kCols;
+        r.j0 = slice * p.per_slice;
+        r.j1 = min(p.stages, r.j0 + p.per_slice);
+        return r;
+    };
+
+    if (warp == 8) {
+        // ------------------------------------------------------------ TMA of the rows' operand, and of a bf16 table
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            constexpr uint32_t kBytes = C::kPacked ? kOperandBytes : kStageBytes;
+            for (int t = tile0; t < p.num_tiles && ok; t += tile_step) {
+                const Tile tl = tile_of(t);
+                const int nb = tl.n0 + static_cast<int>(rank) * 128;   // first of this CTA's half of the columns
+                for (int j = tl.j0; j < tl.j1; ++j, ++it) {
+                    const uint32_t s = it % S;
+                    if (!mbar_wait(&empty[s], ((it / S) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
+                    uint8_t* a = smem + s * kStageBytes;
+                    uint8_t* b = a + kOperandBytes;
+                    if (issuer) mbar_arrive_expect_tx(&full[s], kCtas * kBytes);
+                    auto load = [&](const CUtensorMap* map, uint8_t* dst, int x, int y) {
+                        if (PAIR)
+                            tma_load_2d_pair(map, on_issuer(&full[s]), dst, x, y);
+                        else
+                            tma_load_2d(map, &full[s], dst, x, y);
+                    };
+                    if (MODE == kVocabDw) {          // G [m][v], X [m][k]: 64 tokens, two boxes of 64 columns each
+                        load(&map_a, a, tl.m0, j * 64);
+                        load(&map_a, a + 8192, tl.m0 + 64, j * 64);
+                        load(&map_b, b, nb, j * 64);
+                        load(&map_b, b + 8192, nb + 64, j * 64);
+                    } else {
+                        load(&map_a, a, (j / T) * 64, tl.m0);
+                        if (MODE == kVocabDx && !C::kPacked) {   // W [v][k]: 64 rows
+                            load(&map_b, b, nb, p.v0 + j * 64);
+                            load(&map_b, b + 8192, nb + 64, p.v0 + j * 64);
+                        } else if (!C::kPacked) {
+                            load(&map_b, b, j * 64, p.v0 + nb);
+                        }
+                    }
+                }
+            }
+            if (!ok) {
+                // Wait (bounded) for the copies still in flight before the CTA exits. The second CTA of a pair cannot
+                // wait on the issuer's barrier that its copies count on: it gives them a fixed time instead.
+                if (PAIR && !issuer) {
+                    const long long t0 = clock64();
+                    while (clock64() - t0 < kWaitLimitCycles / 64) {
+                    }
+                } else {
+                    for (uint32_t j = it > static_cast<uint32_t>(S) ? it - S : 0u; j < it; ++j) {
+                        const long long t0 = clock64();
+                        while (!mbar_try_wait(&full[j % S], (j / S) & 1u) && clock64() - t0 < kWaitLimitCycles / 64) {
+                        }
+                    }
+                }
+            }
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0 && issuer) {
+            uint32_t it = 0, n = 0;
+            bool ok = true, issued = false;
+            for (int t = tile0; t < p.num_tiles && ok; t += tile_step, ++n) {
+                const Tile tl = tile_of(t);
+                const uint32_t b = n & 1u;
+                if (!mbar_wait(&accempty[b], ((n >> 1) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d = tmem_base + b * C::kCols;
+                for (int j = tl.j0; j < tl.j1; ++j, ++it) {
+                    const uint32_t s = it % S, ph = (it / S) & 1u;
+                    if (!mbar_wait(&full[s], ph, abort_flag, p.status) ||
+                        (C::kPacked && !mbar_wait(&bfull[s], ph, abort_flag, p.status))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t as = smem_u32(smem + s * kStageBytes), bs = as + kOperandBytes;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t ad = C::kAMn ? smem_desc_mn(as + kk * 2048, 128, 8192) : smem_desc_k_sw128(as + kk * 32);
+                        const uint64_t bd = C::kBMn ? smem_desc_mn(bs + kk * 2048, 128, 8192) : smem_desc_k_sw128(bs + kk * 32);
+                        const uint32_t more = (j > tl.j0 || kk > 0) ? 1u : 0u;
+                        if (PAIR)
+                            mma_f16_ss_pair(d, ad, bd, C::kIdesc, more);
+                        else
+                            mma_f16_ss(d, ad, bd, C::kIdesc, more);
+                    }
+                    issued = true;
+                    if (PAIR)
+                        mma_commit_pair_mc(&empty[s], 0x3);
+                    else
+                        mma_commit(&empty[s]);
+                }
+                if (!ok) break;
+                if (PAIR)
+                    mma_commit_pair_mc(&accfull[b], 0x3);
+                else
+                    mma_commit(&accfull[b]);
+            }
+            if (!ok && issued) {   // no MMA may still write tensor memory when it is freed
+                if (PAIR)
+                    mma_commit_pair(drain);
+                else
+                    mma_commit(drain);
+                const long long t0 = clock64();
+                while (!mbar_try_wait(drain, 0) && clock64() - t0 < kWaitLimitCycles / 64) {
+                }
+            }
+        }
+    } else if (C::kPacked && warp == 10) {
+        // ------------------------------------------------------------ TMA of words and scales
+        if constexpr (C::kPacked) {
+            if (lane == 0) {
+                uint32_t it = 0;
+                bool ok = true;
+                for (int t = tile0; t < p.num_tiles && ok; t += tile_step) {
+                    const Tile tl = tile_of(t);
+                    const int nb = tl.n0 + static_cast<int>(rank) * 128;
+                    // (kLogits: a stage of words is 2 * T stages of the ring, and a tile has them all)
+                    const int w1 = C::kLogits ? p.stages / (2 * T) : tl.j1;
+                    for (int w = C::kLogits ? 0 : tl.j0; w < w1; ++w, ++it) {
+                        const uint32_t s = it % SW;
+                        if (!mbar_wait(&wempty[s], ((it / SW) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
+                        uint8_t* st = smem + C::kWOff + s * C::kWStageBytes;
+                        mbar_arrive_expect_tx(&wfull[s], p.wtx);
+                        const int wx = C::kLogits ? w * (4 * BITS) : nb * BITS / 32, v = p.v0 + (C::kLogits ? nb : w * 64);
+                        const int sy = (C::kLogits ? w : nb / 128) * p.groups;
+                        tma_load_2d(&map_b, &wfull[s], st, wx, v);
+                        tma_load_2d(&map_s, &wfull[s], st + C::kWBytes, v, sy);
+                        if (BITS == 4) tma_load_2d(&map_z, &wfull[s], st + C::kWBytes + C::kSBytes, v, sy);
+                    }
+                }
+                if (!ok) {
+                    for (uint32_t j = it > static_cast<uint32_t>(SW) ? it - SW : 0u; j < it; ++j) {
+                        const long long t0 = clock64();
+                        while (!mbar_try_wait(&wfull[j % SW], (j / SW) & 1u) && clock64() - t0 < kWaitLimitCycles / 64) {
+                        }
+                    }
+                }
+            }
+        }
+    } else if (C::kPacked && warp >= 11) {
+        // ------------------------------------------------------------ decoding warps
+        if constexpr (C::kPacked) {
+            const int dq = warp - 11;
+            const int row = (C::kLogits ? (dq & 3) : (dq & 1)) * 32 + lane;
+            const int half = C::kLogits ? dq >> 2 : (dq >> 1) & 1;   // which 64 of a row's 128 codes
+            uint32_t wit = 0;   // stages of words seen
+            uint32_t it = 0;    // stages of the ring before the present stage of words
+            bool ok = true;
+            for (int t = tile0; t < p.num_tiles && ok; t += tile_step) {
+                const Tile tl = tile_of(t);
+                const int count = C::kLogits ? p.stages / (2 * T) : tl.j1 - tl.j0;
+                for (int w = 0; w < count; ++w, ++wit, it += C::kLogits ? 2 * T : 1) {
+                    if (!C::kLogits && (it & 1u) != static_cast<uint32_t>(dq >> 2)) continue;   // the other four warps'
+                    const uint32_t ws = wit % SW;
+                    if (!__all_sync(0xffffffffu, mbar_wait(&wfull[ws], (wit / SW) & 1u, abort_flag, p.status))) { ok = false; break; }
+                    const uint8_t* st = smem + C::kWOff + ws * C::kWStageBytes;
+                    const uint8_t* wrow = st + row * C::kWRowBytes;
+                    uint32_t words[2 * BITS];
+                    if (BITS == 1) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(wrow + half * 8);
+                        words[0] = v.x;
+                        words[1] = v.y;
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < BITS / 2; ++q) {
+                            // (TMA's 32- and 64-byte swizzles)
+                            const int chunk = BITS == 2 ? half ^ ((row >> 2) & 1) : (2 * half + q) ^ ((row >> 1) & 3);
+                            const uint4 v = *reinterpret_cast<const uint4*>(wrow + chunk * 16);
+                            words[4 * q] = v.x; words[4 * q + 1] = v.y; words[4 * q + 2] = v.z; words[4 * q + 3] = v.w;
+                        }
+                    }
+                    const int at = (p.groups == 2 ? half : 0) * C::kWRows + row;
+                    const uint16_t sb = reinterpret_cast<const uint16_t*>(st + C::kWBytes)[at];
+                    float cz = 0.f;
+                    if (BITS == 4)   // -z * s, exact in fp32
+                        cz = -__half2float(reinterpret_cast<const __half*>(st + C::kWBytes + C::kSBytes)[at]) *
+                             __half2float(__ushort_as_half(sb));
+#pragma unroll
+                    for (int term = 0; term < T; ++term) {
+                        uint32_t out[32];
+                        if constexpr (BITS == 1) {
+                            decode_half_b1(words[0], words[1], sb | (static_cast<uint32_t>(sb) << 16), out);
+                        } else if constexpr (BITS == 2) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) decode_word_b2(words[q], sb | (static_cast<uint32_t>(sb) << 16), out, q);
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                if (term == 0)
+                                    decode_word_b4(words[q], sb, cz, out, q);
+                                else
+                                    decode_rest_b4(words[q], sb, cz, out, q);
+                            }
+                        }
+                        const uint32_t i = it + (C::kLogits ? half * T + term : 0), s = i % S;
+                        if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / S) & 1u) ^ 1u, abort_flag, p.status))) {
+                            ok = false;
+                            break;
+                        }
+                        // kLogits: 128 rows of 64 columns; kVocabDx: two halves of 64 rows
+                        const uint32_t dst = smem_u32(smem + s * kStageBytes + kOperandBytes) + (C::kLogits ? 0 : half * 8192) + row * 128;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            st_shared_v4(dst + ((c ^ (row & 7)) << 4), out[4 * c], out[4 * c + 1], out[4 * c + 2], out[4 * c + 3]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) arrive_on_issuer(&bfull[s]);
+                    }
+                    if (!ok) break;
+                    // (freed behind the last use of what was read from it)
+                    if (lane == 0) mbar_arrive(&wempty[ws]);
+                }
+            }
+        }
+    } else if (warp < kEpiWarps) {
+        // ------------------------------------------------------------ epilogue
+        const int quarter = warp & 3, part = warp >> 2;
+        constexpr int kCols = C::kCols / 2;                  // this warp's half of the tile's columns
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+        [[maybe_unused]] const uint32_t staging = smem_u32(smem + C::kStagingOff + warp * 4096);
+        uint32_t n = 0;
+        for (int t = tile0; t < p.num_tiles; t += tile_step, ++n) {
+            const Tile tl = tile_of(t);
+            const uint32_t b = n & 1u;
+            const int r0 = tl.m0 + quarter * 32, row = r0 + lane;
+            const int c0 = tl.n0 + part * kCols;             // first column, within the piece
+            const int left = p.vocab - (p.v0 + c0);          // columns of the vocabulary from there on
+            // what the token needs, requested before the accumulator is waited for
+            [[maybe_unused]] int label = -1;
+            [[maybe_unused]] float mul = 1.f, shift = 0.f, f = 0.f;
+            if (C::kLogits && row < p.M) {
+                label = p.labels[row];
+                if (static_cast<unsigned>(label) >= static_cast<unsigned>(p.vocab)) label = -1;
+                if (C::kPacked) mul = p.rowmul[row];
+                if (MODE == kVocabGrad) {
+                    shift = p.lse[row] * kLog2e;
+                    f = C::kPacked ? p.gscale : p.grad[row];
+                }
+            }
+            const uint32_t acc = lane_base + b * C::kCols + part * kCols;
+            if (!__all_sync(0xffffffffu, mbar_wait(&accfull[b], (n >> 1) & 1u, abort_flag, p.status))) break;
+            tc_fence_after();
+            if constexpr (MODE == kVocabStats) {
+                if (r0 < p.M) {
+                    const float rl = mul * kLog2e;
+                    const int want = label >= 0 ? label - (p.v0 + c0) : -1;   // the label's place in this warp's columns
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < kCols; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(acc + c, v);
+                        tmem_wait_ld();
+                        if (left < c + 32) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (c + j < left) top = fmaxf(top, __uint_as_float(v[j]));
+                        } else {
+                            float m4[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(v[j]));
+                            top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                        }
+                        if (static_cast<unsigned>(want - c) < 32u) {
+                            float l = 0.f;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j == want - c) l = __uint_as_float(v[j]);
+                            p.target[row] = l * mul;
+                        }
+                    }
+                    // An infinite maximum stands aside: with no column at all s is 0, with +inf s is +inf.
+                    const bool inf = fabsf(top) == INFINITY;
+                    const float off = inf ? 0.f : -top * rl;
+                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int c = 0; c < kCols; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(acc + c, v);
+                        tmem_wait_ld();
+                        if (left < c + 32) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (c + j < left) s4[0] += ex2(fmaf(__uint_as_float(v[j]), rl, off));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) s4[j & 3] += ex2(fmaf(__uint_as_float(v[j]), rl, off));
+                        }
+                    }
+                    const float s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    const float r = inf ? (top > 0.f ? 3.4e38f : -INFINITY) : top * mul;
+                    if (row < p.M) p.part[static_cast<size_t>(2 * (tl.n0 / C::kCols) + part) * p.M + row] = make_float2(r, s);
+                }
+            } else if constexpr (MODE == kVocabGrad || MODE == kVocabDw) {
+                const float rl = mul * kLog2e;
+                const int want = label >= 0 ? label - (p.v0 + c0) : -1;
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 64) {
+                    // the staging rows are read out by the previous store
+                    if (lane == 0) bulk_wait_read_all();
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[32];
+                        tmem_ld32(acc + c + h * 32, v);
+                        tmem_wait_ld();
+                        uint32_t o[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float e[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int col = c + h * 32 + j + k;
+                                e[k] = __uint_as_float(v[j + k]);
+                                if constexpr (MODE == kVocabGrad) {
+                                    float g = ex2(fmaf(e[k], rl, -shift));
+                                    if (col == want) g -= 1.f;
+                                    e[k] = label >= 0 && col < left ? g * f : 0.f;
+                                }
+                            }
+                            o[j / 2] = BITS == kDense ? pack_bf16x2(e[0], e[1]) : pack_f16x2(e[0], e[1]);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            st_shared_v4(staging + lane * 128 + (((h * 4 + q) ^ (lane & 7)) << 4), o[4 * q], o[4 * q + 1],
+                                         o[4 * q + 2], o[4 * q + 3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && r0 < p.out_rows && c0 + c < p.out_cols) {
+                        tma_store_2d(&map_out, smem + C::kStagingOff + warp * 4096, c0 + c, r0);
+                        bulk_commit_group();
+                    }
+                }
+            } else {
+                float4* dst = p.acc + ((static_cast<size_t>(t) * kCtas + rank) * kEpiWarps + warp) * (kCols / 4) * 32 + lane;
+                if (r0 < p.M) {
+#pragma unroll 1
+                    for (int c = 0; c < kCols; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(acc + c, v);
+                        float4 old[8];
+                        if (p.accumulate) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) old[q] = dst[(c / 4 + q) * 32];
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) old[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            dst[(c / 4 + q) * 32] =
+                                make_float4(old[q].x + __uint_as_float(v[4 * q]), old[q].y + __uint_as_float(v[4 * q + 1]),
+                                            old[q].z + __uint_as_float(v[4 * q + 2]), old[q].w + __uint_as_float(v[4 * q + 3]));
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_on_issuer(&accempty[b]);
+        }
+        if (C::kStagingBytes > 0 && lane == 0) bulk_wait_read_all();
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    // a pair's tensor memory is freed by both CTAs together, once neither uses it (and no remote arrival or copy of
+    // one CTA targets the other after it has exited)
+    if (PAIR) cluster_sync_all();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc<PAIR>(tmem_base, C::kTmemCols);
+    }
+}
+
+template <int MODE, int BITS, bool PAIR>
+lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
+    using C = Cfg<MODE, BITS, PAIR>;
+    auto kernel = vocab_kernel<MODE, BITS, PAIR>;
+    const void* fn = reinterpret_cast<const void*>(kernel);
+    static std::atomic<uint64_t> devices{0};   // the shared-memory opt-in is per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
+    const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+    if (!bit || !(devices.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+            return LOWBIT_ERR_CUDA;
+        devices.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    const LossProblem& q = *v.p;
+    const LossLayout& l = *v.l;
+    const Table& w = q.table;
+    const uint64_t M = q.M, K = w.K, vocab = q.vocab, ld = l.piece;
+    const CUtensorMapDataType half =
+        BITS == kDense ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    CUtensorMap ma, mb, ms, mz, mo;
+    bool ok = true;
+    uint64_t rows = M;
+    void* g = v.ws + l.g;
+    if (MODE == kVocabDw) {
+        ok = ok && make_map_2d(&ma, half, 2, g, ld, M, ld * 2, 64, 64, sw);
+        ok = ok && make_map_2d(&mb, half, 2, v.ws + l.xz, K, M, K * 2, 64, 64, sw);
+        rows = v.cols;
+        ok = ok && make_map_2d(&mo, half, 2, static_cast<uint8_t*>(q.dW) + static_cast<size_t>(v.v0) * K * 2, K, rows, K * 2, 64, 32, sw);
+    } else {
+        const void* x = BITS == kDense ? q.X : v.ws + l.xh;
+        ok = ok && (C::kLogits ? make_map_2d(&ma, half, 2, x, K, M, K * 2, 64, 128, sw)
+                               : make_map_2d(&ma, half, 2, g, ld, M, ld * 2, 64, 128, sw));
+        if (!C::kPacked) {
+            ok = ok && make_map_2d(&mb, half, 2, w.rows, K, vocab, K * 2, 64, C::kLogits ? 128 : 64, sw);
+        } else {
+            const CUtensorMapSwizzle wsw = C::kWRowBytes == 16   ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                           : C::kWRowBytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                                 : CU_TENSOR_MAP_SWIZZLE_64B;
+            ok = ok && make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, w.rows, K * BITS / 32, vocab, K * BITS / 8,
+                                   C::kWRowBytes / 4, C::kWRows, wsw);
+            const uint32_t groups = 128 / w.group_size;
+            ok = ok && make_map_2d(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w.scales, vocab, K / w.group_size,
+                                   static_cast<uint64_t>(w.N) * 2, C::kWRows, groups, CU_TENSOR_MAP_SWIZZLE_NONE);
+            if (BITS == 4)
+                ok = ok && make_map_2d(&mz, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w.zeros, vocab, K / w.group_size,
+                                       static_cast<uint64_t>(w.N) * 2, C::kWRows, groups, CU_TENSOR_MAP_SWIZZLE_NONE);
+        }
+        mo = ma;
+        if (MODE == kVocabGrad) ok = ok && make_map_2d(&mo, half, 2, g, ld, M, ld * 2, 64, 32, sw);
+    }
+    if (!C::kPacked) ms = mb;
+    if (BITS != 4) mz = ms;
+    Params p = {};
+    p.status = device_status_address();
+    if (!ok || !p.status) return LOWBIT_ERR_CUDA;
+    p.M = static_cast<int>(M);
+    p.vocab = static_cast<int>(vocab);
+    p.v0 = static_cast<int>(v.v0);
+    if (C::kPacked) {
+        p.groups = 128 / w.group_size;
+        p.wtx = static_cast<uint32_t>(C::kWBytes + (BITS == 4 ? 2 : 1) * p.groups * C::kWRows * 2);
+    }
+    const int64_t cols = v.cols;
+    if (C::kLogits) {
+        p.stages = static_cast<int>(C::kPacked ? (K + 127) / 128 * 2 * C::kTerms : (K + 63) / 64);
+        p.m_tiles = static_cast<int>(l.m_tiles);
+        p.n_tiles = static_cast<int>((cols + C::kCols - 1) / C::kCols);
+    } else if (MODE == kVocabDx) {
+        p.stages = static_cast<int>((cols + 63) / 64);
+        p.m_tiles = static_cast<int>(l.m_tiles);
+        p.n_tiles = static_cast<int>(l.dx_tiles);
+    } else {
+        p.stages = static_cast<int>((M + 63) / 64);
+        p.m_tiles = static_cast<int>((cols + C::kRows - 1) / C::kRows);
+        p.n_tiles = static_cast<int>((K + C::kCols - 1) / C::kCols);
+    }
+    int slices = 1;
+    if (MODE == kVocabDx) {
+        slices = l.slices < p.stages ? l.slices : p.stages;
+        p.per_slice = (p.stages + slices - 1) / slices;
+        slices = (p.stages + p.per_slice - 1) / p.per_slice;
+    } else {
+        p.per_slice = p.stages;
+    }
+    p.num_tiles = p.m_tiles * p.n_tiles * slices;
+    p.rowmul = reinterpret_cast<const float*>(v.ws + l.rowmul);
+    p.labels = q.labels;
+    p.lse = q.lse;
+    p.grad = q.grad;
+    p.part = reinterpret_cast<float2*>(v.ws + l.part);
+    p.target = reinterpret_cast<float*>(v.ws + l.target);
+    p.acc = reinterpret_cast<float4*>(v.ws + l.acc);
+    p.accumulate = v.first ? 0 : 1;
+    p.gscale = 32768.f;
+    p.out_rows = static_cast<int>(rows);
+    p.out_cols = static_cast<int>(MODE == kVocabDw ? K : ld);
+
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attrs[2];
+    int na = 0;
+    attrs[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+    if (PAIR) {
+        int pairs = cluster_capacity(fn, 2, C::kThreads, C::kSmemBytes, true);
+        if (pairs > num_sms() / 2) pairs = num_sms() / 2;
+        if (pairs < 1) pairs = 1;
+        cfg.gridDim = dim3(2 * (p.num_tiles < pairs ? p.num_tiles : pairs), 1, 1);
+        attrs[na].id = cudaLaunchAttributeClusterDimension;
+        attrs[na].val.clusterDim.x = 2;
+        attrs[na].val.clusterDim.y = 1;
+        attrs[na].val.clusterDim.z = 1;
+        ++na;
+    } else {
+        const int slots = num_sms();
+        cfg.gridDim = dim3(p.num_tiles < slots ? p.num_tiles : slots, 1, 1);
+    }
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = attrs;
+    cfg.numAttrs = na;
+    if (take_injected_failure(kInjectLaunch)) return LOWBIT_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, ms, mz, mo, p) == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
+}
+
+template <int BITS>
+lowbit_status dispatch(const VocabProduct& v, cudaStream_t s) {
+    switch (v.mode) {
+        case kVocabStats: return v.pair ? launch<kVocabStats, BITS, true>(v, s) : launch<kVocabStats, BITS, false>(v, s);
+        case kVocabGrad: return v.pair ? launch<kVocabGrad, BITS, true>(v, s) : launch<kVocabGrad, BITS, false>(v, s);
+        case kVocabDx: return v.pair ? launch<kVocabDx, BITS, true>(v, s) : launch<kVocabDx, BITS, false>(v, s);
+        default: break;
+    }
+    if constexpr (BITS == kDense)
+        if (v.mode == kVocabDw) return launch<kVocabDw, BITS, true>(v, s);
+    return LOWBIT_ERR_UNSUPPORTED;
+}
+
+}  // namespace vocab
+}  // namespace lowbit

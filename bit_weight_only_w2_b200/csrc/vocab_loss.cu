@@ -1,0 +1,277 @@
+// The softmax cross entropy over a vocabulary: workspace, order of the launches, and the small kernels around the
+// products of vocab_gemm.cuh.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "sm100_ptx.cuh"
+#include "vocab_internal.h"
+
+namespace lowbit {
+namespace {
+
+constexpr int64_t kTokensAtOnce = 16384;              // forward: tokens whose tiles' sums are kept at a time
+constexpr int64_t kPieceBytes = int64_t(128) << 20;   // backward: bytes of G formed at a time
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+template <class... P, class... A>
+lowbit_status launch_after(void (*kernel)(P...), int64_t blocks, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (take_injected_failure(kInjectLaunch)) return LOWBIT_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
+}
+
+// lse and loss of each token from its tiles' (maximum, sum): 8 tokens a block, 32 threads each, joined in a fixed
+// order.
+constexpr int kJoinTokens = 8, kJoinThreads = 256;
+__device__ __forceinline__ void join(float& R, float& S, float r, float s) {
+    const float n = fmaxf(R, r);
+    if (n == -INFINITY) {   // nothing yet: sums of zero, or a NaN
+        S += s;
+    } else {
+        S = S * exp2f((R - n) * 1.4426950408889634f) + s * exp2f((r - n) * 1.4426950408889634f);
+        R = n;
+    }
+}
+__global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const float2* __restrict__ part, const float* __restrict__ target,
+                                                                 const int32_t* __restrict__ labels, int parts, int M, int vocab,
+                                                                 float* __restrict__ loss, float* __restrict__ lse) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int k = threadIdx.x % kJoinTokens, lane = threadIdx.x / kJoinTokens;
+    constexpr int kLanes = kJoinThreads / kJoinTokens;
+    const int m = blockIdx.x * kJoinTokens + k;
+    float R = -INFINITY, S = 0.f;
+    if (m < M) {
+#pragma unroll 4
+        for (int i = lane; i < parts; i += kLanes) {
+            const float2 v = part[static_cast<size_t>(i) * M + m];
+            join(R, S, v.x, v.y);
+        }
+    }
+    __shared__ float2 sh[kLanes][kJoinTokens];
+    sh[lane][k] = make_float2(R, S);
+    __syncthreads();
+    if (lane == 0 && m < M) {
+        for (int i = 1; i < kLanes; ++i) join(R, S, sh[i][k].x, sh[i][k].y);
+        const float l = R + logf(S);
+        lse[m] = l;
+        const int label = labels[m];
+        loss[m] = static_cast<unsigned>(label) < static_cast<unsigned>(vocab) ? l - target[m] : 0.f;
+    }
+}
+
+// X with zeros in the rows of tokens without a label, which have no part in dW whatever they hold.
+__global__ void __launch_bounds__(256) keep_labelled_kernel(const uint4* __restrict__ X, const int32_t* __restrict__ labels, int vocab,
+                                                            int64_t count, int K8, uint4* __restrict__ out) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < count; i += int64_t(gridDim.x) * 256) {
+        const uint4 v = X[i];
+        out[i] = static_cast<unsigned>(labels[i / K8]) < static_cast<unsigned>(vocab) ? v : make_uint4(0, 0, 0, 0);
+    }
+}
+
+// dX from the tiles of its sums: a block takes 32 tokens of one tile, adds the slices in order and scales.
+// Tiles as vocab_kernel<kVocabDx> writes them: [slice][column tile][token tile][CTA][warp][column / 4][lane].
+template <bool PAIR>
+__global__ void __launch_bounds__(256) dx_out_kernel(const float4* __restrict__ acc, int slices, int m_tiles, int n_tiles, int M, int K,
+                                                     const int32_t* __restrict__ labels, const float* __restrict__ grad, int vocab,
+                                                     float unscale, __nv_bfloat16* __restrict__ dX) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    constexpr int kCtas = PAIR ? 2 : 1, kCols = PAIR ? 256 : 128, kHalf = kCols / 2;
+    const int b = blockIdx.x, quarter = b & 3, rank = (b >> 2) % kCtas, tile = (b >> 2) / kCtas;   // tile within a slice
+    const int m = tile % m_tiles, n = tile / m_tiles;
+    const int r0 = m * (PAIR ? 256 : 128) + rank * 128 + quarter * 32;
+    if (r0 >= M) return;
+    __shared__ uint2 sh[32][kCols / 4 + 1];
+    const int lane = threadIdx.x & 31;
+    float f = 0.f;
+    if (r0 + lane < M) {
+        f = 1.f;
+        if (unscale != 1.f) {   // packed tables: G came without the tokens' own factor
+            const bool has = static_cast<unsigned>(labels[r0 + lane]) < static_cast<unsigned>(vocab);
+            f = has ? grad[r0 + lane] * unscale : 0.f;
+        }
+    }
+    const size_t slice = static_cast<size_t>(m_tiles) * n_tiles * kCtas * 8 * (kHalf / 4) * 32;
+    for (int c = threadIdx.x >> 5; c < kCols / 4; c += 8) {
+        const int warp = quarter + 4 * (c / (kHalf / 4));
+        const float4* at = acc + ((static_cast<size_t>(tile) * kCtas + rank) * 8 + warp) * (kHalf / 4) * 32 + (c % (kHalf / 4)) * 32 + lane;
+        float4 s = at[0];
+        for (int i = 1; i < slices; ++i) {
+            const float4 v = at[i * slice];
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x * f, s.y * f), hi = __floats2bfloat162_rn(s.z * f, s.w * f);
+        sh[lane][c] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+    __syncthreads();
+    // (K is a multiple of 8: whole 16-byte stores)
+    for (int i = threadIdx.x; i < 32 * (kCols / 8); i += 256) {
+        const int r = i / (kCols / 8), c = i % (kCols / 8), col = n * kCols + 8 * c;
+        if (r0 + r < M && col < K) {
+            const uint2 a = sh[r][2 * c], d = sh[r][2 * c + 1];
+            *reinterpret_cast<uint4*>(dX + static_cast<size_t>(r0 + r) * K + col) = make_uint4(a.x, a.y, d.x, d.y);
+        }
+    }
+}
+
+lowbit_status product(int mode, bool pair, const LossProblem& p, const LossLayout& l, uint8_t* ws, int64_t v0, int64_t cols, bool first,
+                      cudaStream_t stream) {
+    VocabProduct v;
+    v.mode = mode;
+    v.pair = pair;
+    v.p = &p;
+    v.l = &l;
+    v.ws = ws;
+    v.v0 = v0;
+    v.cols = cols;
+    v.first = first;
+    switch (p.table.bits) {
+        case 1: return vocab_product_b1(v, stream);
+        case 2: return vocab_product_b2(v, stream);
+        case 4: return vocab_product_b4(v, stream);
+        default: return vocab_product_dense(v, stream);
+    }
+}
+
+// The fp16 copy of X that packed tables are multiplied with.
+lowbit_status copy_x(const LossProblem& p, const LossLayout& l, uint8_t* ws, cudaStream_t stream) {
+    if (p.table.bits == kDense) return LOWBIT_OK;
+    GemmProblem g = {};
+    g.M = p.M;
+    g.K = p.table.K;
+    g.X = p.X;
+    g.workspace = ws + l.xh;
+    return launch_convert_x(g, stream);
+}
+
+}  // namespace
+
+LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backward, bool need_dw) {
+    LossLayout l = {};
+    if (!backward && M > kTokensAtOnce) M = kTokensAtOnce;
+    // 128 x 128 tiles: up to 128 tokens, where the table's rows are read once in any case and the wider tile's
+    // second 128 rows would stay empty.
+    l.pair = M > 128;
+    const int64_t side = l.pair ? 256 : 128;
+    l.m_tiles = (M + side - 1) / side;
+    l.n_tiles = (vocab + side - 1) / side;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    const WorkspaceLayout x = workspace_layout(M, K);
+    if (bits != kDense) {
+        l.xh = take(x.total);
+        l.rowmul = l.xh + x.rowmul_offset;
+    }
+    if (!backward) {
+        l.target = take(static_cast<size_t>(M) * 4);
+        l.part = take(static_cast<size_t>(2 * l.n_tiles) * M * 8);
+        l.total = at;
+        return l;
+    }
+    const int64_t whole = up(vocab, 256), tokens = M > 0 ? M : 1;
+    int64_t most = kPieceBytes / (2 * tokens) / 256 * 256;
+    if (most < 256) most = 256;
+    const int64_t pieces = (vocab + most - 1) / most;
+    l.piece = up((vocab + pieces - 1) / pieces, 256);
+    l.dx_tiles = (K + side - 1) / side;
+    // Slices of a piece's reduction, whose sums are kept apart: as many as make the last wave of tiles full, each of
+    // at least 8 stages, weighed against 4 stages' worth of time for each tile's beginning and end.
+    const int64_t tiles = l.m_tiles * l.dx_tiles, slots = l.pair ? 74 : 148, stages = (l.piece + 63) / 64;
+    double best = 0;
+    for (int s = 1; s <= 64 && (s == 1 || (s * 8 <= stages && s * tiles <= 8 * slots)); ++s) {
+        const double cost = static_cast<double>((tiles * s + slots - 1) / slots) * (static_cast<double>((stages + s - 1) / s) + 4.0);
+        if (s == 1 || cost < 0.97 * best) {
+            best = cost;
+            l.slices = s;
+        }
+    }
+    const int64_t per = (stages + l.slices - 1) / l.slices;
+    l.slices = static_cast<int>((stages + per - 1) / per);   // (no empty ones; a shorter last piece never has more)
+    // G and the sums take room that grows with M, so that a workspace for M tokens serves fewer too.
+    const size_t tile = static_cast<size_t>(side) * side * 4;
+    size_t g = static_cast<size_t>(kPieceBytes) > static_cast<size_t>(tokens) * 512 ? kPieceBytes : static_cast<size_t>(tokens) * 512;
+    if (g > static_cast<size_t>(tokens) * whole * 2) g = static_cast<size_t>(tokens) * whole * 2;
+    size_t acc = 8 * slots * tile < 64 * tiles * tile ? 8 * slots * tile : 64 * tiles * tile;
+    if (acc < tiles * tile) acc = tiles * tile;
+    if (need_dw) l.xz = take(static_cast<size_t>(M) * K * 2);
+    l.g = take(g);
+    l.acc = take(acc);
+    l.total = at;
+    return l;
+}
+
+lowbit_status loss_forward(const LossProblem& all, const LossLayout& l0, uint8_t* ws, cudaStream_t stream) {
+    for (int64_t m0 = 0; m0 < all.M; m0 += kTokensAtOnce) {
+        LossProblem p = all;
+        p.M = all.M - m0 < kTokensAtOnce ? all.M - m0 : kTokensAtOnce;
+        p.X = static_cast<const uint8_t*>(all.X) + static_cast<size_t>(m0) * all.table.K * 2;
+        p.labels = all.labels + m0;
+        p.loss = all.loss + m0;
+        p.lse_out = all.lse_out + m0;
+        const LossLayout l = m0 == 0 ? l0 : loss_layout(p.M, p.vocab, p.table.K, p.table.bits, false, false);
+        lowbit_status st = copy_x(p, l, ws, stream);
+        if (st == LOWBIT_OK) st = product(kVocabStats, l.pair, p, l, ws, 0, p.vocab, true, stream);
+        if (st == LOWBIT_OK)
+            st = launch_after(loss_join_kernel, (p.M + kJoinTokens - 1) / kJoinTokens, kJoinThreads, stream,
+                              reinterpret_cast<const float2*>(ws + l.part), reinterpret_cast<const float*>(ws + l.target), p.labels,
+                              static_cast<int>(2 * l.n_tiles), static_cast<int>(p.M), static_cast<int>(p.vocab), p.loss, p.lse_out);
+        if (st != LOWBIT_OK) return st;
+    }
+    return LOWBIT_OK;
+}
+
+lowbit_status loss_backward(const LossProblem& p, const LossLayout& l, uint8_t* ws, cudaStream_t stream) {
+    const int64_t K = p.table.K;
+    lowbit_status st = copy_x(p, l, ws, stream);
+    if (st != LOWBIT_OK) return st;
+    if (p.dW) {
+        if (p.table.N > p.vocab &&
+            cudaMemsetAsync(static_cast<uint8_t*>(p.dW) + static_cast<size_t>(p.vocab) * K * 2, 0,
+                            static_cast<size_t>(p.table.N - p.vocab) * K * 2, stream) != cudaSuccess)
+            return LOWBIT_ERR_CUDA;
+        const int64_t count = p.M * (K / 8), blocks = (count + 255) / 256;
+        st = launch_after(keep_labelled_kernel, blocks < 148 * 8 ? blocks : 148 * 8, 256, stream, static_cast<const uint4*>(p.X), p.labels,
+                          static_cast<int>(p.vocab), count, static_cast<int>(K / 8), reinterpret_cast<uint4*>(ws + l.xz));
+        if (st != LOWBIT_OK) return st;
+    }
+    int slices = l.slices;   // of a whole piece: the buffers that every piece adds to
+    for (int64_t v0 = 0; v0 < p.vocab; v0 += l.piece) {
+        const int64_t cols = p.vocab - v0 < l.piece ? p.vocab - v0 : l.piece;
+        if ((st = product(kVocabGrad, l.pair, p, l, ws, v0, cols, v0 == 0, stream)) != LOWBIT_OK) return st;
+        if ((st = product(kVocabDx, l.pair, p, l, ws, v0, cols, v0 == 0, stream)) != LOWBIT_OK) return st;
+        if (v0 == 0) {   // (as the launch cuts the first piece, which a small vocabulary does not fill)
+            const int64_t stages = (cols + 63) / 64, per = (stages + slices - 1) / slices;
+            slices = static_cast<int>((stages + per - 1) / per);
+        }
+        if (p.dW && (st = product(kVocabDw, true, p, l, ws, v0, cols, true, stream)) != LOWBIT_OK) return st;
+    }
+    const int64_t blocks = l.m_tiles * l.dx_tiles * (l.pair ? 2 : 1) * 4;
+    const float unscale = p.table.bits == kDense ? 1.f : 1.f / 32768.f;
+    return launch_after(l.pair ? dx_out_kernel<true> : dx_out_kernel<false>, blocks, 256, stream,
+                        reinterpret_cast<const float4*>(ws + l.acc), slices, static_cast<int>(l.m_tiles), static_cast<int>(l.dx_tiles),
+                        static_cast<int>(p.M), static_cast<int>(K), p.labels, p.grad, static_cast<int>(p.vocab), unscale,
+                        static_cast<__nv_bfloat16*>(p.dX));
+}
+
+}  // namespace lowbit

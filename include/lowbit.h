@@ -341,6 +341,65 @@ lowbit_status lowbit_checkpoint_store(const void* X, int64_t M, int64_t K, uint8
 lowbit_status lowbit_checkpoint_load(const uint8_t* codes, const uint8_t* exps, int64_t M, int64_t K, void* X,
                                      void* stream);
 
+/* ---- A vocabulary: token embeddings and the softmax cross entropy --------------------------------
+ *
+ * The two ends of a model whose linears the entry points above run. A table [N][K] holds a row per token of the
+ * vocabulary; it is packed as a linear's W is (`bits` 1, 2 or 4, with scales and zeros, N a multiple of 8, filled
+ * up with rows that no token has), or bf16 (`bits` 16: W bf16 [N][K], K a multiple of 8, scales and zeros NULL,
+ * group_size ignored). Tokens and labels are int32.
+ *
+ *   embedding       Y[t] = multiplier * W[token t], zeros for a token outside 0 .. N-1
+ *   its gradient    dE[v] = multiplier * the sum of dY[t] over the tokens t of row first + v, v = 0 .. rows-1
+ *   cross entropy   l = X W^T over the first `vocab` rows, lse[m] = log(sum_v exp l[m][v]),
+ *                   loss[m] = lse[m] - l[m][label m], or 0 for a label outside 0 .. vocab-1
+ *   its gradients   G[m][v] = grad[m] * (exp(l[m][v] - lse[m]) - [v = label m]), zeros for such a label;
+ *                   dX = G W, dW = G^T X
+ *
+ * The logits are never stored: the forward keeps a maximum and a sum per token and 128 columns, the backward forms
+ * them again, a piece of the vocabulary at a time. The pages have no counterpart. All calls are asynchronous on
+ * `stream` and never synchronise; results do not depend on timing. No output and no workspace may overlap an input
+ * or another output; a workspace belongs to one call until its work on the GPU is done. */
+
+/* Bytes of workspace of lowbit_cross_entropy (backward = 0) and lowbit_cross_entropy_backward (1, or 2 where dW is
+ * wanted), for M tokens or any fewer. The backward's holds up to 128 MB of G (at least 256 columns of it) and fp32
+ * sums of dX. 0 for invalid arguments. */
+size_t lowbit_cross_entropy_workspace_size(int64_t M, int64_t vocab, int64_t K, int bits, int backward);
+
+/* loss fp32 [M] and lse fp32 [M] of X bf16 [M][K] (16-byte aligned). Sums are fp32. A packed table's weights are the
+ * values that lowbit_gemm decodes, a uint4 weight as the sum of two fp16 values (2^-22 relative; 2^-25 absolute below
+ * fp16's normal range), so the loss is good to fp32 sums of K products. A row of X with an infinity or NaN has a lse
+ * and loss that are not finite; other rows are not touched by it. 1 <= vocab <= N (else LOWBIT_ERR_INVALID_ARG). */
+lowbit_status lowbit_cross_entropy(int64_t M, int64_t vocab, int64_t N, int64_t K, int bits, int group_size, const void* X,
+                                   const void* W, const void* scales, const void* zeros, const int32_t* labels, float* loss,
+                                   float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients for grad fp32 [M], the gradient of each token's loss, and the forward's lse:
+ *   dX   bf16 [M][K], 16-byte aligned; zeros for a token without a label
+ *   dW   bf16 [N][K], 16-byte aligned, or NULL (bf16 tables only, else LOWBIT_ERR_UNSUPPORTED); zeros from row
+ *        `vocab` on. What X holds for a token without a label does not matter.
+ * G is rounded once, to bf16 (bf16 tables, after the factor grad) or to fp16 (packed ones, before it, times 2^15:
+ * 2^-40 absolute at the least); a uint4 weight is rounded to fp16 once for dX; sums are fp32; dX and dW are rounded once. */
+lowbit_status lowbit_cross_entropy_backward(int64_t M, int64_t vocab, int64_t N, int64_t K, int bits, int group_size,
+                                            const void* X, const void* W, const void* scales, const void* zeros,
+                                            const int32_t* labels, const float* lse, const float* grad, void* dX, void* dW,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Y bf16 [T][K], 16-byte aligned, of tokens int32 [T]. The product with the multiplier is rounded to bf16 once (a packed
+ * row's values are formed in fp32, 2^-24 relative for each product). */
+lowbit_status lowbit_embedding(int64_t T, int64_t N, int64_t K, int bits, int group_size, const int32_t* tokens, const void* W,
+                               const void* scales, const void* zeros, float multiplier, void* Y, void* stream);
+
+/* Bytes of workspace of lowbit_embedding_backward, for T tokens or any fewer. 0 for invalid arguments. */
+size_t lowbit_embedding_workspace_size(int64_t T, int64_t rows, int64_t K);
+
+/* dE bf16 [rows][K], written in full (zeros for a row without tokens), of dY bf16 [T][K], both 16-byte aligned, K a
+ * multiple of 8. Only the rows first .. first + rows - 1 of the table have a gradient (the whole table, or the tokens
+ * added to a frozen one); tokens outside them count for nothing. A row's sum is fp32, in the tokens' order, and is
+ * rounded once. */
+lowbit_status lowbit_embedding_backward(int64_t T, int64_t K, int64_t first, int64_t rows, const int32_t* tokens,
+                                        const void* dY, float multiplier, void* dE, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif
