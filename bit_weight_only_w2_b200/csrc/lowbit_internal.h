@@ -64,7 +64,8 @@ struct LowRank {            // a low-rank term added before Y is rounded: Y[m] +
     int num, rank;
 };
 lowbit_status smallm_launch(const GemmProblem& g, int rows, int ksplit, bool swap, cudaStream_t stream,
-                            const LowRank* lr = nullptr);
+                            const LowRank* lr = nullptr, bool f32 = false, int64_t pitch = 0);
+// (f32: Y is float [M][N]; pitch: elements between the scales' rows, N unless given)
 
 // Device address of the current device's status word (nullptr on failure).
 unsigned* device_status_address();

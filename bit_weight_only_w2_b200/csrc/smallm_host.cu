@@ -12,7 +12,8 @@ namespace lowbit {
 namespace smallm {
 namespace {
 
-const void* kernel_for(int bits, int gs, int noct, bool swap, bool lr) {
+const void* kernel_for(int bits, int gs, int noct, bool swap, bool lr, bool f32) {
+    if (f32) return bits == 1 ? kernel_f32_b1(gs, noct, swap) : bits == 2 ? kernel_f32_b2(gs, noct, swap) : kernel_f32_b4(gs, noct, swap);
     if (lr) return bits == 1 ? kernel_lr_b1(gs, noct, swap) : bits == 2 ? kernel_lr_b2(gs, noct, swap) : kernel_lr_b4(gs, noct, swap);
     switch (bits) {
         case 1: return kernel_b1(gs, noct, swap);
@@ -31,7 +32,7 @@ bool prepare(const void* fn) {
         const void* fn;
         int dev;
     };
-    static Done done[2 * 8 * 3 * 2 * (kMaxOct + kMaxOct / 2)];
+    static Done done[3 * 8 * 3 * 2 * (kMaxOct + kMaxOct / 2)];
     static int used = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
@@ -125,14 +126,14 @@ Choice choose(const void* probe, int bits, int gs, int N, int K, int force_rows,
 }
 
 template <int BITS, int GS>
-lowbit_status launch(const GemmProblem& g, int force_rows, int force_split, bool swap, const LowRank* lr,
+lowbit_status launch(const GemmProblem& g, int force_rows, int force_split, bool swap, const LowRank* lr, bool f32, int64_t pitch,
                      cudaStream_t stream) {
     using F = Fmt<BITS, GS>;
     const int M = static_cast<int>(g.M), N = static_cast<int>(g.N), K = static_cast<int>(g.K);
-    const void* probe = kernel_for(BITS, GS, 8, swap, lr != nullptr);
+    const void* probe = kernel_for(BITS, GS, 8, swap, lr != nullptr, f32);
     if (!probe || !prepare(probe)) return LOWBIT_ERR_CUDA;
     const Choice ch = choose(probe, BITS, GS, N, K, force_rows, force_split, swap);
-    const void* fn = kernel_for(BITS, GS, ch.rows / 8, swap, lr != nullptr);
+    const void* fn = kernel_for(BITS, GS, ch.rows / 8, swap, lr != nullptr, f32);
     if (!fn || !prepare(fn)) return LOWBIT_ERR_CUDA;
     LrParams p = {};
     int smem = 0;
@@ -162,10 +163,10 @@ lowbit_status launch(const GemmProblem& g, int force_rows, int force_split, bool
     ok = ok && make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, g.Wp, uint64_t(K) * BITS / 32, N,
                            uint64_t(K) * BITS / 8, F::kWBoxWords, ch.rows,
                            BITS == 1 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
-    ok = ok && make_map_2d(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, g.scales, N, K / GS, uint64_t(N) * 2, ch.rows,
+    ok = ok && make_map_2d(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, g.scales, N, K / GS, uint64_t(pitch) * 2, ch.rows,
                            F::kGroups, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (BITS == 4)
-        ok = ok && make_map_2d(&mz, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, g.zeros, N, K / GS, uint64_t(N) * 2,
+        ok = ok && make_map_2d(&mz, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, g.zeros, N, K / GS, uint64_t(pitch) * 2,
                                ch.rows, F::kGroups, CU_TENSOR_MAP_SWIZZLE_NONE);
     else
         mz = ms;
@@ -201,17 +202,18 @@ lowbit_status launch(const GemmProblem& g, int force_rows, int force_split, bool
 bool smallm_supported(const GemmProblem& g) { return g.M >= 1 && g.M <= smallm::kTokens; }
 
 lowbit_status smallm_launch(const GemmProblem& g, int rows, int ksplit, bool swap, cudaStream_t stream,
-                            const LowRank* lr) {
+                            const LowRank* lr, bool f32, int64_t pitch) {
+    if (!pitch) pitch = g.N;
     if (!smallm_supported(g) || (swap && g.M > smallm::kSwapTokens)) return LOWBIT_ERR_UNSUPPORTED;
     if (rows < 0 || rows > smallm::kMaxRows || rows % (swap ? 16 : 8) != 0 || ksplit < 0 || ksplit > 8)
         return LOWBIT_ERR_UNSUPPORTED;
     switch (g.bits * 1000 + g.group_size) {
-        case 1064: return smallm::launch<1, 64>(g, rows, ksplit, swap, lr, stream);
-        case 1128: return smallm::launch<1, 128>(g, rows, ksplit, swap, lr, stream);
-        case 2064: return smallm::launch<2, 64>(g, rows, ksplit, swap, lr, stream);
-        case 2128: return smallm::launch<2, 128>(g, rows, ksplit, swap, lr, stream);
-        case 4064: return smallm::launch<4, 64>(g, rows, ksplit, swap, lr, stream);
-        case 4128: return smallm::launch<4, 128>(g, rows, ksplit, swap, lr, stream);
+        case 1064: return smallm::launch<1, 64>(g, rows, ksplit, swap, lr, f32, pitch, stream);
+        case 1128: return smallm::launch<1, 128>(g, rows, ksplit, swap, lr, f32, pitch, stream);
+        case 2064: return smallm::launch<2, 64>(g, rows, ksplit, swap, lr, f32, pitch, stream);
+        case 2128: return smallm::launch<2, 128>(g, rows, ksplit, swap, lr, f32, pitch, stream);
+        case 4064: return smallm::launch<4, 64>(g, rows, ksplit, swap, lr, f32, pitch, stream);
+        case 4128: return smallm::launch<4, 128>(g, rows, ksplit, swap, lr, f32, pitch, stream);
         default: return LOWBIT_ERR_UNSUPPORTED;
     }
 }

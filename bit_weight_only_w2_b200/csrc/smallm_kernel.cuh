@@ -233,7 +233,7 @@ __device__ __forceinline__ float2 lr_term(const LrParams& p, int a, int m, int n
     return s;
 }
 
-template <int BITS, int GS, int NOCT, bool SWAP, bool LR>
+template <int BITS, int GS, int NOCT, bool SWAP, bool LR, bool F32 = false>
 __global__ void __launch_bounds__(kThreads, 1)
     lowbit_smallm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_z,
@@ -701,12 +701,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int ne = n + (e >> 1) * 8, te = t0 + (e & 1);
-                        if (ne < p.N && te < p.M) p.Y[static_cast<size_t>(te) * p.N + ne] = __float2bfloat16_rn(vv[e]);
+                        if (ne < p.N && te < p.M) {
+                            if constexpr (F32)
+                                reinterpret_cast<float*>(p.Y)[static_cast<size_t>(te) * p.N + ne] = vv[e];
+                            else
+                                p.Y[static_cast<size_t>(te) * p.N + ne] = __float2bfloat16_rn(vv[e]);
+                        }
                     }
                 }
             } else {
                 const int n = n0 + 8 * o + 2 * q;
                 if (n < p.N && dcheck(n >= 0 && n + 1 < p.N && o < NUT, p.status)) {
+                    if constexpr (F32) {
+                        float* y = reinterpret_cast<float*>(p.Y) + n;
+                        if (g < p.M) *reinterpret_cast<float2*>(y + static_cast<size_t>(g) * p.N) = make_float2(v.x, v.y);
+                        if (g + 8 < p.M) *reinterpret_cast<float2*>(y + static_cast<size_t>(g + 8) * p.N) = make_float2(v.z, v.w);
+                        return;
+                    }
                     if (g < p.M)
                         *reinterpret_cast<__nv_bfloat162*>(p.Y + static_cast<size_t>(g) * p.N + n) =
                             __floats2bfloat162_rn(v.x, v.y);
@@ -770,7 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Kernel entry for (BITS, GS), `noct` octets per tile (1..16) and the orientation (`swap`:
-// weights as the 16-row operand, even `noct` only), or nullptr; kernel_lr_*: with the low-rank term.
+// weights as the 16-row operand, even `noct` only), or nullptr; kernel_lr_*: with the low-rank term,
+// kernel_f32_*: Y in fp32.
 // One definition per code width and variant lives in its own translation unit so the
 // instantiations build in parallel.
 const void* kernel_b1(int group_size, int noct, bool swap);
@@ -779,25 +791,29 @@ const void* kernel_b4(int group_size, int noct, bool swap);
 const void* kernel_lr_b1(int group_size, int noct, bool swap);
 const void* kernel_lr_b2(int group_size, int noct, bool swap);
 const void* kernel_lr_b4(int group_size, int noct, bool swap);
+const void* kernel_f32_b1(int group_size, int noct, bool swap);
+const void* kernel_f32_b2(int group_size, int noct, bool swap);
+const void* kernel_f32_b4(int group_size, int noct, bool swap);
 
 }  // namespace smallm
 }  // namespace lowbit
 
 // Defines NAME: tables of the sixteen octet counts (and the eight even ones with weights as the
 // 16-row operand) for both group sizes.
-#define LOWBIT_SMALLM_TABLE(NAME, BITS, LR)                                                           \
+#define LOWBIT_SMALLM_TABLE(NAME, BITS, LR) LOWBIT_SMALLM_TABLE_OF(NAME, BITS, LR, false)
+#define LOWBIT_SMALLM_TABLE_OF(NAME, BITS, LR, F32)                                                   \
     namespace lowbit {                                                                                \
     namespace smallm {                                                                                \
     template <int GS, int... Ns>                                                                      \
     static const void* pick(int noct, std::integer_sequence<int, Ns...>) {                            \
         static const void* const table[] = {                                                          \
-            reinterpret_cast<const void*>(&lowbit_smallm_kernel<BITS, GS, Ns + 1, false, LR>)...};    \
+            reinterpret_cast<const void*>(&lowbit_smallm_kernel<BITS, GS, Ns + 1, false, LR, F32>)...}; \
         return (noct >= 1 && noct <= static_cast<int>(sizeof...(Ns))) ? table[noct - 1] : nullptr;    \
     }                                                                                                 \
     template <int GS, int... Ns>                                                                      \
     static const void* pick_swap(int noct, std::integer_sequence<int, Ns...>) {                       \
         static const void* const table[] = {                                                          \
-            reinterpret_cast<const void*>(&lowbit_smallm_kernel<BITS, GS, 2 * (Ns + 1), true, LR>)...}; \
+            reinterpret_cast<const void*>(&lowbit_smallm_kernel<BITS, GS, 2 * (Ns + 1), true, LR, F32>)...}; \
         return (noct >= 2 && noct % 2 == 0 && noct / 2 <= static_cast<int>(sizeof...(Ns)))           \
                    ? table[noct / 2 - 1] : nullptr;                                                   \
     }                                                                                                 \

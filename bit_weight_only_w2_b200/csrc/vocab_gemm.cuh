@@ -82,6 +82,7 @@ struct Params {
     int v0;                 // first column (vocabulary row) of the piece
     int groups;             // scale groups per 128 codes: 1 or 2
     uint32_t wtx;           // bytes of a stage of words
+    float evened;           // kLogits: makes up for the sums' truncation
     const float* rowmul;    // packed: the power of two taken out of each token's row
     const int32_t* labels;
     const float* lse;
@@ -118,24 +119,68 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return d;
 }
 
-// What rounding (q - z) s to fp16 left of the four pairs of a uint4 word, itself rounded to fp16 (decode_word_b4
-// gave the first terms).
-__device__ __forceinline__ void decode_rest_b4(uint32_t v, uint16_t s, float cz, uint32_t* out, int w) {
-    uint32_t first[32];
-    decode_word_b4(v, s, cz, first, w);
-    constexpr uint32_t kMagic = 0x64006400u;
-    constexpr uint32_t kMul[2] = {0x3C003C00u, 0x2C002C00u};
-    constexpr uint32_t kAdd[2] = {0xE400E400u, 0xD400D400u};
+// One row's 64 codes of a stage of words, and their group's scale (and zero). piece(c) decodes columns 8c .. 8c + 7,
+// one 16-byte piece of the operand's row, into `hi` and, for uint4 logits, what is left into `lo`, with packed fp16
+// arithmetic only (conversions between fp32 and fp16 run at a fraction of its rate: forming (q - z) s in fp32 took
+// 4600 clocks for 128 x 128 codes, this 1/5 of it). In block order pair p of a block's four words is one such piece.
+template <int BITS, int TERMS>
+struct Row64 {
+    uint32_t words[2 * BITS];
+    uint32_t s2, zh2, zl2;   // scale; zero, and what was left of it, in both halves
+
+    __device__ __forceinline__ void load(const uint8_t* wrow, int row, int half, uint16_t s, uint16_t z) {
+        if (BITS == 1) {
+            const uint2 v = *reinterpret_cast<const uint2*>(wrow + half * 8);
+            words[0] = v.x;
+            words[1] = v.y;
+        } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int i = 16 * (w >> 2) + 4 * c + (w & 3);
-        const uint32_t e = and_or(v >> (c < 2 ? 0 : 8), 0x000F000Fu << (4 * (c & 1)), kMagic);
-        float lo, hi;
-        fma_f16x2_f32(f16x2_fma(e, kMul[c & 1], kAdd[c & 1]), s, cz, lo, hi);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&first[i]));
-        out[i] = pack_f16x2(lo - f.x, hi - f.y);
+            for (int q = 0; q < BITS / 2; ++q) {
+                // (TMA's 32- and 64-byte swizzles)
+                const int chunk = BITS == 2 ? half ^ ((row >> 2) & 1) : (2 * half + q) ^ ((row >> 1) & 3);
+                const uint4 v = *reinterpret_cast<const uint4*>(wrow + chunk * 16);
+                words[4 * q] = v.x; words[4 * q + 1] = v.y; words[4 * q + 2] = v.z; words[4 * q + 3] = v.w;
+            }
+        }
+        s2 = s | (static_cast<uint32_t>(s) << 16);
+        if (BITS == 4) {
+            zh2 = z | (static_cast<uint32_t>(z) << 16);
+            if (TERMS == 2) {
+                // z = zh + zl, both exact, with zh so coarse (2^-6 up to |z| = 8, then by |z|) that q - zh is exact in
+                // fp16: (z + 24) - 24 rounds z to the step of fp16 at 16 .. 32. (Beyond 2^14 zh = z.)
+                constexpr uint32_t k24 = 0x4E004E00u;
+                const uint32_t zr = f16x2_sub(f16x2_fma(zh2, 0x3C003C00u, k24), k24);
+                const uint32_t rest = f16x2_sub(zr, zh2);   // -zl
+                const bool coarse = (z & 0x7FFFu) < 0x7400u;
+                zl2 = coarse ? rest : 0u;
+                zh2 = coarse ? zr : zh2;
+            }
+        }
     }
-}
+    __device__ __forceinline__ void piece(int c, uint32_t (&hi)[4], uint32_t (&lo)[4]) const {
+        constexpr uint32_t kMagic = 0x64006400u;   // 1024.0, and the constants of decode_word_b2 / _b4
+        constexpr uint32_t kMul[5] = {0x3C003C00u, 0x34003400u, 0x2C002C00u, 0x24002400u, 0x1C001C00u};
+        constexpr uint32_t kAdd2[5] = {0xE401E401u, 0xDC04DC04u, 0xD410D410u, 0xCC40CC40u, 0xC500C500u};
+        constexpr uint32_t kAdd4[2] = {0xE400E400u, 0xD400D400u};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (BITS == 1) {            // plain order: pairs 4 (c % 4) .. + 3 of word c / 4
+                hi[q] = xor_andnot(s2, words[c >> 2] << (15 - (4 * (c & 3) + q)), 0x80008000u);
+            } else if (BITS == 2) {     // pair c of word q: f - 1 exactly, times s exactly
+                const int j = c < 5 ? c : c - 5;
+                const uint32_t e = and_or(words[q] >> (c < 5 ? 0 : 10), 0x00030003u << (2 * j), kMagic);
+                hi[q] = f16x2_mul(f16x2_fma(e, kMul[j], kAdd2[j]), s2);
+            } else {                    // pair c % 4 of word q of block c / 4
+                const int k = c & 3;
+                const uint32_t e = and_or(words[4 * (c >> 2) + q] >> (k < 2 ? 0 : 8), 0x000F000Fu << (4 * (k & 1)), kMagic);
+                const uint32_t d = f16x2_sub(f16x2_fma(e, kMul[2 * (k & 1)], kAdd4[k & 1]), zh2);
+                hi[q] = f16x2_mul(d, s2);
+                // d s = hi + (d s - hi), the second exact in fp16 (above its smallest step), and (q - z) s = d s - zl s
+                if (TERMS == 2) lo[q] = f16x2_fma(zl2, s2, f16x2_fma(d, s2, hi[q] ^ 0x80008000u));
+            }
+        }
+    }
+};
 
 template <int MODE, int BITS, bool PAIR>
 __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
@@ -377,58 +422,34 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                     if (!__all_sync(0xffffffffu, mbar_wait(&wfull[ws], (wit / SW) & 1u, abort_flag, p.status))) { ok = false; break; }
                     const uint8_t* st = smem + C::kWOff + ws * C::kWStageBytes;
                     const uint8_t* wrow = st + row * C::kWRowBytes;
-                    uint32_t words[2 * BITS];
-                    if (BITS == 1) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(wrow + half * 8);
-                        words[0] = v.x;
-                        words[1] = v.y;
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < BITS / 2; ++q) {
-                            // (TMA's 32- and 64-byte swizzles)
-                            const int chunk = BITS == 2 ? half ^ ((row >> 2) & 1) : (2 * half + q) ^ ((row >> 1) & 3);
-                            const uint4 v = *reinterpret_cast<const uint4*>(wrow + chunk * 16);
-                            words[4 * q] = v.x; words[4 * q + 1] = v.y; words[4 * q + 2] = v.z; words[4 * q + 3] = v.w;
-                        }
-                    }
                     const int at = (p.groups == 2 ? half : 0) * C::kWRows + row;
-                    const uint16_t sb = reinterpret_cast<const uint16_t*>(st + C::kWBytes)[at];
-                    float cz = 0.f;
-                    if (BITS == 4)   // -z * s, exact in fp32
-                        cz = -__half2float(reinterpret_cast<const __half*>(st + C::kWBytes + C::kSBytes)[at]) *
-                             __half2float(__ushort_as_half(sb));
+                    Row64<BITS, T> codes;
+                    codes.load(wrow, row, half, reinterpret_cast<const uint16_t*>(st + C::kWBytes)[at],
+                               BITS == 4 ? reinterpret_cast<const uint16_t*>(st + C::kWBytes + C::kSBytes)[at] : uint16_t(0));
+                    const uint32_t i0 = it + (C::kLogits ? half * T : 0);   // the ring's stage, or stages, that it fills
+                    uint32_t dst[T];
 #pragma unroll
                     for (int term = 0; term < T; ++term) {
-                        uint32_t out[32];
-                        if constexpr (BITS == 1) {
-                            decode_half_b1(words[0], words[1], sb | (static_cast<uint32_t>(sb) << 16), out);
-                        } else if constexpr (BITS == 2) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) decode_word_b2(words[q], sb | (static_cast<uint32_t>(sb) << 16), out, q);
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                if (term == 0)
-                                    decode_word_b4(words[q], sb, cz, out, q);
-                                else
-                                    decode_rest_b4(words[q], sb, cz, out, q);
-                            }
-                        }
-                        const uint32_t i = it + (C::kLogits ? half * T + term : 0), s = i % S;
-                        if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / S) & 1u) ^ 1u, abort_flag, p.status))) {
-                            ok = false;
-                            break;
-                        }
+                        const uint32_t i = i0 + term, s = i % S;
+                        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / S) & 1u) ^ 1u, abort_flag, p.status));
                         // kLogits: 128 rows of 64 columns; kVocabDx: two halves of 64 rows
-                        const uint32_t dst = smem_u32(smem + s * kStageBytes + kOperandBytes) + (C::kLogits ? 0 : half * 8192) + row * 128;
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            st_shared_v4(dst + ((c ^ (row & 7)) << 4), out[4 * c], out[4 * c + 1], out[4 * c + 2], out[4 * c + 3]);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) arrive_on_issuer(&bfull[s]);
+                        dst[term] = smem_u32(smem + s * kStageBytes + kOperandBytes) + (C::kLogits ? 0 : half * 8192) + row * 128;
                     }
                     if (!ok) break;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t hi[4], lo[4];
+                        codes.piece(c, hi, lo);
+                        const uint32_t to = (c ^ (row & 7)) << 4;
+                        st_shared_v4(dst[0] + to, hi[0], hi[1], hi[2], hi[3]);
+                        if (T == 2) st_shared_v4(dst[T - 1] + to, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int term = 0; term < T; ++term) arrive_on_issuer(&bfull[(i0 + term) % S]);
+                    }
                     // (freed behind the last use of what was read from it)
                     if (lane == 0) mbar_arrive(&wempty[ws]);
                 }
@@ -453,7 +474,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
             if (C::kLogits && row < p.M) {
                 label = p.labels[row];
                 if (static_cast<unsigned>(label) >= static_cast<unsigned>(p.vocab)) label = -1;
-                if (C::kPacked) mul = p.rowmul[row];
+                mul = C::kPacked ? p.rowmul[row] * p.evened : p.evened;
                 if (MODE == kVocabGrad) {
                     shift = p.lse[row] * kLog2e;
                     f = C::kPacked ? p.gscale : p.grad[row];
@@ -674,6 +695,10 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
         p.m_tiles = static_cast<int>((cols + C::kRows - 1) / C::kRows);
         p.n_tiles = static_cast<int>((K + C::kCols - 1) / C::kCols);
     }
+    // The tensor cores cut what they add to an accumulator off below its last bit, towards zero: a sum that grows evenly
+    // over n MMA steps to l loses about 0.26 n 2^-24 l (measured for n = 32 .. 320 and all formats: 2.5e-6 l at K = 2560,
+    // with a spread of a fifth of that), always to the same side. The logits are scaled up by as much.
+    p.evened = 1.f + 0.26f * 5.9604645e-8f * 4.f * static_cast<float>(p.stages);
     int slices = 1;
     if (MODE == kVocabDx) {
         slices = l.slices < p.stages ? l.slices : p.stages;

@@ -71,6 +71,79 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const float2* _
     }
 }
 
+// Up to 16 tokens of a packed table: lse and loss from logits in fp32, a cluster of CTAs per token whose (maximum, sum)
+// are joined in rank order. The logits lie in L2: 131072 of one token take 3 us.
+constexpr int kRowCtas = 8, kRowThreads = 256;
+__global__ void __cluster_dims__(kRowCtas, 1, 1) __launch_bounds__(kRowThreads)
+    loss_rows_kernel(const float* __restrict__ logits, int64_t ld, const int32_t* __restrict__ labels, int vocab, float* __restrict__ loss,
+                     float* __restrict__ lse) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int m = blockIdx.x / kRowCtas, rank = blockIdx.x % kRowCtas, tid = threadIdx.x;
+    const float* row = logits + m * ld;
+    const int per = ((vocab + kRowCtas - 1) / kRowCtas + 3) / 4 * 4, c1 = min(vocab, (rank + 1) * per);
+    float R = -INFINITY, S = 0.f;
+    auto take = [&](float v) {
+        if (v == INFINITY) {   // (R stays finite, for the joins)
+            R = 3.4e38f;
+            S += v;
+            return;
+        }
+        if (v > R) {
+            S = R == -INFINITY ? S : S * exp2f((R - v) * 1.4426950408889634f);
+            R = v;
+        }
+        S += v == -INFINITY ? 0.f : exp2f((v - R) * 1.4426950408889634f);   // (NaN stays NaN)
+    };
+    int c = rank * per + 4 * tid;
+#pragma unroll 4
+    for (; c + 3 < c1; c += 4 * kRowThreads) {
+        const float4 v = *reinterpret_cast<const float4*>(row + c);
+        const float top = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+        if (fabsf(top) < INFINITY) {
+            if (top > R) {
+                S = R == -INFINITY ? S : S * exp2f((R - top) * 1.4426950408889634f);
+                R = top;
+            }
+            S += (exp2f((v.x - R) * 1.4426950408889634f) + exp2f((v.y - R) * 1.4426950408889634f)) +
+                 (exp2f((v.z - R) * 1.4426950408889634f) + exp2f((v.w - R) * 1.4426950408889634f));
+        } else {
+            take(v.x);
+            take(v.y);
+            take(v.z);
+            take(v.w);
+        }
+    }
+    // (the last, partial group of four is this thread's)
+    for (; c < c1; ++c) take(row[c]);
+    __shared__ float2 sh[kRowThreads];
+    __shared__ float2 mine;
+    sh[tid] = make_float2(R, S);
+    __syncthreads();
+    for (int o = kRowThreads / 2; o > 0; o /= 2) {
+        if (tid < o) {
+            join(R, S, sh[tid + o].x, sh[tid + o].y);
+            sh[tid] = make_float2(R, S);
+        }
+        __syncthreads();
+    }
+    if (tid == 0) mine = make_float2(R, S);
+    cluster_sync_all();
+    if (rank == 0 && tid == 0) {
+        for (int r = 1; r < kRowCtas; ++r) {
+            const uint32_t at = map_shared_rank(smem_u32(&mine), r);
+            float a, b;
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(at) : "memory");
+            join(R, S, a, b);
+        }
+        const float l = R + logf(S);
+        lse[m] = l;
+        const int label = labels[m];
+        loss[m] = static_cast<unsigned>(label) < static_cast<unsigned>(vocab) ? l - row[label] : 0.f;
+    }
+    cluster_sync_all();   // (the others' sums are read before they exit)
+}
+
 // X with zeros in the rows of tokens without a label, which have no part in dW whatever they hold.
 __global__ void __launch_bounds__(256) keep_labelled_kernel(const uint4* __restrict__ X, const int32_t* __restrict__ labels, int vocab,
                                                             int64_t count, int K8, uint4* __restrict__ out) {
@@ -178,6 +251,13 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
         at += (bytes + 255) / 256 * 256;
         return here;
     };
+    const size_t logits = static_cast<size_t>(M < kSmallTokens ? M : kSmallTokens) * up(vocab, 8) * 4;
+    if (bits != kDense && !backward && M <= kSmallTokens) {
+        l.small = true;
+        l.logits = take(logits);
+        l.total = at;
+        return l;
+    }
     const WorkspaceLayout x = workspace_layout(M, K);
     if (bits != kDense) {
         l.xh = take(x.total);
@@ -186,7 +266,7 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
     if (!backward) {
         l.target = take(static_cast<size_t>(M) * 4);
         l.part = take(static_cast<size_t>(2 * l.n_tiles) * M * 8);
-        l.total = at;
+        l.total = bits != kDense && at < logits ? logits : at;   // (serves the small batches too)
         return l;
     }
     const int64_t whole = up(vocab, 256), tokens = M > 0 ? M : 1;
@@ -222,6 +302,24 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
 }
 
 lowbit_status loss_forward(const LossProblem& all, const LossLayout& l0, uint8_t* ws, cudaStream_t stream) {
+    if (l0.small) {
+        const Table& t = all.table;
+        GemmProblem g = {};
+        g.M = all.M;
+        g.N = up(all.vocab, 8);   // (at most t.N: the rows behind the vocabulary are not read)
+        g.K = t.K;
+        g.bits = t.bits;
+        g.group_size = t.group_size;
+        g.X = all.X;
+        g.Wp = static_cast<const uint32_t*>(t.rows);
+        g.scales = t.scales;
+        g.zeros = t.zeros;
+        g.Y = ws + l0.logits;
+        const lowbit_status st = smallm_launch(g, 0, 0, g.M <= 8, stream, nullptr, true, t.N);
+        if (st != LOWBIT_OK) return st;
+        return launch_after(loss_rows_kernel, g.M * kRowCtas, kRowThreads, stream, reinterpret_cast<const float*>(ws + l0.logits), g.N,
+                            all.labels, static_cast<int>(all.vocab), all.loss, all.lse_out);
+    }
     for (int64_t m0 = 0; m0 < all.M; m0 += kTokensAtOnce) {
         LossProblem p = all;
         p.M = all.M - m0 < kTokensAtOnce ? all.M - m0 : kTokensAtOnce;

@@ -366,8 +366,8 @@ lowbit_status lowbit_checkpoint_load(const uint8_t* codes, const uint8_t* exps, 
 size_t lowbit_cross_entropy_workspace_size(int64_t M, int64_t vocab, int64_t K, int bits, int backward);
 
 /* loss fp32 [M] and lse fp32 [M] of X bf16 [M][K] (16-byte aligned). Sums are fp32. A packed table's weights are the
- * values that lowbit_gemm decodes, a uint4 weight as the sum of two fp16 values (2^-22 relative; 2^-25 absolute below
- * fp16's normal range), so the loss is good to fp32 sums of K products. A row of X with an infinity or NaN has a lse
+ * values that lowbit_gemm decodes, a uint4 weight as the sum of two fp16 values (2^-17 of its scale, 2^-25 absolute
+ * at the least; zeros up to 2^14 in magnitude), so the loss is good to fp32 sums of K products. A row of X with an infinity or NaN has a lse
  * and loss that are not finite; other rows are not touched by it. 1 <= vocab <= N (else LOWBIT_ERR_INVALID_ARG). */
 lowbit_status lowbit_cross_entropy(int64_t M, int64_t vocab, int64_t N, int64_t K, int bits, int group_size, const void* X,
                                    const void* W, const void* scales, const void* zeros, const int32_t* labels, float* loss,
@@ -378,7 +378,8 @@ lowbit_status lowbit_cross_entropy(int64_t M, int64_t vocab, int64_t N, int64_t 
  *   dW   bf16 [N][K], 16-byte aligned, or NULL (bf16 tables only, else LOWBIT_ERR_UNSUPPORTED); zeros from row
  *        `vocab` on. What X holds for a token without a label does not matter.
  * G is rounded once, to bf16 (bf16 tables, after the factor grad) or to fp16 (packed ones, before it, times 2^15:
- * 2^-40 absolute at the least); a uint4 weight is rounded to fp16 once for dX; sums are fp32; dX and dW are rounded once. */
+ * 2^-40 absolute at the least); for dX a uint4 weight is
+ * (q - z) * s with the difference and the product rounded to fp16 (as in lowbit_gemm_dx); sums are fp32; dX and dW are rounded once. */
 lowbit_status lowbit_cross_entropy_backward(int64_t M, int64_t vocab, int64_t N, int64_t K, int bits, int group_size,
                                             const void* X, const void* W, const void* scales, const void* zeros,
                                             const int32_t* labels, const float* lse, const float* grad, void* dX, void* dW,

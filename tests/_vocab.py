@@ -72,8 +72,11 @@ class Loss:
         self.el = K * H32 * s           # fp32 sums of K products
         if table.bits != 16:            # X's fp16 copy: 2^-25 of fp16 on rows scaled to 2^15 .. 2^16
             self.el = self.el + (2.0 ** -40 * self.x.abs().amax(1))[:, None] * self.w.abs().sum(1)[None, :]
-        if table.bits == 4:             # weights as two fp16 values
-            self.el = self.el + 2.0 ** -22 * s + 2.0 ** -25 * self.x.abs().sum(1)[:, None]
+        if table.bits == 4:
+            # weights as two fp16 values, the second rounded: it is at most 2^-11 of the first and 2^-7 (2^-6 for
+            # |z| > 8) of s, so 2^-11 of that, and 2^-25 of its smallest step
+            step = table.scales.double()[:, :V].T.repeat_interleave(table.gs, 1)
+            self.el = self.el + 2.0 ** -22 * s + 2.0 ** -17 * (self.x.abs() @ step.T) + 2.0 ** -25 * self.x.abs().sum(1)[:, None]
         self.lse = torch.logsumexp(self.l, 1)
         self.target = self.l.gather(1, self.label[:, None])[:, 0]
         self.loss = torch.where(self.valid, self.lse - self.target, 0.0)
@@ -103,9 +106,9 @@ class Loss:
         eG = f.abs() * ep * (1 + half) + (half + 2 * H32) * G.abs() + f.abs() * (0 if dense else 2.0 ** -40)
         w = self.w
         dx = G @ w
-        ex = eG @ w.abs() + ((V + 16) * H32 + (H16 if self.table.bits == 4 else 0)) * (G.abs() @ w.abs())
-        if self.table.bits == 4:
-            ex = ex + 2.0 ** -25 * G.abs().sum(1)[:, None]
+        ex = eG @ w.abs() + (V + 16) * H32 * (G.abs() @ w.abs())
+        if self.table.bits == 4:   # q - z and its product with s, each rounded to fp16
+            ex = ex + (2 * H16 + H16 * H16) * (G.abs() @ w.abs()) + 2.0 ** -25 * G.abs().sum(1)[:, None]
         ex = ex + HB16 * (dx.abs() + ex)
         x = torch.where(self.valid[:, None], self.x, 0.0)
         dw = G.T @ x
