@@ -33,8 +33,7 @@
 namespace lowbit {
 namespace vocab {
 
-constexpr int kStageBytes = 32768;      // 128 x 64 of the rows' operand, 128 x 64 of the columns'
-constexpr int kOperandBytes = 16384;
+constexpr int kOperandBytes = 16384;    // 128 x 64 of the rows' operand, or of the columns' (of each of its terms)
 constexpr int kEpiWarps = 8;
 
 template <int MODE, int BITS, bool PAIR>
@@ -55,7 +54,8 @@ struct Cfg {
     static constexpr int kSBytes = kPacked ? 2 * kWRows * 2 : 0;  // room for two groups
     static constexpr int kZBytes = BITS == 4 ? kSBytes : 0;
     static constexpr int kWStageBytes = (kWBytes + kSBytes + kZBytes + 1023) / 1024 * 1024;
-    static constexpr int kWStages = kPacked ? 4 : 0;
+    static constexpr int kStageBytes = (1 + kTerms) * kOperandBytes;
+    static constexpr int kWStages = kPacked ? (kTerms == 2 ? 3 : 4) : 0;
     static constexpr int kStagingBytes = (MODE == kVocabGrad || MODE == kVocabDw) ? kEpiWarps * 4096 : 0;
     static constexpr int kFit = (kSmemLimit - 2048 - kStagingBytes - kWStages * kWStageBytes) / kStageBytes;
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
@@ -272,14 +272,14 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            constexpr uint32_t kBytes = C::kPacked ? kOperandBytes : kStageBytes;
+            constexpr uint32_t kBytes = C::kPacked ? kOperandBytes : C::kStageBytes;
             for (int t = tile0; t < p.num_tiles && ok; t += tile_step) {
                 const Tile tl = tile_of(t);
                 const int nb = tl.n0 + static_cast<int>(rank) * 128;   // first of this CTA's half of the columns
                 for (int j = tl.j0; j < tl.j1; ++j, ++it) {
                     const uint32_t s = it % S;
                     if (!mbar_wait(&empty[s], ((it / S) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
-                    uint8_t* a = smem + s * kStageBytes;
+                    uint8_t* a = smem + s * C::kStageBytes;
                     uint8_t* b = a + kOperandBytes;
                     if (issuer) mbar_arrive_expect_tx(&full[s], kCtas * kBytes);
                     auto load = [&](const CUtensorMap* map, uint8_t* dst, int x, int y) {
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                         load(&map_b, b, nb, j * 64);
                         load(&map_b, b + 8192, nb + 64, j * 64);
                     } else {
-                        load(&map_a, a, (j / T) * 64, tl.m0);
+                        load(&map_a, a, j * 64, tl.m0);
                         if (MODE == kVocabDx && !C::kPacked) {   // W [v][k]: 64 rows
                             load(&map_b, b, nb, p.v0 + j * 64);
                             load(&map_b, b + 8192, nb + 64, p.v0 + j * 64);
@@ -339,12 +339,14 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t as = smem_u32(smem + s * kStageBytes), bs = as + kOperandBytes;
+                    const uint32_t as = smem_u32(smem + s * C::kStageBytes);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
+                    for (int i = 0; i < 4 * T; ++i) {
+                        const int kk = i & 3;
+                        const uint32_t bs = as + (1 + (i >> 2)) * kOperandBytes;
                         const uint64_t ad = C::kAMn ? smem_desc_mn(as + kk * 2048, 128, 8192) : smem_desc_k_sw128(as + kk * 32);
                         const uint64_t bd = C::kBMn ? smem_desc_mn(bs + kk * 2048, 128, 8192) : smem_desc_k_sw128(bs + kk * 32);
-                        const uint32_t more = (j > tl.j0 || kk > 0) ? 1u : 0u;
+                        const uint32_t more = (j > tl.j0 || i > 0) ? 1u : 0u;
                         if (PAIR)
                             mma_f16_ss_pair(d, ad, bd, C::kIdesc, more);
                         else
@@ -381,8 +383,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                 for (int t = tile0; t < p.num_tiles && ok; t += tile_step) {
                     const Tile tl = tile_of(t);
                     const int nb = tl.n0 + static_cast<int>(rank) * 128;
-                    // (kLogits: a stage of words is 2 * T stages of the ring, and a tile has them all)
-                    const int w1 = C::kLogits ? p.stages / (2 * T) : tl.j1;
+                    // (kLogits: a stage of words is two stages of the ring, and a tile has them all)
+                    const int w1 = C::kLogits ? p.stages / 2 : tl.j1;
                     for (int w = C::kLogits ? 0 : tl.j0; w < w1; ++w, ++it) {
                         const uint32_t s = it % SW;
                         if (!mbar_wait(&wempty[s], ((it / SW) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
@@ -415,8 +417,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
             bool ok = true;
             for (int t = tile0; t < p.num_tiles && ok; t += tile_step) {
                 const Tile tl = tile_of(t);
-                const int count = C::kLogits ? p.stages / (2 * T) : tl.j1 - tl.j0;
-                for (int w = 0; w < count; ++w, ++wit, it += C::kLogits ? 2 * T : 1) {
+                const int count = C::kLogits ? p.stages / 2 : tl.j1 - tl.j0;
+                for (int w = 0; w < count; ++w, ++wit, it += C::kLogits ? 2 : 1) {
                     if (!C::kLogits && (it & 1u) != static_cast<uint32_t>(dq >> 2)) continue;   // the other four warps'
                     const uint32_t ws = wit % SW;
                     if (!__all_sync(0xffffffffu, mbar_wait(&wfull[ws], (wit / SW) & 1u, abort_flag, p.status))) { ok = false; break; }
@@ -426,30 +428,21 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                     Row64<BITS, T> codes;
                     codes.load(wrow, row, half, reinterpret_cast<const uint16_t*>(st + C::kWBytes)[at],
                                BITS == 4 ? reinterpret_cast<const uint16_t*>(st + C::kWBytes + C::kSBytes)[at] : uint16_t(0));
-                    const uint32_t i0 = it + (C::kLogits ? half * T : 0);   // the ring's stage, or stages, that it fills
-                    uint32_t dst[T];
-#pragma unroll
-                    for (int term = 0; term < T; ++term) {
-                        const uint32_t i = i0 + term, s = i % S;
-                        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / S) & 1u) ^ 1u, abort_flag, p.status));
-                        // kLogits: 128 rows of 64 columns; kVocabDx: two halves of 64 rows
-                        dst[term] = smem_u32(smem + s * kStageBytes + kOperandBytes) + (C::kLogits ? 0 : half * 8192) + row * 128;
-                    }
-                    if (!ok) break;
+                    const uint32_t i = it + (C::kLogits ? half : 0), s = i % S;   // the stage of the ring that it fills
+                    if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / S) & 1u) ^ 1u, abort_flag, p.status))) { ok = false; break; }
+                    // kLogits: 128 rows of 64 columns; kVocabDx: two halves of 64 rows
+                    const uint32_t dst = smem_u32(smem + s * C::kStageBytes + kOperandBytes) + (C::kLogits ? 0 : half * 8192) + row * 128;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         uint32_t hi[4], lo[4];
                         codes.piece(c, hi, lo);
                         const uint32_t to = (c ^ (row & 7)) << 4;
-                        st_shared_v4(dst[0] + to, hi[0], hi[1], hi[2], hi[3]);
-                        if (T == 2) st_shared_v4(dst[T - 1] + to, lo[0], lo[1], lo[2], lo[3]);
+                        st_shared_v4(dst + to, hi[0], hi[1], hi[2], hi[3]);
+                        if (T == 2) st_shared_v4(dst + kOperandBytes + to, lo[0], lo[1], lo[2], lo[3]);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-#pragma unroll
-                        for (int term = 0; term < T; ++term) arrive_on_issuer(&bfull[(i0 + term) % S]);
-                    }
+                    if (lane == 0) arrive_on_issuer(&bfull[s]);
                     // (freed behind the last use of what was read from it)
                     if (lane == 0) mbar_arrive(&wempty[ws]);
                 }
@@ -683,7 +676,7 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
     }
     const int64_t cols = v.cols;
     if (C::kLogits) {
-        p.stages = static_cast<int>(C::kPacked ? (K + 127) / 128 * 2 * C::kTerms : (K + 63) / 64);
+        p.stages = static_cast<int>(C::kPacked ? (K + 127) / 128 * 2 : (K + 63) / 64);
         p.m_tiles = static_cast<int>(l.m_tiles);
         p.n_tiles = static_cast<int>((cols + C::kCols - 1) / C::kCols);
     } else if (MODE == kVocabDx) {
@@ -698,7 +691,7 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
     // The tensor cores cut what they add to an accumulator off below its last bit, towards zero: a sum that grows evenly
     // over n MMA steps to l loses about 0.26 n 2^-24 l (measured for n = 32 .. 320 and all formats: 2.5e-6 l at K = 2560,
     // with a spread of a fifth of that), always to the same side. The logits are scaled up by as much.
-    p.evened = 1.f + 0.26f * 5.9604645e-8f * 4.f * static_cast<float>(p.stages);
+    p.evened = 1.f + 0.26f * 5.9604645e-8f * 4.f * C::kTerms * static_cast<float>(p.stages);
     int slices = 1;
     if (MODE == kVocabDx) {
         slices = l.slices < p.stages ? l.slices : p.stages;

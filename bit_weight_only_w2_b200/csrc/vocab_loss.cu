@@ -31,9 +31,10 @@ lowbit_status launch_after(void (*kernel)(P...), int64_t blocks, int threads, cu
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
 
-// lse and loss of each token from its tiles' (maximum, sum): 8 tokens a block, 32 threads each, joined in a fixed
-// order.
-constexpr int kJoinTokens = 8, kJoinThreads = 256;
+// lse and loss of each token from its tiles' (maximum, sum), joined in a fixed order: 8 tokens a block, 32 threads each
+// (the parts of neighbouring tokens are neighbours), or one token a block where few tokens would leave most SMs idle:
+// 16 tokens of 2048 parts take 17 us eight a block and 4 one a block.
+constexpr int kJoinThreads = 256;
 __device__ __forceinline__ void join(float& R, float& S, float r, float s) {
     const float n = fmaxf(R, r);
     if (n == -INFINITY) {   // nothing yet: sums of zero, or a NaN
@@ -43,6 +44,7 @@ __device__ __forceinline__ void join(float& R, float& S, float r, float s) {
         R = n;
     }
 }
+template <int kJoinTokens>
 __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const float2* __restrict__ part, const float* __restrict__ target,
                                                                  const int32_t* __restrict__ labels, int parts, int M, int vocab,
                                                                  float* __restrict__ loss, float* __restrict__ lse) {
@@ -62,8 +64,14 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const float2* _
     __shared__ float2 sh[kLanes][kJoinTokens];
     sh[lane][k] = make_float2(R, S);
     __syncthreads();
+    for (int o = kLanes / 2; o > 0; o /= 2) {
+        if (lane < o) {
+            join(R, S, sh[lane + o][k].x, sh[lane + o][k].y);
+            sh[lane][k] = make_float2(R, S);
+        }
+        __syncthreads();
+    }
     if (lane == 0 && m < M) {
-        for (int i = 1; i < kLanes; ++i) join(R, S, sh[i][k].x, sh[i][k].y);
         const float l = R + logf(S);
         lse[m] = l;
         const int label = labels[m];
@@ -331,7 +339,7 @@ lowbit_status loss_forward(const LossProblem& all, const LossLayout& l0, uint8_t
         lowbit_status st = copy_x(p, l, ws, stream);
         if (st == LOWBIT_OK) st = product(kVocabStats, l.pair, p, l, ws, 0, p.vocab, true, stream);
         if (st == LOWBIT_OK)
-            st = launch_after(loss_join_kernel, (p.M + kJoinTokens - 1) / kJoinTokens, kJoinThreads, stream,
+            st = launch_after(p.M <= 1024 ? loss_join_kernel<1> : loss_join_kernel<8>, p.M <= 1024 ? p.M : (p.M + 7) / 8, kJoinThreads, stream,
                               reinterpret_cast<const float2*>(ws + l.part), reinterpret_cast<const float*>(ws + l.target), p.labels,
                               static_cast<int>(2 * l.n_tiles), static_cast<int>(p.M), static_cast<int>(p.vocab), p.loss, p.lse_out);
         if (st != LOWBIT_OK) return st;
