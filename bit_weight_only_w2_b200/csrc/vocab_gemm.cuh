@@ -54,13 +54,20 @@ struct Cfg {
     static constexpr int kSBytes = kPacked ? 2 * kWRows * 2 : 0;  // room for two groups
     static constexpr int kZBytes = BITS == 4 ? kSBytes : 0;
     static constexpr int kWStageBytes = (kWBytes + kSBytes + kZBytes + 1023) / 1024 * 1024;
-    static constexpr int kStageBytes = (1 + kTerms) * kOperandBytes;
+    // Rings: one of both operands (bf16 tables), or one of the rows' operand, which comes from L2 with some 1500 clocks
+    // of latency, and a shorter one of the decoded columns' (in one ring the gradient of 77 tokens against uint4 rows
+    // waited for its rows: 60 against TODO us).
+    static constexpr int kAStageBytes = kPacked ? kOperandBytes : 2 * kOperandBytes;
+    static constexpr int kBStageBytes = kPacked ? kTerms * kOperandBytes : 0;
     static constexpr int kWStages = kPacked ? (kTerms == 2 ? 3 : 4) : 0;
     static constexpr int kStagingBytes = (MODE == kVocabGrad || MODE == kVocabDw) ? kEpiWarps * 4096 : 0;
-    static constexpr int kFit = (kSmemLimit - 2048 - kStagingBytes - kWStages * kWStageBytes) / kStageBytes;
-    static constexpr int kStages = kFit > 6 ? 6 : kFit;
-    static_assert(kStages >= 3, "shared memory");
-    static constexpr int kWOff = kStages * kStageBytes;
+    static constexpr int kRoom = kSmemLimit - 2048 - kStagingBytes - kWStages * kWStageBytes;
+    static constexpr int kAStages = !kPacked ? kRoom / kAStageBytes : kTerms == 2 && kStagingBytes > 0 ? 4 : 6;
+    static constexpr int kBFit = kPacked ? (kRoom - kAStages * kAStageBytes) / (kPacked ? kBStageBytes : 1) : 0;
+    static constexpr int kBStages = kBFit > 6 ? 6 : kBFit;
+    static_assert(kAStages >= 4 && (!kPacked || kBStages >= 3), "shared memory");
+    static constexpr int kBOff = kAStages * kAStageBytes;
+    static constexpr int kWOff = kBOff + kBStages * kBStageBytes;
     static constexpr int kStagingOff = kWOff + kWStages * kWStageBytes;
     static constexpr int kBarOff = kStagingOff + kStagingBytes;
     static constexpr int kSmemBytes = 1024 + kBarOff + 1024;
@@ -80,6 +87,7 @@ struct Params {
     int per_slice;          // of a slice of it (kVocabDx), else `stages`
     int m_tiles, n_tiles, num_tiles;
     int v0;                 // first column (vocabulary row) of the piece
+    int a_rows;             // rows of the rows' operand per stage (a tile of fewer tokens leaves the rest as it is)
     int groups;             // scale groups per 128 codes: 1 or 2
     uint32_t wtx;           // bytes of a stage of words
     float evened;           // kLogits: makes up for the sums' truncation
@@ -188,15 +196,16 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                  const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_z,
                  const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Params p) {
     using C = Cfg<MODE, BITS, PAIR>;
-    constexpr int S = C::kStages, SW = C::kWStages > 0 ? C::kWStages : 1, T = C::kTerms;
+    constexpr int S = C::kAStages, SB = C::kBStages > 0 ? C::kBStages : 1, SW = C::kWStages > 0 ? C::kWStages : 1, T = C::kTerms;
     constexpr int kCtas = PAIR ? 2 : 1;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-    uint64_t* bfull = full + S;       // packed: the decoded half of a stage
-    uint64_t* empty = bfull + S;
-    uint64_t* wfull = empty + S;
+    uint64_t* empty = full + S;
+    uint64_t* bfull = empty + S;      // packed: the decoded operand's ring
+    uint64_t* bempty = bfull + SB;
+    uint64_t* wfull = bempty + SB;
     uint64_t* wempty = wfull + SW;
     uint64_t* accfull = wempty + SW;
     uint64_t* accempty = accfull + 2;
@@ -218,8 +227,11 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&bfull[i], C::kDqArrivals);
             mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < SB; ++i) {
+            mbar_init(&bfull[i], C::kDqArrivals);
+            mbar_init(&bempty[i], 1);
         }
         for (int i = 0; i < SW; ++i) {
             mbar_init(&wfull[i], 1);
@@ -272,16 +284,16 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            constexpr uint32_t kBytes = C::kPacked ? kOperandBytes : C::kStageBytes;
+            const uint32_t bytes = MODE == kVocabDw ? C::kAStageBytes : (C::kPacked ? 0 : kOperandBytes) + p.a_rows * 128;
             for (int t = tile0; t < p.num_tiles && ok; t += tile_step) {
                 const Tile tl = tile_of(t);
                 const int nb = tl.n0 + static_cast<int>(rank) * 128;   // first of this CTA's half of the columns
                 for (int j = tl.j0; j < tl.j1; ++j, ++it) {
                     const uint32_t s = it % S;
                     if (!mbar_wait(&empty[s], ((it / S) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
-                    uint8_t* a = smem + s * C::kStageBytes;
+                    uint8_t* a = smem + s * C::kAStageBytes;
                     uint8_t* b = a + kOperandBytes;
-                    if (issuer) mbar_arrive_expect_tx(&full[s], kCtas * kBytes);
+                    if (issuer) mbar_arrive_expect_tx(&full[s], kCtas * bytes);
                     auto load = [&](const CUtensorMap* map, uint8_t* dst, int x, int y) {
                         if (PAIR)
                             tma_load_2d_pair(map, on_issuer(&full[s]), dst, x, y);
@@ -332,18 +344,19 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                 tc_fence_after();
                 const uint32_t d = tmem_base + b * C::kCols;
                 for (int j = tl.j0; j < tl.j1; ++j, ++it) {
-                    const uint32_t s = it % S, ph = (it / S) & 1u;
-                    if (!mbar_wait(&full[s], ph, abort_flag, p.status) ||
-                        (C::kPacked && !mbar_wait(&bfull[s], ph, abort_flag, p.status))) {
+                    const uint32_t s = it % S, sb = it % SB;
+                    if (!mbar_wait(&full[s], (it / S) & 1u, abort_flag, p.status) ||
+                        (C::kPacked && !mbar_wait(&bfull[sb], (it / SB) & 1u, abort_flag, p.status))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t as = smem_u32(smem + s * C::kStageBytes);
+                    const uint32_t as = smem_u32(smem + s * C::kAStageBytes);
+                    const uint32_t b0 = C::kPacked ? smem_u32(smem + C::kBOff + sb * C::kBStageBytes) : as + kOperandBytes;
 #pragma unroll
                     for (int i = 0; i < 4 * T; ++i) {
                         const int kk = i & 3;
-                        const uint32_t bs = as + (1 + (i >> 2)) * kOperandBytes;
+                        const uint32_t bs = b0 + (i >> 2) * kOperandBytes;
                         const uint64_t ad = C::kAMn ? smem_desc_mn(as + kk * 2048, 128, 8192) : smem_desc_k_sw128(as + kk * 32);
                         const uint64_t bd = C::kBMn ? smem_desc_mn(bs + kk * 2048, 128, 8192) : smem_desc_k_sw128(bs + kk * 32);
                         const uint32_t more = (j > tl.j0 || i > 0) ? 1u : 0u;
@@ -353,10 +366,14 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                             mma_f16_ss(d, ad, bd, C::kIdesc, more);
                     }
                     issued = true;
-                    if (PAIR)
-                        mma_commit_pair_mc(&empty[s], 0x3);
-                    else
-                        mma_commit(&empty[s]);
+                    auto release = [&](uint64_t* bar) {
+                        if (PAIR)
+                            mma_commit_pair_mc(bar, 0x3);
+                        else
+                            mma_commit(bar);
+                    };
+                    release(&empty[s]);
+                    if (C::kPacked) release(&bempty[sb]);
                 }
                 if (!ok) break;
                 if (PAIR)
@@ -428,10 +445,10 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                     Row64<BITS, T> codes;
                     codes.load(wrow, row, half, reinterpret_cast<const uint16_t*>(st + C::kWBytes)[at],
                                BITS == 4 ? reinterpret_cast<const uint16_t*>(st + C::kWBytes + C::kSBytes)[at] : uint16_t(0));
-                    const uint32_t i = it + (C::kLogits ? half : 0), s = i % S;   // the stage of the ring that it fills
-                    if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / S) & 1u) ^ 1u, abort_flag, p.status))) { ok = false; break; }
+                    const uint32_t i = it + (C::kLogits ? half : 0), s = i % SB;   // the stage of the ring that it fills
+                    if (!__all_sync(0xffffffffu, mbar_wait(&bempty[s], ((i / SB) & 1u) ^ 1u, abort_flag, p.status))) { ok = false; break; }
                     // kLogits: 128 rows of 64 columns; kVocabDx: two halves of 64 rows
-                    const uint32_t dst = smem_u32(smem + s * C::kStageBytes + kOperandBytes) + (C::kLogits ? 0 : half * 8192) + row * 128;
+                    const uint32_t dst = smem_u32(smem + C::kBOff + s * C::kBStageBytes) + (C::kLogits ? 0 : half * 8192) + row * 128;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         uint32_t hi[4], lo[4];
@@ -634,6 +651,7 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
     CUtensorMap ma, mb, ms, mz, mo;
     bool ok = true;
     uint64_t rows = M;
+    const uint32_t a_rows = M >= 128 ? 128 : (static_cast<uint32_t>(M) + 7) / 8 * 8;
     void* g = v.ws + l.g;
     if (MODE == kVocabDw) {
         ok = ok && make_map_2d(&ma, half, 2, g, ld, M, ld * 2, 64, 64, sw);
@@ -642,8 +660,8 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
         ok = ok && make_map_2d(&mo, half, 2, static_cast<uint8_t*>(q.dW) + static_cast<size_t>(v.v0) * K * 2, K, rows, K * 2, 64, 32, sw);
     } else {
         const void* x = BITS == kDense ? q.X : v.ws + l.xh;
-        ok = ok && (C::kLogits ? make_map_2d(&ma, half, 2, x, K, M, K * 2, 64, 128, sw)
-                               : make_map_2d(&ma, half, 2, g, ld, M, ld * 2, 64, 128, sw));
+        ok = ok && (C::kLogits ? make_map_2d(&ma, half, 2, x, K, M, K * 2, 64, a_rows, sw)
+                               : make_map_2d(&ma, half, 2, g, ld, M, ld * 2, 64, a_rows, sw));
         if (!C::kPacked) {
             ok = ok && make_map_2d(&mb, half, 2, w.rows, K, vocab, K * 2, 64, C::kLogits ? 128 : 64, sw);
         } else {
@@ -670,6 +688,7 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
     p.M = static_cast<int>(M);
     p.vocab = static_cast<int>(vocab);
     p.v0 = static_cast<int>(v.v0);
+    p.a_rows = static_cast<int>(a_rows);
     if (C::kPacked) {
         p.groups = 128 / w.group_size;
         p.wtx = static_cast<uint32_t>(C::kWBytes + (BITS == 4 ? 2 : 1) * p.groups * C::kWRows * 2);

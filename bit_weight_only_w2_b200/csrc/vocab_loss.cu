@@ -163,19 +163,20 @@ __global__ void __launch_bounds__(256) keep_labelled_kernel(const uint4* __restr
     }
 }
 
-// dX from the tiles of its sums: a block takes 32 tokens of one tile, adds the slices in order and scales.
-// Tiles as vocab_kernel<kVocabDx> writes them: [slice][column tile][token tile][CTA][warp][column / 4][lane].
+// dX from the tiles of its sums: a block takes what one warp of vocab_kernel<kVocabDx> left, 32 tokens by half a
+// tile's columns, adds the slices in order and scales.
+// Tiles as that kernel writes them: [slice][column tile][token tile][CTA][warp][column / 4][lane].
 template <bool PAIR>
 __global__ void __launch_bounds__(256) dx_out_kernel(const float4* __restrict__ acc, int slices, int m_tiles, int n_tiles, int M, int K,
                                                      const int32_t* __restrict__ labels, const float* __restrict__ grad, int vocab,
                                                      float unscale, __nv_bfloat16* __restrict__ dX) {
     grid_launch_dependents();
     grid_dependency_wait();
-    constexpr int kCtas = PAIR ? 2 : 1, kCols = PAIR ? 256 : 128, kHalf = kCols / 2;
-    const int b = blockIdx.x, quarter = b & 3, rank = (b >> 2) % kCtas, tile = (b >> 2) / kCtas;   // tile within a slice
+    constexpr int kCtas = PAIR ? 2 : 1, kCols = PAIR ? 128 : 64;
+    const int warp = blockIdx.x & 7, rank = (blockIdx.x >> 3) % kCtas, tile = (blockIdx.x >> 3) / kCtas;   // tile within a slice
     const int m = tile % m_tiles, n = tile / m_tiles;
-    const int r0 = m * (PAIR ? 256 : 128) + rank * 128 + quarter * 32;
-    if (r0 >= M) return;
+    const int r0 = m * (PAIR ? 256 : 128) + rank * 128 + (warp & 3) * 32, c0 = n * 2 * kCols + (warp >> 2) * kCols;
+    if (r0 >= M || c0 >= K) return;
     __shared__ uint2 sh[32][kCols / 4 + 1];
     const int lane = threadIdx.x & 31;
     float f = 0.f;
@@ -186,13 +187,15 @@ __global__ void __launch_bounds__(256) dx_out_kernel(const float4* __restrict__ 
             f = has ? grad[r0 + lane] * unscale : 0.f;
         }
     }
-    const size_t slice = static_cast<size_t>(m_tiles) * n_tiles * kCtas * 8 * (kHalf / 4) * 32;
-    for (int c = threadIdx.x >> 5; c < kCols / 4; c += 8) {
-        const int warp = quarter + 4 * (c / (kHalf / 4));
-        const float4* at = acc + ((static_cast<size_t>(tile) * kCtas + rank) * 8 + warp) * (kHalf / 4) * 32 + (c % (kHalf / 4)) * 32 + lane;
-        float4 s = at[0];
-        for (int i = 1; i < slices; ++i) {
-            const float4 v = at[i * slice];
+    const size_t slice = static_cast<size_t>(m_tiles) * n_tiles * kCtas * 8 * (kCols / 4) * 32;
+    const float4* at = acc + static_cast<size_t>(blockIdx.x) * (kCols / 4) * 32 + lane;
+#pragma unroll
+    for (int i = 0; i < kCols / 32; ++i) {
+        const int c = (threadIdx.x >> 5) + 8 * i;
+        float4 s = at[c * 32];
+#pragma unroll 8
+        for (int k = 1; k < slices; ++k) {
+            const float4 v = at[k * slice + c * 32];
             s.x += v.x;
             s.y += v.y;
             s.z += v.z;
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(256) dx_out_kernel(const float4* __restrict__ 
     __syncthreads();
     // (K is a multiple of 8: whole 16-byte stores)
     for (int i = threadIdx.x; i < 32 * (kCols / 8); i += 256) {
-        const int r = i / (kCols / 8), c = i % (kCols / 8), col = n * kCols + 8 * c;
+        const int r = i / (kCols / 8), c = i % (kCols / 8), col = c0 + 8 * c;
         if (r0 + r < M && col < K) {
             const uint2 a = sh[r][2 * c], d = sh[r][2 * c + 1];
             *reinterpret_cast<uint4*>(dX + static_cast<size_t>(r0 + r) * K + col) = make_uint4(a.x, a.y, d.x, d.y);
@@ -372,7 +375,7 @@ lowbit_status loss_backward(const LossProblem& p, const LossLayout& l, uint8_t* 
         }
         if (p.dW && (st = product(kVocabDw, true, p, l, ws, v0, cols, true, stream)) != LOWBIT_OK) return st;
     }
-    const int64_t blocks = l.m_tiles * l.dx_tiles * (l.pair ? 2 : 1) * 4;
+    const int64_t blocks = l.m_tiles * l.dx_tiles * (l.pair ? 2 : 1) * 8;
     const float unscale = p.table.bits == kDense ? 1.f : 1.f / 32768.f;
     return launch_after(l.pair ? dx_out_kernel<true> : dx_out_kernel<false>, blocks, 256, stream,
                         reinterpret_cast<const float4*>(ws + l.acc), slices, static_cast<int>(l.m_tiles), static_cast<int>(l.dx_tiles),
