@@ -373,8 +373,11 @@ class _Marshalled:
         size = self._address("adapter_workspace_size")
         for name in ("adapter_gemm", "gemm_dx", "adapter_backward"):
             self._set(_marshal, name, size)
-        for name in ("checkpoint_store", "checkpoint_load"):
+        for name in ("checkpoint_store", "checkpoint_load", "embedding"):
             self._set(_marshal, name)
+        self._set(_marshal, "embedding_backward", self._address("embedding_workspace_size"))
+        for name in ("cross_entropy", "cross_entropy_backward"):
+            self._set(_marshal, name, self._address("cross_entropy_workspace_size"))
 
     def _address(self, name: str) -> int:
         return ctypes.cast(getattr(self.lib, "lowbit_" + name), ctypes.c_void_p).value
@@ -756,6 +759,11 @@ def cross_entropy(x: torch.Tensor, labels: torch.Tensor, weight: torch.Tensor, s
     x bf16 [M][K]; labels int32 [M], a label outside 0 .. vocab-1 (-100, say) having no loss; the table W is
     bf16 (bits=16) or packed; vocab: the rows that take part (default: all; rows behind them fill a packed
     table up). Records no autograd graph: call cross_entropy_backward with the lse."""
+    r = _calls().cross_entropy(x, labels, weight, scales, zeros, bits, group_size, vocab, loss, lse, ws)
+    if r is not None:
+        if type(r) is int:
+            raise LowbitError(r, "lowbit_cross_entropy")
+        return r
     M, N, K, vocab = _loss_args(x, labels, weight, scales, zeros, bits, group_size, vocab)
     dev = x.get_device()
     if loss is None:
@@ -781,6 +789,11 @@ def cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, labels: torch.Te
                            dw: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
     """(dx bf16 [M][K], dw bf16 [N][K] or None), the gradients of cross_entropy for grad fp32 [M], the gradient of
     each token's loss (1 / number of tokens for their mean). dw: a bf16 table's, with need_dw; a packed one is frozen."""
+    r = _calls().cross_entropy_backward(grad, x, labels, lse, weight, scales, zeros, bits, group_size, vocab, need_dw, dx, dw, ws)
+    if r is not None:
+        if type(r) is int:
+            raise LowbitError(r, "lowbit_cross_entropy_backward")
+        return r
     M, N, K, vocab = _loss_args(x, labels, weight, scales, zeros, bits, group_size, vocab)
     _check_like(grad, "grad", (M,), _F32, x.device)
     _check_like(lse, "lse", (M,), _F32, x.device)
@@ -810,6 +823,11 @@ def embedding(tokens: torch.Tensor, weight: torch.Tensor, scales: Optional[torch
               zeros: Optional[torch.Tensor] = None, bits: int = 16, group_size: int = 0, multiplier: float = 1.0,
               out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """multiplier * the table's rows of tokens int32 [T]: bf16 [T][K], zeros for a token outside the table."""
+    r = _calls().embedding(tokens, weight, scales, zeros, bits, group_size, multiplier, out)
+    if r is not None:
+        if type(r) is int:
+            raise LowbitError(r, "lowbit_embedding")
+        return r
     N, K = _table_shape(weight, scales, zeros, bits, group_size)
     _need(tokens, _I32, "tokens", ndim=1)
     T = tokens.shape[0]
@@ -831,6 +849,11 @@ def embedding_backward(tokens: torch.Tensor, dy: torch.Tensor, rows: int, first:
                        out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient of rows first .. first + rows - 1 of a table, bf16 [rows][K], for dy bf16 [T][K] of the
     embeddings of tokens int32 [T]. Rows without tokens are zeros; a row's sum is fp32, in the tokens' order."""
+    r = _calls().embedding_backward(tokens, dy, rows, first, multiplier, out, ws)
+    if r is not None:
+        if type(r) is int:
+            raise LowbitError(r, "lowbit_embedding_backward")
+        return r
     _need(dy, _BF16, "dy")
     T, K = dy.shape
     _check_like(tokens, "tokens", (T,), _I32, dy.device)

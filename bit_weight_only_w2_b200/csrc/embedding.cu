@@ -6,13 +6,16 @@
 // which as many lanes read together.
 //
 // Gradient: dE[v] = multiplier * the sum of dy[t] over the tokens t of v, in the tokens' order, whatever the timing:
-//   1. the tokens are sorted by row (stable radix sort): up to kSortMost tokens in one CTA, whose launch's other CTAs
-//      meanwhile fill dE with zeros (that is most of the time where dE is a whole table); more tokens take a launch for
-//      the counts, one for their sums and one for the moves of each digit;
+//   1. the tokens are sorted by row (stable radix sort, digits of up to 9 bits): up to kSortMost tokens in one CTA,
+//      more in tiles of kTile, with a launch for the digits' counts and one for the moves of each digit, and one for the
+//      counts' sums between them where there are more than kFewTiles tiles (32768 tokens in one CTA took 140 us, in tiles TODO);
 //   2. a CTA adds up kRun tokens of the sorted list for 1024 columns, in fp32: a row whose tokens all lie in the run is
-//      stored at once; the parts of rows that go over a run's ends are kept in fp32
-//   3. and joined, run by run, by the CTA of the run that such a row begins in.
-// Runs of equal length bound the work of a CTA however often a token repeats.
+//      stored at once; the parts of rows that go over a run's ends are kept in fp32. Other CTAs of the launch fill the
+//      rows without tokens with zeros, which is what bounds the whole where dE is a whole table (writes alone run at
+//      3.9 TB/s here, 131072 x 2560 take 172 us);
+//   3. the parts are joined in order by the CTA of the run that such a row begins in, beside the rest of the zeros.
+// Runs of equal length bound the work of a CTA however often a token repeats. Few rows (tokens added to a frozen table)
+// take one launch: a CTA picks a row's tokens out of the list itself.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -160,11 +163,9 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const void* __restr
 // Gradient: the sort. Keys are rows of dE (tokens outside them: `rows`, which puts them last).
 // ---------------------------------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWarps = 32;
-constexpr int kSortItems = 32;                           // per thread, at most
+constexpr int kSortItems = 2;                            // per thread, at most
 constexpr int kSortMost = kSortThreads * kSortItems;     // tokens of one CTA
-constexpr int kMaxDigits = 256;
-// keys and positions of the tokens, each warp's counts of the digits, the digits' starts
-constexpr size_t kSortSmem = kSortMost * 4 + kSortMost * 2 + kSortWarps * kMaxDigits * 2 + kMaxDigits * 4 + 256;
+constexpr int kDigitBits = 9, kMaxDigits = 1 << kDigitBits;
 
 struct SortPlan {
     int passes, bits;   // digits of `bits` bits
@@ -172,7 +173,7 @@ struct SortPlan {
 SortPlan sort_plan(int64_t rows) {   // keys 0 .. rows
     int bits = 1;
     while ((int64_t(1) << bits) <= rows) ++bits;
-    const int passes = (bits + 7) / 8;
+    const int passes = (bits + kDigitBits - 1) / kDigitBits;
     return SortPlan{passes, (bits + passes - 1) / passes};
 }
 
@@ -200,7 +201,7 @@ __device__ void sort_in_cta(const int32_t* tokens, int T, int64_t first, int64_t
     uint16_t* pos = reinterpret_cast<uint16_t*>(keys + kSortThreads * ITEMS);
     uint16_t* count = pos + kSortThreads * ITEMS;               // [warp][digit]
     uint32_t* start = reinterpret_cast<uint32_t*>(count + kSortWarps * kMaxDigits);   // [digit]
-    uint32_t* sums = start + kMaxDigits;                        // [8]
+    uint32_t* sums = start + kMaxDigits;                        // [kMaxDigits / 32]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t below = (1u << lane) - 1u;
     const int base = warp * 32 * ITEMS + lane;
@@ -279,38 +280,26 @@ __device__ void sort_in_cta(const int32_t* tokens, int T, int64_t first, int64_t
     }
 }
 
-__device__ __forceinline__ void fill_zeros(uint4* out, int64_t count, int64_t block, int64_t blocks) {
-    for (int64_t i = block * blockDim.x + threadIdx.x; i < count; i += blocks * blockDim.x) out[i] = make_uint4(0, 0, 0, 0);
-}
-
-// CTA 0 sorts, the others fill dE (count 16-byte pieces) with zeros; a grid of one does both.
 template <int ITEMS>
 __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const int32_t* __restrict__ tokens, int T, int64_t first, int64_t rows,
-                                                                  SortPlan plan, uint32_t* __restrict__ keys, uint32_t* __restrict__ pos,
-                                                                  uint4* __restrict__ out, int64_t count) {
+                                                                  SortPlan plan, uint32_t* __restrict__ keys, uint32_t* __restrict__ pos) {
     extern __shared__ __align__(16) uint8_t smem[];
     grid_launch_dependents();
     grid_dependency_wait();
-    if (gridDim.x == 1) fill_zeros(out, count, 0, 1);
-    else if (blockIdx.x > 0) fill_zeros(out, count, blockIdx.x - 1, gridDim.x - 1);
-    if (blockIdx.x == 0) sort_in_cta<ITEMS>(tokens, T, first, rows, plan, keys, pos, smem);
+    sort_in_cta<ITEMS>(tokens, T, first, rows, plan, keys, pos, smem);
 }
 
 // More tokens: tiles of kTile tokens. count: the digits' counts of each tile, [digit][tile].
-constexpr int kTileItems = 8, kTile = kSortThreads * kTileItems;
+constexpr int kTileItems = 2, kTile = kSortThreads * kTileItems;
+constexpr int kFewTiles = 64;
 
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int32_t* __restrict__ tokens, const uint32_t* __restrict__ keys,
                                                                   int64_t T, int64_t first, int64_t rows, int shift, int bits,
-                                                                  uint32_t* __restrict__ counts, int tiles, uint4* __restrict__ out,
-                                                                  int64_t zeros) {
+                                                                  uint32_t* __restrict__ counts, int tiles) {
     grid_launch_dependents();
     grid_dependency_wait();
-    if (static_cast<int>(blockIdx.x) >= tiles) {
-        fill_zeros(out, zeros, blockIdx.x - tiles, gridDim.x - tiles);
-        return;
-    }
     __shared__ uint32_t hist[kMaxDigits];
-    if (threadIdx.x < kMaxDigits) hist[threadIdx.x] = 0;
+    for (int d = threadIdx.x; d < kMaxDigits; d += kSortThreads) hist[d] = 0;
     __syncthreads();
     const int64_t base = int64_t(blockIdx.x) * kTile;
     for (int i = threadIdx.x; i < kTile; i += kSortThreads)
@@ -363,7 +352,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_scan_kernel(uint32_t* __res
 
 __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const int32_t* __restrict__ tokens, const uint32_t* __restrict__ keys,
                                                                  const uint32_t* __restrict__ pos, int64_t T, int64_t first, int64_t rows,
-                                                                 int shift, int bits, const uint32_t* __restrict__ starts, int tiles,
+                                                                 int shift, int bits, const uint32_t* __restrict__ counts, int tiles,
                                                                  uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out) {
     grid_launch_dependents();
     grid_dependency_wait();
@@ -392,7 +381,33 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const int32_t* 
         if (t < T && (peers & below) == 0) mine[d] = static_cast<uint16_t>(before + __popc(peers));
         __syncwarp();
     }
+    // The tile's starts: from sort_scan_kernel, or where the tiles are few summed up here, a digit a thread.
+    __shared__ uint32_t start[kMaxDigits];
+    __shared__ uint32_t sums[kMaxDigits / 32];
+    if (tiles <= kFewTiles && threadIdx.x < kMaxDigits) {
+        uint32_t total = 0, mine_before = 0;
+        if (static_cast<int>(threadIdx.x) < 1 << bits) {
+#pragma unroll 8
+            for (int t = 0; t < tiles; ++t) {
+                if (t == static_cast<int>(blockIdx.x)) mine_before = total;
+                total += counts[int64_t(threadIdx.x) * tiles + t];
+            }
+        }
+        uint32_t incl = total;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sums[warp] = incl;
+        start[threadIdx.x] = incl - total + mine_before;
+    }
     __syncthreads();
+    if (tiles <= kFewTiles && threadIdx.x < kMaxDigits) {
+        uint32_t before = 0;
+        for (int w = 0; w < warp; ++w) before += sums[w];
+        start[threadIdx.x] += before;
+    }
     for (int d = threadIdx.x; d < 1 << bits; d += kSortThreads) {
         uint32_t total = 0;
         for (int w = 0; w < kSortWarps; ++w) {
@@ -407,7 +422,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const int32_t* 
         const int64_t t = base + 32 * i;
         if (t < T) {
             const uint32_t d = (key[i] >> shift) & ((1u << bits) - 1);
-            const int64_t to = int64_t(starts[int64_t(d) * tiles + blockIdx.x]) + count[warp * kMaxDigits + d] + rank[i];
+            const int64_t to = int64_t(tiles <= kFewTiles ? start[d] : counts[int64_t(d) * tiles + blockIdx.x]) + count[warp * kMaxDigits + d] + rank[i];
             keys_out[to] = key[i];
             pos_out[to] = at[i];
         }
@@ -419,6 +434,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const int32_t* 
 // ---------------------------------------------------------------------------------------------
 constexpr int kRun = 32;            // sorted tokens per CTA
 constexpr int kSumThreads = 128;    // 8 columns each
+constexpr int kFillRows = 32;
 
 struct Sum {
     float v[8];
@@ -436,13 +452,35 @@ struct Sum {
     }
 };
 
+// Zeros for the rows without tokens among row0 .. row1 - 1, kFillRows of them for CTA `i`: each lane of every warp looks
+// for one row in the sorted list (32768 tokens: 15 reads from L2, hidden behind the other CTAs' stores).
+__device__ __forceinline__ void fill_rows(uint4* __restrict__ out, const uint32_t* __restrict__ keys, int64_t T, int K8, int64_t i,
+                                          int64_t row0, int64_t row1) {
+    const int64_t r0 = row0 + i * kFillRows, mine = r0 + (threadIdx.x & 31);
+    int64_t lo = 0, hi = T;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (keys[mid] < mine) lo = mid + 1;
+        else hi = mid;
+    }
+    const uint32_t present = __ballot_sync(0xffffffffu, lo < T && keys[lo] == mine);
+    const int n = static_cast<int>(row1 - r0 < kFillRows ? row1 - r0 : kFillRows);
+    for (int r = 0; r < n; ++r) {
+        if ((present >> r) & 1u) continue;
+        uint4* to = out + (r0 + r) * K8;
+        for (int c = threadIdx.x; c < K8; c += blockDim.x) to[c] = make_uint4(0, 0, 0, 0);
+    }
+}
+
 // parts [2][runs][K]: a run's part of a row that began in an earlier run, and of one that it begins and does not end.
 __global__ void __launch_bounds__(kSumThreads) sum_runs_kernel(const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos, int64_t T,
                                                                uint32_t rows, const uint4* __restrict__ dy, int K8, float multiplier,
-                                                               uint4* __restrict__ out, float4* __restrict__ parts, int64_t runs) {
+                                                               uint4* __restrict__ out, float4* __restrict__ parts, int64_t runs,
+                                                               int64_t filled) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int64_t run = blockIdx.x, i0 = run * kRun;
+    if (run >= runs) return fill_rows(out, keys, T, K8, (run - runs) * gridDim.y + blockIdx.y, 0, filled);
     const int n = static_cast<int>(T - i0 < kRun ? T - i0 : kRun);
     const int lane = threadIdx.x & 31;
     // every warp holds the run's keys and positions, one a lane
@@ -489,37 +527,92 @@ __global__ void __launch_bounds__(kSumThreads) sum_runs_kernel(const uint32_t* _
     }
 }
 
-__global__ void __launch_bounds__(kSumThreads) join_runs_kernel(const uint32_t* __restrict__ keys, int64_t T, uint32_t rows, int K8,
-                                                                float multiplier, const float4* __restrict__ parts, int64_t runs,
-                                                                uint4* __restrict__ out) {
+// 256 columns a CTA, eight warps that each add an eighth of the row's parts, joined in order.
+constexpr int kJoinWarps = 8;
+__device__ __forceinline__ bool join_warps(Sum& s, float (&sh)[kJoinWarps][32][9]) {   // true for warp 0: s is the sum
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sh[warp][lane][i] = s.v[i];
+    __syncthreads();
+    if (warp > 0) return false;
+    for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s.v[i] += sh[w][lane][i];
+    return true;
+}
+
+__global__ void __launch_bounds__(32 * kJoinWarps) join_runs_kernel(const uint32_t* __restrict__ keys, int64_t T, uint32_t rows, int K8,
+                                                                    float multiplier, const float4* __restrict__ parts, int64_t runs,
+                                                                    uint4* __restrict__ out, int64_t filled) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int64_t run = blockIdx.x, end = (run + 1) * kRun;
+    if (run >= runs) return fill_rows(out, keys, T, K8, (run - runs) * gridDim.y + blockIdx.y, filled, rows);
     if (end >= T) return;                                  // the last run's rows end in it
     const uint32_t k = keys[end - 1];
     if (k >= rows || keys[end] != k) return;               // no row goes over this run's end
     if (keys[run * kRun] == k && run > 0 && keys[run * kRun - 1] == k) return;   // it began in an earlier run
-    const int c = blockIdx.y * kSumThreads + threadIdx.x;
-    if (c >= K8) return;
-    // the last run with tokens of the row: keys ascend, so the runs that begin with k are neighbours
+    // the last run with tokens of the row: keys ascend, so the runs that begin with k are neighbours; 32 probes at a time
     int64_t lo = run + 1, hi = runs - 1;
     while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) / 2;
-        if (keys[mid * kRun] == k) lo = mid;
-        else hi = mid - 1;
+        const int64_t step = (hi - lo + 31) / 32, probe = lo + step * (1 + (threadIdx.x & 31));
+        const int in = __popc(__ballot_sync(0xffffffffu, probe <= hi && keys[probe * kRun] == k));
+        lo += step * in;
+        hi = min(hi, lo + step - 1);
     }
+    __shared__ float sh[kJoinWarps][32][9];
+    const int warp = threadIdx.x >> 5, c = blockIdx.y * 32 + (threadIdx.x & 31);
+    const int64_t count = lo - run + 1, per = (count + kJoinWarps - 1) / kJoinWarps;
     Sum s;
-    auto add = [&](int64_t at) {
-        const float4 a = parts[at * (2 * int64_t(K8)) + 2 * c], b = parts[at * (2 * int64_t(K8)) + 2 * c + 1];
-        s.v[0] += a.x; s.v[1] += a.y; s.v[2] += a.z; s.v[3] += a.w;
-        s.v[4] += b.x; s.v[5] += b.y; s.v[6] += b.z; s.v[7] += b.w;
-    };
     s.zero();
-    add(runs + run);
+    if (c < K8) {
 #pragma unroll 4
-    for (int64_t r = run + 1; r <= lo; ++r) add(r);
-    out[int64_t(k) * K8 + c] = s.rounded(multiplier);
+        for (int64_t r = run + warp * per; r < run + min(count, (warp + 1) * per); ++r) {
+            const float4* from = parts + ((r == run ? runs : 0) + r) * (2 * int64_t(K8)) + 2 * c;
+            const float4 a = from[0], b = from[1];
+            s.v[0] += a.x; s.v[1] += a.y; s.v[2] += a.z; s.v[3] += a.w;
+            s.v[4] += b.x; s.v[5] += b.y; s.v[6] += b.z; s.v[7] += b.w;
+        }
+    }
+    if (join_warps(s, sh) && c < K8) out[int64_t(k) * K8 + c] = s.rounded(multiplier);
 }
+
+// Few rows: a CTA takes 256 columns of one row, finds its tokens (kept in order: each of the eight warps looks through
+// an eighth of the list and adds what it finds) and joins the warps' sums in order. T tokens read from L2 by each CTA,
+// 3 us for 1537 tokens and 24 rows of 2560 where the sort, sums and joins take 12.
+__global__ void __launch_bounds__(32 * kJoinWarps) sum_few_rows_kernel(const int32_t* __restrict__ tokens, int T, int64_t first,
+                                                                       const uint4* __restrict__ dy, int K8, float multiplier,
+                                                                       uint4* __restrict__ out) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    __shared__ float sh[kJoinWarps][32][9];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.y * 32 + lane;
+    const int64_t want = first + blockIdx.x;
+    const int per = ((T + kJoinWarps - 1) / kJoinWarps + 31) / 32 * 32, t1 = min(T, (warp + 1) * per);
+    Sum s;
+    s.zero();
+#pragma unroll 4
+    for (int t0 = warp * per; t0 < t1; t0 += 32) {
+        const int token = t0 + lane < t1 ? __ldg(tokens + t0 + lane) : -1;
+        uint32_t found = __ballot_sync(0xffffffffu, token >= 0 && token == want);
+        while (found) {   // eight tokens' loads in flight
+            uint4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int t = t0 + __ffs(found) - 1;
+                v[j] = make_uint4(0, 0, 0, 0);
+                if (found && c < K8) v[j] = __ldg(dy + int64_t(t) * K8 + c);
+                found &= found - 1;   // (0 stays 0)
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s.add(v[j]);
+        }
+    }
+    if (join_warps(s, sh) && c < K8) out[int64_t(blockIdx.x) * K8 + c] = s.rounded(multiplier);
+}
+
+// Few: as many CTAs as the GPU holds at once, each with a list it looks through in a few microseconds.
+bool few_rows(int64_t T, int64_t rows, int64_t K) { return T <= 4096 && rows * ((K + 255) / 256) <= 148 * 8; }
 
 struct GradLayout {
     int64_t runs, tiles;
@@ -528,6 +621,10 @@ struct GradLayout {
 GradLayout grad_layout(int64_t T, int64_t rows, int64_t K) {
     GradLayout l = {};
     l.runs = (T + kRun - 1) / kRun;
+    if (few_rows(T, rows, K)) {
+        l.total = 256;
+        return l;
+    }
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -549,9 +646,9 @@ GradLayout grad_layout(int64_t T, int64_t rows, int64_t K) {
 
 template <int ITEMS>
 lowbit_status sort_small(const int32_t* tokens, int64_t T, int64_t first, int64_t rows, SortPlan plan, uint32_t* keys, uint32_t* pos,
-                         void* out, int64_t zeros, cudaStream_t stream) {
+                         cudaStream_t stream) {
     constexpr size_t smem = size_t(kSortThreads) * ITEMS * 6 + kSortWarps * kMaxDigits * 2 + kMaxDigits * 4 + 256;
-    static_assert(smem <= kSortSmem && kSortSmem <= 232448, "shared memory");
+    static_assert(smem <= 232448, "shared memory");
     static std::atomic<uint64_t> devices{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
@@ -561,11 +658,8 @@ lowbit_status sort_small(const int32_t* tokens, int64_t T, int64_t first, int64_
             return LOWBIT_ERR_CUDA;
         devices.fetch_or(bit, std::memory_order_acq_rel);
     }
-    // CTAs for the zeros: one per 64 KB, up to one per SM beside the sorting one
-    int64_t fill = (zeros + 4095) / 4096;
-    if (fill > num_sms() - 1) fill = num_sms() - 1;
-    return launch_after(sort_small_kernel<ITEMS>, dim3(static_cast<unsigned>(1 + fill)), kSortThreads, smem, stream, tokens,
-                        static_cast<int>(T), first, rows, plan, keys, pos, static_cast<uint4*>(out), zeros);
+    return launch_after(sort_small_kernel<ITEMS>, dim3(1), kSortThreads, smem, stream, tokens, static_cast<int>(T), first, rows, plan, keys,
+                        pos);
 }
 
 }  // namespace
@@ -594,15 +688,15 @@ lowbit_status embedding_backward_launch(const int32_t* tokens, const void* dy, i
     uint8_t* base = static_cast<uint8_t*>(ws);
     auto at = [&](size_t o) { return reinterpret_cast<uint32_t*>(base + o); };
     const SortPlan plan = sort_plan(rows);
-    const int64_t zeros = rows * (K / 8);
     const int K8 = static_cast<int>(K / 8);
+    if (few_rows(T, rows, K))
+        return launch_after(sum_few_rows_kernel, dim3(static_cast<unsigned>(rows), (K8 + 31) / 32), 32 * kJoinWarps, 0, stream, tokens,
+                            static_cast<int>(T), first, static_cast<const uint4*>(dy), K8, multiplier, static_cast<uint4*>(out));
     uint32_t *keys = at(l.keys), *pos = at(l.pos);
     lowbit_status st = LOWBIT_OK;
     if (T <= kSortMost) {
-        const int64_t per = (T + kSortThreads - 1) / kSortThreads;
-        auto args = [&](auto f) { return f(tokens, T, first, rows, plan, keys, pos, out, zeros, stream); };
-        st = per <= 1 ? args(sort_small<1>) : per <= 2 ? args(sort_small<2>) : per <= 4 ? args(sort_small<4>)
-           : per <= 8 ? args(sort_small<8>) : per <= 16 ? args(sort_small<16>) : args(sort_small<32>);
+        st = T <= kSortThreads ? sort_small<1>(tokens, T, first, rows, plan, keys, pos, stream)
+                               : sort_small<2>(tokens, T, first, rows, plan, keys, pos, stream);
         if (st != LOWBIT_OK) return st;
     } else {
         uint32_t *k2 = at(l.keys2), *p2 = at(l.pos2), *counts = at(l.counts);
@@ -612,12 +706,13 @@ lowbit_status embedding_backward_launch(const int32_t* tokens, const void* dy, i
             uint32_t *ko = (plan.passes - pass) % 2 ? keys : k2, *po = (plan.passes - pass) % 2 ? pos : p2;
             const int32_t* tok = pass == 0 ? tokens : nullptr;
             const int shift = pass * plan.bits, tiles = static_cast<int>(l.tiles);
-            const int64_t fill = pass == 0 ? ((zeros + 4095) / 4096 < 592 ? (zeros + 4095) / 4096 : 592) : 0;
-            st = launch_after(sort_count_kernel, dim3(static_cast<unsigned>(tiles + fill)), kSortThreads, 0, stream, tok, kin, T, first, rows,
-                              shift, plan.bits, counts, tiles, static_cast<uint4*>(out), zeros);
+            st = launch_after(sort_count_kernel, dim3(static_cast<unsigned>(tiles)), kSortThreads, 0, stream, tok, kin, T, first, rows,
+                              shift, plan.bits, counts, tiles);
             if (st != LOWBIT_OK) return st;
-            st = launch_after(sort_scan_kernel, dim3(1), kSortThreads, 0, stream, counts, (int64_t(1) << plan.bits) * tiles);
-            if (st != LOWBIT_OK) return st;
+            if (tiles > kFewTiles) {
+                st = launch_after(sort_scan_kernel, dim3(1), kSortThreads, 0, stream, counts, (int64_t(1) << plan.bits) * tiles);
+                if (st != LOWBIT_OK) return st;
+            }
             st = launch_after(sort_move_kernel, dim3(static_cast<unsigned>(tiles)), kSortThreads, 0, stream, tok, kin, pin, T, first, rows, shift,
                               plan.bits, counts, tiles, ko, po);
             if (st != LOWBIT_OK) return st;
@@ -625,13 +720,18 @@ lowbit_status embedding_backward_launch(const int32_t* tokens, const void* dy, i
             pin = po;
         }
     }
-    const dim3 grid(static_cast<unsigned>(l.runs), (K8 + kSumThreads - 1) / kSumThreads);
+    const unsigned slabs = (K8 + kSumThreads - 1) / kSumThreads;
+    // Three fifths of the zeros beside the sums, which read as much as a fifth of them, the others beside the joins.
+    const int64_t filled = rows * 3 / 5;
+    auto fillers = [](int64_t n, int64_t y) { return (n + kFillRows * y - 1) / (kFillRows * y); };
     float4* parts = reinterpret_cast<float4*>(base + l.parts);
-    st = launch_after(sum_runs_kernel, grid, kSumThreads, 0, stream, keys, pos, T, static_cast<uint32_t>(rows),
-                      static_cast<const uint4*>(dy), K8, multiplier, static_cast<uint4*>(out), parts, l.runs);
+    uint4* dE = static_cast<uint4*>(out);
+    st = launch_after(sum_runs_kernel, dim3(static_cast<unsigned>(l.runs + fillers(filled, slabs)), slabs), kSumThreads, 0, stream, keys, pos, T,
+                      static_cast<uint32_t>(rows), static_cast<const uint4*>(dy), K8, multiplier, dE, parts, l.runs, filled);
     if (st != LOWBIT_OK) return st;
-    return launch_after(join_runs_kernel, grid, kSumThreads, 0, stream, keys, T, static_cast<uint32_t>(rows), K8, multiplier, parts, l.runs,
-                        static_cast<uint4*>(out));
+    const unsigned strips = (K8 + 31) / 32;
+    return launch_after(join_runs_kernel, dim3(static_cast<unsigned>(l.runs + fillers(rows - filled, strips)), strips), 32 * kJoinWarps, 0,
+                        stream, keys, T, static_cast<uint32_t>(rows), K8, multiplier, parts, l.runs, dE, filled);
 }
 
 }  // namespace lowbit

@@ -1,5 +1,5 @@
 // Argument marshalling of the Python binding's short calls, compiled: the checks, allocations and the
-// call into liblowbit.so of adapter_gemm, adapter_backward, gemm_dx and the 8-bit copies. A call's host
+// call into liblowbit.so of adapter_gemm, adapter_backward, gemm_dx, the 8-bit copies and the vocabulary calls. A call's host
 // time with it and in Python: 10.2 and 19.0 us for one token (6 us on the GPU), 17.2 and 30.7 for the
 // backward of 77 tokens, 5.6 and 10.9 for the 8-bit copy of 77 x 2560 values.
 //
@@ -303,9 +303,192 @@ PyObject* checkpoint_load(PyObject*, PyObject* const* v, Py_ssize_t n) {
     });
 }
 
+// ---- a vocabulary ----
+// A table [N][K]: weight bf16 (bits 16), or words with scales (and zeros).
+struct Table {
+    Tensor weight;
+    int64_t N, K;
+    int bits, group;
+    at::Device dev;
+    Tensor scales, zeros;
+    const void *s = nullptr, *z = nullptr;
+    Table(PyObject* w_, PyObject* s_, PyObject* z_, PyObject* b_, PyObject* g_)
+        : weight(tensor(w_)), bits(Linear::between(b_, 1, 16)), group(Linear::between(g_, 0, 1 << 20)), dev(weight.device()) {
+        need(weight.is_cuda() && weight.dim() == 2);
+        if (bits == 16) {
+            need(s_ == Py_None && z_ == Py_None);
+            fits(weight, kBf16, weight.sizes(), dev);
+            N = weight.size(0);
+            K = weight.size(1);
+            return;
+        }
+        need((bits == 1 || bits == 2 || bits == 4) && group > 0);
+        fits(weight, kI32, weight.sizes(), dev);
+        N = weight.size(0);
+        K = weight.size(1) * 32 / bits;
+        need(K % group == 0 && s_ != Py_None);
+        scales = tensor(s_);
+        fits(scales, kF16, {K / group, N}, dev);
+        s = ptr(scales);
+        if (z_ != Py_None) {
+            zeros = tensor(z_);
+            fits(zeros, kF16, {K / group, N}, dev);
+            z = ptr(zeros);
+        }
+    }
+};
+double number(PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        throw Unfit{};
+    }
+    return v;
+}
+int64_t rows_of(PyObject* vocab, const Table& t) {
+    const int64_t v = vocab == Py_None ? t.N : integer(vocab);
+    need(v >= 1 && v <= t.N);
+    return v;
+}
+// A workspace given, or allocated on the current stream.
+struct Bytes {
+    Tensor t;
+    size_t bytes;
+    template <class F>
+    Bytes(PyObject* given, const Tensor& like, F size) {
+        if (given != Py_None) {
+            t = tensor(given);
+            need(t.dim() == 1);
+            fits(t, kU8, t.sizes(), like.device());
+            bytes = static_cast<size_t>(t.numel());
+            return;
+        }
+        bytes = size();
+        t = at::empty({static_cast<int64_t>(bytes) + 1}, like.options().dtype(kU8));
+    }
+};
+Tensor fp32_output(PyObject* o, int64_t M, const Tensor& like) {
+    if (o == Py_None) return at::empty({M}, like.options().dtype(kF32));
+    const Tensor& t = tensor(o);
+    fits(t, kF32, {M}, like.device());
+    return t;
+}
+const int32_t* ints(const Tensor& t) { return static_cast<const int32_t*>(ptr(t)); }
+PyObject* two(PyObject* a, PyObject* b) {
+    PyObject* r = PyTuple_New(2);
+    PyTuple_SET_ITEM(r, 0, a);
+    PyTuple_SET_ITEM(r, 1, b);
+    return r;
+}
+
+// (fn, tokens, weight, scales, zeros, bits, group, multiplier, out)
+PyObject* embedding(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject* {
+        const Table t(v[2], v[3], v[4], v[5], v[6]);
+        const Tensor& tokens = tensor(v[1]);
+        need(tokens.dim() == 1);
+        const int64_t T = tokens.size(0);
+        fits(tokens, kI32, {T}, t.dev);
+        const float multiplier = static_cast<float>(number(v[7]));
+        const c10::cuda::CUDAGuard guard(t.dev);
+        Tensor out;
+        if (v[8] == Py_None) {
+            out = at::empty({T, t.K}, t.weight.options().dtype(kBf16));
+        } else {
+            out = tensor(v[8]);
+            fits(out, kBf16, {T, t.K}, t.dev);
+        }
+        const auto fn = function<decltype(&lowbit_embedding)>(v[0]);
+        const lowbit_status st = without_gil([&] {
+            return fn(T, t.N, t.K, t.bits, t.group, ints(tokens), ptr(t.weight), t.s, t.z, multiplier, ptr(out), stream_of(t.dev));
+        });
+        return st == LOWBIT_OK ? THPVariable_Wrap(out) : status(st);
+    });
+}
+
+// (fn, size_fn, tokens, dy, rows, first, multiplier, out, ws)
+PyObject* embedding_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject* {
+        const Tensor &tokens = tensor(v[2]), &dy = tensor(v[3]);
+        need(dy.is_cuda() && dy.dim() == 2);
+        const int64_t T = dy.size(0), K = dy.size(1), rows = integer(v[4]), first = integer(v[5]);
+        fits(dy, kBf16, {T, K}, dy.device());
+        fits(tokens, kI32, {T}, dy.device());
+        need(rows >= 0 && first >= 0);
+        const float multiplier = static_cast<float>(number(v[6]));
+        const c10::cuda::CUDAGuard guard(dy.device());
+        const Tensor out = output(v[7], {rows, K}, dy);
+        const Bytes ws(v[8], dy, [&] { return function<decltype(&lowbit_embedding_workspace_size)>(v[1])(T, rows, K); });
+        const auto fn = function<decltype(&lowbit_embedding_backward)>(v[0]);
+        const lowbit_status st = without_gil([&] {
+            return fn(T, K, first, rows, ints(tokens), ptr(dy), multiplier, ptr(out), ptr(ws.t), ws.bytes, stream_of(dy.device()));
+        });
+        return st == LOWBIT_OK ? THPVariable_Wrap(out) : status(st);
+    });
+}
+
+// (fn, size_fn, x, labels, weight, scales, zeros, bits, group, vocab, loss, lse, ws)
+PyObject* cross_entropy(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded(n, 13, [&]() -> PyObject* {
+        const Table t(v[4], v[5], v[6], v[7], v[8]);
+        const Tensor &x = tensor(v[2]), &labels = tensor(v[3]);
+        need(x.dim() == 2);
+        const int64_t M = x.size(0), vocab = rows_of(v[9], t);
+        fits(x, kBf16, {M, t.K}, t.dev);
+        fits(labels, kI32, {M}, t.dev);
+        const c10::cuda::CUDAGuard guard(t.dev);
+        const Tensor loss = fp32_output(v[10], M, x), lse = fp32_output(v[11], M, x);
+        const Bytes ws(v[12], x, [&] {
+            return function<decltype(&lowbit_cross_entropy_workspace_size)>(v[1])(M, vocab, t.K, t.bits, 0);
+        });
+        const auto fn = function<decltype(&lowbit_cross_entropy)>(v[0]);
+        const lowbit_status st = without_gil([&] {
+            return fn(M, vocab, t.N, t.K, t.bits, t.group, ptr(x), ptr(t.weight), t.s, t.z, ints(labels), static_cast<float*>(ptr(loss)),
+                      static_cast<float*>(ptr(lse)), ptr(ws.t), ws.bytes, stream_of(t.dev));
+        });
+        return st == LOWBIT_OK ? two(THPVariable_Wrap(loss), THPVariable_Wrap(lse)) : status(st);
+    });
+}
+
+// (fn, size_fn, grad, x, labels, lse, weight, scales, zeros, bits, group, vocab, need_dw, dx, dw, ws)
+PyObject* cross_entropy_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded(n, 16, [&]() -> PyObject* {
+        const Table t(v[6], v[7], v[8], v[9], v[10]);
+        const Tensor &grad = tensor(v[2]), &x = tensor(v[3]), &labels = tensor(v[4]), &lse = tensor(v[5]);
+        need(x.dim() == 2);
+        const int64_t M = x.size(0), vocab = rows_of(v[11], t);
+        fits(x, kBf16, {M, t.K}, t.dev);
+        fits(labels, kI32, {M}, t.dev);
+        fits(grad, kF32, {M}, t.dev);
+        fits(lse, kF32, {M}, t.dev);
+        need(v[12] == Py_True || v[12] == Py_False);
+        const bool need_dw = v[12] == Py_True;
+        need(need_dw ? t.bits == 16 : v[14] == Py_None);
+        const c10::cuda::CUDAGuard guard(t.dev);
+        const Tensor dx = output(v[13], {M, t.K}, x);
+        Tensor dw;
+        if (need_dw) dw = output(v[14], {t.N, t.K}, x);
+        const Bytes ws(v[15], x, [&] {
+            return function<decltype(&lowbit_cross_entropy_workspace_size)>(v[1])(M, vocab, t.K, t.bits, need_dw ? 2 : 1);
+        });
+        const auto fn = function<decltype(&lowbit_cross_entropy_backward)>(v[0]);
+        const lowbit_status st = without_gil([&] {
+            return fn(M, vocab, t.N, t.K, t.bits, t.group, ptr(x), ptr(t.weight), t.s, t.z, ints(labels), static_cast<const float*>(ptr(lse)),
+                      static_cast<const float*>(ptr(grad)), ptr(dx), need_dw ? ptr(dw) : nullptr, ptr(ws.t), ws.bytes, stream_of(t.dev));
+        });
+        if (st != LOWBIT_OK) return status(st);
+        PyObject* second = Py_None;
+        if (need_dw) second = THPVariable_Wrap(dw);
+        else Py_INCREF(Py_None);
+        return two(THPVariable_Wrap(dx), second);
+    });
+}
+
 #define LOWBIT_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {LOWBIT_METHOD(adapter_gemm),     LOWBIT_METHOD(gemm_dx),         LOWBIT_METHOD(adapter_backward),
-                         LOWBIT_METHOD(checkpoint_store), LOWBIT_METHOD(checkpoint_load), {nullptr, nullptr, 0, nullptr}};
+                         LOWBIT_METHOD(checkpoint_store), LOWBIT_METHOD(checkpoint_load),
+                         LOWBIT_METHOD(embedding), LOWBIT_METHOD(embedding_backward), LOWBIT_METHOD(cross_entropy),
+                         LOWBIT_METHOD(cross_entropy_backward), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

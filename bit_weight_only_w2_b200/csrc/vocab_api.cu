@@ -156,7 +156,7 @@ LOWBIT_API lowbit_status lowbit_embedding_backward(int64_t T, int64_t K, int64_t
     if (rows == 0) return LOWBIT_OK;
     if (!dE || (T > 0 && (!tokens || !dY))) return LOWBIT_ERR_INVALID_ARG;
     if (!aligned(tokens, 4) || !aligned(dY, 16) || !aligned(dE, 16)) return LOWBIT_ERR_ALIGNMENT;
-    if (K % 8 != 0 || T >= kMaxSize || K >= int64_t(1) << 26 || first >= kMaxSize || rows >= kMaxSize) return LOWBIT_ERR_UNSUPPORTED;
+    if (K % 8 != 0 || T >= kMaxSize || K >= int64_t(1) << 23 || first >= kMaxSize || rows >= kMaxSize) return LOWBIT_ERR_UNSUPPORTED;
     lowbit_status st;
     if (T == 0) {   // sums over nothing
         if ((st = check_device()) != LOWBIT_OK) return st;
