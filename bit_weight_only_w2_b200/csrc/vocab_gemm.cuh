@@ -56,7 +56,7 @@ struct Cfg {
     static constexpr int kWStageBytes = (kWBytes + kSBytes + kZBytes + 1023) / 1024 * 1024;
     // Rings: one of both operands (bf16 tables), or one of the rows' operand, which comes from L2 with some 1500 clocks
     // of latency, and a shorter one of the decoded columns' (in one ring the gradient of 77 tokens against uint4 rows
-    // waited for its rows: 60 against TODO us).
+    // would wait for its rows).
     static constexpr int kAStageBytes = kPacked ? kOperandBytes : 2 * kOperandBytes;
     static constexpr int kBStageBytes = kPacked ? kTerms * kOperandBytes : 0;
     static constexpr int kWStages = kPacked ? (kTerms == 2 ? 3 : 4) : 0;
@@ -110,6 +110,14 @@ __device__ __forceinline__ float ex2(float x) {   // 2^x, within 2 ulp; 0 below 
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// True in one lane of the (converged) warp. The compiler knows it for one lane, and forms the operands of tcgen05.mma and
+// TMA instructions in uniform registers at once: behind `lane == 0` an MMA took 90 clocks to issue, which held the tensor
+// pipe at 53 % of its cycles for ternary tables (1537 tokens, gradient: 1375 us, with this 1143) and at 85 % for bf16.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t cluster_bar, void* dst, int c0, int c1) {
     asm volatile(
@@ -281,7 +289,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
 
     if (warp == 8) {
         // ------------------------------------------------------------ TMA of the rows' operand, and of a bf16 table
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t it = 0;
             bool ok = true;
             const uint32_t bytes = MODE == kVocabDw ? C::kAStageBytes : (C::kPacked ? 0 : kOperandBytes) + p.a_rows * 128;
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
         }
     } else if (warp == 9) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0 && issuer) {
+        if (issuer && elect_one()) {
             uint32_t it = 0, n = 0;
             bool ok = true, issued = false;
             for (int t = tile0; t < p.num_tiles && ok; t += tile_step, ++n) {
@@ -394,7 +402,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
     } else if (C::kPacked && warp == 10) {
         // ------------------------------------------------------------ TMA of words and scales
         if constexpr (C::kPacked) {
-            if (lane == 0) {
+            if (elect_one()) {
                 uint32_t it = 0;
                 bool ok = true;
                 for (int t = tile0; t < p.num_tiles && ok; t += tile_step) {
