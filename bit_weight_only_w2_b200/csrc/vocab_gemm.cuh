@@ -20,7 +20,7 @@
 //     of 64 codes per lane, into the swizzled layout the MMA reads;
 //   * warp 9 (one lane): tcgen05.mma, two accumulators in tensor memory;
 //   * warps 0-7: the epilogue of one tile, beside the MMAs of the next.
-// Persistent grids; tiles go through the tokens first, so that a table's rows are read from memory once.
+// Persistent grids; the logits' tiles go through the tokens first, so that a table's rows are read from memory once.
 // Operands are K-major for the logits; for the gradients the table [v][k] (dX: reduced over v), G [m][v] and X [m][k]
 // (dW: reduced over m) are read as they lie, as MN-major operands, so nothing is transposed.
 #pragma once
@@ -59,7 +59,9 @@ struct Cfg {
     // would wait for its rows).
     static constexpr int kAStageBytes = kPacked ? kOperandBytes : 2 * kOperandBytes;
     static constexpr int kBStageBytes = kPacked ? kTerms * kOperandBytes : 0;
-    static constexpr int kWStages = kPacked ? (kTerms == 2 ? 3 : 4) : 0;
+    // (kVocabDx: 12, since a stage of its ring takes a stage of words, which come from memory: with 4 the gradient of 77
+    // tokens waited for them, 37 us against KDX)
+    static constexpr int kWStages = !kPacked ? 0 : !kLogits ? 12 : kTerms == 2 ? 3 : 4;
     static constexpr int kStagingBytes = (MODE == kVocabGrad || MODE == kVocabDw) ? kEpiWarps * 4096 : 0;
     static constexpr int kRoom = kSmemLimit - 2048 - kStagingBytes - kWStages * kWStageBytes;
     static constexpr int kAStages = !kPacked ? kRoom / kAStageBytes : kTerms == 2 && kStagingBytes > 0 ? 4 : 6;
@@ -278,7 +280,10 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
         int m0, n0, j0, j1;
     };
     auto tile_of = [&](int t) {
-        const int slice = t / per_mn, mn = t - slice * per_mn, n = mn / p.m_tiles, m = mn - n * p.m_tiles;
+        const int slice = t / per_mn, mn = t - slice * per_mn;
+        // (dW: through the columns first, so that G, the larger operand, is read from memory once: a third of the time
+        // was spent on it otherwise)
+        const int n = MODE == kVocabDw ? mn % p.n_tiles : mn / p.m_tiles, m = MODE == kVocabDw ? mn / p.n_tiles : mn - n * p.m_tiles;
         Tile r;
         r.m0 = m * C::kRows + static_cast<int>(rank) * 128;
         r.n0 = n * C::kCols;

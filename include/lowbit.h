@@ -361,7 +361,7 @@ lowbit_status lowbit_checkpoint_load(const uint8_t* codes, const uint8_t* exps, 
  * or another output; a workspace belongs to one call until its work on the GPU is done. */
 
 /* Bytes of workspace of lowbit_cross_entropy (backward = 0) and lowbit_cross_entropy_backward (1, or 2 where dW is
- * wanted), for M tokens or any fewer. The backward's holds up to 128 MB of G (at least 256 columns of it) and fp32
+ * wanted), for M tokens or any fewer. The backward's holds up to 256 MB of G (at least 256 columns of it) and fp32
  * sums of dX. 0 for invalid arguments. */
 size_t lowbit_cross_entropy_workspace_size(int64_t M, int64_t vocab, int64_t K, int bits, int backward);
 
