@@ -20,7 +20,9 @@
 //   uint4    w = s * (q - z)                     -> decode 128 + q exactly, subtract s * (128 + z) * Sx
 // where Sx is the sum of the group's X entries per token (an MMA against a ones operand). Each
 // product is exact in fp32, so the only roundings are the fp32 accumulations and the final bf16
-// store; no X conversion pass is needed.
+// store; no X conversion pass is needed. What is subtracted can be a hundred times what is left, which an
+// fp32 Y would show (a token whose values have one sign: logits off by 1e-5 of |x||w|): with fp32 Y the
+// codes are t and q - 8 (one exact packed subtraction more each), and only s * (z - 8) * Sx is subtracted.
 //
 // Work decomposition. A CTA (one per SM) owns 8 * NOCT weight rows (<= 128) and one K slice; the
 // K slices of a row block run on the CTAs of a thread-block cluster and are summed in rank
@@ -195,6 +197,11 @@ __device__ __forceinline__ uint32_t dec_u4(uint32_t v, int c) {       // 128 + q
 }
 __device__ __forceinline__ uint32_t dec_t2(uint32_t v, int c) {       // 128 + f, f = t + 1
     return and_or(v >> (2 * c), 0x00030003u, 0x43004300u);
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 __device__ __forceinline__ uint32_t dec_b1(uint32_t v, int c) {       // +-1 by the code bit
     return xor_andnot(0x3F803F80u, v << (15 - c), 0x80008000u);
@@ -425,6 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return v;
     };
     // ---- the phases of one ring step, shared by both loop drivers below ----
+    constexpr bool kSums = BITS == 4 || (BITS == 2 && !F32);   // a multiple of Sx is subtracted
+    constexpr float kZeroBias = F32 ? -8.f : 128.f;            // the codes stand for q + kZeroBias
     // P1: this warp's group: fp32 (s, -s * c) of every row of its units, into `tab` (negated so
     // that the scale epilogue is two packed FMAs per pair of accumulators)
     auto build_table = [&](const uint8_t* st, float4* tab) {
@@ -432,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const __half* zh = reinterpret_cast<const __half*>(st + p.z_off) + gi * R;
         auto sc_of = [&](int r, float& sf, float& cf) {
             sf = __half2float(sh[r]);
-            cf = BITS == 4 ? -(sf * (128.f + __half2float(zh[r]))) : BITS == 2 ? -(129.f * sf) : 0.f;
+            cf = BITS == 4 ? -(sf * (kZeroBias + __half2float(zh[r]))) : kSums ? -(129.f * sf) : 0.f;
         };
         if constexpr (SWAP) {
             // entry 8u + g: rows 16u + g and 16u + g + 8 of the warp's units
@@ -458,9 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float c0 = 0.f, c1 = 0.f;
                     if (BITS == 4) {
                         const float2 zf = __half22float2(zp[i]);
-                        c0 = -(sf.x * (128.f + zf.x));
-                        c1 = -(sf.y * (128.f + zf.y));
-                    } else if (BITS == 2) {
+                        c0 = -(sf.x * (kZeroBias + zf.x));
+                        c1 = -(sf.y * (kZeroBias + zf.y));
+                    } else if (kSums) {
                         c0 = -(129.f * sf.x);
                         c1 = -(129.f * sf.y);
                     }
@@ -489,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // P3: group sums of X: tokens g (0) and g + 8 (2), or with SWAP tokens 2q (0) and 2q + 1 (1)
     auto group_sums = [&](const uint32_t (&a)[4][4], float (&tsx)[4]) {
         tsx[0] = tsx[1] = tsx[2] = tsx[3] = 0.f;
-        if (BITS != 1) {
+        if (kSums) {
             if constexpr (SWAP) {
                 const uint32_t ones[4] = {kBf16One2, kBf16One2, kBf16One2, kBf16One2};
                 mma_bf16_z(tsx, ones, a[0][0], a[0][1]);
@@ -546,6 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             b0[h] = dec_b1(wd[u][h][j >> 1], pc);
                             b1[h] = dec_b1(wd[u][h][j >> 1], pc + 4);
                         }
+                        if (F32 && BITS != 1) {    // 136 and 129, exact
+                            b0[h] = sub_bf16x2(b0[h], BITS == 4 ? 0x43084308u : 0x43014301u);
+                            b1[h] = sub_bf16x2(b1[h], BITS == 4 ? 0x43084308u : 0x43014301u);
+                        }
                     }
                     if constexpr (SWAP) {
                         // A = rows g (octet 2u) and g + 8 (octet 2u + 1) of the unit
@@ -573,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float4 sc = tab[8 * (ob + u) + g];
                     fma_f32x2(d[0], d[1], sc.x, sc.x, T[u][0], T[u][1]);
                     fma_f32x2(d[2], d[3], sc.y, sc.y, T[u][2], T[u][3]);
-                    if (BITS != 1) {
+                    if (kSums) {
                         fma_f32x2(d[0], d[1], sc.z, sc.z, tsx[0], tsx[1]);
                         fma_f32x2(d[2], d[3], sc.w, sc.w, tsx[0], tsx[1]);
                     }
@@ -582,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float4 sc = tab[4 * (ob + u) + q];
                     fma_f32x2(d[0], d[1], sc.x, sc.y, T[u][0], T[u][1]);
                     fma_f32x2(d[2], d[3], sc.x, sc.y, T[u][2], T[u][3]);
-                    if (BITS != 1) {
+                    if (kSums) {
                         fma_f32x2(d[0], d[1], sc.z, sc.w, tsx[0], tsx[0]);
                         fma_f32x2(d[2], d[3], sc.z, sc.w, tsx[2], tsx[2]);
                     }

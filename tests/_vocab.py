@@ -77,6 +77,10 @@ class Loss:
             # |z| > 8) of s, so 2^-11 of that, and 2^-25 of its smallest step
             step = table.scales.double()[:, :V].T.repeat_interleave(table.gs, 1)
             self.el = self.el + 2.0 ** -22 * s + 2.0 ** -17 * (self.x.abs() @ step.T) + 2.0 ** -25 * self.x.abs().sum(1)[:, None]
+            if len(x) <= 16:
+                # few tokens: sums of x (q - 8), less (z - 8) times a sum of x, both times s
+                q = (table.codes.double()[:V] - 8).abs() + (table.zeros.double()[:, :V].T - 8).abs().repeat_interleave(table.gs, 1)
+                self.el = self.el + K * H32 * (self.x.abs() @ (q * step).T)
         self.lse = torch.logsumexp(self.l, 1)
         self.target = self.l.gather(1, self.label[:, None])[:, 0]
         self.loss = torch.where(self.valid, self.lse - self.target, 0.0)
