@@ -84,10 +84,13 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const float2* _
 // Up to 16 tokens of a packed table: lse and loss from logits in fp32, a cluster of CTAs per token whose (maximum, sum)
 // are joined in rank order. The logits lie in L2: 131072 of one token take 3 us.
 constexpr int kRowCtas = 8, kRowThreads = 256;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __global__ void __cluster_dims__(kRowCtas, 1, 1) __launch_bounds__(kRowThreads)
     loss_rows_kernel(const float* __restrict__ logits, int64_t ld, const int32_t* __restrict__ labels, int vocab, float* __restrict__ loss,
                      float* __restrict__ lse) {
     grid_launch_dependents();
+    cluster_arrive();   // (waited for before a CTA stores into rank 0's: that one has then begun)
     grid_dependency_wait();
     const int m = blockIdx.x / kRowCtas, rank = blockIdx.x % kRowCtas, tid = threadIdx.x;
     const float* row = logits + m * ld;
@@ -138,12 +141,15 @@ __global__ void __cluster_dims__(kRowCtas, 1, 1) __launch_bounds__(kRowThreads)
         join(R, S, r, s);
     }
     if ((tid & 31) == 0) sums[tid >> 5] = make_float2(R, S);
+    __syncwarp();
+    cluster_wait();
     __syncthreads();
     if (tid == 0) {
 #pragma unroll
         for (int i = 1; i < kRowThreads / 32; ++i) join(R, S, sums[i].x, sums[i].y);
         asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(map_shared_rank(smem_u32(&of_cta[rank]), 0)), "f"(R), "f"(S) : "memory");
     }
+    __syncwarp();
     cluster_sync_all();
     if (rank == 0 && tid == 0) {
         R = of_cta[0].x;
@@ -183,14 +189,10 @@ __global__ void __launch_bounds__(256) dx_out_kernel(const float4* __restrict__ 
     if (r0 >= M || c0 >= K) return;
     __shared__ uint2 sh[32][kCols / 4 + 1];
     const int lane = threadIdx.x & 31;
-    float f = 0.f;
-    if (r0 + lane < M) {
-        f = 1.f;
-        if (unscale != 1.f) {   // packed tables: G came without the tokens' own factor
-            const bool has = static_cast<unsigned>(labels[r0 + lane]) < static_cast<unsigned>(vocab);
-            f = has ? grad[r0 + lane] * unscale : 0.f;
-        }
-    }
+    // (a token without a label has no gradient, though zeros times an infinite row are no zeros)
+    const bool has = r0 + lane < M && static_cast<unsigned>(labels[r0 + lane]) < static_cast<unsigned>(vocab);
+    float f = 1.f;
+    if (has && unscale != 1.f) f = grad[r0 + lane] * unscale;   // packed tables: G came without the tokens' own factor
     const size_t slice = static_cast<size_t>(m_tiles) * n_tiles * kCtas * 8 * (kCols / 4) * 32;
     const float4* at = acc + static_cast<size_t>(blockIdx.x) * (kCols / 4) * 32 + lane;
 #pragma unroll
@@ -205,6 +207,7 @@ __global__ void __launch_bounds__(256) dx_out_kernel(const float4* __restrict__ 
             s.z += v.z;
             s.w += v.w;
         }
+        if (!has) s = make_float4(0.f, 0.f, 0.f, 0.f);
         const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x * f, s.y * f), hi = __floats2bfloat162_rn(s.z * f, s.w * f);
         sh[lane][c] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
@@ -280,7 +283,9 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
     }
     if (!backward) {
         l.target = take(static_cast<size_t>(M) * 4);
-        l.part = take(static_cast<size_t>(2 * l.n_tiles) * M * 8);
+        // (room for the narrow tiles of 128 tokens too, so that a workspace for M tokens serves fewer)
+        const int64_t narrow = 2 * ((vocab + 127) / 128) * (M < 128 ? M : 128), parts = 2 * l.n_tiles * M;
+        l.part = take(static_cast<size_t>(parts > narrow ? parts : narrow) * 8);
         l.total = bits != kDense && at < logits ? logits : at;   // (serves the small batches too)
         return l;
     }
@@ -316,29 +321,43 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
     return l;
 }
 
-lowbit_status loss_forward(const LossProblem& all, const LossLayout& l0, uint8_t* ws, cudaStream_t stream) {
-    if (l0.small) {
-        const Table& t = all.table;
+namespace {
+
+// The forward of at most kTokensAtOnce tokens.
+lowbit_status forward_of(const LossProblem& p, const LossLayout& l, uint8_t* ws, cudaStream_t stream) {
+    if (l.small) {
+        const Table& t = p.table;
         GemmProblem g = {};
-        g.M = all.M;
-        g.N = up(all.vocab, 8);   // (at most t.N: the rows behind the vocabulary are not read)
+        g.M = p.M;
+        g.N = up(p.vocab, 8);   // (at most t.N: the rows behind the vocabulary are not read)
         g.K = t.K;
         g.bits = t.bits;
         g.group_size = t.group_size;
-        g.X = all.X;
+        g.X = p.X;
         g.Wp = static_cast<const uint32_t*>(t.rows);
         g.scales = t.scales;
         g.zeros = t.zeros;
-        g.Y = ws + l0.logits;
+        g.Y = ws + l.logits;
         // Rows per CTA: the fewest that take no more waves than the most (128), which the kernel's own choice, made for
         // linears, does not look for (112 instead of 128 for 32768: 7 % less). Short vocabularies are left to it.
         const int64_t sms = num_sms(), waves = (g.N + 128 * sms - 1) / (128 * sms), rows = up((g.N + waves * sms - 1) / (waves * sms), 16);
         const lowbit_status st =
             smallm_launch(g, g.N >= 64 * sms ? static_cast<int>(rows) : 0, g.N >= 64 * sms ? 1 : 0, g.M <= 8, stream, nullptr, true, t.N);
         if (st != LOWBIT_OK) return st;
-        return launch_after(loss_rows_kernel, g.M * kRowCtas, kRowThreads, stream, reinterpret_cast<const float*>(ws + l0.logits), g.N,
-                            all.labels, static_cast<int>(all.vocab), all.loss, all.lse_out);
+        return launch_after(loss_rows_kernel, g.M * kRowCtas, kRowThreads, stream, reinterpret_cast<const float*>(ws + l.logits), g.N,
+                            p.labels, static_cast<int>(p.vocab), p.loss, p.lse_out);
     }
+    lowbit_status st = copy_x(p, l, ws, stream);
+    if (st == LOWBIT_OK) st = product(kVocabStats, l.pair, p, l, ws, 0, p.vocab, true, stream);
+    if (st != LOWBIT_OK) return st;
+    return launch_after(p.M <= 1024 ? loss_join_kernel<1> : loss_join_kernel<8>, p.M <= 1024 ? p.M : (p.M + 7) / 8, kJoinThreads, stream,
+                        reinterpret_cast<const float2*>(ws + l.part), reinterpret_cast<const float*>(ws + l.target), p.labels,
+                        static_cast<int>(2 * l.n_tiles), static_cast<int>(p.M), static_cast<int>(p.vocab), p.loss, p.lse_out);
+}
+
+}  // namespace
+
+lowbit_status loss_forward(const LossProblem& all, const LossLayout& l0, uint8_t* ws, cudaStream_t stream) {
     for (int64_t m0 = 0; m0 < all.M; m0 += kTokensAtOnce) {
         LossProblem p = all;
         p.M = all.M - m0 < kTokensAtOnce ? all.M - m0 : kTokensAtOnce;
@@ -347,12 +366,7 @@ lowbit_status loss_forward(const LossProblem& all, const LossLayout& l0, uint8_t
         p.loss = all.loss + m0;
         p.lse_out = all.lse_out + m0;
         const LossLayout l = m0 == 0 ? l0 : loss_layout(p.M, p.vocab, p.table.K, p.table.bits, false, false);
-        lowbit_status st = copy_x(p, l, ws, stream);
-        if (st == LOWBIT_OK) st = product(kVocabStats, l.pair, p, l, ws, 0, p.vocab, true, stream);
-        if (st == LOWBIT_OK)
-            st = launch_after(p.M <= 1024 ? loss_join_kernel<1> : loss_join_kernel<8>, p.M <= 1024 ? p.M : (p.M + 7) / 8, kJoinThreads, stream,
-                              reinterpret_cast<const float2*>(ws + l.part), reinterpret_cast<const float*>(ws + l.target), p.labels,
-                              static_cast<int>(2 * l.n_tiles), static_cast<int>(p.M), static_cast<int>(p.vocab), p.loss, p.lse_out);
+        const lowbit_status st = forward_of(p, l, ws, stream);
         if (st != LOWBIT_OK) return st;
     }
     return LOWBIT_OK;
