@@ -8,14 +8,14 @@
 // Gradient: dE[v] = multiplier * the sum of dy[t] over the tokens t of v, in the tokens' order, whatever the timing:
 //   1. the tokens are sorted by row (stable radix sort, digits of up to 9 bits): up to kSortMost tokens in one CTA,
 //      more in tiles of kTile, with a launch for the digits' counts and one for the moves of each digit, and one for the
-//      counts' sums between them where there are more than kFewTiles tiles (32768 tokens in one CTA took 140 us, in tiles TODO);
+//      counts' sums between them where there are more than kFewTiles tiles (the sort of 32768 tokens in one CTA took
+//      140 us; in tiles all of the gradient of 32000 x 512 takes 35). Beside the sort dE is filled with zeros;
 //   2. a CTA adds up kRun tokens of the sorted list for 1024 columns, in fp32: a row whose tokens all lie in the run is
-//      stored at once; the parts of rows that go over a run's ends are kept in fp32. Other CTAs of the launch fill the
-//      rows without tokens with zeros, which is what bounds the whole where dE is a whole table (writes alone run at
-//      3.9 TB/s here, 131072 x 2560 take 172 us);
-//   3. the parts are joined in order by the CTA of the run that such a row begins in, beside the rest of the zeros.
-// Runs of equal length bound the work of a CTA however often a token repeats. Few rows (tokens added to a frozen table)
-// take one launch: a CTA picks a row's tokens out of the list itself.
+//      stored at once; the parts of rows that go over a run's ends are kept in fp32;
+//   3. the parts are joined in order by the CTA of the run that such a row begins in.
+// Runs of equal length bound the work of a CTA however often a token repeats. The zeros bound a whole table (131072 x
+// 2560: 115 of 180 us with 32768 tokens). Few rows (tokens added to a frozen table), or few tokens on a small table, take
+// one launch instead.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -280,12 +280,25 @@ __device__ void sort_in_cta(const int32_t* tokens, int T, int64_t first, int64_t
     }
 }
 
+// Beside the sorting CTAs of a launch the others fill a part of dE with zeros, whatever its rows hold later: a plain
+// stream of stores by neighbouring threads (131072 x 2560 in 115 us, 5.8 TB/s; row by row, only those without tokens, 172).
+struct Zeros {
+    uint4* out;
+    int64_t from, to;   // 16-byte pieces
+};
+__device__ __forceinline__ void fill(const Zeros& z, int cta, int ctas) {
+    for (int64_t i = z.from + int64_t(cta) * kSortThreads + threadIdx.x; i < z.to; i += int64_t(ctas) * kSortThreads)
+        z.out[i] = make_uint4(0, 0, 0, 0);
+}
+
 template <int ITEMS>
 __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const int32_t* __restrict__ tokens, int T, int64_t first, int64_t rows,
-                                                                  SortPlan plan, uint32_t* __restrict__ keys, uint32_t* __restrict__ pos) {
+                                                                  SortPlan plan, uint32_t* __restrict__ keys, uint32_t* __restrict__ pos,
+                                                                  Zeros zeros) {
     extern __shared__ __align__(16) uint8_t smem[];
     grid_launch_dependents();
     grid_dependency_wait();
+    if (blockIdx.x > 0) return fill(zeros, blockIdx.x - 1, gridDim.x - 1);
     sort_in_cta<ITEMS>(tokens, T, first, rows, plan, keys, pos, smem);
 }
 
@@ -295,9 +308,10 @@ constexpr int kFewTiles = 64;
 
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int32_t* __restrict__ tokens, const uint32_t* __restrict__ keys,
                                                                   int64_t T, int64_t first, int64_t rows, int shift, int bits,
-                                                                  uint32_t* __restrict__ counts, int tiles) {
+                                                                  uint32_t* __restrict__ counts, int tiles, Zeros zeros) {
     grid_launch_dependents();
     grid_dependency_wait();
+    if (static_cast<int>(blockIdx.x) >= tiles) return fill(zeros, blockIdx.x - tiles, gridDim.x - tiles);
     __shared__ uint32_t hist[kMaxDigits];
     for (int d = threadIdx.x; d < kMaxDigits; d += kSortThreads) hist[d] = 0;
     __syncthreads();
@@ -353,9 +367,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_scan_kernel(uint32_t* __res
 __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const int32_t* __restrict__ tokens, const uint32_t* __restrict__ keys,
                                                                  const uint32_t* __restrict__ pos, int64_t T, int64_t first, int64_t rows,
                                                                  int shift, int bits, const uint32_t* __restrict__ counts, int tiles,
-                                                                 uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out) {
+                                                                 uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
+                                                                 Zeros zeros) {
     grid_launch_dependents();
     grid_dependency_wait();
+    if (static_cast<int>(blockIdx.x) >= tiles) return fill(zeros, blockIdx.x - tiles, gridDim.x - tiles);
     __shared__ uint16_t count[kSortWarps * kMaxDigits];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t below = (1u << lane) - 1u;
@@ -434,7 +450,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const int32_t* 
 // ---------------------------------------------------------------------------------------------
 constexpr int kRun = 32;            // sorted tokens per CTA
 constexpr int kSumThreads = 128;    // 8 columns each
-constexpr int kFillRows = 32;
 
 struct Sum {
     float v[8];
@@ -452,35 +467,13 @@ struct Sum {
     }
 };
 
-// Zeros for the rows without tokens among row0 .. row1 - 1, kFillRows of them for CTA `i`: each lane of every warp looks
-// for one row in the sorted list (32768 tokens: 15 reads from L2, hidden behind the other CTAs' stores).
-__device__ __forceinline__ void fill_rows(uint4* __restrict__ out, const uint32_t* __restrict__ keys, int64_t T, int K8, int64_t i,
-                                          int64_t row0, int64_t row1) {
-    const int64_t r0 = row0 + i * kFillRows, mine = r0 + (threadIdx.x & 31);
-    int64_t lo = 0, hi = T;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (keys[mid] < mine) lo = mid + 1;
-        else hi = mid;
-    }
-    const uint32_t present = __ballot_sync(0xffffffffu, lo < T && keys[lo] == mine);
-    const int n = static_cast<int>(row1 - r0 < kFillRows ? row1 - r0 : kFillRows);
-    for (int r = 0; r < n; ++r) {
-        if ((present >> r) & 1u) continue;
-        uint4* to = out + (r0 + r) * K8;
-        for (int c = threadIdx.x; c < K8; c += blockDim.x) to[c] = make_uint4(0, 0, 0, 0);
-    }
-}
-
 // parts [2][runs][K]: a run's part of a row that began in an earlier run, and of one that it begins and does not end.
 __global__ void __launch_bounds__(kSumThreads) sum_runs_kernel(const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos, int64_t T,
                                                                uint32_t rows, const uint4* __restrict__ dy, int K8, float multiplier,
-                                                               uint4* __restrict__ out, float4* __restrict__ parts, int64_t runs,
-                                                               int64_t filled) {
+                                                               uint4* __restrict__ out, float4* __restrict__ parts, int64_t runs) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int64_t run = blockIdx.x, i0 = run * kRun;
-    if (run >= runs) return fill_rows(out, keys, T, K8, (run - runs) * gridDim.y + blockIdx.y, 0, filled);
     const int n = static_cast<int>(T - i0 < kRun ? T - i0 : kRun);
     const int lane = threadIdx.x & 31;
     // every warp holds the run's keys and positions, one a lane
@@ -543,11 +536,10 @@ __device__ __forceinline__ bool join_warps(Sum& s, float (&sh)[kJoinWarps][32][9
 
 __global__ void __launch_bounds__(32 * kJoinWarps) join_runs_kernel(const uint32_t* __restrict__ keys, int64_t T, uint32_t rows, int K8,
                                                                     float multiplier, const float4* __restrict__ parts, int64_t runs,
-                                                                    uint4* __restrict__ out, int64_t filled) {
+                                                                    uint4* __restrict__ out) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int64_t run = blockIdx.x, end = (run + 1) * kRun;
-    if (run >= runs) return fill_rows(out, keys, T, K8, (run - runs) * gridDim.y + blockIdx.y, filled, rows);
     if (end >= T) return;                                  // the last run's rows end in it
     const uint32_t k = keys[end - 1];
     if (k >= rows || keys[end] != k) return;               // no row goes over this run's end
@@ -611,6 +603,71 @@ __global__ void __launch_bounds__(32 * kJoinWarps) sum_few_rows_kernel(const int
     if (join_warps(s, sh) && c < K8) out[int64_t(blockIdx.x) * K8 + c] = s.rounded(multiplier);
 }
 
+// Few tokens: a CTA takes 256 columns of 32 rows, whose tokens it marks in shared memory. A warp adds up a row of up to
+// kAlone tokens by itself; a row of more takes all eight warps, an eighth of the list each, joined in order.
+// One launch of 6 to 14 us where the sort, sums and joins take 14 (256 tokens, 1 to 16 MB); but it fills zeros row by row,
+// at half the rate (82 MB: 39 us, 25 with the sort).
+constexpr int kFewTokens = 256, kAlone = 24;
+constexpr int64_t kSmallTable = int64_t(8) << 20;   // values
+bool few_tokens(int64_t T, int64_t rows, int64_t K) { return T <= kFewTokens && rows <= kSmallTable / K; }
+__global__ void __launch_bounds__(32 * kJoinWarps) sum_few_tokens_kernel(const int32_t* __restrict__ tokens, int T, int64_t first,
+                                                                         int64_t rows, const uint4* __restrict__ dy, int K8,
+                                                                         float multiplier, uint4* __restrict__ out) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    __shared__ uint8_t key[kFewTokens];   // row of a token among the 32, or 32
+    __shared__ int count[32];
+    __shared__ float sh[kJoinWarps][32][9];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.y * 32 + lane;
+    const int64_t row0 = int64_t(blockIdx.x) * 32;
+    const int n = static_cast<int>(rows - row0 < 32 ? rows - row0 : 32);
+    if (threadIdx.x < 32) count[threadIdx.x] = 0;
+    __syncthreads();
+    const int padded = (T + 255) / 256 * 256;
+    for (int t = threadIdx.x; t < padded; t += 32 * kJoinWarps) {
+        const int64_t at = t < T ? int64_t(tokens[t]) - first - row0 : -1;
+        const bool in = at >= 0 && at < n;
+        key[t] = static_cast<uint8_t>(in ? at : 32);
+        if (in) atomicAdd(&count[at], 1);
+    }
+    __syncthreads();
+    auto add_up = [&](Sum& s, int r, int t0, int t1) {
+        s.zero();
+        for (; t0 < t1; t0 += 32) {
+            uint32_t found = __ballot_sync(0xffffffffu, key[t0 + lane] == r);
+            while (found) {   // eight tokens' loads in flight
+                uint4 v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int t = t0 + __ffs(found) - 1;
+                    v[j] = make_uint4(0, 0, 0, 0);
+                    if (found && c < K8) v[j] = __ldg(dy + int64_t(t) * K8 + c);
+                    found &= found - 1;   // (0 stays 0)
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s.add(v[j]);
+            }
+        }
+    };
+    uint4* to = out + row0 * K8 + c;
+    Sum s;
+    for (int r = warp; r < n; r += kJoinWarps) {
+        if (count[r] > kAlone) continue;
+        if (count[r] > 0) {
+            add_up(s, r, 0, padded);
+            if (c < K8) to[int64_t(r) * K8] = s.rounded(multiplier);
+        } else if (c < K8) {
+            to[int64_t(r) * K8] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    for (int r = 0; r < n; ++r) {
+        if (count[r] <= kAlone) continue;
+        add_up(s, r, warp * (padded / kJoinWarps), (warp + 1) * (padded / kJoinWarps));
+        if (join_warps(s, sh) && c < K8) to[int64_t(r) * K8] = s.rounded(multiplier);
+        __syncthreads();
+    }
+}
+
 // Few: as many CTAs as the GPU holds at once, each with a list it looks through in a few microseconds.
 bool few_rows(int64_t T, int64_t rows, int64_t K) { return T <= 4096 && rows * ((K + 255) / 256) <= 148 * 8; }
 
@@ -621,7 +678,7 @@ struct GradLayout {
 GradLayout grad_layout(int64_t T, int64_t rows, int64_t K) {
     GradLayout l = {};
     l.runs = (T + kRun - 1) / kRun;
-    if (few_rows(T, rows, K)) {
+    if (few_rows(T, rows, K) || few_tokens(T, rows, K)) {
         l.total = 256;
         return l;
     }
@@ -644,9 +701,15 @@ GradLayout grad_layout(int64_t T, int64_t rows, int64_t K) {
     return l;
 }
 
+// CTAs that fill zeros: two an SM, each with four pieces a thread at least.
+unsigned fill_ctas(const Zeros& z) {
+    const int64_t n = (z.to - z.from + 4 * kSortThreads - 1) / (4 * kSortThreads);
+    return static_cast<unsigned>(n < 2 * 148 ? n : 2 * 148);
+}
+
 template <int ITEMS>
 lowbit_status sort_small(const int32_t* tokens, int64_t T, int64_t first, int64_t rows, SortPlan plan, uint32_t* keys, uint32_t* pos,
-                         cudaStream_t stream) {
+                         const Zeros& zeros, cudaStream_t stream) {
     constexpr size_t smem = size_t(kSortThreads) * ITEMS * 6 + kSortWarps * kMaxDigits * 2 + kMaxDigits * 4 + 256;
     static_assert(smem <= 232448, "shared memory");
     static std::atomic<uint64_t> devices{0};
@@ -658,8 +721,8 @@ lowbit_status sort_small(const int32_t* tokens, int64_t T, int64_t first, int64_
             return LOWBIT_ERR_CUDA;
         devices.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_after(sort_small_kernel<ITEMS>, dim3(1), kSortThreads, smem, stream, tokens, static_cast<int>(T), first, rows, plan, keys,
-                        pos);
+    return launch_after(sort_small_kernel<ITEMS>, dim3(1 + fill_ctas(zeros)), kSortThreads, smem, stream, tokens, static_cast<int>(T), first,
+                        rows, plan, keys, pos, zeros);
 }
 
 }  // namespace
@@ -692,46 +755,54 @@ lowbit_status embedding_backward_launch(const int32_t* tokens, const void* dy, i
     if (few_rows(T, rows, K))
         return launch_after(sum_few_rows_kernel, dim3(static_cast<unsigned>(rows), (K8 + 31) / 32), 32 * kJoinWarps, 0, stream, tokens,
                             static_cast<int>(T), first, static_cast<const uint4*>(dy), K8, multiplier, static_cast<uint4*>(out));
+    uint4* dE = static_cast<uint4*>(out);
+    if (few_tokens(T, rows, K))
+        return launch_after(sum_few_tokens_kernel, dim3(static_cast<unsigned>((rows + 31) / 32), (K8 + 31) / 32), 32 * kJoinWarps, 0, stream,
+                            tokens, static_cast<int>(T), first, rows, static_cast<const uint4*>(dy), K8, multiplier, dE);
     uint32_t *keys = at(l.keys), *pos = at(l.pos);
     lowbit_status st = LOWBIT_OK;
     if (T <= kSortMost) {
-        st = T <= kSortThreads ? sort_small<1>(tokens, T, first, rows, plan, keys, pos, stream)
-                               : sort_small<2>(tokens, T, first, rows, plan, keys, pos, stream);
+        const Zeros all{dE, 0, rows * K8};
+        st = T <= kSortThreads ? sort_small<1>(tokens, T, first, rows, plan, keys, pos, all, stream)
+                               : sort_small<2>(tokens, T, first, rows, plan, keys, pos, all, stream);
         if (st != LOWBIT_OK) return st;
     } else {
         uint32_t *k2 = at(l.keys2), *p2 = at(l.pos2), *counts = at(l.counts);
         const uint32_t *kin = nullptr, *pin = nullptr;
+        // (zeros in equal parts beside the launches)
+        const int64_t n = rows * K8, part = (n + 2 * plan.passes - 1) / (2 * plan.passes);
+        auto zeros = [&](int i) {
+            const int64_t from = i * part < n ? i * part : n, to = (i + 1) * part < n ? (i + 1) * part : n;
+            return Zeros{dE, from, to};
+        };
         for (int pass = 0; pass < plan.passes; ++pass) {
             // (the last pass ends in `keys`)
             uint32_t *ko = (plan.passes - pass) % 2 ? keys : k2, *po = (plan.passes - pass) % 2 ? pos : p2;
             const int32_t* tok = pass == 0 ? tokens : nullptr;
             const int shift = pass * plan.bits, tiles = static_cast<int>(l.tiles);
-            st = launch_after(sort_count_kernel, dim3(static_cast<unsigned>(tiles)), kSortThreads, 0, stream, tok, kin, T, first, rows,
-                              shift, plan.bits, counts, tiles);
+            const Zeros z0 = zeros(2 * pass), z1 = zeros(2 * pass + 1);
+            st = launch_after(sort_count_kernel, dim3(tiles + fill_ctas(z0)), kSortThreads, 0, stream, tok, kin, T, first, rows, shift,
+                              plan.bits, counts, tiles, z0);
             if (st != LOWBIT_OK) return st;
             if (tiles > kFewTiles) {
                 st = launch_after(sort_scan_kernel, dim3(1), kSortThreads, 0, stream, counts, (int64_t(1) << plan.bits) * tiles);
                 if (st != LOWBIT_OK) return st;
             }
-            st = launch_after(sort_move_kernel, dim3(static_cast<unsigned>(tiles)), kSortThreads, 0, stream, tok, kin, pin, T, first, rows, shift,
-                              plan.bits, counts, tiles, ko, po);
+            st = launch_after(sort_move_kernel, dim3(tiles + fill_ctas(z1)), kSortThreads, 0, stream, tok, kin, pin, T, first, rows, shift,
+                              plan.bits, counts, tiles, ko, po, z1);
             if (st != LOWBIT_OK) return st;
             kin = ko;
             pin = po;
         }
     }
     const unsigned slabs = (K8 + kSumThreads - 1) / kSumThreads;
-    // Three fifths of the zeros beside the sums, which read as much as a fifth of them, the others beside the joins.
-    const int64_t filled = rows * 3 / 5;
-    auto fillers = [](int64_t n, int64_t y) { return (n + kFillRows * y - 1) / (kFillRows * y); };
     float4* parts = reinterpret_cast<float4*>(base + l.parts);
-    uint4* dE = static_cast<uint4*>(out);
-    st = launch_after(sum_runs_kernel, dim3(static_cast<unsigned>(l.runs + fillers(filled, slabs)), slabs), kSumThreads, 0, stream, keys, pos, T,
-                      static_cast<uint32_t>(rows), static_cast<const uint4*>(dy), K8, multiplier, dE, parts, l.runs, filled);
+    st = launch_after(sum_runs_kernel, dim3(static_cast<unsigned>(l.runs), slabs), kSumThreads, 0, stream, keys, pos, T,
+                      static_cast<uint32_t>(rows), static_cast<const uint4*>(dy), K8, multiplier, dE, parts, l.runs);
     if (st != LOWBIT_OK) return st;
     const unsigned strips = (K8 + 31) / 32;
-    return launch_after(join_runs_kernel, dim3(static_cast<unsigned>(l.runs + fillers(rows - filled, strips)), strips), 32 * kJoinWarps, 0,
-                        stream, keys, T, static_cast<uint32_t>(rows), K8, multiplier, parts, l.runs, dE, filled);
+    return launch_after(join_runs_kernel, dim3(static_cast<unsigned>(l.runs), strips), 32 * kJoinWarps, 0,
+                        stream, keys, T, static_cast<uint32_t>(rows), K8, multiplier, parts, l.runs, dE);
 }
 
 }  // namespace lowbit

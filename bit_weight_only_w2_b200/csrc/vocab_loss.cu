@@ -19,12 +19,12 @@ constexpr int64_t kPieceBytes = int64_t(256) << 20;
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 template <class... P, class... A>
-lowbit_status launch_after(void (*kernel)(P...), int64_t blocks, int threads, cudaStream_t stream, A... args) {
+lowbit_status launch_after(void (*kernel)(P...), int64_t blocks, unsigned strips, int threads, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), strips, 1);
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -174,47 +174,75 @@ __global__ void __launch_bounds__(256) keep_labelled_kernel(const uint4* __restr
 }
 
 // dX from the tiles of its sums: a block takes what one warp of vocab_kernel<kVocabDx> left, 32 tokens by half a
-// tile's columns, adds the slices in order and scales.
+// tile's columns, adds the slices in order and scales. Where there are many slices (few tokens: 64 of them, in 8 blocks)
+// it takes 32 columns, and each of its warps adds an eighth of the slices for them, joined in order: 16 tokens x 128
+// columns took 26 us without.
 // Tiles as that kernel writes them: [slice][column tile][token tile][CTA][warp][column / 4][lane].
-template <bool PAIR>
+constexpr int kManySlices = 8;
+template <bool PAIR, bool MANY>
 __global__ void __launch_bounds__(256) dx_out_kernel(const float4* __restrict__ acc, int slices, int m_tiles, int n_tiles, int M, int K,
                                                      const int32_t* __restrict__ labels, const float* __restrict__ grad, int vocab,
                                                      float unscale, __nv_bfloat16* __restrict__ dX) {
     grid_launch_dependents();
     grid_dependency_wait();
     constexpr int kCtas = PAIR ? 2 : 1, kCols = PAIR ? 128 : 64;
+    constexpr int kMine = MANY ? 32 : kCols;   // of the columns, this block's
     const int warp = blockIdx.x & 7, rank = (blockIdx.x >> 3) % kCtas, tile = (blockIdx.x >> 3) / kCtas;   // tile within a slice
     const int m = tile % m_tiles, n = tile / m_tiles;
-    const int r0 = m * (PAIR ? 256 : 128) + rank * 128 + (warp & 3) * 32, c0 = n * 2 * kCols + (warp >> 2) * kCols;
+    const int r0 = m * (PAIR ? 256 : 128) + rank * 128 + (warp & 3) * 32;
+    const int c0 = n * 2 * kCols + (warp >> 2) * kCols + blockIdx.y * kMine;
     if (r0 >= M || c0 >= K) return;
-    __shared__ uint2 sh[32][kCols / 4 + 1];
-    const int lane = threadIdx.x & 31;
+    __shared__ uint2 sh[32][kMine / 4 + 1];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     // (a token without a label has no gradient, though zeros times an infinite row are no zeros)
     const bool has = r0 + lane < M && static_cast<unsigned>(labels[r0 + lane]) < static_cast<unsigned>(vocab);
     float f = 1.f;
     if (has && unscale != 1.f) f = grad[r0 + lane] * unscale;   // packed tables: G came without the tokens' own factor
     const size_t slice = static_cast<size_t>(m_tiles) * n_tiles * kCtas * 8 * (kCols / 4) * 32;
-    const float4* at = acc + static_cast<size_t>(blockIdx.x) * (kCols / 4) * 32 + lane;
-#pragma unroll
-    for (int i = 0; i < kCols / 32; ++i) {
-        const int c = (threadIdx.x >> 5) + 8 * i;
-        float4 s = at[c * 32];
-#pragma unroll 8
-        for (int k = 1; k < slices; ++k) {
-            const float4 v = at[k * slice + c * 32];
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
-        }
+    const float4* at = acc + (static_cast<size_t>(blockIdx.x) * (kCols / 4) + blockIdx.y * (kMine / 4)) * 32 + lane;
+    auto add = [](float4& a, const float4& v) {
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+    };
+    auto put = [&](int c, float4 s) {
         if (!has) s = make_float4(0.f, 0.f, 0.f, 0.f);
         const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x * f, s.y * f), hi = __floats2bfloat162_rn(s.z * f, s.w * f);
         sh[lane][c] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    };
+    if constexpr (MANY) {
+        __shared__ float4 part[8][8][32];   // [warp][column / 4][lane]
+        const int per = (slices + 7) / 8, k1 = min(slices, (w + 1) * per);
+        float4 s[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int k = w * per; k < k1; ++k) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) add(s[c], at[k * slice + c * 32]);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) part[w][c][lane] = s[c];
+        __syncthreads();
+        float4 sum = part[0][w][lane];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) add(sum, part[k][w][lane]);
+        put(w, sum);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kCols / 32; ++i) {
+            const int c = w + 8 * i;
+            float4 s = at[c * 32];
+#pragma unroll 8
+            for (int k = 1; k < slices; ++k) add(s, at[k * slice + c * 32]);
+            put(c, s);
+        }
     }
     __syncthreads();
     // (K is a multiple of 8: whole 16-byte stores)
-    for (int i = threadIdx.x; i < 32 * (kCols / 8); i += 256) {
-        const int r = i / (kCols / 8), c = i % (kCols / 8), col = c0 + 8 * c;
+    for (int i = threadIdx.x; i < 32 * (kMine / 8); i += 256) {
+        const int r = i / (kMine / 8), c = i % (kMine / 8), col = c0 + 8 * c;
         if (r0 + r < M && col < K) {
             const uint2 a = sh[r][2 * c], d = sh[r][2 * c + 1];
             *reinterpret_cast<uint4*>(dX + static_cast<size_t>(r0 + r) * K + col) = make_uint4(a.x, a.y, d.x, d.y);
@@ -344,13 +372,13 @@ lowbit_status forward_of(const LossProblem& p, const LossLayout& l, uint8_t* ws,
         const lowbit_status st =
             smallm_launch(g, g.N >= 64 * sms ? static_cast<int>(rows) : 0, g.N >= 64 * sms ? 1 : 0, g.M <= 8, stream, nullptr, true, t.N);
         if (st != LOWBIT_OK) return st;
-        return launch_after(loss_rows_kernel, g.M * kRowCtas, kRowThreads, stream, reinterpret_cast<const float*>(ws + l.logits), g.N,
+        return launch_after(loss_rows_kernel, g.M * kRowCtas, 1, kRowThreads, stream, reinterpret_cast<const float*>(ws + l.logits), g.N,
                             p.labels, static_cast<int>(p.vocab), p.loss, p.lse_out);
     }
     lowbit_status st = copy_x(p, l, ws, stream);
     if (st == LOWBIT_OK) st = product(kVocabStats, l.pair, p, l, ws, 0, p.vocab, true, stream);
     if (st != LOWBIT_OK) return st;
-    return launch_after(p.M <= 1024 ? loss_join_kernel<1> : loss_join_kernel<8>, p.M <= 1024 ? p.M : (p.M + 7) / 8, kJoinThreads, stream,
+    return launch_after(p.M <= 1024 ? loss_join_kernel<1> : loss_join_kernel<8>, p.M <= 1024 ? p.M : (p.M + 7) / 8, 1, kJoinThreads, stream,
                         reinterpret_cast<const float2*>(ws + l.part), reinterpret_cast<const float*>(ws + l.target), p.labels,
                         static_cast<int>(2 * l.n_tiles), static_cast<int>(p.M), static_cast<int>(p.vocab), p.loss, p.lse_out);
 }
@@ -382,7 +410,7 @@ lowbit_status loss_backward(const LossProblem& p, const LossLayout& l, uint8_t* 
                             static_cast<size_t>(p.table.N - p.vocab) * K * 2, stream) != cudaSuccess)
             return LOWBIT_ERR_CUDA;
         const int64_t count = p.M * (K / 8), blocks = (count + 255) / 256;
-        st = launch_after(keep_labelled_kernel, blocks < 148 * 8 ? blocks : 148 * 8, 256, stream, static_cast<const uint4*>(p.X), p.labels,
+        st = launch_after(keep_labelled_kernel, blocks < 148 * 8 ? blocks : 148 * 8, 1, 256, stream, static_cast<const uint4*>(p.X), p.labels,
                           static_cast<int>(p.vocab), count, static_cast<int>(K / 8), reinterpret_cast<uint4*>(ws + l.xz));
         if (st != LOWBIT_OK) return st;
     }
@@ -399,7 +427,10 @@ lowbit_status loss_backward(const LossProblem& p, const LossLayout& l, uint8_t* 
     }
     const int64_t blocks = l.m_tiles * l.dx_tiles * (l.pair ? 2 : 1) * 8;
     const float unscale = p.table.bits == kDense ? 1.f : 1.f / 32768.f;
-    return launch_after(l.pair ? dx_out_kernel<true> : dx_out_kernel<false>, blocks, 256, stream,
+    const bool many = slices >= kManySlices;
+    const auto out = l.pair ? (many ? dx_out_kernel<true, true> : dx_out_kernel<true, false>)
+                            : (many ? dx_out_kernel<false, true> : dx_out_kernel<false, false>);
+    return launch_after(out, blocks, many ? (l.pair ? 4 : 2) : 1, 256, stream,
                         reinterpret_cast<const float4*>(ws + l.acc), slices, static_cast<int>(l.m_tiles), static_cast<int>(l.dx_tiles),
                         static_cast<int>(p.M), static_cast<int>(K), p.labels, p.grad, static_cast<int>(p.vocab), unscale,
                         static_cast<__nv_bfloat16*>(p.dX));

@@ -487,3 +487,26 @@ def test_same_results_every_time(V):
             a @ a
         got = loss_step(table, x, labels, grad, V) + (lb.embedding_backward(tokens, x, 300),)
         assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("T,K,first,rows", [(1, 8, 0, 4000), (7, 1240, 3, 4001), (200, 1032, 0, 3000), (256, 136, 50, 20011),
+                                            (256, 2560, 0, 3276), (256, 2560, 0, 3278), (257, 136, 5, 2000)])
+@pytest.mark.parametrize("spread", [1, 6])
+def test_few_tokens_of_a_table(T, K, first, rows, spread):
+    """Tokens spread out and on few rows (some by a warp, some by eight), zeros in all other rows."""
+    g = torch.Generator(device="cuda").manual_seed(T + K)
+    tokens = (first - 2 + (rows + 4) * torch.rand(T, generator=g, device="cuda") ** spread).int()
+    dy = torch.randn(T, K, generator=g, **BF16)
+    de, ok = guarded((rows, K), torch.bfloat16)
+    lb.embedding_backward(tokens, dy, rows, first=first, multiplier=0.7, out=de)
+    check(de, *embedding_grad_ref(tokens, dy, first, rows, 0.7), "de")
+    assert ok()
+
+
+@pytest.mark.parametrize("bits,gs", [(1, 128), (2, 64), (4, 64), (16, 0)])
+@pytest.mark.parametrize("M,K,V", [(3, 128, 43000), (90, 256, 30001), (300, 128, 60000), (140, 384, 9001)])
+def test_many_slices(bits, gs, M, K, V):
+    """Few tiles of dX whose reduction over a long vocabulary is cut into many slices."""
+    table = Table((V + 7) // 8 * 8, K, bits, gs)
+    x, labels, grad = inputs(M, K, V)
+    check_loss(table, x, labels, grad, V, loss_step(table, x, labels, grad, V))
