@@ -640,20 +640,39 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
     }
 }
 
+// The shared-memory opt-in, once per kernel and device.
+template <int MODE, int BITS, bool PAIR, bool FEW>
+bool opt_in(const void* fn, int bytes) {
+    static std::atomic<uint64_t> devices{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+    if (!bit || !(devices.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+        devices.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    return true;
+}
+inline CUtensorMapSwizzle word_swizzle(int row_bytes) {
+    return row_bytes == 16 ? CU_TENSOR_MAP_SWIZZLE_NONE : row_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B;
+}
+// The tensor cores cut what they add to an accumulator off below its last bit, towards zero: a sum that grows evenly
+// over n MMA steps to l loses about 0.26 n 2^-24 l (measured for n = 32 .. 320 and all formats: 2.5e-6 l at K = 2560,
+// with a spread of a fifth of that), always to the same side. The logits are scaled up by as much.
+inline float evened(int terms, int stages) { return 1.f + 0.26f * 5.9604645e-8f * 4.f * static_cast<float>(terms * stages); }
+// CTA pairs that the GPU holds at once.
+inline int pair_slots(const void* fn, int threads, int smem_bytes) {
+    int pairs = cluster_capacity(fn, 2, threads, smem_bytes, true);
+    if (pairs > num_sms() / 2) pairs = num_sms() / 2;
+    return pairs < 1 ? 1 : pairs;
+}
+
 template <int MODE, int BITS, bool PAIR>
 lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
     using C = Cfg<MODE, BITS, PAIR>;
     auto kernel = vocab_kernel<MODE, BITS, PAIR>;
     const void* fn = reinterpret_cast<const void*>(kernel);
-    static std::atomic<uint64_t> devices{0};   // the shared-memory opt-in is per device
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
-    const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
-    if (!bit || !(devices.load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
-            return LOWBIT_ERR_CUDA;
-        devices.fetch_or(bit, std::memory_order_acq_rel);
-    }
+    if (!opt_in<MODE, BITS, PAIR, false>(fn, C::kSmemBytes)) return LOWBIT_ERR_CUDA;
     const LossProblem& q = *v.p;
     const LossLayout& l = *v.l;
     const Table& w = q.table;
@@ -678,11 +697,8 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
         if (!C::kPacked) {
             ok = ok && make_map_2d(&mb, half, 2, w.rows, K, vocab, K * 2, 64, C::kLogits ? 128 : 64, sw);
         } else {
-            const CUtensorMapSwizzle wsw = C::kWRowBytes == 16   ? CU_TENSOR_MAP_SWIZZLE_NONE
-                                           : C::kWRowBytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
-                                                                 : CU_TENSOR_MAP_SWIZZLE_64B;
             ok = ok && make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, w.rows, K * BITS / 32, vocab, K * BITS / 8,
-                                   C::kWRowBytes / 4, C::kWRows, wsw);
+                                   C::kWRowBytes / 4, C::kWRows, word_swizzle(C::kWRowBytes));
             const uint32_t groups = 128 / w.group_size;
             ok = ok && make_map_2d(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w.scales, vocab, K / w.group_size,
                                    static_cast<uint64_t>(w.N) * 2, C::kWRows, groups, CU_TENSOR_MAP_SWIZZLE_NONE);
@@ -720,10 +736,7 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
         p.m_tiles = static_cast<int>((cols + C::kRows - 1) / C::kRows);
         p.n_tiles = static_cast<int>((K + C::kCols - 1) / C::kCols);
     }
-    // The tensor cores cut what they add to an accumulator off below its last bit, towards zero: a sum that grows evenly
-    // over n MMA steps to l loses about 0.26 n 2^-24 l (measured for n = 32 .. 320 and all formats: 2.5e-6 l at K = 2560,
-    // with a spread of a fifth of that), always to the same side. The logits are scaled up by as much.
-    p.evened = 1.f + 0.26f * 5.9604645e-8f * 4.f * C::kTerms * static_cast<float>(p.stages);
+    p.evened = evened(C::kTerms, p.stages);
     int slices = 1;
     if (MODE == kVocabDx) {
         slices = l.slices < p.stages ? l.slices : p.stages;
@@ -752,9 +765,7 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
     attrs[na].val.programmaticStreamSerializationAllowed = 1;
     ++na;
     if (PAIR) {
-        int pairs = cluster_capacity(fn, 2, C::kThreads, C::kSmemBytes, true);
-        if (pairs > num_sms() / 2) pairs = num_sms() / 2;
-        if (pairs < 1) pairs = 1;
+        const int pairs = pair_slots(fn, C::kThreads, C::kSmemBytes);
         cfg.gridDim = dim3(2 * (p.num_tiles < pairs ? p.num_tiles : pairs), 1, 1);
         attrs[na].id = cudaLaunchAttributeClusterDimension;
         attrs[na].val.clusterDim.x = 2;
@@ -774,17 +785,15 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kernel, ma, mb, ms, mz, mo, p) == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
 
-template <int BITS>
-lowbit_status dispatch(const VocabProduct& v, cudaStream_t s) {
+// The products over a bf16 table.
+inline lowbit_status dispatch_dense(const VocabProduct& v, cudaStream_t s) {
     switch (v.mode) {
-        case kVocabStats: return v.pair ? launch<kVocabStats, BITS, true>(v, s) : launch<kVocabStats, BITS, false>(v, s);
-        case kVocabGrad: return v.pair ? launch<kVocabGrad, BITS, true>(v, s) : launch<kVocabGrad, BITS, false>(v, s);
-        case kVocabDx: return v.pair ? launch<kVocabDx, BITS, true>(v, s) : launch<kVocabDx, BITS, false>(v, s);
-        default: break;
+        case kVocabStats: return v.pair ? launch<kVocabStats, kDense, true>(v, s) : launch<kVocabStats, kDense, false>(v, s);
+        case kVocabGrad: return v.pair ? launch<kVocabGrad, kDense, true>(v, s) : launch<kVocabGrad, kDense, false>(v, s);
+        case kVocabDx: return v.pair ? launch<kVocabDx, kDense, true>(v, s) : launch<kVocabDx, kDense, false>(v, s);
+        case kVocabDw: return launch<kVocabDw, kDense, true>(v, s);
+        default: return LOWBIT_ERR_UNSUPPORTED;
     }
-    if constexpr (BITS == kDense)
-        if (v.mode == kVocabDw) return launch<kVocabDw, BITS, true>(v, s);
-    return LOWBIT_ERR_UNSUPPORTED;
 }
 
 }  // namespace vocab

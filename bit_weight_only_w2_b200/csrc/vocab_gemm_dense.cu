@@ -2,5 +2,5 @@
 #include "vocab_gemm.cuh"
 
 namespace lowbit {
-lowbit_status vocab_product_dense(const VocabProduct& v, cudaStream_t stream) { return vocab::dispatch<kDense>(v, stream); }
+lowbit_status vocab_product_dense(const VocabProduct& v, cudaStream_t stream) { return vocab::dispatch_dense(v, stream); }
 }  // namespace lowbit

@@ -298,7 +298,7 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
         return here;
     };
     const size_t logits = static_cast<size_t>(M < kSmallTokens ? M : kSmallTokens) * up(vocab, 8) * 4;
-    if (bits != kDense && !backward && M <= kSmallTokens) {
+    if (bits == 4 && !backward && M <= kSmallTokens) {
         l.small = true;
         l.logits = take(logits);
         l.total = at;
@@ -312,9 +312,10 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
     if (!backward) {
         l.target = take(static_cast<size_t>(M) * 4);
         // (room for the narrow tiles of 128 tokens too, so that a workspace for M tokens serves fewer)
-        const int64_t narrow = 2 * ((vocab + 127) / 128) * (M < 128 ? M : 128), parts = 2 * l.n_tiles * M;
-        l.part = take(static_cast<size_t>(parts > narrow ? parts : narrow) * 8);
-        l.total = bits != kDense && at < logits ? logits : at;   // (serves the small batches too)
+        const int64_t few = bits == kDense ? 2 * ((vocab + 127) / 128) : 8 * ((vocab + 255) / 256), narrow = few * (M < 128 ? M : 128);
+        l.parts = l.pair ? 2 * l.n_tiles : few;
+        l.part = take(static_cast<size_t>(l.parts * M > narrow ? l.parts * M : narrow) * 8);
+        l.total = bits == 4 && at < logits ? logits : at;   // (serves the small batches too)
         return l;
     }
     const int64_t whole = up(vocab, 256), tokens = M > 0 ? M : 1;
@@ -380,7 +381,7 @@ lowbit_status forward_of(const LossProblem& p, const LossLayout& l, uint8_t* ws,
     if (st != LOWBIT_OK) return st;
     return launch_after(p.M <= 1024 ? loss_join_kernel<1> : loss_join_kernel<8>, p.M <= 1024 ? p.M : (p.M + 7) / 8, 1, kJoinThreads, stream,
                         reinterpret_cast<const float2*>(ws + l.part), reinterpret_cast<const float*>(ws + l.target), p.labels,
-                        static_cast<int>(2 * l.n_tiles), static_cast<int>(p.M), static_cast<int>(p.vocab), p.loss, p.lse_out);
+                        static_cast<int>(l.parts), static_cast<int>(p.M), static_cast<int>(p.vocab), p.loss, p.lse_out);
 }
 
 }  // namespace
