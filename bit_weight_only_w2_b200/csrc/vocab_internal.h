@@ -39,7 +39,7 @@ struct LossProblem {
 //             small: logits [M][N] fp32
 //   backward  xh, xz (the tokens with a label, dW only), g [M][piece], acc (fp32 tiles of dX)
 struct LossLayout {
-    bool small;              // up to 16 tokens, uint4: fp32 logits by the small-M kernel
+    bool small;              // up to 16 tokens, packed: fp32 logits by the small-M kernel
     bool pair;               // tiles of 256 tokens x 256 columns on CTA pairs, else 128 x 128 (logits of a packed table:
                              // 256 rows of it x the tokens, on CTA pairs, vocab_few.cuh)
     int64_t m_tiles, n_tiles;

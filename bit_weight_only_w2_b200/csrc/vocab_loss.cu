@@ -298,7 +298,7 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
         return here;
     };
     const size_t logits = static_cast<size_t>(M < kSmallTokens ? M : kSmallTokens) * up(vocab, 8) * 4;
-    if (bits == 4 && !backward && M <= kSmallTokens) {
+    if (bits != kDense && !backward && M <= kSmallTokens) {
         l.small = true;
         l.logits = take(logits);
         l.total = at;
@@ -315,7 +315,7 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
         const int64_t few = bits == kDense ? 2 * ((vocab + 127) / 128) : 8 * ((vocab + 255) / 256), narrow = few * (M < 128 ? M : 128);
         l.parts = l.pair ? 2 * l.n_tiles : few;
         l.part = take(static_cast<size_t>(l.parts * M > narrow ? l.parts * M : narrow) * 8);
-        l.total = bits == 4 && at < logits ? logits : at;   // (serves the small batches too)
+        l.total = bits != kDense && at < logits ? logits : at;   // (serves the small batches too)
         return l;
     }
     const int64_t whole = up(vocab, 256), tokens = M > 0 ? M : 1;
