@@ -1,6 +1,6 @@
 // Argument marshalling of the Python binding's short calls, compiled: the checks, allocations and the
-// call into liblowbit.so of adapter_gemm, adapter_backward, gemm_dx, the 8-bit copies and the vocabulary calls. A call's host
-// time with it and in Python: 10.2 and 19.0 us for one token (6 us on the GPU), 17.2 and 30.7 for the
+// call into liblowbit.so of adapter_gemm, adapter_backward, gemm_dx, the 8-bit copies and the vocabulary calls. A call's
+// host time with it and in Python: 10.2 and 19.0 us for one token (6 us on the GPU), 17.2 and 30.7 for the
 // backward of 77 tokens, 5.6 and 10.9 for the 8-bit copy of 77 x 2560 values.
 //
 // Each function returns its outputs, or the library's status as an int if that is not 0, or None if

@@ -23,6 +23,7 @@
 // Persistent grids; the logits' tiles go through the tokens first, so that a table's rows are read from memory once.
 // Operands are K-major for the logits; for the gradients the table [v][k] (dX: reduced over v), G [m][v] and X [m][k]
 // (dW: reduced over m) are read as they lie, as MN-major operands, so nothing is transposed.
+// The narrow tiles serve up to 128 tokens: logits of bf16 tables, and dX; logits of packed ones are vocab_few.cuh's.
 #pragma once
 
 #include <atomic>
@@ -60,7 +61,7 @@ struct Cfg {
     static constexpr int kAStageBytes = kPacked ? kOperandBytes : 2 * kOperandBytes;
     static constexpr int kBStageBytes = kPacked ? kTerms * kOperandBytes : 0;
     // (kVocabDx: 12, since a stage of its ring takes a stage of words, which come from memory: with 4 the gradient of 77
-    // tokens waited for them, 37 us against KDX)
+    // tokens waited for them, 37 us against 28)
     static constexpr int kWStages = !kPacked ? 0 : !kLogits ? 12 : kTerms == 2 ? 3 : 4;
     static constexpr int kStagingBytes = (MODE == kVocabGrad || MODE == kVocabDw) ? kEpiWarps * 4096 : 0;
     static constexpr int kRoom = kSmemLimit - 2048 - kStagingBytes - kWStages * kWStageBytes;
@@ -99,6 +100,7 @@ struct Params {
     const float* grad;
     float2* part;           // kVocabStats: [2 * n_tiles][M]
     float* target;          // [M]
+    float* rest;            // kVocabGrad, bf16 tables: what rounding took from G's value at each token's label
     float4* acc;            // kVocabDx: [tile][CTA of the pair][warp][column / 4][lane]
     int accumulate;         // add to what acc holds
     float gscale;           // packed: the power of two in G
@@ -581,6 +583,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                                     float g = ex2(fmaf(e[k], rl, -shift));
                                     if (col == want) g -= 1.f;
                                     e[k] = label >= 0 && col < left ? g * f : 0.f;
+                                    if (BITS == kDense && col == want) p.rest[row] = e[k] - __bfloat162float(__float2bfloat16_rn(e[k]));
                                 }
                             }
                             o[j / 2] = BITS == kDense ? pack_bf16x2(e[0], e[1]) : pack_f16x2(e[0], e[1]);
@@ -752,6 +755,7 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
     p.grad = q.grad;
     p.part = reinterpret_cast<float2*>(v.ws + l.part);
     p.target = reinterpret_cast<float*>(v.ws + l.target);
+    p.rest = reinterpret_cast<float*>(v.ws + l.rest);
     p.acc = reinterpret_cast<float4*>(v.ws + l.acc);
     p.accumulate = v.first ? 0 : 1;
     p.gscale = 32768.f;

@@ -182,7 +182,8 @@ constexpr int kManySlices = 8;
 template <bool PAIR, bool MANY>
 __global__ void __launch_bounds__(256) dx_out_kernel(const float4* __restrict__ acc, int slices, int m_tiles, int n_tiles, int M, int K,
                                                      const int32_t* __restrict__ labels, const float* __restrict__ grad, int vocab,
-                                                     float unscale, __nv_bfloat16* __restrict__ dX) {
+                                                     float unscale, const float* __restrict__ rest,
+                                                     const __nv_bfloat16* __restrict__ W, __nv_bfloat16* __restrict__ dX) {
     grid_launch_dependents();
     grid_dependency_wait();
     constexpr int kCtas = PAIR ? 2 : 1, kCols = PAIR ? 128 : 64;
@@ -206,7 +207,18 @@ __global__ void __launch_bounds__(256) dx_out_kernel(const float4* __restrict__ 
         a.z += v.z;
         a.w += v.w;
     };
+    // bf16 tables: G's value at the label, often most of a token's gradient, was rounded to bf16 like the others; what that
+    // took (half a step, as much as dX's own rounding) is made up for here, from the label's row.
+    const float more = rest && has ? rest[r0 + lane] : 0.f;
+    const __nv_bfloat16* wrow = rest && has ? W + static_cast<size_t>(labels[r0 + lane]) * K : nullptr;
     auto put = [&](int c, float4 s) {
+        if (wrow && c0 + 4 * c < K) {
+            const uint2 w = *reinterpret_cast<const uint2*>(wrow + c0 + 4 * c);
+            s.x = fmaf(more, __uint_as_float(w.x << 16), s.x);
+            s.y = fmaf(more, __uint_as_float(w.x & 0xFFFF0000u), s.y);
+            s.z = fmaf(more, __uint_as_float(w.y << 16), s.z);
+            s.w = fmaf(more, __uint_as_float(w.y & 0xFFFF0000u), s.w);
+        }
         if (!has) s = make_float4(0.f, 0.f, 0.f, 0.f);
         const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x * f, s.y * f), hi = __floats2bfloat162_rn(s.z * f, s.w * f);
         sh[lane][c] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
@@ -343,6 +355,7 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
     if (g > static_cast<size_t>(tokens) * whole * 2) g = static_cast<size_t>(tokens) * whole * 2;
     size_t acc = 8 * slots * tile < 64 * tiles * tile ? 8 * slots * tile : 64 * tiles * tile;
     if (acc < tiles * tile) acc = tiles * tile;
+    if (bits == kDense) l.rest = take(static_cast<size_t>(M) * 4);
     if (need_dw) l.xz = take(static_cast<size_t>(M) * K * 2);
     l.g = take(g);
     l.acc = take(acc);
@@ -434,7 +447,8 @@ lowbit_status loss_backward(const LossProblem& p, const LossLayout& l, uint8_t* 
     return launch_after(out, blocks, many ? (l.pair ? 4 : 2) : 1, 256, stream,
                         reinterpret_cast<const float4*>(ws + l.acc), slices, static_cast<int>(l.m_tiles), static_cast<int>(l.dx_tiles),
                         static_cast<int>(p.M), static_cast<int>(K), p.labels, p.grad, static_cast<int>(p.vocab), unscale,
-                        static_cast<__nv_bfloat16*>(p.dX));
+                        p.table.bits == kDense ? reinterpret_cast<const float*>(ws + l.rest) : nullptr,
+                        static_cast<const __nv_bfloat16*>(p.table.rows), static_cast<__nv_bfloat16*>(p.dX));
 }
 
 }  // namespace lowbit

@@ -355,8 +355,9 @@ lowbit_status lowbit_checkpoint_load(const uint8_t* codes, const uint8_t* exps, 
  *   its gradients   G[m][v] = grad[m] * (exp(l[m][v] - lse[m]) - [v = label m]), zeros for such a label;
  *                   dX = G W, dW = G^T X
  *
- * The logits are never stored: the forward keeps a maximum and a sum per token and 128 columns, the backward forms
- * them again, a piece of the vocabulary at a time. The pages have no counterpart. All calls are asynchronous on
+ * The logits are not kept: the forward leaves a maximum and a sum per token and 32 to 128 of them, the backward forms
+ * them again, a piece of the vocabulary at a time. (Up to 16 tokens of a packed table pass through the workspace in
+ * fp32, 64 bytes a row of the table at most.) The pages have no counterpart. All calls are asynchronous on
  * `stream` and never synchronise; results do not depend on timing. No output and no workspace may overlap an input
  * or another output; a workspace belongs to one call until its work on the GPU is done. */
 
@@ -367,8 +368,9 @@ size_t lowbit_cross_entropy_workspace_size(int64_t M, int64_t vocab, int64_t K, 
 
 /* loss fp32 [M] and lse fp32 [M] of X bf16 [M][K] (16-byte aligned). Sums are fp32. A packed table's weights are the
  * values that lowbit_gemm decodes, a uint4 weight as the sum of two fp16 values (2^-17 of its scale, 2^-25 absolute
- * at the least; zeros up to 2^14 in magnitude), so the loss is good to fp32 sums of K products. A row of X with an infinity or NaN has a lse
- * and loss that are not finite; other rows are not touched by it. 1 <= vocab <= N (else LOWBIT_ERR_INVALID_ARG). */
+ * at the least; zeros up to 2^14 in magnitude), or up to 16 tokens as q - 8 and z - 8, multiplied apart; so the loss is
+ * good to fp32 sums of K products. A row of X with an infinity or NaN has a lse and loss that are not finite; other rows
+ * are not touched by it. 1 <= vocab <= N (else LOWBIT_ERR_INVALID_ARG). */
 lowbit_status lowbit_cross_entropy(int64_t M, int64_t vocab, int64_t N, int64_t K, int bits, int group_size, const void* X,
                                    const void* W, const void* scales, const void* zeros, const int32_t* labels, float* loss,
                                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
@@ -377,9 +379,10 @@ lowbit_status lowbit_cross_entropy(int64_t M, int64_t vocab, int64_t N, int64_t 
  *   dX   bf16 [M][K], 16-byte aligned; zeros for a token without a label
  *   dW   bf16 [N][K], 16-byte aligned, or NULL (bf16 tables only, else LOWBIT_ERR_UNSUPPORTED); zeros from row
  *        `vocab` on. What X holds for a token without a label does not matter.
- * G is rounded once, to bf16 (bf16 tables, after the factor grad) or to fp16 (packed ones, before it, times 2^15:
- * 2^-40 absolute at the least); for dX a uint4 weight is
- * (q - z) * s with the difference and the product rounded to fp16 (as in lowbit_gemm_dx); sums are fp32; dX and dW are rounded once. */
+ * G is rounded once, to bf16 (bf16 tables, after the factor grad; for dX the values at the labels are not) or to fp16 (packed ones, before it, times 2^15:
+ * 2^-40 absolute at the least, and infinite where exp(l - lse) passes 2, as it can with a lse that is not the
+ * forward's); for dX a uint4 weight is (q - z) * s with the difference and the product rounded to fp16 (as in
+ * lowbit_gemm_dx); sums are fp32; dX and dW are rounded once. */
 lowbit_status lowbit_cross_entropy_backward(int64_t M, int64_t vocab, int64_t N, int64_t K, int bits, int group_size,
                                             const void* X, const void* W, const void* scales, const void* zeros,
                                             const int32_t* labels, const float* lse, const float* grad, void* dX, void* dW,

@@ -510,3 +510,23 @@ def test_many_slices(bits, gs, M, K, V):
     table = Table((V + 7) // 8 * 8, K, bits, gs)
     x, labels, grad = inputs(M, K, V)
     check_loss(table, x, labels, grad, V, loss_step(table, x, labels, grad, V))
+
+
+@pytest.mark.parametrize("M,K,V", [(1, 128, 1000), (40, 264, 5000), (300, 512, 3003)])
+def test_the_label_is_most_of_the_gradient(M, K, V):
+    """Tokens that know nothing (all p near 1 / V): dX is the label's row and little else, and G's rounding to bf16 there
+    does not show: |G| of the others is at most 2 / V of it, so dX is off by its own rounding and 2^-8 2 sum |w| / V."""
+    table = Table(V, K, 16, norm=1.0)
+    x, labels, grad = inputs(M, K, V)
+    x = (x.float() / 64).bfloat16()
+    loss, lse = lb.cross_entropy(x, labels, *table.args())
+    dx, _ = lb.cross_entropy_backward(grad, x, labels, lse, *table.args())
+    ref = Loss(x, labels, table, V)
+    (rx, _), _ = ref.gradients(grad, lse)
+    p = (ref.l - lse.double()[:, None]).exp()
+    assert p.max() <= 2 / V
+    f = torch.where(ref.valid, grad, 0.0).double().abs()[:, None]
+    w = ref.w.abs()
+    sums = f * (w.sum(0) / V * 2 + w[ref.label])
+    e = HB16 * f * 2 / V * w.sum(0) + (V + 16) * H32 * sums + 2.0 ** -20 * f * w[ref.label]
+    check(dx, rx, e + HB16 * (rx.abs() + e), "dx")
