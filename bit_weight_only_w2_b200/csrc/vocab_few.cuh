@@ -136,6 +136,10 @@ __global__ void __launch_bounds__(FewCfg<MODE, BITS>::kThreads, 1)
     const int tile0 = static_cast<int>(blockIdx.x >> 1), tile_step = static_cast<int>(gridDim.x >> 1);
     auto row0_of = [&](int t) { return 256 * t + static_cast<int>(rank) * 128; };   // this CTA's first row, within the piece
     const int half_tokens = p.a_rows;                                               // of the CTA's half: a multiple of 16
+    // Two accumulators of 128 columns in turn; uint4 keeps the terms' sums apart (as vocab_kernel does), in two of 64
+    // columns each, or for more tokens in one of 128.
+    const bool wide = T == 2 && half_tokens > 32;
+    const uint32_t bufs = wide ? 1 : 2, term = T == 1 ? 0 : wide ? kFewTokens : kFewTokens / 2;
 
     if (warp == 8) {
         // ------------------------------------------------------------ TMA of the tokens
@@ -174,8 +178,8 @@ __global__ void __launch_bounds__(FewCfg<MODE, BITS>::kThreads, 1)
             uint32_t it = 0, n = 0;
             bool ok = true, issued = false;
             for (int t = tile0; t < p.num_tiles && ok; t += tile_step, ++n) {
-                const uint32_t b = n & 1u;
-                if (!mbar_wait(&accempty[b], ((n >> 1) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
+                const uint32_t b = wide ? 0u : n & 1u;
+                if (!mbar_wait(&accempty[b], ((n / bufs) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem_base + b * kFewTokens;
                 for (int j = 0; j < p.stages; ++j, ++it) {
@@ -189,7 +193,8 @@ __global__ void __launch_bounds__(FewCfg<MODE, BITS>::kThreads, 1)
                     const uint32_t xs = smem_u32(smem + s * C::kXStageBytes), wa = tmem_base + C::kACol0 + a * C::kACols;
 #pragma unroll
                     for (int i = 0; i < 4 * T; ++i)
-                        mma_f16_ts_pair(d, wa + i * 8, smem_desc_k_sw128(xs + (i & 3) * 32), idesc, (j > 0 || i > 0) ? 1u : 0u);
+                        mma_f16_ts_pair(d + (i >> 2) * term, wa + i * 8, smem_desc_k_sw128(xs + (i & 3) * 32), idesc,
+                                        (j > 0 || (i & 3) > 0) ? 1u : 0u);
                     issued = true;
                     mma_commit_pair_mc(&empty[s], 0x3);
                     mma_commit_pair_mc(&aempty[a], 0x3);
@@ -288,17 +293,25 @@ __global__ void __launch_bounds__(FewCfg<MODE, BITS>::kThreads, 1)
         named_bar_sync(1, 32 * kEpiWarps);
         uint32_t n = 0;
         for (int t = tile0; t < p.num_tiles; t += tile_step, ++n) {
-            const uint32_t b = n & 1u;
+            const uint32_t b = wide ? 0u : n & 1u;
             const int first = row0_of(t) + quarter * 32;    // the warp's first row, within the piece
             const int row = p.v0 + first + lane;
             const bool live = row < p.vocab;
-            if (!__all_sync(0xffffffffu, mbar_wait(&accfull[b], (n >> 1) & 1u, abort_flag, p.status))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&accfull[b], (n / bufs) & 1u, abort_flag, p.status))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int m0 = 32 * (warp >> 2); m0 < p.M; m0 += 64) {
                 uint32_t v[32];
                 tmem_ld32(lane_base + b * kFewTokens + m0, v);
-                tmem_wait_ld();
+                if constexpr (T == 2) {
+                    uint32_t w[32];
+                    tmem_ld32(lane_base + b * kFewTokens + term + m0, w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+                } else {
+                    tmem_wait_ld();
+                }
                 const float4* rl4 = reinterpret_cast<const float4*>(rl + m0);
                 if constexpr (MODE == kVocabStats) {
                     const int m = m0 + lane;                 // the token that this lane ends up with
@@ -420,7 +433,7 @@ lowbit_status launch_few(const VocabProduct& v, cudaStream_t stream) {
     p.wtx = static_cast<uint32_t>(C::kWBytes + (BITS == 4 ? 2 : 1) * p.groups * 256);
     p.stages = static_cast<int>((K + 127) / 128 * 2);
     p.num_tiles = static_cast<int>((v.cols + 255) / 256);
-    p.evened = evened(C::kTerms, p.stages);
+    p.evened = evened(p.stages);
     p.rowmul = reinterpret_cast<const float*>(v.ws + l.rowmul);
     p.labels = q.labels;
     p.lse = q.lse;

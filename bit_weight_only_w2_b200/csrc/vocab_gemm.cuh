@@ -47,7 +47,12 @@ struct Cfg {
     static constexpr int kThreads = 32 * (kEpiWarps + (kPacked ? 3 : 2) + kDqWarps);
     static constexpr int kCols = PAIR ? 256 : 128;                // of a tile
     static constexpr int kRows = PAIR ? 256 : 128;
+    // Two accumulators in turn; or one, of each term apart: the second term's sums are 2^-11 of the first's, and adding
+    // them to those would cut twice as much off (the loss of 509 tokens against 100003 x 2560 uint4: 1.0e-6 off in the
+    // norm, apart 5.8e-7, at 411 us instead of 382).
+    static constexpr int kBufs = kTerms == 2 ? 1 : 2;
     static constexpr int kTmemCols = 2 * kCols;
+    static_assert(kTerms == 1 || PAIR, "few tokens of uint4 tables: vocab_few.cuh");
     // Stages of words: kLogits 128 rows, kVocabDx 64 (one stage of the reduction), 128 codes of each
     static constexpr int kWRows = kLogits ? 128 : 64;
     static constexpr int kWRowBytes = kPacked ? 128 * BITS / 8 : 0;
@@ -354,10 +359,9 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
             bool ok = true, issued = false;
             for (int t = tile0; t < p.num_tiles && ok; t += tile_step, ++n) {
                 const Tile tl = tile_of(t);
-                const uint32_t b = n & 1u;
-                if (!mbar_wait(&accempty[b], ((n >> 1) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
+                const uint32_t b = n % C::kBufs;
+                if (!mbar_wait(&accempty[b], ((n / C::kBufs) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t d = tmem_base + b * C::kCols;
                 for (int j = tl.j0; j < tl.j1; ++j, ++it) {
                     const uint32_t s = it % S, sb = it % SB;
                     if (!mbar_wait(&full[s], (it / S) & 1u, abort_flag, p.status) ||
@@ -374,7 +378,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                         const uint32_t bs = b0 + (i >> 2) * kOperandBytes;
                         const uint64_t ad = C::kAMn ? smem_desc_mn(as + kk * 2048, 128, 8192) : smem_desc_k_sw128(as + kk * 32);
                         const uint64_t bd = C::kBMn ? smem_desc_mn(bs + kk * 2048, 128, 8192) : smem_desc_k_sw128(bs + kk * 32);
-                        const uint32_t more = (j > tl.j0 || i > 0) ? 1u : 0u;
+                        const uint32_t d = tmem_base + (T == 2 ? i >> 2 : b) * C::kCols;
+                        const uint32_t more = (j > tl.j0 || kk > 0) ? 1u : 0u;
                         if (PAIR)
                             mma_f16_ss_pair(d, ad, bd, C::kIdesc, more);
                         else
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
         uint32_t n = 0;
         for (int t = tile0; t < p.num_tiles; t += tile_step, ++n) {
             const Tile tl = tile_of(t);
-            const uint32_t b = n & 1u;
+            const uint32_t b = n % C::kBufs;
             const int r0 = tl.m0 + quarter * 32, row = r0 + lane;
             const int c0 = tl.n0 + part * kCols;             // first column, within the piece
             const int left = p.vocab - (p.v0 + c0);          // columns of the vocabulary from there on
@@ -506,8 +511,21 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                 }
             }
             const uint32_t acc = lane_base + b * C::kCols + part * kCols;
-            if (!__all_sync(0xffffffffu, mbar_wait(&accfull[b], (n >> 1) & 1u, abort_flag, p.status))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&accfull[b], (n / C::kBufs) & 1u, abort_flag, p.status))) break;
             tc_fence_after();
+            // 32 columns of the accumulator (both terms' sums)
+            auto load32 = [&](int c, uint32_t (&v)[32]) {
+                tmem_ld32(acc + c, v);
+                if constexpr (T == 2) {
+                    uint32_t w[32];
+                    tmem_ld32(acc + C::kCols + c, w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+                } else {
+                    tmem_wait_ld();
+                }
+            };
             if constexpr (MODE == kVocabStats) {
                 if (r0 < p.M) {
                     const float rl = mul * kLog2e;
@@ -516,8 +534,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
 #pragma unroll 1
                     for (int c = 0; c < kCols; c += 32) {
                         uint32_t v[32];
-                        tmem_ld32(acc + c, v);
-                        tmem_wait_ld();
+                        load32(c, v);
                         if (left < c + 32) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
@@ -543,8 +560,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
 #pragma unroll 1
                     for (int c = 0; c < kCols; c += 32) {
                         uint32_t v[32];
-                        tmem_ld32(acc + c, v);
-                        tmem_wait_ld();
+                        load32(c, v);
                         if (left < c + 32) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
@@ -569,8 +585,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t v[32];
-                        tmem_ld32(acc + c + h * 32, v);
-                        tmem_wait_ld();
+                        load32(c + h * 32, v);
                         uint32_t o[16];
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
@@ -662,7 +677,7 @@ inline CUtensorMapSwizzle word_swizzle(int row_bytes) {
 // The tensor cores cut what they add to an accumulator off below its last bit, towards zero: a sum that grows evenly
 // over n MMA steps to l loses about 0.26 n 2^-24 l (measured for n = 32 .. 320 and all formats: 2.5e-6 l at K = 2560,
 // with a spread of a fifth of that), always to the same side. The logits are scaled up by as much.
-inline float evened(int terms, int stages) { return 1.f + 0.26f * 5.9604645e-8f * 4.f * static_cast<float>(terms * stages); }
+inline float evened(int stages) { return 1.f + 0.26f * 5.9604645e-8f * 4.f * static_cast<float>(stages); }
 // CTA pairs that the GPU holds at once.
 inline int pair_slots(const void* fn, int threads, int smem_bytes) {
     int pairs = cluster_capacity(fn, 2, threads, smem_bytes, true);
@@ -739,7 +754,7 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
         p.m_tiles = static_cast<int>((cols + C::kRows - 1) / C::kRows);
         p.n_tiles = static_cast<int>((K + C::kCols - 1) / C::kCols);
     }
-    p.evened = evened(C::kTerms, p.stages);
+    p.evened = evened(p.stages);
     int slices = 1;
     if (MODE == kVocabDx) {
         slices = l.slices < p.stages ? l.slices : p.stages;

@@ -379,7 +379,8 @@ lowbit_status lowbit_cross_entropy(int64_t M, int64_t vocab, int64_t N, int64_t 
  *   dX   bf16 [M][K], 16-byte aligned; zeros for a token without a label
  *   dW   bf16 [N][K], 16-byte aligned, or NULL (bf16 tables only, else LOWBIT_ERR_UNSUPPORTED); zeros from row
  *        `vocab` on. What X holds for a token without a label does not matter.
- * G is rounded once, to bf16 (bf16 tables, after the factor grad; for dX the values at the labels are not) or to fp16 (packed ones, before it, times 2^15:
+ * G is rounded once, to bf16 (bf16 tables, after the factor grad; for dX the values at the labels are not, and dW of up
+ * to 512 tokens takes G as two such values, 2^-16) or to fp16 (packed ones, before it, times 2^15:
  * 2^-40 absolute at the least, and infinite where exp(l - lse) passes 2, as it can with a lse that is not the
  * forward's); for dX a uint4 weight is (q - z) * s with the difference and the product rounded to fp16 (as in
  * lowbit_gemm_dx); sums are fp32; dX and dW are rounded once. */
