@@ -4,7 +4,8 @@
 //                columns and s = sum exp(l - r), and the logit of the token's label
 //   kVocabGrad   l again, and G = f (exp(l - lse) - [column = label]) in 16 bits, a piece of the columns at a time
 //   kVocabDx     dX += G W over a piece (fp32 sums in the workspace)
-//   kVocabDw     dW = G^T X, the rows of a piece
+//   kVocabDw     dW = G^T X, the rows of a piece (of few tokens with G as two bf16 values, whose products are reduced one
+//                after the other)
 //
 // W is bf16, or decoded from packed binary, ternary or uint4 words inside the kernel. Precision: bf16 tables
 // multiply bf16 x bf16; packed ones fp16 x fp16 on an exact fp16 copy of X (a power of two per row taken out),
@@ -110,6 +111,7 @@ struct Params {
     int accumulate;         // add to what acc holds
     float gscale;           // packed: the power of two in G
     int out_rows, out_cols; // kVocabGrad, kVocabDw: of what map_out covers
+    int g_terms;            // bf16 tables: 2 where G is kept as two bf16 values for dW (map_s covers the second)
     unsigned* status;
 };
 
@@ -321,10 +323,12 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                             tma_load_2d(map, &full[s], dst, x, y);
                     };
                     if (MODE == kVocabDw) {          // G [m][v], X [m][k]: 64 tokens, two boxes of 64 columns each
-                        load(&map_a, a, tl.m0, j * 64);
-                        load(&map_a, a + 8192, tl.m0 + 64, j * 64);
-                        load(&map_b, b, nb, j * 64);
-                        load(&map_b, b + 8192, nb + 64, j * 64);
+                        const int of_term = p.stages / p.g_terms, y = (j < of_term ? j : j - of_term) * 64;
+                        const CUtensorMap* map_g = j < of_term ? &map_a : &map_s;
+                        load(map_g, a, tl.m0, y);
+                        load(map_g, a + 8192, tl.m0 + 64, y);
+                        load(&map_b, b, nb, y);
+                        load(&map_b, b + 8192, nb + 64, y);
                     } else {
                         load(&map_a, a, j * 64, tl.m0);
                         if (MODE == kVocabDx && !C::kPacked) {   // W [v][k]: 64 rows
@@ -577,8 +581,12 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
             } else if constexpr (MODE == kVocabGrad || MODE == kVocabDw) {
                 const float rl = mul * kLog2e;
                 const int want = label >= 0 ? label - (p.v0 + c0) : -1;
+                // (64 columns at a time; G's second term, where it is kept, behind the first)
+                const int terms = MODE == kVocabGrad && BITS == kDense ? p.g_terms : 1;
 #pragma unroll 1
-                for (int c = 0; c < kCols; c += 64) {
+                for (int i = 0; i < kCols / 64 * terms; ++i) {
+                    const int c = (terms == 1 ? i : i >> 1) * 64;
+                    const bool second = terms == 2 && (i & 1);
                     // the staging rows are read out by the previous store
                     if (lane == 0) bulk_wait_read_all();
                     __syncwarp();
@@ -598,7 +606,11 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                                     float g = ex2(fmaf(e[k], rl, -shift));
                                     if (col == want) g -= 1.f;
                                     e[k] = label >= 0 && col < left ? g * f : 0.f;
-                                    if (BITS == kDense && col == want) p.rest[row] = e[k] - __bfloat162float(__float2bfloat16_rn(e[k]));
+                                    if (BITS == kDense && (second || col == want)) {
+                                        const float left_over = e[k] - __bfloat162float(__float2bfloat16_rn(e[k]));
+                                        if (col == want) p.rest[row] = left_over;
+                                        if (second) e[k] = fabsf(e[k]) < INFINITY ? left_over : 0.f;
+                                    }
                                 }
                             }
                             o[j / 2] = BITS == kDense ? pack_bf16x2(e[0], e[1]) : pack_f16x2(e[0], e[1]);
@@ -611,7 +623,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && r0 < p.out_rows && c0 + c < p.out_cols) {
-                        tma_store_2d(&map_out, smem + C::kStagingOff + warp * 4096, c0 + c, r0);
+                        tma_store_2d(second ? &map_s : &map_out, smem + C::kStagingOff + warp * 4096, c0 + c, r0);
                         bulk_commit_group();
                     }
                 }
@@ -728,6 +740,8 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
         if (MODE == kVocabGrad) ok = ok && make_map_2d(&mo, half, 2, g, ld, M, ld * 2, 64, 32, sw);
     }
     if (!C::kPacked) ms = mb;
+    if (BITS == kDense && l.g_terms == 2 && (MODE == kVocabGrad || MODE == kVocabDw))
+        ok = ok && make_map_2d(&ms, half, 2, v.ws + l.g + M * ld * 2, ld, M, ld * 2, 64, MODE == kVocabDw ? 64 : 32, sw);
     if (BITS != 4) mz = ms;
     Params p = {};
     p.status = device_status_address();
@@ -750,7 +764,7 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
         p.m_tiles = static_cast<int>(l.m_tiles);
         p.n_tiles = static_cast<int>(l.dx_tiles);
     } else {
-        p.stages = static_cast<int>((M + 63) / 64);
+        p.stages = static_cast<int>((M + 63) / 64) * l.g_terms;
         p.m_tiles = static_cast<int>((cols + C::kRows - 1) / C::kRows);
         p.n_tiles = static_cast<int>((K + C::kCols - 1) / C::kCols);
     }
@@ -774,6 +788,7 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
     p.acc = reinterpret_cast<float4*>(v.ws + l.acc);
     p.accumulate = v.first ? 0 : 1;
     p.gscale = 32768.f;
+    p.g_terms = l.g_terms;
     p.out_rows = static_cast<int>(rows);
     p.out_cols = static_cast<int>(MODE == kVocabDw ? K : ld);
 

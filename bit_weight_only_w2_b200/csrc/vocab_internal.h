@@ -37,7 +37,7 @@ struct LossProblem {
 // Workspace of the loss, offsets in bytes (each part 256-byte aligned), and the choices made with it:
 //   forward   xh (with rowmul behind it, packed tables only), target [M], part [parts][M] (float2);
 //             small: logits [M][N] fp32
-//   backward  xh, xz (the tokens with a label, dW only), rest [M] (bf16 tables), g [M][piece], acc (fp32 tiles of dX)
+//   backward  xh, xz (the tokens with a label, dW only), rest [M] (bf16 tables), g [g_terms][M][piece], acc (fp32 tiles of dX)
 struct LossLayout {
     bool small;              // up to 16 tokens, packed: fp32 logits by the small-M kernel
     bool pair;               // tiles of 256 tokens x 256 columns on CTA pairs, else 128 x 128 (logits of a packed table:
@@ -46,6 +46,7 @@ struct LossLayout {
     int64_t parts;           // forward: (maximum, sum) of each token that the tiles leave
     int64_t piece;           // columns of G formed at a time
     int64_t dx_tiles;        // tiles of dX in the columns' direction
+    int g_terms;             // bf16 values that G is kept as
     int slices;              // slices of a piece whose products are summed apart
     size_t xh, rowmul, logits, target, part, xz, rest, g, acc, total;
 };

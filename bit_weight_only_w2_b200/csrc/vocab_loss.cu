@@ -15,6 +15,9 @@ constexpr int64_t kTokensAtOnce = 16384;              // forward: tokens whose t
 // Backward: bytes of G formed at a time. dX's sums are read and written once a piece: 4096 tokens against 131072 x 2560
 // take 6.33 ms with 256 MB, 6.44 with 128 and 6.75 with 64.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
+// dW of so few tokens takes G as two bf16 values: a row of dW that one token makes up shows G's rounding as much as its
+// own (3 tokens: 3.5e-3 off in the norm, with two 1.9e-3, its own rounding), and writing dW bounds the time anyway.
+constexpr int64_t kTwoTermTokens = 512;
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
@@ -331,7 +334,8 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
         return l;
     }
     const int64_t whole = up(vocab, 256), tokens = M > 0 ? M : 1;
-    int64_t most = kPieceBytes / (2 * tokens) / 256 * 256;
+    l.g_terms = need_dw && M <= kTwoTermTokens ? 2 : 1;
+    int64_t most = kPieceBytes / (2 * l.g_terms * tokens) / 256 * 256;
     if (most < 256) most = 256;
     const int64_t pieces = (vocab + most - 1) / most;
     l.piece = up((vocab + pieces - 1) / pieces, 256);
@@ -351,8 +355,13 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
     l.slices = static_cast<int>((stages + per - 1) / per);   // (no empty ones; a shorter last piece never has more)
     // G and the sums take room that grows with M, so that a workspace for M tokens serves fewer too.
     const size_t tile = static_cast<size_t>(side) * side * 4;
-    size_t g = static_cast<size_t>(kPieceBytes) > static_cast<size_t>(tokens) * 512 ? kPieceBytes : static_cast<size_t>(tokens) * 512;
-    if (g > static_cast<size_t>(tokens) * whole * 2) g = static_cast<size_t>(tokens) * whole * 2;
+    auto g_bytes = [&](int64_t m, int64_t terms) {
+        const int64_t value = 2 * terms, least = m * 256 * value, all = m * whole * value;
+        const int64_t some = kPieceBytes > least ? kPieceBytes : least;
+        return static_cast<size_t>(some < all ? some : all);
+    };
+    size_t g = g_bytes(tokens, l.g_terms);
+    if (need_dw && tokens > kTwoTermTokens && g < g_bytes(kTwoTermTokens, 2)) g = g_bytes(kTwoTermTokens, 2);
     size_t acc = 8 * slots * tile < 64 * tiles * tile ? 8 * slots * tile : 64 * tiles * tile;
     if (acc < tiles * tile) acc = tiles * tile;
     if (bits == kDense) l.rest = take(static_cast<size_t>(M) * 4);

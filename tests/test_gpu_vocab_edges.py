@@ -530,3 +530,26 @@ def test_the_label_is_most_of_the_gradient(M, K, V):
     sums = f * (w.sum(0) / V * 2 + w[ref.label])
     e = HB16 * f * 2 / V * w.sum(0) + (V + 16) * H32 * sums + 2.0 ** -20 * f * w[ref.label]
     check(dx, rx, e + HB16 * (rx.abs() + e), "dx")
+
+
+@pytest.mark.parametrize("M,K,V", [(1, 128, 1000), (3, 264, 5003), (65, 128, 999), (512, 136, 2000)])
+def test_dw_of_few_tokens(M, K, V):
+    """G enters dW as two bf16 values, so a row that one token makes up is off by its own rounding: p's error in fp32 (as
+    Loss counts it), 2^-16 of G, fp32 sums of 2 M products, and one rounding."""
+    table = Table(V, K, 16)
+    x, labels, grad = inputs(M, K, V)
+    lse = lb.cross_entropy(x, labels, *table.args())[1]
+    _, dw = lb.cross_entropy_backward(grad, x, labels, lse, *table.args(), need_dw=True)
+    ref = Loss(x, labels, table, V)
+    l = lse.double()[:, None]
+    p = (ref.l - l).exp()
+    hot = torch.zeros_like(p)
+    hot[torch.arange(M, device="cuda"), ref.label] = 1.0
+    f = torch.where(ref.valid, grad, 0.0).double()[:, None]
+    G = f * (p - hot)
+    ep = p * torch.expm1(1.01 * (ref.el + 1.4427 * 3 * (ref.l.abs() + l.abs()) * H32) + 2.0 ** -21) + H32
+    eG = 1.01 * f.abs() * ep + (2.0 ** -16 + 2 * H32) * G.abs()
+    xs = torch.where(ref.valid[:, None], x.double(), 0.0)
+    want = G.T @ xs
+    e = eG.T @ xs.abs() + (2 * M + 16) * H32 * (G.abs().T @ xs.abs())
+    check(dw, want, e + HB16 * (want.abs() + e), "dw")
