@@ -3,10 +3,11 @@
 // tensor memory as the MMA's first operand and never through shared memory. With the tokens on the lanes a stage of 64
 // columns moved 16 KB of decoded weights into shared memory and 32 KB out of it for the MMA, which took 700 clocks (ternary;
 // uint4, of two terms, 1000) where the MMAs need 256. Here shared memory holds the tokens only, half of them in each CTA,
-// and a stage takes 500 (840): 77 tokens against 32768 x 2560 uint4 in 45 us with all launches (53 before), 16 to 25 %
-// of what memory and tensor cores would allow. It is the decoding warps' chain of waits and latencies that is left, not
-// the MMAs (one instead of four a stage: 450 clocks), the barriers (half as many: the same) nor the width of the loads of
-// words (128 bytes of a row at a time: the same). Without the decoding's arithmetic a uint4 stage takes 515.
+// and a stage takes 500 (840): 77 tokens against 32768 x 2560 uint4 in 45 us with all launches (53 before; 48 with the
+// terms' sums apart), a sixth of what memory and tensor cores would allow. It is the decoding warps' chain of waits and
+// latencies that is left, not the MMAs (one instead of four a stage: 450 clocks), the barriers (half as many: the same)
+// nor the width of the loads of words (128 bytes of a row at a time: the same). Without the decoding's arithmetic a uint4
+// stage takes 515.
 //
 //   * warp 8 (one lane): TMA of the CTA's half of the tokens, 64 columns a stage;
 //   * warp 10 (one lane): TMA of the words and scales of its 128 rows x 128 columns;
