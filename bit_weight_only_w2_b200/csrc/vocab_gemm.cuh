@@ -173,9 +173,11 @@ struct Row64 {
         if (BITS == 4) {
             zh2 = z | (static_cast<uint32_t>(z) << 16);
             if (TERMS == 2) {
-                // z = zh + zl, both exact, with zh so coarse (2^-6 up to |z| = 8, then by |z|) that q - zh is exact in
-                // fp16: (z + 24) - 24 rounds z to the step of fp16 at 16 .. 32. (Beyond 2^14 zh = z.)
-                constexpr uint32_t k24 = 0x4E004E00u;
+                // z = zh + zl, both exact, with zh of the step that fp16 has at |z| + 24 (2^-6 up to |z| = 8), so that
+                // q - zh, at most |z| + 15.5, is exact in fp16 as long as that step is at most 1 (|z| <= 2000): adding 24 of
+                // z's own sign and taking it off again rounds z to it. (With 24 of one sign a z below -8 kept its finer
+                // step, and q - z was rounded: 2^-7 of the scale at -9.0078.) From 2^14 on zh = z.
+                const uint32_t k24 = 0x4E004E00u | (zh2 & 0x80008000u);
                 const uint32_t zr = f16x2_sub(f16x2_fma(zh2, 0x3C003C00u, k24), k24);
                 const uint32_t rest = f16x2_sub(zr, zh2);   // -zl
                 const bool coarse = (z & 0x7FFFu) < 0x7400u;
@@ -202,7 +204,8 @@ struct Row64 {
                 const uint32_t e = and_or(words[4 * (c >> 2) + q] >> (k < 2 ? 0 : 8), 0x000F000Fu << (4 * (k & 1)), kMagic);
                 const uint32_t d = f16x2_sub(f16x2_fma(e, kMul[2 * (k & 1)], kAdd4[k & 1]), zh2);
                 hi[q] = f16x2_mul(d, s2);
-                // d s = hi + (d s - hi), the second exact in fp16 (above its smallest step), and (q - z) s = d s - zl s
+                // d s = hi + (d s - hi), the second exact in fp16 (above its smallest step), and (q - z) s = d s - zl s:
+                // |lo| <= 2^-11 (|d| + |z| + 24) s, rounded once (its parts below fp16's normal range: 2^-24)
                 if (TERMS == 2) lo[q] = f16x2_fma(zl2, s2, f16x2_fma(d, s2, hi[q] ^ 0x80008000u));
             }
         }

@@ -367,8 +367,9 @@ lowbit_status lowbit_checkpoint_load(const uint8_t* codes, const uint8_t* exps, 
 size_t lowbit_cross_entropy_workspace_size(int64_t M, int64_t vocab, int64_t K, int bits, int backward);
 
 /* loss fp32 [M] and lse fp32 [M] of X bf16 [M][K] (16-byte aligned). Sums are fp32. A packed table's weights are the
- * values that lowbit_gemm decodes, a uint4 weight as the sum of two fp16 values (2^-17 of its scale, 2^-25 absolute
- * at the least; zeros up to 2^14 in magnitude), or up to 16 tokens as q - 8 and z - 8, multiplied apart; so the loss is
+ * values that lowbit_gemm decodes, a uint4 weight as the sum of two fp16 values (off by at most
+ * 2^-22 (|q - z| + |z| + 25) of its scale, which is 2^-17 for zeros within 0 .. 15, and 2^-24 absolute; where |z| passes 2000,
+ * as in lowbit_gemm, 2^-10 of itself), or up to 16 tokens as q - 8 and z - 8, multiplied apart; so the loss is
  * good to fp32 sums of K products. A row of X with an infinity or NaN has a lse and loss that are not finite; other rows
  * are not touched by it. 1 <= vocab <= N (else LOWBIT_ERR_INVALID_ARG). */
 lowbit_status lowbit_cross_entropy(int64_t M, int64_t vocab, int64_t N, int64_t K, int bits, int group_size, const void* X,
