@@ -4,8 +4,8 @@
 //                columns and s = sum exp(l - r), and the logit of the token's label
 //   kVocabGrad   l again, and G = f (exp(l - lse) - [column = label]) in 16 bits, a piece of the columns at a time
 //   kVocabDx     dX += G W over a piece (fp32 sums in the workspace)
-//   kVocabDw     dW = G^T X, the rows of a piece (of few tokens with G as two bf16 values, whose products are reduced one
-//                after the other)
+//   kVocabDw     dW = G^T X, the rows of a piece, with G as two bf16 values, whose products are reduced one after the other:
+//                of few tokens everywhere, of more where a label makes a block of 64 tokens by 256 rows (vocab_loss.cu)
 //
 // W is bf16, or decoded from packed binary, ternary or uint4 words inside the kernel. Precision: bf16 tables
 // multiply bf16 x bf16; packed ones fp16 x fp16 on an exact fp16 copy of X (a power of two per row taken out),
@@ -112,6 +112,9 @@ struct Params {
     float gscale;           // packed: the power of two in G
     int out_rows, out_cols; // kVocabGrad, kVocabDw: of what map_out covers
     int g_terms;            // bf16 tables: 2 where G is kept as two bf16 values for dW (map_s covers the second)
+    int of_term;            // kVocabDw: stages of G's first term
+    const uint32_t* marks;  // [rows / 256][mark_words]: a bit per 64 tokens whose second term is kept; nullptr: all
+    int mark_words;
     unsigned* status;
 };
 
@@ -212,6 +215,22 @@ struct Row64 {
     }
 };
 
+// The stages of a tile of dW behind those of G's first term: of its second, 64 tokens each, where `marks` has a bit.
+struct MarkedStages {
+    const uint32_t* marks = nullptr;   // of the tile's 256 rows
+    int words = 0, next_word = 0;
+    uint32_t left = 0;
+    __device__ __forceinline__ int next() {   // the next one's tokens / 64, or -1
+        while (!left) {
+            if (next_word == words) return -1;
+            left = marks[next_word++];
+        }
+        const int bit = __ffs(left) - 1;
+        left &= left - 1;
+        return 32 * (next_word - 1) + bit;
+    }
+};
+
 template <int MODE, int BITS, bool PAIR>
 __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
     vocab_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -303,6 +322,21 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
         r.j1 = min(p.stages, r.j0 + p.per_slice);
         return r;
     };
+    auto marked_of = [&](const Tile& tl) {
+        MarkedStages w;
+        if (MODE == kVocabDw && p.marks) {
+            w.marks = p.marks + static_cast<size_t>((p.v0 + tl.m0) / 256) * p.mark_words;
+            w.words = p.mark_words;
+        }
+        return w;
+    };
+    // The stage after j of a tile (those of G's second term count on behind the first's), or -1.
+    auto stage_after = [&](int j, const Tile& tl, MarkedStages& marked) {
+        if (j + 1 < tl.j1) return j + 1;
+        if (MODE != kVocabDw) return -1;
+        const int s = marked.next();
+        return s < 0 ? -1 : p.of_term + s;
+    };
 
     if (warp == 8) {
         // ------------------------------------------------------------ TMA of the rows' operand, and of a bf16 table
@@ -313,7 +347,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
             for (int t = tile0; t < p.num_tiles && ok; t += tile_step) {
                 const Tile tl = tile_of(t);
                 const int nb = tl.n0 + static_cast<int>(rank) * 128;   // first of this CTA's half of the columns
-                for (int j = tl.j0; j < tl.j1; ++j, ++it) {
+                MarkedStages marked = marked_of(tl);
+                for (int j = tl.j0; j >= 0; j = stage_after(j, tl, marked), ++it) {
                     const uint32_t s = it % S;
                     if (!mbar_wait(&empty[s], ((it / S) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     uint8_t* a = smem + s * C::kAStageBytes;
@@ -326,8 +361,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                             tma_load_2d(map, &full[s], dst, x, y);
                     };
                     if (MODE == kVocabDw) {          // G [m][v], X [m][k]: 64 tokens, two boxes of 64 columns each
-                        const int of_term = p.stages / p.g_terms, y = (j < of_term ? j : j - of_term) * 64;
-                        const CUtensorMap* map_g = j < of_term ? &map_a : &map_s;
+                        const int y = (j < p.of_term ? j : j - p.of_term) * 64;
+                        const CUtensorMap* map_g = j < p.of_term ? &map_a : &map_s;
                         load(map_g, a, tl.m0, y);
                         load(map_g, a + 8192, tl.m0 + 64, y);
                         load(&map_b, b, nb, y);
@@ -369,7 +404,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                 const uint32_t b = n % C::kBufs;
                 if (!mbar_wait(&accempty[b], ((n / C::kBufs) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
                 tc_fence_after();
-                for (int j = tl.j0; j < tl.j1; ++j, ++it) {
+                MarkedStages marked = marked_of(tl);
+                for (int j = tl.j0; j >= 0; j = stage_after(j, tl, marked), ++it) {
                     const uint32_t s = it % S, sb = it % SB;
                     if (!mbar_wait(&full[s], (it / S) & 1u, abort_flag, p.status) ||
                         (C::kPacked && !mbar_wait(&bfull[sb], (it / SB) & 1u, abort_flag, p.status))) {
@@ -508,6 +544,9 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
             // what the token needs, requested before the accumulator is waited for
             [[maybe_unused]] int label = -1;
             [[maybe_unused]] float mul = 1.f, shift = 0.f, f = 0.f;
+            [[maybe_unused]] uint32_t marks = 0xffffffffu;   // (a tile's columns are 256 rows of dW)
+            if (MODE == kVocabGrad && BITS == kDense && PAIR && p.marks && r0 < p.M)
+                marks = p.marks[static_cast<size_t>((p.v0 + tl.n0) / 256) * p.mark_words + r0 / 2048];
             if (C::kLogits && row < p.M) {
                 label = p.labels[row];
                 if (static_cast<unsigned>(label) >= static_cast<unsigned>(p.vocab)) label = -1;
@@ -585,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BITS, PAIR>::kThreads, 1)
                 const float rl = mul * kLog2e;
                 const int want = label >= 0 ? label - (p.v0 + c0) : -1;
                 // (64 columns at a time; G's second term, where it is kept, behind the first)
-                const int terms = MODE == kVocabGrad && BITS == kDense ? p.g_terms : 1;
+                const int terms = MODE == kVocabGrad && BITS == kDense ? (((marks >> (r0 / 64 % 32)) & 1u) ? p.g_terms : 1) : 1;
 #pragma unroll 1
                 for (int i = 0; i < kCols / 64 * terms; ++i) {
                     const int c = (terms == 1 ? i : i >> 1) * 64;
@@ -767,7 +806,8 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
         p.m_tiles = static_cast<int>(l.m_tiles);
         p.n_tiles = static_cast<int>(l.dx_tiles);
     } else {
-        p.stages = static_cast<int>((M + 63) / 64) * l.g_terms;
+        p.of_term = static_cast<int>((M + 63) / 64);
+        p.stages = p.of_term * (l.mark_words ? 1 : l.g_terms);
         p.m_tiles = static_cast<int>((cols + C::kRows - 1) / C::kRows);
         p.n_tiles = static_cast<int>((K + C::kCols - 1) / C::kCols);
     }
@@ -792,6 +832,8 @@ lowbit_status launch(const VocabProduct& v, cudaStream_t stream) {
     p.accumulate = v.first ? 0 : 1;
     p.gscale = 32768.f;
     p.g_terms = l.g_terms;
+    p.marks = l.mark_words ? reinterpret_cast<const uint32_t*>(v.ws + l.marks) : nullptr;
+    p.mark_words = static_cast<int>(l.mark_words);
     p.out_rows = static_cast<int>(rows);
     p.out_cols = static_cast<int>(MODE == kVocabDw ? K : ld);
 

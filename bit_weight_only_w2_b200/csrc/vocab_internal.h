@@ -37,7 +37,8 @@ struct LossProblem {
 // Workspace of the loss, offsets in bytes (each part 256-byte aligned), and the choices made with it:
 //   forward   xh (with rowmul behind it, packed tables only), target [M], part [parts][M] (float2);
 //             small: logits [M][N] fp32
-//   backward  xh, xz (the tokens with a label, dW only), rest [M] (bf16 tables), g [g_terms][M][piece], acc (fp32 tiles of dX)
+//   backward  xh, xz (the tokens with a label, dW only), marks [rows / 256][M / 2048] (dW of many tokens), rest [M] (bf16
+//             tables), g [g_terms][M][piece], acc (fp32 tiles of dX)
 struct LossLayout {
     bool small;              // up to 16 tokens, packed: fp32 logits by the small-M kernel
     bool pair;               // tiles of 256 tokens x 256 columns on CTA pairs, else 128 x 128 (logits of a packed table:
@@ -48,7 +49,8 @@ struct LossLayout {
     int64_t dx_tiles;        // tiles of dX in the columns' direction
     int g_terms;             // bf16 values that G is kept as
     int slices;              // slices of a piece whose products are summed apart
-    size_t xh, rowmul, logits, target, part, xz, rest, g, acc, total;
+    int64_t mark_words;      // words of marks per 256 rows of the table; 0: G's second term is taken everywhere
+    size_t xh, rowmul, logits, target, part, xz, marks, rest, g, acc, total;
 };
 constexpr int64_t kSmallTokens = 16;
 LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backward, bool need_dw);

@@ -12,11 +12,16 @@ namespace lowbit {
 namespace {
 
 constexpr int64_t kTokensAtOnce = 16384;              // forward: tokens whose tiles' sums are kept at a time
-// Backward: bytes of G formed at a time. dX's sums are read and written once a piece: 4096 tokens against 131072 x 2560
-// take 6.33 ms with 256 MB, 6.44 with 128 and 6.75 with 64.
+// Backward: bytes of a term of G formed at a time. dX's sums are read and written once a piece: 4096 tokens against
+// 131072 x 2560 took 6.33 ms with 256 MB, 6.44 with 128 and 6.75 with 64 (of one term).
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
-// dW of so few tokens takes G as two bf16 values: a row of dW that one token makes up shows G's rounding as much as its
-// own (3 tokens: 3.5e-3 off in the norm, with two 1.9e-3, its own rounding), and writing dW bounds the time anyway.
+// dW takes G as two bf16 values at the labels, where one of them makes up most of a row of dW and would show its rounding as
+// much as the row's own (3 tokens: 3.5e-3 off in the norm, with two 1.9e-3), and where that rounding is the same for all
+// tokens: with the mean over 900 labels (G near -1 / 900) all of dW came out 2.5e-3 too large and 3.0e-3 off in the norm, with
+// two terms 1.66e-3, its own rounding. So of many tokens G's second term is kept for the blocks of 64 tokens by 256 rows that
+// hold a label, marked beforehand: 16384 / rows more products for dW at most, and never twice as many (both gradients of
+// 4096 tokens against 131072 x 2560: 6.26 ms without, 6.36 with). Up to this many tokens, where writing dW bounds the time
+// anyway, all blocks have it.
 constexpr int64_t kTwoTermTokens = 512;
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
@@ -165,14 +170,21 @@ __global__ void __cluster_dims__(kRowCtas, 1, 1) __launch_bounds__(kRowThreads)
     }
 }
 
-// X with zeros in the rows of tokens without a label, which have no part in dW whatever they hold.
+// X with zeros in the rows of tokens without a label, which have no part in dW whatever they hold; and for each token with
+// one the mark of its block (an OR: the same whatever the order).
 __global__ void __launch_bounds__(256) keep_labelled_kernel(const uint4* __restrict__ X, const int32_t* __restrict__ labels, int vocab,
-                                                            int64_t count, int K8, uint4* __restrict__ out) {
+                                                            int64_t count, int K8, uint4* __restrict__ out,
+                                                            uint32_t* __restrict__ marks, int mark_words) {
     grid_launch_dependents();
     grid_dependency_wait();
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < count; i += int64_t(gridDim.x) * 256) {
         const uint4 v = X[i];
-        out[i] = static_cast<unsigned>(labels[i / K8]) < static_cast<unsigned>(vocab) ? v : make_uint4(0, 0, 0, 0);
+        const int64_t m = i / K8;
+        const int label = labels[m];
+        const bool has = static_cast<unsigned>(label) < static_cast<unsigned>(vocab);
+        out[i] = has ? v : make_uint4(0, 0, 0, 0);
+        if (marks && has && i == m * K8)
+            atomicOr(marks + static_cast<size_t>(label / 256) * mark_words + m / 2048, 1u << (m / 64 % 32));
     }
 }
 
@@ -295,6 +307,9 @@ lowbit_status copy_x(const LossProblem& p, const LossLayout& l, uint8_t* ws, cud
     return launch_convert_x(g, stream);
 }
 
+// Marks of a whole table: bits of 64 tokens, words of 2048, by 256 rows.
+size_t mark_bytes(const LossLayout& l, int64_t vocab) { return static_cast<size_t>((vocab + 255) / 256) * l.mark_words * 4; }
+
 }  // namespace
 
 LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backward, bool need_dw) {
@@ -334,8 +349,8 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
         return l;
     }
     const int64_t whole = up(vocab, 256), tokens = M > 0 ? M : 1;
-    l.g_terms = need_dw && M <= kTwoTermTokens ? 2 : 1;
-    int64_t most = kPieceBytes / (2 * l.g_terms * tokens) / 256 * 256;
+    l.g_terms = need_dw ? 2 : 1;
+    int64_t most = kPieceBytes / (2 * tokens) / 256 * 256;
     if (most < 256) most = 256;
     const int64_t pieces = (vocab + most - 1) / most;
     l.piece = up((vocab + pieces - 1) / pieces, 256);
@@ -355,17 +370,16 @@ LossLayout loss_layout(int64_t M, int64_t vocab, int64_t K, int bits, bool backw
     l.slices = static_cast<int>((stages + per - 1) / per);   // (no empty ones; a shorter last piece never has more)
     // G and the sums take room that grows with M, so that a workspace for M tokens serves fewer too.
     const size_t tile = static_cast<size_t>(side) * side * 4;
-    auto g_bytes = [&](int64_t m, int64_t terms) {
-        const int64_t value = 2 * terms, least = m * 256 * value, all = m * whole * value;
-        const int64_t some = kPieceBytes > least ? kPieceBytes : least;
-        return static_cast<size_t>(some < all ? some : all);
-    };
-    size_t g = g_bytes(tokens, l.g_terms);
-    if (need_dw && tokens > kTwoTermTokens && g < g_bytes(kTwoTermTokens, 2)) g = g_bytes(kTwoTermTokens, 2);
+    const int64_t least = tokens * 256 * 2, all = tokens * whole * 2, some = kPieceBytes > least ? kPieceBytes : least;
+    const size_t g = static_cast<size_t>(some < all ? some : all) * l.g_terms;
     size_t acc = 8 * slots * tile < 64 * tiles * tile ? 8 * slots * tile : 64 * tiles * tile;
     if (acc < tiles * tile) acc = tiles * tile;
     if (bits == kDense) l.rest = take(static_cast<size_t>(M) * 4);
     if (need_dw) l.xz = take(static_cast<size_t>(M) * K * 2);
+    if (need_dw && M > kTwoTermTokens) {
+        l.mark_words = (M + 2047) / 2048;
+        l.marks = take(mark_bytes(l, vocab));
+    }
     l.g = take(g);
     l.acc = take(acc);
     l.total = at;
@@ -432,9 +446,12 @@ lowbit_status loss_backward(const LossProblem& p, const LossLayout& l, uint8_t* 
             cudaMemsetAsync(static_cast<uint8_t*>(p.dW) + static_cast<size_t>(p.vocab) * K * 2, 0,
                             static_cast<size_t>(p.table.N - p.vocab) * K * 2, stream) != cudaSuccess)
             return LOWBIT_ERR_CUDA;
+        uint32_t* marks = l.mark_words ? reinterpret_cast<uint32_t*>(ws + l.marks) : nullptr;
+        if (marks && cudaMemsetAsync(marks, 0, mark_bytes(l, p.vocab), stream) != cudaSuccess) return LOWBIT_ERR_CUDA;
         const int64_t count = p.M * (K / 8), blocks = (count + 255) / 256;
         st = launch_after(keep_labelled_kernel, blocks < 148 * 8 ? blocks : 148 * 8, 1, 256, stream, static_cast<const uint4*>(p.X), p.labels,
-                          static_cast<int>(p.vocab), count, static_cast<int>(K / 8), reinterpret_cast<uint4*>(ws + l.xz));
+                          static_cast<int>(p.vocab), count, static_cast<int>(K / 8), reinterpret_cast<uint4*>(ws + l.xz),
+                          marks, static_cast<int>(l.mark_words));
         if (st != LOWBIT_OK) return st;
     }
     int slices = l.slices;   // of a whole piece: the buffers that every piece adds to

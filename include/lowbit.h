@@ -362,8 +362,8 @@ lowbit_status lowbit_checkpoint_load(const uint8_t* codes, const uint8_t* exps, 
  * or another output; a workspace belongs to one call until its work on the GPU is done. */
 
 /* Bytes of workspace of lowbit_cross_entropy (backward = 0) and lowbit_cross_entropy_backward (1, or 2 where dW is
- * wanted), for M tokens or any fewer. The backward's holds up to 256 MB of G (at least 256 columns of it) and fp32
- * sums of dX. 0 for invalid arguments. */
+ * wanted), for M tokens or any fewer. The backward's holds up to 256 MB of G (at least 256 columns of it; twice that
+ * with dW) and fp32 sums of dX. 0 for invalid arguments. */
 size_t lowbit_cross_entropy_workspace_size(int64_t M, int64_t vocab, int64_t K, int bits, int backward);
 
 /* loss fp32 [M] and lse fp32 [M] of X bf16 [M][K] (16-byte aligned). Sums are fp32. A packed table's weights are the
@@ -380,8 +380,9 @@ lowbit_status lowbit_cross_entropy(int64_t M, int64_t vocab, int64_t N, int64_t 
  *   dX   bf16 [M][K], 16-byte aligned; zeros for a token without a label
  *   dW   bf16 [N][K], 16-byte aligned, or NULL (bf16 tables only, else LOWBIT_ERR_UNSUPPORTED); zeros from row
  *        `vocab` on. What X holds for a token without a label does not matter.
- * G is rounded once, to bf16 (bf16 tables, after the factor grad; for dX the values at the labels are not, and dW of up
- * to 512 tokens takes G as two such values, 2^-16) or to fp16 (packed ones, before it, times 2^15:
+ * G is rounded once, to bf16 (bf16 tables, after the factor grad; the values at the labels are not: dX takes them as they
+ * are, and dW as two such values, 2^-16, as it does all of G of up to 512 tokens, and of more in the blocks of 64 tokens by
+ * 256 rows with a label) or to fp16 (packed ones, before it, times 2^15:
  * 2^-40 absolute at the least, and infinite where exp(l - lse) passes 2, as it can with a lse that is not the
  * forward's); for dX a uint4 weight is (q - z) * s with the difference and the product rounded to fp16 (as in
  * lowbit_gemm_dx); sums are fp32; dX and dW are rounded once. */

@@ -5,7 +5,7 @@ import torch
 
 import bit_weight_only_w2_b200 as lb
 from tests._adapters import check
-from tests._vocab import Loss, Table
+from tests._vocab import H32, HB16, Loss, Table
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,48 @@ def test_weights_of_one_zero(M, z):
     weight = 2.0 ** -3 * (2.0 ** -22 * ((q - z).abs() + abs(z) + 25) + 2.0 ** -24)
     # the sum's own rounding and what scales it (2^-24 of 8 steps), lse and loss in fp32
     check(target, want, weight + 2.0 ** -24 * (8 * want.abs() + 2 * lse.double().abs() + 2 * loss.double().abs()), "target")
+
+
+def half_step(v):
+    """Half a step of bf16 at v >= 0."""
+    return torch.exp2(torch.floor(torch.log2(v.clamp_min(2.0 ** -126))) - 8)
+
+
+@pytest.mark.parametrize("M,K,N,V,labelled,repeat", [
+    (513, 128, 4000, 4000, 513, 1), (1024, 256, 20000, 20000, 900, 1), (1024, 136, 20000, 19999, 1020, 2), (2049, 72, 9000, 8990, 900, 3),
+    (4133, 128, 70000, 70000, 4097, 1), (1500, 64, 300, 290, 1111, 1), (700, 128, 5000, 4099, 3, 1), (640, 64, 260, 257, 0, 1)])
+def test_dw_of_many_tokens(M, K, N, V, labelled, repeat):
+    """The mean over the labelled tokens, a factor that bf16 does not hold: at the labels G is -1 / labelled and a little, and
+    enters dW as two bf16 values, so a row that a label makes up is off by its own rounding (half a step, taken exactly). Nothing
+    else of G is larger than 2 / V of that, and is rounded to 2^-8; p's error as Loss counts it; fp32 sums of 2 M products."""
+    table = Table(N, K, 16, norm=1.0)
+    g = torch.Generator(device="cuda").manual_seed(M + V)
+    x = (torch.randn(M, K, generator=g, device="cuda") / 64).bfloat16()     # tokens that know nothing: p near 1 / V
+    labels = torch.randint(0, max(V // repeat, 1), (M,), generator=g, device="cuda", dtype=torch.int32)
+    out = torch.randperm(M, generator=g, device="cuda")[labelled:]
+    labels[out] = torch.tensor([-100, V, 2 ** 31 - 1], device="cuda", dtype=torch.int32).repeat(M)[:len(out)]
+    x[out[:5]] = float("nan")
+    grad = torch.full((M,), 1.0 / max(labelled, 1), device="cuda")
+    lse = lb.cross_entropy(x, labels, *table.args(), vocab=V)[1]
+    dx, dw = lb.cross_entropy_backward(grad, x, labels, lse, *table.args(), vocab=V, need_dw=True)
+    torch.cuda.synchronize()
+    assert lb.device_status() == 0
+    x = torch.where(((labels >= 0) & (labels < V))[:, None], x, 0.0).bfloat16()
+    ref = Loss(x, labels, table, V)
+    l = torch.where(ref.valid, lse, 0.0).double()[:, None]
+    p = torch.where(ref.valid[:, None], (ref.l - l).exp(), 0.0)
+    assert p.max() <= 2 / V
+    hot = torch.zeros_like(p)
+    hot[torch.arange(M, device="cuda"), ref.label] = 1.0
+    f = torch.where(ref.valid, grad, 0.0).double()[:, None]
+    G = f * (p - hot)
+    ep = p * torch.expm1(1.01 * (ref.el + 1.4427 * 3 * (ref.l.abs() + l.abs()) * H32) + 2.0 ** -21) + H32
+    eG = 1.01 * f * ep + torch.where(hot > 0, 2.0 ** -16 + 2 * H32, HB16 + 2 * H32) * G.abs()
+    want = G.T @ x.double()
+    e = eG.T @ x.double().abs() + (2 * M + 16) * H32 * (G.abs().T @ x.double().abs())
+    check(dw[:V], want, e + half_step(want.abs() + e), "dw")
+    assert not dw[V:].any() and not dx[out].any()
+    (rx, ex), _ = ref.gradients(torch.where(ref.valid, grad, 0.0), torch.where(ref.valid, lse, 0.0))
+    check(dx, rx, ex, "dx")
+    again = lb.cross_entropy_backward(grad, torch.where(ref.valid[:, None], x, 7.0), labels, lse, *table.args(), vocab=V, need_dw=True)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
