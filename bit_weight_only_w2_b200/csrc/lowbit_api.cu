@@ -77,8 +77,7 @@ lowbit_status validate_gemm(const GemmProblem& g) {
     if (g.group_size != 64 && g.group_size != 128) return LOWBIT_ERR_UNSUPPORTED;
     if (g.bits == 1 && g.K % 128 != 0) return LOWBIT_ERR_UNSUPPORTED;
     if (g.N % 8 != 0) return LOWBIT_ERR_UNSUPPORTED;
-    if (g.M >= (int64_t(1) << 31) || g.N >= (int64_t(1) << 31) || g.K >= (int64_t(1) << 31))
-        return LOWBIT_ERR_UNSUPPORTED;
+    if (g.M > kMaxExtent || g.N > kMaxExtent || g.K > kMaxExtent) return LOWBIT_ERR_UNSUPPORTED;
     if (!g.workspace || (reinterpret_cast<uintptr_t>(g.workspace) & 255u) != 0 ||
         g.workspace_bytes < workspace_layout(g.M, g.K).total)
         return LOWBIT_ERR_WORKSPACE;

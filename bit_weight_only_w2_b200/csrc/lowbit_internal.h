@@ -33,6 +33,10 @@ inline WorkspaceLayout workspace_layout(int64_t M, int64_t K) {
     return WorkspaceLayout{xh, xh + rm};
 }
 
+// Sizes that the products take: kernels and launches count rows and columns in 32 bits, a tile or a stride of a block past the
+// last one included.
+constexpr int64_t kMaxExtent = (int64_t(1) << 31) - (int64_t(1) << 16);
+
 // Validates one problem against the ABI's preconditions (no launch, no CUDA call).
 lowbit_status validate_gemm(const GemmProblem& g);
 

@@ -58,8 +58,8 @@ lowbit_status check_loss(const LossProblem& p) {
         if (!p.X || !p.labels) return LOWBIT_ERR_INVALID_ARG;
         if (!aligned(p.X, 16) || !aligned(p.labels, 4)) return LOWBIT_ERR_ALIGNMENT;
     }
-    // (the grids' tiles are counted in 32 bits)
-    if (p.M >= kMaxSize || (p.M + 255) / 256 * ((p.table.K + 255) / 256) >= int64_t(1) << 24) return LOWBIT_ERR_UNSUPPORTED;
+    // (tiles of the products are counted in 32 bits, and so are their rows and columns)
+    if (p.M > kMaxExtent || p.vocab > kMaxExtent || p.table.K > kMaxExtent || (p.M + 255) / 256 * ((p.table.K + 255) / 256) >= int64_t(1) << 24) return LOWBIT_ERR_UNSUPPORTED;
     return LOWBIT_OK;
 }
 
@@ -74,7 +74,7 @@ using namespace lowbit;
 
 LOWBIT_API size_t lowbit_cross_entropy_workspace_size(int64_t M, int64_t vocab, int64_t K, int bits, int backward) {
     if (M < 0 || vocab < 1 || K < 1 || (bits != 1 && bits != 2 && bits != 4 && bits != kDense) || backward < 0 || backward > 2) return 0;
-    if (M >= kMaxSize || vocab >= kMaxSize || K >= kMaxSize) return 0;
+    if (M > kMaxExtent || vocab > kMaxExtent || K > kMaxExtent) return 0;
     return loss_layout(M, vocab, K, bits, backward > 0, backward == 2).total;
 }
 

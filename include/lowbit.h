@@ -118,7 +118,7 @@ size_t lowbit_gemm_workspace_size(int64_t M, int64_t K);
  *              the caller, overwritten by the call, and must not be used by concurrently
  *              running work until the call's kernels have finished
  * GPU path preconditions (else LOWBIT_ERR_UNSUPPORTED): group_size 64 or 128,
- * K % group_size == 0, K % 128 == 0 when bits == 1, N % 8 == 0, M, N, K < 2^31.
+ * K % group_size == 0, K % 128 == 0 when bits == 1, N % 8 == 0, M, N, K <= 2^31 - 2^16.
  * M == 0 or N == 0 is a no-op. Kernel-side bounded waits that give up set the device
  * status word (see lowbit_device_status) instead of trapping. */
 lowbit_status lowbit_gemm(int64_t M, int64_t N, int64_t K, int bits, int group_size, const void* X,
@@ -371,7 +371,8 @@ size_t lowbit_cross_entropy_workspace_size(int64_t M, int64_t vocab, int64_t K, 
  * 2^-22 (|q - z| + |z| + 25) of its scale, which is 2^-17 for zeros within 0 .. 15, and 2^-24 absolute; where |z| passes 2000,
  * as in lowbit_gemm, 2^-10 of itself), or up to 16 tokens as q - 8 and z - 8, multiplied apart; so the loss is
  * good to fp32 sums of K products. A row of X with an infinity or NaN has a lse and loss that are not finite; other rows
- * are not touched by it. 1 <= vocab <= N (else LOWBIT_ERR_INVALID_ARG). */
+ * are not touched by it. 1 <= vocab <= N (else LOWBIT_ERR_INVALID_ARG); M, vocab, K <= 2^31 - 2^16 (else
+ * LOWBIT_ERR_UNSUPPORTED). */
 lowbit_status lowbit_cross_entropy(int64_t M, int64_t vocab, int64_t N, int64_t K, int bits, int group_size, const void* X,
                                    const void* W, const void* scales, const void* zeros, const int32_t* labels, float* loss,
                                    float* lse, void* workspace, size_t workspace_bytes, void* stream);

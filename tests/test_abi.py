@@ -246,3 +246,12 @@ def test_binding_without_the_library_raises(tmp_path):
                        text=True, timeout=300, env={**os.environ, "PYTHONPATH": str(tmp_path)})
     assert r.returncode == 0, r.stderr + r.stdout
     assert "raised" in r.stdout and "liblowbit.so is missing" in r.stdout
+
+
+def test_gemm_rejects_sizes_whose_tiles_would_pass_32_bits(lib):
+    last = (1 << 31) - (1 << 16)
+    call = lambda M, N, K, ws=A: lib.lowbit_gemm(M, N, K, 2, 64, A, A, A, None, A, ws, 1 << 60, None)
+    for n in (last + 64, (1 << 31) - 64):
+        assert call(1, n, 64) == call(n, 8, 64) == call(1, 8, n) == 3
+        assert lib.lowbit_gemm_dx(1, n, 64, 2, 64, A, A, A, None, A, A, 1 << 60, None) == 3
+    assert call(1, last, 64, None) == 8          # (on to the workspace)

@@ -155,3 +155,20 @@ def test_binding_refuses_before_the_library():
     for bad in (dict(tokens=labels.long()), dict(tokens=labels[:2]), dict(dy=x.float()), dict(dy=x[0])):
         with pytest.raises(ValueError):
             lb.embedding_backward(**dict(dict(tokens=labels, dy=x, rows=3), **bad))
+
+
+def test_sizes_whose_tiles_would_pass_32_bits(lib):
+    """A vocabulary (or K) that ends within a tile or a block's stride of 2^31 is refused: its last indices would not fit."""
+    last = (1 << 31) - (1 << 16)
+    size = lib.lowbit_cross_entropy_workspace_size
+    for N in (last + 8, (1 << 31) - 1024, (1 << 31) - 8):
+        for kw in (dict(bits=2), DENSE):
+            for M in (1, 17, 300):
+                assert forward(lib, N=N, vocab=N, K=64, M=M, **kw) == 3
+                assert backward(lib, N=N, vocab=N, K=64, M=M, **kw) == 3
+            assert size(1, N, 64, kw["bits"], 0) == size(1, N, 64, kw["bits"], 1) == 0
+        assert forward(lib, **DENSE, N=8, vocab=8, K=N) == 3 and backward(lib, **DENSE, N=8, vocab=8, K=N) == 3
+        assert size(1, 8, N, 16, 0) == 0
+    # the largest that is taken goes on to the checks of the workspace; a table may be longer than its vocabulary
+    assert forward(lib, N=last, vocab=last, K=64, ws=None) == 8 and size(1, last, 64, 2, 0) == 4 * last
+    assert forward(lib, N=(1 << 31) - 8, vocab=last, K=64, ws=None) == 8
