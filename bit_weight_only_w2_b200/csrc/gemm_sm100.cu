@@ -14,6 +14,7 @@
 #include <cstdio>
 
 #include "adapter_internal.h"
+#include "capacity_cache.h"
 #include "lowbit_internal.h"
 #include "sm100_ptx.cuh"
 #include "tcgen05_ptx.cuh"
@@ -284,42 +285,28 @@ bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, int elem_bytes, co
 }
 
 int cluster_capacity(const void* kernel, int ks, int threads, int smem_bytes, bool along_x) {
-    struct Entry {
-        const void* fn;
-        int dev, ks;
-        bool x;
-        int cap;
-    };
-    static Entry cache[64];
-    static int used = 0;
-    static std::mutex mu;
+    static CapacityCache cache;
     int dev = 0;
     cudaGetDevice(&dev);
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        for (int i = 0; i < used; ++i)
-            if (cache[i].fn == kernel && cache[i].dev == dev && cache[i].ks == ks && cache[i].x == along_x)
-                return cache[i].cap;
-    }
-    int n = 0;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = along_x ? ks : 1;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = along_x ? 1 : ks;
-    cfg.gridDim = along_x ? dim3(ks, 1, 1) : dim3(1, 1, ks);
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem_bytes;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
-        cudaGetLastError();
-        n = num_sms() / ks;
-    }
-    std::lock_guard<std::mutex> lock(mu);
-    if (used < 64) cache[used++] = Entry{kernel, dev, ks, along_x, n};
-    return n;
+    return cache.get(kernel, dev, ks, along_x, [&] {
+        int n = 0;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = along_x ? ks : 1;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = along_x ? 1 : ks;
+        cfg.gridDim = along_x ? dim3(ks, 1, 1) : dim3(1, 1, ks);
+        cfg.blockDim = dim3(threads, 1, 1);
+        cfg.dynamicSmemBytes = smem_bytes;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+            cudaGetLastError();
+            n = num_sms() / ks;
+        }
+        return n;
+    });
 }
 
 // SM count of the current device (cached per device; 148 if the query fails).
