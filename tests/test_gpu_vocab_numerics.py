@@ -115,3 +115,68 @@ def test_dw_of_many_tokens(M, K, N, V, labelled, repeat):
     check(dx, rx, ex, "dx")
     again = lb.cross_entropy_backward(grad, torch.where(ref.valid[:, None], x, 7.0), labels, lse, *table.args(), vocab=V, need_dw=True)
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+FORMATS = [(16, 0), (1, 128), (2, 64), (4, 64)]
+
+
+@pytest.mark.parametrize("bits,gs", FORMATS)
+@pytest.mark.parametrize("M,K", [(509, 1280), (509, 2560), (77, 2560), (300, 8192), (77, 8192)])
+def test_error_in_the_norm(bits, gs, M, K):
+    """What the tensor cores cut off a sum over n = K / 16 steps is 0.26 n 2^-24 of it on average, and made up for; a fifth of
+    that is its spread over the tokens, which is left, with two roundings to fp32 (2^-23) and nothing that adds up over tokens."""
+    V = 6007
+    table = Table(6008, K, bits, gs, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(K + M)
+    x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    labels = torch.randint(0, V, (M,), generator=g, device="cuda", dtype=torch.int32)
+    loss, lse = lb.cross_entropy(x, labels, *table.args(), vocab=V)
+    l = x.double() @ table.rows()[:V].T
+    want = torch.logsumexp(l, 1)
+    left = 0.26 * (K / 16) * 2.0 ** -24 / 5 + 2.0 ** -23
+    assert float((lse.double() - want).norm() / want.norm()) <= left
+    want = want - l.gather(1, labels.long()[:, None])[:, 0]
+    assert float((loss.double() - want).norm() / want.norm()) <= left
+
+
+@pytest.mark.parametrize("bits,gs", FORMATS)
+@pytest.mark.parametrize("M", [40, 200])
+@pytest.mark.parametrize("K", [2560, 8192])
+@pytest.mark.parametrize("large", ["first", "last", "spread"])
+def test_a_few_large_columns(bits, gs, M, K, large):
+    """Four columns of x that carry the logit, and small ones of the same sign. Last, they lose nothing, and the factor that
+    makes up for the usual loss stays: 0.26 K / 16 2^-24, and a tenth for what the small ones lose among themselves. First or
+    in between, each step of the small ones may lose on the whole sum: at most half of what K fp32 additions may. (One row:
+    lse is its logit, rounded once, and scaled once.)"""
+    table = Table(8, K, bits, gs)
+    at = {"first": torch.arange(4), "last": torch.arange(K - 4, K), "spread": torch.arange(4) * (K // 4) + 7}[large].cuda()
+    if bits == 16:
+        table.weight.copy_(table.weight.abs())
+        table.weight[:, at] = 0.05
+    else:
+        table.codes.copy_(torch.full_like(table.codes, 13 if bits == 4 else 1))
+        table.weight = lb.pack(table.codes, bits)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = 1e-3 + 2e-3 * torch.rand(M, K, generator=g, device="cuda")
+    x[:, at] = K / 50 * (1 + torch.rand(M, 4, generator=g, device="cuda"))
+    x = x.bfloat16()
+    labels = torch.full((M,), -1, device="cuda", dtype=torch.int32)
+    _, lse = lb.cross_entropy(x, labels, *table.args(), vocab=1)
+    w = table.rows()[0]
+    assert bool((w >= 0).all())
+    want = x.double() @ w
+    bound = (0.36 * K / 16 * 2.0 ** -24 if large == "last" else K * 2.0 ** -25) + 2.0 ** -22
+    if bits == 4:   # the weights' two fp16 values: 2^-22 (|q - z| + |z| + 25) s, of weights of 4 s and more with |z| <= 9
+        bound = bound + 2.0 ** -22 * (4 + 9 + 25) / 4
+    check(lse, want, bound * want, "lse")
+
+
+def test_the_factor_of_very_long_rows():
+    """Behind K = 65536 the factor grows no more: a single product, which loses nothing, is off by 0.26 * 4096 * 2^-24 at most."""
+    K, M = 1 << 20, 20
+    w = torch.zeros(8, K, device="cuda", dtype=torch.bfloat16)
+    x = torch.zeros(M, K, device="cuda", dtype=torch.bfloat16)
+    w[:, -1], x[:, -1] = 1.0, torch.arange(1, M + 1, device="cuda").bfloat16()
+    _, lse = lb.cross_entropy(x, torch.zeros(M, device="cuda", dtype=torch.int32), w, vocab=1)
+    want = x[:, -1].double()
+    check(lse, want, (0.26 * 4096 * 2.0 ** -24 + 2.0 ** -22) * want, "lse")
