@@ -848,7 +848,8 @@ def embedding(tokens: torch.Tensor, weight: torch.Tensor, scales: Optional[torch
 def embedding_backward(tokens: torch.Tensor, dy: torch.Tensor, rows: int, first: int = 0, multiplier: float = 1.0,
                        out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient of rows first .. first + rows - 1 of a table, bf16 [rows][K], for dy bf16 [T][K] of the
-    embeddings of tokens int32 [T]. Rows without tokens are zeros; a row's sum is fp32, in the tokens' order."""
+    embeddings of tokens int32 [T]. Rows without tokens are zeros; a row's sum is fp32, of stretches in the tokens' order
+    that are added in that order."""
     r = _calls().embedding_backward(tokens, dy, rows, first, multiplier, out, ws)
     if r is not None:
         if type(r) is int:

@@ -1,11 +1,13 @@
 // Lookup of vocabulary rows by token, and its gradient by sorted tokens.
 //
-// Lookup: y[t] = multiplier * E[token t] (zeros for a token outside the table), one pass bound by memory: a warp
-// takes 1024 columns of a token, four 16-byte pieces a lane, all requested before the first is used. Packed rows are
-// decoded on the way: the four words of a block hold the pairs of four (ternary: eight) neighbouring 8-column pieces,
-// which as many lanes read together.
+// Lookup: y[t] = multiplier * E[token t] (zeros for a token outside the table), one pass: a warp takes 1024 columns of a
+// token, four 16-byte pieces a lane, all requested before the first is used. Rows of bf16 are bound by memory. Packed rows
+// are decoded on the way: the four words of a block hold the pairs of four (ternary: eight) neighbouring 8-column pieces,
+// which as many lanes read together; that is bound by the issue of instructions (16384 tokens of 2560 ternary columns: 78 % of
+// the slots, DRAM 17 % of its rate, since most of Y is still in L2 at the end).
 //
-// Gradient: dE[v] = multiplier * the sum of dy[t] over the tokens t of v, in the tokens' order, whatever the timing:
+// Gradient: dE[v] = multiplier * the sum of dy[t] over the tokens t of v, of stretches in the tokens' order that are joined in
+// that order, whatever the timing:
 //   1. the tokens are sorted by row (stable radix sort, digits of up to 9 bits): up to kSortMost tokens in one CTA,
 //      more in tiles of kTile, with a launch for the digits' counts and one for the moves of each digit, and one for the
 //      counts' sums between them where there are more than kFewTiles tiles (the sort of 32768 tokens in one CTA took
@@ -13,8 +15,9 @@
 //   2. a CTA adds up kRun tokens of the sorted list for 1024 columns, in fp32: a row whose tokens all lie in the run is
 //      stored at once; the parts of rows that go over a run's ends are kept in fp32;
 //   3. the parts are joined in order by the CTA of the run that such a row begins in.
-// Runs of equal length bound the work of a CTA however often a token repeats. The zeros bound a whole table (131072 x
-// 2560: 115 of 180 us with 32768 tokens). Few rows (tokens added to a frozen table), or few tokens on a small table, take
+// Runs of equal length bound the work of step 2 however often a token repeats; step 3 is a CTA's per 256 columns of the row,
+// whose parts it reads: 100000 tokens of one row take 250 us for 300 x 2560, of all rows alike 154 (72 columns: 102 and 50).
+// The zeros bound a whole table (131072 x 2560: 115 of 180 us with 32768 tokens). Few rows (tokens added to a frozen table), or few tokens on a small table, take
 // one launch instead.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -668,7 +671,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) sum_few_tokens_kernel(const i
     }
 }
 
-// Few: as many CTAs as the GPU holds at once, each with a list it looks through in a few microseconds.
+// Few: as many CTAs as the GPU holds at once, each with a list it looks through in a few microseconds. 4096 tokens, one in
+// twenty on 24 rows of 2560 (100 rows): 5.9 (8.4) us, sorted 14.1 (14.7); 8192: 9.7 (15.3) and 15.1 (16.3); 16384: 17.5 (27.9)
+// and 18.8 (19.8). The limit keeps away from where they meet, since tokens that are all on the rows take longer.
 bool few_rows(int64_t T, int64_t rows, int64_t K) { return T <= 4096 && rows * ((K + 255) / 256) <= 148 * 8; }
 
 struct GradLayout {

@@ -405,8 +405,8 @@ size_t lowbit_embedding_workspace_size(int64_t T, int64_t rows, int64_t K);
 
 /* dE bf16 [rows][K], written in full (zeros for a row without tokens), of dY bf16 [T][K], both 16-byte aligned, K a
  * multiple of 8. Only the rows first .. first + rows - 1 of the table have a gradient (the whole table, or the tokens
- * added to a frozen one); tokens outside them count for nothing. A row's sum is fp32, in the tokens' order, and is
- * rounded once. */
+ * added to a frozen one); tokens outside them count for nothing. A row's sum is fp32, of stretches in the
+ * tokens' order that are added in that order, and is rounded once. */
 lowbit_status lowbit_embedding_backward(int64_t T, int64_t K, int64_t first, int64_t rows, const int32_t* tokens,
                                         const void* dY, float multiplier, void* dE, void* workspace, size_t workspace_bytes,
                                         void* stream);
