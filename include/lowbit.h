@@ -368,13 +368,14 @@ size_t lowbit_cross_entropy_workspace_size(int64_t M, int64_t vocab, int64_t K, 
 
 /* loss fp32 [M] and lse fp32 [M] of X bf16 [M][K] (16-byte aligned). Sums are fp32. A packed table's weights are the
  * values that lowbit_gemm decodes, a uint4 weight as the sum of two fp16 values (off by at most
- * 2^-22 (|q - z| + |z| + 25) of its scale, which is 2^-17 for zeros within 0 .. 15, and 2^-24 absolute; where |z| passes 2000,
- * as in lowbit_gemm, 2^-10 of itself), or up to 16 tokens as q - 8 and z - 8, multiplied apart; so the loss is
+ * 2^-22 (|q - z| + |z| + 25) of its scale, which is under 2^-16 for zeros within 0 .. 15, and 2^-24 absolute; where |z|
+ * passes 2000, as in lowbit_gemm, 2^-10 of itself), or up to 16 tokens as q - 8 and z - 8, multiplied apart; so the loss is
  * good to fp32 sums of K products. On the tensor cores (bf16 tables, and packed ones from 17 tokens on) those sums are cut
  * off towards zero, and the logits are scaled by 1 + 0.26 * 2^-24 * K / 16 (K up to 65536), what sums of products of both
  * signs lose on average: a logit whose large products come last keeps that factor (2.5e-6 at K = 2560), one whose large
- * products come first is up to 4.4 * 2^-24 * K / 16 too small before it (4.2e-5). A row of X with an infinity or NaN has a lse and loss that are not finite; other rows
- * are not touched by it. 1 <= vocab <= N (else LOWBIT_ERR_INVALID_ARG); M, vocab, K <= 2^31 - 2^16 (else
+ * products come first is up to 4.4 * 2^-24 * K / 16 too small before it (4.2e-5). A row of X with an infinity or NaN has
+ * a lse and loss that are not finite; other rows are not touched by it. 1 <= vocab <= N (else LOWBIT_ERR_INVALID_ARG);
+ * M, vocab, K <= 2^31 - 2^16 (else
  * LOWBIT_ERR_UNSUPPORTED). */
 lowbit_status lowbit_cross_entropy(int64_t M, int64_t vocab, int64_t N, int64_t K, int bits, int group_size, const void* X,
                                    const void* W, const void* scales, const void* zeros, const int32_t* labels, float* loss,
